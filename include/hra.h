@@ -59,6 +59,11 @@ extern "C" {
 #define HRA_DEVERR_CODE_RANGE 4u   /* a code index outside [0, codebook_size) was clamped        */
 #define HRA_DEVERR_POS_RANGE 8u    /* a device-resident position was outside [0, n_slots); the row
                                        ran at the nearest slot inside the cache                   */
+#define HRA_DEVERR_PAGE_RANGE 16u  /* a page table entry names no page of the pool; its tokens were
+                                       neither written nor attended                               */
+#define HRA_DEVERR_PARENT_RANGE 32u /* a parent row outside [-1, rows); the row was emptied        */
+#define HRA_DEVERR_PAGES_SPENT 64u /* the pool (or a row's table) has too few pages left: nothing
+                                       was changed                                                */
 
 /* ---- model description ---------------------------------------------------------------------- */
 /* Backbone and audio-head shape.  Supported: head_dim in {64, 128}; n_q_heads % n_kv_heads == 0;
@@ -418,6 +423,99 @@ int hra_prefill_fp8(const hra_dims* dims, const hra_weights* weights, const hra_
                     const int32_t* tokens_dev, const int32_t* seq_lens, int32_t batch, int32_t max_len,
                     const hra_kv_cache* kv, void* last_hidden_dev, void* workspace,
                     size_t workspace_bytes, uint32_t flags, void* stream);
+
+/* ---- paged 8-bit K/V cache -------------------------------------------------------------------- */
+/* K and V in OCP E4M3 with one fp32 scale for each block of 16 tokens, kv head, and K or V, in pages
+ * that rows share: half the bytes of the bf16 cache, and several continuations of one prompt hold its
+ * pages once.  An element's value is code * scale.  All pointers are device memory of the caller.
+ *   codes       uint8 [n_layers][n_pages][2][n_kv_heads][page_size][head_dim] (0 = K, 1 = V)
+ *   scales      fp32 [n_layers][n_pages][2][n_kv_heads][page_size / 16]; powers of two
+ *   page_table  int32 [rows][max_pages]: entry i of row b is the page of its positions
+ *               [i * page_size, (i + 1) * page_size); -1 = none.  The same pages in every layer.
+ *   lens        int32 [rows]: positions each row holds (written by hra_kv8_append and the path)
+ *   refs        int32 [n_pages]: rows that list the page; NULL where only append / attention are used
+ *   errors      one word, set to 0 by the caller: HRA_DEVERR_* bits are OR-ed into it and stay until
+ *               the caller clears it (hra_device_error(errors, stream) reads it)
+ * codes and scales 16-byte aligned, the rest 4-byte.  head_dim 64 or 128, page_size 16, 32, 64 or 128,
+ * n_kv_heads <= 1024, rows <= 65535, max_pages * page_size <= 2^30.
+ * A page that several rows list must not be written: only positions of pages that are full are shared
+ * (hra_kv8_update sees to it as long as rows are only appended to). */
+typedef struct hra_kv8_cache {
+    void* codes;
+    float* scales;
+    int32_t* page_table;
+    int32_t* lens;
+    int32_t* refs;
+    uint32_t* errors;
+    int32_t n_layers, n_pages, n_kv_heads, head_dim, page_size, rows, max_pages;
+} hra_kv8_cache;
+
+/* New tokens of `batch` sequences into one layer.
+ *   k_dev, v_dev bf16 [total_rows] rows of [n_kv_heads][head_dim], row_stride elements apart (>= n_kv_heads *
+ *                head_dim, a multiple of 8: K and V may lie inside a merged projection's rows)
+ *   cu_dev       int32 [batch + 1]: row b of the table gets packed rows cu[b] .. cu[b + 1) (0 = cu[0]; a
+ *                row may get none and is then left alone)
+ *   start_dev    int32 [batch]: position of the first of them; they follow in order
+ *   max_new      most new tokens of a row (1 .. total_rows)
+ * For each block of 16 positions, head, and K or V: a = max |x| over the block's new tokens, s the smallest
+ * power of two >= 2^-126 with a <= 448 s; if the block held tokens before the first new one, s = max(stored
+ * scale, s) and, where s has grown, their codes become e4m3(value * stored / s).  code = e4m3(x / s): to nearest,
+ * ties to even; infinities saturate, a NaN stays one.  lens[b] = start[b] + new tokens.  Slots behind
+ * the last new token keep their bytes.
+ * Positions outside [0, max_pages * page_size) are not written (HRA_DEVERR_POS_RANGE), nor those whose
+ * table entry is no page of the pool (HRA_DEVERR_PAGE_RANGE), nor a row's tokens beyond max_new
+ * (HRA_DEVERR_POS_RANGE).  Two rows of one call must not write the same block. */
+int hra_kv8_append(const hra_kv8_cache* cache, int32_t layer, const void* k_dev, const void* v_dev,
+                   int64_t row_stride, const int32_t* cu_dev, const int32_t* start_dev, int32_t batch,
+                   int32_t total_rows, int32_t max_new, void* stream);
+
+/* Causal grouped-query attention of the new tokens over the cache (which holds them already).
+ *   q_dev        bf16 [total_rows] rows of [n_q_heads][head_dim], q_row_stride elements apart (a multiple of 8)
+ *   scale        of the scores; 0 = 1 / sqrt(head_dim).  n_q_heads a multiple of n_kv_heads, at most 16 times
+ *                as many; q head h reads kv head h / (n_q_heads / n_kv_heads)
+ *   kv_len_dev   int32 [batch]: positions row b holds, its new tokens' among them.  New token i of n sits at
+ *                position kv_len - n + i and attends positions 0 .. kv_len - n + i; one that sees
+ *                none gets zeros.
+ *   max_new      most new tokens of a row (1 .. total_rows); the tokens of a row beyond it get no output
+ *                (HRA_DEVERR_POS_RANGE)
+ *   max_len      host upper bound of kv_len (<= max_pages * page_size).  It chooses how the work is split;
+ *                larger lengths give the same values
+ *   out_dev      bf16 [total_rows][n_q_heads][head_dim]; rows behind cu[batch] are left as they are
+ * A kv_len outside [0, max_pages * page_size] is clamped (HRA_DEVERR_POS_RANGE); a table entry that is no page of
+ * the pool hides its positions (HRA_DEVERR_PAGE_RANGE).  Slots that hold no token are never used, whatever they
+ * contain.  Scores, softmax statistics and output sums are fp32; q and the probabilities enter the products in f16
+ * under powers of two (q exactly, probabilities rounded to 11 bits).  The call can be captured and replayed
+ * while max_new and max_len hold.  Calls that may overlap need workspaces of their own. */
+size_t hra_kv8_attention_workspace_size(const hra_kv8_cache* cache, int32_t batch, int32_t total_rows,
+                                        int32_t n_q_heads, int32_t max_new, int32_t max_len);
+int hra_kv8_attention(const hra_kv8_cache* cache, int32_t layer, const void* q_dev, int64_t q_row_stride,
+                      int32_t n_q_heads, float scale, const int32_t* cu_dev, const int32_t* kv_len_dev,
+                      int32_t batch, int32_t total_rows, int32_t max_new, int32_t max_len, void* out_dev,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* The rows of the next step: forked, reordered, freed, extended.
+ *   parents_dev  int32 [rows]: new row b is a copy of old row parents[b]; -1 empties it; NULL: every row stays
+ *   room_dev     int32 [rows]: pages are taken for lens[b] + room[b] positions; NULL: 0
+ *   table_out, lens_out, refs_out: as the cache's page_table, lens, refs (which they may be, or else must
+ *                not overlap)
+ * Pages whose page_size tokens are all filled are shared by the rows that copy them.  The pages behind (the
+ * part-filled one, and reserved ones) stay with the lowest row of each parent; the others get fresh pages, and the
+ * part-filled one's codes and scales are copied in every layer.  Rows take fresh pages in order, each the
+ * lowest-numbered page that no new row lists; refs_out counts the rows that list each page (a row keeps the pages
+ * reserved for it).  When too few pages are free, or a row would need more than max_pages, the outputs repeat the
+ * inputs, no page is copied and HRA_DEVERR_PAGES_SPENT is set.  A parent outside [-1, rows) counts as -1
+ * (HRA_DEVERR_PARENT_RANGE), a table entry outside [-1, n_pages) as -1 (HRA_DEVERR_PAGE_RANGE), a length outside
+ * [0, max_pages * page_size] as 0 (HRA_DEVERR_POS_RANGE). */
+size_t hra_kv8_pages_workspace_size(const hra_kv8_cache* cache);
+int hra_kv8_update(const hra_kv8_cache* cache, const int32_t* parents_dev, const int32_t* room_dev,
+                   int32_t* table_out, int32_t* lens_out, int32_t* refs_out, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* With U pages in use (refs > 0), the i-th used page numbered U or more (ascending) moves to the i-th unused page
+ * below U, in every layer; table_out and refs_out follow, lens_out = lens.  Pages U .. n_pages - 1 are free
+ * afterwards.  Outputs and workspace as hra_kv8_update. */
+int hra_kv8_compact(const hra_kv8_cache* cache, int32_t* table_out, int32_t* lens_out, int32_t* refs_out,
+                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- measurement ---------------------------------------------------------------------------- */
 /* Number of kernels the library has launched in this process (host-side count). */

@@ -26,6 +26,7 @@ HRA_OK = 0
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported dims", -3: "workspace too small",
           -4: "length or position outside the cache", -5: "CUDA error"}
 DEVERR_TOKEN_RANGE, DEVERR_WAIT_TIMEOUT, DEVERR_CODE_RANGE, DEVERR_POS_RANGE = 1, 2, 4, 8
+DEVERR_PAGE_RANGE, DEVERR_PARENT_RANGE, DEVERR_PAGES_SPENT = 16, 32, 64
 EPI_STORE, EPI_RESIDUAL, EPI_SWIGLU, EPI_F32 = 0, 1, 2, 3
 PREFILL_FULL_LAST_LAYER = 1
 
@@ -40,6 +41,8 @@ EXPORTED = ["hra_prefill_workspace_size", "hra_prefill", "hra_prefill_chunk_work
             "hra_nvfp4_quantize_weight", "hra_linear_nvfp4_workspace_size", "hra_linear_nvfp4",
             "hra_nvfp4_band_scales",
             "hra_prefill_nvfp4_workspace_size", "hra_prefill_nvfp4",
+            "hra_kv8_append", "hra_kv8_attention_workspace_size", "hra_kv8_attention", "hra_kv8_pages_workspace_size",
+            "hra_kv8_update", "hra_kv8_compact",
             "hra_launch_counter", "hra_probe_select", "hra_probe_collect", "hra_set_decode_pass",
             "hra_set_gemm_pairs", "hra_device_error", "hra_status_string"]
 PROBE = {"none": 0, "qkv": 1, "o_proj": 2, "gate_up": 3, "down": 4, "attention": 5, "audio_head": 6,
@@ -81,6 +84,12 @@ class HraFp8Layer(ctypes.Structure):
 class HraNvfp4Layer(ctypes.Structure):
     _fields_ = [("w_qkv", ctypes.c_void_p), ("codes", ctypes.c_void_p * 4), ("scales", ctypes.c_void_p * 4),
                 ("w_scale", ctypes.c_void_p), ("a_scale", ctypes.c_void_p)]
+
+
+class HraKv8Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "scales", "page_table", "lens", "refs", "errors")] + \
+               [(n, ctypes.c_int32) for n in ("n_layers", "n_pages", "n_kv_heads", "head_dim", "page_size", "rows",
+                                              "max_pages")]
 
 
 class HraSampling(ctypes.Structure):
@@ -160,6 +169,17 @@ def lib() -> ctypes.CDLL:
         for f in ("hra_fp8_quantize_weight", "hra_fp8_quantize", "hra_linear_fp8", "hra_fp8_calibrate",
                   "hra_prefill_fp8", "hra_nvfp4_quantize_weight", "hra_linear_nvfp4", "hra_prefill_nvfp4",
                   "hra_nvfp4_band_scales"):
+            getattr(L, f).restype = ctypes.c_int
+        kp = ctypes.POINTER(HraKv8Cache)
+        L.hra_kv8_append.argtypes = [kp, i32, vp, vp, i64, vp, vp, i32, i32, i32, vp]
+        L.hra_kv8_attention_workspace_size.argtypes = [kp, i32, i32, i32, i32, i32]
+        L.hra_kv8_attention_workspace_size.restype = sz
+        L.hra_kv8_attention.argtypes = [kp, i32, vp, i64, i32, ctypes.c_float, vp, vp, i32, i32, i32, i32, vp, vp, sz, vp]
+        L.hra_kv8_pages_workspace_size.argtypes = [kp]
+        L.hra_kv8_pages_workspace_size.restype = sz
+        L.hra_kv8_update.argtypes = [kp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.hra_kv8_compact.argtypes = [kp, vp, vp, vp, vp, sz, vp]
+        for f in ("hra_kv8_append", "hra_kv8_attention", "hra_kv8_update", "hra_kv8_compact"):
             getattr(L, f).restype = ctypes.c_int
         L.hra_linear_workspace_size.argtypes = [i32, i32, i32, i32, i32]
         L.hra_linear_workspace_size.restype = sz
@@ -750,6 +770,150 @@ class Nvfp4Backbone:
                                        _stream(stream)), "hra_prefill_nvfp4")
         self.last_ws = ws
         return out
+
+
+class Kv8Cache:
+    """A paged 8-bit K/V cache (``hra_kv8_cache``): E4M3 codes uint8 [n_layers, n_pages, 2, n_kv_heads, page_size,
+    head_dim], fp32 scales [n_layers, n_pages, 2, n_kv_heads, page_size / 16], the page table int32 [rows,
+    max_pages], the rows' lengths int32 [rows] and the pages' reference counts int32 [n_pages], all CUDA tensors of
+    one device that the object reads and writes in place.
+
+    Calls run on the current stream of the cache's device (or `stream`); the workspaces belong to the object, so
+    calls of one object on several streams must be ordered by the caller."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                 refs: Optional[torch.Tensor] = None):
+        if codes.dim() != 6 or codes.shape[2] != 2:
+            raise HraError("codes must be uint8 [n_layers, n_pages, 2, n_kv_heads, page_size, head_dim]")
+        n_layers, n_pages, _, n_kv, page, hd = codes.shape
+        if tuple(scales.shape) != (n_layers, n_pages, 2, n_kv, page // 16):
+            raise HraError("scales must be float32 [n_layers, n_pages, 2, n_kv_heads, page_size / 16]")
+        if page_table.dim() != 2 or tuple(lens.shape) != (page_table.shape[0],):
+            raise HraError("page_table must be int32 [rows, max_pages] and lens int32 [rows]")
+        if refs is not None and tuple(refs.shape) != (n_pages,):
+            raise HraError("refs must be int32 [n_pages]")
+        self.codes, self.scales, self.page_table, self.lens, self.refs = codes, scales, page_table, lens, refs
+        self.device = codes.device
+        for t, name in ((scales, "scales"), (page_table, "page_table"), (lens, "lens"), (refs, "refs")):
+            if t is not None and t.device != self.device:
+                raise HraError(f"{name} must be on the device of codes")
+        self.n_layers, self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n_layers, n_pages, n_kv, page, hd
+        self.rows, self.max_pages = page_table.shape
+        p_codes, p_scales = _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.float32, "scales")
+        p_table, p_lens = _ptr(page_table, torch.int32, "page_table"), _ptr(lens, torch.int32, "lens")
+        p_refs = _ptr(refs, torch.int32, "refs")
+        self.errors = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.struct = HraKv8Cache(p_codes.value, p_scales.value, p_table.value, p_lens.value,
+                                  p_refs.value if p_refs is not None else None, self.errors.data_ptr(), n_layers, n_pages,
+                                  n_kv, hd, page, self.rows, self.max_pages)
+        self._ref = ctypes.byref(self.struct)
+        self._attn_ws, self._pages_ws = _Workspace(), _Workspace()
+
+    @classmethod
+    def new(cls, d, rows: int, n_slots: int, n_pages: Optional[int] = None, page_size: int = 64,
+            device="cuda") -> "Kv8Cache":
+        """An empty cache for a model with the Dims field names: `rows` rows of up to n_slots positions; n_pages (by
+        default enough for all of them) pages of page_size tokens."""
+        width = (n_slots + page_size - 1) // page_size
+        n_pages = rows * width if n_pages is None else n_pages
+        codes = torch.zeros(d.n_layers, n_pages, 2, d.n_kv_heads, page_size, d.head_dim, dtype=torch.uint8, device=device)
+        scales = torch.zeros(d.n_layers, n_pages, 2, d.n_kv_heads, page_size // 16, dtype=torch.float32, device=device)
+        return cls(codes, scales, torch.full((rows, width), -1, dtype=torch.int32, device=device),
+                   torch.zeros(rows, dtype=torch.int32, device=device),
+                   torch.zeros(n_pages, dtype=torch.int32, device=device))
+
+    def empty_pages(self):
+        """Tensors for the out argument of update and compact: (page table, lens, refs)."""
+        return tuple(torch.empty_like(t) for t in (self.page_table, self.lens, self.refs))
+
+    def _rows(self, t: torch.Tensor, heads: int, name: str):
+        if t.device != self.device:
+            raise HraError(f"{name} must be on the device of the cache")
+        if t.dtype != torch.bfloat16:
+            raise HraError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        if t.dim() != 3 or t.shape[2] != self.head_dim or (heads and t.shape[1] != heads) \
+                or (t.shape[0] and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != self.head_dim))):
+            raise HraError(f"{name} must be [rows, heads, head_dim] with contiguous heads")
+        stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+        return ctypes.c_void_p(t.data_ptr()), stride
+
+    def _ints(self, t: torch.Tensor, n: int, name: str):
+        if t.device != self.device or t.dim() != 1 or t.shape[0] != n:
+            raise HraError(f"{name} must be int32 [{n}] on the device of the cache")
+        return _ptr(t, torch.int32, name)
+
+    def _on(self, stream):
+        return ctypes.c_void_p((stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream)
+
+    def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, start: torch.Tensor, max_new: int,
+               stream=None) -> None:
+        """hra_kv8_append: k, v bf16 [T, n_kv_heads, head_dim] (rows may be strided), cu int32 [B + 1] and start int32
+        [B] on the device: row b's tokens cu[b] .. cu[b + 1) go to its positions from start[b] on."""
+        pk, sk = self._rows(k, self.n_kv_heads, "k")
+        pv, sv = self._rows(v, self.n_kv_heads, "v")
+        if k.shape[0] != v.shape[0] or sk != sv:
+            raise HraError("k and v must have the same rows and row stride")
+        B = start.shape[0]
+        with torch.cuda.device(self.device):
+            rc = lib().hra_kv8_append(self._ref, layer, pk, pv, sk, self._ints(cu, B + 1, "cu"),
+                                      self._ints(start, B, "start"), B, k.shape[0], max_new, self._on(stream))
+        _check(rc, "hra_kv8_append")
+
+    def attend(self, layer: int, q: torch.Tensor, cu: torch.Tensor, kv_len: torch.Tensor, max_new: int, max_len: int,
+               scale: float = 0.0, out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+        """hra_kv8_attention: q bf16 [T, n_q_heads, head_dim] (rows may be strided) of rows' last tokens, kv_len int32
+        [B] positions held -> bf16 [T, n_q_heads, head_dim]."""
+        pq, sq = self._rows(q, 0, "q")
+        T, nq = q.shape[0], q.shape[1]
+        B = kv_len.shape[0]
+        if out is None:
+            out = torch.empty(T, nq, self.head_dim, dtype=torch.bfloat16, device=self.device)
+        elif tuple(out.shape) != (T, nq, self.head_dim) or out.device != self.device:
+            raise HraError("out must be bf16 [T, n_q_heads, head_dim] on the device of the cache")
+        with torch.cuda.device(self.device):
+            ws = workspace
+            if ws is None:
+                need = lib().hra_kv8_attention_workspace_size(self._ref, B, T, nq, max_new, max_len)
+                ws = self._attn_ws.get(need, self.device)
+            rc = lib().hra_kv8_attention(self._ref, layer, pq, sq, nq, scale, self._ints(cu, B + 1, "cu"),
+                                         self._ints(kv_len, B, "kv_len"), B, T, max_new, max_len,
+                                         _ptr(out, torch.bfloat16, "out"), _ptr(ws, None, "workspace"), ws.numel(),
+                                         self._on(stream))
+        _check(rc, "hra_kv8_attention")
+        return out
+
+    def _pages(self, name, args, out, workspace, stream):
+        if self.refs is None:
+            raise HraError(f"{name} needs the cache's refs")
+        table, lens, refs = out if out is not None else (self.page_table, self.lens, self.refs)
+        if table.shape != self.page_table.shape or lens.shape != self.lens.shape or refs.shape != self.refs.shape or \
+                not table.device == lens.device == refs.device == self.device:
+            raise HraError("out must be tensors as empty_pages() makes them")
+        with torch.cuda.device(self.device):
+            ws = workspace if workspace is not None else \
+                self._pages_ws.get(lib().hra_kv8_pages_workspace_size(self._ref), self.device)
+            rc = getattr(lib(), name)(self._ref, *args, _ptr(table, torch.int32, "page table"),
+                                      _ptr(lens, torch.int32, "lens"), _ptr(refs, torch.int32, "refs"),
+                                      _ptr(ws, None, "workspace"), ws.numel(), self._on(stream))
+        _check(rc, name)
+        return table, lens, refs
+
+    def update(self, parents: Optional[torch.Tensor] = None, room: Optional[torch.Tensor] = None, out=None,
+               workspace: Optional[torch.Tensor] = None, stream=None):
+        """hra_kv8_update: rows forked, reordered or freed by parents (int32 [rows], -1 = empty) and given pages for
+        room (int32 [rows]) more tokens.  In place, or into out (see empty_pages): (page table, lens, refs)."""
+        args = (None if parents is None else self._ints(parents, self.rows, "parents"),
+                None if room is None else self._ints(room, self.rows, "room"))
+        return self._pages("hra_kv8_update", args, out, workspace, stream)
+
+    def compact(self, out=None, workspace: Optional[torch.Tensor] = None, stream=None):
+        """hra_kv8_compact: the pages in use to the low end of the pool; outputs as update."""
+        return self._pages("hra_kv8_compact", (), out, workspace, stream)
+
+    def device_error(self, stream=None) -> int:
+        """Synchronise and return the sticky error bits of every call since the errors word was last zeroed."""
+        return int(lib().hra_device_error(_ptr(self.errors, None, "errors"), self._on(stream)))
 
 
 def hra_device_error(workspace: torch.Tensor, stream=None) -> int:

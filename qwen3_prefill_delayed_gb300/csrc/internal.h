@@ -8,6 +8,7 @@
 #include <utility>
 
 #include "common.cuh"
+#include "kv8.cuh"
 
 namespace hra {
 
@@ -335,5 +336,55 @@ cudaError_t launch_absmax(const bf16* x, long long n, float* amax, cudaStream_t 
 cudaError_t launch_zero_floats(float* v, int n, cudaStream_t st);
 // scale[i] = amax[i] > 0 ? amax[i] / 448 : 1
 cudaError_t launch_amax_to_scale(const float* amax, float* scale, int n, cudaStream_t st);
+
+// ------------------------------------------------------------------ paged 8-bit K/V cache (kv8_*.cu)
+struct Kv8AppendArgs {
+    Kv8View view;
+    const bf16* k;          // rows of n_kv heads, heads contiguous, row_stride elements apart
+    const bf16* v;
+    long long row_stride;
+    const int32_t* cu;      // [batch + 1] device
+    const int32_t* start;   // [batch] device: position of each row's first new token
+    int32_t* lens;          // [batch] or null: receives start + new tokens of rows that get any
+    int batch, total_rows, max_new;
+};
+cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t st);
+
+// Causal attention of the last q_len positions of each sequence over its kv_len cached positions.
+struct Kv8AttnArgs {
+    Kv8View view;
+    const bf16* q;          // [total_rows] rows of nq heads, row_stride elements apart
+    long long row_stride;
+    bf16* out;              // [total_rows, nq, hd]
+    const int32_t* cu;      // [batch + 1] device
+    const int32_t* kv_len;  // [batch] device: cached positions, the new tokens' among them
+    float scale_log2;       // softmax scale * log2(e)
+    int batch, total_rows, nq, max_new, max_len;
+    void* scratch;
+};
+size_t kv8_attention_scratch_bytes(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int max_len);
+cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st);
+
+// Page tables, row lengths and reference counts of the next step, and the page copies they need.
+struct Kv8PagesArgs {
+    uint8_t* codes;
+    float* scales;
+    const int32_t* table;   // [rows][max_pages]
+    const int32_t* lens;    // [rows]
+    const int32_t* refs;    // [n_pages]
+    const int32_t* parents; // [rows] or null (every row keeps itself)
+    const int32_t* room;    // [rows] or null (0)
+    int32_t* table_out;     // may be the inputs themselves
+    int32_t* lens_out;
+    int32_t* refs_out;
+    unsigned int* err;
+    void* scratch;
+    long long code_page;    // bytes of a page's codes and of its scales
+    int scale_page;
+    int n_layers, n_pages, page_shift, rows, max_pages;
+};
+size_t kv8_pages_scratch_bytes(int rows, int max_pages, int n_pages);
+cudaError_t launch_kv8_update(const Kv8PagesArgs& a, cudaStream_t st);
+cudaError_t launch_kv8_compact(const Kv8PagesArgs& a, cudaStream_t st);
 
 }  // namespace hra
