@@ -1209,6 +1209,17 @@ bool make_map_u8(CUtensorMap* m, const void* base, int rows, int cols, int box_r
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_codes(CUtensorMap* m, const void* base, long long rows, int hd, int box_rows) {
+    if (!get_encoder()) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)hd, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)hd};
+    cuuint32_t box[2] = {(cuuint32_t)hd, (cuuint32_t)box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_map_2d(CUtensorMap* m, const void* base, int rows, int cols, int box_rows) {
     return get_encoder() && make_map(m, base, rows, cols, box_rows, 2);
 }

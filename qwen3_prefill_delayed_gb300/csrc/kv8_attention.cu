@@ -38,6 +38,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kStages = 3;      // blocks of 16 keys in flight per warp
+constexpr int kShortRows = 16;  // (position, head) rows of a kv head that fit this kernel's tile
+constexpr int kSerialKeys = 2048;   // keys that a short sequence may walk alone among prompts
 constexpr float kPScale = 15.f; // log2 of the largest p
 
 __device__ __forceinline__ void cp_async_ca(uint32_t dst, const void* src, int bytes) {
@@ -79,7 +81,7 @@ struct Piece {
 // One CTA = one (sequence, tile of query positions, kv head); its four warps take every fourth block
 // of 16 keys and join their (m, l, M, O) through shared memory.  NG x 8 rows a tile.
 template <int HD, int NG>
-__global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const Kv8AttnArgs a, int G, int QT) {
+__global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const Kv8AttnArgs a, int G, int QT, int max_rows) {
     pdl_launch();
     pdl_wait();
     using Pc = Piece<HD>;
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const Kv8AttnA
     const int tile = blockIdx.x, head = blockIdx.y, b = blockIdx.z;
     int row0, n;
     kv8_rows(a.cu, b, a.total_rows, row0, n);
-    if (tile * QT >= n) return;
+    if (tile * QT >= n || n * G > max_rows) return;
     const long long room = (long long)c.max_pages << c.page_shift;
     int kv_len = a.kv_len[b];
     if (kv_len < 0 || kv_len > room) {
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const Kv8AttnA
 }
 
 template <int HD, int NG>
-cudaError_t launch_ng(const Kv8AttnArgs& a, int G, int QT, int tiles, cudaStream_t st) {
+cudaError_t launch_ng(const Kv8AttnArgs& a, int G, int QT, int tiles, int max_rows, cudaStream_t st) {
     constexpr int queue = kWarps * kStages * Piece<HD>::STAGE;
     constexpr int join = kWarps * 8 * NG * (HD + 3) * 4;
     constexpr int smem = queue > join ? queue : join;
@@ -388,23 +390,36 @@ cudaError_t launch_ng(const Kv8AttnArgs& a, int G, int QT, int tiles, cudaStream
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
     const dim3 grid((unsigned)tiles, (unsigned)a.view.n_kv, (unsigned)a.batch);
-    HRA_LAUNCH((kv8_attn_kernel<HD, NG>), grid, dim3(kWarps * 32), smem, st, a, G, QT);
+    HRA_LAUNCH((kv8_attn_kernel<HD, NG>), grid, dim3(kWarps * 32), smem, st, a, G, QT, max_rows);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t kv8_attention_scratch_bytes(const Kv8View&, int, int, int, int, int) { return 0; }
+size_t kv8_attention_scratch_bytes(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int max_len) {
+    const int G = nq / c.n_kv;
+    if ((long long)G * max_new <= kShortRows) return 0;
+    return kv8_prompt_scratch_bytes(batch, total_rows, G);
+}
 
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st) {
     const int G = a.nq / a.view.n_kv;
+    const bool prompts = (long long)G * a.max_new > kShortRows && kv8_prompt_supported(a.view);
+    const int long_keys = a.max_len > kSerialKeys;
+    // short sequences go with the prompts unless they may hold many keys
+    const int short_rows = prompts && !long_keys ? 0 : kShortRows;
+    if (prompts) {
+        cudaError_t e = launch_kv8_prompt(a, short_rows, st);
+        if (e != cudaSuccess || short_rows == 0 || (long long)a.batch * a.max_new == a.total_rows) return e;
+    }
     // one n = 8 column group while the rows of a tile fit it, else two
+    const int rows = prompts ? kShortRows : 1 << 30;
     const int ng = (long long)G * a.max_new <= 8 ? 1 : 2;
     const int QT = 8 * ng / G;
-    const int tiles = (a.max_new + QT - 1) / QT;
+    const int tiles = prompts ? 1 : (a.max_new + QT - 1) / QT;
     if (a.view.head_dim == 128)
-        return ng == 1 ? launch_ng<128, 1>(a, G, QT, tiles, st) : launch_ng<128, 2>(a, G, QT, tiles, st);
-    return ng == 1 ? launch_ng<64, 1>(a, G, QT, tiles, st) : launch_ng<64, 2>(a, G, QT, tiles, st);
+        return ng == 1 ? launch_ng<128, 1>(a, G, QT, tiles, rows, st) : launch_ng<128, 2>(a, G, QT, tiles, rows, st);
+    return ng == 1 ? launch_ng<64, 1>(a, G, QT, tiles, rows, st) : launch_ng<64, 2>(a, G, QT, tiles, rows, st);
 }
 
 }  // namespace hra

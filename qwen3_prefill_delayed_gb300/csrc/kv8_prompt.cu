@@ -1,0 +1,653 @@
+// kv8_prompt.cu -- prompt and chunk attention over the paged 8-bit cache on the tensor cores.
+//
+// The formulas and the treatment of the scales are those of kv8_attention.cu.  Here an item is one
+// kv head and QT = 128 / G query positions of a sequence (128 rows (position, head), row r = (r / G, r % G))
+// over all their keys, in tiles of 128 keys:
+//   S = Q K^T    kind::f8f6f4 on the codes as they lie in the pages.  Q enters as the sum of two E4M3
+//                matrices under a power of two s per row: hi = e4m3(q / s), lo = e4m3(q / s - hi).  A bf16 value
+//                has 8 significant bits and each E4M3 value 4, so hi + lo is q / s exactly, except that elements
+//                below 2^-10 of the row's largest are off by at most 2^-18 of it (E4M3's subnormals).  Two MMAs
+//                at twice the f16 rate cost what one f16 MMA would, and no K is converted.
+//   O += P V     kind::f16: P, the probabilities times their blocks' V scales in f16 relative to a lazy
+//                running maximum M (it moves when it is exceeded by 2^4; 2^11 is the unit, so weights stay
+//                below 2^15), from tensor memory over the columns of S; V converted to f16 (exact).
+// Measured on GB300 (one thread issuing, SM clocks an instruction): 128 x N x 32 bytes takes 64 for N = 128 and
+// 53-63 for any smaller N, so a tile has 128 keys: 8 MMAs for S and 8 for PV.
+//
+// 320 threads, two CTAs an SM (256 tensor memory columns and 97 KB each), so that one CTA's softmax runs
+// under the other's MMAs:
+//   warp 0     TMA of K (one 16-key box a lane, page by page) into two stages, and the blocks' scales;
+//   warp 1     tensor memory, and one thread that issues the MMAs;
+//   warps 2-5  softmax, one row a thread, S read twice from tensor memory (maximum, then weights), O rescaled
+//              when M moves, and the output;
+//   warps 6-9  V: codes from global memory in registers, a tile ahead, to f16 in shared memory (keys that
+//              do not count as zeros, so stale slots never reach a product); and the items' Q.
+// The items come from a list built on the device (kv8_schedule_kernel), most key tiles first, and CTA c takes
+// entries in snake order.
+#include <cuda_fp8.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <math.h>
+
+#include "internal.h"
+
+namespace hra {
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int TROWS = 128;
+constexpr int TK = 128;            // keys a tile
+constexpr int NB = TK / kKv8Block; // blocks a tile
+constexpr float kUnit = 11.f;      // log2 of the weight of the reference maximum
+constexpr float kSlack = 4.f;      // how far a maximum may pass the reference before it moves
+
+struct PromptRec {   // 32 bytes: one (query tile, sequence) pair
+    int b, row0, n, q_lo, kv_len, keys, pad0, pad1;
+};
+constexpr int kRecWords = 8;
+
+template <int HD>
+struct Cfg {
+    static constexpr int QB = TROWS * HD;               // bytes of Q hi (and of lo)
+    static constexpr int KB = TK * HD;                  // one K stage
+    static constexpr int VB = TK * HD * 2;              // V as f16
+    static constexpr int OFF_K = 2 * QB;
+    static constexpr int OFF_V = OFF_K + 2 * KB;
+    static constexpr int OFF_BAR = OFF_V + VB;
+    static constexpr int OFF_SC = OFF_BAR + 256;        // [4][2][NB] scales of the last tiles
+    static constexpr int OFF_QS = OFF_SC + 4 * 2 * NB * 4;   // [2][TROWS] q scales
+    static constexpr int SMEM = OFF_QS + 2 * TROWS * 4;
+    static constexpr int ALLOC = SMEM + 1024;           // the base is aligned up to 1024 bytes
+    // q_full, q_empty, k_full[2], k_empty[2], s_full, p_full, v_full, pv_done, o_free, idle, sc_full[4], qs_full[2]
+    static constexpr int B_QF = 0, B_QE = 1, B_KF = 2, B_KE = 4, B_SF = 6, B_PF = 7, B_VF = 8, B_PV = 9, B_OF = 10,
+                         B_IDLE = 11, B_SC = 12, B_QS = 16, NBARS = 18;
+    static_assert(NBARS * 8 + 16 <= 256, "barrier area");
+    static_assert(ALLOC <= 115712, "two CTAs an SM");
+};
+
+struct PromptArgs {
+    Kv8View view;
+    const bf16* q;
+    long long row_stride;
+    bf16* out;
+    const int32_t* list;    // [0] = pairs, records from word 8 on
+    float scale_log2;
+    int nq, G, QT;
+    int v8;                 // out 32-byte aligned
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((unsigned short)w));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// D[tmem] (+)= A[tmem, f16 pairs] * B[smem]
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// 32 lanes x 16 columns, no wait
+__device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ int snake(int k) {
+    return k * (int)gridDim.x + ((k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+}
+
+// One CTA.  Counting sort of the non-empty (query tile, sequence) pairs by key tiles, most first.
+constexpr int kBins = 1024;
+__global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a, int G, int QT, int tiles,
+                                                            int short_rows, int32_t* __restrict__ list) {
+    pdl_launch();
+    pdl_wait();
+    __shared__ int hist[kBins];
+    __shared__ int total;
+    for (int i = threadIdx.x; i < kBins; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    const long long room = (long long)a.view.max_pages << a.view.page_shift;
+    const long long pairs = (long long)tiles * a.batch;
+    auto pair = [&](long long pr, PromptRec& r) -> int {   // -1: nothing there
+        const int tile = (int)(pr / a.batch);
+        r.b = (int)(pr - (long long)tile * a.batch);
+        kv8_rows(a.cu, r.b, a.total_rows, r.row0, r.n);
+        r.q_lo = tile * QT;
+        if (r.q_lo >= r.n || r.n * G <= short_rows) return -1;
+        const int len = a.kv_len[r.b];
+        if (tile == 0 && (len < 0 || len > room || r.n > a.max_new)) raise_error(a.view.err, HRA_DEVERR_POS_RANGE);
+        r.kv_len = len < 0 ? 0 : (int)min(room, (long long)len);
+        r.keys = max(0, r.kv_len - r.n + min(r.n, r.q_lo + QT));
+        r.pad0 = r.pad1 = 0;
+        return kBins - 1 - min(kBins - 1, (r.keys + TK - 1) / TK);
+    };
+    PromptRec r;
+    for (long long pr = threadIdx.x; pr < pairs; pr += blockDim.x) {
+        const int bin = pair(pr, r);
+        if (bin >= 0) atomicAdd(&hist[bin], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        constexpr int per = kBins / 32;
+        int s = 0;
+        for (int i = 0; i < per; ++i) s += hist[threadIdx.x * per + i];
+        int incl = s;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if ((int)threadIdx.x >= o) incl += v;
+        }
+        int run = incl - s;
+        for (int i = 0; i < per; ++i) {
+            const int h = hist[threadIdx.x * per + i];
+            hist[threadIdx.x * per + i] = run;
+            run += h;
+        }
+        if (threadIdx.x == 31) total = incl;
+    }
+    __syncthreads();
+    for (long long pr = threadIdx.x; pr < pairs; pr += blockDim.x) {
+        const int bin = pair(pr, r);
+        if (bin >= 0) {
+            int4* at = reinterpret_cast<int4*>(list + kRecWords * (1 + (long long)atomicAdd(&hist[bin], 1)));
+            at[0] = make_int4(r.b, r.row0, r.n, r.q_lo);
+            at[1] = make_int4(r.kv_len, r.keys, 0, 0);
+        }
+    }
+    if (threadIdx.x == 0) list[0] = total;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const PromptArgs p) {
+    using C = Cfg<HD>;
+    pdl_launch();
+    pdl_wait();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint32_t* slots = reinterpret_cast<uint32_t*>(bars + C::NBARS);   // tmem, abort, K tiles requested
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(slots + 1);
+    volatile int* issued = reinterpret_cast<volatile int*>(slots + 2);
+    float* sc = reinterpret_cast<float*>(smem + C::OFF_SC);
+    float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
+    auto bar = [&](int i) { return smem_u32(bars + i); };
+    const Kv8View& c = p.view;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_items = p.list[0] * c.n_kv;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NBARS; ++i) {
+            const bool four = i == C::B_QF || i == C::B_PF || i == C::B_VF || i == C::B_OF || i >= C::B_QS;
+            mbar_init(bar(i), four ? 4 : 1);
+        }
+        *abort_flag = 0;
+        *issued = 0;
+        mbar_fence_init();
+        tma_prefetch_map(&tmK);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(slots), 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tS = slots[0], tO = tS + TK;
+    auto record = [&](int i, PromptRec& r, int& head) {
+        const int pi = i / c.n_kv;
+        head = i - pi * c.n_kv;
+        const int4* at = reinterpret_cast<const int4*>(p.list + kRecWords * (1 + (long long)pi));
+        const int4 x = at[0], y = at[1];
+        r.b = x.x;
+        r.row0 = x.y;
+        r.n = x.z;
+        r.q_lo = x.w;
+        r.kv_len = y.x;
+        r.keys = y.y;
+        return max(1, (r.keys + TK - 1) / TK);   // an item without keys has one empty tile: its rows get 0
+    };
+    PromptRec r;
+    int head;
+    bool ok = true;
+
+    if (warp == 0) {
+        // ---- K tiles and scales: lanes 0-7 block `lane` of K, lanes 8-15 block lane - 8 of V (its scale only)
+        const int blk = lane & 7, which = (lane >> 3) & 1;
+        int g = 0;
+        for (int k = 0; ok; ++k) {
+            const int i = snake(k);
+            if (i >= n_items) break;
+            const int n_kt = record(i, r, head);
+            auto page_of = [&](int t) {
+                const int pos = t * TK + blk * kKv8Block;
+                return lane < 16 && pos < r.keys ? kv8_page_of(c, r.b, pos) : -1;
+            };
+            auto scale_of = [&](int t, int page) {   // -1: the block's keys are absent
+                const int pos = t * TK + blk * kKv8Block;
+                return page < 0 ? -1.f : c.scales[kv8_scale_at(c, page, which, head, pos & (c.page_size - 1))];
+            };
+            int page = page_of(0), page1 = n_kt > 1 ? page_of(1) : -1;
+            float s = scale_of(0, page);
+            for (int t = 0; t < n_kt && ok; ++t, ++g) {
+                // a tile ahead: its scale; two ahead: its page
+                const float s1 = t + 1 < n_kt ? scale_of(t + 1, page1) : 0.f;
+                const int page2 = t + 2 < n_kt ? page_of(t + 2) : -1;
+                const int st = g & 1;
+                if (g >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_KE + st), (uint32_t)((g >> 1) - 1) & 1u, abort_flag));
+                if (!ok) break;
+                const bool want = lane < 8 && page >= 0;
+                const int pos = t * TK + blk * kKv8Block;
+                if (lane < 8 && pos < r.keys && page < 0) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
+                if (lane < 16) sc[((g & 3) * 2 + which) * NB + blk] = s;
+                const int boxes = __popc(__ballot_sync(0xffffffffu, want));
+                __syncwarp();   // the scales are written
+                if (lane == 0) {
+                    *issued = g + 1;
+                    mbar_arrive(bar(C::B_SC + (g & 3)));
+                    if (boxes) mbar_expect_tx(bar(C::B_KF + st), (uint32_t)(boxes * kKv8Block * HD));
+                    else mbar_arrive(bar(C::B_KF + st));
+                }
+                __syncwarp();
+                if (want) {
+                    const long long row = kv8_code_at(c, page, 0, head, pos & (c.page_size - 1)) / HD;
+                    tma_load_2d(smem_u32(smem + C::OFF_K + st * C::KB + blk * kKv8Block * HD), &tmK, bar(C::B_KF + st), 0,
+                                (int)row);
+                }
+                page = page1;
+                page1 = page2;
+                s = s1;
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_e4m3_f32(TROWS, TK);
+            // A and B f16 (type code 0), D fp32, B transposed (MN-major), N = HD
+            constexpr uint32_t idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((uint32_t)(TROWS >> 4) << 24);
+            const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + C::OFF_K), sV = smem_u32(smem + C::OFF_V);
+            int g = 0, it = 0;
+            for (int k = 0; ok; ++k) {
+                const int i = snake(k);
+                if (i >= n_items) break;
+                const int n_kt = record(i, r, head);
+                ok = mbar_wait(bar(C::B_QF), (uint32_t)it & 1u, abort_flag);
+                for (int t = 0; t < n_kt && ok; ++t, ++g) {
+                    // S over the columns of P(g - 1): its PV is done
+                    ok = mbar_wait(bar(C::B_KF + (g & 1)), (uint32_t)(g >> 1) & 1u, abort_flag) &&
+                         (g == 0 || mbar_wait(bar(C::B_PV), (uint32_t)(g - 1) & 1u, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t kt = sK + (g & 1) * C::KB;
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int kk = 0; kk < HD / 32; ++kk) {
+                            const uint32_t qa = sQ + part * C::QB;
+                            const uint64_t ad = (HD == 128 ? sdesc_sw128(qa) : sdesc_sw64(qa)) + 2ull * kk;
+                            const uint64_t bd = (HD == 128 ? sdesc_sw128(kt) : sdesc_sw64(kt)) + 2ull * kk;
+                            tc_mma_f8(tS, ad, bd, idesc_s, part + kk > 0 ? 1u : 0u);
+                        }
+                    tc_commit(bar(C::B_SF));
+                    tc_commit(bar(C::B_KE + (g & 1)));
+                    if (t + 1 == n_kt) tc_commit(bar(C::B_QE));
+                    ok = mbar_wait(bar(C::B_PF), (uint32_t)g & 1u, abort_flag) &&
+                         mbar_wait(bar(C::B_VF), (uint32_t)g & 1u, abort_flag) &&
+                         (t > 0 || it == 0 || mbar_wait(bar(C::B_OF), (uint32_t)(it - 1) & 1u, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < TK / 16; ++ks)
+                        tc_mma_f16_ts(tO, tS + 8 * ks, sdesc_sw128_mn(sV + ks * 16 * 128, TK * 128, 1024), idesc_o,
+                                      (t > 0 || ks > 0) ? 1u : 0u);
+                    tc_commit(bar(C::B_PV));
+                }
+                ++it;
+            }
+            tc_commit(bar(C::B_IDLE));   // completes once every MMA of this thread has
+        }
+    } else if (warp < 6) {
+        // ---- softmax: one row a thread
+        const int quad = warp & 3;
+        const int row = quad * 32 + lane;
+        const int qi = row / p.G, hq = row - qi * p.G;
+        const uint32_t lS = tS + ((uint32_t)(quad * 32) << 16), lO = tO + ((uint32_t)(quad * 32) << 16);
+        int g = 0, it = 0;
+        for (int k = 0; ok; ++k) {
+            const int i = snake(k);
+            if (i >= n_items) break;
+            const int n_kt = record(i, r, head);
+            const bool row_ok = qi < p.QT && r.q_lo + qi < r.n;
+            const int limit = row_ok ? r.kv_len - r.n + r.q_lo + qi + 1 : 0;      // keys below it count
+            const int clear = r.kv_len - r.n + r.q_lo + 1;                        // ... for every row of the tile
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QS + (it & 1)), (uint32_t)(it >> 1) & 1u, abort_flag));
+            if (!ok) break;
+            const float q_unscale = qs[(it & 1) * TROWS + row] * p.scale_log2;
+            float m = -INFINITY, M = -INFINITY, l = 0.f;
+            for (int t = 0; t < n_kt && ok; ++t, ++g) {
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(bar(C::B_SC + (g & 3)), (uint32_t)(g >> 2) & 1u, abort_flag) &&
+                                    mbar_wait(bar(C::B_SF), (uint32_t)g & 1u, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                const float* ks = sc + (g & 3) * 2 * NB;
+                const float* vs = ks + NB;
+                const int j0 = t * TK;
+                bool whole = j0 + TK <= clear;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) whole &= ks[b] >= 0.f;
+                // pass 1: the row's maximum of s, and of s + log2 of the V scale
+                float mx = -INFINITY, Mx = -INFINITY;
+#pragma unroll
+                for (int ch = 0; ch < TK / 32; ++ch) {
+                    float a[32];
+                    tmem_ld32(lS + 32 * ch, a);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int b = 2 * ch + h;
+                        float top[2] = {-INFINITY, -INFINITY};
+                        if (whole) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) top[e & 1] = fmaxf(top[e & 1], a[16 * h + e]);
+                        } else if (ks[b] >= 0.f) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (j0 + 16 * b + e < limit) top[e & 1] = fmaxf(top[e & 1], a[16 * h + e]);
+                        }
+                        const float bm = fmaxf(top[0], top[1]);
+                        const float z = bm == -INFINITY ? bm : bm * (q_unscale * ks[b]);
+                        mx = fmaxf(mx, z);
+                        Mx = fmaxf(Mx, z + (float)((int)((__float_as_uint(vs[b]) >> 23) & 255u) - 127));
+                    }
+                }
+                const float mn = fmaxf(m, mx);
+                const float mr = mn == -INFINITY ? 0.f : mn;
+                l *= ex2(m - mr);
+                m = mn;
+                const float Mn = Mx > M + kSlack ? Mx : M;
+                const float Mr = Mn == -INFINITY ? 0.f : Mn;
+                const float alpha = ex2(M - Mr);   // exactly 1 while the reference stays
+                M = Mn;
+                // PV(g - 1) was done before S(g) was issued, so O is at rest
+                if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                    for (int ch = 0; ch < HD; ch += 32) {
+                        float o[32];
+                        tmem_ld32(lO + ch, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                        tmem_st32(lO + ch, o);
+                    }
+                }
+                // pass 2: weights, 32 keys at a time into columns 16 ch of S, all of which this row has read
+                float ls[2] = {0.f, 0.f};
+                const float up = mr - Mr + kUnit;
+#pragma unroll
+                for (int ch = 0; ch < TK / 32; ++ch) {
+                    float a[32];
+                    tmem_ld32(lS + 32 * ch, a);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int b = 2 * ch + h;
+                        const float coef = q_unscale * ks[b];
+                        const uint32_t vb = __float_as_uint(vs[b]);
+                        const float f = ex2(fminf(up + (float)((int)((vb >> 23) & 255u) - 127), 126.f)) *
+                                        __uint_as_float((vb & 0x807FFFFFu) | 0x3F800000u);
+                        if (whole) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) a[16 * h + e] = ex2(fmaf(a[16 * h + e], coef, -mr));
+                        } else {
+                            const bool there = ks[b] >= 0.f;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                a[16 * h + e] = there && j0 + 16 * b + e < limit ? ex2(fmaf(a[16 * h + e], coef, -mr)) : 0.f;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) ls[e & 1] += a[16 * h + e];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[8 * h + e] = pack_h2(a[16 * h + 2 * e] * f, a[16 * h + 2 * e + 1] * f);
+                    }
+                    tmem_st16_async(lS + 16 * ch, w);
+                }
+                l += ls[0] + ls[1];
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_PF));
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV), (uint32_t)(g - 1) & 1u, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            // O is in units of 2^(M - 11); l is 0 for a row that saw no key, and NaN when a score was
+            const float f = l == 0.f ? 0.f : exp2f((M == -INFINITY ? 0.f : M) - (m == -INFINITY ? 0.f : m)) / l;
+            bf16* dst = p.out + ((long long)(r.row0 + r.q_lo + qi) * p.nq + head * p.G + hq) * HD;
+#pragma unroll 1
+            for (int ch = 0; ch < HD; ch += 32) {
+                float o[32];
+                tmem_ld32(lO + ch, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = o[e] * 0x1p-11f * f;
+                if (row_ok) {
+                    if (p.v8) {
+                        st_global_32(dst + ch, pack8(o), pack8(o + 8));
+                        st_global_32(dst + ch + 16, pack8(o + 16), pack8(o + 24));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) *reinterpret_cast<uint4*>(dst + ch + e) = pack8(o + e);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_OF));
+            ++it;
+        }
+    } else {
+        // ---- Q of each item, then its V tiles
+        const int w = warp - 6, row = w * 32 + lane;
+        // V: this lane's codes are 16 of the row (key) kq of eight rows at a time
+        constexpr int HALVES = HD / 64;
+        const int kq = ((lane >> 2) & 1) + 2 * (lane >> 3), c16 = lane & 3;
+        int g = 0, it = 0;
+        for (int k = 0; ok; ++k) {
+            const int i = snake(k);
+            if (i >= n_items) break;
+            const int n_kt = record(i, r, head);
+            uint4 raw[4 * HALVES];
+            auto request = [&](int t) {   // keys 32 w .. 32 w + 31 of tile t
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int pos = t * TK + w * 32 + 16 * x;
+                    const int page = pos < r.keys ? kv8_page_of(c, r.b, pos) : -1;
+                    const uint8_t* src = c.codes + kv8_code_at(c, page < 0 ? 0 : page, 1, head, pos & (c.page_size - 1));
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h) {
+                            const int key = 8 * y + kq;
+                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                            if (page >= 0 && pos + key < r.keys)
+                                v = *reinterpret_cast<const uint4*>(src + key * HD + h * 64 + c16 * 16);
+                            raw[(2 * x + y) * HALVES + h] = v;
+                        }
+                }
+            };
+            {   // Q: hi and lo codes of one row a thread
+                const int qi = row / p.G, hq = row - qi * p.G;
+                const bool row_ok = qi < p.QT && r.q_lo + qi < r.n;
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(r.row0 + r.q_lo + (row_ok ? qi : 0)) * p.row_stride +
+                                                                  (long long)(head * p.G + (row_ok ? hq : 0)) * HD);
+                float mx = 0.f;
+                bool finite = true;
+#pragma unroll
+                for (int x = 0; x < HD / 8; ++x) {
+                    const uint4 u = row_ok ? src[x] : make_uint4(0u, 0u, 0u, 0u);
+                    float f[8];
+                    unpack8(u, f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        mx = fmaxf(mx, fabsf(f[e]));
+                        finite &= fabsf(f[e]) < INFINITY;
+                    }
+                }
+                const float s = __uint_as_float(kv8_scale_bits(__float_as_uint(fminf(mx, __uint_as_float(0x7F7F0000u)))));
+                const float inv = 1.0f / s;
+                if (it >= 1) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QE), (uint32_t)(it - 1) & 1u, abort_flag));
+                if (!ok) break;
+#pragma unroll
+                for (int x = 0; x < HD / 16; ++x) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint4 u = row_ok ? src[2 * x + y] : make_uint4(0u, 0u, 0u, 0u);
+                        float f[8];
+                        unpack8(u, f);
+#pragma unroll
+                        for (int e = 0; e < 8; e += 4) {
+                            uint32_t hw = 0, lw = 0;
+#pragma unroll
+                            for (int z = 0; z < 4; z += 2) {
+                                const float2 v = make_float2(f[e + z] * inv, f[e + z + 1] * inv);
+                                const uint32_t hc = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+                                const uint32_t h2 = e4m3x2_f16x2(hc);
+                                const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                                const uint32_t lc = __nv_cvt_float2_to_fp8x2(make_float2(v.x - hv.x, v.y - hv.y), __NV_SATFINITE, __NV_E4M3);
+                                hw |= hc << (8 * z);
+                                lw |= lc << (8 * z);
+                            }
+                            hi[2 * y + e / 4] = hw;
+                            lo[2 * y + e / 4] = lw;
+                        }
+                    }
+                    const int at = row * HD + ((HD == 128 ? x ^ (row & 7) : x ^ ((row >> 1) & 3)) << 4);
+                    *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(smem + C::QB + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                // a row with an infinity or a NaN gives NaN
+                qs[(it & 1) * TROWS + row] = finite ? s : __uint_as_float(0x7FC00000u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(C::B_QF));
+                    mbar_arrive(bar(C::B_QS + (it & 1)));
+                }
+            }
+            request(0);
+            for (int t = 0; t < n_kt; ++t, ++g) {
+                if (g >= 1) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV), (uint32_t)(g - 1) & 1u, abort_flag));
+                if (!ok) break;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h) {
+                            const uint4 v = raw[(2 * x + y) * HALVES + h];
+                            const int key = w * 32 + 16 * x + 8 * y + kq;
+                            uint8_t* at = smem + C::OFF_V + h * TK * 128 + key * 128;
+                            *reinterpret_cast<uint4*>(at + (((2 * c16) ^ (key & 7)) << 4)) =
+                                make_uint4(e4m3x2_f16x2(v.x & 0xFFFFu), e4m3x2_f16x2(v.x >> 16), e4m3x2_f16x2(v.y & 0xFFFFu),
+                                           e4m3x2_f16x2(v.y >> 16));
+                            *reinterpret_cast<uint4*>(at + (((2 * c16 + 1) ^ (key & 7)) << 4)) =
+                                make_uint4(e4m3x2_f16x2(v.z & 0xFFFFu), e4m3x2_f16x2(v.z >> 16), e4m3x2_f16x2(v.w & 0xFFFFu),
+                                           e4m3x2_f16x2(v.w >> 16));
+                        }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_VF));
+                if (t + 1 < n_kt) request(t + 1);
+            }
+            ++it;
+        }
+    }
+    if (!ok) {
+        *abort_flag = 1;
+        raise_error(c.err, HRA_DEVERR_WAIT_TIMEOUT);
+    }
+
+    // ---- teardown: on abort, let every requested copy and every MMA land first
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        volatile int never = 0;
+        if (*abort_flag)
+            for (int g = max(0, *issued - 2); g < *issued; ++g) (void)mbar_wait(bar(C::B_KF + (g & 1)), (uint32_t)(g >> 1) & 1u, &never);
+        (void)mbar_wait(bar(C::B_IDLE), 0u, &never);
+    }
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tS, 256);
+    }
+}
+
+template <int HD>
+cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int tiles, int short_rows, cudaStream_t st) {
+    using C = Cfg<HD>;
+    alignas(64) CUtensorMap map;
+    const long long rows = 2LL * a.view.n_pages * a.view.n_kv * a.view.page_size;
+    if (!make_map_codes(&map, a.view.codes, rows, HD, kKv8Block)) return cudaErrorInvalidValue;
+    static bool configured[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(kv8_prompt_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev] = true;
+    }
+    int32_t* list = reinterpret_cast<int32_t*>(a.scratch);
+    HRA_LAUNCH(kv8_schedule_kernel, dim3(1), dim3(1024), 0, st, a, G, QT, tiles, short_rows, list);
+    PromptArgs p{};
+    p.view = a.view;
+    p.q = a.q;
+    p.row_stride = a.row_stride;
+    p.out = a.out;
+    p.list = list;
+    p.scale_log2 = a.scale_log2;
+    p.nq = a.nq;
+    p.G = G;
+    p.QT = QT;
+    p.v8 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
+    const long long pairs = std::min((long long)tiles * a.batch, (long long)a.total_rows / QT + a.batch);
+    const int grid = (int)std::max<long long>(1, std::min(pairs * a.view.n_kv, 2LL * device_sm_count()));
+    HRA_LAUNCH(kv8_prompt_kernel<HD>, dim3(grid), dim3(kThreads), C::ALLOC, st, map, p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t kv8_prompt_scratch_bytes(int batch, int total_rows, int G) {
+    return ((size_t)total_rows / (TROWS / G) + (size_t)batch + 1) * kRecWords * sizeof(int32_t);
+}
+
+// The rows of the tensor map are counted in 32 bits.
+bool kv8_prompt_supported(const Kv8View& c) {
+    return 2LL * c.n_pages * c.n_kv * c.page_size < (1LL << 31);
+}
+
+cudaError_t launch_kv8_prompt(const Kv8AttnArgs& a, int short_rows, cudaStream_t st) {
+    const int G = a.nq / a.view.n_kv, QT = TROWS / G;
+    const int tiles = (a.max_new + QT - 1) / QT;
+    return a.view.head_dim == 128 ? launch_hd<128>(a, G, QT, tiles, short_rows, st)
+                                  : launch_hd<64>(a, G, QT, tiles, short_rows, st);
+}
+
+}  // namespace hra
