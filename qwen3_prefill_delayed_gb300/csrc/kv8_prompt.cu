@@ -58,7 +58,8 @@ struct Cfg {
     static constexpr int OFF_BAR = OFF_V + VB;
     static constexpr int OFF_SC = OFF_BAR + 256;        // [4][2][NB] scales of the last tiles
     static constexpr int OFF_QS = OFF_SC + 4 * 2 * NB * 4;   // [2][TROWS] q scales
-    static constexpr int SMEM = OFF_QS + 2 * TROWS * 4;
+    static constexpr int OFF_TH = OFF_QS + 2 * TROWS * 4;   // [4] whether a tile's blocks are all there
+    static constexpr int SMEM = OFF_TH + 16;
     static constexpr int ALLOC = SMEM + 1024;           // the base is aligned up to 1024 bytes
     // q_full, q_empty, k_full[2], k_empty[2], s_full, p_full, v_full, pv_done, o_free, idle, sc_full[4], qs_full[2]
     static constexpr int B_QF = 0, B_QE = 1, B_KF = 2, B_KE = 4, B_SF = 6, B_PF = 7, B_VF = 8, B_PV = 9, B_OF = 10,
@@ -111,6 +112,72 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
 }
 __device__ __forceinline__ int snake(int k) {
     return k * (int)gridDim.x + ((k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+}
+
+__device__ __forceinline__ float exponent_of(float s) { return (float)((int)((__float_as_uint(s) >> 23) & 255u) - 127); }
+
+// One row's tile of S, 32 columns at a time in a rolled loop: unrolled, the softmax warps wait for
+// instructions (a tile of straight code took 4600 clocks instead of 2400).  MASK: only keys below
+// `limit` of blocks that are there (scale >= 0) count.
+// mx: the maximum of s; Mx: the maximum of s + log2 of the block's V scale.
+template <bool MASK>
+__device__ __forceinline__ void max_pass(uint32_t lS, const float* ks, const float* vs, float q_unscale, int limit,
+                                         float& mx, float& Mx) {
+#pragma unroll 1
+    for (int ch = 0; ch < TK / 32; ++ch) {
+        float a[32];
+        tmem_ld32(lS + 32 * ch, a);
+        const float2 k2 = *reinterpret_cast<const float2*>(ks + 2 * ch), v2 = *reinterpret_cast<const float2*>(vs + 2 * ch);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float k = h ? k2.y : k2.x, v = h ? v2.y : v2.x;
+            if (MASK) {
+                const int n = k >= 0.f ? limit - 32 * ch - 16 * h : 0;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (e >= n) a[16 * h + e] = -INFINITY;
+            }
+            float top[2] = {a[16 * h], a[16 * h + 1]};
+#pragma unroll
+            for (int e = 2; e < 16; ++e) top[e & 1] = fmaxf(top[e & 1], a[16 * h + e]);
+            const float bm = fmaxf(top[0], top[1]);
+            const float z = MASK && bm == -INFINITY ? bm : bm * (q_unscale * k);
+            mx = fmaxf(mx, z);
+            Mx = fmaxf(Mx, z + exponent_of(v));
+        }
+    }
+}
+// The weights: l's terms 2^(s - mr) are returned summed; times the block's V scale and 2^(mr - Mr + 11)
+// (`up` its exponent) they go as f16 to columns 16 ch, which this row has read.
+template <bool MASK>
+__device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, const float* vs, float q_unscale, int limit,
+                                             float mr, float up) {
+    float ls[2] = {0.f, 0.f};
+#pragma unroll 1
+    for (int ch = 0; ch < TK / 32; ++ch) {
+        float a[32];
+        tmem_ld32(lS + 32 * ch, a);
+        const float2 k2 = *reinterpret_cast<const float2*>(ks + 2 * ch), v2 = *reinterpret_cast<const float2*>(vs + 2 * ch);
+        uint32_t w[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float k = h ? k2.y : k2.x, v = h ? v2.y : v2.x;
+            const float coef = q_unscale * k;
+            const float f = ex2(fminf(up + exponent_of(v), 126.f)) *
+                            __uint_as_float((__float_as_uint(v) & 0x807FFFFFu) | 0x3F800000u);
+            const int n = MASK ? (k >= 0.f ? limit - 32 * ch - 16 * h : 0) : 16;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                a[16 * h + e] = ex2(fmaf(a[16 * h + e], coef, -mr));
+                if (MASK && e >= n) a[16 * h + e] = 0.f;
+                ls[e & 1] += a[16 * h + e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[8 * h + e] = pack_h2(a[16 * h + 2 * e] * f, a[16 * h + 2 * e + 1] * f);
+        }
+        tmem_st16_async(lS + 16 * ch, w);
+    }
+    return ls[0] + ls[1];
 }
 
 // One CTA.  Counting sort of the non-empty (query tile, sequence) pairs by key tiles, most first.
@@ -186,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     volatile int* issued = reinterpret_cast<volatile int*>(slots + 2);
     float* sc = reinterpret_cast<float*>(smem + C::OFF_SC);
     float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
+    volatile int* there = reinterpret_cast<volatile int*>(smem + C::OFF_TH);
     auto bar = [&](int i) { return smem_u32(bars + i); };
     const Kv8View& c = p.view;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -256,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 if (lane < 8 && pos < r.keys && page < 0) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
                 if (lane < 16) sc[((g & 3) * 2 + which) * NB + blk] = s;
                 const int boxes = __popc(__ballot_sync(0xffffffffu, want));
+                if (lane == 0) there[g & 3] = boxes == NB;
                 __syncwarp();   // the scales are written
                 if (lane == 0) {
                     *issued = g + 1;
@@ -347,33 +416,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const float* ks = sc + (g & 3) * 2 * NB;
                 const float* vs = ks + NB;
                 const int j0 = t * TK;
-                bool whole = j0 + TK <= clear;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) whole &= ks[b] >= 0.f;
-                // pass 1: the row's maximum of s, and of s + log2 of the V scale
+                const bool whole = j0 + TK <= clear && there[g & 3] != 0;   // every key counts for every row
                 float mx = -INFINITY, Mx = -INFINITY;
-#pragma unroll
-                for (int ch = 0; ch < TK / 32; ++ch) {
-                    float a[32];
-                    tmem_ld32(lS + 32 * ch, a);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int b = 2 * ch + h;
-                        float top[2] = {-INFINITY, -INFINITY};
-                        if (whole) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) top[e & 1] = fmaxf(top[e & 1], a[16 * h + e]);
-                        } else if (ks[b] >= 0.f) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (j0 + 16 * b + e < limit) top[e & 1] = fmaxf(top[e & 1], a[16 * h + e]);
-                        }
-                        const float bm = fmaxf(top[0], top[1]);
-                        const float z = bm == -INFINITY ? bm : bm * (q_unscale * ks[b]);
-                        mx = fmaxf(mx, z);
-                        Mx = fmaxf(Mx, z + (float)((int)((__float_as_uint(vs[b]) >> 23) & 255u) - 127));
-                    }
-                }
+                if (whole)
+                    max_pass<false>(lS, ks, vs, q_unscale, 0, mx, Mx);
+                else
+                    max_pass<true>(lS, ks, vs, q_unscale, limit - j0, mx, Mx);
                 const float mn = fmaxf(m, mx);
                 const float mr = mn == -INFINITY ? 0.f : mn;
                 l *= ex2(m - mr);
@@ -393,38 +441,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                         tmem_st32(lO + ch, o);
                     }
                 }
-                // pass 2: weights, 32 keys at a time into columns 16 ch of S, all of which this row has read
-                float ls[2] = {0.f, 0.f};
                 const float up = mr - Mr + kUnit;
-#pragma unroll
-                for (int ch = 0; ch < TK / 32; ++ch) {
-                    float a[32];
-                    tmem_ld32(lS + 32 * ch, a);
-                    uint32_t w[16];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int b = 2 * ch + h;
-                        const float coef = q_unscale * ks[b];
-                        const uint32_t vb = __float_as_uint(vs[b]);
-                        const float f = ex2(fminf(up + (float)((int)((vb >> 23) & 255u) - 127), 126.f)) *
-                                        __uint_as_float((vb & 0x807FFFFFu) | 0x3F800000u);
-                        if (whole) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) a[16 * h + e] = ex2(fmaf(a[16 * h + e], coef, -mr));
-                        } else {
-                            const bool there = ks[b] >= 0.f;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                a[16 * h + e] = there && j0 + 16 * b + e < limit ? ex2(fmaf(a[16 * h + e], coef, -mr)) : 0.f;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) ls[e & 1] += a[16 * h + e];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) w[8 * h + e] = pack_h2(a[16 * h + 2 * e] * f, a[16 * h + 2 * e + 1] * f);
-                    }
-                    tmem_st16_async(lS + 16 * ch, w);
-                }
-                l += ls[0] + ls[1];
+                l += whole ? weight_pass<false>(lS, ks, vs, q_unscale, 0, mr, up)
+                           : weight_pass<true>(lS, ks, vs, q_unscale, limit - j0, mr, up);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
