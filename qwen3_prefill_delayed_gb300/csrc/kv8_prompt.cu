@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kThreads = 320;
 constexpr int TROWS = 128;
-constexpr int TK = 128;            // keys a tile
+constexpr int TK = 64;             // keys a tile
 constexpr int NB = TK / kKv8Block; // blocks a tile
 constexpr float kUnit = 11.f;      // log2 of the weight of the reference maximum
 constexpr float kSlack = 4.f;      // how far a maximum may pass the reference before it moves
@@ -48,23 +48,28 @@ struct PromptRec {   // 32 bytes: one (query tile, sequence) pair
 };
 constexpr int kRecWords = 8;
 
+constexpr int NK = 4;              // K stages
+constexpr int NSC = 8;             // tiles whose scales are held
+constexpr int NQS = 4;             // items whose q scales are held
+
 template <int HD>
 struct Cfg {
     static constexpr int QB = TROWS * HD;               // bytes of Q hi (and of lo)
     static constexpr int KB = TK * HD;                  // one K stage
-    static constexpr int VB = TK * HD * 2;              // V as f16
+    static constexpr int VB = TK * HD * 2;              // one of two stages of V as f16
     static constexpr int OFF_K = 2 * QB;
-    static constexpr int OFF_V = OFF_K + 2 * KB;
-    static constexpr int OFF_BAR = OFF_V + VB;
-    static constexpr int OFF_SC = OFF_BAR + 256;        // [4][2][NB] scales of the last tiles
-    static constexpr int OFF_QS = OFF_SC + 4 * 2 * NB * 4;   // [2][TROWS] q scales
-    static constexpr int OFF_TH = OFF_QS + 2 * TROWS * 4;   // [4] whether a tile's blocks are all there
-    static constexpr int SMEM = OFF_TH + 16;
+    static constexpr int OFF_V = OFF_K + NK * KB;
+    static constexpr int OFF_BAR = OFF_V + 2 * VB;
+    static constexpr int OFF_SC = OFF_BAR + 320;             // [NSC][2][NB] scales
+    static constexpr int OFF_QS = OFF_SC + NSC * 2 * NB * 4; // [NQS][TROWS] q scales
+    static constexpr int OFF_TH = OFF_QS + NQS * TROWS * 4;  // [NSC] whether a tile's blocks are all there
+    static constexpr int SMEM = OFF_TH + NSC * 4;
     static constexpr int ALLOC = SMEM + 1024;           // the base is aligned up to 1024 bytes
-    // q_full, q_empty, k_full[2], k_empty[2], s_full, p_full, v_full, pv_done, o_free, idle, sc_full[4], qs_full[2]
-    static constexpr int B_QF = 0, B_QE = 1, B_KF = 2, B_KE = 4, B_SF = 6, B_PF = 7, B_VF = 8, B_PV = 9, B_OF = 10,
-                         B_IDLE = 11, B_SC = 12, B_QS = 16, NBARS = 18;
-    static_assert(NBARS * 8 + 16 <= 256, "barrier area");
+    // tile g: K stage g % NK, S / P / V buffer g & 1, scales g % NSC; item it: q scales it % NQS
+    static constexpr int B_QF = 0, B_QE = 1, B_KF = 2, B_KE = B_KF + NK, B_SF = B_KE + NK, B_PF = B_SF + 2, B_VF = B_PF + 2,
+                         B_PV = B_VF + 2, B_OF = B_PV + 2, B_IDLE = B_OF + 1, B_SC = B_IDLE + 1, B_QS = B_SC + NSC,
+                         NBARS = B_QS + NQS;
+    static_assert(NBARS * 8 + 16 <= 320, "barrier area");
     static_assert(ALLOC <= 115712, "two CTAs an SM");
 };
 
@@ -92,6 +97,34 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tmov.b64 c, {%5, %6};\n\t"
+        "fma.rn.f32x2 %0, a, b, c;\n\t}"
+        : "=l"(d)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return make_float2(__uint_as_float((uint32_t)d), __uint_as_float((uint32_t)(d >> 32)));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tadd.rn.f32x2 %0, a, b;\n\t}"
+        : "=l"(d)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return make_float2(__uint_as_float((uint32_t)d), __uint_as_float((uint32_t)(d >> 32)));
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tmul.rn.f32x2 %0, a, b;\n\t}"
+        : "=l"(d)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return make_float2(__uint_as_float((uint32_t)d), __uint_as_float((uint32_t)(d >> 32)));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 // D[tmem] (+)= A[tmem, f16 pairs] * B[smem]
 __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
@@ -137,9 +170,9 @@ __device__ __forceinline__ void max_pass(uint32_t lS, const float* ks, const flo
                 for (int e = 0; e < 16; ++e)
                     if (e >= n) a[16 * h + e] = -INFINITY;
             }
-            float top[2] = {a[16 * h], a[16 * h + 1]};
+            float top[2] = {fmaxf(a[16 * h], a[16 * h + 1]), fmaxf(a[16 * h + 2], a[16 * h + 3])};
 #pragma unroll
-            for (int e = 2; e < 16; ++e) top[e & 1] = fmaxf(top[e & 1], a[16 * h + e]);
+            for (int e = 4; e < 16; e += 2) top[(e >> 1) & 1] = max3(top[(e >> 1) & 1], a[16 * h + e], a[16 * h + e + 1]);
             const float bm = fmaxf(top[0], top[1]);
             const float z = MASK && bm == -INFINITY ? bm : bm * (q_unscale * k);
             mx = fmaxf(mx, z);
@@ -152,7 +185,8 @@ __device__ __forceinline__ void max_pass(uint32_t lS, const float* ks, const flo
 template <bool MASK>
 __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, const float* vs, float q_unscale, int limit,
                                              float mr, float up) {
-    float ls[2] = {0.f, 0.f};
+    float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    const float2 neg = make_float2(-mr, -mr);
 #pragma unroll 1
     for (int ch = 0; ch < TK / 32; ++ch) {
         float a[32];
@@ -166,18 +200,23 @@ __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, const
             const float f = ex2(fminf(up + exponent_of(v), 126.f)) *
                             __uint_as_float((__float_as_uint(v) & 0x807FFFFFu) | 0x3F800000u);
             const int n = MASK ? (k >= 0.f ? limit - 32 * ch - 16 * h : 0) : 16;
+            const float2 coef2 = make_float2(coef, coef), f2 = make_float2(f, f);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                a[16 * h + e] = ex2(fmaf(a[16 * h + e], coef, -mr));
-                if (MASK && e >= n) a[16 * h + e] = 0.f;
-                ls[e & 1] += a[16 * h + e];
+            for (int e = 0; e < 16; e += 2) {
+                const float2 z = fma2(make_float2(a[16 * h + e], a[16 * h + e + 1]), coef2, neg);
+                float2 x = make_float2(ex2(z.x), ex2(z.y));
+                if (MASK) {
+                    if (e >= n) x.x = 0.f;
+                    if (e + 1 >= n) x.y = 0.f;
+                }
+                ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], x);
+                const float2 y = mul2(x, f2);
+                w[8 * h + e / 2] = pack_h2(y.x, y.y);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[8 * h + e] = pack_h2(a[16 * h + 2 * e] * f, a[16 * h + 2 * e + 1] * f);
         }
         tmem_st16_async(lS + 16 * ch, w);
     }
-    return ls[0] + ls[1];
+    return (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
 }
 
 // One CTA.  Counting sort of the non-empty (query tile, sequence) pairs by key tiles, most first.
@@ -261,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBARS; ++i) {
-            const bool four = i == C::B_QF || i == C::B_PF || i == C::B_VF || i == C::B_OF || i >= C::B_QS;
+            const bool four = i == C::B_QF || (i >= C::B_PF && i < C::B_PV) || i == C::B_OF || i >= C::B_QS;
             mbar_init(bar(i), four ? 4 : 1);
         }
         *abort_flag = 0;
@@ -276,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tS = slots[0], tO = tS + TK;
+    const uint32_t tS = slots[0], tO = tS + 2 * TK;   // two S buffers, then O
     auto record = [&](int i, PromptRec& r, int& head) {
         const int pi = i / c.n_kv;
         head = i - pi * c.n_kv;
@@ -295,8 +334,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     bool ok = true;
 
     if (warp == 0) {
-        // ---- K tiles and scales: lanes 0-7 block `lane` of K, lanes 8-15 block lane - 8 of V (its scale only)
-        const int blk = lane & 7, which = (lane >> 3) & 1;
+        // ---- K tiles and scales: lanes 0-3 block `lane` of K, lanes 4-7 block lane - 4 of V (its scale only)
+        const int blk = lane & (NB - 1), which = (lane / NB) & 1;
         int g = 0;
         for (int k = 0; ok; ++k) {
             const int i = snake(k);
@@ -304,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             const int n_kt = record(i, r, head);
             auto page_of = [&](int t) {
                 const int pos = t * TK + blk * kKv8Block;
-                return lane < 16 && pos < r.keys ? kv8_page_of(c, r.b, pos) : -1;
+                return lane < 2 * NB && pos < r.keys ? kv8_page_of(c, r.b, pos) : -1;
             };
             auto scale_of = [&](int t, int page) {   // -1: the block's keys are absent
                 const int pos = t * TK + blk * kKv8Block;
@@ -316,19 +355,19 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 // a tile ahead: its scale; two ahead: its page
                 const float s1 = t + 1 < n_kt ? scale_of(t + 1, page1) : 0.f;
                 const int page2 = t + 2 < n_kt ? page_of(t + 2) : -1;
-                const int st = g & 1;
-                if (g >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_KE + st), (uint32_t)((g >> 1) - 1) & 1u, abort_flag));
+                const int st = g % NK;
+                if (g >= NK) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_KE + st), (uint32_t)(g / NK - 1) & 1u, abort_flag));
                 if (!ok) break;
-                const bool want = lane < 8 && page >= 0;
+                const bool want = lane < NB && page >= 0;
                 const int pos = t * TK + blk * kKv8Block;
-                if (lane < 8 && pos < r.keys && page < 0) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
-                if (lane < 16) sc[((g & 3) * 2 + which) * NB + blk] = s;
+                if (lane < NB && pos < r.keys && page < 0) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
+                if (lane < 2 * NB) sc[((g % NSC) * 2 + which) * NB + blk] = s;
                 const int boxes = __popc(__ballot_sync(0xffffffffu, want));
-                if (lane == 0) there[g & 3] = boxes == NB;
+                if (lane == 0) there[g % NSC] = boxes == NB;
                 __syncwarp();   // the scales are written
                 if (lane == 0) {
                     *issued = g + 1;
-                    mbar_arrive(bar(C::B_SC + (g & 3)));
+                    mbar_arrive(bar(C::B_SC + g % NSC));
                     if (boxes) mbar_expect_tx(bar(C::B_KF + st), (uint32_t)(boxes * kKv8Block * HD));
                     else mbar_arrive(bar(C::B_KF + st));
                 }
@@ -354,14 +393,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const int i = snake(k);
                 if (i >= n_items) break;
                 const int n_kt = record(i, r, head);
-                ok = mbar_wait(bar(C::B_QF), (uint32_t)it & 1u, abort_flag);
-                for (int t = 0; t < n_kt && ok; ++t, ++g) {
-                    // S over the columns of P(g - 1): its PV is done
-                    ok = mbar_wait(bar(C::B_KF + (g & 1)), (uint32_t)(g >> 1) & 1u, abort_flag) &&
-                         (g == 0 || mbar_wait(bar(C::B_PV), (uint32_t)(g - 1) & 1u, abort_flag));
-                    if (!ok) break;
+                // S(x) into buffer x & 1, over P(x - 2): its PV is done
+                auto issue_s = [&](int x) {
+                    const int st = x % NK;
+                    if (!mbar_wait(bar(C::B_KF + st), (uint32_t)(x / NK) & 1u, abort_flag) ||
+                        (x >= 2 && !mbar_wait(bar(C::B_PV + (x & 1)), (uint32_t)((x >> 1) - 1) & 1u, abort_flag)))
+                        return false;
                     tc_fence_after();
-                    const uint32_t kt = sK + (g & 1) * C::KB;
+                    const uint32_t kt = sK + st * C::KB;
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -369,21 +408,31 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                             const uint32_t qa = sQ + part * C::QB;
                             const uint64_t ad = (HD == 128 ? sdesc_sw128(qa) : sdesc_sw64(qa)) + 2ull * kk;
                             const uint64_t bd = (HD == 128 ? sdesc_sw128(kt) : sdesc_sw64(kt)) + 2ull * kk;
-                            tc_mma_f8(tS, ad, bd, idesc_s, part + kk > 0 ? 1u : 0u);
+                            tc_mma_f8(tS + (x & 1) * TK, ad, bd, idesc_s, part + kk > 0 ? 1u : 0u);
                         }
-                    tc_commit(bar(C::B_SF));
-                    tc_commit(bar(C::B_KE + (g & 1)));
-                    if (t + 1 == n_kt) tc_commit(bar(C::B_QE));
-                    ok = mbar_wait(bar(C::B_PF), (uint32_t)g & 1u, abort_flag) &&
-                         mbar_wait(bar(C::B_VF), (uint32_t)g & 1u, abort_flag) &&
+                    tc_commit(bar(C::B_SF + (x & 1)));
+                    tc_commit(bar(C::B_KE + st));
+                    return true;
+                };
+                ok = mbar_wait(bar(C::B_QF), (uint32_t)it & 1u, abort_flag) && issue_s(g);
+                if (n_kt == 1) tc_commit(bar(C::B_QE));
+                for (int t = 0; t < n_kt && ok; ++t, ++g) {
+                    if (t + 1 < n_kt) {
+                        ok = issue_s(g + 1);
+                        if (!ok) break;
+                        if (t + 2 == n_kt) tc_commit(bar(C::B_QE));
+                    }
+                    const uint32_t ph = (uint32_t)(g >> 1) & 1u;
+                    ok = mbar_wait(bar(C::B_PF + (g & 1)), ph, abort_flag) && mbar_wait(bar(C::B_VF + (g & 1)), ph, abort_flag) &&
                          (t > 0 || it == 0 || mbar_wait(bar(C::B_OF), (uint32_t)(it - 1) & 1u, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
+                    const uint32_t tP = tS + (g & 1) * TK, v0 = sV + (g & 1) * C::VB;
 #pragma unroll
                     for (int ks = 0; ks < TK / 16; ++ks)
-                        tc_mma_f16_ts(tO, tS + 8 * ks, sdesc_sw128_mn(sV + ks * 16 * 128, TK * 128, 1024), idesc_o,
+                        tc_mma_f16_ts(tO, tP + 8 * ks, sdesc_sw128_mn(v0 + ks * 16 * 128, TK * 128, 1024), idesc_o,
                                       (t > 0 || ks > 0) ? 1u : 0u);
-                    tc_commit(bar(C::B_PV));
+                    tc_commit(bar(C::B_PV + (g & 1)));
                 }
                 ++it;
             }
@@ -394,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         const int quad = warp & 3;
         const int row = quad * 32 + lane;
         const int qi = row / p.G, hq = row - qi * p.G;
-        const uint32_t lS = tS + ((uint32_t)(quad * 32) << 16), lO = tO + ((uint32_t)(quad * 32) << 16);
+        const uint32_t lS0 = tS + ((uint32_t)(quad * 32) << 16), lO = tO + ((uint32_t)(quad * 32) << 16);
         int g = 0, it = 0;
         for (int k = 0; ok; ++k) {
             const int i = snake(k);
@@ -403,20 +452,21 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             const bool row_ok = qi < p.QT && r.q_lo + qi < r.n;
             const int limit = row_ok ? r.kv_len - r.n + r.q_lo + qi + 1 : 0;      // keys below it count
             const int clear = r.kv_len - r.n + r.q_lo + 1;                        // ... for every row of the tile
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QS + (it & 1)), (uint32_t)(it >> 1) & 1u, abort_flag));
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QS + it % NQS), (uint32_t)(it / NQS) & 1u, abort_flag));
             if (!ok) break;
-            const float q_unscale = qs[(it & 1) * TROWS + row] * p.scale_log2;
+            const float q_unscale = qs[(it % NQS) * TROWS + row] * p.scale_log2;
             float m = -INFINITY, M = -INFINITY, l = 0.f;
             for (int t = 0; t < n_kt && ok; ++t, ++g) {
                 ok = __all_sync(0xffffffffu,
-                                mbar_wait(bar(C::B_SC + (g & 3)), (uint32_t)(g >> 2) & 1u, abort_flag) &&
-                                    mbar_wait(bar(C::B_SF), (uint32_t)g & 1u, abort_flag));
+                                mbar_wait(bar(C::B_SC + g % NSC), (uint32_t)(g / NSC) & 1u, abort_flag) &&
+                                    mbar_wait(bar(C::B_SF + (g & 1)), (uint32_t)(g >> 1) & 1u, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
-                const float* ks = sc + (g & 3) * 2 * NB;
+                const uint32_t lS = lS0 + (g & 1) * TK;
+                const float* ks = sc + (g % NSC) * 2 * NB;
                 const float* vs = ks + NB;
                 const int j0 = t * TK;
-                const bool whole = j0 + TK <= clear && there[g & 3] != 0;   // every key counts for every row
+                const bool whole = j0 + TK <= clear && there[g % NSC] != 0;   // every key counts for every row
                 float mx = -INFINITY, Mx = -INFINITY;
                 if (whole)
                     max_pass<false>(lS, ks, vs, q_unscale, 0, mx, Mx);
@@ -430,8 +480,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const float Mr = Mn == -INFINITY ? 0.f : Mn;
                 const float alpha = ex2(M - Mr);   // exactly 1 while the reference stays
                 M = Mn;
-                // PV(g - 1) was done before S(g) was issued, so O is at rest
                 if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV + ((g - 1) & 1)), (uint32_t)((g - 1) >> 1) & 1u, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll 1
                     for (int ch = 0; ch < HD; ch += 32) {
                         float o[32];
@@ -447,10 +499,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_PF));
+                if (lane == 0) mbar_arrive(bar(C::B_PF + (g & 1)));
             }
             if (!ok) break;
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV), (uint32_t)(g - 1) & 1u, abort_flag));
+            // the commit of an item's last PV covers the ones before it
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV + ((g - 1) & 1)), (uint32_t)((g - 1) >> 1) & 1u, abort_flag));
             if (!ok) break;
             tc_fence_after();
             // O is in units of 2^(M - 11); l is 0 for a row that saw no key, and NaN when a score was
@@ -480,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     } else {
         // ---- Q of each item, then its V tiles
         const int w = warp - 6, row = w * 32 + lane;
-        // V: this lane's codes are 16 of the row (key) kq of eight rows at a time
+        // V: keys 16 w .. 16 w + 15 of a tile, one block; this lane's codes are 16 of the rows kq and 8 + kq
         constexpr int HALVES = HD / 64;
         const int kq = ((lane >> 2) & 1) + 2 * (lane >> 3), c16 = lane & 3;
         int g = 0, it = 0;
@@ -488,25 +541,26 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             const int i = snake(k);
             if (i >= n_items) break;
             const int n_kt = record(i, r, head);
-            uint4 raw[4 * HALVES];
-            auto request = [&](int t) {   // keys 32 w .. 32 w + 31 of tile t
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int pos = t * TK + w * 32 + 16 * x;
-                    const int page = pos < r.keys ? kv8_page_of(c, r.b, pos) : -1;
-                    const uint8_t* src = c.codes + kv8_code_at(c, page < 0 ? 0 : page, 1, head, pos & (c.page_size - 1));
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-#pragma unroll
-                        for (int h = 0; h < HALVES; ++h) {
-                            const int key = 8 * y + kq;
-                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                            if (page >= 0 && pos + key < r.keys)
-                                v = *reinterpret_cast<const uint4*>(src + key * HD + h * 64 + c16 * 16);
-                            raw[(2 * x + y) * HALVES + h] = v;
-                        }
-                }
+            uint4 raw[2][2 * HALVES];   // the codes of two tiles on their way
+            auto page_of = [&](int t) {
+                const int pos = t * TK + w * kKv8Block;
+                return pos < r.keys ? kv8_page_of(c, r.b, pos) : -1;
             };
+            auto request = [&](uint4(&v)[2 * HALVES], int t, int page) {
+                const int pos = t * TK + w * kKv8Block;
+                const uint8_t* src = c.codes + kv8_code_at(c, page < 0 ? 0 : page, 1, head, pos & (c.page_size - 1));
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h) {
+                        const int key = 8 * y + kq;
+                        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                        if (page >= 0 && pos + key < r.keys)
+                            u = *reinterpret_cast<const uint4*>(src + key * HD + h * 64 + c16 * 16);
+                        v[y * HALVES + h] = u;
+                    }
+            };
+            int page = page_of(0), page1 = page_of(1);
             {   // Q: hi and lo codes of one row a thread
                 const int qi = row / p.G, hq = row - qi * p.G;
                 const bool row_ok = qi < p.QT && r.q_lo + qi < r.n;
@@ -514,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                                                                   (long long)(head * p.G + (row_ok ? hq : 0)) * HD);
                 float mx = 0.f;
                 bool finite = true;
-#pragma unroll
+#pragma unroll 4
                 for (int x = 0; x < HD / 8; ++x) {
                     const uint4 u = row_ok ? src[x] : make_uint4(0u, 0u, 0u, 0u);
                     float f[8];
@@ -529,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const float inv = 1.0f / s;
                 if (it >= 1) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QE), (uint32_t)(it - 1) & 1u, abort_flag));
                 if (!ok) break;
-#pragma unroll
+#pragma unroll 2
                 for (int x = 0; x < HD / 16; ++x) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
@@ -559,38 +613,45 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     *reinterpret_cast<uint4*>(smem + C::QB + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 // a row with an infinity or a NaN gives NaN
-                qs[(it & 1) * TROWS + row] = finite ? s : __uint_as_float(0x7FC00000u);
+                qs[(it % NQS) * TROWS + row] = finite ? s : __uint_as_float(0x7FC00000u);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(bar(C::B_QF));
-                    mbar_arrive(bar(C::B_QS + (it & 1)));
+                    mbar_arrive(bar(C::B_QS + it % NQS));
                 }
             }
-            request(0);
-            for (int t = 0; t < n_kt; ++t, ++g) {
-                if (g >= 1) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV), (uint32_t)(g - 1) & 1u, abort_flag));
-                if (!ok) break;
+            request(raw[0], 0, page);
+            request(raw[1], 1, page1);
+            page = page_of(2);
+            // tile t from v, tile t + 2 into it
+            auto turn = [&](uint4(&v)[2 * HALVES], int t) {
+                if (g >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV + (g & 1)), (uint32_t)((g >> 1) - 1) & 1u, abort_flag));
+                if (!ok) return;
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int y = 0; y < 2; ++y)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-#pragma unroll
-                        for (int h = 0; h < HALVES; ++h) {
-                            const uint4 v = raw[(2 * x + y) * HALVES + h];
-                            const int key = w * 32 + 16 * x + 8 * y + kq;
-                            uint8_t* at = smem + C::OFF_V + h * TK * 128 + key * 128;
-                            *reinterpret_cast<uint4*>(at + (((2 * c16) ^ (key & 7)) << 4)) =
-                                make_uint4(e4m3x2_f16x2(v.x & 0xFFFFu), e4m3x2_f16x2(v.x >> 16), e4m3x2_f16x2(v.y & 0xFFFFu),
-                                           e4m3x2_f16x2(v.y >> 16));
-                            *reinterpret_cast<uint4*>(at + (((2 * c16 + 1) ^ (key & 7)) << 4)) =
-                                make_uint4(e4m3x2_f16x2(v.z & 0xFFFFu), e4m3x2_f16x2(v.z >> 16), e4m3x2_f16x2(v.w & 0xFFFFu),
-                                           e4m3x2_f16x2(v.w >> 16));
-                        }
+                    for (int h = 0; h < HALVES; ++h) {
+                        const uint4 u = v[y * HALVES + h];
+                        const int key = w * kKv8Block + 8 * y + kq;
+                        uint8_t* at = smem + C::OFF_V + (g & 1) * C::VB + h * TK * 128 + key * 128;
+                        *reinterpret_cast<uint4*>(at + (((2 * c16) ^ (key & 7)) << 4)) =
+                            make_uint4(e4m3x2_f16x2(u.x & 0xFFFFu), e4m3x2_f16x2(u.x >> 16), e4m3x2_f16x2(u.y & 0xFFFFu),
+                                       e4m3x2_f16x2(u.y >> 16));
+                        *reinterpret_cast<uint4*>(at + (((2 * c16 + 1) ^ (key & 7)) << 4)) =
+                            make_uint4(e4m3x2_f16x2(u.z & 0xFFFFu), e4m3x2_f16x2(u.z >> 16), e4m3x2_f16x2(u.w & 0xFFFFu),
+                                       e4m3x2_f16x2(u.w >> 16));
+                    }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_VF));
-                if (t + 1 < n_kt) request(t + 1);
+                if (lane == 0) mbar_arrive(bar(C::B_VF + (g & 1)));
+                if (t + 2 < n_kt) request(v, t + 2, page);
+                if (t + 3 < n_kt) page = page_of(t + 3);
+                ++g;
+            };
+            for (int t = 0; t < n_kt && ok; t += 2) {
+                turn(raw[0], t);
+                if (t + 1 < n_kt && ok) turn(raw[1], t + 1);
             }
             ++it;
         }
@@ -606,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     if (threadIdx.x == 0) {
         volatile int never = 0;
         if (*abort_flag)
-            for (int g = max(0, *issued - 2); g < *issued; ++g) (void)mbar_wait(bar(C::B_KF + (g & 1)), (uint32_t)(g >> 1) & 1u, &never);
+            for (int g = max(0, *issued - NK); g < *issued; ++g) (void)mbar_wait(bar(C::B_KF + g % NK), (uint32_t)(g / NK) & 1u, &never);
         (void)mbar_wait(bar(C::B_IDLE), 0u, &never);
     }
     __syncthreads();
