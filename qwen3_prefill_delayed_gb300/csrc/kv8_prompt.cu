@@ -316,19 +316,30 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tS = slots[0], tO = tS + 2 * TK;   // two S buffers, then O
-    auto record = [&](int i, PromptRec& r, int& head) {
-        const int pi = i / c.n_kv;
-        head = i - pi * c.n_kv;
-        const int4* at = reinterpret_cast<const int4*>(p.list + kRecWords * (1 + (long long)pi));
-        const int4 x = at[0], y = at[1];
-        r.b = x.x;
-        r.row0 = x.y;
-        r.n = x.z;
-        r.q_lo = x.w;
-        r.kv_len = y.x;
-        r.keys = y.y;
+    // Items k = 0, 1, ... of this CTA; the next one's record is on its way while one is worked on.
+    int4 next_x = make_int4(0, 0, 0, 0), next_y = next_x;
+    auto fetch = [&](int k) {
+        const int i = snake(k);
+        if (i < n_items) {
+            const int4* at = reinterpret_cast<const int4*>(p.list + kRecWords * (1 + (long long)(i / c.n_kv)));
+            next_x = at[0];
+            next_y = at[1];
+        }
+    };
+    auto item = [&](int k, PromptRec& r, int& head) {   // key tiles of item k, 0 when there is none
+        const int i = snake(k);
+        if (i >= n_items) return 0;
+        head = i % c.n_kv;
+        r.b = next_x.x;
+        r.row0 = next_x.y;
+        r.n = next_x.z;
+        r.q_lo = next_x.w;
+        r.kv_len = next_y.x;
+        r.keys = next_y.y;
+        fetch(k + 1);
         return max(1, (r.keys + TK - 1) / TK);   // an item without keys has one empty tile: its rows get 0
     };
+    fetch(0);
     PromptRec r;
     int head;
     bool ok = true;
@@ -338,9 +349,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         const int blk = lane & (NB - 1), which = (lane / NB) & 1;
         int g = 0;
         for (int k = 0; ok; ++k) {
-            const int i = snake(k);
-            if (i >= n_items) break;
-            const int n_kt = record(i, r, head);
+            const int n_kt = item(k, r, head);
+            if (n_kt == 0) break;
             auto page_of = [&](int t) {
                 const int pos = t * TK + blk * kKv8Block;
                 return lane < 2 * NB && pos < r.keys ? kv8_page_of(c, r.b, pos) : -1;
@@ -390,9 +400,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + C::OFF_K), sV = smem_u32(smem + C::OFF_V);
             int g = 0, it = 0;
             for (int k = 0; ok; ++k) {
-                const int i = snake(k);
-                if (i >= n_items) break;
-                const int n_kt = record(i, r, head);
+                const int n_kt = item(k, r, head);
+                if (n_kt == 0) break;
                 // S(x) into buffer x & 1, over P(x - 2): its PV is done
                 auto issue_s = [&](int x) {
                     const int st = x % NK;
@@ -446,9 +455,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         const uint32_t lS0 = tS + ((uint32_t)(quad * 32) << 16), lO = tO + ((uint32_t)(quad * 32) << 16);
         int g = 0, it = 0;
         for (int k = 0; ok; ++k) {
-            const int i = snake(k);
-            if (i >= n_items) break;
-            const int n_kt = record(i, r, head);
+            const int n_kt = item(k, r, head);
+            if (n_kt == 0) break;
             const bool row_ok = qi < p.QT && r.q_lo + qi < r.n;
             const int limit = row_ok ? r.kv_len - r.n + r.q_lo + qi + 1 : 0;      // keys below it count
             const int clear = r.kv_len - r.n + r.q_lo + 1;                        // ... for every row of the tile
@@ -532,15 +540,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         }
     } else {
         // ---- Q of each item, then its V tiles
-        const int w = warp - 6, row = w * 32 + lane;
+        const int w = warp - 6;
         // V: keys 16 w .. 16 w + 15 of a tile, one block; this lane's codes are 16 of the rows kq and 8 + kq
         constexpr int HALVES = HD / 64;
         const int kq = ((lane >> 2) & 1) + 2 * (lane >> 3), c16 = lane & 3;
         int g = 0, it = 0;
         for (int k = 0; ok; ++k) {
-            const int i = snake(k);
-            if (i >= n_items) break;
-            const int n_kt = record(i, r, head);
+            const int n_kt = item(k, r, head);
+            if (n_kt == 0) break;
             uint4 raw[2][2 * HALVES];   // the codes of two tiles on their way
             auto page_of = [&](int t) {
                 const int pos = t * TK + w * kKv8Block;
@@ -561,59 +568,60 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     }
             };
             int page = page_of(0), page1 = page_of(1);
-            {   // Q: hi and lo codes of one row a thread
-                const int qi = row / p.G, hq = row - qi * p.G;
-                const bool row_ok = qi < p.QT && r.q_lo + qi < r.n;
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(r.row0 + r.q_lo + (row_ok ? qi : 0)) * p.row_stride +
-                                                                  (long long)(head * p.G + (row_ok ? hq : 0)) * HD);
-                float mx = 0.f;
-                bool finite = true;
-#pragma unroll 4
-                for (int x = 0; x < HD / 8; ++x) {
-                    const uint4 u = row_ok ? src[x] : make_uint4(0u, 0u, 0u, 0u);
-                    float f[8];
-                    unpack8(u, f);
+            {   // Q: hi and lo codes of rows 32 w .. 32 w + 31, LPR lanes a row, 16 elements a lane
+                constexpr int LPR = HD / 16, RPP = 32 / LPR;
+                const int x = lane % LPR;
+#pragma unroll 1
+                for (int p0 = 0; p0 < LPR; p0 += 4) {
+                    uint4 u[4][2];   // four passes in flight; the first ones while the item before still runs
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        mx = fmaxf(mx, fabsf(f[e]));
-                        finite &= fabsf(f[e]) < INFINITY;
-                    }
-                }
-                const float s = __uint_as_float(kv8_scale_bits(__float_as_uint(fminf(mx, __uint_as_float(0x7F7F0000u)))));
-                const float inv = 1.0f / s;
-                if (it >= 1) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QE), (uint32_t)(it - 1) & 1u, abort_flag));
-                if (!ok) break;
-#pragma unroll 2
-                for (int x = 0; x < HD / 16; ++x) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const uint4 u = row_ok ? src[2 * x + y] : make_uint4(0u, 0u, 0u, 0u);
-                        float f[8];
-                        unpack8(u, f);
-#pragma unroll
-                        for (int e = 0; e < 8; e += 4) {
-                            uint32_t hw = 0, lw = 0;
-#pragma unroll
-                            for (int z = 0; z < 4; z += 2) {
-                                const float2 v = make_float2(f[e + z] * inv, f[e + z + 1] * inv);
-                                const uint32_t hc = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-                                const uint32_t h2 = e4m3x2_f16x2(hc);
-                                const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                                const uint32_t lc = __nv_cvt_float2_to_fp8x2(make_float2(v.x - hv.x, v.y - hv.y), __NV_SATFINITE, __NV_E4M3);
-                                hw |= hc << (8 * z);
-                                lw |= lc << (8 * z);
-                            }
-                            hi[2 * y + e / 4] = hw;
-                            lo[2 * y + e / 4] = lw;
+                    for (int y = 0; y < 4; ++y) {
+                        const int row = w * 32 + (p0 + y) * RPP + lane / LPR;
+                        const int qi = row / p.G, hq = row - qi * p.G;
+                        u[y][0] = u[y][1] = make_uint4(0u, 0u, 0u, 0u);
+                        if (qi < p.QT && r.q_lo + qi < r.n) {
+                            const uint4* src = reinterpret_cast<const uint4*>(
+                                p.q + (long long)(r.row0 + r.q_lo + qi) * p.row_stride + (long long)(head * p.G + hq) * HD + 16 * x);
+                            u[y][0] = src[0];
+                            u[y][1] = src[1];
                         }
                     }
-                    const int at = row * HD + ((HD == 128 ? x ^ (row & 7) : x ^ ((row >> 1) & 3)) << 4);
-                    *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(smem + C::QB + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    if (p0 == 0 && it >= 1)
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QE), (uint32_t)(it - 1) & 1u, abort_flag));
+                    if (!ok) break;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int row = w * 32 + (p0 + y) * RPP + lane / LPR;
+                        const uint32_t in[8] = {u[y][0].x, u[y][0].y, u[y][0].z, u[y][0].w,
+                                                u[y][1].x, u[y][1].y, u[y][1].z, u[y][1].w};
+                        // the row's largest magnitude: bf16 bits without their sign order like the values
+                        uint32_t top = 0u;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) top = __vmaxu2(top, in[e] & 0x7FFF7FFFu);
+                        top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+                        for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const float s = __uint_as_float(kv8_scale_bits(min(top, 0x7F7Fu) << 16));
+                        const float inv = 1.0f / s;
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 v = make_float2(__uint_as_float(in[e] << 16) * inv, __uint_as_float(in[e] & 0xFFFF0000u) * inv);
+                            const uint32_t hc = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+                            const uint32_t h2 = e4m3x2_f16x2(hc);
+                            const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                            const uint32_t lc = __nv_cvt_float2_to_fp8x2(make_float2(v.x - hv.x, v.y - hv.y), __NV_SATFINITE, __NV_E4M3);
+                            hi[e >> 1] = e & 1 ? hi[e >> 1] | hc << 16 : hc;
+                            lo[e >> 1] = e & 1 ? lo[e >> 1] | lc << 16 : lc;
+                        }
+                        const int at = row * HD + ((HD == 128 ? x ^ (row & 7) : x ^ ((row >> 1) & 3)) << 4);
+                        *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(smem + C::QB + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        // a row with an infinity or a NaN gives NaN
+                        if (x == 0) qs[(it % NQS) * TROWS + row] = top < 0x7F80u ? s : __uint_as_float(0x7FC00000u);
+                    }
                 }
-                // a row with an infinity or a NaN gives NaN
-                qs[(it % NQS) * TROWS + row] = finite ? s : __uint_as_float(0x7FC00000u);
+                if (!ok) break;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
