@@ -16,6 +16,11 @@
 //           the output's bf16 rounding of 2^-8.  The sum 2^(s_j - m) is kept in fp32 from the unrounded
 //           values, with its own maximum m: a block whose V is zero or tiny still counts in it.
 //
+// The work is a line of units of 64 keys, sequence by sequence and head by head; every CTA takes an equal share
+// of it, wherever the borders between sequences fall, so ragged lengths cost nothing and one long sequence
+// spreads over the whole GPU.  An item (sequence, head) that lies inside one share is written at once; the parts
+// of the others go to scratch as fp32 sums with their (m, l, M), and a second kernel joins them in order.
+//
 // A warp takes 16 keys (one block) at a time straight from global memory into fragments: the order of
 // the dims inside a dot product and of the dims among the output rows is free, so it is chosen such
 // that every lane's share of a block is a few whole 16-byte pieces that only this lane reads.
@@ -38,21 +43,24 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kStages = 3;      // blocks of 16 keys in flight per warp
+constexpr int kUnit = kWarps * kKv8Block;   // keys of a unit: one block a warp
+constexpr int kMaxBatch = 2048;             // sequences whose units fit the CTA's table
+constexpr int kMinShare = 4;    // units of a share at least: below it the join costs more than it spreads
+constexpr int kWholeUnits = 8;  // items of at most so many units go whole, one a CTA, and need no second kernel
 constexpr int kShortRows = 16;  // (position, head) rows of a kv head that fit this kernel's tile
 constexpr int kSerialKeys = 2048;   // keys that a short sequence may walk alone among prompts
 constexpr float kPScale = 15.f; // log2 of the largest p
 
-__device__ __forceinline__ void cp_async_ca(uint32_t dst, const void* src, int bytes) {
-    if (bytes == 4)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+// 4 or 8 bytes; src_bytes = 0 zero-fills the destination
+template <int N>
+__device__ __forceinline__ void cp_async_ca(uint32_t dst, const void* src, int src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(src_bytes) : "memory");
 }
-// two E4M3 codes (low 16 bits of w) -> two f16
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
-    uint32_t d;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((unsigned short)w));
-    return d;
+// four E4M3 codes -> two pairs of f16
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -66,7 +74,11 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float ex2(float x) { return exp2f(x); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // Bytes of one lane's share of a block of 16 keys, and where its parts lie in a stage.
 template <int HD>
@@ -78,10 +90,30 @@ struct Piece {
     static constexpr int STAGE = OFF_S + 32 * 8;  // the block's two scales, one copy a lane
 };
 
-// One CTA = one (sequence, tile of query positions, kv head); its four warps take every fourth block
-// of 16 keys and join their (m, l, M, O) through shared memory.  NG x 8 rows a tile.
+// Parts of split items: CTA c has slots 2 c (the item that its share begins in) and 2 c + 1 (the one it ends in).
+// A slot: [ROWS][HD] sums, then [ROWS][3] (m, l, M).  desc[c]: the item whose first part is CTA c's slot 2 c + 1 and
+// the last CTA that has a part of it.
+struct SplitDesc {
+    int row0, n, head, last;   // n: tokens; row0 < 0: no item begins in this share and goes on behind it
+};
 template <int HD, int NG>
-__global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const Kv8AttnArgs a, int G, int QT, int max_rows) {
+struct Slot {
+    static constexpr int ROWS = 8 * NG;
+    static constexpr int FLOATS = ROWS * (HD + 3);
+};
+
+struct SplitArgs {
+    Kv8AttnArgs a;
+    SplitDesc* desc;
+    float* parts;
+    int G, max_rows;   // sequences with at most max_rows (position, head) rows a kv head
+    int whole;         // one item a CTA: blockIdx = (tile, head, sequence)
+    int QT;
+};
+
+// NG x 8 rows of (position, head) pairs.
+template <int HD, int NG>
+__global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArgs s) {
     pdl_launch();
     pdl_wait();
     using Pc = Piece<HD>;
@@ -89,294 +121,452 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const Kv8AttnA
     constexpr int DT = HD / 16;       // 16-dim tiles of O^T
     constexpr int ROWS = 8 * NG;
     extern __shared__ __align__(16) uint8_t sm[];
+    __shared__ int before[kMaxBatch + 1];   // units of one head of the sequences before
+    __shared__ int warp_total[kWarps];
+    const Kv8AttnArgs& a = s.a;
     const Kv8View& c = a.view;
+    const int G = s.G;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const int tile = blockIdx.x, head = blockIdx.y, b = blockIdx.z;
-    int row0, n;
-    kv8_rows(a.cu, b, a.total_rows, row0, n);
-    if (tile * QT >= n || n * G > max_rows) return;
-    const long long room = (long long)c.max_pages << c.page_shift;
-    int kv_len = a.kv_len[b];
-    if (kv_len < 0 || kv_len > room) {
-        if (threadIdx.x == 0) raise_error(c.err, HRA_DEVERR_POS_RANGE);
-        kv_len = kv_len < 0 ? 0 : (int)room;
-    }
-    if (n > a.max_new && threadIdx.x == 0) raise_error(c.err, HRA_DEVERR_POS_RANGE);
-    const int q_lo = tile * QT, q_n = min(QT, n - q_lo);
-    const int keys = max(0, kv_len - n + q_lo + q_n);   // positions below the tile's last row's
-    const int n_blk = (keys + kKv8Block - 1) / kKv8Block;
+    const int room = c.max_pages << c.page_shift;
+    auto length = [&](int b) { return min(room, max(0, a.kv_len[b])); };
 
-    // ---- q fragments: f16, each row scaled by a power of two
-    uint32_t qa[KS][2 * NG];
-    float q_unscale[NG];
-    int limit[NG];             // keys below this one count for the row
-#pragma unroll
-    for (int x = 0; x < NG; ++x) {
-        const int r = g + 8 * x, qi = r / G, hq = r - qi * G;
-        const bool ok = qi < q_n;
-        limit[x] = ok ? min(keys, kv_len - n + q_lo + qi + 1) : 0;
-        const bf16* src = a.q + (long long)(row0 + q_lo + (ok ? qi : 0)) * a.row_stride + (long long)(head * G + hq) * HD;
-        float f[HD / 64][16];
-        float mx = 0.f;
-#pragma unroll
-        for (int h = 0; h < HD / 64; ++h) {
-            uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-            if (ok) {
-                u0 = *reinterpret_cast<const uint4*>(src + h * 64 + t4 * 16);
-                u1 = *reinterpret_cast<const uint4*>(src + h * 64 + t4 * 16 + 8);
+    // ---- this CTA's share
+    long long u = 0, u_end = 1;
+    long long share = 0;
+    if (!s.whole) {
+        // units of the sequences, summed up front: consecutive sequences a thread, then across threads
+        const int per = (a.batch + kWarps * 32 - 1) / (kWarps * 32);
+        const int b0 = threadIdx.x * per;
+        int mine = 0;
+        for (int i = 0; i < per; ++i) {
+            const int b = b0 + i;
+            int units = 0;
+            if (b < a.batch) {
+                int row0, n;
+                kv8_rows(a.cu, b, a.total_rows, row0, n);
+                // a sequence with new tokens but no keys has one unit: its rows get 0
+                if (n > 0 && n * G <= s.max_rows) units = max(1, (length(b) + kUnit - 1) / kUnit);
+                before[b] = units;
             }
-            float lo[8], hi[8];
-            unpack8(u0, lo);
-            unpack8(u1, hi);
+            mine += units;
+        }
+        int incl = mine;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                f[h][e] = lo[e];
-                f[h][8 + e] = hi[e];
-                mx = fmaxf(mx, fmaxf(fabsf(lo[e]), fabsf(hi[e])));
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) warp_total[warp] = incl;
+        __syncthreads();
+        int run = incl - mine;
+        for (int w = 0; w < warp; ++w) run += warp_total[w];
+        for (int i = 0; i < per; ++i) {
+            const int b = b0 + i;
+            if (b < a.batch) {
+                const int v = before[b];
+                before[b] = run;
+                run += v;
             }
         }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // 2^(14 - floor(log2 mx)), its exponent kept inside fp32's normal range
-        const int ex = min(254, max(14, (int)(__float_as_uint(mx) >> 23)));
-        const float mul = __uint_as_float((uint32_t)(268 - ex) << 23);
-        q_unscale[x] = __uint_as_float((uint32_t)max(1, ex - 14) << 23) * a.scale_log2;
-#pragma unroll
-        for (int h = 0; h < HD / 64; ++h)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                qa[h * 4 + q][x] = pack_h2(f[h][4 * q] * mul, f[h][4 * q + 1] * mul);
-                qa[h * 4 + q][NG + x] = pack_h2(f[h][4 * q + 2] * mul, f[h][4 * q + 3] * mul);
-            }
-    }
-
-    float o[NG][DT][4];
-#pragma unroll
-    for (int x = 0; x < NG; ++x)
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[x][d][0] = o[x][d][1] = o[x][d][2] = o[x][d][3] = 0.f;
-    float m[NG], l[NG], M[NG];
-#pragma unroll
-    for (int x = 0; x < NG; ++x) {
-        m[x] = M[x] = -INFINITY;
-        l[x] = 0.f;
+        if (threadIdx.x == kWarps * 32 - 1) before[a.batch] = run;
+        __syncthreads();
+        const long long all = (long long)before[a.batch] * c.n_kv;
+        share = max((long long)kMinShare, (all + gridDim.x - 1) / gridDim.x);
+        u = blockIdx.x * share;
+        u_end = min(all, u + share);
+        if (threadIdx.x == 0) s.desc[blockIdx.x].row0 = -1;
+        if (u >= u_end) return;
     }
 
     const uint32_t queue = smem_u32(sm) + warp * kStages * Pc::STAGE;
-    // this lane's pieces of block `blk` into stage st; keys at or past `keys`, and blocks whose page is
-    // not in the pool, are zero-filled and masked below
+    const long long page_bytes = 2LL * c.n_kv * c.page_size * HD;
+    const int v_bytes = c.n_kv * c.page_size * HD;   // from a block's K to its V: below 2^24
+    const int page_scales = 2 * c.n_kv * (c.page_size / kKv8Block), v_scales = page_scales / 2;
     bool bad_page = false;
-    auto request = [&](int blk, int st) {
-        const int pos0 = blk * kKv8Block;
-        const int page = kv8_page_of(c, b, pos0);
-        bad_page |= page < 0;
-        const int slot0 = pos0 & (c.page_size - 1);
-        const int pg = page < 0 ? 0 : page;
-        const int left = page < 0 ? 0 : keys - pos0;          // keys of this block that count
-        const uint8_t* kb = c.codes + kv8_code_at(c, pg, 0, head, slot0);
-        const uint8_t* vb = c.codes + kv8_code_at(c, pg, 1, head, slot0);
-        const uint32_t base = queue + st * Pc::STAGE;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int h = 0; h < Pc::KP; ++h)
-                cp_async16(base + ((i * Pc::KP + h) * 32 + lane) * 16, kb + (g + 8 * i) * HD + h * 64 + t4 * 16,
-                           g + 8 * i < left ? 16u : 0u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = 2 * t4 + (i & 1) + 8 * (i >> 1);
-            const uint32_t dst = base + Pc::OFF_V + (i * 32 + lane) * Pc::VB;
-            if (HD == 128) {
-                cp_async16(dst, vb + key * HD + g * 16, key < left ? 16u : 0u);
-            } else {
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(vb + key * HD + g * 8),
-                             "r"(key < left ? 8 : 0)
-                             : "memory");
-            }
-        }
-        const uint32_t sc = base + Pc::OFF_S + lane * 8;
-        cp_async_ca(sc, c.scales + kv8_scale_at(c, pg, 0, head, slot0), 4);
-        cp_async_ca(sc + 4, c.scales + kv8_scale_at(c, pg, 1, head, slot0), 4);
-    };
 
-    // ---- the warp's blocks: warp, warp + 4, ...
-    int ahead = warp;
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-        if (ahead < n_blk) request(ahead, s);
-        cp_async_commit();
-        ahead += kWarps;
-    }
-    int st = 0, st_in = kStages - 1;
-    for (int blk = warp; blk < n_blk; blk += kWarps) {
-        if (ahead < n_blk) request(ahead, st_in);
-        cp_async_commit();
-        ahead += kWarps;
-        st_in = st_in + 1 == kStages ? 0 : st_in + 1;
-        cp_async_wait<kStages - 1>();
-        const uint8_t* sp = sm + warp * kStages * Pc::STAGE + st * Pc::STAGE;
-        st = st + 1 == kStages ? 0 : st + 1;
-        const float2 sc = *reinterpret_cast<const float2*>(sp + Pc::OFF_S + lane * 8);
-
-        float s[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-#pragma unroll
-            for (int h = 0; h < Pc::KP; ++h) {
-                const uint4 w = *reinterpret_cast<const uint4*>(sp + ((i * Pc::KP + h) * 32 + lane) * 16);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t b0 = e4m3x2_f16x2(ww[q] & 0xFFFFu), b1 = e4m3x2_f16x2(ww[q] >> 16);
-                    if (NG == 1)
-                        mma_f16(s[i], qa[h * 4 + q][0], 0u, qa[h * 4 + q][1], 0u, b0, b1);
-                    else
-                        mma_f16(s[i], qa[h * 4 + q][0], qa[h * 4 + q][NG - 1], qa[h * 4 + q][NG], qa[h * 4 + q][2 * NG - 1],
-                                b0, b1);
-                }
+    while (u < u_end) {
+        // ---- the segment: units [i0, i1) of item (b, head), tile of query positions q_lo ..
+        int b, head, i0 = 0, i1, q_lo = 0, row0, n;
+        bool first_part = true, last_part = true;
+        if (s.whole) {
+            b = blockIdx.z;
+            head = blockIdx.y;
+            q_lo = blockIdx.x * s.QT;
+            kv8_rows(a.cu, b, a.total_rows, row0, n);
+            if (q_lo >= n || n * G > s.max_rows) return;
+            i1 = 1 << 30;
+            u = u_end;
+        } else {
+            const int ub = (int)(u / c.n_kv);
+            int lo = 0, hi = a.batch;      // the last b with before[b] * n_kv <= u
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (before[mid] <= ub) lo = mid;
+                else hi = mid;
             }
+            b = lo;
+            const int units = before[b + 1] - before[b];
+            const int at = (int)(u - (long long)before[b] * c.n_kv);
+            head = at / units;
+            i0 = at - head * units;
+            i1 = (int)min((long long)units, i0 + (u_end - u));
+            first_part = i0 == 0;
+            last_part = i1 == units;
+            u += i1 - i0;
+            kv8_rows(a.cu, b, a.total_rows, row0, n);
         }
-        // a page outside the pool: its keys are absent
-        const bool there = kv8_page_of(c, b, blk * kKv8Block) >= 0;
-        const uint32_t vbits = __float_as_uint(sc.y);
-        const float ev = (float)((int)((vbits >> 23) & 255u) - 127);
-        const float vm = __uint_as_float((vbits & 0x807FFFFFu) | 0x3F800000u);
-        uint32_t pb[NG][2];
-        float al[NG];
-        bool moved = false;
+        const int kv_len = length(b);
+        if (head == 0 && threadIdx.x == 0 && first_part && q_lo == 0 &&
+            (a.kv_len[b] != kv_len || n > a.max_new))
+            raise_error(c.err, HRA_DEVERR_POS_RANGE);
+        const int q_n = min(s.QT, n - q_lo);
+        const int keys = max(0, kv_len - n + q_lo + q_n);   // positions below the tile's last row's
+        const int blk1 = min((keys + kKv8Block - 1) / kKv8Block, i1 >= (1 << 28) ? 1 << 28 : i1 * kWarps);
+        int blk = i0 * kWarps + warp;
+
+        // ---- page numbers two blocks of this warp ahead of the requests, requests kStages - 1 ahead of the use
+        const int32_t* table = c.table + (long long)b * c.max_pages;
+        auto page_of = [&](int x) {
+            if (x >= blk1) return -1;
+            const int page = table[x * kKv8Block >> c.page_shift];   // x * 16 < keys <= max_pages * page_size
+            return page >= 0 && page < c.n_pages ? page : -1;
+        };
+        const uint8_t* head_codes = c.codes + (long long)head * c.page_size * HD;
+        const float* head_scales = c.scales + head * (c.page_size / kKv8Block);
+        // this lane's pieces of block x into stage st: keys at or past `keys`, and blocks whose page is not in the
+        // pool (their scales become 0), are zero-filled and masked below
+        auto request = [&](int x, int page, int st) {
+            bad_page |= page < 0;
+            const int slot0 = (x * kKv8Block) & (c.page_size - 1);
+            const int pg = max(page, 0);
+            const int left = page < 0 ? 0 : keys - x * kKv8Block;          // keys of this block that count
+            const uint8_t* kb = head_codes + pg * page_bytes + slot0 * HD;
+            const uint8_t* vb = kb + v_bytes;
+            const uint32_t base = queue + st * Pc::STAGE;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int h = 0; h < Pc::KP; ++h)
+                    cp_async16(base + ((i * Pc::KP + h) * 32 + lane) * 16, kb + (g + 8 * i) * HD + h * 64 + t4 * 16,
+                               g + 8 * i < left ? 16u : 0u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = 2 * t4 + (i & 1) + 8 * (i >> 1);
+                const uint32_t dst = base + Pc::OFF_V + (i * 32 + lane) * Pc::VB;
+                if (HD == 128)
+                    cp_async16(dst, vb + key * HD + g * 16, key < left ? 16u : 0u);
+                else
+                    cp_async_ca<8>(dst, vb + key * HD + g * 8, key < left ? 8 : 0);
+            }
+            const uint32_t at = base + Pc::OFF_S + lane * 8;
+            const float* sp = head_scales + (long long)pg * page_scales + (slot0 / kKv8Block);
+            cp_async_ca<4>(at, sp, page < 0 ? 0 : 4);
+            cp_async_ca<4>(at + 4, sp + v_scales, page < 0 ? 0 : 4);
+        };
+        int ahead = blk;
+        int page0 = page_of(ahead), page1 = page_of(ahead + kWarps);
+#pragma unroll
+        for (int st = 0; st < kStages - 1; ++st) {
+            const int page2 = page_of(ahead + 2 * kWarps);
+            if (ahead < blk1) request(ahead, page0, st);
+            cp_async_commit();
+            ahead += kWarps;
+            page0 = page1;
+            page1 = page2;
+        }
+
+        // ---- q fragments: f16, each row scaled by a power of two
+        uint32_t qa[KS][2 * NG];
+        float q_unscale[NG];
+        int limit[NG];             // keys below this one count for the row
 #pragma unroll
         for (int x = 0; x < NG; ++x) {
-            const float coef = q_unscale[x] * sc.x;
-            float z[4];
-            float mx = -INFINITY;
+            const int r = g + 8 * x, qi = r / G, hq = r - qi * G;
+            const bool ok = qi < q_n;
+            limit[x] = ok ? min(keys, kv_len - n + q_lo + qi + 1) : 0;
+            const bf16* src = a.q + (long long)(row0 + q_lo + (ok ? qi : 0)) * a.row_stride + (long long)(head * G + hq) * HD;
+            uint4 raw[HD / 64][2];
+            uint32_t top = 0u;     // bf16 bits without their sign order like the values
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int key = blk * kKv8Block + (e >> 1) * 8 + 2 * t4 + (e & 1);
-                z[e] = there && key < limit[x] ? s[e >> 1][2 * x + (e & 1)] * coef : -INFINITY;
-                mx = fmaxf(mx, z[e]);
+            for (int h = 0; h < HD / 64; ++h) {
+                raw[h][0] = raw[h][1] = make_uint4(0u, 0u, 0u, 0u);
+                if (ok) {
+                    raw[h][0] = *reinterpret_cast<const uint4*>(src + h * 64 + t4 * 16);
+                    raw[h][1] = *reinterpret_cast<const uint4*>(src + h * 64 + t4 * 16 + 8);
+                }
             }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float mn = fmaxf(m[x], mx), Mn = fmaxf(M[x], mx + ev);
-            const float mr = mn == -INFINITY ? 0.f : mn, Mr = Mn == -INFINITY ? 0.f : Mn;
-            l[x] *= ex2(m[x] - mr);
-            al[x] = ex2(M[x] - Mr);
-            moved |= al[x] != 1.f;
-            m[x] = mn;
-            M[x] = Mn;
-            const float off = ev + kPScale - Mr;
-            float w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                l[x] += ex2(z[e] - mr);
-                w[e] = ex2(z[e] + off) * vm;
-            }
-            pb[x][0] = pack_h2(w[0], w[1]);
-            pb[x][1] = pack_h2(w[2], w[3]);
-        }
-        if (__any_sync(0xffffffffu, moved)) {   // O's columns are rows 2 t, 2 t + 1 (+ 8 x)
+            for (int h = 0; h < HD / 64; ++h)
 #pragma unroll
-            for (int x = 0; x < NG; ++x) {
-                const float a0 = __shfl_sync(0xffffffffu, al[x], 8 * t4), a1 = __shfl_sync(0xffffffffu, al[x], 8 * t4 + 4);
+                for (int e = 0; e < 2; ++e) {
+                    const uint4 w = raw[h][e];
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                                 __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+                }
+            top = max(top & 0xFFFFu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^(14 - floor(log2 of it)), its exponent kept inside fp32's normal range
+            const int ex = min(254, max(14, (int)(top >> 7)));
+            const float mul = __uint_as_float((uint32_t)(268 - ex) << 23);
+            q_unscale[x] = __uint_as_float((uint32_t)max(1, ex - 14) << 23) * a.scale_log2;
 #pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    o[x][d][0] *= a0;
-                    o[x][d][1] *= a1;
-                    o[x][d][2] *= a0;
-                    o[x][d][3] *= a1;
+            for (int h = 0; h < HD / 64; ++h) {
+                float f[16], f1[8];
+                unpack8(raw[h][0], f1);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = f1[e];
+                unpack8(raw[h][1], f1);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[8 + e] = f1[e];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    qa[h * 4 + q][x] = pack_h2(f[4 * q] * mul, f[4 * q + 1] * mul);
+                    qa[h * 4 + q][NG + x] = pack_h2(f[4 * q + 2] * mul, f[4 * q + 3] * mul);
                 }
             }
         }
-        // O^T += V^T P^T: words of keys 2t and 2t + 1 interleave into pairs of one dim
-        uint32_t vw[4][HD / 32];
+
+        float o[NG][DT][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint8_t* at = sp + Pc::OFF_V + (i * 32 + lane) * Pc::VB;
-            if (HD == 128) {
-                const uint4 w = *reinterpret_cast<const uint4*>(at);
-                vw[i][0] = w.x;
-                vw[i][1] = w.y;
-                vw[i][HD / 32 - 2] = w.z;
-                vw[i][HD / 32 - 1] = w.w;
-            } else {
-                const uint2 w = *reinterpret_cast<const uint2*>(at);
-                vw[i][0] = w.x;
-                vw[i][1] = w.y;
-            }
+        for (int x = 0; x < NG; ++x)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[x][d][0] = o[x][d][1] = o[x][d][2] = o[x][d][3] = 0.f;
+        float m[NG], l[NG], M[NG];
+#pragma unroll
+        for (int x = 0; x < NG; ++x) {
+            m[x] = M[x] = -INFINITY;
+            l[x] = 0.f;
         }
+
+        int st = 0, st_in = kStages - 1;
+#pragma unroll 1
+        for (; blk < blk1; blk += kWarps) {
+            {
+                const int page2 = page_of(ahead + 2 * kWarps);
+                if (ahead < blk1) request(ahead, page0, st_in);
+                page0 = page1;
+                page1 = page2;
+            }
+            cp_async_commit();
+            ahead += kWarps;
+            st_in = st_in + 1 == kStages ? 0 : st_in + 1;
+            cp_async_wait<kStages - 1>();
+            const uint8_t* sp = sm + warp * kStages * Pc::STAGE + st * Pc::STAGE;
+            st = st + 1 == kStages ? 0 : st + 1;
+            const float2 sc = *reinterpret_cast<const float2*>(sp + Pc::OFF_S + lane * 8);
+
+            float sv[2][4];
 #pragma unroll
-        for (int j = 0; j < HD / 32; ++j) {
-            const uint32_t p0 = __byte_perm(vw[0][j], vw[1][j], 0x5140), p1 = __byte_perm(vw[0][j], vw[1][j], 0x7362);
-            const uint32_t p2 = __byte_perm(vw[2][j], vw[3][j], 0x5140), p3 = __byte_perm(vw[2][j], vw[3][j], 0x7362);
-            const uint32_t a0 = e4m3x2_f16x2(p0 & 0xFFFFu), a1 = e4m3x2_f16x2(p0 >> 16);
-            const uint32_t a2 = e4m3x2_f16x2(p2 & 0xFFFFu), a3 = e4m3x2_f16x2(p2 >> 16);
-            const uint32_t c0 = e4m3x2_f16x2(p1 & 0xFFFFu), c1 = e4m3x2_f16x2(p1 >> 16);
-            const uint32_t c2 = e4m3x2_f16x2(p3 & 0xFFFFu), c3 = e4m3x2_f16x2(p3 >> 16);
+            for (int i = 0; i < 2; ++i) {
+                sv[i][0] = sv[i][1] = sv[i][2] = sv[i][3] = 0.f;
+#pragma unroll
+                for (int h = 0; h < Pc::KP; ++h) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(sp + ((i * Pc::KP + h) * 32 + lane) * 16);
+                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t b0, b1;
+                        e4m3x4_f16x4(ww[q], b0, b1);
+                        if (NG == 1)
+                            mma_f16(sv[i], qa[h * 4 + q][0], 0u, qa[h * 4 + q][1], 0u, b0, b1);
+                        else
+                            mma_f16(sv[i], qa[h * 4 + q][0], qa[h * 4 + q][NG - 1], qa[h * 4 + q][NG],
+                                    qa[h * 4 + q][2 * NG - 1], b0, b1);
+                    }
+                }
+            }
+            const bool there = sc.x > 0.f;   // 0: a page outside the pool, whose keys are absent
+            const uint32_t vbits = __float_as_uint(sc.y);
+            const float ev = (float)((int)((vbits >> 23) & 255u) - 127);
+            const float vm = __uint_as_float((vbits & 0x807FFFFFu) | 0x3F800000u);
+            uint32_t pb[NG][2];
+            float al[NG];
+            bool moved = false;
 #pragma unroll
             for (int x = 0; x < NG; ++x) {
-                mma_f16(o[x][2 * j], a0, a1, a2, a3, pb[x][0], pb[x][1]);
-                mma_f16(o[x][2 * j + 1], c0, c1, c2, c3, pb[x][0], pb[x][1]);
+                const float coef = q_unscale[x] * sc.x;
+                const int lim = there ? limit[x] - blk * kKv8Block - 2 * t4 : 0;   // of this lane's keys 0, 1, 8, 9
+                float z[4];
+                float mx = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    z[e] = (e >> 1) * 8 + (e & 1) < lim ? sv[e >> 1][2 * x + (e & 1)] * coef : -INFINITY;
+                    mx = fmaxf(mx, z[e]);
+                }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float mn = fmaxf(m[x], mx), Mn = fmaxf(M[x], mx + ev);
+                const float mr = mn == -INFINITY ? 0.f : mn, Mr = Mn == -INFINITY ? 0.f : Mn;
+                al[x] = ex2(M[x] - Mr);
+                l[x] *= ex2(m[x] - mr);
+                moved |= al[x] != 1.f;
+                m[x] = mn;
+                M[x] = Mn;
+                const float off = ev + kPScale - Mr;
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    l[x] += ex2(z[e] - mr);
+                    w[e] = ex2(z[e] + off) * vm;
+                }
+                pb[x][0] = pack_h2(w[0], w[1]);
+                pb[x][1] = pack_h2(w[2], w[3]);
+            }
+            if (__any_sync(0xffffffffu, moved)) {   // O's columns are rows 2 t, 2 t + 1 (+ 8 x)
+#pragma unroll
+                for (int x = 0; x < NG; ++x) {
+                    const float a0 = __shfl_sync(0xffffffffu, al[x], 8 * t4), a1 = __shfl_sync(0xffffffffu, al[x], 8 * t4 + 4);
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) {
+                        o[x][d][0] *= a0;
+                        o[x][d][1] *= a1;
+                        o[x][d][2] *= a0;
+                        o[x][d][3] *= a1;
+                    }
+                }
+            }
+            // O^T += V^T P^T: words of keys 2t and 2t + 1 interleave into pairs of one dim
+            uint32_t vw[4][HD / 32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t* at = sp + Pc::OFF_V + (i * 32 + lane) * Pc::VB;
+                if (HD == 128) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(at);
+                    vw[i][0] = w.x;
+                    vw[i][1] = w.y;
+                    vw[i][HD / 32 - 2] = w.z;
+                    vw[i][HD / 32 - 1] = w.w;
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(at);
+                    vw[i][0] = w.x;
+                    vw[i][1] = w.y;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < HD / 32; ++j) {
+                uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
+                e4m3x4_f16x4(__byte_perm(vw[0][j], vw[1][j], 0x5140), a0, a1);
+                e4m3x4_f16x4(__byte_perm(vw[2][j], vw[3][j], 0x5140), a2, a3);
+                e4m3x4_f16x4(__byte_perm(vw[0][j], vw[1][j], 0x7362), c0, c1);
+                e4m3x4_f16x4(__byte_perm(vw[2][j], vw[3][j], 0x7362), c2, c3);
+#pragma unroll
+                for (int x = 0; x < NG; ++x) {
+                    mma_f16(o[x][2 * j], a0, a1, a2, a3, pb[x][0], pb[x][1]);
+                    mma_f16(o[x][2 * j + 1], c0, c1, c2, c3, pb[x][0], pb[x][1]);
+                }
             }
         }
-    }
-    cp_async_wait<0>();
-    if (bad_page) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
-    __syncthreads();   // the queues are free: the warps' results go over them
+        cp_async_wait<0>();
+        __syncthreads();   // the queues are free: the warps' results go over them
 
-    // ---- join the four warps: [warp][row][HD] sums and [warp][row] (m, l, M)
-    float* s_o = reinterpret_cast<float*>(sm);
-    float* s_m = s_o + kWarps * ROWS * HD;
+        // ---- join the four warps: [warp][row][HD] sums and [warp][row] (m, l, M)
+        float* s_o = reinterpret_cast<float*>(sm);
+        float* s_m = s_o + kWarps * ROWS * HD;
 #pragma unroll
-    for (int x = 0; x < NG; ++x) {
-        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-        if (t4 == 0) {
-            float* at = s_m + (warp * ROWS + g + 8 * x) * 3;
-            at[0] = m[x];
-            at[1] = l[x];
-            at[2] = M[x];
-        }
+        for (int x = 0; x < NG; ++x) {
+            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+            if (t4 == 0) {
+                float* at = s_m + (warp * ROWS + g + 8 * x) * 3;
+                at[0] = m[x];
+                at[1] = l[x];
+                at[2] = M[x];
+            }
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            // rows 2 t, 2 t + 1 (+ 8 x); dims g * (HD / 8) + 2 d, + 1
-            float* at = s_o + (warp * ROWS + 2 * t4 + 8 * x) * HD + g * (HD / 8) + 2 * d;
-            *reinterpret_cast<float2*>(at) = make_float2(o[x][d][0], o[x][d][2]);
-            *reinterpret_cast<float2*>(at + HD) = make_float2(o[x][d][1], o[x][d][3]);
+            for (int d = 0; d < DT; ++d) {
+                // rows 2 t, 2 t + 1 (+ 8 x); dims g * (HD / 8) + 2 d, + 1
+                float* at = s_o + (warp * ROWS + 2 * t4 + 8 * x) * HD + g * (HD / 8) + 2 * d;
+                *reinterpret_cast<float2*>(at) = make_float2(o[x][d][0], o[x][d][2]);
+                *reinterpret_cast<float2*>(at + HD) = make_float2(o[x][d][1], o[x][d][3]);
+            }
         }
+        __syncthreads();
+        const bool whole = first_part && last_part;
+        float* part = s.parts + (2LL * blockIdx.x + (first_part ? 1 : 0)) * Slot<HD, NG>::FLOATS;
+        for (int i = threadIdx.x; i < q_n * G * (HD / 2); i += kWarps * 32) {
+            const int r = i / (HD / 2), d = (i - r * (HD / 2)) * 2;
+            const int qi = r / G, hq = r - qi * G;
+            float mm = -INFINITY, MM = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                mm = fmaxf(mm, s_m[(w * ROWS + r) * 3]);
+                MM = fmaxf(MM, s_m[(w * ROWS + r) * 3 + 2]);
+            }
+            const float mr = mm == -INFINITY ? 0.f : mm, Mr = MM == -INFINITY ? 0.f : MM;
+            float L = 0.f, x0 = 0.f, x1 = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float* at = s_m + (w * ROWS + r) * 3;
+                L += at[1] * ex2(at[0] - mr);
+                const float f = ex2(at[2] - Mr);
+                const float2 ov = *reinterpret_cast<const float2*>(s_o + (w * ROWS + r) * HD + d);
+                x0 += ov.x * f;
+                x1 += ov.y * f;
+            }
+            if (whole) {
+                // L is 0 for a row that saw no key, and NaN when a score was
+                const float f = L == 0.f ? 0.f : exp2f(Mr - mr) / L;
+                bf16* dst = a.out + ((long long)(row0 + q_lo + qi) * a.nq + head * G + hq) * HD + d;
+                *reinterpret_cast<uint32_t*>(dst) = pack_bf2(x0 * 0x1p-15f * f, x1 * 0x1p-15f * f);
+            } else {
+                *reinterpret_cast<float2*>(part + r * HD + d) = make_float2(x0, x1);
+                if (d == 0) {
+                    float* at = part + ROWS * HD + r * 3;
+                    at[0] = mm;
+                    at[1] = L;
+                    at[2] = MM;
+                }
+            }
+        }
+        if (first_part && !last_part && threadIdx.x == 0) {
+            const long long end = (long long)before[b] * c.n_kv + (long long)(head + 1) * (before[b + 1] - before[b]);
+            s.desc[blockIdx.x] = SplitDesc{row0, q_n, head, (int)((end - 1) / share)};
+        }
+        __syncthreads();   // the results are read: the queues may be filled again
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < q_n * G * (HD / 2); i += kWarps * 32) {
-        const int r = i / (HD / 2), d = (i - r * (HD / 2)) * 2;
-        const int qi = r / G, hq = r - qi * G;
-        float mm = -INFINITY, MM = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            mm = fmaxf(mm, s_m[(w * ROWS + r) * 3]);
-            MM = fmaxf(MM, s_m[(w * ROWS + r) * 3 + 2]);
+    if (bad_page) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
+}
+
+// One CTA per share: the item that begins in it and goes on behind it.
+template <int HD, int NG>
+__global__ void __launch_bounds__(128) kv8_join_kernel(const SplitArgs s) {
+    pdl_launch();
+    pdl_wait();
+    constexpr int ROWS = 8 * NG;
+    const int c0 = blockIdx.x;
+    const SplitDesc d = s.desc[c0];
+    if (d.row0 < 0) return;
+    auto slot = [&](int c) { return s.parts + (2LL * c + (c == c0 ? 1 : 0)) * Slot<HD, NG>::FLOATS; };
+    for (int i = threadIdx.x; i < d.n * s.G * (HD / 2); i += 128) {
+        const int r = i / (HD / 2), dd = (i - r * (HD / 2)) * 2;
+        const int qi = r / s.G, hq = r - qi * s.G;
+        float m = -INFINITY, M = -INFINITY, L = 0.f, x0 = 0.f, x1 = 0.f;
+#pragma unroll 4
+        for (int c = c0; c <= d.last; ++c) {
+            const float* p = slot(c);
+            const float* q = p + ROWS * HD + r * 3;
+            const float2 ov = *reinterpret_cast<const float2*>(p + r * HD + dd);
+            const float mn = fmaxf(m, q[0]), Mn = fmaxf(M, q[2]);
+            const float mr = mn == -INFINITY ? 0.f : mn, Mr = Mn == -INFINITY ? 0.f : Mn;
+            const float f0 = ex2(M - Mr), f1 = ex2(q[2] - Mr);
+            L = L * ex2(m - mr) + q[1] * ex2(q[0] - mr);
+            x0 = x0 * f0 + ov.x * f1;
+            x1 = x1 * f0 + ov.y * f1;
+            m = mn;
+            M = Mn;
         }
-        const float mr = mm == -INFINITY ? 0.f : mm, Mr = MM == -INFINITY ? 0.f : MM;
-        float L = 0.f, x0 = 0.f, x1 = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float* at = s_m + (w * ROWS + r) * 3;
-            L += at[1] * ex2(at[0] - mr);
-            const float f = ex2(at[2] - Mr);
-            const float2 ov = *reinterpret_cast<const float2*>(s_o + (w * ROWS + r) * HD + d);
-            x0 += ov.x * f;
-            x1 += ov.y * f;
-        }
-        // L is 0 for a row that saw no key, and NaN when a score was
-        const float f = L == 0.f ? 0.f : ex2(Mr - mr) / L;
-        x0 = x0 * 0x1p-15f * f;
-        x1 = x1 * 0x1p-15f * f;
-        bf16* dst = a.out + ((long long)(row0 + q_lo + qi) * a.nq + head * G + hq) * HD + d;
-        *reinterpret_cast<uint32_t*>(dst) = pack_bf2(x0, x1);
+        const float mr = m == -INFINITY ? 0.f : m, Mr = M == -INFINITY ? 0.f : M;
+        const float f = L == 0.f ? 0.f : exp2f(Mr - mr) / L;
+        bf16* dst = s.a.out + ((long long)(d.row0 + qi) * s.a.nq + d.head * s.G + hq) * HD + dd;
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf2(x0 * 0x1p-15f * f, x1 * 0x1p-15f * f);
     }
 }
 
+int split_grid() { return 3 * device_sm_count(); }
+
 template <int HD, int NG>
-cudaError_t launch_ng(const Kv8AttnArgs& a, int G, int QT, int tiles, int max_rows, cudaStream_t st) {
+cudaError_t launch_ng(const SplitArgs& s, int tiles, cudaStream_t st) {
     constexpr int queue = kWarps * kStages * Piece<HD>::STAGE;
     constexpr int join = kWarps * 8 * NG * (HD + 3) * 4;
     constexpr int smem = queue > join ? queue : join;
@@ -389,37 +579,64 @@ cudaError_t launch_ng(const Kv8AttnArgs& a, int G, int QT, int tiles, int max_ro
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
-    const dim3 grid((unsigned)tiles, (unsigned)a.view.n_kv, (unsigned)a.batch);
-    HRA_LAUNCH((kv8_attn_kernel<HD, NG>), grid, dim3(kWarps * 32), smem, st, a, G, QT, max_rows);
+    if (s.whole) {
+        const dim3 grid((unsigned)tiles, (unsigned)s.a.view.n_kv, (unsigned)s.a.batch);
+        HRA_LAUNCH((kv8_attn_kernel<HD, NG>), grid, dim3(kWarps * 32), smem, st, s);
+        return cudaGetLastError();
+    }
+    const dim3 grid((unsigned)split_grid());
+    HRA_LAUNCH((kv8_attn_kernel<HD, NG>), grid, dim3(kWarps * 32), smem, st, s);
+    HRA_LAUNCH((kv8_join_kernel<HD, NG>), grid, dim3(128), 0, st, s);
     return cudaGetLastError();
+}
+
+// One n = 8 column group while the rows of a tile fit it, else two.
+int column_groups(int G, int max_new) { return (long long)G * max_new <= 8 ? 1 : 2; }
+
+// Items go whole, one a CTA: while they are short, for tiles of longer sequences (the prompts' fallback), and where
+// the sequences do not fit the table of a CTA.
+bool goes_whole(const Kv8View& c, int batch, int G, int max_new, int max_len, bool prompts) {
+    return max_len <= kWholeUnits * kUnit || (!prompts && (long long)G * max_new > kShortRows) || batch > kMaxBatch;
+}
+
+size_t split_scratch(const Kv8View& c, int ng) {
+    const size_t grid = (size_t)split_grid();
+    return grid * sizeof(SplitDesc) + grid * 2 * 8 * ng * (c.head_dim + 3) * sizeof(float);
 }
 
 }  // namespace
 
 size_t kv8_attention_scratch_bytes(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int max_len) {
     const int G = nq / c.n_kv;
-    if ((long long)G * max_new <= kShortRows) return 0;
-    return kv8_prompt_scratch_bytes(batch, total_rows, G);
+    const bool prompts = (long long)G * max_new > kShortRows && kv8_prompt_supported(c);
+    size_t n = prompts ? (kv8_prompt_scratch_bytes(batch, total_rows, G) + 255) & ~size_t(255) : 0;
+    if (!goes_whole(c, batch, G, max_new, max_len, prompts)) n += split_scratch(c, column_groups(G, max_new));
+    return n;
 }
 
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st) {
     const int G = a.nq / a.view.n_kv;
     const bool prompts = (long long)G * a.max_new > kShortRows && kv8_prompt_supported(a.view);
-    const int long_keys = a.max_len > kSerialKeys;
-    // short sequences go with the prompts unless they may hold many keys
-    const int short_rows = prompts && !long_keys ? 0 : kShortRows;
+    uint8_t* scratch = reinterpret_cast<uint8_t*>(a.scratch);
     if (prompts) {
+        // short sequences go with the prompts unless they may hold many keys
+        const int short_rows = a.max_len > kSerialKeys ? kShortRows : 0;
         cudaError_t e = launch_kv8_prompt(a, short_rows, st);
         if (e != cudaSuccess || short_rows == 0 || (long long)a.batch * a.max_new == a.total_rows) return e;
+        scratch += (kv8_prompt_scratch_bytes(a.batch, a.total_rows, G) + 255) & ~size_t(255);
     }
-    // one n = 8 column group while the rows of a tile fit it, else two
-    const int rows = prompts ? kShortRows : 1 << 30;
-    const int ng = (long long)G * a.max_new <= 8 ? 1 : 2;
-    const int QT = 8 * ng / G;
-    const int tiles = prompts ? 1 : (a.max_new + QT - 1) / QT;
-    if (a.view.head_dim == 128)
-        return ng == 1 ? launch_ng<128, 1>(a, G, QT, tiles, rows, st) : launch_ng<128, 2>(a, G, QT, tiles, rows, st);
-    return ng == 1 ? launch_ng<64, 1>(a, G, QT, tiles, rows, st) : launch_ng<64, 2>(a, G, QT, tiles, rows, st);
+    SplitArgs s{};
+    s.a = a;
+    s.G = G;
+    s.max_rows = prompts ? kShortRows : 1 << 30;
+    s.whole = goes_whole(a.view, a.batch, G, a.max_new, a.max_len, prompts) ? 1 : 0;
+    const int ng = column_groups(G, a.max_new);
+    s.QT = 8 * ng / G;
+    const int tiles = prompts ? 1 : (a.max_new + s.QT - 1) / s.QT;
+    s.desc = reinterpret_cast<SplitDesc*>(scratch);
+    s.parts = reinterpret_cast<float*>(scratch + split_grid() * sizeof(SplitDesc));
+    if (a.view.head_dim == 128) return ng == 1 ? launch_ng<128, 1>(s, tiles, st) : launch_ng<128, 2>(s, tiles, st);
+    return ng == 1 ? launch_ng<64, 1>(s, tiles, st) : launch_ng<64, 2>(s, tiles, st);
 }
 
 }  // namespace hra
