@@ -807,7 +807,12 @@ class Kv8Cache:
                                   p_refs.value if p_refs is not None else None, self.errors.data_ptr(), n_layers, n_pages,
                                   n_kv, hd, page, self.rows, self.max_pages)
         self._ref = ctypes.byref(self.struct)
+        self._index = codes.get_device()
+        L = lib()
+        self._append, self._attend = L.hra_kv8_append, L.hra_kv8_attention
+        self._update, self._compact = L.hra_kv8_update, L.hra_kv8_compact
         self._attn_ws, self._pages_ws = _Workspace(), _Workspace()
+        self._attn_key = self._attn_need = self._pages_need = None
 
     @classmethod
     def new(cls, d, rows: int, n_slots: int, n_pages: Optional[int] = None, page_size: int = 64,
@@ -826,78 +831,97 @@ class Kv8Cache:
         """Tensors for the out argument of update and compact: (page table, lens, refs)."""
         return tuple(torch.empty_like(t) for t in (self.page_table, self.lens, self.refs))
 
+    # One frame's calls take microseconds on the GPU, so these checks read every attribute once and leave the
+    # words of a refusal to _refuse_rows.
     def _rows(self, t: torch.Tensor, heads: int, name: str):
+        n, h, hd = t.shape if t.dim() == 3 else (0, 0, 0)
+        s0, s1, s2 = t.stride() if t.dim() == 3 else (0, 0, 0)
+        if t.dtype is not torch.bfloat16 or t.get_device() != self._index or hd != self.head_dim or (heads and h != heads) \
+                or (n and (s2 != 1 or (h > 1 and s1 != hd))):
+            self._refuse_rows(t, heads, name)
+        return n, h, s0 if n > 1 else h * hd
+
+    def _refuse_rows(self, t, heads, name):
         if t.device != self.device:
             raise HraError(f"{name} must be on the device of the cache")
         if t.dtype != torch.bfloat16:
             raise HraError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-        if t.dim() != 3 or t.shape[2] != self.head_dim or (heads and t.shape[1] != heads) \
-                or (t.shape[0] and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != self.head_dim))):
-            raise HraError(f"{name} must be [rows, heads, head_dim] with contiguous heads")
-        stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-        return ctypes.c_void_p(t.data_ptr()), stride
+        raise HraError(f"{name} must be [rows, {heads or 'heads'}, {self.head_dim}] with contiguous heads")
 
-    def _ints(self, t: torch.Tensor, n: int, name: str):
-        if t.device != self.device or t.dim() != 1 or t.shape[0] != n:
-            raise HraError(f"{name} must be int32 [{n}] on the device of the cache")
-        return _ptr(t, torch.int32, name)
+    def _ints(self, t: torch.Tensor, n: int, name: str) -> int:
+        if t.dtype is not torch.int32 or t.get_device() != self._index or t.shape != (n,) or not t.is_contiguous():
+            raise HraError(f"{name} must be contiguous int32 [{n}] on the device of the cache")
+        return t.data_ptr()
 
-    def _on(self, stream):
-        return ctypes.c_void_p((stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream)
+    def _call(self, name, f, args, stream):
+        # the launches go to the cache's device, whichever is current
+        s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self._index)
+        if torch._C._cuda_getDevice() == self._index:
+            rc = f(self._ref, *args, s)
+        else:
+            with torch.cuda.device(self._index):
+                rc = f(self._ref, *args, s)
+        if rc:
+            _check(rc, name)
 
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, start: torch.Tensor, max_new: int,
                stream=None) -> None:
         """hra_kv8_append: k, v bf16 [T, n_kv_heads, head_dim] (rows may be strided), cu int32 [B + 1] and start int32
         [B] on the device: row b's tokens cu[b] .. cu[b + 1) go to its positions from start[b] on."""
-        pk, sk = self._rows(k, self.n_kv_heads, "k")
-        pv, sv = self._rows(v, self.n_kv_heads, "v")
-        if k.shape[0] != v.shape[0] or sk != sv:
+        n, _, stride = self._rows(k, self.n_kv_heads, "k")
+        if self._rows(v, self.n_kv_heads, "v") != (n, self.n_kv_heads, stride):
             raise HraError("k and v must have the same rows and row stride")
-        B = start.shape[0]
-        with torch.cuda.device(self.device):
-            rc = lib().hra_kv8_append(self._ref, layer, pk, pv, sk, self._ints(cu, B + 1, "cu"),
-                                      self._ints(start, B, "start"), B, k.shape[0], max_new, self._on(stream))
-        _check(rc, "hra_kv8_append")
+        B = start.shape[0] if start.dim() else 0
+        self._call("hra_kv8_append", self._append, (layer, k.data_ptr(), v.data_ptr(), stride, self._ints(cu, B + 1, "cu"),
+                                                    self._ints(start, B, "start"), B, n, max_new), stream)
+
+    def attention_workspace_size(self, batch: int, total_rows: int, n_q_heads: int, max_new: int, max_len: int) -> int:
+        return lib().hra_kv8_attention_workspace_size(self._ref, batch, total_rows, n_q_heads, max_new, max_len)
 
     def attend(self, layer: int, q: torch.Tensor, cu: torch.Tensor, kv_len: torch.Tensor, max_new: int, max_len: int,
                scale: float = 0.0, out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
         """hra_kv8_attention: q bf16 [T, n_q_heads, head_dim] (rows may be strided) of rows' last tokens, kv_len int32
         [B] positions held -> bf16 [T, n_q_heads, head_dim]."""
-        pq, sq = self._rows(q, 0, "q")
-        T, nq = q.shape[0], q.shape[1]
-        B = kv_len.shape[0]
+        T, nq, stride = self._rows(q, 0, "q")
+        B = kv_len.shape[0] if kv_len.dim() else 0
         if out is None:
-            out = torch.empty(T, nq, self.head_dim, dtype=torch.bfloat16, device=self.device)
-        elif tuple(out.shape) != (T, nq, self.head_dim) or out.device != self.device:
-            raise HraError("out must be bf16 [T, n_q_heads, head_dim] on the device of the cache")
-        with torch.cuda.device(self.device):
-            ws = workspace
-            if ws is None:
-                need = lib().hra_kv8_attention_workspace_size(self._ref, B, T, nq, max_new, max_len)
-                ws = self._attn_ws.get(need, self.device)
-            rc = lib().hra_kv8_attention(self._ref, layer, pq, sq, nq, scale, self._ints(cu, B + 1, "cu"),
-                                         self._ints(kv_len, B, "kv_len"), B, T, max_new, max_len,
-                                         _ptr(out, torch.bfloat16, "out"), _ptr(ws, None, "workspace"), ws.numel(),
-                                         self._on(stream))
-        _check(rc, "hra_kv8_attention")
+            out = torch.empty((T, nq, self.head_dim), dtype=torch.bfloat16, device=self.device)
+        elif out.shape != (T, nq, self.head_dim) or out.dtype is not torch.bfloat16 or out.get_device() != self._index \
+                or not out.is_contiguous():
+            raise HraError("out must be contiguous bf16 [T, n_q_heads, head_dim] on the device of the cache")
+        if workspace is None:
+            key = (B, T, nq, max_new, max_len)
+            if key != self._attn_key:   # the size depends on the shape alone
+                with torch.cuda.device(self._index):
+                    self._attn_need = self.attention_workspace_size(*key)
+                self._attn_key = key
+            workspace = self._attn_ws.get(self._attn_need, self.device)
+        elif workspace.get_device() != self._index or not workspace.is_contiguous():
+            raise HraError("workspace must be contiguous on the device of the cache")
+        self._call("hra_kv8_attention", self._attend,
+                   (layer, q.data_ptr(), stride, nq, scale, self._ints(cu, B + 1, "cu"), self._ints(kv_len, B, "kv_len"), B, T,
+                    max_new, max_len, out.data_ptr(), workspace.data_ptr(), workspace.nbytes), stream)
         return out
 
-    def _pages(self, name, args, out, workspace, stream):
+    def _pages(self, name, f, args, out, workspace, stream):
         if self.refs is None:
             raise HraError(f"{name} needs the cache's refs")
-        table, lens, refs = out if out is not None else (self.page_table, self.lens, self.refs)
-        if table.shape != self.page_table.shape or lens.shape != self.lens.shape or refs.shape != self.refs.shape or \
-                not table.device == lens.device == refs.device == self.device:
-            raise HraError("out must be tensors as empty_pages() makes them")
-        with torch.cuda.device(self.device):
-            ws = workspace if workspace is not None else \
-                self._pages_ws.get(lib().hra_kv8_pages_workspace_size(self._ref), self.device)
-            rc = getattr(lib(), name)(self._ref, *args, _ptr(table, torch.int32, "page table"),
-                                      _ptr(lens, torch.int32, "lens"), _ptr(refs, torch.int32, "refs"),
-                                      _ptr(ws, None, "workspace"), ws.numel(), self._on(stream))
-        _check(rc, name)
-        return table, lens, refs
+        if out is None:
+            out = (self.page_table, self.lens, self.refs)
+        ptrs = []
+        for t, mine, what in zip(out, (self.page_table, self.lens, self.refs), ("page table", "lens", "refs")):
+            if t.shape != mine.shape or t.dtype is not torch.int32 or t.get_device() != self._index or not t.is_contiguous():
+                raise HraError(f"out must be tensors as empty_pages() makes them ({what})")
+            ptrs.append(t.data_ptr())
+        if workspace is None:
+            if self._pages_need is None:
+                self._pages_need = lib().hra_kv8_pages_workspace_size(self._ref)
+            workspace = self._pages_ws.get(self._pages_need, self.device)
+        elif workspace.get_device() != self._index or not workspace.is_contiguous():
+            raise HraError("workspace must be contiguous on the device of the cache")
+        self._call(name, f, (*args, *ptrs, workspace.data_ptr(), workspace.nbytes), stream)
+        return tuple(out)
 
     def update(self, parents: Optional[torch.Tensor] = None, room: Optional[torch.Tensor] = None, out=None,
                workspace: Optional[torch.Tensor] = None, stream=None):
@@ -905,15 +929,16 @@ class Kv8Cache:
         room (int32 [rows]) more tokens.  In place, or into out (see empty_pages): (page table, lens, refs)."""
         args = (None if parents is None else self._ints(parents, self.rows, "parents"),
                 None if room is None else self._ints(room, self.rows, "room"))
-        return self._pages("hra_kv8_update", args, out, workspace, stream)
+        return self._pages("hra_kv8_update", self._update, args, out, workspace, stream)
 
     def compact(self, out=None, workspace: Optional[torch.Tensor] = None, stream=None):
         """hra_kv8_compact: the pages in use to the low end of the pool; outputs as update."""
-        return self._pages("hra_kv8_compact", (), out, workspace, stream)
+        return self._pages("hra_kv8_compact", self._compact, (), out, workspace, stream)
 
     def device_error(self, stream=None) -> int:
         """Synchronise and return the sticky error bits of every call since the errors word was last zeroed."""
-        return int(lib().hra_device_error(_ptr(self.errors, None, "errors"), self._on(stream)))
+        return int(lib().hra_device_error(_ptr(self.errors, None, "errors"),
+                                          _stream(stream if stream is not None else torch.cuda.current_stream(self.device))))
 
 
 def hra_device_error(workspace: torch.Tensor, stream=None) -> int:

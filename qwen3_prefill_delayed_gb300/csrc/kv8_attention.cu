@@ -16,12 +16,12 @@
 //           the output's bf16 rounding of 2^-8.  The sum 2^(s_j - m) is kept in fp32 from the unrounded
 //           values, with its own maximum m: a block whose V is zero or tiny still counts in it.
 //
-// The work is a line of units of 64 keys, sequence by sequence and head by head; every CTA takes an equal share
+// The work is a line of units of 128 keys, sequence by sequence and head by head; every CTA takes an equal share
 // of it, wherever the borders between sequences fall, so ragged lengths cost nothing and one long sequence
 // spreads over the whole GPU.  An item (sequence, head) that lies inside one share is written at once; the parts
 // of the others go to scratch as fp32 sums with their (m, l, M), and a second kernel joins them in order.
 //
-// A warp takes 16 keys (one block) at a time straight from global memory into fragments: the order of
+// A warp takes two blocks of 16 keys at a time straight from global memory into fragments: the order of
 // the dims inside a dot product and of the dims among the output rows is free, so it is chosen such
 // that every lane's share of a block is a few whole 16-byte pieces that only this lane reads.
 //   S = Q K^T   (m16n8k16): rows are up to 16 (position, head) pairs, lane (g, t) = (lane / 4, lane % 4)
@@ -42,11 +42,12 @@ namespace hra {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kStages = 3;      // blocks of 16 keys in flight per warp
-constexpr int kUnit = kWarps * kKv8Block;   // keys of a unit: one block a warp
-constexpr int kMaxBatch = 2048;             // sequences whose units fit the CTA's table
-constexpr int kMinShare = 4;    // units of a share at least: below it the join costs more than it spreads
-constexpr int kWholeUnits = 8;  // items of at most so many units go whole, one a CTA, and need no second kernel
+constexpr int kPair = 2;        // blocks a warp works on at once: two chains of MMAs and shuffles instead of one
+constexpr int kStages = 2;      // pairs in flight per warp
+constexpr int kUnit = kWarps * kPair * kKv8Block;   // keys of a unit: a pair of blocks a warp
+constexpr int kMaxBatch = 1024;             // sequences whose units fit the CTA's table
+constexpr int kMinShare = 2;    // units of a share at least: below it the join costs more than it spreads
+constexpr int kWholeUnits = 4;  // items of at most so many units go whole, one a CTA, and need no second kernel
 constexpr int kShortRows = 16;  // (position, head) rows of a kv head that fit this kernel's tile
 constexpr int kSerialKeys = 2048;   // keys that a short sequence may walk alone among prompts
 constexpr float kPScale = 15.f; // log2 of the largest p
@@ -80,14 +81,15 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Bytes of one lane's share of a block of 16 keys, and where its parts lie in a stage.
+// Bytes of one lane's share of a block of 16 keys, and where its parts lie in its half of a stage.
 template <int HD>
 struct Piece {
     static constexpr int KP = HD / 64;            // 16-byte pieces of each of the lane's two keys
     static constexpr int VB = HD / 8;             // bytes of each of the lane's four value rows
     static constexpr int OFF_V = 2 * KP * 512;    // [piece][lane][16]
     static constexpr int OFF_S = OFF_V + 4 * VB * 32;
-    static constexpr int STAGE = OFF_S + 32 * 8;  // the block's two scales, one copy a lane
+    static constexpr int BLOCK = OFF_S + 32 * 8;  // the block's two scales, one copy a lane
+    static constexpr int STAGE = kPair * BLOCK;
 };
 
 // Parts of split items: CTA c has slots 2 c (the item that its share begins in) and 2 c + 1 (the one it ends in).
@@ -221,56 +223,89 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
             raise_error(c.err, HRA_DEVERR_POS_RANGE);
         const int q_n = min(s.QT, n - q_lo);
         const int keys = max(0, kv_len - n + q_lo + q_n);   // positions below the tile's last row's
-        const int blk1 = min((keys + kKv8Block - 1) / kKv8Block, i1 >= (1 << 28) ? 1 << 28 : i1 * kWarps);
-        int blk = i0 * kWarps + warp;
+        const int blk1 = min((keys + kKv8Block - 1) / kKv8Block, i1 >= (1 << 28) ? 1 << 28 : i1 * (kWarps * kPair));
+        int blk = (i0 * kWarps + warp) * kPair;
+        constexpr int STEP = kWarps * kPair;
 
-        // ---- page numbers two blocks of this warp ahead of the requests, requests kStages - 1 ahead of the use
+        // ---- page numbers two turns of this warp ahead of the use, requests kStages - 1 ahead
         const int32_t* table = c.table + (long long)b * c.max_pages;
-        auto page_of = [&](int x) {
-            if (x >= blk1) return -1;
-            const int page = table[x * kKv8Block >> c.page_shift];   // x * 16 < keys <= max_pages * page_size
-            return page >= 0 && page < c.n_pages ? page : -1;
+        struct Pages {
+            int p[kPair];
         };
-        const uint8_t* head_codes = c.codes + (long long)head * c.page_size * HD;
-        const float* head_scales = c.scales + head * (c.page_size / kKv8Block);
-        // this lane's pieces of block x into stage st: keys at or past `keys`, and blocks whose page is not in the
-        // pool (their scales become 0), are zero-filled and masked below
-        auto request = [&](int x, int page, int st) {
-            bad_page |= page < 0;
-            const int slot0 = (x * kKv8Block) & (c.page_size - 1);
-            const int pg = max(page, 0);
-            const int left = page < 0 ? 0 : keys - x * kKv8Block;          // keys of this block that count
-            const uint8_t* kb = head_codes + pg * page_bytes + slot0 * HD;
-            const uint8_t* vb = kb + v_bytes;
-            const uint32_t base = queue + st * Pc::STAGE;
+        auto pages_of = [&](int x) {   // -1: no page of the pool; -2: behind the last block
+            Pages r;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int h = 0; h < Pc::KP; ++h)
-                    cp_async16(base + ((i * Pc::KP + h) * 32 + lane) * 16, kb + (g + 8 * i) * HD + h * 64 + t4 * 16,
-                               g + 8 * i < left ? 16u : 0u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = 2 * t4 + (i & 1) + 8 * (i >> 1);
-                const uint32_t dst = base + Pc::OFF_V + (i * 32 + lane) * Pc::VB;
-                if (HD == 128)
-                    cp_async16(dst, vb + key * HD + g * 16, key < left ? 16u : 0u);
-                else
-                    cp_async_ca<8>(dst, vb + key * HD + g * 8, key < left ? 8 : 0);
+            for (int y = 0; y < kPair; ++y) {
+                r.p[y] = -2;
+                if (x + y < blk1) {   // (x + y) * 16 < keys <= max_pages * page_size
+                    const int page = table[(x + y) * kKv8Block >> c.page_shift];
+                    r.p[y] = page >= 0 && page < c.n_pages ? page : -1;
+                }
             }
-            const uint32_t at = base + Pc::OFF_S + lane * 8;
-            const float* sp = head_scales + (long long)pg * page_scales + (slot0 / kKv8Block);
-            cp_async_ca<4>(at, sp, page < 0 ? 0 : 4);
-            cp_async_ca<4>(at + 4, sp + v_scales, page < 0 ? 0 : 4);
+            return r;
+        };
+        const uint8_t* lane_k = c.codes + (long long)head * c.page_size * HD + g * HD + t4 * 16;
+        const uint8_t* lane_v = c.codes + (long long)head * c.page_size * HD + v_bytes + 2 * t4 * HD + g * (HD / 8);
+        const float* head_scales = c.scales + head * (c.page_size / kKv8Block);
+        // this lane's pieces of blocks x0, x0 + 1 into stage st: keys at or past `keys`, and blocks without a page
+        // (their scales become 0), are zero-filled and masked below
+        auto request = [&](int x0, const Pages& pages, int st) {
+#pragma unroll
+            for (int y = 0; y < kPair; ++y) {
+                const int x = x0 + y, page = pages.p[y];
+                bad_page |= page == -1;
+                const int slot0 = (x * kKv8Block) & (c.page_size - 1);
+                const int pg = max(page, 0);
+                const int left = page < 0 ? 0 : keys - x * kKv8Block;          // keys of this block that count
+                const long long at = pg * page_bytes + slot0 * HD;
+                const uint8_t* kb = lane_k + at;
+                const uint8_t* vb = lane_v + at;
+                const uint32_t base = queue + st * Pc::STAGE + y * Pc::BLOCK;
+                const uint32_t to = base + lane * 16, to_v = base + Pc::OFF_V + lane * Pc::VB;
+                const float* sp = head_scales + (long long)pg * page_scales + (slot0 / kKv8Block);
+                const uint32_t to_s = base + Pc::OFF_S + lane * 8;
+                if (left >= kKv8Block) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int h = 0; h < Pc::KP; ++h) cp_async16(to + (i * Pc::KP + h) * 512, kb + 8 * i * HD + h * 64, 16u);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = (i & 1) + 8 * (i >> 1);   // + 2 t
+                        if (HD == 128)
+                            cp_async16(to_v + i * 32 * Pc::VB, vb + key * HD, 16u);
+                        else
+                            cp_async_ca<8>(to_v + i * 32 * Pc::VB, vb + key * HD, 8);
+                    }
+                    cp_async_ca<4>(to_s, sp, 4);
+                    cp_async_ca<4>(to_s + 4, sp + v_scales, 4);
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll 1
+                        for (int h = 0; h < Pc::KP; ++h)
+                            cp_async16(to + (i * Pc::KP + h) * 512, kb + 8 * i * HD + h * 64, g + 8 * i < left ? 16u : 0u);
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = (i & 1) + 8 * (i >> 1);
+                        if (HD == 128)
+                            cp_async16(to_v + i * 32 * Pc::VB, vb + key * HD, 2 * t4 + key < left ? 16u : 0u);
+                        else
+                            cp_async_ca<8>(to_v + i * 32 * Pc::VB, vb + key * HD, 2 * t4 + key < left ? 8 : 0);
+                    }
+                    cp_async_ca<4>(to_s, sp, page < 0 ? 0 : 4);
+                    cp_async_ca<4>(to_s + 4, sp + v_scales, page < 0 ? 0 : 4);
+                }
+            }
         };
         int ahead = blk;
-        int page0 = page_of(ahead), page1 = page_of(ahead + kWarps);
+        Pages page0 = pages_of(ahead), page1 = pages_of(ahead + STEP);
 #pragma unroll
         for (int st = 0; st < kStages - 1; ++st) {
-            const int page2 = page_of(ahead + 2 * kWarps);
+            const Pages page2 = pages_of(ahead + 2 * STEP);
             if (ahead < blk1) request(ahead, page0, st);
             cp_async_commit();
-            ahead += kWarps;
+            ahead += STEP;
             page0 = page1;
             page1 = page2;
         }
@@ -341,77 +376,96 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
 
         int st = 0, st_in = kStages - 1;
 #pragma unroll 1
-        for (; blk < blk1; blk += kWarps) {
+        for (; blk < blk1; blk += STEP) {
             {
-                const int page2 = page_of(ahead + 2 * kWarps);
+                const Pages page2 = pages_of(ahead + 2 * STEP);
                 if (ahead < blk1) request(ahead, page0, st_in);
                 page0 = page1;
                 page1 = page2;
             }
             cp_async_commit();
-            ahead += kWarps;
+            ahead += STEP;
             st_in = st_in + 1 == kStages ? 0 : st_in + 1;
             cp_async_wait<kStages - 1>();
-            const uint8_t* sp = sm + warp * kStages * Pc::STAGE + st * Pc::STAGE;
+            const uint8_t* sp0 = sm + warp * kStages * Pc::STAGE + st * Pc::STAGE;
             st = st + 1 == kStages ? 0 : st + 1;
-            const float2 sc = *reinterpret_cast<const float2*>(sp + Pc::OFF_S + lane * 8);
 
-            float sv[2][4];
+            float sv[kPair][2][4];
+            float2 sc[kPair];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                sv[i][0] = sv[i][1] = sv[i][2] = sv[i][3] = 0.f;
+            for (int y = 0; y < kPair; ++y) {
+                sc[y] = *reinterpret_cast<const float2*>(sp0 + y * Pc::BLOCK + Pc::OFF_S + lane * 8);
 #pragma unroll
-                for (int h = 0; h < Pc::KP; ++h) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(sp + ((i * Pc::KP + h) * 32 + lane) * 16);
-                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t b0, b1;
-                        e4m3x4_f16x4(ww[q], b0, b1);
-                        if (NG == 1)
-                            mma_f16(sv[i], qa[h * 4 + q][0], 0u, qa[h * 4 + q][1], 0u, b0, b1);
-                        else
-                            mma_f16(sv[i], qa[h * 4 + q][0], qa[h * 4 + q][NG - 1], qa[h * 4 + q][NG],
-                                    qa[h * 4 + q][2 * NG - 1], b0, b1);
-                    }
-                }
+                for (int i = 0; i < 2; ++i) sv[y][i][0] = sv[y][i][1] = sv[y][i][2] = sv[y][i][3] = 0.f;
             }
-            const bool there = sc.x > 0.f;   // 0: a page outside the pool, whose keys are absent
-            const uint32_t vbits = __float_as_uint(sc.y);
-            const float ev = (float)((int)((vbits >> 23) & 255u) - 127);
-            const float vm = __uint_as_float((vbits & 0x807FFFFFu) | 0x3F800000u);
-            uint32_t pb[NG][2];
+#pragma unroll
+            for (int h = 0; h < Pc::KP; ++h)
+#pragma unroll
+                for (int y = 0; y < kPair; ++y)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(sp0 + y * Pc::BLOCK + ((i * Pc::KP + h) * 32 + lane) * 16);
+                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t b0, b1;
+                            e4m3x4_f16x4(ww[q], b0, b1);
+                            if (NG == 1)
+                                mma_f16(sv[y][i], qa[h * 4 + q][0], 0u, qa[h * 4 + q][1], 0u, b0, b1);
+                            else
+                                mma_f16(sv[y][i], qa[h * 4 + q][0], qa[h * 4 + q][NG - 1], qa[h * 4 + q][NG],
+                                        qa[h * 4 + q][2 * NG - 1], b0, b1);
+                        }
+                    }
+            uint32_t pb[kPair][NG][2];
             float al[NG];
             bool moved = false;
+            float ev[kPair], vm[kPair];
+#pragma unroll
+            for (int y = 0; y < kPair; ++y) {
+                const uint32_t vbits = __float_as_uint(sc[y].y);
+                ev[y] = (float)((int)((vbits >> 23) & 255u) - 127);
+                vm[y] = __uint_as_float((vbits & 0x807FFFFFu) | 0x3F800000u);
+            }
 #pragma unroll
             for (int x = 0; x < NG; ++x) {
-                const float coef = q_unscale[x] * sc.x;
-                const int lim = there ? limit[x] - blk * kKv8Block - 2 * t4 : 0;   // of this lane's keys 0, 1, 8, 9
-                float z[4];
-                float mx = -INFINITY;
+                float z[kPair][4];
+                float mx[kPair];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    z[e] = (e >> 1) * 8 + (e & 1) < lim ? sv[e >> 1][2 * x + (e & 1)] * coef : -INFINITY;
-                    mx = fmaxf(mx, z[e]);
+                for (int y = 0; y < kPair; ++y) {
+                    const float coef = q_unscale[x] * sc[y].x;
+                    // of this lane's keys 0, 1, 8, 9 those below it count; a scale of 0: the block is absent
+                    const int lim = sc[y].x > 0.f ? limit[x] - (blk + y) * kKv8Block - 2 * t4 : 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        z[y][e] = (e >> 1) * 8 + (e & 1) < lim ? sv[y][e >> 1][2 * x + (e & 1)] * coef : -INFINITY;
+                    mx[y] = fmaxf(fmaxf(z[y][0], z[y][1]), fmaxf(z[y][2], z[y][3]));
                 }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(m[x], mx), Mn = fmaxf(M[x], mx + ev);
+                float top = fmaxf(mx[0], mx[1]), Top = fmaxf(mx[0] + ev[0], mx[1] + ev[1]);
+#pragma unroll
+                for (int o2 = 1; o2 < 4; o2 <<= 1) {
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
+                    Top = fmaxf(Top, __shfl_xor_sync(0xffffffffu, Top, o2));
+                }
+                const float mn = fmaxf(m[x], top), Mn = fmaxf(M[x], Top);
                 const float mr = mn == -INFINITY ? 0.f : mn, Mr = Mn == -INFINITY ? 0.f : Mn;
                 al[x] = ex2(M[x] - Mr);
                 l[x] *= ex2(m[x] - mr);
                 moved |= al[x] != 1.f;
                 m[x] = mn;
                 M[x] = Mn;
-                const float off = ev + kPScale - Mr;
-                float w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    l[x] += ex2(z[e] - mr);
-                    w[e] = ex2(z[e] + off) * vm;
+                for (int y = 0; y < kPair; ++y) {
+                    const float off = ev[y] + kPScale - Mr;
+                    float w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        l[x] += ex2(z[y][e] - mr);
+                        w[e] = ex2(z[y][e] + off) * vm[y];
+                    }
+                    pb[y][x][0] = pack_h2(w[0], w[1]);
+                    pb[y][x][1] = pack_h2(w[2], w[3]);
                 }
-                pb[x][0] = pack_h2(w[0], w[1]);
-                pb[x][1] = pack_h2(w[2], w[3]);
             }
             if (__any_sync(0xffffffffu, moved)) {   // O's columns are rows 2 t, 2 t + 1 (+ 8 x)
 #pragma unroll
@@ -427,33 +481,36 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
                 }
             }
             // O^T += V^T P^T: words of keys 2t and 2t + 1 interleave into pairs of one dim
-            uint32_t vw[4][HD / 32];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint8_t* at = sp + Pc::OFF_V + (i * 32 + lane) * Pc::VB;
-                if (HD == 128) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(at);
-                    vw[i][0] = w.x;
-                    vw[i][1] = w.y;
-                    vw[i][HD / 32 - 2] = w.z;
-                    vw[i][HD / 32 - 1] = w.w;
-                } else {
-                    const uint2 w = *reinterpret_cast<const uint2*>(at);
-                    vw[i][0] = w.x;
-                    vw[i][1] = w.y;
+            for (int y = 0; y < kPair; ++y) {
+                uint32_t vw[4][HD / 32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint8_t* at = sp0 + y * Pc::BLOCK + Pc::OFF_V + (i * 32 + lane) * Pc::VB;
+                    if (HD == 128) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(at);
+                        vw[i][0] = w.x;
+                        vw[i][1] = w.y;
+                        vw[i][HD / 32 - 2] = w.z;
+                        vw[i][HD / 32 - 1] = w.w;
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2*>(at);
+                        vw[i][0] = w.x;
+                        vw[i][1] = w.y;
+                    }
                 }
-            }
 #pragma unroll
-            for (int j = 0; j < HD / 32; ++j) {
-                uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
-                e4m3x4_f16x4(__byte_perm(vw[0][j], vw[1][j], 0x5140), a0, a1);
-                e4m3x4_f16x4(__byte_perm(vw[2][j], vw[3][j], 0x5140), a2, a3);
-                e4m3x4_f16x4(__byte_perm(vw[0][j], vw[1][j], 0x7362), c0, c1);
-                e4m3x4_f16x4(__byte_perm(vw[2][j], vw[3][j], 0x7362), c2, c3);
+                for (int j = 0; j < HD / 32; ++j) {
+                    uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
+                    e4m3x4_f16x4(__byte_perm(vw[0][j], vw[1][j], 0x5140), a0, a1);
+                    e4m3x4_f16x4(__byte_perm(vw[2][j], vw[3][j], 0x5140), a2, a3);
+                    e4m3x4_f16x4(__byte_perm(vw[0][j], vw[1][j], 0x7362), c0, c1);
+                    e4m3x4_f16x4(__byte_perm(vw[2][j], vw[3][j], 0x7362), c2, c3);
 #pragma unroll
-                for (int x = 0; x < NG; ++x) {
-                    mma_f16(o[x][2 * j], a0, a1, a2, a3, pb[x][0], pb[x][1]);
-                    mma_f16(o[x][2 * j + 1], c0, c1, c2, c3, pb[x][0], pb[x][1]);
+                    for (int x = 0; x < NG; ++x) {
+                        mma_f16(o[x][2 * j], a0, a1, a2, a3, pb[y][x][0], pb[y][x][1]);
+                        mma_f16(o[x][2 * j + 1], c0, c1, c2, c3, pb[y][x][0], pb[y][x][1]);
+                    }
                 }
             }
         }
@@ -528,36 +585,64 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
     if (bad_page) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
 }
 
-// One CTA per share: the item that begins in it and goes on behind it.
+// One CTA per share: the item that begins in it and goes on behind it.  The rows' maxima and sums over all parts
+// come first (a warp a row, a lane a part), then every thread adds its columns, parts in order, with the loads free of
+// each other.
 template <int HD, int NG>
-__global__ void __launch_bounds__(128) kv8_join_kernel(const SplitArgs s) {
+__global__ void __launch_bounds__(256) kv8_join_kernel(const SplitArgs s) {
     pdl_launch();
     pdl_wait();
     constexpr int ROWS = 8 * NG;
+    __shared__ float s_m[ROWS], s_M[ROWS], s_l[ROWS];
     const int c0 = blockIdx.x;
     const SplitDesc d = s.desc[c0];
     if (d.row0 < 0) return;
-    auto slot = [&](int c) { return s.parts + (2LL * c + (c == c0 ? 1 : 0)) * Slot<HD, NG>::FLOATS; };
-    for (int i = threadIdx.x; i < d.n * s.G * (HD / 2); i += 128) {
+    const int rows = d.n * s.G, parts = d.last - c0 + 1;
+    // part i: the end of share c0, then the beginnings of the shares behind it
+    auto slot = [&](int i) { return s.parts + (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * Slot<HD, NG>::FLOATS; };
+    for (int r = threadIdx.x >> 5; r < rows; r += 8) {
+        const int lane = threadIdx.x & 31;
+        float m = -INFINITY, M = -INFINITY, l = 0.f;
+        for (int i = lane; i < parts; i += 32) {
+            const float* q = slot(i) + ROWS * HD + r * 3;
+            const float mn = fmaxf(m, q[0]);
+            const float mr = mn == -INFINITY ? 0.f : mn;
+            l = l * ex2(m - mr) + q[1] * ex2(q[0] - mr);
+            m = mn;
+            M = fmaxf(M, q[2]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+            const float mn = fmaxf(m, m2);
+            const float mr = mn == -INFINITY ? 0.f : mn;
+            // the lower lane's term first on both sides: every lane has the same sum
+            const float x = l * ex2(m - mr), y = l2 * ex2(m2 - mr);
+            l = (lane & o) ? y + x : x + y;
+            m = mn;
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        }
+        if (lane == 0) {
+            s_m[r] = m == -INFINITY ? 0.f : m;
+            s_M[r] = M == -INFINITY ? 0.f : M;
+            s_l[r] = l;
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * (HD / 2); i += 256) {
         const int r = i / (HD / 2), dd = (i - r * (HD / 2)) * 2;
         const int qi = r / s.G, hq = r - qi * s.G;
-        float m = -INFINITY, M = -INFINITY, L = 0.f, x0 = 0.f, x1 = 0.f;
-#pragma unroll 4
-        for (int c = c0; c <= d.last; ++c) {
-            const float* p = slot(c);
-            const float* q = p + ROWS * HD + r * 3;
+        const float Mr = s_M[r], L = s_l[r];
+        float x0 = 0.f, x1 = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < parts; ++k) {
+            const float* p = slot(k);
             const float2 ov = *reinterpret_cast<const float2*>(p + r * HD + dd);
-            const float mn = fmaxf(m, q[0]), Mn = fmaxf(M, q[2]);
-            const float mr = mn == -INFINITY ? 0.f : mn, Mr = Mn == -INFINITY ? 0.f : Mn;
-            const float f0 = ex2(M - Mr), f1 = ex2(q[2] - Mr);
-            L = L * ex2(m - mr) + q[1] * ex2(q[0] - mr);
-            x0 = x0 * f0 + ov.x * f1;
-            x1 = x1 * f0 + ov.y * f1;
-            m = mn;
-            M = Mn;
+            const float f = ex2(p[ROWS * HD + r * 3 + 2] - Mr);
+            x0 += ov.x * f;
+            x1 += ov.y * f;
         }
-        const float mr = m == -INFINITY ? 0.f : m, Mr = M == -INFINITY ? 0.f : M;
-        const float f = L == 0.f ? 0.f : exp2f(Mr - mr) / L;
+        const float f = L == 0.f ? 0.f : exp2f(Mr - s_m[r]) / L;
         bf16* dst = s.a.out + ((long long)(d.row0 + qi) * s.a.nq + d.head * s.G + hq) * HD + dd;
         *reinterpret_cast<uint32_t*>(dst) = pack_bf2(x0 * 0x1p-15f * f, x1 * 0x1p-15f * f);
     }
@@ -586,7 +671,7 @@ cudaError_t launch_ng(const SplitArgs& s, int tiles, cudaStream_t st) {
     }
     const dim3 grid((unsigned)split_grid());
     HRA_LAUNCH((kv8_attn_kernel<HD, NG>), grid, dim3(kWarps * 32), smem, st, s);
-    HRA_LAUNCH((kv8_join_kernel<HD, NG>), grid, dim3(128), 0, st, s);
+    HRA_LAUNCH((kv8_join_kernel<HD, NG>), grid, dim3(256), 0, st, s);
     return cudaGetLastError();
 }
 
