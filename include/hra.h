@@ -437,7 +437,8 @@ int hra_prefill_fp8(const hra_dims* dims, const hra_weights* weights, const hra_
  *   errors      one word, set to 0 by the caller: HRA_DEVERR_* bits are OR-ed into it and stay until
  *               the caller clears it (hra_device_error(errors, stream) reads it)
  * codes and scales 16-byte aligned, the rest 4-byte.  head_dim 64 or 128, page_size 16, 32, 64 or 128,
- * n_kv_heads <= 1024, rows <= 65535, max_pages * page_size <= 2^30.
+ * n_kv_heads <= 1024, rows <= 65535, max_pages * page_size <= 2^30, rows * max_pages <= 2^30, and 2 * n_pages *
+ * n_kv_heads * page_size < 2^31 (else HRA_ERR_UNSUPPORTED).
  * A page that several rows list must not be written: only positions of pages that are full are shared
  * (hra_kv8_update sees to it as long as rows are only appended to). */
 typedef struct hra_kv8_cache {

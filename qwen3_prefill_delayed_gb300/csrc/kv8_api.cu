@@ -34,8 +34,8 @@ int kv8_check(const hra_kv8_cache* c) {
         (c->page_size & (c->page_size - 1)) != 0 || c->n_kv_heads > 1024 || c->rows > 65535)
         return HRA_ERR_UNSUPPORTED;
     if ((long long)c->max_pages * c->page_size > (1 << 30) || (long long)c->rows * c->max_pages > (1 << 30) ||
-        c->n_pages > (1 << 28))
-        return HRA_ERR_UNSUPPORTED;   // positions, table cells and scratch words stay inside 32 bits
+        2LL * c->n_pages * c->n_kv_heads * c->page_size >= (1LL << 31))
+        return HRA_ERR_UNSUPPORTED;   // positions, table cells, scratch words and a layer's rows stay inside 32 bits
     return HRA_OK;
 }
 

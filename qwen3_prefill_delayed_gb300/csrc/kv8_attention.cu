@@ -21,15 +21,16 @@
 // spreads over the whole GPU.  An item (sequence, head) that lies inside one share is written at once; the parts
 // of the others go to scratch as fp32 sums with their (m, l, M), and a second kernel joins them in order.
 //
-// A warp takes two blocks of 16 keys at a time straight from global memory into fragments: the order of
-// the dims inside a dot product and of the dims among the output rows is free, so it is chosen such
-// that every lane's share of a block is a few whole 16-byte pieces that only this lane reads.
+// A warp takes two blocks of 16 keys at a time.  The order of the dims inside a dot product, of the dims among the
+// output rows and of the keys of a block is free, so it is chosen such that every lane reads its share of a block as
+// whole 16-byte pieces that become MMA fragments with no exchange between lanes:
 //   S = Q K^T   (m16n8k16): rows are up to 16 (position, head) pairs, lane (g, t) = (lane / 4, lane % 4)
-//               holds 16-byte pieces 16 t and 64 + 16 t of keys g and g + 8;
-//   O^T = V^T P^T: lane (g, t) holds dims 16 g .. 16 g + 15 of keys 2t, 2t + 1, 2t + 8, 2t + 9, and the
-//               P^T fragment is the lane's own S accumulators.
-// Each lane copies its pieces with cp.async into a private queue in shared memory: no barrier and
-// no bank conflict stands between the copies and the arithmetic.
+//               reads pieces 16 t and 64 + 16 t of keys k(g) and k(g) + 8;
+//   O^T = V^T P^T: lane (g, t) reads dims 16 g .. 16 g + 15 of keys k(2t), k(2t + 1) and those + 8, and the P^T
+//               fragment is the lane's own S accumulators;
+//   k(2 j) = 2 j, k(2 j + 1) = (2 j ^ 4) + 1: with the copies' 128-byte swizzle no read has a bank conflict.
+// Each warp has its own ring of stages that TMA fills, one box of 16 rows for K and one for V a block, so a
+// block costs one lane two instructions to request (32 cp.async an address each before: 4.3 -> MEASURED TB/s).
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -52,10 +53,8 @@ constexpr int kShortRows = 16;  // (position, head) rows of a kv head that fit t
 constexpr int kSerialKeys = 2048;   // keys that a short sequence may walk alone among prompts
 constexpr float kPScale = 15.f; // log2 of the largest p
 
-// 4 or 8 bytes; src_bytes = 0 zero-fills the destination
-template <int N>
-__device__ __forceinline__ void cp_async_ca(uint32_t dst, const void* src, int src_bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(src_bytes) : "memory");
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int src_bytes) {   // 0 bytes: zero
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 // four E4M3 codes -> two pairs of f16
 __device__ __forceinline__ void e4m3x4_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -81,15 +80,19 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Bytes of one lane's share of a block of 16 keys, and where its parts lie in its half of a stage.
+// A stage: K and V of a pair of blocks as TMA writes them (rows of HD bytes, swizzled over the row: 1024- or
+// 512-byte atoms), and the blocks' scales, a copy a lane.
 template <int HD>
-struct Piece {
-    static constexpr int KP = HD / 64;            // 16-byte pieces of each of the lane's two keys
-    static constexpr int VB = HD / 8;             // bytes of each of the lane's four value rows
-    static constexpr int OFF_V = 2 * KP * 512;    // [piece][lane][16]
-    static constexpr int OFF_S = OFF_V + 4 * VB * 32;
-    static constexpr int BLOCK = OFF_S + 32 * 8;  // the block's two scales, one copy a lane
-    static constexpr int STAGE = kPair * BLOCK;
+struct Ring {
+    static constexpr int BLOCK = kKv8Block * HD;               // K (or V) of a block
+    static constexpr int CODES = kPair * 2 * BLOCK;            // of a stage: [pair][K, V]
+    static constexpr int SCALES = kPair * 32 * 8;
+    static constexpr int ALL_CODES = kWarps * kStages * CODES;
+    static constexpr int BYTES = ALL_CODES + kWarps * kStages * SCALES;
+    // byte offset of 16-byte chunk `chunk` of row `row`
+    static __device__ __forceinline__ int at(int row, int chunk) {
+        return row * HD + ((HD == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4);
+    }
 };
 
 // Parts of split items: CTA c has slots 2 c (the item that its share begins in) and 2 c + 1 (the one it ends in).
@@ -109,20 +112,23 @@ struct SplitArgs {
     SplitDesc* desc;
     float* parts;
     int G, max_rows;   // sequences with at most max_rows (position, head) rows a kv head
-    int whole;         // one item a CTA: blockIdx = (tile, head, sequence)
-    int QT;
+    int whole;         // one item a CTA: blockIdx = (head, sequence)
 };
 
 // NG x 8 rows of (position, head) pairs.
 template <int HD, int NG>
-__global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArgs s) {
+__global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_constant__ CUtensorMap codes_map,
+                                                                  const SplitArgs s) {
     pdl_launch();
     pdl_wait();
-    using Pc = Piece<HD>;
+    using R = Ring<HD>;
     constexpr int KS = HD / 16;       // k steps of S
     constexpr int DT = HD / 16;       // 16-dim tiles of O^T
     constexpr int ROWS = 8 * NG;
-    extern __shared__ __align__(16) uint8_t sm[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t bars[kWarps * kStages];
+    __shared__ int abort_flag;
     __shared__ int before[kMaxBatch + 1];   // units of one head of the sequences before
     __shared__ int warp_total[kWarps];
     const Kv8AttnArgs& a = s.a;
@@ -130,6 +136,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
     const int G = s.G;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int room = c.max_pages << c.page_shift;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(bars + i), 1);
+        abort_flag = 0;
+        mbar_fence_init();
+        tma_prefetch_map(&codes_map);
+    }
+    __syncthreads();
     auto length = [&](int b) { return min(room, max(0, a.kv_len[b])); };
 
     // ---- this CTA's share
@@ -180,22 +193,25 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
         if (u >= u_end) return;
     }
 
-    const uint32_t queue = smem_u32(sm) + warp * kStages * Pc::STAGE;
-    const long long page_bytes = 2LL * c.n_kv * c.page_size * HD;
-    const int v_bytes = c.n_kv * c.page_size * HD;   // from a block's K to its V: below 2^24
+    uint8_t* ring = sm + warp * kStages * R::CODES;
+    uint8_t* ring_scales = sm + R::ALL_CODES + warp * kStages * R::SCALES + lane * 8;
+    const uint32_t ring_bar = smem_u32(bars + warp * kStages);
+    uint32_t phases = 0u;      // the next phase of each stage's barrier
+    const int page_rows = 2 * c.n_kv * c.page_size, v_rows = c.n_kv * c.page_size;   // rows of the tensor map
     const int page_scales = 2 * c.n_kv * (c.page_size / kKv8Block), v_scales = page_scales / 2;
+    const int key_g = g & 1 ? ((g - 1) ^ 4) + 1 : g;   // k(g), k(2 t), k(2 t + 1)
+    const int key_0 = 2 * t4, key_1 = (key_0 ^ 4) + 1;
     bool bad_page = false;
 
     while (u < u_end) {
-        // ---- the segment: units [i0, i1) of item (b, head), tile of query positions q_lo ..
-        int b, head, i0 = 0, i1, q_lo = 0, row0, n;
+        // ---- the segment: units [i0, i1) of item (b, head)
+        int b, head, i0 = 0, i1, row0, n;
         bool first_part = true, last_part = true;
         if (s.whole) {
-            b = blockIdx.z;
-            head = blockIdx.y;
-            q_lo = blockIdx.x * s.QT;
+            b = blockIdx.y;
+            head = blockIdx.x;
             kv8_rows(a.cu, b, a.total_rows, row0, n);
-            if (q_lo >= n || n * G > s.max_rows) return;
+            if (n == 0 || n * G > s.max_rows) return;
             i1 = 1 << 30;
             u = u_end;
         } else {
@@ -218,11 +234,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
             kv8_rows(a.cu, b, a.total_rows, row0, n);
         }
         const int kv_len = length(b);
-        if (head == 0 && threadIdx.x == 0 && first_part && q_lo == 0 &&
+        if (head == 0 && threadIdx.x == 0 && first_part &&
             (a.kv_len[b] != kv_len || n > a.max_new))
             raise_error(c.err, HRA_DEVERR_POS_RANGE);
-        const int q_n = min(s.QT, n - q_lo);
-        const int keys = max(0, kv_len - n + q_lo + q_n);   // positions below the tile's last row's
+        const int q_n = min(ROWS / G, n);              // tokens beyond max_new get no output
+        const int keys = max(0, kv_len - n + q_n);     // positions below the last of them
         const int blk1 = min((keys + kKv8Block - 1) / kKv8Block, i1 >= (1 << 28) ? 1 << 28 : i1 * (kWarps * kPair));
         int blk = (i0 * kWarps + warp) * kPair;
         constexpr int STEP = kWarps * kPair;
@@ -244,57 +260,35 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
             }
             return r;
         };
-        const uint8_t* lane_k = c.codes + (long long)head * c.page_size * HD + g * HD + t4 * 16;
-        const uint8_t* lane_v = c.codes + (long long)head * c.page_size * HD + v_bytes + 2 * t4 * HD + g * (HD / 8);
         const float* head_scales = c.scales + head * (c.page_size / kKv8Block);
-        // this lane's pieces of blocks x0, x0 + 1 into stage st: keys at or past `keys`, and blocks without a page
-        // (their scales become 0), are zero-filled and masked below
+        // blocks x0, x0 + 1 into stage st; one without a page gets scales of 0 and is masked below
         auto request = [&](int x0, const Pages& pages, int st) {
+            int boxes = 0;
 #pragma unroll
             for (int y = 0; y < kPair; ++y) {
-                const int x = x0 + y, page = pages.p[y];
+                const int page = pages.p[y];
                 bad_page |= page == -1;
-                const int slot0 = (x * kKv8Block) & (c.page_size - 1);
-                const int pg = max(page, 0);
-                const int left = page < 0 ? 0 : keys - x * kKv8Block;          // keys of this block that count
-                const long long at = pg * page_bytes + slot0 * HD;
-                const uint8_t* kb = lane_k + at;
-                const uint8_t* vb = lane_v + at;
-                const uint32_t base = queue + st * Pc::STAGE + y * Pc::BLOCK;
-                const uint32_t to = base + lane * 16, to_v = base + Pc::OFF_V + lane * Pc::VB;
-                const float* sp = head_scales + (long long)pg * page_scales + (slot0 / kKv8Block);
-                const uint32_t to_s = base + Pc::OFF_S + lane * 8;
-                if (left >= kKv8Block) {
+                boxes += page >= 0 ? 2 : 0;
+                const int slot0 = ((x0 + y) * kKv8Block) & (c.page_size - 1);
+                const float* sp = head_scales + (long long)max(page, 0) * page_scales + (slot0 / kKv8Block);
+                const uint32_t to = smem_u32(ring_scales + st * R::SCALES + y * 32 * 8);
+                cp_async4(to, sp, page < 0 ? 0 : 4);
+                cp_async4(to + 4, sp + v_scales, page < 0 ? 0 : 4);
+            }
+            if (lane == 0) {
+                const uint32_t bar = ring_bar + 8 * st;
+                if (boxes)
+                    mbar_expect_tx(bar, boxes * R::BLOCK);
+                else
+                    mbar_arrive(bar);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int h = 0; h < Pc::KP; ++h) cp_async16(to + (i * Pc::KP + h) * 512, kb + 8 * i * HD + h * 64, 16u);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = (i & 1) + 8 * (i >> 1);   // + 2 t
-                        if (HD == 128)
-                            cp_async16(to_v + i * 32 * Pc::VB, vb + key * HD, 16u);
-                        else
-                            cp_async_ca<8>(to_v + i * 32 * Pc::VB, vb + key * HD, 8);
+                for (int y = 0; y < kPair; ++y) {
+                    if (pages.p[y] >= 0) {   // rows of the map are counted in 32 bits (checked before the launch)
+                        const int row = pages.p[y] * page_rows + head * c.page_size + (((x0 + y) * kKv8Block) & (c.page_size - 1));
+                        const uint32_t to = smem_u32(ring + st * R::CODES + 2 * y * R::BLOCK);
+                        tma_load_2d(to, &codes_map, bar, 0, row);
+                        tma_load_2d(to + R::BLOCK, &codes_map, bar, 0, row + v_rows);
                     }
-                    cp_async_ca<4>(to_s, sp, 4);
-                    cp_async_ca<4>(to_s + 4, sp + v_scales, 4);
-                } else {
-#pragma unroll 1
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll 1
-                        for (int h = 0; h < Pc::KP; ++h)
-                            cp_async16(to + (i * Pc::KP + h) * 512, kb + 8 * i * HD + h * 64, g + 8 * i < left ? 16u : 0u);
-#pragma unroll 1
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = (i & 1) + 8 * (i >> 1);
-                        if (HD == 128)
-                            cp_async16(to_v + i * 32 * Pc::VB, vb + key * HD, 2 * t4 + key < left ? 16u : 0u);
-                        else
-                            cp_async_ca<8>(to_v + i * 32 * Pc::VB, vb + key * HD, 2 * t4 + key < left ? 8 : 0);
-                    }
-                    cp_async_ca<4>(to_s, sp, page < 0 ? 0 : 4);
-                    cp_async_ca<4>(to_s + 4, sp + v_scales, page < 0 ? 0 : 4);
                 }
             }
         };
@@ -318,8 +312,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
         for (int x = 0; x < NG; ++x) {
             const int r = g + 8 * x, qi = r / G, hq = r - qi * G;
             const bool ok = qi < q_n;
-            limit[x] = ok ? min(keys, kv_len - n + q_lo + qi + 1) : 0;
-            const bf16* src = a.q + (long long)(row0 + q_lo + (ok ? qi : 0)) * a.row_stride + (long long)(head * G + hq) * HD;
+            limit[x] = ok ? min(keys, kv_len - n + qi + 1) : 0;
+            const bf16* src = a.q + (long long)(row0 + (ok ? qi : 0)) * a.row_stride + (long long)(head * G + hq) * HD;
             uint4 raw[HD / 64][2];
             uint32_t top = 0u;     // bf16 bits without their sign order like the values
 #pragma unroll
@@ -379,6 +373,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
         for (; blk < blk1; blk += STEP) {
             {
                 const Pages page2 = pages_of(ahead + 2 * STEP);
+                __syncwarp();   // every lane's pieces of the stage before are in its MMAs: the stage may be filled
                 if (ahead < blk1) request(ahead, page0, st_in);
                 page0 = page1;
                 page1 = page2;
@@ -387,24 +382,30 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
             ahead += STEP;
             st_in = st_in + 1 == kStages ? 0 : st_in + 1;
             cp_async_wait<kStages - 1>();
-            const uint8_t* sp0 = sm + warp * kStages * Pc::STAGE + st * Pc::STAGE;
+            if (!mbar_wait(ring_bar + 8 * st, (phases >> st) & 1u, &abort_flag)) {
+                abort_flag = 1;
+                raise_error(c.err, HRA_DEVERR_WAIT_TIMEOUT);
+            }
+            phases ^= 1u << st;
+            const uint8_t* codes = ring + st * R::CODES;
+            const uint8_t* scales = ring_scales + st * R::SCALES;
             st = st + 1 == kStages ? 0 : st + 1;
 
             float sv[kPair][2][4];
             float2 sc[kPair];
 #pragma unroll
             for (int y = 0; y < kPair; ++y) {
-                sc[y] = *reinterpret_cast<const float2*>(sp0 + y * Pc::BLOCK + Pc::OFF_S + lane * 8);
+                sc[y] = *reinterpret_cast<const float2*>(scales + y * 32 * 8);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) sv[y][i][0] = sv[y][i][1] = sv[y][i][2] = sv[y][i][3] = 0.f;
             }
 #pragma unroll
-            for (int h = 0; h < Pc::KP; ++h)
+            for (int h = 0; h < HD / 64; ++h)
 #pragma unroll
                 for (int y = 0; y < kPair; ++y)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(sp0 + y * Pc::BLOCK + ((i * Pc::KP + h) * 32 + lane) * 16);
+                        const uint4 w = *reinterpret_cast<const uint4*>(codes + 2 * y * R::BLOCK + R::at(key_g + 8 * i, t4 + 4 * h));
                         const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -434,11 +435,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
 #pragma unroll
                 for (int y = 0; y < kPair; ++y) {
                     const float coef = q_unscale[x] * sc[y].x;
-                    // of this lane's keys 0, 1, 8, 9 those below it count; a scale of 0: the block is absent
-                    const int lim = sc[y].x > 0.f ? limit[x] - (blk + y) * kKv8Block - 2 * t4 : 0;
+                    // a scale of 0: the block is absent
+                    const int lim = sc[y].x > 0.f ? limit[x] - (blk + y) * kKv8Block : 0;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        z[y][e] = (e >> 1) * 8 + (e & 1) < lim ? sv[y][e >> 1][2 * x + (e & 1)] * coef : -INFINITY;
+                        z[y][e] = (e & 1 ? key_1 : key_0) + 8 * (e >> 1) < lim ? sv[y][e >> 1][2 * x + (e & 1)] * coef : -INFINITY;
                     mx[y] = fmaxf(fmaxf(z[y][0], z[y][1]), fmaxf(z[y][2], z[y][3]));
                 }
                 float top = fmaxf(mx[0], mx[1]), Top = fmaxf(mx[0] + ev[0], mx[1] + ev[1]);
@@ -486,18 +487,28 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
                 uint32_t vw[4][HD / 32];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint8_t* at = sp0 + y * Pc::BLOCK + Pc::OFF_V + (i * 32 + lane) * Pc::VB;
+                    const int key = (i & 1 ? key_1 : key_0) + 8 * (i >> 1);
+                    const uint8_t* at = codes + (2 * y + 1) * R::BLOCK;
                     if (HD == 128) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(at);
+                        const uint4 w = *reinterpret_cast<const uint4*>(at + R::at(key, g));
                         vw[i][0] = w.x;
                         vw[i][1] = w.y;
                         vw[i][HD / 32 - 2] = w.z;
                         vw[i][HD / 32 - 1] = w.w;
                     } else {
-                        const uint2 w = *reinterpret_cast<const uint2*>(at);
+                        const uint2 w = *reinterpret_cast<const uint2*>(at + R::at(key, g >> 1) + 8 * (g & 1));
                         vw[i][0] = w.x;
                         vw[i][1] = w.y;
                     }
+                }
+                // keys that do not count: whatever their slots hold (a NaN times a weight of 0 is none)
+                const int left = sc[y].x > 0.f ? keys - (blk + y) * kKv8Block : 0;
+                if (left < kKv8Block) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if ((i & 1 ? key_1 : key_0) + 8 * (i >> 1) >= left)
+#pragma unroll
+                            for (int j = 0; j < HD / 32; ++j) vw[i][j] = 0u;
                 }
 #pragma unroll
                 for (int j = 0; j < HD / 32; ++j) {
@@ -515,7 +526,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
             }
         }
         cp_async_wait<0>();
-        __syncthreads();   // the queues are free: the warps' results go over them
+        __syncthreads();   // the rings are empty: the warps' results go over them
 
         // ---- join the four warps: [warp][row][HD] sums and [warp][row] (m, l, M)
         float* s_o = reinterpret_cast<float*>(sm);
@@ -564,7 +575,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
             if (whole) {
                 // L is 0 for a row that saw no key, and NaN when a score was
                 const float f = L == 0.f ? 0.f : exp2f(Mr - mr) / L;
-                bf16* dst = a.out + ((long long)(row0 + q_lo + qi) * a.nq + head * G + hq) * HD + d;
+                bf16* dst = a.out + ((long long)(row0 + qi) * a.nq + head * G + hq) * HD + d;
                 *reinterpret_cast<uint32_t*>(dst) = pack_bf2(x0 * 0x1p-15f * f, x1 * 0x1p-15f * f);
             } else {
                 *reinterpret_cast<float2*>(part + r * HD + d) = make_float2(x0, x1);
@@ -580,7 +591,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const SplitArg
             const long long end = (long long)before[b] * c.n_kv + (long long)(head + 1) * (before[b + 1] - before[b]);
             s.desc[blockIdx.x] = SplitDesc{row0, q_n, head, (int)((end - 1) / share)};
         }
-        __syncthreads();   // the results are read: the queues may be filled again
+        fence_proxy_async_smem();   // the sums below the next copies
+        __syncthreads();            // the results are read: the rings may be filled again
     }
     if (bad_page) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
 }
@@ -651,10 +663,12 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const SplitArgs s) {
 int split_grid() { return 3 * device_sm_count(); }
 
 template <int HD, int NG>
-cudaError_t launch_ng(const SplitArgs& s, int tiles, cudaStream_t st) {
-    constexpr int queue = kWarps * kStages * Piece<HD>::STAGE;
+cudaError_t launch_ng(const SplitArgs& s, cudaStream_t st) {
     constexpr int join = kWarps * 8 * NG * (HD + 3) * 4;
-    constexpr int smem = queue > join ? queue : join;
+    constexpr int smem = (Ring<HD>::BYTES > join ? Ring<HD>::BYTES : join) + 1024;   // aligned up to 1024 bytes
+    alignas(64) CUtensorMap map;
+    if (!make_map_codes(&map, s.a.view.codes, 2LL * s.a.view.n_pages * s.a.view.n_kv * s.a.view.page_size, HD, kKv8Block))
+        return cudaErrorInvalidValue;
     static bool configured[64] = {false};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -665,12 +679,12 @@ cudaError_t launch_ng(const SplitArgs& s, int tiles, cudaStream_t st) {
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
     if (s.whole) {
-        const dim3 grid((unsigned)tiles, (unsigned)s.a.view.n_kv, (unsigned)s.a.batch);
-        HRA_LAUNCH((kv8_attn_kernel<HD, NG>), grid, dim3(kWarps * 32), smem, st, s);
+        const dim3 grid((unsigned)s.a.view.n_kv, (unsigned)s.a.batch);
+        HRA_LAUNCH((kv8_attn_kernel<HD, NG>), grid, dim3(kWarps * 32), smem, st, map, s);
         return cudaGetLastError();
     }
     const dim3 grid((unsigned)split_grid());
-    HRA_LAUNCH((kv8_attn_kernel<HD, NG>), grid, dim3(kWarps * 32), smem, st, s);
+    HRA_LAUNCH((kv8_attn_kernel<HD, NG>), grid, dim3(kWarps * 32), smem, st, map, s);
     HRA_LAUNCH((kv8_join_kernel<HD, NG>), grid, dim3(256), 0, st, s);
     return cudaGetLastError();
 }
@@ -678,11 +692,8 @@ cudaError_t launch_ng(const SplitArgs& s, int tiles, cudaStream_t st) {
 // One n = 8 column group while the rows of a tile fit it, else two.
 int column_groups(int G, int max_new) { return (long long)G * max_new <= 8 ? 1 : 2; }
 
-// Items go whole, one a CTA: while they are short, for tiles of longer sequences (the prompts' fallback), and where
-// the sequences do not fit the table of a CTA.
-bool goes_whole(const Kv8View& c, int batch, int G, int max_new, int max_len, bool prompts) {
-    return max_len <= kWholeUnits * kUnit || (!prompts && (long long)G * max_new > kShortRows) || batch > kMaxBatch;
-}
+// Items go whole, one a CTA, while they are short, and where the sequences do not fit the table of a CTA.
+bool goes_whole(int batch, int max_len) { return max_len <= kWholeUnits * kUnit || batch > kMaxBatch; }
 
 size_t split_scratch(const Kv8View& c, int ng) {
     const size_t grid = (size_t)split_grid();
@@ -693,15 +704,15 @@ size_t split_scratch(const Kv8View& c, int ng) {
 
 size_t kv8_attention_scratch_bytes(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int max_len) {
     const int G = nq / c.n_kv;
-    const bool prompts = (long long)G * max_new > kShortRows && kv8_prompt_supported(c);
-    size_t n = prompts ? (kv8_prompt_scratch_bytes(batch, total_rows, G) + 255) & ~size_t(255) : 0;
-    if (!goes_whole(c, batch, G, max_new, max_len, prompts)) n += split_scratch(c, column_groups(G, max_new));
+    size_t n = 0;
+    if ((long long)G * max_new > kShortRows) n = (kv8_prompt_scratch_bytes(batch, total_rows, G) + 255) & ~size_t(255);
+    if (!goes_whole(batch, max_len)) n += split_scratch(c, column_groups(G, max_new));
     return n;
 }
 
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st) {
     const int G = a.nq / a.view.n_kv;
-    const bool prompts = (long long)G * a.max_new > kShortRows && kv8_prompt_supported(a.view);
+    const bool prompts = (long long)G * a.max_new > kShortRows;
     uint8_t* scratch = reinterpret_cast<uint8_t*>(a.scratch);
     if (prompts) {
         // short sequences go with the prompts unless they may hold many keys
@@ -714,14 +725,12 @@ cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st) {
     s.a = a;
     s.G = G;
     s.max_rows = prompts ? kShortRows : 1 << 30;
-    s.whole = goes_whole(a.view, a.batch, G, a.max_new, a.max_len, prompts) ? 1 : 0;
-    const int ng = column_groups(G, a.max_new);
-    s.QT = 8 * ng / G;
-    const int tiles = prompts ? 1 : (a.max_new + s.QT - 1) / s.QT;
+    s.whole = goes_whole(a.batch, a.max_len) ? 1 : 0;
     s.desc = reinterpret_cast<SplitDesc*>(scratch);
     s.parts = reinterpret_cast<float*>(scratch + split_grid() * sizeof(SplitDesc));
-    if (a.view.head_dim == 128) return ng == 1 ? launch_ng<128, 1>(s, tiles, st) : launch_ng<128, 2>(s, tiles, st);
-    return ng == 1 ? launch_ng<64, 1>(s, tiles, st) : launch_ng<64, 2>(s, tiles, st);
+    const bool one = column_groups(G, a.max_new) == 1;
+    if (a.view.head_dim == 128) return one ? launch_ng<128, 1>(s, st) : launch_ng<128, 2>(s, st);
+    return one ? launch_ng<64, 1>(s, st) : launch_ng<64, 2>(s, st);
 }
 
 }  // namespace hra

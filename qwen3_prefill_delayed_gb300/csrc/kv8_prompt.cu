@@ -726,11 +726,6 @@ size_t kv8_prompt_scratch_bytes(int batch, int total_rows, int G) {
     return ((size_t)total_rows / (TROWS / G) + (size_t)batch + 1) * kRecWords * sizeof(int32_t);
 }
 
-// The rows of the tensor map are counted in 32 bits.
-bool kv8_prompt_supported(const Kv8View& c) {
-    return 2LL * c.n_pages * c.n_kv * c.page_size < (1LL << 31);
-}
-
 cudaError_t launch_kv8_prompt(const Kv8AttnArgs& a, int short_rows, cudaStream_t st) {
     const int G = a.nq / a.view.n_kv, QT = TROWS / G;
     const int tiles = (a.max_new + QT - 1) / QT;

@@ -41,7 +41,8 @@ BAD_CACHE = [(dict(codes=None), -1), (dict(codes=FAKE + 8), -1), (dict(scales=No
              (dict(refs=FAKE + 1), -1), (dict(n_layers=0), -1), (dict(n_pages=0), -1), (dict(n_kv_heads=0), -1),
              (dict(rows=0), -1), (dict(max_pages=-1), -1), (dict(head_dim=96), -2), (dict(page_size=8), -2),
              (dict(page_size=48), -2), (dict(page_size=256), -2), (dict(n_kv_heads=1025), -2), (dict(rows=65536), -2),
-             (dict(max_pages=1 << 27), -2), (dict(n_pages=(1 << 28) + 1), -2)]
+             (dict(max_pages=1 << 27), -2), (dict(n_pages=(1 << 28) + 1), -2), (dict(n_pages=1 << 25), -2),
+             (dict(rows=65535, max_pages=20000), -2)]
 
 
 def _append(hra, cache, layer=0, k=FAKE, v=FAKE, stride=128, cu=FAKE, start=FAKE, batch=2, total=3, max_new=2):
