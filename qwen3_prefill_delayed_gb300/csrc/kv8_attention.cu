@@ -64,7 +64,7 @@ __device__ __forceinline__ void e4m3x4_f16x4(uint32_t w, uint32_t& lo, uint32_t&
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -442,7 +442,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
                         z[y][e] = (e & 1 ? key_1 : key_0) + 8 * (e >> 1) < lim ? sv[y][e >> 1][2 * x + (e & 1)] * coef : -INFINITY;
                     mx[y] = fmaxf(fmaxf(z[y][0], z[y][1]), fmaxf(z[y][2], z[y][3]));
                 }
-                float top = fmaxf(mx[0], mx[1]), Top = fmaxf(mx[0] + ev[0], mx[1] + ev[1]);
+                float top = mx[0], Top = mx[0] + ev[0];
+#pragma unroll
+                for (int y = 1; y < kPair; ++y) {
+                    top = fmaxf(top, mx[y]);
+                    Top = fmaxf(Top, mx[y] + ev[y]);
+                }
 #pragma unroll
                 for (int o2 = 1; o2 < 4; o2 <<= 1) {
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
