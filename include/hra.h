@@ -518,6 +518,33 @@ int hra_kv8_update(const hra_kv8_cache* cache, const int32_t* parents_dev, const
 int hra_kv8_compact(const hra_kv8_cache* cache, int32_t* table_out, int32_t* lens_out, int32_t* refs_out,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* The path over the 8-bit cache: hra_prefill_chunk (start_pos NULL: every prompt from position 0), hra_decode,
+ * hra_decode_dev and hra_ar_frame with a hra_kv8_cache in the place of the bf16 cache, in BF16 weights.  The cache has
+ * the model's n_layers, n_kv_heads and head_dim (else HRA_ERR_INVALID_ARG); batch row b is row b of its table;
+ * positions reach up to max_pages * page_size.  The rows must own pages for the positions a call writes (hra_kv8_update
+ * with room): a missing one drops the token's K and V (HRA_DEVERR_PAGE_RANGE in cache->errors).  Each layer's K and V
+ * are quantised from their bf16 rounding, and its attention reads them from the cache, the new tokens' included.
+ * cache->lens is set to the positions each row holds.  The error word of the pass itself stays the workspace's. */
+size_t hra_prefill_kv8_workspace_size(const hra_dims* dims, const hra_kv8_cache* cache, int32_t batch,
+                                      int32_t total_tokens, int32_t max_len, int32_t max_end);
+int hra_prefill_kv8(const hra_dims* dims, const hra_weights* weights, const int32_t* tokens_dev,
+                    const int32_t* seq_lens, const int32_t* start_pos, int32_t batch, int32_t max_len,
+                    const hra_kv8_cache* cache, void* last_hidden_dev, void* workspace, size_t workspace_bytes,
+                    uint32_t flags, void* stream);
+size_t hra_decode_kv8_workspace_size(const hra_dims* dims, const hra_kv8_cache* cache, int32_t batch);
+int hra_decode_kv8(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev, const int32_t* pos,
+                   int32_t batch, const hra_kv8_cache* cache, void* hidden_dev, void* workspace,
+                   size_t workspace_bytes, void* stream);
+int hra_decode_dev_kv8(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev, int32_t* pos_dev,
+                       int32_t pos_bound, int32_t advance, int32_t batch, const hra_kv8_cache* cache,
+                       void* hidden_dev, void* workspace, size_t workspace_bytes, void* stream);
+int hra_ar_frame_kv8(const hra_dims* dims, const hra_weights* weights, const void* head_w_dev,
+                     const void* code_emb_dev, hra_delay_state* state_dev, const float* eoc_bias_dev,
+                     const hra_sampling* sampling, const uint64_t* seeds_dev, void* hidden_dev, int32_t* pos_dev,
+                     int32_t pos_bound, int32_t batch, const hra_kv8_cache* cache, int32_t* codes_dev,
+                     void* next_emb_dev, int32_t* done_dev, void* backbone_ws, size_t backbone_ws_bytes,
+                     void* codebook_ws, size_t codebook_ws_bytes, void* stream);
+
 /* ---- measurement ---------------------------------------------------------------------------- */
 /* Number of kernels the library has launched in this process (host-side count). */
 uint64_t hra_launch_counter(void);

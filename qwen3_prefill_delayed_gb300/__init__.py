@@ -42,7 +42,8 @@ EXPORTED = ["hra_prefill_workspace_size", "hra_prefill", "hra_prefill_chunk_work
             "hra_nvfp4_band_scales",
             "hra_prefill_nvfp4_workspace_size", "hra_prefill_nvfp4",
             "hra_kv8_append", "hra_kv8_attention_workspace_size", "hra_kv8_attention", "hra_kv8_pages_workspace_size",
-            "hra_kv8_update", "hra_kv8_compact",
+            "hra_kv8_update", "hra_kv8_compact", "hra_prefill_kv8_workspace_size", "hra_prefill_kv8",
+            "hra_decode_kv8_workspace_size", "hra_decode_kv8", "hra_decode_dev_kv8", "hra_ar_frame_kv8",
             "hra_launch_counter", "hra_probe_select", "hra_probe_collect", "hra_set_decode_pass",
             "hra_set_gemm_pairs", "hra_device_error", "hra_status_string"]
 PROBE = {"none": 0, "qkv": 1, "o_proj": 2, "gate_up": 3, "down": 4, "attention": 5, "audio_head": 6,
@@ -179,7 +180,18 @@ def lib() -> ctypes.CDLL:
         L.hra_kv8_pages_workspace_size.restype = sz
         L.hra_kv8_update.argtypes = [kp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.hra_kv8_compact.argtypes = [kp, vp, vp, vp, vp, sz, vp]
-        for f in ("hra_kv8_append", "hra_kv8_attention", "hra_kv8_update", "hra_kv8_compact"):
+        L.hra_prefill_kv8_workspace_size.argtypes = [dp, kp, i32, i32, i32, i32]
+        L.hra_prefill_kv8_workspace_size.restype = sz
+        L.hra_prefill_kv8.argtypes = [dp, ctypes.POINTER(HraWeights), vp, ctypes.POINTER(i32), ctypes.POINTER(i32), i32,
+                                      i32, kp, vp, vp, sz, u32, vp]
+        L.hra_decode_kv8_workspace_size.argtypes = [dp, kp, i32]
+        L.hra_decode_kv8_workspace_size.restype = sz
+        L.hra_decode_kv8.argtypes = [dp, ctypes.POINTER(HraWeights), vp, ctypes.POINTER(i32), i32, kp, vp, vp, sz, vp]
+        L.hra_decode_dev_kv8.argtypes = [dp, ctypes.POINTER(HraWeights), vp, vp, i32, i32, i32, kp, vp, vp, sz, vp]
+        L.hra_ar_frame_kv8.argtypes = [dp, ctypes.POINTER(HraWeights), vp, vp, vp, vp, ctypes.POINTER(HraSampling), vp,
+                                       vp, vp, i32, i32, kp, vp, vp, vp, vp, sz, vp, sz, vp]
+        for f in ("hra_kv8_append", "hra_kv8_attention", "hra_kv8_update", "hra_kv8_compact", "hra_prefill_kv8",
+                  "hra_decode_kv8", "hra_decode_dev_kv8", "hra_ar_frame_kv8"):
             getattr(L, f).restype = ctypes.c_int
         L.hra_linear_workspace_size.argtypes = [i32, i32, i32, i32, i32]
         L.hra_linear_workspace_size.restype = sz
@@ -292,12 +304,26 @@ class Backbone:
         """hra_prefill: tokens int32 [B, P_max] (CUDA), seq_lens host ints -> last hidden [B, H].
 
         With start_pos (host ints), hra_prefill_chunk: row b's tokens sit at positions
-        start_pos[b] .. start_pos[b] + seq_lens[b] - 1 after the ones already in the cache."""
+        start_pos[b] .. start_pos[b] + seq_lens[b] - 1 after the ones already in the cache.
+
+        With a Kv8Cache, hra_prefill_kv8; the rows must own pages for these positions (Kv8Cache.update)."""
         B, P = tokens.shape
         lens = (ctypes.c_int32 * B)(*[int(x) for x in seq_lens])
         if out is None:
             out = torch.empty(B, self.d.hidden, dtype=torch.bfloat16, device=tokens.device)
         flags = PREFILL_FULL_LAST_LAYER if full_last_layer else 0
+        if isinstance(cache, Kv8Cache):
+            starts = None if start_pos is None else (ctypes.c_int32 * B)(*[int(x) for x in start_pos])
+            max_end = max(int(n) + (0 if start_pos is None else int(start_pos[b])) for b, n in enumerate(seq_lens))
+            need = lib().hra_prefill_kv8_workspace_size(ctypes.byref(self.dims), cache.ref, B, int(sum(seq_lens)), P, max_end)
+            ws = workspace if workspace is not None else self.ws.get(need, tokens.device)
+            rc = lib().hra_prefill_kv8(ctypes.byref(self.dims), ctypes.byref(self.table),
+                                       _ptr(tokens, torch.int32, "tokens"), lens, starts, B, P, cache.ref,
+                                       _ptr(out, torch.bfloat16, "last_hidden"), _ptr(ws, None, "workspace"), ws.numel(),
+                                       flags, _stream(stream))
+            _check(rc, "hra_prefill_kv8")
+            self.last_ws = ws
+            return out
         kv = self.kv(cache)
         if start_pos is None:
             need = self.prefill_workspace_size(B, int(sum(seq_lens)), P)
@@ -325,12 +351,21 @@ class Backbone:
                    advance: bool = True, out: Optional[torch.Tensor] = None,
                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """hra_decode_dev: positions in the CUDA int32 tensor `pos` (advanced in place when
-        `advance`); pos_bound is a host upper bound of every position."""
+        `advance`); pos_bound is a host upper bound of every position.  With a Kv8Cache, hra_decode_dev_kv8."""
         B = in_emb.shape[0]
         if out is None:
             out = torch.empty(B, self.d.hidden, dtype=torch.bfloat16, device=in_emb.device)
-        need = self.decode_workspace_size(B, cache.shape[4])
+        need = self._decode_need(B, cache)
         ws = workspace if workspace is not None else self.ws.get(need, in_emb.device)
+        if isinstance(cache, Kv8Cache):
+            rc = lib().hra_decode_dev_kv8(ctypes.byref(self.dims), ctypes.byref(self.table),
+                                          _ptr(in_emb, torch.bfloat16, "in_emb"), _ptr(pos, torch.int32, "pos"),
+                                          int(pos_bound), 1 if advance else 0, B, cache.ref,
+                                          _ptr(out, torch.bfloat16, "hidden"), _ptr(ws, None, "workspace"), ws.numel(),
+                                          _stream(stream))
+            _check(rc, "hra_decode_dev_kv8")
+            self.last_ws = ws
+            return out
         kv = self.kv(cache)
         rc = lib().hra_decode_dev(ctypes.byref(self.dims), ctypes.byref(self.table),
                                   _ptr(in_emb, torch.bfloat16, "in_emb"), _ptr(pos, torch.int32, "pos"),
@@ -341,19 +376,32 @@ class Backbone:
         self.last_ws = ws
         return out
 
+    def _decode_need(self, batch, cache) -> int:
+        if isinstance(cache, Kv8Cache):
+            return lib().hra_decode_kv8_workspace_size(ctypes.byref(self.dims), cache.ref, batch)
+        return self.decode_workspace_size(batch, cache.shape[4])
+
     def decode_workspace_size(self, batch, n_slots) -> int:
         return lib().hra_decode_workspace_size(ctypes.byref(self.dims), batch, n_slots)
 
     def decode(self, in_emb: torch.Tensor, pos: Sequence[int], cache: torch.Tensor,
                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
-        """hra_decode: in_emb bf16 [B, H] (CUDA), pos host ints -> hidden [B, H]."""
+        """hra_decode: in_emb bf16 [B, H] (CUDA), pos host ints -> hidden [B, H].  With a Kv8Cache, hra_decode_kv8."""
         B = in_emb.shape[0]
         p = (ctypes.c_int32 * B)(*[int(x) for x in pos])
         if out is None:
             out = torch.empty(B, self.d.hidden, dtype=torch.bfloat16, device=in_emb.device)
-        need = self.decode_workspace_size(B, cache.shape[4])
+        need = self._decode_need(B, cache)
         ws = workspace if workspace is not None else self.ws.get(need, in_emb.device)
+        if isinstance(cache, Kv8Cache):
+            rc = lib().hra_decode_kv8(ctypes.byref(self.dims), ctypes.byref(self.table),
+                                      _ptr(in_emb, torch.bfloat16, "in_emb"), p, B, cache.ref,
+                                      _ptr(out, torch.bfloat16, "hidden"), _ptr(ws, None, "workspace"), ws.numel(),
+                                      _stream(stream))
+            _check(rc, "hra_decode_kv8")
+            self.last_ws = ws
+            return out
         kv = self.kv(cache)
         rc = lib().hra_decode(ctypes.byref(self.dims), ctypes.byref(self.table),
                               _ptr(in_emb, torch.bfloat16, "in_emb"), p, B, ctypes.byref(kv),
@@ -371,7 +419,8 @@ class ARLoop:
     `replay()` runs them with a single launch from the host.
 
     pos0: host ints, the position of each row's first decoded frame (its prompt length); pos_bound
-    (host) must cover every position the loop will reach."""
+    (host) must cover every position the loop will reach.  cache: the bf16 tensor, or a Kv8Cache (hra_ar_frame_kv8) whose
+    rows own pages for those positions."""
 
     def __init__(self, bb: "Backbone", head: "AudioHead", cache: torch.Tensor, hidden: torch.Tensor,
                  pos0: Sequence[int], pos_bound: int, eoc_bias: Optional[torch.Tensor] = None,
@@ -392,9 +441,10 @@ class ARLoop:
         self.codes = torch.empty(B, d.n_codebooks, dtype=torch.int32, device=dev)
         self.next_emb = torch.empty(B, d.hidden, dtype=torch.bfloat16, device=dev)
         self.done = torch.empty(B, dtype=torch.int32, device=dev)
-        self.bws = torch.empty(bb.decode_workspace_size(B, cache.shape[4]), dtype=torch.uint8, device=dev)
+        self.bws = torch.empty(bb._decode_need(B, cache), dtype=torch.uint8, device=dev)
         self.cws = torch.empty(head.workspace_size(B), dtype=torch.uint8, device=dev)
-        self.kv = bb.kv(cache)
+        self.paged = isinstance(cache, Kv8Cache)
+        self.kv = cache.ref if self.paged else ctypes.byref(bb.kv(cache))
         self.graph = None
 
     def frame(self, codes: Optional[torch.Tensor] = None, done: Optional[torch.Tensor] = None,
@@ -404,7 +454,8 @@ class ARLoop:
         codes = self.codes if codes is None else codes
         done = self.done if done is None else done
         bias = self.eoc_bias if eoc_bias is None else eoc_bias
-        rc = lib().hra_ar_frame(ctypes.byref(self.bb.dims), ctypes.byref(self.bb.table),
+        name = "hra_ar_frame_kv8" if self.paged else "hra_ar_frame"
+        rc = getattr(lib(), name)(ctypes.byref(self.bb.dims), ctypes.byref(self.bb.table),
                                 _ptr(self.head.head_w, torch.bfloat16, "head_w"),
                                 _ptr(self.head.code_emb, torch.bfloat16, "code_emb"),
                                 _ptr(self.state, torch.int32, "state"),
@@ -412,12 +463,12 @@ class ARLoop:
                                 ctypes.byref(self.sampling) if self.sampling is not None else None,
                                 _ptr(self.seeds, torch.int64, "seeds"),
                                 _ptr(self.hidden, torch.bfloat16, "hidden"), _ptr(self.pos, torch.int32, "pos"),
-                                self.pos_bound, self.B, ctypes.byref(self.kv),
+                                self.pos_bound, self.B, self.kv,
                                 _ptr(codes, torch.int32, "codes"), _ptr(self.next_emb, torch.bfloat16, "next_emb"),
                                 _ptr(done, torch.int32, "done"), _ptr(self.bws, None, "backbone workspace"),
                                 self.bws.numel(), _ptr(self.cws, None, "codebook workspace"), self.cws.numel(),
                                 _stream(stream))
-        _check(rc, "hra_ar_frame")
+        _check(rc, name)
         return codes, done
 
     def capture(self, n_frames: int, eoc_bias_seq: Optional[torch.Tensor] = None) -> None:
@@ -806,7 +857,7 @@ class Kv8Cache:
         self.struct = HraKv8Cache(p_codes.value, p_scales.value, p_table.value, p_lens.value,
                                   p_refs.value if p_refs is not None else None, self.errors.data_ptr(), n_layers, n_pages,
                                   n_kv, hd, page, self.rows, self.max_pages)
-        self._ref = ctypes.byref(self.struct)
+        self._ref = self.ref = ctypes.byref(self.struct)
         self._index = codes.get_device()
         L = lib()
         self._append, self._attend = L.hra_kv8_append, L.hra_kv8_attention

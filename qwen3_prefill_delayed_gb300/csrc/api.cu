@@ -22,6 +22,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "kv8_host.h"
 
 using namespace hra;
 
@@ -77,8 +78,15 @@ struct Region {
 struct Layout {
     size_t err, row_seq, row_pos, cu, last_row, start, rope, r, y, qkv, q, att, h, rl, part, apart, x8, xs, sync, asched,
         total;
+    size_t stage, kv_len, one_each, q_last, kscratch;   // paged 8-bit cache only
     size_t part_bytes;
     int attn_splits;
+};
+
+// The 8-bit cache a pass runs on and its host bounds: most new tokens of a sequence, most positions.
+struct Kv8Pass {
+    const hra_kv8_cache* cache;
+    int max_new, max_end;
 };
 
 bool dims_ok(const hra_dims* d) {
@@ -106,7 +114,7 @@ bool audio_dims_ok(const hra_dims* d) {
 // Shared plan of the backbone passes.  `rows` = packed rows that run the full layers, `last_rows`
 // = rows of the last-layer tail (batch), `rope_rows` = rows of the RoPE table.
 Layout backbone_layout(const hra_dims& d, int batch, int rows, int rope_rows, int max_pos, bool fp8 = false,
-                      bool nvfp4 = false) {
+                      bool nvfp4 = false, const Kv8Pass* k8 = nullptr) {
     const size_t H = d.hidden, hd = d.head_dim, Dq = (size_t)d.n_q_heads * hd;
     const size_t Dqkv = (size_t)(d.n_q_heads + 2 * d.n_kv_heads) * hd, F = d.ffn;
     const size_t T = (size_t)std::max(rows, batch);
@@ -146,6 +154,16 @@ Layout backbone_layout(const hra_dims& d, int batch, int rows, int rope_rows, in
     L.sync = g.take(decode_pass_sync_bytes((int)std::min<size_t>(T, 64), d.n_kv_heads, (int)F, (int)H));
     // the prefill attention's work list (built once per call)
     L.asched = g.take(attention_schedule_bytes((int)T, batch));
+    if (k8 != nullptr) {
+        // the layer's new K/V in bf16 by row, the sequences' lengths, and the attention's scratch
+        const Kv8View v = kv8_view(*k8->cache, 0);
+        L.stage = g.take(T * 2 * d.n_kv_heads * hd * 2);
+        L.kv_len = g.take((size_t)batch * 4);
+        L.one_each = g.take((size_t)(batch + 1) * 4);
+        L.q_last = g.take((size_t)batch * Dq * 2);
+        L.kscratch = g.take(std::max(kv8_attention_scratch_bytes(v, batch, (int)T, d.n_q_heads, k8->max_new, k8->max_end),
+                                     kv8_attention_scratch_bytes(v, batch, batch, d.n_q_heads, 1, k8->max_end)) + 16);
+    }
     L.total = g.off;
     return L;
 }
@@ -277,7 +295,7 @@ int run_layers(const hra_dims& d, const hra_weights& w, const hra_kv_cache& kv, 
                int rows, int batch, int max_len, bool prefill, bool full_last, bf16* out_hidden,
                const int32_t* seq_lens_host, int max_pos, cudaStream_t st, int rope_rows = 0,
                const int32_t* start_host = nullptr, const hra_fp8_layer* fp8 = nullptr, float* amax = nullptr,
-               const hra_nvfp4_layer* nv4 = nullptr) {
+               const hra_nvfp4_layer* nv4 = nullptr, const Kv8Pass* k8 = nullptr) {
     const int H = d.hidden, hd = d.head_dim, nq = d.n_q_heads, nkv = d.n_kv_heads, F = d.ffn;
     const int Dq = nq * hd, Dqkv = (nq + 2 * nkv) * hd;
     const float eps = d.rms_eps;
@@ -299,14 +317,14 @@ int run_layers(const hra_dims& d, const hra_weights& w, const hra_kv_cache& kv, 
     for (int b = 0; b < batch && seq_lens_host != nullptr; ++b) {
         const double n = (double)seq_lens_host[b];
         const double s0 = start_host ? (double)start_host[b] : 0.0;
-        attn_work += prefill ? 4.0 * nq * hd * (n * s0 + n * (n + 1.0) / 2.0) : 4.0 * nkv * hd * (n + 1.0);
+        attn_work += prefill ? 4.0 * nq * hd * (n * s0 + n * (n + 1.0) / 2.0) : (k8 ? 2.0 : 4.0) * nkv * hd * (n + 1.0);
     }
     const int lin_probe = prefill ? 0 : HRA_PROBE_DECODE_LINEAR;
 
     // At most 64 rows in BF16, when selected (hra_set_decode_pass): the whole pass is one persistent
     // kernel (decode_pass.cu).  Every row runs every layer; the final norm goes to the last row of
     // each sequence (prefill) or to every row (decode).
-    if (g_decode_pass_enabled && rows <= 64 && fp8 == nullptr && amax == nullptr && nv4 == nullptr &&
+    if (g_decode_pass_enabled && k8 == nullptr && rows <= 64 && fp8 == nullptr && amax == nullptr && nv4 == nullptr &&
         d.n_layers <= kDecodePassMaxLayers) {
         DecodePassCall c{};
         for (int l = 0; l < d.n_layers; ++l) {
@@ -365,9 +383,31 @@ int run_layers(const hra_dims& d, const hra_weights& w, const hra_kv_cache& kv, 
 
     // the prefill attention's work list: the same sequences for every layer (a single sequence needs
     // none: its query tiles in order)
-    if (prefill && batch > 1 && (d.n_layers > 1 || full_last))
+    if (prefill && k8 == nullptr && batch > 1 && (d.n_layers > 1 || full_last))
         HRA_TRY(launch_attention_schedule(P.at<int32_t>(L.cu), P.at<int32_t>(L.start), batch, max_len, nq, nkv,
                                           P.at<int32_t>(L.asched), st));
+
+    // the 8-bit cache: each layer's new K/V in bf16 to the staging rows, from there into the pages, then
+    // attention of `n` rows of q over the pages
+    auto attend8 = [&](int l, const bf16* q_rows, const int32_t* cu, int n, int max_new, bf16* out) {
+        Kv8AttnArgs a{};
+        a.view = kv8_view(*k8->cache, l);
+        a.q = q_rows;
+        a.row_stride = Dq;
+        a.out = out;
+        a.cu = cu;
+        a.kv_len = P.at<int32_t>(L.kv_len);
+        a.scale_log2 = (1.0f / sqrtf((float)hd)) * 1.4426950408889634f;
+        a.batch = batch;
+        a.total_rows = n;
+        a.nq = nq;
+        a.max_new = max_new;
+        a.max_len = k8->max_end;
+        a.scratch = P.at<uint8_t>(L.kscratch);
+        return launch_kv8_attention(a, st);
+    };
+    if (k8 != nullptr)
+        HRA_TRY(launch_kv8_lens(row_pos, last_row, batch, P.at<int32_t>(L.kv_len), P.at<int32_t>(L.one_each), st));
 
     for (int l = 0; l < d.n_layers; ++l) {
         const hra_layer_weights& lw = w.layers[l];
@@ -393,14 +433,37 @@ int run_layers(const hra_dims& d, const hra_weights& w, const hra_kv_cache& kv, 
         qa.nkv = nkv;
         qa.hd = hd;
         qa.eps = eps;
+        if (k8 != nullptr) {
+            qa.kv_layer = P.at<bf16>(L.stage);
+            qa.n_slots = 1;
+            qa.kv_by_row = 1;
+        }
         bool qk_done = false;
         HRA_TRY(linear(y, lw.w_qkv, qkv, rows, Dqkv, H, EPI_STORE, P, L, st, prefill ? HRA_PROBE_QKV : lin_probe, nullptr,
                        nullptr, 0.f, nullptr, 0, &qa, &qk_done, qcp, PROJ_QKV));
         if (!qk_done) HRA_TRY(launch_qk_rope_kv(qa, st));
+        if (k8 != nullptr) {
+            Kv8AppendArgs ap{};
+            ap.view = kv8_view(*k8->cache, l);
+            ap.k = P.at<bf16>(L.stage);
+            ap.v = ap.k + nkv * hd;
+            ap.row_stride = 2LL * nkv * hd;
+            ap.cu = prefill ? P.at<int32_t>(L.cu) : P.at<int32_t>(L.one_each);
+            ap.start = prefill ? P.at<int32_t>(L.start) : row_pos;
+            ap.lens = last ? k8->cache->lens : nullptr;
+            ap.batch = batch;
+            ap.total_rows = rows;
+            ap.max_new = k8->max_new;
+            HRA_TRY(launch_kv8_append(ap, st));
+        }
 
         const bool tail = prefill && last && !full_last;
         if (!tail) {
-            if (prefill) {
+            if (k8 != nullptr) {
+                HRA_TRY(probed(prefill ? HRA_PROBE_ATTENTION : HRA_PROBE_DECODE_ATTENTION, attn_work, st, [&] {
+                    return attend8(l, q, prefill ? P.at<int32_t>(L.cu) : P.at<int32_t>(L.one_each), rows, k8->max_new, att);
+                }));
+            } else if (prefill) {
                 PrefillAttnArgs pa{q, kvl, P.at<int32_t>(L.cu), P.at<int32_t>(L.start), att, batch, max_len,
                                    kv.n_slots, nq, nkv, hd, rows, kv.batch, P.at<unsigned int>(L.err),
                                    batch > 1 ? P.at<int32_t>(L.asched) : nullptr};
@@ -446,6 +509,11 @@ int run_layers(const hra_dims& d, const hra_weights& w, const hra_kv_cache& kv, 
             }
         } else {
             // last prefill layer, rows that feed the last hidden only
+            if (k8 != nullptr) {
+                bf16* q_last = P.at<bf16>(L.q_last);
+                HRA_TRY(launch_rmsnorm(q, last_row, nullptr, nullptr, q_last, batch, Dq, eps, st));   // gather
+                HRA_TRY(attend8(l, q_last, P.at<int32_t>(L.one_each), batch, 1, att));
+            }
             DecodeAttnArgs da{};
             da.q = q;
             da.kv_layer = kvl;
@@ -461,7 +529,7 @@ int run_layers(const hra_dims& d, const hra_weights& w, const hra_kv_cache& kv, 
             da.nkv = nkv;
             da.hd = hd;
             da.splits = std::min(L.attn_splits, decode_attention_splits(batch, nkv, max_pos));
-            HRA_TRY(launch_decode_attention(da, st));
+            if (k8 == nullptr) HRA_TRY(launch_decode_attention(da, st));
             HRA_TRY(launch_rmsnorm(r, last_row, nullptr, nullptr, rl, batch, H, eps, st));   // gather
             HRA_TRY(linear(att, lw.w_o, rl, batch, H, Dq, EPI_RESIDUAL, P, L, st, 0, lw.mlp_norm, y, eps, nullptr, 0,
                            nullptr, nullptr, qcp, PROJ_O));
@@ -479,6 +547,18 @@ bool weights_ok(const hra_dims& d, const hra_weights* w) {
     for (int l = 0; l < d.n_layers; ++l)
         if (!layer_ptrs_ok(w->layers[l])) return false;
     return true;
+}
+
+// The 8-bit cache as the model's: its rows and positions in the terms of a bf16 cache.
+int kv8_for_model(const hra_dims& d, const hra_kv8_cache* c, hra_kv_cache& as) {
+    const int rc = kv8_check(c);
+    if (rc != HRA_OK) return rc;
+    if (c->n_layers != d.n_layers || c->n_kv_heads != d.n_kv_heads || c->head_dim != d.head_dim)
+        return HRA_ERR_INVALID_ARG;
+    as.base = nullptr;
+    as.batch = c->rows;
+    as.n_slots = c->max_pages * c->page_size;
+    return HRA_OK;
 }
 
 bool kv_ok(const hra_kv_cache* kv) {
@@ -550,14 +630,21 @@ int prefill_impl(const hra_dims* dims, const hra_weights* weights, const int32_t
                  const int32_t* start_pos, int32_t batch, int32_t max_len, const hra_kv_cache* kv,
                  void* last_hidden_dev, void* workspace, size_t workspace_bytes, uint32_t flags, void* stream,
                  const hra_fp8_layer* fp8 = nullptr, float* amax = nullptr, bool validate_only = false,
-                 const hra_nvfp4_layer* nv4 = nullptr) {
-    if (dims == nullptr || weights == nullptr || tokens_dev == nullptr || seq_lens == nullptr || kv == nullptr)
+                 const hra_nvfp4_layer* nv4 = nullptr, const hra_kv8_cache* kv8 = nullptr) {
+    if (dims == nullptr || weights == nullptr || tokens_dev == nullptr || seq_lens == nullptr ||
+        (kv == nullptr && kv8 == nullptr))
         return HRA_ERR_INVALID_ARG;
     if (!dims_ok(dims)) return HRA_ERR_UNSUPPORTED;
     const hra_dims& d = *dims;
     if (batch < 1 || batch > kMaxBatch || max_len < 1) return HRA_ERR_INVALID_ARG;
-    if (!aligned16(weights->embed) || !weights_ok(d, weights) || !kv_ok(kv) || !aligned16(last_hidden_dev) ||
-        !aligned16(workspace) || (reinterpret_cast<uintptr_t>(tokens_dev) & 3u) != 0)
+    hra_kv_cache paged{};   // the 8-bit cache's rows and positions, for the checks below
+    if (kv8 != nullptr) {
+        const int rc = kv8_for_model(d, kv8, paged);
+        if (rc != HRA_OK) return rc;
+        kv = &paged;
+    }
+    if (!aligned16(weights->embed) || !weights_ok(d, weights) || (kv8 == nullptr && !kv_ok(kv)) ||
+        !aligned16(last_hidden_dev) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(tokens_dev) & 3u) != 0)
         return HRA_ERR_INVALID_ARG;
     if (batch > kv->batch) return HRA_ERR_INVALID_ARG;
     SeqMeta meta{};
@@ -598,7 +685,9 @@ int prefill_impl(const hra_dims* dims, const hra_weights* weights, const int32_t
                 if (!aligned16(f.codes[p]) || f.scales[p] == nullptr) return HRA_ERR_INVALID_ARG;
         }
     }
-    const Layout L = backbone_layout(d, batch, (int)T, max_end, max_end - 1, fp8 != nullptr, nv4 != nullptr);
+    const Kv8Pass pass{kv8, max_len, max_end};
+    const Kv8Pass* k8 = kv8 != nullptr ? &pass : nullptr;
+    const Layout L = backbone_layout(d, batch, (int)T, max_end, max_end - 1, fp8 != nullptr, nv4 != nullptr, k8);
     if (workspace_bytes < L.total) return HRA_ERR_WORKSPACE;
     if (validate_only) return HRA_OK;
 
@@ -615,10 +704,29 @@ int prefill_impl(const hra_dims* dims, const hra_weights* weights, const int32_t
                                  P.at<bf16>(L.y), (int)T, d.hidden, d.rms_eps, P.at<unsigned int>(L.err), st));
     return run_layers(d, *weights, *kv, P, L, (int)T, batch, max_len, true,
                       (flags & HRA_PREFILL_FULL_LAST_LAYER) != 0, reinterpret_cast<bf16*>(last_hidden_dev), seq_lens,
-                      max_end - 1, st, max_end, start_pos, fp8, amax, nv4);
+                      max_end - 1, st, max_end, start_pos, fp8, amax, nv4, k8);
 }
 
 }  // namespace
+
+size_t hra_prefill_kv8_workspace_size(const hra_dims* dims, const hra_kv8_cache* cache, int32_t batch,
+                                      int32_t total_tokens, int32_t max_len, int32_t max_end) {
+    hra_kv_cache paged{};
+    if (!dims_ok(dims) || kv8_for_model(*dims, cache, paged) != HRA_OK || batch < 1 || total_tokens < batch ||
+        max_len < 1 || max_end < 1 || max_end > paged.n_slots)
+        return 0;
+    const Kv8Pass pass{cache, max_len, max_end};
+    return backbone_layout(*dims, batch, total_tokens, max_end, max_end - 1, false, false, &pass).total;
+}
+
+int hra_prefill_kv8(const hra_dims* dims, const hra_weights* weights, const int32_t* tokens_dev,
+                    const int32_t* seq_lens, const int32_t* start_pos, int32_t batch, int32_t max_len,
+                    const hra_kv8_cache* cache, void* last_hidden_dev, void* workspace, size_t workspace_bytes,
+                    uint32_t flags, void* stream) {
+    if (cache == nullptr) return HRA_ERR_INVALID_ARG;
+    return prefill_impl(dims, weights, tokens_dev, seq_lens, start_pos, batch, max_len, nullptr, last_hidden_dev,
+                        workspace, workspace_bytes, flags, stream, nullptr, nullptr, false, nullptr, cache);
+}
 
 int hra_prefill(const hra_dims* dims, const hra_weights* weights, const int32_t* tokens_dev,
                 const int32_t* seq_lens, int32_t batch, int32_t max_len, const hra_kv_cache* kv,
@@ -798,14 +906,21 @@ namespace {
 // pos_bound, a host upper bound of every position, for the attention split count.
 int decode_impl(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev, const int32_t* pos_host,
                 int32_t* pos_dev, int32_t pos_bound, int advance, int32_t batch, const hra_kv_cache* kv,
-                void* hidden_dev, void* workspace, size_t workspace_bytes, void* stream, bool validate_only = false) {
-    if (dims == nullptr || weights == nullptr || in_emb_dev == nullptr || kv == nullptr ||
+                void* hidden_dev, void* workspace, size_t workspace_bytes, void* stream, bool validate_only = false,
+                const hra_kv8_cache* kv8 = nullptr) {
+    if (dims == nullptr || weights == nullptr || in_emb_dev == nullptr || (kv == nullptr && kv8 == nullptr) ||
         (pos_host == nullptr && pos_dev == nullptr))
         return HRA_ERR_INVALID_ARG;
     if (!dims_ok(dims)) return HRA_ERR_UNSUPPORTED;
     const hra_dims& d = *dims;
     if (batch < 1 || batch > kMaxBatch) return HRA_ERR_INVALID_ARG;
-    if (!weights_ok(d, weights) || !kv_ok(kv) || !aligned16(in_emb_dev) || !aligned16(hidden_dev) ||
+    hra_kv_cache paged{};   // the 8-bit cache's rows and positions, for the checks below
+    if (kv8 != nullptr) {
+        const int rc = kv8_for_model(d, kv8, paged);
+        if (rc != HRA_OK) return rc;
+        kv = &paged;
+    }
+    if (!weights_ok(d, weights) || (kv8 == nullptr && !kv_ok(kv)) || !aligned16(in_emb_dev) || !aligned16(hidden_dev) ||
         !aligned16(workspace) || (pos_dev != nullptr && (reinterpret_cast<uintptr_t>(pos_dev) & 3u) != 0))
         return HRA_ERR_INVALID_ARG;
     if (batch > kv->batch) return HRA_ERR_INVALID_ARG;
@@ -827,7 +942,8 @@ int decode_impl(const hra_dims* dims, const hra_weights* weights, const void* in
         meta.advance = advance ? 1 : 0;
         max_pos = pos_bound;
     }
-    const Layout L = backbone_layout(d, batch, batch, batch, kv->n_slots - 1);
+    const Kv8Pass whole{kv8, 1, kv->n_slots}, pass{kv8, 1, max_pos + 1};
+    const Layout L = backbone_layout(d, batch, batch, batch, kv->n_slots - 1, false, false, kv8 ? &whole : nullptr);
     if (workspace_bytes < L.total) return HRA_ERR_WORKSPACE;
     if (validate_only) return HRA_OK;
 
@@ -843,10 +959,33 @@ int decode_impl(const hra_dims* dims, const hra_weights* weights, const void* in
                            reinterpret_cast<const bf16*>(weights->layers[0].attn_norm), P.at<bf16>(L.y),
                            P.at<bf16>(L.r), batch, d.hidden, d.rms_eps, st));
     return run_layers(d, *weights, *kv, P, L, batch, batch, 0, false, false, reinterpret_cast<bf16*>(hidden_dev),
-                      pos_host, max_pos, st);
+                      pos_host, max_pos, st, 0, nullptr, nullptr, nullptr, nullptr, kv8 ? &pass : nullptr);
 }
 
 }  // namespace
+
+size_t hra_decode_kv8_workspace_size(const hra_dims* dims, const hra_kv8_cache* cache, int32_t batch) {
+    hra_kv_cache paged{};
+    if (!dims_ok(dims) || kv8_for_model(*dims, cache, paged) != HRA_OK || batch < 1) return 0;
+    const Kv8Pass pass{cache, 1, paged.n_slots};
+    return backbone_layout(*dims, batch, batch, batch, paged.n_slots - 1, false, false, &pass).total;
+}
+
+int hra_decode_kv8(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev, const int32_t* pos,
+                   int32_t batch, const hra_kv8_cache* cache, void* hidden_dev, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+    if (pos == nullptr || cache == nullptr) return HRA_ERR_INVALID_ARG;
+    return decode_impl(dims, weights, in_emb_dev, pos, nullptr, 0, 0, batch, nullptr, hidden_dev, workspace,
+                       workspace_bytes, stream, false, cache);
+}
+
+int hra_decode_dev_kv8(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev, int32_t* pos_dev,
+                       int32_t pos_bound, int32_t advance, int32_t batch, const hra_kv8_cache* cache, void* hidden_dev,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    if (pos_dev == nullptr || cache == nullptr) return HRA_ERR_INVALID_ARG;
+    return decode_impl(dims, weights, in_emb_dev, nullptr, pos_dev, pos_bound, advance, batch, nullptr, hidden_dev,
+                       workspace, workspace_bytes, stream, false, cache);
+}
 
 int hra_decode(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev, const int32_t* pos,
                int32_t batch, const hra_kv_cache* kv, void* hidden_dev, void* workspace, size_t workspace_bytes,
@@ -1009,15 +1148,18 @@ int hra_codebook_step_sampled(const hra_dims* dims, const void* hidden_dev, cons
                          false);
 }
 
-int hra_ar_frame(const hra_dims* dims, const hra_weights* weights, const void* head_w_dev, const void* code_emb_dev,
+namespace {
+
+int ar_frame_impl(const hra_dims* dims, const hra_weights* weights, const void* head_w_dev, const void* code_emb_dev,
                  hra_delay_state* state_dev, const float* eoc_bias_dev, const hra_sampling* sampling,
                  const uint64_t* seeds_dev, void* hidden_dev, int32_t* pos_dev, int32_t pos_bound, int32_t batch,
                  const hra_kv_cache* kv, int32_t* codes_dev, void* next_emb_dev, int32_t* done_dev, void* backbone_ws,
-                 size_t backbone_ws_bytes, void* codebook_ws, size_t codebook_ws_bytes, void* stream) {
+                 size_t backbone_ws_bytes, void* codebook_ws, size_t codebook_ws_bytes, void* stream,
+                 const hra_kv8_cache* kv8 = nullptr) {
     if (pos_dev == nullptr) return HRA_ERR_INVALID_ARG;
     // both steps' arguments are checked before anything is enqueued
     int rc = decode_impl(dims, weights, next_emb_dev, nullptr, pos_dev, pos_bound, 1, batch, kv, hidden_dev,
-                         backbone_ws, backbone_ws_bytes, stream, /*validate_only=*/true);
+                         backbone_ws, backbone_ws_bytes, stream, /*validate_only=*/true, kv8);
     if (rc != HRA_OK) return rc;
     rc = codebook_impl(dims, hidden_dev, head_w_dev, code_emb_dev, state_dev, eoc_bias_dev, sampling, seeds_dev, batch,
                        codes_dev, next_emb_dev, done_dev, nullptr, codebook_ws, codebook_ws_bytes, stream, true);
@@ -1026,7 +1168,31 @@ int hra_ar_frame(const hra_dims* dims, const hra_weights* weights, const void* h
                        codes_dev, next_emb_dev, done_dev, nullptr, codebook_ws, codebook_ws_bytes, stream, false);
     if (rc != HRA_OK) return rc;
     return decode_impl(dims, weights, next_emb_dev, nullptr, pos_dev, pos_bound, 1, batch, kv, hidden_dev,
-                       backbone_ws, backbone_ws_bytes, stream);
+                       backbone_ws, backbone_ws_bytes, stream, false, kv8);
+}
+
+}  // namespace
+
+int hra_ar_frame(const hra_dims* dims, const hra_weights* weights, const void* head_w_dev, const void* code_emb_dev,
+                 hra_delay_state* state_dev, const float* eoc_bias_dev, const hra_sampling* sampling,
+                 const uint64_t* seeds_dev, void* hidden_dev, int32_t* pos_dev, int32_t pos_bound, int32_t batch,
+                 const hra_kv_cache* kv, int32_t* codes_dev, void* next_emb_dev, int32_t* done_dev, void* backbone_ws,
+                 size_t backbone_ws_bytes, void* codebook_ws, size_t codebook_ws_bytes, void* stream) {
+    return ar_frame_impl(dims, weights, head_w_dev, code_emb_dev, state_dev, eoc_bias_dev, sampling, seeds_dev,
+                         hidden_dev, pos_dev, pos_bound, batch, kv, codes_dev, next_emb_dev, done_dev, backbone_ws,
+                         backbone_ws_bytes, codebook_ws, codebook_ws_bytes, stream);
+}
+
+int hra_ar_frame_kv8(const hra_dims* dims, const hra_weights* weights, const void* head_w_dev,
+                     const void* code_emb_dev, hra_delay_state* state_dev, const float* eoc_bias_dev,
+                     const hra_sampling* sampling, const uint64_t* seeds_dev, void* hidden_dev, int32_t* pos_dev,
+                     int32_t pos_bound, int32_t batch, const hra_kv8_cache* cache, int32_t* codes_dev,
+                     void* next_emb_dev, int32_t* done_dev, void* backbone_ws, size_t backbone_ws_bytes,
+                     void* codebook_ws, size_t codebook_ws_bytes, void* stream) {
+    if (cache == nullptr) return HRA_ERR_INVALID_ARG;
+    return ar_frame_impl(dims, weights, head_w_dev, code_emb_dev, state_dev, eoc_bias_dev, sampling, seeds_dev,
+                         hidden_dev, pos_dev, pos_bound, batch, nullptr, codes_dev, next_emb_dev, done_dev, backbone_ws,
+                         backbone_ws_bytes, codebook_ws, codebook_ws_bytes, stream, cache);
 }
 
 size_t hra_linear_workspace_size(int32_t M, int32_t N, int32_t K, int32_t epilogue, int32_t split_k) {

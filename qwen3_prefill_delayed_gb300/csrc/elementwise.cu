@@ -203,7 +203,8 @@ __global__ void qk_rope_kv_kernel(const QkRopeArgs a) {
     const int sub = threadIdx.x & 15;
     const int nhw = blockDim.x >> 4;
     const int hw0 = (threadIdx.x >> 4) + blockIdx.y * nhw;   // this CTA's group of heads
-    const int seq = a.row_seq[row], pos = a.row_pos[row];
+    const int pos = a.row_pos[row];
+    const int seq = a.kv_by_row ? row : a.row_seq[row], slot = a.kv_by_row ? 0 : pos;
     const int trow = a.rope_row_is_pos ? pos : row;
     for (int i = threadIdx.x; i < HALF; i += blockDim.x) s_cs[i] = a.rope[(long long)i * a.rope_rows + trow];
     __syncthreads();
@@ -279,7 +280,7 @@ __global__ void qk_rope_kv_kernel(const QkRopeArgs a) {
         bf16* dst;
         if (is_v) {
             dst = a.kv_layer + ((long long)(seq * 2 + 1) * a.nkv + (hh - a.nq - a.nkv)) * head_stride +
-                  (long long)pos * HD + sub * E;
+                  (long long)slot * HD + sub * E;
             if (a.part != nullptr) {
                 if constexpr (E == 8) {
                     *reinterpret_cast<uint4*>(dst) = pack8(x);
@@ -306,7 +307,7 @@ __global__ void qk_rope_kv_kernel(const QkRopeArgs a) {
                 out[e] = __fadd_rn(__fmul_rn(xn[e], c.x), __fmul_rn(pn[e], c.y));
         }
         if (is_q) dst = a.q_out + ((long long)row * a.nq + hh) * HD + sub * E;
-        else dst = a.kv_layer + ((long long)(seq * 2) * a.nkv + (hh - a.nq)) * head_stride + (long long)pos * HD + sub * E;
+        else dst = a.kv_layer + ((long long)(seq * 2) * a.nkv + (hh - a.nq)) * head_stride + (long long)slot * HD + sub * E;
         if constexpr (E == 8) {
             *reinterpret_cast<uint4*>(dst) = pack8(out);
         } else {

@@ -168,8 +168,9 @@ template <int BN, int HD>
 __device__ __forceinline__ void qk_rope_epilogue_hd(uint32_t tq, int n0, int half, int row, bool row_ok,
                                                     const QkRopeArgs& a, bool v8) {
     constexpr int HALF = HD / 2;
-    const int seq = row_ok ? a.row_seq[row] : 0;
+    const int seq = a.kv_by_row ? row : row_ok ? a.row_seq[row] : 0;
     const int pos = row_ok ? a.row_pos[row] : 0;
+    const int slot = a.kv_by_row ? 0 : pos;
     const float2* cs = a.rope + (a.rope_row_is_pos ? pos : row);   // pair i at cs[i * rope_rows]
     const long long head_stride = (long long)a.n_slots * HD;
     // Two passes over each head's TMEM columns keep at most 64 values in registers: the first
@@ -181,7 +182,7 @@ __device__ __forceinline__ void qk_rope_epilogue_hd(uint32_t tq, int n0, int hal
         if (hh >= a.nq + 2 * a.nkv) break;
         const bool is_v = hh >= a.nq + a.nkv;
         bf16* vdst = a.kv_layer + ((long long)(seq * 2 + 1) * a.nkv + (hh - a.nq - a.nkv)) * head_stride +
-                     (long long)pos * HD;
+                     (long long)slot * HD;
         // four interleaved compensated sums (short dependency chains), combined compensated
         float s4[4] = {0.f, 0.f, 0.f, 0.f}, c4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -219,7 +220,7 @@ __device__ __forceinline__ void qk_rope_epilogue_hd(uint32_t tq, int n0, int hal
         const bool is_q = hh < a.nq;
         const bf16* gain = is_q ? a.q_norm : a.k_norm;
         bf16* dst = is_q ? a.q_out + ((long long)row * a.nq + hh) * HD
-                         : a.kv_layer + ((long long)(seq * 2) * a.nkv + (hh - a.nq)) * head_stride + (long long)pos * HD;
+                         : a.kv_layer + ((long long)(seq * 2) * a.nkv + (hh - a.nq)) * head_stride + (long long)slot * HD;
 #pragma unroll
         for (int c = 0; c < HALF; c += 32) {
             float xl[32], xh[32];

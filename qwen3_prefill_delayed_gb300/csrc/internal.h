@@ -60,6 +60,7 @@ struct QkRopeArgs {
     int n_slots;
     int rows, nq, nkv, hd;
     float eps;
+    int kv_by_row;      // k and v of row r go to kv_layer [rows][2][nkv][hd] instead (n_slots 1)
     // optional: take the merged row as the sum of fp32 split partials (part[s * split_stride +
     // row * ldp + col], s in split order) rounded to bf16, instead of reading qkv
     const float* part;
@@ -349,6 +350,9 @@ struct Kv8AppendArgs {
     int batch, total_rows, max_new;
 };
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t st);
+// kv_len[b] = row_pos[last_row[b]] + 1, one_each[b] = b (b <= batch: the cu of one row a sequence)
+cudaError_t launch_kv8_lens(const int32_t* row_pos, const int32_t* last_row, int batch, int32_t* kv_len,
+                            int32_t* one_each, cudaStream_t st);
 
 // Causal attention of the last q_len positions of each sequence over its kv_len cached positions.
 struct Kv8AttnArgs {

@@ -125,7 +125,23 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(const Kv8AppendArgs a) 
     if (lane == 0 && s != before) *scale = s;
 }
 
+__global__ void kv8_lens_kernel(const int32_t* __restrict__ row_pos, const int32_t* __restrict__ last_row, int batch,
+                                int32_t* kv_len, int32_t* one_each) {
+    pdl_launch();
+    pdl_wait();
+    for (int b = threadIdx.x; b <= batch; b += blockDim.x) {
+        if (b < batch) kv_len[b] = row_pos[last_row[b]] + 1;
+        one_each[b] = b;
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_kv8_lens(const int32_t* row_pos, const int32_t* last_row, int batch, int32_t* kv_len,
+                            int32_t* one_each, cudaStream_t st) {
+    HRA_LAUNCH(kv8_lens_kernel, dim3(1), dim3(256), 0, st, row_pos, last_row, batch, kv_len, one_each);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t st) {
     const int units = kv8_max_blocks(a.max_new) * 2 * a.view.n_kv;
