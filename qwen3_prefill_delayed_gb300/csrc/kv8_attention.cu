@@ -31,12 +31,11 @@
 //   k(2 j) = 2 j, k(2 j + 1) = (2 j ^ 4) + 1: with the copies' 128-byte swizzle no read has a bank conflict.
 // Each warp has its own ring of stages that TMA fills, one box of 16 rows for K and one for V a block, so a
 // block costs one lane two instructions to request (32 cp.async an address each before: 4.3 -> MEASURED TB/s).
-#include <cuda_fp16.h>
 #include <math.h>
 
 #include <algorithm>
 
-#include "internal.h"
+#include "kv8_device.cuh"
 
 namespace hra {
 
@@ -56,12 +55,6 @@ constexpr float kPScale = 15.f; // log2 of the largest p
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int src_bytes) {   // 0 bytes: zero
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
-// four E4M3 codes -> two pairs of f16
-__device__ __forceinline__ void e4m3x4_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-}
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm(
@@ -70,16 +63,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // A stage: K and V of a pair of blocks as TMA writes them (rows of HD bytes, swizzled over the row: 1024- or
 // 512-byte atoms), and the blocks' scales, a copy a lane.
 template <int HD>
@@ -424,9 +407,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
             float ev[kPair], vm[kPair];
 #pragma unroll
             for (int y = 0; y < kPair; ++y) {
-                const uint32_t vbits = __float_as_uint(sc[y].y);
-                ev[y] = (float)((int)((vbits >> 23) & 255u) - 127);
-                vm[y] = __uint_as_float((vbits & 0x807FFFFFu) | 0x3F800000u);
+                ev[y] = exponent_of(sc[y].y);
+                vm[y] = mantissa_of(sc[y].y);
             }
 #pragma unroll
             for (int x = 0; x < NG; ++x) {
@@ -710,7 +692,7 @@ size_t split_scratch(const Kv8View& c, int ng) {
 size_t kv8_attention_scratch_bytes(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int max_len) {
     const int G = nq / c.n_kv;
     size_t n = 0;
-    if ((long long)G * max_new > kShortRows) n = (kv8_prompt_scratch_bytes(batch, total_rows, G) + 255) & ~size_t(255);
+    if ((long long)G * max_new > kShortRows) n = (kv8_prompt_scratch_bytes(c, batch, total_rows, G, max_new, max_len) + 255) & ~size_t(255);
     if (!goes_whole(batch, max_len)) n += split_scratch(c, column_groups(G, max_new));
     return n;
 }
@@ -724,7 +706,7 @@ cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st) {
         const int short_rows = a.max_len > kSerialKeys ? kShortRows : 0;
         cudaError_t e = launch_kv8_prompt(a, short_rows, st);
         if (e != cudaSuccess || short_rows == 0 || (long long)a.batch * a.max_new == a.total_rows) return e;
-        scratch += (kv8_prompt_scratch_bytes(a.batch, a.total_rows, G) + 255) & ~size_t(255);
+        scratch += (kv8_prompt_scratch_bytes(a.view, a.batch, a.total_rows, G, a.max_new, a.max_len) + 255) & ~size_t(255);
     }
     SplitArgs s{};
     s.a = a;

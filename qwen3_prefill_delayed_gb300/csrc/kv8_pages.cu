@@ -16,13 +16,13 @@
 // the outputs may be the inputs.
 #include <algorithm>
 
-#include "internal.h"
+#include "kv8_device.cuh"
 
 namespace hra {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;   // what block_scan takes
 constexpr int kPart = 16384;   // bytes of one copy item
 
 // Scratch of both operations, in 4-byte words.
@@ -47,35 +47,6 @@ struct PlanScratch {
         table = list + n_pages;
     }
 };
-
-// Exclusive scan of one value a thread over the CTA; total gets the sum.
-__device__ __forceinline__ int block_scan(int v, int& total) {
-    __shared__ int warp_sum_s[32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += u;
-    }
-    if (lane == 31) warp_sum_s[warp] = incl;
-    __syncthreads();
-    if (warp == 0) {
-        const int s = warp_sum_s[lane];
-        int t = s;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += u;
-        }
-        warp_sum_s[lane] = t;
-    }
-    __syncthreads();
-    const int before = warp ? warp_sum_s[warp - 1] : 0;
-    total = warp_sum_s[31];
-    __syncthreads();
-    return before + incl - v;
-}
 
 __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8PagesArgs a) {
     pdl_launch();

@@ -22,15 +22,16 @@
 //              when M moves, and the output;
 //   warps 6-9  V: codes from global memory in registers, a tile ahead, to f16 in shared memory (keys that
 //              do not count as zeros, so stale slots never reach a product); and the items' Q.
-// The items come from a list built on the device (kv8_schedule_kernel), most key tiles first, and CTA c takes
-// entries in snake order.
-#include <cuda_fp8.h>
-#include <cuda_fp16.h>
+// The items come from a list built on the device (kv8_schedule_kernel).  Many items: most key tiles first, and CTA c
+// takes entries in snake order.  Few long ones (prompt chunks after many cached positions): the tiles of all items
+// form a line of which every CTA takes an equal share; parts of an item go to scratch as fp32 sums with their
+// (m, l, M) and a second kernel joins them in order.  2 rows of 500-1021 tokens after 9-16 thousand: 376 items on 304
+// CTAs took two turns of the longest; MEASURED.
 
 #include <algorithm>
 #include <math.h>
 
-#include "internal.h"
+#include "kv8_device.cuh"
 
 namespace hra {
 
@@ -41,10 +42,24 @@ constexpr int TROWS = 128;
 constexpr int TK = 64;             // keys a tile
 constexpr int NB = TK / kKv8Block; // blocks a tile
 constexpr float kUnit = 11.f;      // log2 of the weight of the reference maximum
+constexpr int kSharesFrom = 2048;  // keys from which items count as long
 constexpr float kSlack = 4.f;      // how far a maximum may pass the reference before it moves
 
 struct PromptRec {   // 32 bytes: one (query tile, sequence) pair
-    int b, row0, n, q_lo, kv_len, keys, pad0, pad1;
+    int b, row0, n, q_lo, kv_len, keys;
+    long long before;   // equal shares: tiles of the items of the pairs before
+};
+__host__ __device__ __forceinline__ int key_tiles(int keys) {   // an item without keys has one empty tile: its rows get 0
+    return keys > 0 ? (keys + TK - 1) / TK : 1;
+}
+// Parts of split items, as for single tokens: CTA c has slots 2 c (the item that its share begins in) and 2 c + 1 (the
+// one it ends in); a slot is [TROWS][HD] sums, then m, l and M of the rows.
+struct PromptDesc {   // the item whose first part is slot 2 c + 1, and the last CTA that has a part of it
+    int row0, n, q_lo, head, last, pad[3];   // row0 < 0: none
+};
+template <int HD>
+struct PromptSlot {
+    static constexpr int FLOATS = TROWS * (HD + 3);
 };
 constexpr int kRecWords = 8;
 
@@ -78,26 +93,14 @@ struct PromptArgs {
     const bf16* q;
     long long row_stride;
     bf16* out;
-    const int32_t* list;    // [0] = pairs, records from word 8 on
+    const int32_t* list;    // [0] = pairs, [2..3] all items' tiles, records from word 8 on
+    PromptDesc* desc;       // equal shares (null: snake order)
+    float* parts;
     float scale_log2;
     int nq, G, QT;
     int v8;                 // out 32-byte aligned
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
-    uint32_t d;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((unsigned short)w));
-    return d;
-}
-__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 // two fp32 operations in one instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     unsigned long long d;
@@ -147,8 +150,6 @@ __device__ __forceinline__ int snake(int k) {
     return k * (int)gridDim.x + ((k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
 }
 
-__device__ __forceinline__ float exponent_of(float s) { return (float)((int)((__float_as_uint(s) >> 23) & 255u) - 127); }
-
 // One row's tile of S, 32 columns at a time in a rolled loop: unrolled, the softmax warps wait for
 // instructions (a tile of straight code took 4600 clocks instead of 2400).  MASK: only keys below
 // `limit` of blocks that are there (scale >= 0) count.
@@ -197,8 +198,7 @@ __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, const
         for (int h = 0; h < 2; ++h) {
             const float k = h ? k2.y : k2.x, v = h ? v2.y : v2.x;
             const float coef = q_unscale * k;
-            const float f = ex2(fminf(up + exponent_of(v), 126.f)) *
-                            __uint_as_float((__float_as_uint(v) & 0x807FFFFFu) | 0x3F800000u);
+            const float f = ex2(fminf(up + exponent_of(v), 126.f)) * mantissa_of(v);
             const int n = MASK ? (k >= 0.f ? limit - 32 * ch - 16 * h : 0) : 16;
             const float2 coef2 = make_float2(coef, coef), f2 = make_float2(f, f);
 #pragma unroll
@@ -219,10 +219,12 @@ __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, const
     return (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
 }
 
-// One CTA.  Counting sort of the non-empty (query tile, sequence) pairs by key tiles, most first.
+// One CTA.  The non-empty (query tile, sequence) pairs: by a counting sort, most key tiles first, or, for equal shares,
+// in the order of the sequences with the tiles before each (the shares' borders decide where sums are split, so the
+// order must not depend on which thread comes first).
 constexpr int kBins = 1024;
 __global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a, int G, int QT, int tiles,
-                                                            int short_rows, int32_t* __restrict__ list) {
+                                                            int short_rows, int shares, int32_t* __restrict__ list) {
     pdl_launch();
     pdl_wait();
     __shared__ int hist[kBins];
@@ -231,9 +233,8 @@ __global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a,
     __syncthreads();
     const long long room = (long long)a.view.max_pages << a.view.page_shift;
     const long long pairs = (long long)tiles * a.batch;
-    auto pair = [&](long long pr, PromptRec& r) -> int {   // -1: nothing there
-        const int tile = (int)(pr / a.batch);
-        r.b = (int)(pr - (long long)tile * a.batch);
+    auto pair = [&](int tile, int b, PromptRec& r) -> int {   // -1: nothing there
+        r.b = b;
         kv8_rows(a.cu, r.b, a.total_rows, r.row0, r.n);
         r.q_lo = tile * QT;
         if (r.q_lo >= r.n || r.n * G <= short_rows) return -1;
@@ -241,12 +242,35 @@ __global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a,
         if (tile == 0 && (len < 0 || len > room || r.n > a.max_new)) raise_error(a.view.err, HRA_DEVERR_POS_RANGE);
         r.kv_len = len < 0 ? 0 : (int)min(room, (long long)len);
         r.keys = max(0, r.kv_len - r.n + min(r.n, r.q_lo + QT));
-        r.pad0 = r.pad1 = 0;
         return kBins - 1 - min(kBins - 1, (r.keys + TK - 1) / TK);
     };
     PromptRec r;
+    if (shares) {
+        int count = 0;
+        long long before = 0;
+        for (long long p0 = 0; p0 < pairs; p0 += 1024) {
+            const long long pr = p0 + threadIdx.x;
+            const int b = (int)(pr / tiles);
+            const bool in = pr < pairs && pair((int)(pr - (long long)b * tiles), b, r) >= 0;
+            int n, units;
+            const int at = count + block_scan(in ? 1 : 0, n);
+            const long long at_unit = before + (long long)a.view.n_kv * block_scan(in ? key_tiles(r.keys) : 0, units);
+            if (in) {
+                int4* to = reinterpret_cast<int4*>(list + kRecWords * (1 + (long long)at));
+                to[0] = make_int4(r.b, r.row0, r.n, r.q_lo);
+                to[1] = make_int4(r.kv_len, r.keys, (int)(at_unit & 0xFFFFFFFFll), (int)(at_unit >> 32));
+            }
+            count += n;
+            before += (long long)a.view.n_kv * units;
+        }
+        if (threadIdx.x == 0) {
+            list[0] = count;
+            *reinterpret_cast<long long*>(list + 2) = before;
+        }
+        return;
+    }
     for (long long pr = threadIdx.x; pr < pairs; pr += blockDim.x) {
-        const int bin = pair(pr, r);
+        const int bin = pair((int)(pr / a.batch), (int)(pr % a.batch), r);
         if (bin >= 0) atomicAdd(&hist[bin], 1);
     }
     __syncthreads();
@@ -269,7 +293,7 @@ __global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a,
     }
     __syncthreads();
     for (long long pr = threadIdx.x; pr < pairs; pr += blockDim.x) {
-        const int bin = pair(pr, r);
+        const int bin = pair((int)(pr / a.batch), (int)(pr % a.batch), r);
         if (bin >= 0) {
             int4* at = reinterpret_cast<int4*>(list + kRecWords * (1 + (long long)atomicAdd(&hist[bin], 1)));
             at[0] = make_int4(r.b, r.row0, r.n, r.q_lo);
@@ -292,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     volatile int* issued = reinterpret_cast<volatile int*>(slots + 2);
     float* sc = reinterpret_cast<float*>(smem + C::OFF_SC);
     float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
+    __shared__ int first_s[3];   // equal shares: the first item, its first tile, the tiles of the share
     volatile int* there = reinterpret_cast<volatile int*>(smem + C::OFF_TH);
     auto bar = [&](int i) { return smem_u32(bars + i); };
     const Kv8View& c = p.view;
@@ -305,6 +330,28 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         }
         *abort_flag = 0;
         *issued = 0;
+        if (p.desc != nullptr) {
+            const long long all = *reinterpret_cast<const long long*>(p.list + 2);
+            const long long share = (all + gridDim.x - 1) / gridDim.x, u = blockIdx.x * share;
+            p.desc[blockIdx.x].row0 = -1;
+            first_s[0] = first_s[1] = 0;
+            first_s[2] = (int)max(0LL, min(share, all - u));
+            if (u < all) {
+                int lo = 0, hi = p.list[0];   // the last pair with before <= u
+                auto before = [&](int i) {
+                    return *reinterpret_cast<const long long*>(p.list + kRecWords * (1 + (long long)i) + 6);
+                };
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (before(mid) <= u) lo = mid;
+                    else hi = mid;
+                }
+                const int n = key_tiles(p.list[kRecWords * (1 + (long long)lo) + 5]);
+                const long long at = u - before(lo);
+                first_s[0] = lo * c.n_kv + (int)(at / n);
+                first_s[1] = (int)(at % n);
+            }
+        }
         mbar_fence_init();
         tma_prefetch_map(&tmK);
     }
@@ -316,19 +363,24 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tS = slots[0], tO = tS + 2 * TK;   // two S buffers, then O
-    // Items k = 0, 1, ... of this CTA; the next one's record is on its way while one is worked on.
+    // Items k = 0, 1, ... of this CTA; the next one's record is on its way while one is worked on.  Every role calls
+    // item(0), item(1), ... until there is none.
+    const bool shares = p.desc != nullptr;
+    int left = shares ? first_s[2] : 0;   // tiles of the share
     int4 next_x = make_int4(0, 0, 0, 0), next_y = next_x;
+    auto index = [&](int k) { return shares ? first_s[0] + k : snake(k); };
     auto fetch = [&](int k) {
-        const int i = snake(k);
+        const int i = index(k);
         if (i < n_items) {
             const int4* at = reinterpret_cast<const int4*>(p.list + kRecWords * (1 + (long long)(i / c.n_kv)));
             next_x = at[0];
             next_y = at[1];
         }
     };
-    auto item = [&](int k, PromptRec& r, int& head) {   // key tiles of item k, 0 when there is none
-        const int i = snake(k);
-        if (i >= n_items) return 0;
+    int t_first = 0, t_all = 0;                         // this item's tiles [t_first, t_first + count) of t_all
+    auto item = [&](int k, PromptRec& r, int& head) {   // its count, 0 when there is none
+        const int i = index(k);
+        if (i >= n_items || (shares && left == 0)) return 0;
         head = i % c.n_kv;
         r.b = next_x.x;
         r.row0 = next_x.y;
@@ -337,7 +389,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         r.kv_len = next_y.x;
         r.keys = next_y.y;
         fetch(k + 1);
-        return max(1, (r.keys + TK - 1) / TK);   // an item without keys has one empty tile: its rows get 0
+        t_all = key_tiles(r.keys);
+        if (!shares) return t_all;
+        t_first = k == 0 ? first_s[1] : 0;
+        const int n = min(left, t_all - t_first);
+        left -= n;
+        return n;
     };
     fetch(0);
     PromptRec r;
@@ -352,11 +409,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             const int n_kt = item(k, r, head);
             if (n_kt == 0) break;
             auto page_of = [&](int t) {
-                const int pos = t * TK + blk * kKv8Block;
+                const int pos = (t_first + t) * TK + blk * kKv8Block;
                 return lane < 2 * NB && pos < r.keys ? kv8_page_of(c, r.b, pos) : -1;
             };
             auto scale_of = [&](int t, int page) {   // -1: the block's keys are absent
-                const int pos = t * TK + blk * kKv8Block;
+                const int pos = (t_first + t) * TK + blk * kKv8Block;
                 return page < 0 ? -1.f : c.scales[kv8_scale_at(c, page, which, head, pos & (c.page_size - 1))];
             };
             int page = page_of(0), page1 = n_kt > 1 ? page_of(1) : -1;
@@ -369,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 if (g >= NK) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_KE + st), (uint32_t)(g / NK - 1) & 1u, abort_flag));
                 if (!ok) break;
                 const bool want = lane < NB && page >= 0;
-                const int pos = t * TK + blk * kKv8Block;
+                const int pos = (t_first + t) * TK + blk * kKv8Block;
                 if (lane < NB && pos < r.keys && page < 0) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
                 if (lane < 2 * NB) sc[((g % NSC) * 2 + which) * NB + blk] = s;
                 const int boxes = __popc(__ballot_sync(0xffffffffu, want));
@@ -473,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const uint32_t lS = lS0 + (g & 1) * TK;
                 const float* ks = sc + (g % NSC) * 2 * NB;
                 const float* vs = ks + NB;
-                const int j0 = t * TK;
+                const int j0 = (t_first + t) * TK;
                 const bool whole = j0 + TK <= clear && there[g % NSC] != 0;   // every key counts for every row
                 float mx = -INFINITY, Mx = -INFINITY;
                 if (whole)
@@ -514,6 +571,32 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV + ((g - 1) & 1)), (uint32_t)((g - 1) >> 1) & 1u, abort_flag));
             if (!ok) break;
             tc_fence_after();
+            if (shares && n_kt < t_all) {   // a part: the sums as they are
+                float* part = p.parts + (2LL * blockIdx.x + (t_first == 0 ? 1 : 0)) * PromptSlot<HD>::FLOATS;
+#pragma unroll 1
+                for (int ch = 0; ch < HD; ch += 32) {
+                    float o[32];
+                    tmem_ld32(lO + ch, o);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(part + row * HD + ch + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+                part += TROWS * HD;
+                part[row] = m;
+                part[TROWS + row] = l;
+                part[2 * TROWS + row] = M;
+                if (t_first == 0 && row == 0) {   // its first part; the share is at its end
+                    const long long all = *reinterpret_cast<const long long*>(p.list + 2);
+                    const long long share = (all + gridDim.x - 1) / gridDim.x;
+                    const long long end = (blockIdx.x + 1LL) * share - n_kt + t_all;
+                    p.desc[blockIdx.x] = PromptDesc{r.row0, r.n, r.q_lo, head, (int)((end - 1) / share), {0, 0, 0}};
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_OF));
+                ++it;
+                continue;
+            }
             // O is in units of 2^(M - 11); l is 0 for a row that saw no key, and NaN when a score was
             const float f = l == 0.f ? 0.f : exp2f((M == -INFINITY ? 0.f : M) - (m == -INFINITY ? 0.f : m)) / l;
             bf16* dst = p.out + ((long long)(r.row0 + r.q_lo + qi) * p.nq + head * p.G + hq) * HD;
@@ -550,11 +633,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             if (n_kt == 0) break;
             uint4 raw[2][2 * HALVES];   // the codes of two tiles on their way
             auto page_of = [&](int t) {
-                const int pos = t * TK + w * kKv8Block;
+                const int pos = (t_first + t) * TK + w * kKv8Block;
                 return pos < r.keys ? kv8_page_of(c, r.b, pos) : -1;
             };
             auto request = [&](uint4(&v)[2 * HALVES], int t, int page) {
-                const int pos = t * TK + w * kKv8Block;
+                const int pos = (t_first + t) * TK + w * kKv8Block;
                 const uint8_t* src = c.codes + kv8_code_at(c, page < 0 ? 0 : page, 1, head, pos & (c.page_size - 1));
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
@@ -601,24 +684,29 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                         top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
                         for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const float s = __uint_as_float(kv8_scale_bits(min(top, 0x7F7Fu) << 16));
-                        const float inv = 1.0f / s;
+                        const uint32_t s = kv8_scale_bits(min(top, 0x7F7Fu) << 16);
+                        const float inv = __uint_as_float((254u << 23) - s);   // 1 / s: a power of two
                         uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 v = make_float2(__uint_as_float(in[e] << 16) * inv, __uint_as_float(in[e] & 0xFFFF0000u) * inv);
-                            const uint32_t hc = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-                            const uint32_t h2 = e4m3x2_f16x2(hc);
-                            const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                            const uint32_t lc = __nv_cvt_float2_to_fp8x2(make_float2(v.x - hv.x, v.y - hv.y), __NV_SATFINITE, __NV_E4M3);
-                            hi[e >> 1] = e & 1 ? hi[e >> 1] | hc << 16 : hc;
-                            lo[e >> 1] = e & 1 ? lo[e >> 1] | lc << 16 : lc;
+                        for (int e = 0; e < 8; e += 2) {
+                            uint32_t hc[2], lc[2];
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {   // q / s fits f16 exactly, but for what is under 2^-25
+                                const uint32_t v = pack_h2(__uint_as_float(in[e + z] << 16) * inv,
+                                                           __uint_as_float(in[e + z] & 0xFFFF0000u) * inv);
+                                hc[z] = f16x2_e4m3x2(v);
+                                const uint32_t back = e4m3x2_f16x2(hc[z]);
+                                const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&back));
+                                lc[z] = f16x2_e4m3x2(*reinterpret_cast<const uint32_t*>(&d));
+                            }
+                            hi[e >> 1] = __byte_perm(hc[0], hc[1], 0x5410);
+                            lo[e >> 1] = __byte_perm(lc[0], lc[1], 0x5410);
                         }
                         const int at = row * HD + ((HD == 128 ? x ^ (row & 7) : x ^ ((row >> 1) & 3)) << 4);
                         *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4*>(smem + C::QB + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         // a row with an infinity or a NaN gives NaN
-                        if (x == 0) qs[(it % NQS) * TROWS + row] = top < 0x7F80u ? s : __uint_as_float(0x7FC00000u);
+                        if (x == 0) qs[(it % NQS) * TROWS + row] = __uint_as_float(top < 0x7F80u ? s : 0x7FC00000u);
                     }
                 }
                 if (!ok) break;
@@ -641,14 +729,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
 #pragma unroll
                     for (int h = 0; h < HALVES; ++h) {
                         const uint4 u = v[y * HALVES + h];
+                        uint32_t f[8];
+                        e4m3x4_f16x4(u.x, f[0], f[1]);
+                        e4m3x4_f16x4(u.y, f[2], f[3]);
+                        e4m3x4_f16x4(u.z, f[4], f[5]);
+                        e4m3x4_f16x4(u.w, f[6], f[7]);
                         const int key = w * kKv8Block + 8 * y + kq;
                         uint8_t* at = smem + C::OFF_V + (g & 1) * C::VB + h * TK * 128 + key * 128;
                         *reinterpret_cast<uint4*>(at + (((2 * c16) ^ (key & 7)) << 4)) =
-                            make_uint4(e4m3x2_f16x2(u.x & 0xFFFFu), e4m3x2_f16x2(u.x >> 16), e4m3x2_f16x2(u.y & 0xFFFFu),
-                                       e4m3x2_f16x2(u.y >> 16));
+                            make_uint4(f[0], f[1], f[2], f[3]);
                         *reinterpret_cast<uint4*>(at + (((2 * c16 + 1) ^ (key & 7)) << 4)) =
-                            make_uint4(e4m3x2_f16x2(u.z & 0xFFFFu), e4m3x2_f16x2(u.z >> 16), e4m3x2_f16x2(u.w & 0xFFFFu),
-                                       e4m3x2_f16x2(u.w >> 16));
+                            make_uint4(f[4], f[5], f[6], f[7]);
                     }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -686,6 +777,60 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     }
 }
 
+// The parts of the item that begins in share blockIdx.x and goes on behind it, in order; 8 rows a CTA.
+template <int HD>
+__global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const PromptArgs p) {
+    pdl_launch();
+    pdl_wait();
+    const int c0 = blockIdx.x;
+    const PromptDesc d = p.desc[c0];
+    if (d.row0 < 0) return;
+    const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int qi = row / p.G, hq = row - qi * p.G;
+    if (qi >= p.QT || d.q_lo + qi >= d.n) return;
+    constexpr int E = HD / 32;
+    const int parts = d.last - c0 + 1;
+    auto slot = [&](int i) { return p.parts + (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * PromptSlot<HD>::FLOATS; };
+    float m = -INFINITY, M = -INFINITY;
+    for (int i = 0; i < parts; ++i) {
+        const float* q = slot(i) + TROWS * HD + row;
+        m = fmaxf(m, q[0]);
+        M = fmaxf(M, q[2 * TROWS]);
+    }
+    const float mr = m == -INFINITY ? 0.f : m, Mr = M == -INFINITY ? 0.f : M;
+    float l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const float* q = slot(i) + TROWS * HD + row;
+        const float* x = slot(i) + row * HD + lane * E;
+        l += q[TROWS] * ex2(q[0] - mr);
+        const float f = ex2(q[2 * TROWS] - Mr);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += x[e] * f;
+    }
+    const float f = l == 0.f ? 0.f : exp2f(Mr - mr) / l;
+    bf16* dst = p.out + ((long long)(d.row0 + d.q_lo + qi) * p.nq + d.head * p.G + hq) * HD + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + e) = pack_bf2(o[e] * 0x1p-11f * f, o[e + 1] * 0x1p-11f * f);
+}
+
+int prompt_slots() { return 2 * device_sm_count(); }
+
+// Equal shares where the items are long and so few that the CTAs' turns would not come out even.
+bool prompt_shares(long long pairs, int n_kv, int max_len) {
+    return max_len > kSharesFrom && pairs * n_kv < 8LL * prompt_slots();
+}
+long long most_pairs(int batch, int total_rows, int QT, int max_new) {
+    return std::min((long long)((max_new + QT - 1) / QT) * batch, (long long)total_rows / QT + batch);
+}
+
+size_t list_bytes(int batch, int total_rows, int G) {
+    return ((size_t)total_rows / (TROWS / G) + (size_t)batch + 1) * kRecWords * sizeof(int32_t);
+}
+
 template <int HD>
 cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int tiles, int short_rows, cudaStream_t st) {
     using C = Cfg<HD>;
@@ -702,7 +847,9 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int tiles, int short_
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
     int32_t* list = reinterpret_cast<int32_t*>(a.scratch);
-    HRA_LAUNCH(kv8_schedule_kernel, dim3(1), dim3(1024), 0, st, a, G, QT, tiles, short_rows, list);
+    const long long pairs = most_pairs(a.batch, a.total_rows, QT, a.max_new);
+    const bool shares = prompt_shares(pairs, a.view.n_kv, a.max_len);
+    HRA_LAUNCH(kv8_schedule_kernel, dim3(1), dim3(1024), 0, st, a, G, QT, tiles, short_rows, shares ? 1 : 0, list);
     PromptArgs p{};
     p.view = a.view;
     p.q = a.q;
@@ -714,16 +861,25 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int tiles, int short_
     p.G = G;
     p.QT = QT;
     p.v8 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
-    const long long pairs = std::min((long long)tiles * a.batch, (long long)a.total_rows / QT + a.batch);
-    const int grid = (int)std::max<long long>(1, std::min(pairs * a.view.n_kv, 2LL * device_sm_count()));
+    const int grid = shares ? prompt_slots() : (int)std::max<long long>(1, std::min<long long>(pairs * a.view.n_kv, prompt_slots()));
+    if (shares) {
+        uint8_t* at = reinterpret_cast<uint8_t*>(a.scratch) + list_bytes(a.batch, a.total_rows, G);
+        p.desc = reinterpret_cast<PromptDesc*>(at);
+        p.parts = reinterpret_cast<float*>(at + grid * sizeof(PromptDesc));
+    }
     HRA_LAUNCH(kv8_prompt_kernel<HD>, dim3(grid), dim3(kThreads), C::ALLOC, st, map, p);
+    if (shares) HRA_LAUNCH(kv8_prompt_join_kernel<HD>, dim3(grid, TROWS / 8), dim3(256), 0, st, p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t kv8_prompt_scratch_bytes(int batch, int total_rows, int G) {
-    return ((size_t)total_rows / (TROWS / G) + (size_t)batch + 1) * kRecWords * sizeof(int32_t);
+size_t kv8_prompt_scratch_bytes(const Kv8View& c, int batch, int total_rows, int G, int max_new, int max_len) {
+    const int QT = TROWS / G;
+    size_t n = list_bytes(batch, total_rows, G);
+    if (prompt_shares(most_pairs(batch, total_rows, QT, max_new), c.n_kv, max_len))
+        n += (size_t)prompt_slots() * (sizeof(PromptDesc) + 2 * sizeof(float) * TROWS * (c.head_dim + 3));
+    return n;
 }
 
 cudaError_t launch_kv8_prompt(const Kv8AttnArgs& a, int short_rows, cudaStream_t st) {

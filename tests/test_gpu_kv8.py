@@ -195,6 +195,32 @@ def test_prompts(hra, H, G, D, P, new, kept):
     check(hra, c, new, lens, G)
 
 
+@pytest.mark.parametrize("H,G,D,P", [(2, 4, 128, 64), (1, 2, 64, 16), (1, 5, 128, 128)])
+@pytest.mark.parametrize("new,kept", [
+    ([130], [2500]), ([33, 1, 90, 0, 2], [2100, 3000, 5, 40, 2047]), ([70, 70], [2049, 4000]), ([1, 200], [5000, 0])])
+def test_prompts_after_many_positions(hra, H, G, D, P, new, kept):
+    """Long items in equal shares; single tokens beside them with many keys of their own."""
+    lens = [a + b for a, b in zip(new, kept)]
+    c = build(lens, H=H, D=D, P=P, seed=sum(kept))
+    kv = gpu(hra, c)
+    a = check(hra, c, new, lens, G, kv=kv)
+    assert torch.equal(a, check(hra, c, new, lens, G, kv=kv))       # the shares' borders do not move
+    assert bool(torch.isfinite(a).all())
+
+
+def test_long_prompt_with_hidden_pages_and_rows_before_the_cache(hra):
+    c = build([2300, 2100], H=2, D=64, P=16, seed=3)
+    c["table"][0, 20:60], c["table"][1, :] = -1, 5000
+    check(hra, c, [150, 40], [2300, 30], 2, max_len=2300, errors=hra.DEVERR_PAGE_RANGE)
+
+
+def test_more_sequences_than_a_share_table_holds(hra):
+    lens = [1 + (i * 37) % 70 for i in range(1100)]
+    lens[500] = 1500
+    c = build(lens, H=1, D=64, P=16, seed=3)
+    check(hra, c, [1] * 1100, lens, 2)
+
+
 def test_prompt_many_rows(hra):
     rng = random.Random(5)
     new = [rng.choice([0, 1, 2, 40, 77]) for _ in range(37)]
