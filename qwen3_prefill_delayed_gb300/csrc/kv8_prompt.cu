@@ -75,8 +75,8 @@ struct Cfg {
     static constexpr int OFF_K = 2 * QB;
     static constexpr int OFF_V = OFF_K + NK * KB;
     static constexpr int OFF_BAR = OFF_V + 2 * VB;
-    static constexpr int OFF_SC = OFF_BAR + 320;             // [NSC][2][NB] scales
-    static constexpr int OFF_QS = OFF_SC + NSC * 2 * NB * 4; // [NQS][TROWS] q scales
+    static constexpr int OFF_SC = OFF_BAR + 320;             // [NSC][3][NB]: K scale, V scale's exponent and mantissa
+    static constexpr int OFF_QS = OFF_SC + NSC * 3 * NB * 4; // [NQS][TROWS] q scales
     static constexpr int OFF_TH = OFF_QS + NQS * TROWS * 4;  // [NSC] whether a tile's blocks are all there
     static constexpr int SMEM = OFF_TH + NSC * 4;
     static constexpr int ALLOC = SMEM + 1024;           // the base is aligned up to 1024 bytes
@@ -155,16 +155,16 @@ __device__ __forceinline__ int snake(int k) {
 // `limit` of blocks that are there (scale >= 0) count.
 // mx: the maximum of s; Mx: the maximum of s + log2 of the block's V scale.
 template <bool MASK>
-__device__ __forceinline__ void max_pass(uint32_t lS, const float* ks, const float* vs, float q_unscale, int limit,
-                                         float& mx, float& Mx) {
+__device__ __forceinline__ void max_pass(uint32_t lS, const float* ks, float q_unscale, int limit, float& mx,
+                                         float& Mx) {
 #pragma unroll 1
     for (int ch = 0; ch < TK / 32; ++ch) {
         float a[32];
         tmem_ld32(lS + 32 * ch, a);
-        const float2 k2 = *reinterpret_cast<const float2*>(ks + 2 * ch), v2 = *reinterpret_cast<const float2*>(vs + 2 * ch);
+        const float2 k2 = *reinterpret_cast<const float2*>(ks + 2 * ch), e2 = *reinterpret_cast<const float2*>(ks + NB + 2 * ch);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float k = h ? k2.y : k2.x, v = h ? v2.y : v2.x;
+            const float k = h ? k2.y : k2.x, ev = h ? e2.y : e2.x;
             if (MASK) {
                 const int n = k >= 0.f ? limit - 32 * ch - 16 * h : 0;
 #pragma unroll
@@ -177,28 +177,29 @@ __device__ __forceinline__ void max_pass(uint32_t lS, const float* ks, const flo
             const float bm = fmaxf(top[0], top[1]);
             const float z = MASK && bm == -INFINITY ? bm : bm * (q_unscale * k);
             mx = fmaxf(mx, z);
-            Mx = fmaxf(Mx, z + exponent_of(v));
+            Mx = fmaxf(Mx, z + ev);
         }
     }
 }
 // The weights: l's terms 2^(s - mr) are returned summed; times the block's V scale and 2^(mr - Mr + 11)
 // (`up` its exponent) they go as f16 to columns 16 ch, which this row has read.
 template <bool MASK>
-__device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, const float* vs, float q_unscale, int limit,
-                                             float mr, float up) {
+__device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float q_unscale, int limit, float mr,
+                                             float up) {
     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float2 neg = make_float2(-mr, -mr);
 #pragma unroll 1
     for (int ch = 0; ch < TK / 32; ++ch) {
         float a[32];
         tmem_ld32(lS + 32 * ch, a);
-        const float2 k2 = *reinterpret_cast<const float2*>(ks + 2 * ch), v2 = *reinterpret_cast<const float2*>(vs + 2 * ch);
+        const float2 k2 = *reinterpret_cast<const float2*>(ks + 2 * ch), e2 = *reinterpret_cast<const float2*>(ks + NB + 2 * ch),
+                     m2 = *reinterpret_cast<const float2*>(ks + 2 * NB + 2 * ch);
         uint32_t w[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float k = h ? k2.y : k2.x, v = h ? v2.y : v2.x;
+            const float k = h ? k2.y : k2.x, ev = h ? e2.y : e2.x;
             const float coef = q_unscale * k;
-            const float f = ex2(fminf(up + exponent_of(v), 126.f)) * mantissa_of(v);
+            const float f = ex2(fminf(up + ev, 126.f)) * (h ? m2.y : m2.x);
             const int n = MASK ? (k >= 0.f ? limit - 32 * ch - 16 * h : 0) : 16;
             const float2 coef2 = make_float2(coef, coef), f2 = make_float2(f, f);
 #pragma unroll
@@ -428,7 +429,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const bool want = lane < NB && page >= 0;
                 const int pos = (t_first + t) * TK + blk * kKv8Block;
                 if (lane < NB && pos < r.keys && page < 0) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
-                if (lane < 2 * NB) sc[((g % NSC) * 2 + which) * NB + blk] = s;
+                if (lane < NB) {
+                    sc[(g % NSC) * 3 * NB + blk] = s;
+                } else if (lane < 2 * NB) {
+                    sc[((g % NSC) * 3 + 1) * NB + blk] = exponent_of(s);
+                    sc[((g % NSC) * 3 + 2) * NB + blk] = mantissa_of(s);
+                }
                 const int boxes = __popc(__ballot_sync(0xffffffffu, want));
                 if (lane == 0) there[g % NSC] = boxes == NB;
                 __syncwarp();   // the scales are written
@@ -454,7 +460,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             constexpr uint32_t idesc_s = idesc_e4m3_f32(TROWS, TK);
             // A and B f16 (type code 0), D fp32, B transposed (MN-major), N = HD
             constexpr uint32_t idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((uint32_t)(TROWS >> 4) << 24);
-            const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + C::OFF_K), sV = smem_u32(smem + C::OFF_V);
+            const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + C::OFF_K);
+            const uint64_t q_desc = HD == 128 ? sdesc_sw128(sQ) : sdesc_sw64(sQ);
+            const uint64_t k_desc = HD == 128 ? sdesc_sw128(sK) : sdesc_sw64(sK);
+            const uint64_t v_desc = sdesc_sw128_mn(smem_u32(smem + C::OFF_V), TK * 128, 1024);
             int g = 0, it = 0;
             for (int k = 0; ok; ++k) {
                 const int n_kt = item(k, r, head);
@@ -466,16 +475,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                         (x >= 2 && !mbar_wait(bar(C::B_PV + (x & 1)), (uint32_t)((x >> 1) - 1) & 1u, abort_flag)))
                         return false;
                     tc_fence_after();
-                    const uint32_t kt = sK + st * C::KB;
+                    const uint64_t kd = k_desc + (uint64_t)(st * (C::KB >> 4));
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
-                        for (int kk = 0; kk < HD / 32; ++kk) {
-                            const uint32_t qa = sQ + part * C::QB;
-                            const uint64_t ad = (HD == 128 ? sdesc_sw128(qa) : sdesc_sw64(qa)) + 2ull * kk;
-                            const uint64_t bd = (HD == 128 ? sdesc_sw128(kt) : sdesc_sw64(kt)) + 2ull * kk;
-                            tc_mma_f8(tS + (x & 1) * TK, ad, bd, idesc_s, part + kk > 0 ? 1u : 0u);
-                        }
+                        for (int kk = 0; kk < HD / 32; ++kk)
+                            tc_mma_f8(tS + (x & 1) * TK, q_desc + (uint64_t)(part * (C::QB >> 4) + 2 * kk), kd + 2ull * kk, idesc_s,
+                                      part + kk > 0 ? 1u : 0u);
                     tc_commit(bar(C::B_SF + (x & 1)));
                     tc_commit(bar(C::B_KE + st));
                     return true;
@@ -493,10 +499,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                          (t > 0 || it == 0 || mbar_wait(bar(C::B_OF), (uint32_t)(it - 1) & 1u, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t tP = tS + (g & 1) * TK, v0 = sV + (g & 1) * C::VB;
+                    const uint32_t tP = tS + (g & 1) * TK;
 #pragma unroll
                     for (int ks = 0; ks < TK / 16; ++ks)
-                        tc_mma_f16_ts(tO, tP + 8 * ks, sdesc_sw128_mn(v0 + ks * 16 * 128, TK * 128, 1024), idesc_o,
+                        tc_mma_f16_ts(tO, tP + 8 * ks, v_desc + (uint64_t)((g & 1) * (C::VB >> 4) + ks * (16 * 128 >> 4)), idesc_o,
                                       (t > 0 || ks > 0) ? 1u : 0u);
                     tc_commit(bar(C::B_PV + (g & 1)));
                 }
@@ -528,15 +534,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t lS = lS0 + (g & 1) * TK;
-                const float* ks = sc + (g % NSC) * 2 * NB;
-                const float* vs = ks + NB;
+                const float* ks = sc + (g % NSC) * 3 * NB;   // then the V exponents and mantissas
                 const int j0 = (t_first + t) * TK;
                 const bool whole = j0 + TK <= clear && there[g % NSC] != 0;   // every key counts for every row
                 float mx = -INFINITY, Mx = -INFINITY;
                 if (whole)
-                    max_pass<false>(lS, ks, vs, q_unscale, 0, mx, Mx);
+                    max_pass<false>(lS, ks, q_unscale, 0, mx, Mx);
                 else
-                    max_pass<true>(lS, ks, vs, q_unscale, limit - j0, mx, Mx);
+                    max_pass<true>(lS, ks, q_unscale, limit - j0, mx, Mx);
                 const float mn = fmaxf(m, mx);
                 const float mr = mn == -INFINITY ? 0.f : mn;
                 l *= ex2(m - mr);
@@ -559,8 +564,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     }
                 }
                 const float up = mr - Mr + kUnit;
-                l += whole ? weight_pass<false>(lS, ks, vs, q_unscale, 0, mr, up)
-                           : weight_pass<true>(lS, ks, vs, q_unscale, limit - j0, mr, up);
+                l += whole ? weight_pass<false>(lS, ks, q_unscale, 0, mr, up)
+                           : weight_pass<true>(lS, ks, q_unscale, limit - j0, mr, up);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
@@ -627,28 +632,40 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         // V: keys 16 w .. 16 w + 15 of a tile, one block; this lane's codes are 16 of the rows kq and 8 + kq
         constexpr int HALVES = HD / 64;
         const int kq = ((lane >> 2) & 1) + 2 * (lane >> 3), c16 = lane & 3;
+        const long long page_bytes = 2LL * c.n_kv * c.page_size * HD;
         int g = 0, it = 0;
         for (int k = 0; ok; ++k) {
             const int n_kt = item(k, r, head);
             if (n_kt == 0) break;
             uint4 raw[2][2 * HALVES];   // the codes of two tiles on their way
+            const uint8_t* head_v = c.codes + kv8_code_at(c, 0, 1, head, 0) + kq * HD + c16 * 16;
+            const int32_t* table = c.table + (long long)r.b * c.max_pages;
             auto page_of = [&](int t) {
                 const int pos = (t_first + t) * TK + w * kKv8Block;
-                return pos < r.keys ? kv8_page_of(c, r.b, pos) : -1;
+                if (pos >= r.keys) return -1;   // below it: inside the row of the table
+                const int page = table[pos >> c.page_shift];
+                return page < c.n_pages ? page : -1;
             };
             auto request = [&](uint4(&v)[2 * HALVES], int t, int page) {
                 const int pos = (t_first + t) * TK + w * kKv8Block;
-                const uint8_t* src = c.codes + kv8_code_at(c, page < 0 ? 0 : page, 1, head, pos & (c.page_size - 1));
+                const uint8_t* src = head_v + (long long)max(page, 0) * page_bytes + (pos & (c.page_size - 1)) * HD;
+                if (page >= 0 && pos + kKv8Block <= r.keys) {
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+                    for (int y = 0; y < 2; ++y)
 #pragma unroll
-                    for (int h = 0; h < HALVES; ++h) {
-                        const int key = 8 * y + kq;
-                        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                        if (page >= 0 && pos + key < r.keys)
-                            u = *reinterpret_cast<const uint4*>(src + key * HD + h * 64 + c16 * 16);
-                        v[y * HALVES + h] = u;
-                    }
+                        for (int h = 0; h < HALVES; ++h)
+                            v[y * HALVES + h] = *reinterpret_cast<const uint4*>(src + 8 * y * HD + h * 64);
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h) {
+                            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                            if (page >= 0 && pos + 8 * y + kq < r.keys)
+                                u = *reinterpret_cast<const uint4*>(src + 8 * y * HD + h * 64);
+                            v[y * HALVES + h] = u;
+                        }
+                }
             };
             int page = page_of(0), page1 = page_of(1);
             {   // Q: hi and lo codes of rows 32 w .. 32 w + 31, LPR lanes a row, 16 elements a lane
