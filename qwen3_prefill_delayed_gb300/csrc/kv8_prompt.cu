@@ -2,7 +2,7 @@
 //
 // The formulas and the treatment of the scales are those of kv8_attention.cu.  Here an item is one
 // kv head and QT = 128 / G query positions of a sequence (128 rows (position, head), row r = (r / G, r % G))
-// over all their keys, in tiles of 128 keys:
+// over all their keys, in tiles of 64 keys:
 //   S = Q K^T    kind::f8f6f4 on the codes as they lie in the pages.  Q enters as the sum of two E4M3
 //                matrices under a power of two s per row: hi = e4m3(q / s), lo = e4m3(q / s - hi).  A bf16 value
 //                has 8 significant bits and each E4M3 value 4, so hi + lo is q / s exactly, except that elements
@@ -12,21 +12,26 @@
 //                running maximum M (it moves when it is exceeded by 2^4; 2^11 is the unit, so weights stay
 //                below 2^15), from tensor memory over the columns of S; V converted to f16 (exact).
 // Measured on GB300 (one thread issuing, SM clocks an instruction): 128 x N x 32 bytes takes 64 for N = 128 and
-// 53-63 for any smaller N, so a tile has 128 keys: 8 MMAs for S and 8 for PV.
+// 53-63 for any smaller N.  128-key tiles would use the tensor cores a quarter better, but tensor memory then has room
+// for one S only; with 64 keys S(g + 1) is computed while the softmax works on S(g) (8 long prompts: 277 us with one S of
+// 128 keys, 238 with two of 64).
 //
-// 320 threads, two CTAs an SM (256 tensor memory columns and 97 KB each), so that one CTA's softmax runs
+// 320 threads, two CTAs an SM (256 tensor memory columns and 101 KB each), so that one CTA's softmax runs
 // under the other's MMAs:
-//   warp 0     TMA of K (one 16-key box a lane, page by page) into two stages, and the blocks' scales;
+//   warp 0     TMA of K (one 16-key box a lane, page by page) into four stages, and the blocks' scales;
 //   warp 1     tensor memory, and one thread that issues the MMAs;
 //   warps 2-5  softmax, one row a thread, S read twice from tensor memory (maximum, then weights), O rescaled
 //              when M moves, and the output;
-//   warps 6-9  V: codes from global memory in registers, a tile ahead, to f16 in shared memory (keys that
+//   warps 6-9  V: codes from global memory in registers, two tiles ahead, to f16 in shared memory (keys that
 //              do not count as zeros, so stale slots never reach a product); and the items' Q.
+// What bounds it: the chain S -> softmax -> PV of a tile, about 3000 clocks with two CTAs at work, in which the tensor
+// pipe is 34-42% busy and 54% of the issue slots are taken (3250 warp instructions a tile: a third the weights, a
+// sixth each the maxima and V).
 // The items come from a list built on the device (kv8_schedule_kernel).  Many items: most key tiles first, and CTA c
 // takes entries in snake order.  Few long ones (prompt chunks after many cached positions): the tiles of all items
 // form a line of which every CTA takes an equal share; parts of an item go to scratch as fp32 sums with their
 // (m, l, M) and a second kernel joins them in order.  2 rows of 500-1021 tokens after 9-16 thousand: 376 items on 304
-// CTAs took two turns of the longest; MEASURED.
+// CTAs took two turns of the longest, 405 us; equal shares 371.
 
 #include <algorithm>
 #include <math.h>
@@ -633,6 +638,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         constexpr int HALVES = HD / 64;
         const int kq = ((lane >> 2) & 1) + 2 * (lane >> 3), c16 = lane & 3;
         const long long page_bytes = 2LL * c.n_kv * c.page_size * HD;
+        constexpr int LPR = HD / 16, RPP = 32 / LPR;
+        const int x = lane % LPR, qi_first = (w * 32 + lane / LPR) / p.G, hq_first = w * 32 + lane / LPR - qi_first * p.G;
+        const int rpp_qi = RPP / p.G, rpp_hq = RPP - rpp_qi * p.G;
         int g = 0, it = 0;
         for (int k = 0; ok; ++k) {
             const int n_kt = item(k, r, head);
@@ -669,21 +677,24 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             };
             int page = page_of(0), page1 = page_of(1);
             {   // Q: hi and lo codes of rows 32 w .. 32 w + 31, LPR lanes a row, 16 elements a lane
-                constexpr int LPR = HD / 16, RPP = 32 / LPR;
-                const int x = lane % LPR;
+                int qi = qi_first, hq = hq_first;   // of this lane's row of a pass
 #pragma unroll 1
                 for (int p0 = 0; p0 < LPR; p0 += 4) {
                     uint4 u[4][2];   // four passes in flight; the first ones while the item before still runs
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        const int row = w * 32 + (p0 + y) * RPP + lane / LPR;
-                        const int qi = row / p.G, hq = row - qi * p.G;
                         u[y][0] = u[y][1] = make_uint4(0u, 0u, 0u, 0u);
                         if (qi < p.QT && r.q_lo + qi < r.n) {
                             const uint4* src = reinterpret_cast<const uint4*>(
                                 p.q + (long long)(r.row0 + r.q_lo + qi) * p.row_stride + (long long)(head * p.G + hq) * HD + 16 * x);
                             u[y][0] = src[0];
                             u[y][1] = src[1];
+                        }
+                        qi += rpp_qi;   // RPP rows on
+                        hq += rpp_hq;
+                        if (hq >= p.G) {
+                            hq -= p.G;
+                            ++qi;
                         }
                     }
                     if (p0 == 0 && it >= 1)
