@@ -263,6 +263,21 @@ class _Workspace:
         return self.buf
 
 
+class _KeptWorkspace(_Workspace):
+    """A workspace that grows to at least twice its size and keeps what it outgrew (less than it holds now), since a
+    captured graph may still use that."""
+
+    def __init__(self):
+        super().__init__()
+        self.outgrown = []
+
+    def get(self, nbytes: int, device) -> torch.Tensor:
+        if self.buf is not None and self.buf.numel() < nbytes:
+            self.outgrown.append(self.buf)
+            nbytes = max(nbytes, 2 * self.buf.numel())
+        return super().get(nbytes, device)
+
+
 _LAYER_KEYS = ("attn_norm", "w_qkv", "q_norm", "k_norm", "w_o", "mlp_norm", "w_gate_up", "w_down")
 
 
@@ -823,6 +838,25 @@ class Nvfp4Backbone:
         return out
 
 
+_binding = None
+
+
+def _kv8_calls():
+    """The compiled calls of Kv8Cache (csrc/kv8_binding.cpp), connected to the library's entry points."""
+    global _binding
+    if _binding is None:
+        try:
+            from . import _kv8_binding as m
+        except ImportError as e:
+            raise HraError(f"the binding of the 8-bit cache is missing: build it with __graft_entry__.build() ({e})") from e
+        L = lib()
+        m.connect(HraError, *[ctypes.cast(f, ctypes.c_void_p).value for f in
+                              (L.hra_kv8_append, L.hra_kv8_attention, L.hra_kv8_attention_workspace_size, L.hra_kv8_update,
+                               L.hra_kv8_compact, L.hra_status_string)])
+        _binding = m
+    return _binding
+
+
 class Kv8Cache:
     """A paged 8-bit K/V cache (``hra_kv8_cache``): E4M3 codes uint8 [n_layers, n_pages, 2, n_kv_heads, page_size,
     head_dim], fp32 scales [n_layers, n_pages, 2, n_kv_heads, page_size / 16], the page table int32 [rows,
@@ -830,7 +864,8 @@ class Kv8Cache:
     one device that the object reads and writes in place.
 
     Calls run on the current stream of the cache's device (or `stream`); the workspaces belong to the object, so
-    calls of one object on several streams must be ordered by the caller."""
+    calls of one object on several streams, and replays of graphs that captured them, must be ordered by the caller
+    (or given a workspace each)."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
                  refs: Optional[torch.Tensor] = None):
@@ -857,13 +892,10 @@ class Kv8Cache:
         self.struct = HraKv8Cache(p_codes.value, p_scales.value, p_table.value, p_lens.value,
                                   p_refs.value if p_refs is not None else None, self.errors.data_ptr(), n_layers, n_pages,
                                   n_kv, hd, page, self.rows, self.max_pages)
-        self._ref = self.ref = ctypes.byref(self.struct)
+        self.ref, self._at = ctypes.byref(self.struct), ctypes.addressof(self.struct)
         self._index = codes.get_device()
-        L = lib()
-        self._append, self._attend = L.hra_kv8_append, L.hra_kv8_attention
-        self._update, self._compact = L.hra_kv8_update, L.hra_kv8_compact
-        self._attn_ws, self._pages_ws = _Workspace(), _Workspace()
-        self._attn_key = self._attn_need = self._pages_need = None
+        self._call = _kv8_calls()
+        self._attn_ws, self._pages_ws = _KeptWorkspace(), _KeptWorkspace()
 
     @classmethod
     def new(cls, d, rows: int, n_slots: int, n_pages: Optional[int] = None, page_size: int = 64,
@@ -882,109 +914,50 @@ class Kv8Cache:
         """Tensors for the out argument of update and compact: (page table, lens, refs)."""
         return tuple(torch.empty_like(t) for t in (self.page_table, self.lens, self.refs))
 
-    # One frame's calls take microseconds on the GPU, so these checks read every attribute once and leave the
-    # words of a refusal to _refuse_rows.
-    def _rows(self, t: torch.Tensor, heads: int, name: str):
-        n, h, hd = t.shape if t.dim() == 3 else (0, 0, 0)
-        s0, s1, s2 = t.stride() if t.dim() == 3 else (0, 0, 0)
-        if t.dtype is not torch.bfloat16 or t.get_device() != self._index or hd != self.head_dim or (heads and h != heads) \
-                or (n and (s2 != 1 or (h > 1 and s1 != hd))):
-            self._refuse_rows(t, heads, name)
-        return n, h, s0 if n > 1 else h * hd
-
-    def _refuse_rows(self, t, heads, name):
-        if t.device != self.device:
-            raise HraError(f"{name} must be on the device of the cache")
-        if t.dtype != torch.bfloat16:
-            raise HraError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-        raise HraError(f"{name} must be [rows, {heads or 'heads'}, {self.head_dim}] with contiguous heads")
-
-    def _ints(self, t: torch.Tensor, n: int, name: str) -> int:
-        if t.dtype is not torch.int32 or t.get_device() != self._index or t.shape != (n,) or not t.is_contiguous():
-            raise HraError(f"{name} must be contiguous int32 [{n}] on the device of the cache")
-        return t.data_ptr()
-
-    def _call(self, name, f, args, stream):
-        # the launches go to the cache's device, whichever is current
-        s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self._index)
-        if torch._C._cuda_getDevice() == self._index:
-            rc = f(self._ref, *args, s)
-        else:
-            with torch.cuda.device(self._index):
-                rc = f(self._ref, *args, s)
-        if rc:
-            _check(rc, name)
-
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, start: torch.Tensor, max_new: int,
                stream=None) -> None:
         """hra_kv8_append: k, v bf16 [T, n_kv_heads, head_dim] (rows may be strided), cu int32 [B + 1] and start int32
         [B] on the device: row b's tokens cu[b] .. cu[b + 1) go to its positions from start[b] on."""
-        n, _, stride = self._rows(k, self.n_kv_heads, "k")
-        if self._rows(v, self.n_kv_heads, "v") != (n, self.n_kv_heads, stride):
-            raise HraError("k and v must have the same rows and row stride")
-        B = start.shape[0] if start.dim() else 0
-        self._call("hra_kv8_append", self._append, (layer, k.data_ptr(), v.data_ptr(), stride, self._ints(cu, B + 1, "cu"),
-                                                    self._ints(start, B, "start"), B, n, max_new), stream)
+        self._call.append(self._at, self._index, layer, k, v, cu, start, max_new, stream)
 
     def attention_workspace_size(self, batch: int, total_rows: int, n_q_heads: int, max_new: int, max_len: int) -> int:
-        return lib().hra_kv8_attention_workspace_size(self._ref, batch, total_rows, n_q_heads, max_new, max_len)
+        with torch.cuda.device(self._index):
+            return lib().hra_kv8_attention_workspace_size(self.ref, batch, total_rows, n_q_heads, max_new, max_len)
 
     def attend(self, layer: int, q: torch.Tensor, cu: torch.Tensor, kv_len: torch.Tensor, max_new: int, max_len: int,
                scale: float = 0.0, out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
         """hra_kv8_attention: q bf16 [T, n_q_heads, head_dim] (rows may be strided) of rows' last tokens, kv_len int32
-        [B] positions held -> bf16 [T, n_q_heads, head_dim]."""
-        T, nq, stride = self._rows(q, 0, "q")
-        B = kv_len.shape[0] if kv_len.dim() else 0
-        if out is None:
-            out = torch.empty((T, nq, self.head_dim), dtype=torch.bfloat16, device=self.device)
-        elif out.shape != (T, nq, self.head_dim) or out.dtype is not torch.bfloat16 or out.get_device() != self._index \
-                or not out.is_contiguous():
-            raise HraError("out must be contiguous bf16 [T, n_q_heads, head_dim] on the device of the cache")
-        if workspace is None:
-            key = (B, T, nq, max_new, max_len)
-            if key != self._attn_key:   # the size depends on the shape alone
-                with torch.cuda.device(self._index):
-                    self._attn_need = self.attention_workspace_size(*key)
-                self._attn_key = key
-            workspace = self._attn_ws.get(self._attn_need, self.device)
-        elif workspace.get_device() != self._index or not workspace.is_contiguous():
-            raise HraError("workspace must be contiguous on the device of the cache")
-        self._call("hra_kv8_attention", self._attend,
-                   (layer, q.data_ptr(), stride, nq, scale, self._ints(cu, B + 1, "cu"), self._ints(kv_len, B, "kv_len"), B, T,
-                    max_new, max_len, out.data_ptr(), workspace.data_ptr(), workspace.nbytes), stream)
-        return out
+        [B] positions held -> bf16 [T, n_q_heads, head_dim].  Without a workspace, one of the object's own, which grows
+        with the calls."""
+        own = workspace is None
+        r = self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out,
+                              self._attn_ws.buf if own else workspace, own, stream)
+        if type(r) is int:
+            r = self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out,
+                                  self._attn_ws.get(r, self.device), own, stream)
+        return r
 
-    def _pages(self, name, f, args, out, workspace, stream):
+    def _pages(self, update, parents, room, out, workspace, stream):
         if self.refs is None:
-            raise HraError(f"{name} needs the cache's refs")
-        if out is None:
-            out = (self.page_table, self.lens, self.refs)
-        ptrs = []
-        for t, mine, what in zip(out, (self.page_table, self.lens, self.refs), ("page table", "lens", "refs")):
-            if t.shape != mine.shape or t.dtype is not torch.int32 or t.get_device() != self._index or not t.is_contiguous():
-                raise HraError(f"out must be tensors as empty_pages() makes them ({what})")
-            ptrs.append(t.data_ptr())
+            raise HraError("this needs the cache's refs")
+        out = (self.page_table, self.lens, self.refs) if out is None else tuple(out)
         if workspace is None:
-            if self._pages_need is None:
-                self._pages_need = lib().hra_kv8_pages_workspace_size(self._ref)
-            workspace = self._pages_ws.get(self._pages_need, self.device)
-        elif workspace.get_device() != self._index or not workspace.is_contiguous():
-            raise HraError("workspace must be contiguous on the device of the cache")
-        self._call(name, f, (*args, *ptrs, workspace.data_ptr(), workspace.nbytes), stream)
-        return tuple(out)
+            workspace = self._pages_ws.buf   # one size for the object's life
+            if workspace is None:
+                workspace = self._pages_ws.get(lib().hra_kv8_pages_workspace_size(self.ref), self.device)
+        self._call.pages(self._at, self._index, update, parents, room, *out, workspace, stream)
+        return out
 
     def update(self, parents: Optional[torch.Tensor] = None, room: Optional[torch.Tensor] = None, out=None,
                workspace: Optional[torch.Tensor] = None, stream=None):
         """hra_kv8_update: rows forked, reordered or freed by parents (int32 [rows], -1 = empty) and given pages for
         room (int32 [rows]) more tokens.  In place, or into out (see empty_pages): (page table, lens, refs)."""
-        args = (None if parents is None else self._ints(parents, self.rows, "parents"),
-                None if room is None else self._ints(room, self.rows, "room"))
-        return self._pages("hra_kv8_update", self._update, args, out, workspace, stream)
+        return self._pages(True, parents, room, out, workspace, stream)
 
     def compact(self, out=None, workspace: Optional[torch.Tensor] = None, stream=None):
         """hra_kv8_compact: the pages in use to the low end of the pool; outputs as update."""
-        return self._pages("hra_kv8_compact", self._compact, (), out, workspace, stream)
+        return self._pages(False, None, None, out, workspace, stream)
 
     def device_error(self, stream=None) -> int:
         """Synchronise and return the sticky error bits of every call since the errors word was last zeroed."""

@@ -3,6 +3,7 @@
 Each translation unit under ``csrc/`` is compiled by nvcc in parallel into ``_build/`` at the
 repository root, then linked into ``qwen3_prefill_delayed_gb300/libhra.so`` (cudart linked
 statically, so the library loads on a machine without a GPU and its symbols can be listed there).
+Beside it the host compiler builds ``_kv8_binding.so``, the compiled Python calls of the 8-bit cache.
 """
 from __future__ import annotations
 
@@ -17,6 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libhra.so")
+BINDING_SRC = os.path.join(CSRC, "kv8_binding.cpp")
+BINDING = os.path.join(PKG, "_kv8_binding.so")
 SOURCES = ["api.cu", "gemm_tc.cu", "attention.cu", "attention_tc.cu", "elementwise.cu", "codebook.cu", "fp8.cu",
            "noalloc.cu", "head.cu", "nvfp4.cu", "decode_pass.cu", "kv8_append.cu", "kv8_attention.cu", "kv8_prompt.cu", "kv8_pages.cu",
            "kv8_api.cu"]
@@ -39,6 +42,21 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_command(out: str):
+    """g++ of the CPython module: it needs torch's headers and links its shared libraries, and no CUDA compiler."""
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    nvcc_root = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [os.path.join(t, "include"), sysconfig.get_paths()["include"], os.path.join(nvcc_root, "include"),
+           "/usr/local/cuda/include"]
+    cxx = shutil.which("g++") or "g++"
+    return [cxx, "-shared", "-fPIC", "-O2", "-std=c++17", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *["-I" + d for d in inc], BINDING_SRC, "-o", out, "-L" + os.path.join(t, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + os.path.join(t, "lib")]
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -53,6 +71,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, *ARCH, *FLAGS, *extra_flags, "-c", s, "-o", o])
 
+    binding_tmp = BINDING + f".tmp{os.getpid()}"
+    binding = force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "hra.h")])
+    if binding:
+        jobs.append(_binding_command(binding_tmp))
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -63,9 +86,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             if verbose or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
-                failed.append(cmd[-3])
+                failed.append(next(a for a in cmd if a.startswith(CSRC)))
     if failed:
         raise RuntimeError("nvcc failed for: " + ", ".join(failed))
+    if binding:
+        os.replace(binding_tmp, BINDING)
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]

@@ -9,11 +9,14 @@
 // division, the dequantisation and the re-scaling of earlier codes are exact in fp32, the last one
 // except where a code falls under 2^-6 (E4M3's subnormals).
 //
-// One warp per (block, head): it reads the block's rows of K and V with 16-byte loads, all in flight
-// before the first use, reduces the maxima, and writes the codes of each as 2 KB (head_dim 128) of
-// contiguous memory.  No two warps share a block, so there are no atomics.  Bound by memory and its ramp: 13 thousand
-// tokens x 8 heads x 128 (70 MB) take 16.4 us, 4.3 TB/s (a warp for each of K and V: the same; fewer registers for
-// more warps in flight: 20-36 us), one token of 8 rows 2.4 us inside a graph.
+// One warp per (block, head, K|V): it reads the block's rows with 16-byte loads, all in flight
+// before the first use, reduces the maximum, and writes the block's codes as 2 KB (head_dim 128) of
+// contiguous memory.  No two warps share a block, so there are no atomics.
+//
+// Bound by memory: prompts of 11,400 rows x 8 heads x 128 (70 MB read and written) take 16.5 us, 4.2 TB/s,
+// and one frame of 8 rows 2.4 us in a captured graph, a launch's latency.  One warp for a block's K and V
+// together took the same 16.5 us and 3.5 for the frame (its two chains of loads, maximum and stores follow
+// one another); fewer registers for more warps per SM took 20 to 36 us (the loads are then no longer all in flight).
 #include <cuda_fp8.h>
 
 #include "internal.h"
@@ -42,9 +45,10 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(const Kv8AppendArgs a) 
     const Kv8View& c = a.view;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y;
-    const int unit = blockIdx.x * (blockDim.x >> 5) + warp;   // (block of the row, head)
+    const int unit = blockIdx.x * (blockDim.x >> 5) + warp;   // (block of the row, which, head)
     const int head = unit % c.n_kv;
-    const int blk = unit / c.n_kv;
+    const int which = (unit / c.n_kv) & 1;
+    const int blk = unit / (2 * c.n_kv);
     int row0, n;
     kv8_rows(a.cu, b, a.total_rows, row0, n);
     if (n == 0) return;
@@ -68,71 +72,62 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(const Kv8AppendArgs a) 
     const int slot0 = pos0 & (c.page_size - 1);
     const int lo = max(0, first - pos0);                 // new rows are slots [lo, hi) of the block
     const int hi = min(kKv8Block, first - pos0 + n);
+    const bf16* src = (which ? a.v : a.k) + (long long)head * HD;
     const int r = lane / LPR, e8 = (lane % LPR) * 8;
 
-    uint4 raw[2][PASSES];
+    uint4 raw[PASSES];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        const bf16* src = (which ? a.v : a.k) + (long long)(row0 + (pos0 - first) + r) * a.row_stride + head * HD + e8;
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int i = p * RPL + r;
-            raw[which][p] = make_uint4(0u, 0u, 0u, 0u);
-            if (i >= lo && i < hi) raw[which][p] = *reinterpret_cast<const uint4*>(src + (long long)(p * RPL) * a.row_stride);
-        }
+    for (int p = 0; p < PASSES; ++p) {
+        const int i = p * RPL + r;
+        raw[p] = make_uint4(0u, 0u, 0u, 0u);
+        if (i >= lo && i < hi)
+            raw[p] = *reinterpret_cast<const uint4*>(src + (long long)(row0 + (pos0 + i - first)) * a.row_stride + e8);
     }
-    float* scale_k = c.scales + kv8_scale_at(c, page, 0, head, slot0);
-    float* scale_v = c.scales + kv8_scale_at(c, page, 1, head, slot0);
-    const float before_k = lo > 0 ? *scale_k : 0.f, before_v = lo > 0 ? *scale_v : 0.f;
+    float* scale = c.scales + kv8_scale_at(c, page, which, head, slot0);
+    uint8_t* dst = c.codes + kv8_code_at(c, page, which, head, slot0);
+    const float before = lo > 0 ? *scale : 0.f;
+    float m = 0.f;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        // bf16 bits without their sign order like the values; a NaN is ignored, and stays one as a code; infinities
-        // count as the largest bf16 and saturate
-        uint32_t top = 0u;
+    for (int p = 0; p < PASSES; ++p) {
+        float f[8];
+        unpack8(raw[p], f);
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const uint32_t w[4] = {raw[which][p].x, raw[which][p].y, raw[which][p].z, raw[which][p].w};
+        for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(f[q]));   // a NaN is ignored, and stays one as a code
+    }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t m = w[q] & 0x7FFF7FFFu;
-                top = __vmaxu2(top, m & __vcmpleu2(m, 0x7F807F80u));
-            }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-        top = min(max(top & 0xFFFFu, top >> 16), 0x7F7Fu);
-        const float before = which ? before_v : before_k;
-        const float s = fmaxf(before, __uint_as_float(kv8_scale_bits(top << 16)));
-        const float inv = 1.0f / s;
-        uint8_t* dst = c.codes + kv8_code_at(c, page, which, head, slot0) + r * HD + e8;
-        if (lo > 0 && s > before) {   // the block's earlier codes follow its scale
-            const float ratio = before * inv;
-#pragma unroll
-            for (int p = 0; p < PASSES; ++p) {
-                if (p * RPL + r < lo) {
-                    uint2* at = reinterpret_cast<uint2*>(dst + p * RPL * HD);
-                    const uint2 w = *at;
-                    float f[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const uint32_t byte = ((q < 4 ? w.x : w.y) >> (8 * (q & 3))) & 0xFFu;
-                        f[q] = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
-                    }
-                    *at = to_e4m3x8(f, ratio);
-                }
-            }
-        }
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = fminf(m, __uint_as_float(0x7F7F0000u));   // infinities count as the largest bf16 and saturate
+    const float s = fmaxf(before, __uint_as_float(kv8_scale_bits(__float_as_uint(m))));
+    const float inv = 1.0f / s;
+    if (lo > 0 && s > before) {   // the block's earlier codes follow its scale
+        const float ratio = before * inv;
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
             const int i = p * RPL + r;
-            if (i >= lo && i < hi) {
+            if (i < lo) {
+                uint2* at = reinterpret_cast<uint2*>(dst + i * HD + e8);
+                const uint2 w = *at;
                 float f[8];
-                unpack8(raw[which][p], f);
-                *reinterpret_cast<uint2*>(dst + p * RPL * HD) = to_e4m3x8(f, inv);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const uint32_t byte = ((q < 4 ? w.x : w.y) >> (8 * (q & 3))) & 0xFFu;
+                    f[q] = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
+                }
+                *at = to_e4m3x8(f, ratio);
             }
         }
-        if (lane == 0 && s != before) *(which ? scale_v : scale_k) = s;   // every lane has read it: the shuffles above
     }
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+        const int i = p * RPL + r;
+        if (i >= lo && i < hi) {
+            float f[8];
+            unpack8(raw[p], f);
+            *reinterpret_cast<uint2*>(dst + i * HD + e8) = to_e4m3x8(f, inv);
+        }
+    }
+    __syncwarp();   // every lane has read `before`
+    if (lane == 0 && s != before) *scale = s;
 }
 
 __global__ void kv8_lens_kernel(const int32_t* __restrict__ row_pos, const int32_t* __restrict__ last_row, int batch,
@@ -154,7 +149,7 @@ cudaError_t launch_kv8_lens(const int32_t* row_pos, const int32_t* last_row, int
 }
 
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t st) {
-    const int units = kv8_max_blocks(a.max_new) * a.view.n_kv;
+    const int units = kv8_max_blocks(a.max_new) * 2 * a.view.n_kv;
     const dim3 grid((unsigned)((units + 3) / 4), (unsigned)a.batch);
     if (a.view.head_dim == 128)
         HRA_LAUNCH(kv8_append_kernel<128>, grid, dim3(128), 0, st, a);
