@@ -437,8 +437,8 @@ int hra_prefill_fp8(const hra_dims* dims, const hra_weights* weights, const hra_
  *   errors      one word, set to 0 by the caller: HRA_DEVERR_* bits are OR-ed into it and stay until
  *               the caller clears it (hra_device_error(errors, stream) reads it)
  * codes and scales 16-byte aligned, the rest 4-byte.  head_dim 64 or 128, page_size 16, 32, 64 or 128,
- * n_kv_heads <= 1024, rows <= 65535, max_pages * page_size <= 2^30, rows * max_pages <= 2^30, and 2 * n_pages *
- * n_kv_heads * page_size < 2^31 (else HRA_ERR_UNSUPPORTED).
+ * n_kv_heads <= 1024, rows <= 65535, max_pages * page_size <= 2^30 (times n_kv_heads: <= 2^37), rows * max_pages <=
+ * 2^30, and 2 * n_pages * n_kv_heads * page_size < 2^31 (else HRA_ERR_UNSUPPORTED).
  * A page that several rows list must not be written: only positions of pages that are full are shared
  * (hra_kv8_update sees to it as long as rows are only appended to). */
 typedef struct hra_kv8_cache {
@@ -485,7 +485,8 @@ int hra_kv8_append(const hra_kv8_cache* cache, int32_t layer, const void* k_dev,
  * A kv_len outside [0, max_pages * page_size] is clamped (HRA_DEVERR_POS_RANGE); a table entry that is no page of
  * the pool hides its positions (HRA_DEVERR_PAGE_RANGE).  Slots that hold no token are never used, whatever they
  * contain.  Scores, softmax statistics and output sums are fp32; q and the probabilities enter the products in f16
- * under powers of two (q exactly, probabilities rounded to 11 bits).  The call can be captured and replayed
+ * under powers of two, the probabilities rounded to 11 bits, q exactly but for elements below 2^-10 of its row's
+ * largest, which may be off by 2^-18 of that where max_new * (n_q_heads / n_kv_heads) > 16.  The call can be captured and replayed
  * while max_new and max_len hold.  Calls that may overlap need workspaces of their own. */
 size_t hra_kv8_attention_workspace_size(const hra_kv8_cache* cache, int32_t batch, int32_t total_rows,
                                         int32_t n_q_heads, int32_t max_new, int32_t max_len);

@@ -34,8 +34,10 @@ int kv8_check(const hra_kv8_cache* c) {
         (c->page_size & (c->page_size - 1)) != 0 || c->n_kv_heads > 1024 || c->rows > 65535)
         return HRA_ERR_UNSUPPORTED;
     if ((long long)c->max_pages * c->page_size > (1 << 30) || (long long)c->rows * c->max_pages > (1 << 30) ||
-        2LL * c->n_pages * c->n_kv_heads * c->page_size >= (1LL << 31))
-        return HRA_ERR_UNSUPPORTED;   // positions, table cells, scratch words and a layer's rows stay inside 32 bits
+        2LL * c->n_pages * c->n_kv_heads * c->page_size >= (1LL << 31) ||
+        (long long)c->max_pages * c->page_size * c->n_kv_heads > (1LL << 37))
+        return HRA_ERR_UNSUPPORTED;   // positions, table cells, scratch words, a layer's rows and a sequence's units of
+                                      // 128 keys over all heads stay inside 32 bits
     return HRA_OK;
 }
 
@@ -168,10 +170,10 @@ int hra_kv8_attention(const hra_kv8_cache* cache, int32_t layer, const void* q_d
     if (!aligned(q_dev, 16) || !aligned(out_dev, 16) || q_row_stride < (int64_t)n_q_heads * c.head_dim ||
         q_row_stride % 8 != 0 || !aligned(workspace, 16))
         return HRA_ERR_INVALID_ARG;
-    if (workspace_bytes < hra_kv8_attention_workspace_size(cache, batch, total_rows, n_q_heads, max_new, max_len))
-        return HRA_ERR_WORKSPACE;
     Kv8AttnArgs a{};
     a.view = kv8_view(c, layer);
+    if (workspace_bytes < 256 + kv8_attention_scratch_bytes(a.view, batch, total_rows, n_q_heads, max_new, max_len))
+        return HRA_ERR_WORKSPACE;
     a.q = reinterpret_cast<const bf16*>(q_dev);
     a.row_stride = q_row_stride;
     a.out = reinterpret_cast<bf16*>(out_dev);

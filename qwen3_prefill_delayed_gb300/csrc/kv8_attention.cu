@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
                 int row0, n;
                 kv8_rows(a.cu, b, a.total_rows, row0, n);
                 // a sequence with new tokens but no keys has one unit: its rows get 0
-                if (n > 0 && n * G <= s.max_rows) units = max(1, (length(b) + kUnit - 1) / kUnit);
+                if (n > 0 && n <= s.max_rows / G) units = max(1, (length(b) + kUnit - 1) / kUnit);
                 before[b] = units;
             }
             mine += units;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
             b = blockIdx.y;
             head = blockIdx.x;
             kv8_rows(a.cu, b, a.total_rows, row0, n);
-            if (n == 0 || n * G > s.max_rows) return;
+            if (n == 0 || n > s.max_rows / G) return;
             i1 = 1 << 30;
             u = u_end;
         } else {
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
         if (head == 0 && threadIdx.x == 0 && first_part &&
             (a.kv_len[b] != kv_len || n > a.max_new))
             raise_error(c.err, HRA_DEVERR_POS_RANGE);
-        const int q_n = min(ROWS / G, n);              // tokens beyond max_new get no output
+        const int q_n = min(min(ROWS / G, n), a.max_new);   // tokens beyond max_new get no output
         const int keys = max(0, kv_len - n + q_n);     // positions below the last of them
         const int blk1 = min((keys + kKv8Block - 1) / kKv8Block, i1 >= (1 << 28) ? 1 << 28 : i1 * (kWarps * kPair));
         int blk = (i0 * kWarps + warp) * kPair;
@@ -704,10 +704,10 @@ cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st) {
     const bool prompts = (long long)G * a.max_new > kShortRows;
     uint8_t* scratch = reinterpret_cast<uint8_t*>(a.scratch);
     if (prompts) {
-        // short sequences go with the prompts unless they may hold many keys
-        const int short_rows = a.max_len > kSerialKeys ? kShortRows : 0;
+        // short sequences go with the prompts unless they may hold many keys (and unless the counts say that there are none)
+        const int short_rows = a.max_len > kSerialKeys && (long long)a.batch * a.max_new != a.total_rows ? kShortRows : 0;
         cudaError_t e = launch_kv8_prompt(a, short_rows, st);
-        if (e != cudaSuccess || short_rows == 0 || (long long)a.batch * a.max_new == a.total_rows) return e;
+        if (e != cudaSuccess || short_rows == 0) return e;
         scratch += (kv8_prompt_scratch_bytes(a.view, a.batch, a.total_rows, G, a.max_new, a.max_len) + 255) & ~size_t(255);
     }
     SplitArgs s{};

@@ -40,28 +40,29 @@ __device__ __forceinline__ float mantissa_of(float s) {
 }
 
 // Exclusive scan of one value a thread over a CTA of 1024 threads; total gets the sum.
-__device__ __forceinline__ int block_scan(int v, int& total) {
-    __shared__ int warp_sum_s[32];
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T& total) {
+    __shared__ T warp_sum_s[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int incl = v;
+    T incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        const T u = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += u;
     }
     if (lane == 31) warp_sum_s[warp] = incl;
     __syncthreads();
     if (warp == 0) {
-        int t = warp_sum_s[lane];
+        T t = warp_sum_s[lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, t, o);
+            const T u = __shfl_up_sync(0xffffffffu, t, o);
             if (lane >= o) t += u;
         }
         warp_sum_s[lane] = t;
     }
     __syncthreads();
-    const int before = warp ? warp_sum_s[warp - 1] : 0;
+    const T before = warp ? warp_sum_s[warp - 1] : 0;
     total = warp_sum_s[31];
     __syncthreads();
     return before + incl - v;

@@ -227,86 +227,125 @@ __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float
 
 // One CTA.  The non-empty (query tile, sequence) pairs: by a counting sort, most key tiles first, or, for equal shares,
 // in the order of the sequences with the tiles before each (the shares' borders decide where sums are split, so the
-// order must not depend on which thread comes first).
+// order must not depend on which thread comes first).  A thread a sequence counts its tiles, then a thread a pair
+// finds its sequence in their running sum: the time follows the tiles there are, not batch times the longest.
 constexpr int kBins = 1024;
-__global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a, int G, int QT, int tiles,
-                                                            int short_rows, int shares, int32_t* __restrict__ list) {
+__global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a, int G, int QT, int short_rows, int shares,
+                                                            int most, int32_t* __restrict__ list) {
     pdl_launch();
     pdl_wait();
     __shared__ int hist[kBins];
+    __shared__ int at_s[1025], row0_s[1024], n_s[1024], len_s[1024];
     __shared__ int total;
-    for (int i = threadIdx.x; i < kBins; i += blockDim.x) hist[i] = 0;
-    __syncthreads();
+    const int tid = threadIdx.x;
+    for (int i = tid; i < kBins; i += blockDim.x) hist[i] = 0;
     const long long room = (long long)a.view.max_pages << a.view.page_shift;
-    const long long pairs = (long long)tiles * a.batch;
-    auto pair = [&](int tile, int b, PromptRec& r) -> int {   // -1: nothing there
-        r.b = b;
-        kv8_rows(a.cu, r.b, a.total_rows, r.row0, r.n);
-        r.q_lo = tile * QT;
-        if (r.q_lo >= r.n || r.n * G <= short_rows) return -1;
-        const int len = a.kv_len[r.b];
-        if (tile == 0 && (len < 0 || len > room || r.n > a.max_new)) raise_error(a.view.err, HRA_DEVERR_POS_RANGE);
-        r.kv_len = len < 0 ? 0 : (int)min(room, (long long)len);
+    // Sequences b0 .. b0 + 1023, after `count` pairs: their pairs, and at_s = the pairs before each.  Rows beyond
+    // max_new are left out: the first n of a sequence with n fewer positions are what they are.
+    auto chunk = [&](int b0, int count, bool report) {
+        const int b = b0 + tid;
+        int row0 = 0, n = 0, len = 0;
+        if (b < a.batch) {
+            kv8_rows(a.cu, b, a.total_rows, row0, n);
+            if (n > 0) {
+                const int held = a.kv_len[b];
+                len = held < 0 ? 0 : (int)min(room, (long long)held);
+                const int over = max(0, n - a.max_new);
+                if (report && n > short_rows / G && (len != held || over)) raise_error(a.view.err, HRA_DEVERR_POS_RANGE);
+                if (n <= short_rows / G) n = 0;
+                else n -= over;
+                len -= over;
+            }
+        }
+        long long all;
+        const long long at = block_scan((long long)((n + QT - 1) / QT), all);
+        const int left = most - count;   // enough for rows that no two sequences share
+        if (report && tid == 0 && all > left) raise_error(a.view.err, HRA_DEVERR_POS_RANGE);
+        at_s[tid] = (int)min((long long)left, at);
+        row0_s[tid] = row0;
+        n_s[tid] = n;
+        len_s[tid] = len;
+        if (tid == 0) at_s[1024] = (int)min((long long)left, all);
+        __syncthreads();
+        return at_s[1024];
+    };
+    auto pair = [&](int p, int b0, PromptRec& r) {   // pair p of the chunk
+        int lo = 0, hi = min(1024, a.batch - b0);     // the last sequence with at_s <= p that has a tile
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (at_s[mid] <= p) lo = mid;
+            else hi = mid;
+        }
+        r.b = b0 + lo;
+        r.row0 = row0_s[lo];
+        r.n = n_s[lo];
+        r.q_lo = (p - at_s[lo]) * QT;
+        r.kv_len = len_s[lo];
         r.keys = max(0, r.kv_len - r.n + min(r.n, r.q_lo + QT));
         return kBins - 1 - min(kBins - 1, (r.keys + TK - 1) / TK);
     };
+    auto put = [&](int i, const PromptRec& r, long long before) {
+        int4* to = reinterpret_cast<int4*>(list + kRecWords * (1 + (long long)i));
+        to[0] = make_int4(r.b, r.row0, r.n, r.q_lo);
+        to[1] = make_int4(r.kv_len, r.keys, (int)(before & 0xFFFFFFFFll), (int)(before >> 32));
+    };
     PromptRec r;
+    int count = 0;
     if (shares) {
-        int count = 0;
         long long before = 0;
-        for (long long p0 = 0; p0 < pairs; p0 += 1024) {
-            const long long pr = p0 + threadIdx.x;
-            const int b = (int)(pr / tiles);
-            const bool in = pr < pairs && pair((int)(pr - (long long)b * tiles), b, r) >= 0;
-            int n, units;
-            const int at = count + block_scan(in ? 1 : 0, n);
-            const long long at_unit = before + (long long)a.view.n_kv * block_scan(in ? key_tiles(r.keys) : 0, units);
-            if (in) {
-                int4* to = reinterpret_cast<int4*>(list + kRecWords * (1 + (long long)at));
-                to[0] = make_int4(r.b, r.row0, r.n, r.q_lo);
-                to[1] = make_int4(r.kv_len, r.keys, (int)(at_unit & 0xFFFFFFFFll), (int)(at_unit >> 32));
+        for (int b0 = 0; b0 < a.batch; b0 += 1024) {
+            const int here = chunk(b0, count, true);
+            for (int p0 = 0; p0 < here; p0 += 1024) {
+                const bool in = p0 + tid < here;
+                if (in) pair(p0 + tid, b0, r);
+                long long units;
+                const long long at = block_scan((long long)(in ? key_tiles(r.keys) : 0), units);
+                if (in) put(count + p0 + tid, r, before + a.view.n_kv * at);
+                before += a.view.n_kv * units;
             }
-            count += n;
-            before += (long long)a.view.n_kv * units;
+            count += here;
         }
-        if (threadIdx.x == 0) {
+        if (tid == 0) {
             list[0] = count;
             *reinterpret_cast<long long*>(list + 2) = before;
         }
         return;
     }
-    for (long long pr = threadIdx.x; pr < pairs; pr += blockDim.x) {
-        const int bin = pair((int)(pr / a.batch), (int)(pr % a.batch), r);
-        if (bin >= 0) atomicAdd(&hist[bin], 1);
+    for (int b0 = 0; b0 < a.batch; b0 += 1024) {
+        const int here = chunk(b0, count, true);
+        for (int p = tid; p < here; p += 1024) atomicAdd(&hist[pair(p, b0, r)], 1);
+        count += here;
+        __syncthreads();
     }
-    __syncthreads();
-    if (threadIdx.x < 32) {
+    if (tid < 32) {
         constexpr int per = kBins / 32;
         int s = 0;
-        for (int i = 0; i < per; ++i) s += hist[threadIdx.x * per + i];
+        for (int i = 0; i < per; ++i) s += hist[tid * per + i];
         int incl = s;
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if ((int)threadIdx.x >= o) incl += v;
+            if (tid >= o) incl += v;
         }
         int run = incl - s;
         for (int i = 0; i < per; ++i) {
-            const int h = hist[threadIdx.x * per + i];
-            hist[threadIdx.x * per + i] = run;
+            const int h = hist[tid * per + i];
+            hist[tid * per + i] = run;
             run += h;
         }
-        if (threadIdx.x == 31) total = incl;
+        if (tid == 31) total = incl;
     }
     __syncthreads();
-    for (long long pr = threadIdx.x; pr < pairs; pr += blockDim.x) {
-        const int bin = pair((int)(pr / a.batch), (int)(pr % a.batch), r);
-        if (bin >= 0) {
-            int4* at = reinterpret_cast<int4*>(list + kRecWords * (1 + (long long)atomicAdd(&hist[bin], 1)));
-            at[0] = make_int4(r.b, r.row0, r.n, r.q_lo);
-            at[1] = make_int4(r.kv_len, r.keys, 0, 0);
+    count = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 1024) {
+        const int here = a.batch <= 1024 ? at_s[1024] : chunk(b0, count, false);
+        for (int p = tid; p < here; p += 1024) {
+            const int bin = pair(p, b0, r);
+            put(atomicAdd(&hist[bin], 1), r, 0);
         }
+        count += here;
+        __syncthreads();
     }
-    if (threadIdx.x == 0) list[0] = total;
+    if (tid == 0) list[0] = total;
 }
 
 template <int HD>
@@ -855,12 +894,14 @@ long long most_pairs(int batch, int total_rows, int QT, int max_new) {
     return std::min((long long)((max_new + QT - 1) / QT) * batch, (long long)total_rows / QT + batch);
 }
 
+// Sequences that share no rows have sum ceil(n / QT) <= total / QT + batch tiles.
+long long list_pairs(int batch, int total_rows, int G) { return (long long)total_rows / (TROWS / G) + batch; }
 size_t list_bytes(int batch, int total_rows, int G) {
-    return ((size_t)total_rows / (TROWS / G) + (size_t)batch + 1) * kRecWords * sizeof(int32_t);
+    return (size_t)(list_pairs(batch, total_rows, G) + 1) * kRecWords * sizeof(int32_t);
 }
 
 template <int HD>
-cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int tiles, int short_rows, cudaStream_t st) {
+cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaStream_t st) {
     using C = Cfg<HD>;
     alignas(64) CUtensorMap map;
     const long long rows = 2LL * a.view.n_pages * a.view.n_kv * a.view.page_size;
@@ -877,7 +918,8 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int tiles, int short_
     int32_t* list = reinterpret_cast<int32_t*>(a.scratch);
     const long long pairs = most_pairs(a.batch, a.total_rows, QT, a.max_new);
     const bool shares = prompt_shares(pairs, a.view.n_kv, a.max_len);
-    HRA_LAUNCH(kv8_schedule_kernel, dim3(1), dim3(1024), 0, st, a, G, QT, tiles, short_rows, shares ? 1 : 0, list);
+    HRA_LAUNCH(kv8_schedule_kernel, dim3(1), dim3(1024), 0, st, a, G, QT, short_rows, shares ? 1 : 0,
+               (int)list_pairs(a.batch, a.total_rows, G), list);
     PromptArgs p{};
     p.view = a.view;
     p.q = a.q;
@@ -912,9 +954,7 @@ size_t kv8_prompt_scratch_bytes(const Kv8View& c, int batch, int total_rows, int
 
 cudaError_t launch_kv8_prompt(const Kv8AttnArgs& a, int short_rows, cudaStream_t st) {
     const int G = a.nq / a.view.n_kv, QT = TROWS / G;
-    const int tiles = (a.max_new + QT - 1) / QT;
-    return a.view.head_dim == 128 ? launch_hd<128>(a, G, QT, tiles, short_rows, st)
-                                  : launch_hd<64>(a, G, QT, tiles, short_rows, st);
+    return a.view.head_dim == 128 ? launch_hd<128>(a, G, QT, short_rows, st) : launch_hd<64>(a, G, QT, short_rows, st);
 }
 
 }  // namespace hra

@@ -101,7 +101,7 @@ def append(cache, layer, k, v, cu, start):
                     codes[page, which, h, slot + lo - blk * 16:slot + hi - blk * 16] = e4m3_code(part / s)
 
 
-def attend(cache, layer, q, cu, kv_len, scale=None):
+def attend(cache, layer, q, cu, kv_len, scale=None, split=False):
     """(out float64 [T, nq, D], bound [T, nq, D]): the value and how far a kernel may be from it.
 
     The kernel's roundings: the output to bf16 (half a step of it); each probability times its block's scale
@@ -110,7 +110,8 @@ def attend(cache, layer, q, cu, kv_len, scale=None):
     2^-23 of sum |q k| each (the accumulation of a tensor core may truncate), and the product with the scale and
     the log2 conversion, 4 roundings of the score, so the exponential is off by that absolute error and by
     2^-22 of its own; the sums of n terms and their rescalings, 2^-24 (n + 64) relative at most, in numerator
-    and denominator."""
+    and denominator.  split: q as two E4M3 values, each element off by up to 2^-18 of its row's largest, and the score
+    by the sum of that times |k|."""
     T, nq, D = q.shape
     H = cache["codes"].shape[3]
     G = nq // H
@@ -129,13 +130,14 @@ def attend(cache, layer, q, cu, kv_len, scale=None):
         x = q[lo:lo + n].double().view(n, H, G, D)
         s = torch.einsum("nhgd,shd->hgns", x, kv[0]) * scale
         mag = torch.einsum("nhgd,shd->hgns", x.abs(), kv[0].abs()) * scale
+        lost = torch.einsum("nhg,shd->hgns", x.abs().amax(-1), kv[0].abs()) * (scale * 2.0 ** -18 if split else 0.0)
         s = s.masked_fill(~seen, -math.inf)
         top = s.amax(-1, keepdim=True) if L else torch.full(s.shape[:-1] + (1,), -math.inf, dtype=torch.float64)
         p = (s - torch.where(torch.isinf(top), torch.zeros_like(top), top)).exp()
         total = p.sum(-1, keepdim=True)
         p = p / torch.where(total > 0, total, torch.ones_like(total))
         o = torch.einsum("hgns,shd->nhgd", p, kv[1])
-        off = (mag * D * 2.0 ** -23 + s.masked_fill(~seen, 0.0).abs() * 2.0 ** -22).masked_fill(~seen, 0.0)
+        off = (mag * D * 2.0 ** -23 + s.masked_fill(~seen, 0.0).abs() * 2.0 ** -22 + lost).masked_fill(~seen, 0.0)
         worst = off.amax(-1) if L else torch.zeros(s.shape[:-1], dtype=torch.float64)
         rel = U_F16 + 2 * (torch.expm1(worst) + 2.0 ** -22 + U_F32 * (L + 64))
         mean = torch.einsum("hgns,shd->nhgd", p, kv[1].abs()) * rel.permute(2, 0, 1)[..., None]

@@ -565,3 +565,107 @@ def test_wrapper_refusals(hra):
     with pytest.raises(hra.HraError):
         hra.Kv8Cache(kv.codes, kv.scales, kv.page_table, kv.lens).update()
     assert kv.attend(0, k[:0], i32([0, 0]).cuda(), n, 0, 20).shape == (0, 2, 64)
+
+
+# ----------------------------------------------------------------------- calls at the edge of what is allowed
+
+@pytest.mark.parametrize("G,max_len", [(2, 3000), (4, 3000), (2, 1500)])
+def test_padded_rows_behind_a_short_sequence(hra, G, max_len):
+    """batch * max_new = total_rows says nothing when the last rows are padding: a sequence of one token is answered."""
+    kv_len = [40, max_len]
+    c = build(kv_len, H=2, D=64, P=16, seed=5)
+    kv = gpu(hra, c)
+    q = torch.randn(64, 2 * G, 64, generator=torch.Generator().manual_seed(6)).to(BF16)
+    out = torch.full((64, 2 * G, 64), 7.0, dtype=BF16).cuda()
+    kv.attend(0, q.cuda(), i32([0, 32, 33]).cuda(), i32(kv_len).cuda(), 32, max_len, out=out)
+    want, bound = R.attend(c, 0, q, [0, 32, 33], kv_len)
+    assert bool(((out.double().cpu() - want).abs() <= bound)[:33].all())
+    assert bool((out[33:] == 7.0).all()) and kv.device_error() == 0
+
+
+@pytest.mark.parametrize("new,max_new,G,max_len", [([5, 3, 1], 2, 4, 130), ([5, 3], 2, 4, 700), ([70, 40], 50, 2, 300),
+                                                   ([70, 9], 50, 2, 2500)])
+def test_tokens_beyond_max_new_get_no_output(hra, new, max_new, G, max_len):
+    kv_len = [max_len, 60, 20][:len(new)]
+    c = build(kv_len, H=2, D=64, P=16, seed=7)
+    kv = gpu(hra, c)
+    T, cu = sum(new), cu_of(new)
+    q = torch.randn(T, 2 * G, 64, generator=torch.Generator().manual_seed(8)).to(BF16)
+    out = torch.full((T, 2 * G, 64), 7.0, dtype=BF16).cuda()
+    kv.attend(0, q.cuda(), i32(cu).cuda(), i32(kv_len).cuda(), max_new, max_len, out=out)
+    want, bound = R.attend(c, 0, q, cu, kv_len)
+    ok = (out.double().cpu() - want).abs() <= bound
+    for b, n in enumerate(new):
+        m = cu[b] + min(n, max_new)
+        assert bool(ok[cu[b]:m].all()) and bool((out[m:cu[b + 1]] == 7.0).all())
+    assert kv.device_error() == hra.DEVERR_POS_RANGE
+
+
+@pytest.mark.parametrize("max_len", [400, 2500])
+def test_sequences_that_claim_the_same_rows_stay_inside_the_workspace(hra, max_len):
+    """A cu that does not ascend asks for more tiles than the rows have: the list of tiles ends where its room ends."""
+    B, T, G = 40, 200, 4
+    c = build([300] * B, H=1, D=64, P=16, width=160, seed=9)
+    kv = gpu(hra, c)
+    cu = i32([0 if i % 2 == 0 else T for i in range(B + 1)]).cuda()
+    q = torch.randn(T, G, 64, generator=torch.Generator().manual_seed(8)).to(BF16).cuda()
+    size = kv.attention_workspace_size(B, T, G, T, max_len)
+    room = torch.full((size + 65536,), 0x5A, dtype=torch.uint8, device="cuda")
+    out = torch.full((T + 64, G, 64), 7.0, dtype=BF16).cuda()
+    kv.attend(0, q, cu, i32([300] * B).cuda(), T, max_len, out=out[:T], workspace=room[:size])
+    assert kv.device_error() == hra.DEVERR_POS_RANGE
+    assert bool((room[size:] == 0x5A).all()) and bool((out[T:] == 7.0).all())
+
+
+@pytest.mark.parametrize("G,far", [(8, 1500), (1, 2500)])
+def test_prompts_of_more_sequences_than_a_list_chunk(hra, G, far):
+    rng = random.Random(11)
+    new = [rng.choice([0, 1, 3, 20]) for _ in range(1100)]
+    new[3] = new[1090] = 40
+    lens = [n + rng.randrange(50) for n in new]
+    lens[1090] = far
+    check(hra, build(lens, H=1, D=64, P=16, seed=12), new, lens, G)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 9]])
+def test_queries_with_elements_far_below_the_largest(hra, new):
+    """One element of a q row 2^0 .. 2^14 times the others, which alone meet large keys: what the split of q into two E4M3
+    values drops, 2^-18 of the largest (kv8_ref.attend, split)."""
+    kv_len = [300, 170]
+    c = build(kv_len, H=1, D=64, P=16, seed=13)
+    c["codes"][..., 0] &= 0x87                     # dim 0 of K and V: zero or subnormal
+    T = sum(new)
+    g = torch.Generator().manual_seed(14)
+    q = torch.randn(T, 2, 64, generator=g) * 0.1
+    q[..., 0] = 0.2 * torch.exp2(torch.arange(T * 2) % 15).view(T, 2)
+    q = q.to(BF16)
+    kv = gpu(hra, c)
+    got = kv.attend(0, q.cuda(), i32(cu_of(new)).cuda(), i32(kv_len).cuda(), max(new), 300)
+    want, bound = R.attend(c, 0, q, cu_of(new), kv_len, split=2 * max(new) > 16)
+    assert bool(((got.double().cpu() - want).abs() <= bound).all()) and kv.device_error() == 0
+
+
+def test_a_captured_call_keeps_its_workspace(hra):
+    """The object's workspace grows for a longer call; a graph captured before still has the one it was captured with."""
+    c = build([900, 700], H=2, D=64, P=16, seed=15)
+    kv = gpu(hra, c)
+    g = torch.Generator().manual_seed(16)
+    q = torch.randn(2, 4, 64, generator=g).to(BF16).cuda()
+    cu, n = i32([0, 1, 2]).cuda(), i32([900, 700]).cuda()
+    first = kv.attend(0, q, cu, n, 1, 900)
+    out = torch.zeros_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kv.attend(0, q, cu, n, 1, 900, out=out)
+    small = kv._attn_ws.buf
+    long = torch.randn(300, 4, 64, generator=g).to(BF16).cuda()
+    kv.attend(0, long, i32([0, 290, 300]).cuda(), n, 290, 900)
+    need = kv.attention_workspace_size(2, 300, 4, 290, 900)
+    if small.numel() >= need:
+        kv._attn_ws.get(2 * small.numel(), kv.device)
+    assert kv._attn_ws.buf.data_ptr() != small.data_ptr() and kv._attn_ws.outgrown[-1] is small
+    del small
+    fill = [torch.full((kv._attn_ws.outgrown[-1].numel(),), 3, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first) and all(bool((f == 3).all()) for f in fill)
