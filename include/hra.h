@@ -487,7 +487,8 @@ int hra_kv8_append(const hra_kv8_cache* cache, int32_t layer, const void* k_dev,
  * contain.  Scores, softmax statistics and output sums are fp32; q and the probabilities enter the products in f16
  * under powers of two, the probabilities rounded to 11 bits, q exactly but for elements below 2^-10 of its row's
  * largest, which may be off by 2^-18 of that where max_new * (n_q_heads / n_kv_heads) > 16.  The call can be captured and replayed
- * while max_new and max_len hold.  Calls that may overlap need workspaces of their own. */
+ * while max_new and max_len hold.  Calls that may overlap need workspaces of their own; the size never falls when an
+ * argument grows, so one sized for the largest call does for all. */
 size_t hra_kv8_attention_workspace_size(const hra_kv8_cache* cache, int32_t batch, int32_t total_rows,
                                         int32_t n_q_heads, int32_t max_new, int32_t max_len);
 int hra_kv8_attention(const hra_kv8_cache* cache, int32_t layer, const void* q_dev, int64_t q_row_stride,

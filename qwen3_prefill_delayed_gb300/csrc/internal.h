@@ -369,7 +369,7 @@ struct Kv8AttnArgs {
 size_t kv8_attention_scratch_bytes(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int max_len);
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st);
 // the tcgen05 form (kv8_prompt.cu) for sequences with more than short_rows (position, head) rows a kv head
-size_t kv8_prompt_scratch_bytes(const Kv8View& c, int batch, int total_rows, int G, int max_new, int max_len);
+size_t kv8_prompt_scratch_bytes(const Kv8View& c, int batch, int total_rows, int G, int max_len);
 cudaError_t launch_kv8_prompt(const Kv8AttnArgs& a, int short_rows, cudaStream_t st);
 // 2-D map of E4M3 rows [rows, hd]: boxes of box_rows whole rows, swizzled over the row's bytes (128 or 64)
 bool make_map_codes(CUtensorMap* m, const void* base, long long rows, int hd, int box_rows);

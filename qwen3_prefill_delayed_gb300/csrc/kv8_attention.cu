@@ -694,8 +694,8 @@ size_t split_scratch(const Kv8View& c, int ng) {
 size_t kv8_attention_scratch_bytes(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int max_len) {
     const int G = nq / c.n_kv;
     size_t n = 0;
-    if ((long long)G * max_new > kShortRows) n = (kv8_prompt_scratch_bytes(c, batch, total_rows, G, max_new, max_len) + 255) & ~size_t(255);
-    if (!goes_whole(batch, max_len)) n += split_scratch(c, column_groups(G, max_new));
+    if ((long long)G * max_new > kShortRows) n = (kv8_prompt_scratch_bytes(c, batch, total_rows, G, max_len) + 255) & ~size_t(255);
+    if (max_len > kWholeUnits * kUnit) n += split_scratch(c, column_groups(G, max_new));   // also where batch > kMaxBatch
     return n;
 }
 
@@ -708,7 +708,7 @@ cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st) {
         const int short_rows = a.max_len > kSerialKeys && (long long)a.batch * a.max_new != a.total_rows ? kShortRows : 0;
         cudaError_t e = launch_kv8_prompt(a, short_rows, st);
         if (e != cudaSuccess || short_rows == 0) return e;
-        scratch += (kv8_prompt_scratch_bytes(a.view, a.batch, a.total_rows, G, a.max_new, a.max_len) + 255) & ~size_t(255);
+        scratch += (kv8_prompt_scratch_bytes(a.view, a.batch, a.total_rows, G, a.max_len) + 255) & ~size_t(255);
     }
     SplitArgs s{};
     s.a = a;

@@ -944,10 +944,11 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
 
 }  // namespace
 
-size_t kv8_prompt_scratch_bytes(const Kv8View& c, int batch, int total_rows, int G, int max_new, int max_len) {
-    const int QT = TROWS / G;
+// Never less for more of anything, so that a caller may size it for the most: the shares' slots also where there are so
+// many pairs that they are not used.
+size_t kv8_prompt_scratch_bytes(const Kv8View& c, int batch, int total_rows, int G, int max_len) {
     size_t n = list_bytes(batch, total_rows, G);
-    if (prompt_shares(most_pairs(batch, total_rows, QT, max_new), c.n_kv, max_len))
+    if (max_len > kSharesFrom)
         n += (size_t)prompt_slots() * (sizeof(PromptDesc) + 2 * sizeof(float) * TROWS * (c.head_dim + 3));
     return n;
 }

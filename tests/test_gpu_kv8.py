@@ -669,3 +669,26 @@ def test_a_captured_call_keeps_its_workspace(hra):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, first) and all(bool((f == 3).all()) for f in fill)
+
+
+@pytest.mark.parametrize("rows,W,P,seed", [(90, 300, 16, 5), (70, 500, 16, 6), (2100, 20, 16, 7)])
+def test_update_of_large_tables_in_a_chain(hra, rows, W, P, seed):
+    """Tables and pools whose plan takes several CTAs."""
+    test_update_in_a_chain(hra, rows, W, P, seed)
+
+
+def test_large_update_without_enough_pages_changes_nothing(hra):
+    c = build([20, 17], L=1, H=1, D=64, P=16, rows=1500, width=40, spare=3000, stale=0x22)
+    kv = gpu(hra, c)
+    for parents, room in (([0] * 1500, [16] + [40] * 1499), ([0, 1] + [-1] * 1498, [641] + [0] * 1499)):
+        assert R.update(c, parents, room) is None
+        for out in (None, kv.empty_pages()):
+            kv.errors.zero_()
+            t, n, r = kv.update(i32(parents).cuda(), i32(room).cuda(), out=out)
+            assert kv.device_error() == hra.DEVERR_PAGES_SPENT
+            assert torch.equal(t.cpu(), c["table"]) and torch.equal(n.cpu(), c["lens"]) and torch.equal(r.cpu(), c["refs"])
+
+
+@pytest.mark.parametrize("pages,used", [(40000, 9000), (40001, 33000), (33000, 0), (33000, 33000)])
+def test_compact_of_a_large_pool(hra, pages, used):
+    test_compact(hra, pages, used)

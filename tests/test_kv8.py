@@ -255,3 +255,26 @@ def test_reference_update_and_compact():
     assert moves == [(5, 2), (9, 4)] and table.tolist()[1] == [2, 0, 1, -1] and table.tolist()[0] == [2, 4, -1, -1]
     assert refs.tolist() == [1, 1, 2, 1, 1] + [0] * 7
     assert R.update(c, None, [0, 0, 200, 0]) is None
+
+
+def test_attention_workspace_never_falls_when_a_call_grows(hra):
+    c = _cache(hra, rows=4096, max_pages=4096)
+    size = lambda *a: hra.lib().hra_kv8_attention_workspace_size(ctypes.byref(c), *a)  # noqa: E731
+    grow = [[1, 2, 600, 1024, 1025, 4096], [1, 100, 5000, 200000], [2, 4, 16, 32], [1, 2, 9, 100, 5000, 200000],
+            [0, 100, 512, 513, 2048, 2049, 60000]]
+
+    def walk(i, args):
+        if i == len(grow):
+            return {tuple(args): size(*args)} if args[3] <= args[1] else {}
+        out = {}
+        for v in grow[i]:
+            out.update(walk(i + 1, args + [v]))
+        return out
+
+    sizes = walk(0, [])
+    assert all(n > 0 for n in sizes.values())
+    for args, n in sizes.items():
+        for i, values in enumerate(grow):
+            j = values.index(args[i]) + 1
+            more = args[:i] + (values[j],) + args[i + 1:] if j < len(values) else args
+            assert more not in sizes or sizes[more] >= n, (args, more)
