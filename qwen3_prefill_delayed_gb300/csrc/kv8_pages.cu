@@ -58,6 +58,9 @@ struct PlanScratch {
         table = list + n_pages;
     }
 };
+// What one CTA's update keeps in shared memory instead: first, base, lens, refs and list, and the rows' parents.
+size_t one_cta_bytes(int rows, int n_pages) { return 4 * (4 * (size_t)rows + 2 * (size_t)n_pages); }
+constexpr size_t kOneCtaMost = 200 * 1024;
 
 // The CTAs of a plan: CS of them, one cluster.
 template <int CS>
@@ -90,12 +93,27 @@ template <int CS>
 __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8PagesArgs a) {
     pdl_launch();
     pdl_wait();
-    const PlanScratch s(a.scratch, a.rows, a.n_pages);
+    PlanScratch s(a.scratch, a.rows, a.n_pages);
     const Team<CS> team;
     __shared__ unsigned int bad;
+    __shared__ int moved;   // one CTA's moves
+    extern __shared__ int32_t words[];
+    int32_t* const refs_out = s.refs;
+    int32_t* const lens_out = s.lens;
+    int32_t* const parents = words;
+    if (CS == 1) {
+        s.first = words + a.rows;
+        s.base = s.first + a.rows;
+        s.lens = s.base + a.rows;
+        s.refs = s.lens + a.rows;
+        s.list = s.refs + a.n_pages;
+    }
     const int warp = team.tid >> 5, lane = threadIdx.x & 31;
     const int R = a.rows, W = a.max_pages, P = 1 << a.page_shift;
-    if (threadIdx.x == 0) bad = 0u;
+    if (threadIdx.x == 0) {
+        bad = 0u;
+        moved = 0;
+    }
     if (team.tid == 0) {
         s.head[0] = 0;
         s.head[1] = 1;
@@ -105,11 +123,14 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8
     for (int b = team.tid; b < R; b += team.kThreads) s.first[b] = R;
     team.sync();
     auto parent = [&](int b) {
+        if (CS == 1) return parents[b];
         const int p = a.parents ? a.parents[b] : b;
         return p >= 0 && p < R ? p : -1;
     };
     for (int b = team.tid; b < R; b += team.kThreads) {
-        const int p = parent(b);
+        int p = a.parents ? a.parents[b] : b;
+        if (p < 0 || p >= R) p = -1;
+        if (CS == 1) parents[b] = p;
         if (p < 0 && a.parents[b] != -1) atomicOr(&bad, HRA_DEVERR_PARENT_RANGE);
         int len = 0;
         if (p >= 0) {
@@ -121,6 +142,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8
             }
         }
         s.lens[b] = len;
+        if (CS == 1) lens_out[b] = len;
     }
     team.sync();
     // the row's old pages i0 + 32 c + lane, -1 where there is none or (wrong) it is no page of the pool
@@ -230,7 +252,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8
                         now = s.list[at + __popc(mask & ((1u << lane) - 1u))];
                         s.refs[now] = 1;
                         if (old[c] >= 0 && ((long long)i << a.page_shift) < len)
-                            s.moves[atomicAdd(&s.head[0], 1)] = make_int2(old[c], now);
+                            s.moves[atomicAdd(CS == 1 ? &moved : &s.head[0], 1)] = make_int2(old[c], now);
                     }
                     at += __popc(mask);
                     if (i < W) s.table[(long long)b * W + i] = now;
@@ -240,23 +262,31 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8
     } else if (team.tid == 0) {
         s.head[1] = 0;
     }
+    if (CS == 1) {
+        __syncthreads();
+        for (int p = threadIdx.x; p < a.n_pages; p += kPlanThreads) refs_out[p] = s.refs[p];
+    }
     if (threadIdx.x == 0) {
+        if (CS == 1) s.head[0] = moved;
         if (fail) bad |= HRA_DEVERR_PAGES_SPENT;
         if (bad) raise_error(a.err, bad);
     }
 }
 
-template <int CS>
+// One CTA (RUN pages a thread at once, its moves in shared memory) or a cluster.
+template <int CS, int RUN>
 __global__ void __launch_bounds__(kPlanThreads) kv8_compact_plan_kernel(const Kv8PagesArgs a) {
     pdl_launch();
     pdl_wait();
     const PlanScratch s(a.scratch, a.rows, a.n_pages);
     const Team<CS> team;
+    __shared__ int2 moves_s[CS == 1 ? kTeamPages / 2 + 1 : 1];
+    int2* const moves_at = CS == 1 ? moves_s : s.moves;
     const int lo = team.page_lo(a.n_pages), hi = team.page_hi(a.n_pages);
     int used = 0;
-    for (int p0 = lo; p0 < hi; p0 += kRun * kPlanThreads)
+    for (int p0 = lo; p0 < hi; p0 += RUN * kPlanThreads)
 #pragma unroll
-        for (int e = 0; e < kRun; ++e) {   // in any order: neighbours to neighbouring threads
+        for (int e = 0; e < RUN; ++e) {   // in any order: neighbours to neighbouring threads
             const int p = p0 + e * kPlanThreads + (int)threadIdx.x;
             used += p < hi && a.refs[p] > 0 ? 1 : 0;
         }
@@ -271,22 +301,22 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_compact_plan_kernel(const Kv
     }
     // holes: .y of moves; movers: .x
     auto walk = [&](int& holes, int& movers, bool write) {
-        for (int p0 = lo; p0 < hi; p0 += kRun * kPlanThreads) {
-            const int p = p0 + kRun * (int)threadIdx.x;
-            int r[kRun], mine = 0;
+        for (int p0 = lo; p0 < hi; p0 += RUN * kPlanThreads) {
+            const int p = p0 + RUN * (int)threadIdx.x;
+            int r[RUN], mine = 0;
 #pragma unroll
-            for (int e = 0; e < kRun; ++e) r[e] = p + e < hi ? a.refs[p + e] : 0;
+            for (int e = 0; e < RUN; ++e) r[e] = p + e < hi ? a.refs[p + e] : 0;
 #pragma unroll
-            for (int e = 0; e < kRun; ++e)
+            for (int e = 0; e < RUN; ++e)
                 if (p + e < hi) mine += p + e < U ? (r[e] <= 0 ? 1 : 0) : (r[e] > 0 ? 1 << 16 : 0);
             int total;
             const int at = block_scan(mine, total);
             int h = holes + (at & 0xFFFF), m = movers + (at >> 16);
 #pragma unroll
-            for (int e = 0; e < kRun; ++e) {
+            for (int e = 0; e < RUN; ++e) {
                 if (!write || p + e >= hi) continue;
-                if (p + e < U && r[e] <= 0) s.moves[h++].y = p + e;
-                if (p + e >= U && r[e] > 0) s.moves[m++].x = p + e;
+                if (p + e < U && r[e] <= 0) moves_at[h++].y = p + e;
+                if (p + e >= U && r[e] > 0) moves_at[m++].x = p + e;
                 s.list[p + e] = p + e;
                 s.refs[p + e] = p + e < U ? max(r[e], 0) : 0;
             }
@@ -294,7 +324,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_compact_plan_kernel(const Kv
             movers += total >> 16;
         }
     };
-    static_assert(kRun * kPlanThreads < 1 << 15, "two counts in one word");
+    static_assert(RUN * kPlanThreads < 1 << 15, "two counts in one word");
     int holes = 0, movers = 0;
     if (CS > 1) {
         walk(holes, movers, false);
@@ -313,7 +343,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_compact_plan_kernel(const Kv
         team.sums(s.head + 4 + kTeam, below, moves);
     }
     for (int i = team.tid; i < moves; i += team.kThreads) {
-        const int2 mv = s.moves[i];
+        const int2 mv = moves_at[i];
+        if (CS == 1) s.moves[i] = mv;
         s.list[mv.x] = mv.y;
         s.refs[mv.y] = a.refs[mv.x];
     }
@@ -415,21 +446,33 @@ size_t kv8_pages_scratch_bytes(int rows, int max_pages, int n_pages) {
 }
 
 cudaError_t launch_kv8_update(const Kv8PagesArgs& a, cudaStream_t st) {
-    if ((long long)a.rows * a.max_pages + a.n_pages >= kTeamFrom) {
+    const size_t bytes = one_cta_bytes(a.rows, a.n_pages);
+    if ((long long)a.rows * a.max_pages + a.n_pages >= kTeamFrom || bytes > kOneCtaMost) {
         const cudaError_t e = launch_team(kv8_update_plan_kernel<kTeam>, a, st);
         if (e != cudaSuccess) return e;
     } else {
-        HRA_LAUNCH(kv8_update_plan_kernel<1>, dim3(1), dim3(kPlanThreads), 0, st, a);
+        static bool configured[64] = {false};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= 64 || !configured[dev]) {
+            e = cudaFuncSetAttribute(kv8_update_plan_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kOneCtaMost);
+            if (e != cudaSuccess) return e;
+            if (dev >= 0 && dev < 64) configured[dev] = true;
+        }
+        HRA_LAUNCH(kv8_update_plan_kernel<1>, dim3(1), dim3(kPlanThreads), bytes, st, a);
     }
     return launch_copy<false>(a, a.rows, st);
 }
 
 cudaError_t launch_kv8_compact(const Kv8PagesArgs& a, cudaStream_t st) {
     if (a.n_pages >= kTeamPages) {
-        const cudaError_t e = launch_team(kv8_compact_plan_kernel<kTeam>, a, st);
+        const cudaError_t e = launch_team(kv8_compact_plan_kernel<kTeam, kRun>, a, st);
         if (e != cudaSuccess) return e;
+    } else if (a.n_pages > 2 * kPlanThreads) {
+        HRA_LAUNCH((kv8_compact_plan_kernel<1, kRun>), dim3(1), dim3(kPlanThreads), 0, st, a);
     } else {
-        HRA_LAUNCH(kv8_compact_plan_kernel<1>, dim3(1), dim3(kPlanThreads), 0, st, a);
+        HRA_LAUNCH((kv8_compact_plan_kernel<1, 1>), dim3(1), dim3(kPlanThreads), 0, st, a);
     }
     return launch_copy<true>(a, a.n_pages / 2 + 1, st);
 }
