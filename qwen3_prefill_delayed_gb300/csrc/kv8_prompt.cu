@@ -24,9 +24,9 @@
 //              when M moves, and the output;
 //   warps 6-9  V: codes from global memory in registers, two tiles ahead, to f16 in shared memory (keys that
 //              do not count as zeros, so stale slots never reach a product); and the items' Q.
-// What bounds it: the chain S -> softmax -> PV of a tile, about 3000 clocks with two CTAs at work, in which the tensor
-// pipe is 34-42% busy and 54% of the issue slots are taken (3250 warp instructions a tile: a third the weights, a
-// sixth each the maxima and V).
+// What bounds it: the chain S -> softmax -> PV of a tile, about 2800 clocks with two CTAs at work, in which the tensor
+// pipe is 35% busy and 53% of the issue slots are taken (a third by the weights, a sixth by V).  Two groups of softmax
+// warps that take the tiles in turn (448 threads at 72 registers) do not shorten it: 410 us against 353.
 // The items come from a list built on the device (kv8_schedule_kernel).  Many items: most key tiles first, and CTA c
 // takes entries in snake order.  Few long ones (prompt chunks after many cached positions): the tiles of all items
 // form a line of which every CTA takes an equal share; parts of an item go to scratch as fp32 sums with their
@@ -151,17 +151,47 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+// the maxima of columns 0 .. 15 and 16 .. 31 of each lane's row (the columns themselves are dropped)
+__device__ __forceinline__ void tmem_max32(uint32_t taddr, float& top0, float& top1) {
+    float v[16], w[16];
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, %32, [%34];\n\t"
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 "
+        "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %33, [%35];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+          "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
+          "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]), "=f"(w[4]), "=f"(w[5]),
+          "=f"(w[6]), "=f"(w[7]), "=f"(w[8]), "=f"(w[9]), "=f"(w[10]), "=f"(w[11]),
+          "=f"(w[12]), "=f"(w[13]), "=f"(w[14]), "=f"(w[15]),
+          "=f"(top0), "=f"(top1)
+        : "r"(taddr), "r"(taddr + 16));
+}
 __device__ __forceinline__ int snake(int k) {
     return k * (int)gridDim.x + ((k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
 }
 
-// One row's tile of S, 32 columns at a time in a rolled loop: unrolled, the softmax warps wait for
-// instructions (a tile of straight code took 4600 clocks instead of 2400).  MASK: only keys below
-// `limit` of blocks that are there (scale >= 0) count.
-// mx: the maximum of s; Mx: the maximum of s + log2 of the block's V scale.
-template <bool MASK>
-__device__ __forceinline__ void max_pass(uint32_t lS, const float* ks, float q_unscale, int limit, float& mx,
-                                         float& Mx) {
+// One row's tile of S, 32 columns at a time: unrolled as straight code, the weights and masks make the softmax warps wait
+// for instructions (a tile of it took 4600 clocks instead of 2400).  Where not every key of the tile counts, the keys below
+// `limit` of blocks that are there (scale >= 0) do.
+// mx: the maximum of s; Mx: the maximum of s + log2 of the block's V scale.  The loads themselves take the maximum of a
+// block's 16 scores (chunks after many positions: 353 us by max instructions, 339 so; holding the scores for the weights
+// meanwhile spills, 494).
+__device__ __forceinline__ void max_pass_whole(uint32_t lS, const float* ks, float q_unscale, float& mx, float& Mx) {
+#pragma unroll
+    for (int ch = 0; ch < TK / 32; ++ch) {
+        float top0, top1;
+        const float2 k2 = *reinterpret_cast<const float2*>(ks + 2 * ch), e2 = *reinterpret_cast<const float2*>(ks + NB + 2 * ch);
+        tmem_max32(lS + 32 * ch, top0, top1);
+        const float z0 = top0 * (q_unscale * k2.x), z1 = top1 * (q_unscale * k2.y);
+        mx = max3(mx, z0, z1);
+        Mx = max3(Mx, z0 + e2.x, z1 + e2.y);
+    }
+}
+__device__ __forceinline__ void max_pass_masked(uint32_t lS, const float* ks, float q_unscale, int limit, float& mx,
+                                                float& Mx) {
 #pragma unroll 1
     for (int ch = 0; ch < TK / 32; ++ch) {
         float a[32];
@@ -170,17 +200,15 @@ __device__ __forceinline__ void max_pass(uint32_t lS, const float* ks, float q_u
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const float k = h ? k2.y : k2.x, ev = h ? e2.y : e2.x;
-            if (MASK) {
-                const int n = k >= 0.f ? limit - 32 * ch - 16 * h : 0;
+            const int n = k >= 0.f ? limit - 32 * ch - 16 * h : 0;
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (e >= n) a[16 * h + e] = -INFINITY;
-            }
+            for (int e = 0; e < 16; ++e)
+                if (e >= n) a[16 * h + e] = -INFINITY;
             float top[2] = {fmaxf(a[16 * h], a[16 * h + 1]), fmaxf(a[16 * h + 2], a[16 * h + 3])};
 #pragma unroll
             for (int e = 4; e < 16; e += 2) top[(e >> 1) & 1] = max3(top[(e >> 1) & 1], a[16 * h + e], a[16 * h + e + 1]);
             const float bm = fmaxf(top[0], top[1]);
-            const float z = MASK && bm == -INFINITY ? bm : bm * (q_unscale * k);
+            const float z = bm == -INFINITY ? bm : bm * (q_unscale * k);
             mx = fmaxf(mx, z);
             Mx = fmaxf(Mx, z + ev);
         }
@@ -583,9 +611,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const bool whole = j0 + TK <= clear && there[g % NSC] != 0;   // every key counts for every row
                 float mx = -INFINITY, Mx = -INFINITY;
                 if (whole)
-                    max_pass<false>(lS, ks, q_unscale, 0, mx, Mx);
+                    max_pass_whole(lS, ks, q_unscale, mx, Mx);
                 else
-                    max_pass<true>(lS, ks, q_unscale, limit - j0, mx, Mx);
+                    max_pass_masked(lS, ks, q_unscale, limit - j0, mx, Mx);
                 const float mn = fmaxf(m, mx);
                 const float mr = mn == -INFINITY ? 0.f : mn;
                 l *= ex2(m - mr);
