@@ -13,10 +13,11 @@
 // before the first use, reduces the maximum, and writes the block's codes as 2 KB (head_dim 128) of
 // contiguous memory.  No two warps share a block, so there are no atomics.
 //
-// Bound by memory: prompts of 11,400 rows x 8 heads x 128 (70 MB read and written) take 16.5 us, 4.2 TB/s,
-// and one frame of 8 rows 2.4 us in a captured graph, a launch's latency.  One warp for a block's K and V
-// together took the same 16.5 us and 3.5 for the frame (its two chains of loads, maximum and stores follow
-// one another); fewer registers for more warps per SM took 20 to 36 us (the loads are then no longer all in flight).
+// Bound by memory: prompts of 11,400 rows x 8 heads x 128 (70 MB read and written) take 13.3 us, 5.2 TB/s,
+// and one frame of 8 rows 2.4 us in a captured graph, a launch's latency.  The maximum is taken on the bf16 bits
+// and the rows are requested before the page is looked up: in fp32, after it, 100 registers hold 20 warps an SM
+// instead of 32 (16.5 us; 7 CTAs of 4 warps 13.5, 6 13.9).  One warp for a block's K and V together took
+// 16.5 us and 3.5 for the frame (its two chains of loads, maximum and stores follow one another).
 #include <cuda_fp8.h>
 
 #include "internal.h"
@@ -36,7 +37,7 @@ __device__ __forceinline__ uint2 to_e4m3x8(const float (&f)[8], float inv) {
 }
 
 template <int HD>
-__global__ void __launch_bounds__(128) kv8_append_kernel(const Kv8AppendArgs a) {
+__global__ void __launch_bounds__(128, 8) kv8_append_kernel(const Kv8AppendArgs a) {
     pdl_launch();
     pdl_wait();
     constexpr int LPR = HD / 8;                 // lanes that hold one row
@@ -50,9 +51,9 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(const Kv8AppendArgs a) 
     const int which = (unit / c.n_kv) & 1;
     const int blk = unit / (2 * c.n_kv);
     int row0, n;
+    const int first = a.start[b];
     kv8_rows(a.cu, b, a.total_rows, row0, n);
     if (n == 0) return;
-    const int first = a.start[b];
     if (unit == 0 && lane == 0) {
         const long long room = (long long)c.max_pages << c.page_shift;
         if (first < 0 || first + (long long)n > room) raise_error(c.err, HRA_DEVERR_POS_RANGE);
@@ -65,11 +66,6 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(const Kv8AppendArgs a) 
     const int pos0 = (first / kKv8Block + blk) * kKv8Block;   // the block's first position
     if (pos0 < 0 || pos0 - first >= n) return;
     const int page = kv8_page_of(c, b, pos0);
-    if (page < 0) {
-        if (lane == 0 && (pos0 >> c.page_shift) < c.max_pages) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
-        return;
-    }
-    const int slot0 = pos0 & (c.page_size - 1);
     const int lo = max(0, first - pos0);                 // new rows are slots [lo, hi) of the block
     const int hi = min(kKv8Block, first - pos0 + n);
     const bf16* src = (which ? a.v : a.k) + (long long)head * HD;
@@ -83,20 +79,34 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(const Kv8AppendArgs a) 
         if (i >= lo && i < hi)
             raw[p] = *reinterpret_cast<const uint4*>(src + (long long)(row0 + (pos0 + i - first)) * a.row_stride + e8);
     }
+    if (page < 0) {   // (the rows are on their way, whether or not they have one)
+        if (lane == 0 && (pos0 >> c.page_shift) < c.max_pages) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
+        return;
+    }
+    const int slot0 = pos0 & (c.page_size - 1);
     float* scale = c.scales + kv8_scale_at(c, page, which, head, slot0);
     uint8_t* dst = c.codes + kv8_code_at(c, page, which, head, slot0);
     const float before = lo > 0 ? *scale : 0.f;
-    float m = 0.f;
+    // bf16 bits without their sign order like the values; a NaN is ignored, and stays one as a code
+    uint32_t top = 0u;
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-        float f[8];
-        unpack8(raw[p], f);
+    for (int p = 0; p < PASSES; ++p)
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[p].x & 0x7FFF7FFFu, raw[p].y & 0x7FFF7FFFu),
+                                     __vmaxu2(raw[p].z & 0x7FFF7FFFu, raw[p].w & 0x7FFF7FFFu)));
+    top = max(top & 0xFFFFu, top >> 16);
+    if (__any_sync(0xffffffffu, top > 0x7F80u)) {
+        float m = 0.f;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(f[q]));   // a NaN is ignored, and stays one as a code
+        for (int p = 0; p < PASSES; ++p) {
+            float f[8];
+            unpack8(raw[p], f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(f[q]));
+        }
+        top = __float_as_uint(m) >> 16;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    m = fminf(m, __uint_as_float(0x7F7F0000u));   // infinities count as the largest bf16 and saturate
+    top = min(__reduce_max_sync(0xffffffffu, top), 0x7F7Fu);   // infinities count as the largest bf16 and saturate
+    const float m = __uint_as_float(top << 16);
     const float s = fmaxf(before, __uint_as_float(kv8_scale_bits(__float_as_uint(m))));
     const float inv = 1.0f / s;
     if (lo > 0 && s > before) {   // the block's earlier codes follow its scale
