@@ -16,10 +16,13 @@ namespace {
 
 inline bool aligned(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// [a, a + n) and [b, b + n) share a byte without being the same range
-inline bool straddle(const void* a, const void* b, size_t n) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x != y && x < y + n && y < x + n;
+struct Range {
+    const void* at;
+    size_t n;
+};
+inline bool overlap(const Range& a, const Range& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return x < y + b.n && y < x + a.n;
 }
 
 }  // namespace
@@ -86,10 +89,16 @@ int pages_impl(const hra_kv8_cache* cache, const int32_t* parents, const int32_t
         return HRA_ERR_INVALID_ARG;
     if ((parents != nullptr && !aligned(parents, 4)) || (room != nullptr && !aligned(room, 4)))
         return HRA_ERR_INVALID_ARG;
-    if (straddle(table_out, c.page_table, 4 * (size_t)c.rows * c.max_pages) ||
-        straddle(lens_out, c.lens, 4 * (size_t)c.rows) || straddle(refs_out, c.refs, 4 * (size_t)c.n_pages))
-        return HRA_ERR_INVALID_ARG;
-    if (workspace_bytes < hra_kv8_pages_workspace_size(cache)) return HRA_ERR_WORKSPACE;
+    const size_t need = hra_kv8_pages_workspace_size(cache);
+    if (workspace_bytes < need) return HRA_ERR_WORKSPACE;
+    // an output is its own input, or apart from every input and from the other outputs
+    const size_t n_table = 4 * (size_t)c.rows * c.max_pages, n_rows = 4 * (size_t)c.rows, n_refs = 4 * (size_t)c.n_pages;
+    const Range in[3] = {{c.page_table, n_table}, {c.lens, n_rows}, {c.refs, n_refs}};
+    const Range out[4] = {{table_out, n_table}, {lens_out, n_rows}, {refs_out, n_refs}, {workspace, need}};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 3; ++j)
+            if ((i != j && overlap(out[i], out[j])) || (overlap(out[i], in[j]) && (i != j || out[i].at != in[j].at)))
+                return HRA_ERR_INVALID_ARG;
     const Kv8View v = kv8_view(c, 0);
     Kv8PagesArgs a{};
     a.codes = v.codes;

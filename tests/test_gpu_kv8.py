@@ -692,3 +692,73 @@ def test_large_update_without_enough_pages_changes_nothing(hra):
 @pytest.mark.parametrize("pages,used", [(40000, 9000), (40001, 33000), (33000, 0), (33000, 33000)])
 def test_compact_of_a_large_pool(hra, pages, used):
     test_compact(hra, pages, used)
+
+
+@pytest.mark.parametrize("new,kept", [([1, 1, 1], [900, 3, 60]), ([2, 45, 9], [300, 80, 0]), ([100, 40], [2500, 10])])
+def test_rows_and_outputs_at_16_bytes(hra, new, kept):
+    """Rows 16 bytes off a 32-byte border, q strides that are odd multiples of 16 bytes, an output that starts at 16."""
+    H, G, D = 2, 4, 128
+    kv_len = [a + b for a, b in zip(new, kept)]
+    c = build(kv_len, H=H, D=D, P=16, seed=21)
+    kv = gpu(hra, c)
+    T, cu = sum(new), cu_of(new)
+    flat = torch.randn(8 + T * (H * G * D + 8), generator=torch.Generator().manual_seed(22)).to(BF16)
+    q = torch.as_strided(flat, (T, H * G, D), (H * G * D + 8, D, 1), 8)
+    qg = torch.as_strided(flat.cuda(), (T, H * G, D), (H * G * D + 8, D, 1), 8)
+    buf = torch.full((16 + T * H * G * D,), 7.0, dtype=BF16, device="cuda")
+    out = buf[8:8 + T * H * G * D].view(T, H * G, D)
+    kv.attend(0, qg, i32(cu).cuda(), i32(kv_len).cuda(), max(new), max(kv_len), out=out)
+    want, bound = R.attend(c, 0, q, cu, kv_len)
+    assert bool(((out.double().cpu() - want).abs() <= bound).all())
+    assert bool((buf[:8] == 7.0).all()) and bool((buf[-8:] == 7.0).all()) and kv.device_error() == 0
+
+
+def test_calls_at_once_with_workspaces_of_their_own(hra):
+    c = build([3000, 500, 40], H=2, D=128, P=16, seed=23)
+    kv = gpu(hra, c)
+    g = torch.Generator().manual_seed(24)
+    one = torch.randn(3, 8, 128, generator=g).to(BF16).cuda()
+    many = torch.randn(160, 8, 128, generator=g).to(BF16).cuda()
+    calls = [(one, i32([0, 1, 2, 3]).cuda(), 1), (many, i32([0, 90, 150, 160]).cuda(), 90)]
+    n = i32([3000, 500, 40]).cuda()
+    want = [kv.attend(0, q, cu, n, m, 3000).clone() for q, cu, m in calls]
+    ws = [torch.empty(kv.attention_workspace_size(3, q.shape[0], 8, m, 3000), dtype=torch.uint8, device="cuda") for q, _, m in calls]
+    out = [torch.empty_like(q) for q, _, _ in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (q, cu, m), w, o, s in zip(calls, ws, out, streams):
+            kv.attend(0, q, cu, n, m, 3000, out=o, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want)) and kv.device_error() == 0
+
+
+@pytest.mark.parametrize("rows,W", [(6, 5), (1500, 24)])
+def test_update_and_compact_captured_and_replayed(hra, rows, W):
+    """One captured step of forks, reservations and a compaction, replayed with other parents and rooms each time."""
+    P = 16
+    rng = random.Random(rows)
+    c = random_rows(rows, W, P, rows * W, 31)
+    kv = gpu(hra, c)
+    parents, room = torch.zeros(rows, dtype=torch.int32, device="cuda"), torch.zeros(rows, dtype=torch.int32, device="cuda")
+    kv.update(torch.arange(rows, dtype=torch.int32, device="cuda"), out=kv.empty_pages())     # the workspace
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        kv.update(parents, room)
+        kv.compact()
+    for _ in range(4):
+        p = [rng.choice([b, rng.randrange(rows), -1]) for b in range(rows)]
+        lens = c["lens"].tolist()
+        m = [min(rng.choice([0, 1, P]), W * P - lens[x]) if x >= 0 else 0 for x in p]
+        parents.copy_(i32(p))
+        room.copy_(i32(m))
+        graph.replay()
+        for f, args in ((R.update, (p, m)), (R.compact, ())):
+            want = f(c, *args)
+            codes, scales = R.move(c, want[3])
+            c.update(table=want[0], lens=want[1], refs=want[2], codes=codes, scales=scales)
+        same(kv, c)
+        assert torch.equal(kv.refs.cpu(), c["refs"])
+    assert kv.device_error() == 0

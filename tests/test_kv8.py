@@ -278,3 +278,15 @@ def test_attention_workspace_never_falls_when_a_call_grows(hra):
             j = values.index(args[i]) + 1
             more = args[:i] + (values[j],) + args[i + 1:] if j < len(values) else args
             assert more not in sizes or sizes[more] >= n, (args, more)
+
+
+def test_page_outputs_that_overlap_are_refused(hra):
+    L = hra.lib()
+    c = _cache(hra, rows=4, max_pages=4, n_pages=4, page_table=0x10000, lens=0x11000, refs=0x12000)
+    need = L.hra_kv8_pages_workspace_size(ctypes.byref(c))
+    ok = dict(table=0x20000, lens=0x30000, refs=0x40000, ws=0x50000)
+    for f in (lambda **k: L.hra_kv8_update(ctypes.byref(c), FAKE, FAKE, k["table"], k["lens"], k["refs"], k["ws"], need, None),
+              lambda **k: L.hra_kv8_compact(ctypes.byref(c), k["table"], k["lens"], k["refs"], k["ws"], need, None)):
+        for bad in (dict(refs=0x30000), dict(lens=0x20000 + 60), dict(lens=0x10000), dict(refs=0x11000), dict(table=0x12000),
+                    dict(ws=0x20000), dict(ws=0x11000), dict(ws=0x40000 - 16), dict(table=0x10004)):
+            assert f(**{**ok, **bad}) == -1, bad
