@@ -25,8 +25,10 @@
 //   warps 6-9  V: codes from global memory in registers, two tiles ahead, to f16 in shared memory (keys that
 //              do not count as zeros, so stale slots never reach a product); and the items' Q.
 // What bounds it: the chain S -> softmax -> PV of a tile, about 2800 clocks with two CTAs at work, in which the tensor
-// pipe is 35% busy and 53% of the issue slots are taken (a third by the weights, a sixth by V).  Two groups of softmax
-// warps that take the tiles in turn (448 threads at 72 registers) do not shorten it: 410 us against 353.
+// pipe is 35% busy and 53% of the issue slots are taken.  No part carries it alone (chunks after many positions, 338 us,
+// with work left out: the exponentials and packing 0, half of S's MMAs 8%, V's conversion 9%, all but one of PV's MMAs
+// 4%, the maxima 2%): the MMAs and the shared memory of two CTAs queue behind one another.  Two groups of softmax warps
+// that take the tiles in turn (448 threads at 72 registers) took 410 us against 353, a third V buffer 349 against 338.
 // The items come from a list built on the device (kv8_schedule_kernel).  Many items: most key tiles first, and CTA c
 // takes entries in snake order.  Few long ones (prompt chunks after many cached positions): the tiles of all items
 // form a line of which every CTA takes an equal share; parts of an item go to scratch as fp32 sums with their
