@@ -71,7 +71,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, *ARCH, *FLAGS, *extra_flags, "-c", s, "-o", o])
 
-    binding_tmp = BINDING + f".tmp{os.getpid()}"
+    binding_tmp = os.path.join(BUILD, f"{os.path.basename(BINDING)}.tmp{os.getpid()}")
     binding = force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "hra.h")])
     if binding:
         jobs.append(_binding_command(binding_tmp))
