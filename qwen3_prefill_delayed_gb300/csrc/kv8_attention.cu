@@ -31,8 +31,8 @@
 //   k(2 j) = 2 j, k(2 j + 1) = (2 j ^ 4) + 1: with the copies' 128-byte swizzle no read has a bank conflict.
 // Each warp has its own ring of stages that TMA fills, one box of 16 rows for K and one for V a block, so a
 // block costs one lane two instructions to request.  64 sequences of up to 8192 keys, 8 kv heads of 128, 4 q heads
-// each (559 MB): 112 us, 5.0 TB/s; with the pieces copied by cp.async, an address a lane each, 140 us; one block at a
-// time 117-124 us.  What is left is the warps' own work: 43% of issue slots, 12 warps an SM.
+// each (559 MB): 108 us, 5.2 TB/s; with the pieces copied by cp.async, an address a lane each, 140 us; one block at a
+// time 117-124 us (both against 112 then).  What is left is the warps' own work: 43% of issue slots, 12 warps an SM.
 #include <math.h>
 
 #include <algorithm>
@@ -48,7 +48,6 @@ constexpr int kPair = 2;        // blocks a warp works on at once: two chains of
 constexpr int kStages = 2;      // pairs of a warp in shared memory: 12 warps an SM; with 3, 8 warps fit (121 us against 112)
 constexpr int kUnit = kWarps * kPair * kKv8Block;   // keys of a unit: a pair of blocks a warp
 constexpr int kMaxBatch = 1024;             // sequences whose units fit the CTA's table
-constexpr int kMinShare = 2;    // units of a share at least: below it the join costs more than it spreads
 constexpr int kWholeUnits = 4;  // items of at most so many units go whole, one a CTA, and need no second kernel
 constexpr int kShortRows = 16;  // (position, head) rows of a kv head that fit this kernel's tile
 constexpr int kSerialKeys = 2048;   // keys that a short sequence may walk alone among prompts
@@ -171,7 +170,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
         if (threadIdx.x == kWarps * 32 - 1) before[a.batch] = run;
         __syncthreads();
         const long long all = (long long)before[a.batch] * c.n_kv;
-        share = max((long long)kMinShare, (all + gridDim.x - 1) / gridDim.x);
+        share = (all + gridDim.x - 1) / gridDim.x;
         u = blockIdx.x * share;
         u_end = min(all, u + share);
         if (threadIdx.x == 0) s.desc[blockIdx.x].row0 = -1;
@@ -277,6 +276,22 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
                 }
             }
         };
+        // q rows, on their way beside the page numbers
+        uint4 q_raw[NG][HD / 64][2];
+#pragma unroll
+        for (int x = 0; x < NG; ++x) {
+            const int r = g + 8 * x, qi = r / G, hq = r - qi * G;
+            const bool ok = qi < q_n;
+            const bf16* src = a.q + (long long)(row0 + (ok ? qi : 0)) * a.row_stride + (long long)(head * G + hq) * HD;
+#pragma unroll
+            for (int h = 0; h < HD / 64; ++h) {
+                q_raw[x][h][0] = q_raw[x][h][1] = make_uint4(0u, 0u, 0u, 0u);
+                if (ok) {
+                    q_raw[x][h][0] = *reinterpret_cast<const uint4*>(src + h * 64 + t4 * 16);
+                    q_raw[x][h][1] = *reinterpret_cast<const uint4*>(src + h * 64 + t4 * 16 + 8);
+                }
+            }
+        }
         int ahead = blk;
         Pages page0 = pages_of(ahead), page1 = pages_of(ahead + STEP);
 #pragma unroll
@@ -298,17 +313,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
             const int r = g + 8 * x, qi = r / G, hq = r - qi * G;
             const bool ok = qi < q_n;
             limit[x] = ok ? min(keys, kv_len - n + qi + 1) : 0;
-            const bf16* src = a.q + (long long)(row0 + (ok ? qi : 0)) * a.row_stride + (long long)(head * G + hq) * HD;
-            uint4 raw[HD / 64][2];
+            const uint4(&raw)[HD / 64][2] = q_raw[x];
             uint32_t top = 0u;     // bf16 bits without their sign order like the values
-#pragma unroll
-            for (int h = 0; h < HD / 64; ++h) {
-                raw[h][0] = raw[h][1] = make_uint4(0u, 0u, 0u, 0u);
-                if (ok) {
-                    raw[h][0] = *reinterpret_cast<const uint4*>(src + h * 64 + t4 * 16);
-                    raw[h][1] = *reinterpret_cast<const uint4*>(src + h * 64 + t4 * 16 + 8);
-                }
-            }
 #pragma unroll
             for (int h = 0; h < HD / 64; ++h)
 #pragma unroll
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
 
 // One CTA per share: the item that begins in it and goes on behind it.  The rows' maxima and sums over all parts
 // come first (a warp a row, a lane a part), then every thread adds its columns, parts in order, with the loads free of
-// each other.
+// each other and the first ones under way before (8 rows after 1024-2112 positions: 14.6 us without that, 13.2 with).
 template <int HD, int NG>
 __global__ void __launch_bounds__(256) kv8_join_kernel(const SplitArgs s) {
     pdl_launch();
@@ -601,6 +607,20 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const SplitArgs s) {
     const int rows = d.n * s.G, parts = d.last - c0 + 1;
     // part i: the end of share c0, then the beginnings of the shares behind it
     auto slot = [&](int i) { return s.parts + (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * Slot<HD, NG>::FLOATS; };
+    // this thread's first columns of the first parts, on their way while the rows' maxima are found
+    constexpr int AHEAD = 8;
+    float2 ahead[AHEAD];
+    float ahead_M[AHEAD];
+    const int r0 = min((int)threadIdx.x / (HD / 2), ROWS - 1), d0 = ((int)threadIdx.x % (HD / 2)) * 2;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+        ahead[k] = make_float2(0.f, 0.f);
+        ahead_M[k] = 0.f;
+        if (k < parts && r0 < rows) {
+            ahead[k] = *reinterpret_cast<const float2*>(slot(k) + r0 * HD + d0);
+            ahead_M[k] = slot(k)[ROWS * HD + r0 * 3 + 2];
+        }
+    }
     for (int r = threadIdx.x >> 5; r < rows; r += 8) {
         const int lane = threadIdx.x & 31;
         float m = -INFINITY, M = -INFINITY, l = 0.f;
@@ -635,8 +655,19 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const SplitArgs s) {
         const int qi = r / s.G, hq = r - qi * s.G;
         const float Mr = s_M[r], L = s_l[r];
         float x0 = 0.f, x1 = 0.f;
+        const bool held = i < 256;
+        if (held) {
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                if (k < parts) {
+                    const float f = ex2(ahead_M[k] - Mr);
+                    x0 += ahead[k].x * f;
+                    x1 += ahead[k].y * f;
+                }
+            }
+        }
 #pragma unroll 8
-        for (int k = 0; k < parts; ++k) {
+        for (int k = held ? AHEAD : 0; k < parts; ++k) {
             const float* p = slot(k);
             const float2 ov = *reinterpret_cast<const float2*>(p + r * HD + dd);
             const float f = ex2(p[ROWS * HD + r * 3 + 2] - Mr);
