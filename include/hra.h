@@ -457,6 +457,8 @@ typedef struct hra_kv8_cache {
  *   cu_dev       int32 [batch + 1]: row b of the table gets packed rows cu[b] .. cu[b + 1) (0 = cu[0]; a
  *                row may get none and is then left alone)
  *   start_dev    int32 [batch]: position of the first of them; they follow in order
+ *                (neither cu nor start may overlap cache->lens, which the call writes while they are read: HRA_ERR_INVALID_ARG;
+ *                to go on where the rows end, pass a copy of lens, the same one for every layer)
  *   max_new      most new tokens of a row (1 .. total_rows)
  * For each block of 16 positions, head, and K or V: a = max |x| over the block's new tokens, s the smallest
  * power of two >= 2^-126 with a <= 448 s; if the block held tokens before the first new one, s = max(stored

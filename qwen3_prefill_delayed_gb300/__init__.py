@@ -917,7 +917,8 @@ class Kv8Cache:
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, start: torch.Tensor, max_new: int,
                stream=None) -> None:
         """hra_kv8_append: k, v bf16 [T, n_kv_heads, head_dim] (rows may be strided), cu int32 [B + 1] and start int32
-        [B] on the device: row b's tokens cu[b] .. cu[b + 1) go to its positions from start[b] on."""
+        [B] on the device: row b's tokens cu[b] .. cu[b + 1) go to its positions from start[b] on.  start must not be
+        the cache's own lens, which the call writes: pass a copy, the same one for every layer."""
         self._call.append(self._at, self._index, layer, k, v, cu, start, max_new, stream)
 
     def attention_workspace_size(self, batch: int, total_rows: int, n_q_heads: int, max_new: int, max_len: int) -> int:

@@ -141,6 +141,10 @@ int hra_kv8_append(const hra_kv8_cache* cache, int32_t layer, const void* k_dev,
     if (!aligned(k_dev, 16) || !aligned(v_dev, 16) || row_stride < (int64_t)c.n_kv_heads * c.head_dim ||
         row_stride % 8 != 0)
         return HRA_ERR_INVALID_ARG;
+    // every CTA of a row reads start and cu, and one of them writes the row's length
+    const Range lens{c.lens, 4 * (size_t)c.rows};
+    if (overlap(lens, {start_dev, 4 * (size_t)batch}) || overlap(lens, {cu_dev, 4 * ((size_t)batch + 1)}))
+        return HRA_ERR_INVALID_ARG;
     Kv8AppendArgs a{};
     a.view = kv8_view(c, layer);
     a.k = reinterpret_cast<const bf16*>(k_dev);
