@@ -463,11 +463,13 @@ typedef struct hra_kv8_cache {
  * For each block of 16 positions, head, and K or V: a = max |x| over the block's new tokens, s the smallest
  * power of two >= 2^-126 with a <= 448 s; if the block held tokens before the first new one, s = max(stored
  * scale, s) and, where s has grown, their codes become e4m3(value * stored / s).  code = e4m3(x / s): to nearest,
- * ties to even; infinities saturate, a NaN stays one.  lens[b] = start[b] + new tokens.  Slots behind
- * the last new token keep their bytes.
- * Positions outside [0, max_pages * page_size) are not written (HRA_DEVERR_POS_RANGE), nor those whose
- * table entry is no page of the pool (HRA_DEVERR_PAGE_RANGE), nor a row's tokens beyond max_new
- * (HRA_DEVERR_POS_RANGE).  Two rows of one call must not write the same block. */
+ * ties to even; infinities saturate, a NaN stays one.  lens[b] = the position behind the row's last new token.  Slots
+ * behind that token keep their bytes.
+ * Not written are a row's tokens beyond max_new, positions from max_pages * page_size on and all tokens of a row whose
+ * start is negative (HRA_DEVERR_POS_RANGE), and positions whose table entry is no page of the pool
+ * (HRA_DEVERR_PAGE_RANGE).  lens counts the tokens up to max_new and to the end of the table; a row of which nothing is
+ * written keeps its length, or falls to max(0, start + new tokens) where that is less.
+ * Two rows of one call must not write the same block. */
 int hra_kv8_append(const hra_kv8_cache* cache, int32_t layer, const void* k_dev, const void* v_dev,
                    int64_t row_stride, const int32_t* cu_dev, const int32_t* start_dev, int32_t batch,
                    int32_t total_rows, int32_t max_new, void* stream);

@@ -54,18 +54,27 @@ __global__ void __launch_bounds__(128, 8) kv8_append_kernel(const Kv8AppendArgs 
     const int first = a.start[b];
     kv8_rows(a.cu, b, a.total_rows, row0, n);
     if (n == 0) return;
-    if (unit == 0 && lane == 0) {
-        const long long room = (long long)c.max_pages << c.page_shift;
-        if (first < 0 || first + (long long)n > room) raise_error(c.err, HRA_DEVERR_POS_RANGE);
-        if (n > a.max_new) raise_error(c.err, HRA_DEVERR_POS_RANGE);
-        if (a.lens != nullptr) a.lens[b] = (int)max(0LL, min(room, first + (long long)n));
-    }
+    const long long room = (long long)c.max_pages << c.page_shift;
+    if (unit == 0 && lane == 0 && (first < 0 || first + (long long)n > room || n > a.max_new))
+        raise_error(c.err, HRA_DEVERR_POS_RANGE);
     n = min(n, a.max_new);
+    const bool keeps_len = unit == 0 && a.lens != nullptr;   // this warp writes the row's length
     // the error bit says so; the products below stay inside 32 bits
-    if (first < 0 || first >= ((long long)c.max_pages << c.page_shift)) return;
+    if (first < 0 || first >= room) {   // nothing is written: the row holds no more than it did
+        if (keeps_len && lane == 0 && first < 0) a.lens[b] = min(a.lens[b], max(0, first + n));
+        return;
+    }
     const int pos0 = (first / kKv8Block + blk) * kKv8Block;   // the block's first position
     if (pos0 < 0 || pos0 - first >= n) return;
     const int page = kv8_page_of(c, b, pos0);
+    if (keeps_len) {   // nor does one none of whose new tokens has a page
+        const int end = (int)min(room, (long long)first + n);
+        bool any = page >= 0;
+        for (int i = (first >> c.page_shift) + 1 + lane; !any && i <= (end - 1) >> c.page_shift; i += 32)
+            any = kv8_page_of(c, b, i << c.page_shift) >= 0;
+        any = __any_sync(0xffffffffu, any);
+        if (lane == 0) a.lens[b] = any ? end : min(a.lens[b], end);
+    }
     const int lo = max(0, first - pos0);                 // new rows are slots [lo, hi) of the block
     const int hi = min(kKv8Block, first - pos0 + n);
     const bf16* src = (which ? a.v : a.k) + (long long)head * HD;

@@ -1,0 +1,88 @@
+"""The paged 8-bit cache on the GPU at the edges of its contract, beyond tests/test_gpu_kv8.py: lengths after appends that are
+cut short, rows without pages, not-a-numbers behind the causal mask, scales of zero, other streams."""
+import pytest
+import torch
+
+import kv8_ref as R
+from test_gpu_kv8 import BF16, build, check, cu_of, gpu, hra, i32, same  # noqa: F401  (hra: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def give_pages(c, width):
+    """Every row of the CPU cache a page for each of its first `width` table entries."""
+    free = [p for p in range(c["refs"].numel()) if not c["refs"][p]]
+    for b in range(c["table"].shape[0]):
+        for i in range(width):
+            if c["table"][b, i] < 0:
+                c["table"][b, i] = free.pop()
+                c["refs"][c["table"][b, i]] = 1
+
+
+# ----------------------------------------------------------------------------- what an append leaves as the length
+
+@pytest.mark.parametrize("new,start,max_new", [([20, 3, 7], [5, 30, 16], 6), ([1, 40], [15, 0], 17), ([2, 2], [31, 7], 1)])
+def test_tokens_beyond_max_new_are_not_counted(hra, new, start, max_new):  # noqa: F811
+    H, D, P = 2, 64, 16
+    c = build(start, H=H, D=D, P=P, width=4, spare=12, seed=1)
+    give_pages(c, 4)
+    T, cu = sum(new), cu_of(new)
+    x = torch.randn(T, 2 * H, D, generator=torch.Generator().manual_seed(2)).to(BF16)
+    kv, xg = gpu(hra, c), x.cuda()
+    kv.append(0, xg[:, :H], xg[:, H:], i32(cu).cuda(), i32(start).cuda(), max_new)
+    short = [min(n, max_new) for n in new]
+    y = torch.cat([x[cu[b]:cu[b] + n] for b, n in enumerate(short)])
+    R.append(c, 0, y[:, :H], y[:, H:], cu_of(short), start)
+    assert c["lens"].tolist() == [s + n for s, n in zip(start, short)]
+    same(kv, c)
+    assert kv.device_error() == hra.DEVERR_POS_RANGE
+
+
+@pytest.mark.parametrize("held,start,n,want", [(0, -3, 4, 0), (7, -3, 4, 1), (7, -3, 2, 0), (20, 32, 5, 20), (32, 40, 1, 32),
+                                               (5, -2147483648, 3, 0), (9, 2147483647, 3, 9)])
+def test_a_row_that_gets_nothing_holds_no_more_than_before(hra, held, start, n, want):  # noqa: F811
+    c = build([held, 3], H=1, D=64, P=16, width=2, spare=4, seed=4)
+    give_pages(c, 2)
+    kv = gpu(hra, c)
+    x = torch.randn(n + 2, 1, 64, generator=torch.Generator().manual_seed(5)).to(BF16)
+    kv.append(0, x.cuda(), x.cuda(), i32([0, n, n + 2]).cuda(), i32([start, 3]).cuda(), n + 2)
+    R.append(c, 0, x[n:], x[n:], [0, 0, 2], [0, 3])          # the other row's tokens are written
+    c["lens"][0] = want
+    same(kv, c)
+    assert kv.device_error() == hra.DEVERR_POS_RANGE
+
+
+def test_rows_without_pages_keep_their_length(hra):  # noqa: F811
+    """No page for any new token: nothing is written or counted.  A page for some of them: the length covers all."""
+    rows, W, P = 5, 40, 16
+    c = build([0, 20, 0, 0, 17], H=1, D=64, P=P, width=W, spare=60, seed=6)
+    free = [p for p in range(c["refs"].numel()) if not c["refs"][p]]
+    c["table"][1] = -1                                      # held 20 positions, lost its pages
+    c["table"][2, 38] = free[0]                             # the last of the new tokens' pages alone
+    c["table"][3, 0] = 1 << 20                              # no page of the pool
+    new, start = [1, 3, 620, 5, 4], [0, 20, 2, 0, 17]
+    x = torch.randn(sum(new), 1, 64, generator=torch.Generator().manual_seed(7)).to(BF16)
+    kv = gpu(hra, c)
+    kv.append(0, x.cuda(), x.cuda(), i32(cu_of(new)).cuda(), i32(start).cuda(), max(new))
+    R.append(c, 0, x, x, cu_of(new), start)
+    c["lens"][:4] = i32([0, 20, 622, 0])
+    same(kv, c)
+    assert kv.device_error() == hra.DEVERR_PAGE_RANGE
+    kv.append(0, x[:1].cuda(), x[:1].cuda(), i32([0, 0, 1, 1, 1, 1]).cuda(), i32([0, 4, 0, 0, 0]).cuda(), 1)
+    c["lens"][1] = 5                                        # written nowhere, before its end
+    same(kv, c)
+
+
+def test_a_freed_row_in_the_batch_stays_empty(hra):  # noqa: F811
+    """A row that has ended and was freed takes part in no later step: its length stays 0, so an update that extends the others
+    gives it no page."""
+    c = build([20, 33, 18], H=1, D=64, P=16, width=4, spare=6, seed=8)
+    c["scales"] = torch.nan_to_num(c["scales"], nan=0.5)
+    kv = gpu(hra, c)
+    kv.update(i32([0, -1, 2]).cuda(), i32([2, 0, 2]).cuda())
+    x = torch.randn(3, 1, 64, generator=torch.Generator().manual_seed(9)).to(BF16).cuda()
+    for step in range(2):
+        kv.append(0, x, x, i32([0, 1, 2, 3]).cuda(), i32([20 + step, step, 18 + step]).cuda(), 1)
+        assert kv.lens.tolist() == [21 + step, 0, 19 + step]
+    kv.update()
+    assert kv.page_table[1].tolist() == [-1] * 4
