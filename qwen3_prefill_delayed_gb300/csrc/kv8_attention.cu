@@ -84,6 +84,7 @@ struct Ring {
 // the last CTA that has a part of it.
 struct SplitDesc {
     int row0, n, head, last;   // n: tokens; row0 < 0: no item begins in this share and goes on behind it
+    int b, pad[3];
 };
 template <int HD, int NG>
 struct Slot {
@@ -99,10 +100,21 @@ struct SplitArgs {
     int whole;         // one item a CTA: blockIdx = (head, sequence)
 };
 
-// NG x 8 rows of (position, head) pairs.
-template <int HD, int NG>
+// Dims d and d + 1 of row r, written to dst, are or hold a NaN: see kv8_row_again.
+__device__ __noinline__ void look_again(const SplitArgs& s, int b, int head, int r, int d, bf16* dst) {
+    const Kv8View& c = s.a.view;
+    int row0, n;
+    kv8_rows(s.a.cu, b, s.a.total_rows, row0, n);
+    const int qi = r / s.G, hq = r - qi * s.G;
+    const int before = min(c.max_pages << c.page_shift, max(0, s.a.kv_len[b])) - n;   // positions before the first token
+    const bf16* q = s.a.q + (long long)(row0 + qi) * s.a.row_stride + (long long)(head * s.G + hq) * c.head_dim;
+    kv8_row_again(c, q, b, head, before + qi + 1, before + n, d, 2, s.a.scale_log2, dst);
+}
+
+// NG x 8 rows of (position, head) pairs.  ONE: sequences of one new token, whose rows all see the same keys.
+template <int HD, int NG, bool ONE>
 __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_constant__ CUtensorMap codes_map,
-                                                                  const SplitArgs s) {
+                                                                  const __grid_constant__ SplitArgs s) {
     pdl_launch();
     pdl_wait();
     using R = Ring<HD>;
@@ -572,6 +584,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
                 const float f = L == 0.f ? 0.f : exp2f(Mr - mr) / L;
                 bf16* dst = a.out + ((long long)(row0 + qi) * a.nq + head * G + hq) * HD + d;
                 *reinterpret_cast<uint32_t*>(dst) = pack_bf2(x0 * 0x1p-15f * f, x1 * 0x1p-15f * f);
+                if (!ONE && (x0 != x0 || x1 != x1)) look_again(s, b, head, r, d, dst);
             } else {
                 *reinterpret_cast<float2*>(part + r * HD + d) = make_float2(x0, x1);
                 if (d == 0) {
@@ -584,7 +597,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
         }
         if (first_part && !last_part && threadIdx.x == 0) {
             const long long end = (long long)before[b] * c.n_kv + (long long)(head + 1) * (before[b + 1] - before[b]);
-            s.desc[blockIdx.x] = SplitDesc{row0, q_n, head, (int)((end - 1) / share)};
+            s.desc[blockIdx.x] = SplitDesc{row0, q_n, head, (int)((end - 1) / share), b, {0, 0, 0}};
         }
         fence_proxy_async_smem();   // the sums below the next copies
         __syncthreads();            // the results are read: the rings may be filled again
@@ -595,8 +608,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
 // One CTA per share: the item that begins in it and goes on behind it.  The rows' maxima and sums over all parts
 // come first (a warp a row, a lane a part), then every thread adds its columns, parts in order, with the loads free of
 // each other and the first ones under way before (8 rows after 1024-2112 positions: 14.6 us without that, 13.2 with).
-template <int HD, int NG>
-__global__ void __launch_bounds__(256) kv8_join_kernel(const SplitArgs s) {
+template <int HD, int NG, bool ONE>
+__global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ SplitArgs s) {
     pdl_launch();
     pdl_wait();
     constexpr int ROWS = 8 * NG;
@@ -677,12 +690,13 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const SplitArgs s) {
         const float f = L == 0.f ? 0.f : exp2f(Mr - s_m[r]) / L;
         bf16* dst = s.a.out + ((long long)(d.row0 + qi) * s.a.nq + d.head * s.G + hq) * HD + dd;
         *reinterpret_cast<uint32_t*>(dst) = pack_bf2(x0 * 0x1p-15f * f, x1 * 0x1p-15f * f);
+        if (!ONE && (x0 != x0 || x1 != x1)) look_again(s, d.b, d.head, r, dd, dst);
     }
 }
 
 int split_grid() { return 3 * device_sm_count(); }
 
-template <int HD, int NG>
+template <int HD, int NG, bool ONE>
 cudaError_t launch_ng(const SplitArgs& s, cudaStream_t st) {
     constexpr int join = kWarps * 8 * NG * (HD + 3) * 4;
     constexpr int smem = (Ring<HD>::BYTES > join ? Ring<HD>::BYTES : join) + 1024;   // aligned up to 1024 bytes
@@ -694,19 +708,24 @@ cudaError_t launch_ng(const SplitArgs& s, cudaStream_t st) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(kv8_attn_kernel<HD, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(kv8_attn_kernel<HD, NG, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
     if (s.whole) {
         const dim3 grid((unsigned)s.a.view.n_kv, (unsigned)s.a.batch);
-        HRA_LAUNCH((kv8_attn_kernel<HD, NG>), grid, dim3(kWarps * 32), smem, st, map, s);
+        HRA_LAUNCH((kv8_attn_kernel<HD, NG, ONE>), grid, dim3(kWarps * 32), smem, st, map, s);
         return cudaGetLastError();
     }
     const dim3 grid((unsigned)split_grid());
-    HRA_LAUNCH((kv8_attn_kernel<HD, NG>), grid, dim3(kWarps * 32), smem, st, map, s);
-    HRA_LAUNCH((kv8_join_kernel<HD, NG>), grid, dim3(256), 0, st, s);
+    HRA_LAUNCH((kv8_attn_kernel<HD, NG, ONE>), grid, dim3(kWarps * 32), smem, st, map, s);
+    HRA_LAUNCH((kv8_join_kernel<HD, NG, ONE>), grid, dim3(256), 0, st, s);
     return cudaGetLastError();
+}
+
+template <int HD, int NG>
+cudaError_t launch_tokens(const SplitArgs& s, cudaStream_t st) {
+    return s.a.max_new == 1 ? launch_ng<HD, NG, true>(s, st) : launch_ng<HD, NG, false>(s, st);
 }
 
 // One n = 8 column group while the rows of a tile fit it, else two.
@@ -749,8 +768,8 @@ cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st) {
     s.desc = reinterpret_cast<SplitDesc*>(scratch);
     s.parts = reinterpret_cast<float*>(scratch + split_grid() * sizeof(SplitDesc));
     const bool one = column_groups(G, a.max_new) == 1;
-    if (a.view.head_dim == 128) return one ? launch_ng<128, 1>(s, st) : launch_ng<128, 2>(s, st);
-    return one ? launch_ng<64, 1>(s, st) : launch_ng<64, 2>(s, st);
+    if (a.view.head_dim == 128) return one ? launch_tokens<128, 1>(s, st) : launch_tokens<128, 2>(s, st);
+    return one ? launch_tokens<64, 1>(s, st) : launch_tokens<64, 2>(s, st);
 }
 
 }  // namespace hra

@@ -62,7 +62,8 @@ __host__ __device__ __forceinline__ int key_tiles(int keys) {   // an item witho
 // Parts of split items, as for single tokens: CTA c has slots 2 c (the item that its share begins in) and 2 c + 1 (the
 // one it ends in); a slot is [TROWS][HD] sums, then m, l and M of the rows.
 struct PromptDesc {   // the item whose first part is slot 2 c + 1, and the last CTA that has a part of it
-    int row0, n, q_lo, head, last, pad[3];   // row0 < 0: none
+    int row0, n, q_lo, head, last;   // row0 < 0: none
+    int b, kv_len, keys;             // as in the pair's record
 };
 template <int HD>
 struct PromptSlot {
@@ -170,6 +171,12 @@ __device__ __forceinline__ void tmem_max32(uint32_t taddr, float& top0, float& t
           "=f"(w[12]), "=f"(w[13]), "=f"(w[14]), "=f"(w[15]),
           "=f"(top0), "=f"(top1)
         : "r"(taddr), "r"(taddr + 16));
+}
+// Dims dim .. dim + n - 1 of row `row` of an item's tile, written to out, hold a NaN: see kv8_row_again.
+__device__ __noinline__ void look_again(const PromptArgs& p, const PromptRec& r, int head, int row, int dim, int n, bf16* out) {
+    const int qi = row / p.G, hq = row - qi * p.G;
+    const bf16* q = p.q + (long long)(r.row0 + r.q_lo + qi) * p.row_stride + (long long)(head * p.G + hq) * p.view.head_dim;
+    kv8_row_again(p.view, q, r.b, head, r.kv_len - r.n + r.q_lo + qi + 1, r.keys, dim, n, p.scale_log2, out);
 }
 __device__ __forceinline__ int snake(int k) {
     return k * (int)gridDim.x + ((k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
@@ -378,8 +385,38 @@ __global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a,
     if (tid == 0) list[0] = total;
 }
 
+// The outputs of the items that this CTA did alone once more, a thread 32 dims of a row.  first: equal shares' first item, its
+// first tile, the tiles of the share.
 template <int HD>
-__global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const PromptArgs p) {
+__device__ __noinline__ void outputs_again(const PromptArgs& p, const int* first) {
+    const bool shares = p.desc != nullptr;
+    const int n_items = p.list[0] * p.view.n_kv;
+    int left = shares ? first[2] : 0;
+    for (int k = 0;; ++k) {
+        const int i = shares ? first[0] + k : snake(k);
+        if (i >= n_items || (shares && left == 0)) return;
+        const int32_t* rec = p.list + kRecWords * (1 + (long long)(i / p.view.n_kv));
+        const PromptRec r{rec[0], rec[1], rec[2], rec[3], rec[4], rec[5], 0};
+        const int head = i % p.view.n_kv;
+        if (shares) {   // not the parts: they are looked at where they are joined
+            const int from = k == 0 ? first[1] : 0, all = key_tiles(r.keys), n = min(left, all - from);
+            left -= n;
+            if (n < all) continue;
+        }
+        for (int x = threadIdx.x; x < TROWS * (HD / 32); x += kThreads) {
+            const int row = x / (HD / 32), dim = x % (HD / 32) * 32, qi = row / p.G;
+            if (qi >= p.QT || r.q_lo + qi >= r.n) continue;
+            bf16* dst = p.out + ((long long)(r.row0 + r.q_lo + qi) * p.nq + head * p.G + row - qi * p.G) * HD + dim;
+            bool nan = false;
+            for (int e = 0; e < 32; ++e) nan |= __hisnan(dst[e]);
+            if (nan) look_again(p, r, head, row, dim, 32, dst);
+        }
+    }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                                      const __grid_constant__ PromptArgs p) {
     using C = Cfg<HD>;
     pdl_launch();
     pdl_wait();
@@ -391,6 +428,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     volatile int* issued = reinterpret_cast<volatile int*>(slots + 2);
     float* sc = reinterpret_cast<float*>(smem + C::OFF_SC);
     float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
+    __shared__ int nan_out_s;    // a row of an item that this CTA did alone has a NaN
+    volatile int* nan_out = &nan_out_s;   // (looked at behind the items: a call inside them costs 6-12 %, 2 % so)
     __shared__ int first_s[3];   // equal shares: the first item, its first tile, the tiles of the share
     volatile int* there = reinterpret_cast<volatile int*>(smem + C::OFF_TH);
     auto bar = [&](int i) { return smem_u32(bars + i); };
@@ -405,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         }
         *abort_flag = 0;
         *issued = 0;
+        *nan_out = 0;
         if (p.desc != nullptr) {
             const long long all = *reinterpret_cast<const long long*>(p.list + 2);
             const long long share = (all + gridDim.x - 1) / gridDim.x, u = blockIdx.x * share;
@@ -668,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     const long long all = *reinterpret_cast<const long long*>(p.list + 2);
                     const long long share = (all + gridDim.x - 1) / gridDim.x;
                     const long long end = (blockIdx.x + 1LL) * share - n_kt + t_all;
-                    p.desc[blockIdx.x] = PromptDesc{r.row0, r.n, r.q_lo, head, (int)((end - 1) / share), {0, 0, 0}};
+                    p.desc[blockIdx.x] = PromptDesc{r.row0, r.n, r.q_lo, head, (int)((end - 1) / share), r.b, r.kv_len, r.keys};
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -685,6 +725,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 tmem_ld32(lO + ch, o);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = o[e] * 0x1p-11f * f;
+                if (ch == 32 * (quad % (HD / 32))) {   // (a NaN of V is in every row's sum of its dim)
+                    float2 t2 = make_float2(o[0], o[1]);
+#pragma unroll
+                    for (int e = 2; e < 32; e += 2) t2 = add2(t2, make_float2(o[e], o[e + 1]));
+                    if (t2.x != t2.x || t2.y != t2.y) *nan_out = 1;
+                }
                 if (row_ok) {
                     if (p.v8) {
                         st_global_32(dst + ch, pack8(o), pack8(o + 8));
@@ -872,11 +918,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         tc_fence_after();
         tmem_dealloc(tS, 256);
     }
+    if (*nan_out && !*abort_flag) outputs_again<HD>(p, first_s);
 }
 
 // The parts of the item that begins in share blockIdx.x and goes on behind it, in order; 8 rows a CTA.
 template <int HD>
-__global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const PromptArgs p) {
+__global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_constant__ PromptArgs p) {
     pdl_launch();
     pdl_wait();
     const int c0 = blockIdx.x;
@@ -912,6 +959,10 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const PromptArgs p
 #pragma unroll
     for (int e = 0; e < E; e += 2)
         *reinterpret_cast<uint32_t*>(dst + e) = pack_bf2(o[e] * 0x1p-11f * f, o[e + 1] * 0x1p-11f * f);
+    bool nan = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) nan |= o[e] != o[e];
+    if (nan) look_again(p, PromptRec{d.b, d.row0, d.n, d.q_lo, d.kv_len, d.keys, 0}, d.head, row, lane * E, E, dst);
 }
 
 int prompt_slots() { return 2 * device_sm_count(); }

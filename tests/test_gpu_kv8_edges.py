@@ -86,3 +86,46 @@ def test_a_freed_row_in_the_batch_stays_empty(hra):  # noqa: F811
         assert kv.lens.tolist() == [21 + step, 0, 19 + step]
     kv.update()
     assert kv.page_table[1].tolist() == [-1] * 4
+
+
+# ------------------------------------------------------------------------- not-a-numbers behind the causal mask
+
+@pytest.mark.parametrize("H,G,D,P", [(2, 4, 128, 16), (1, 1, 64, 32), (2, 3, 128, 64), (1, 8, 64, 16), (1, 2, 64, 128)])
+@pytest.mark.parametrize("new,kept", [([2], [0]), ([4, 3], [29, 12]), ([2, 5], [15, 600]), ([40, 21], [0, 50]), ([130], [33]),
+                                      ([70, 2], [2300, 2200]), ([4, 2], [1022, 60])])
+@pytest.mark.parametrize("what", ["V", "K"])
+def test_nan_reaches_only_the_rows_that_see_it(hra, H, G, D, P, new, kept, what):  # noqa: F811
+    """A token whose K or V has a NaN: rows before it are what they would be without it, rows from it on have the formula's NaN
+    (of V in its dimension alone)."""
+    lens = [a + b for a, b in zip(new, kept)]
+    c = build(lens, H=H, D=D, P=P, seed=sum(lens) + D)
+    which, cu, T = (1 if what == "V" else 0), cu_of(new), sum(new)
+    q = torch.randn(T, H * G, D, generator=torch.Generator().manual_seed(3)).to(BF16)
+    want, bound = R.attend(c, 0, q, cu, lens)                # without the NaNs
+    nan = torch.zeros(T, H * G, D, dtype=torch.bool)
+    for b, n in enumerate(new):
+        for i in {n // 2, n - 1}:                            # two of the new tokens, the last one among them
+            at, head, dim = kept[b] + i, i % H, (7 * i + 5) % D
+            c["codes"][0, int(c["table"][b, at // P]), which, head, at % P, dim] = 0xFF if i & 1 else 0x7F
+            nan[cu[b] + i:cu[b + 1], head * G:(head + 1) * G, dim if which else slice(None)] = True
+    kv = gpu(hra, c)
+    got = kv.attend(0, q.cuda(), i32(cu).cuda(), i32(lens).cuda(), max(new), max(lens)).double().cpu()
+    assert torch.equal(torch.isnan(got), nan)
+    assert bool(((got - want).abs() <= bound)[~nan].all())
+    assert kv.device_error() == 0
+
+
+@pytest.mark.parametrize("new,kept", [([4, 3], [600, 12]), ([200, 64], [1000, 0])])
+def test_tokens_that_are_nan_throughout(hra, new, kept):  # noqa: F811
+    """K and V of a row's last cached token and of all its new ones are NaN: every output is, soon; of the other row's, none."""
+    H, G, D, P = 2, 4, 128, 16
+    lens = [a + b for a, b in zip(new, kept)]
+    c = build(lens, H=H, D=D, P=P, seed=3)
+    for pos in range(max(0, kept[0] - 1), lens[0]):
+        c["codes"][0, int(c["table"][0, pos // P]), :, :, pos % P] = 0x7F
+    q = torch.randn(sum(new), H * G, D, generator=torch.Generator().manual_seed(4)).to(BF16)
+    kv = gpu(hra, c)
+    got = kv.attend(0, q.cuda(), i32(cu_of(new)).cuda(), i32(lens).cuda(), max(new), max(lens)).double().cpu()
+    assert bool(torch.isnan(got[:new[0]]).all())
+    want, bound = R.attend({**c, "table": c["table"][1:]}, 0, q[new[0]:], [0, new[1]], lens[1:])
+    assert bool(((got[new[0]:] - want).abs() <= bound).all())
