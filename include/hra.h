@@ -429,7 +429,8 @@ int hra_prefill_fp8(const hra_dims* dims, const hra_weights* weights, const hra_
  * that rows share: half the bytes of the bf16 cache, and several continuations of one prompt hold its
  * pages once.  An element's value is code * scale.  All pointers are device memory of the caller.
  *   codes       uint8 [n_layers][n_pages][2][n_kv_heads][page_size][head_dim] (0 = K, 1 = V)
- *   scales      fp32 [n_layers][n_pages][2][n_kv_heads][page_size / 16]; powers of two
+ *   scales      fp32 [n_layers][n_pages][2][n_kv_heads][page_size / 16]; each 0 (its block's values
+ *               are 0) or a power of two from 2^-126 on
  *   page_table  int32 [rows][max_pages]: entry i of row b is the page of its positions
  *               [i * page_size, (i + 1) * page_size); -1 = none.  The same pages in every layer.
  *   lens        int32 [rows]: positions each row holds (written by hra_kv8_append and the path)

@@ -859,7 +859,7 @@ def _kv8_calls():
 
 class Kv8Cache:
     """A paged 8-bit K/V cache (``hra_kv8_cache``): E4M3 codes uint8 [n_layers, n_pages, 2, n_kv_heads, page_size,
-    head_dim], fp32 scales [n_layers, n_pages, 2, n_kv_heads, page_size / 16], the page table int32 [rows,
+    head_dim], fp32 scales [n_layers, n_pages, 2, n_kv_heads, page_size / 16] (each 0 or a power of two), the page table int32 [rows,
     max_pages], the rows' lengths int32 [rows] and the pages' reference counts int32 [n_pages], all CUDA tensors of
     one device that the object reads and writes in place.
 

@@ -2,7 +2,7 @@
 //
 // A pool holds n_pages pages per layer; a page holds page_size consecutive tokens of one sequence
 // for every kv head: codes [2][n_kv][page_size][head_dim] (0 = K, 1 = V; E4M3) and scales
-// [2][n_kv][page_size / 16] (fp32, one for each block of 16 tokens and head).  The value of an
+// [2][n_kv][page_size / 16] (fp32, 0 or a power of two, one for each block of 16 tokens and head).  The value of an
 // element is code * scale.  Row b of the page table lists the pages of sequence b in order.
 //
 // Everything here is plain integer arithmetic and compiles as host code too, so that a test

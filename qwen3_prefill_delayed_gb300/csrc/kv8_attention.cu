@@ -53,8 +53,8 @@ constexpr int kShortRows = 16;  // (position, head) rows of a kv head that fit t
 constexpr int kSerialKeys = 2048;   // keys that a short sequence may walk alone among prompts
 constexpr float kPScale = 15.f; // log2 of the largest p
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int src_bytes) {   // 0 bytes: zero
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
             return r;
         };
         const float* head_scales = c.scales + head * (c.page_size / kKv8Block);
-        // blocks x0, x0 + 1 into stage st; one without a page gets scales of 0 and is masked below
+        // blocks x0, x0 + 1 into stage st; one without a page gets scales of -1 and is masked below
         auto request = [&](int x0, const Pages& pages, int st) {
             int boxes = 0;
 #pragma unroll
@@ -268,8 +268,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
                 const int slot0 = ((x0 + y) * kKv8Block) & (c.page_size - 1);
                 const float* sp = head_scales + (long long)max(page, 0) * page_scales + (slot0 / kKv8Block);
                 const uint32_t to = smem_u32(ring_scales + st * R::SCALES + y * 32 * 8);
-                cp_async4(to, sp, page < 0 ? 0 : 4);
-                cp_async4(to + 4, sp + v_scales, page < 0 ? 0 : 4);
+                if (page >= 0) {
+                    cp_async4(to, sp);
+                    cp_async4(to + 4, sp + v_scales);
+                } else {   // (this lane's own slot, whose last copy it has waited for)
+                    *reinterpret_cast<float2*>(ring_scales + st * R::SCALES + y * 32 * 8) = make_float2(-1.f, -1.f);
+                }
             }
             if (lane == 0) {
                 const uint32_t bar = ring_bar + 8 * st;
@@ -437,8 +441,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
 #pragma unroll
                 for (int y = 0; y < kPair; ++y) {
                     const float coef = q_unscale[x] * sc[y].x;
-                    // a scale of 0: the block is absent
-                    const int lim = sc[y].x > 0.f ? limit[x] - (blk + y) * kKv8Block : 0;
+                    // a scale of -1: the block is absent
+                    const int lim = sc[y].x >= 0.f ? limit[x] - (blk + y) * kKv8Block : 0;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         z[y][e] = (e & 1 ? key_1 : key_0) + 8 * (e >> 1) < lim ? sv[y][e >> 1][2 * x + (e & 1)] * coef : -INFINITY;
@@ -509,7 +513,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
                     }
                 }
                 // keys that do not count: whatever their slots hold (a NaN times a weight of 0 is none)
-                const int left = sc[y].x > 0.f ? keys - (blk + y) * kKv8Block : 0;
+                const int left = sc[y].x >= 0.f ? keys - (blk + y) * kKv8Block : 0;
                 if (left < kKv8Block) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)

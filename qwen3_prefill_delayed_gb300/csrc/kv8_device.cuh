@@ -33,10 +33,11 @@ __device__ __forceinline__ void e4m3x4_f16x4(uint32_t w, uint32_t& lo, uint32_t&
         : "=r"(lo), "=r"(hi)
         : "r"(w));
 }
-// a scale's floor(log2), and the scale over 2^that
+// a scale (0 or a power of two from 2^-126 on; -1 where a kernel marks an absent block) as exponent and factor: the factor is 0
+// for a scale of 0, which so gives a weight of 0, and else 1
 __device__ __forceinline__ float exponent_of(float s) { return (float)((int)((__float_as_uint(s) >> 23) & 255u) - 127); }
 __device__ __forceinline__ float mantissa_of(float s) {
-    return __uint_as_float((__float_as_uint(s) & 0x807FFFFFu) | 0x3F800000u);
+    return s == 0.f ? 0.f : __uint_as_float((__float_as_uint(s) & 0x807FFFFFu) | 0x3F800000u);
 }
 
 // A V with a NaN at a position that some rows of a tile see and others do not: the tile's product carries it, by a weight of 0,

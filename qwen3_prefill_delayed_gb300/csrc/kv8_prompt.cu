@@ -83,7 +83,7 @@ struct Cfg {
     static constexpr int OFF_K = 2 * QB;
     static constexpr int OFF_V = OFF_K + NK * KB;
     static constexpr int OFF_BAR = OFF_V + 2 * VB;
-    static constexpr int OFF_SC = OFF_BAR + 320;             // [NSC][3][NB]: K scale, V scale's exponent and mantissa
+    static constexpr int OFF_SC = OFF_BAR + 320;             // [NSC][3][NB]: K scale, V scale's exponent and factor
     static constexpr int OFF_QS = OFF_SC + NSC * 3 * NB * 4; // [NQS][TROWS] q scales
     static constexpr int OFF_TH = OFF_QS + NQS * TROWS * 4;  // [NSC] whether a tile's blocks are all there
     static constexpr int SMEM = OFF_TH + NSC * 4;
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t lS = lS0 + (g & 1) * TK;
-                const float* ks = sc + (g % NSC) * 3 * NB;   // then the V exponents and mantissas
+                const float* ks = sc + (g % NSC) * 3 * NB;   // then the V exponents and factors
                 const int j0 = (t_first + t) * TK;
                 const bool whole = j0 + TK <= clear && there[g % NSC] != 0;   // every key counts for every row
                 float mx = -INFINITY, Mx = -INFINITY;

@@ -129,3 +129,25 @@ def test_tokens_that_are_nan_throughout(hra, new, kept):  # noqa: F811
     assert bool(torch.isnan(got[:new[0]]).all())
     want, bound = R.attend({**c, "table": c["table"][1:]}, 0, q[new[0]:], [0, new[1]], lens[1:])
     assert bool(((got[new[0]:] - want).abs() <= bound).all())
+
+
+# --------------------------------------------------------------------------------------------- scales of zero
+
+@pytest.mark.parametrize("G,D", [(4, 128), (2, 64)])
+@pytest.mark.parametrize("new", [[1, 1], [3, 2], [60, 30]])
+@pytest.mark.parametrize("which", ["K", "V", "both", "all V"])
+def test_a_scale_of_zero_makes_values_of_zero(hra, G, D, new, which):  # noqa: F811
+    """As Kv8Cache.new fills them: such a block's keys have a score of 0 and count, its values are 0, however it is read."""
+    lens = [200, 77]
+    c = build(lens, H=2, D=D, P=32, seed=11)
+    for b, blocks in ((0, (0, 4, 12)), (1, (1, 4))):
+        for blk in blocks:
+            s = c["scales"][0, int(c["table"][b, blk // 2]), :, :, blk % 2]
+            if which in ("K", "both"):
+                s[0] = 0
+            if which in ("V", "both"):
+                s[1] = 0
+    if which == "all V":
+        c["scales"][0, :, 1] = torch.where(torch.isnan(c["scales"][0, :, 1]), c["scales"][0, :, 1], torch.zeros(()))
+    got = check(hra, c, new, lens, G)
+    assert which != "all V" or bool((got == 0).all())
