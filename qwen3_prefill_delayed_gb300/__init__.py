@@ -13,6 +13,7 @@ weight tables and workspaces.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import List, Optional, Sequence
@@ -253,6 +254,16 @@ def new_kv_cache(d, batch: int, n_slots: int, device="cuda", fill=None) -> torch
     return torch.full(shape, fill, dtype=torch.bfloat16, device=device)
 
 
+def _memory_of(stream, device):
+    """The context in which a call on `stream` (None: the current one) allocates what it writes: memory that the allocator gave
+    to another stream may still be in use there."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    return torch.cuda.stream(stream)
+
+
 class _Workspace:
     def __init__(self):
         self.buf: Optional[torch.Tensor] = None
@@ -271,11 +282,12 @@ class _KeptWorkspace(_Workspace):
         super().__init__()
         self.outgrown = []
 
-    def get(self, nbytes: int, device) -> torch.Tensor:
+    def get(self, nbytes: int, device, stream=None) -> torch.Tensor:
         if self.buf is not None and self.buf.numel() < nbytes:
             self.outgrown.append(self.buf)
             nbytes = max(nbytes, 2 * self.buf.numel())
-        return super().get(nbytes, device)
+        with _memory_of(stream, device):
+            return super().get(nbytes, device)
 
 
 _LAYER_KEYS = ("attn_norm", "w_qkv", "q_norm", "k_norm", "w_o", "mlp_norm", "w_gate_up", "w_down")
@@ -863,9 +875,10 @@ class Kv8Cache:
     max_pages], the rows' lengths int32 [rows] and the pages' reference counts int32 [n_pages], all CUDA tensors of
     one device that the object reads and writes in place.
 
-    Calls run on the current stream of the cache's device (or `stream`); the workspaces belong to the object, so
-    calls of one object on several streams, and replays of graphs that captured them, must be ordered by the caller
-    (or given a workspace each)."""
+    Calls run on the current stream of the cache's device (or `stream`, which must outlive what the call makes); the
+    workspaces belong to the object, so calls of one object on several streams, and replays of graphs that captured them,
+    must be ordered by the caller (or given a workspace each).  Outputs and workspaces that a call allocates are the memory of
+    the stream it runs on; tensors that the caller passes are the caller's to keep until that stream is done with them."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
                  refs: Optional[torch.Tensor] = None):
@@ -936,18 +949,19 @@ class Kv8Cache:
                               self._attn_ws.buf if own else workspace, own, stream)
         if type(r) is int:
             r = self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out,
-                                  self._attn_ws.get(r, self.device), own, stream)
+                                  self._attn_ws.get(r, self.device, stream), own, stream)
         return r
 
     def _pages(self, update, parents, room, out, workspace, stream):
         if self.refs is None:
             raise HraError("this needs the cache's refs")
         out = (self.page_table, self.lens, self.refs) if out is None else tuple(out)
-        if workspace is None:
+        own = workspace is None
+        if own:
             workspace = self._pages_ws.buf   # one size for the object's life
             if workspace is None:
-                workspace = self._pages_ws.get(lib().hra_kv8_pages_workspace_size(self.ref), self.device)
-        self._call.pages(self._at, self._index, update, parents, room, *out, workspace, stream)
+                workspace = self._pages_ws.get(lib().hra_kv8_pages_workspace_size(self.ref), self.device, stream)
+        self._call.pages(self._at, self._index, update, parents, room, *out, workspace, own, stream)
         return out
 
     def update(self, parents: Optional[torch.Tensor] = None, room: Optional[torch.Tensor] = None, out=None,

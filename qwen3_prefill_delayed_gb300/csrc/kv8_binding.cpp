@@ -6,6 +6,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <Python.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -61,14 +62,19 @@ int integer(PyObject* o) {
     if (v != static_cast<int>(v)) refuse("an integer argument is out of range");
     return static_cast<int>(v);
 }
-void* stream_of(PyObject* o, int index) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(index).stream();
+// The stream of a call: the device's current one (None), or any object's cuda_stream.
+c10::cuda::CUDAStream stream_of(PyObject* o, int index) {
+    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index));
     PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
     if (h == nullptr) throw std::nullopt;
     void* p = PyLong_AsVoidPtr(h);
     Py_DECREF(h);
     if (PyErr_Occurred()) throw std::nullopt;
-    return p;
+    return c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), static_cast<c10::DeviceIndex>(index));
+}
+// The allocator must not hand out t's memory before `st` is done with it, whichever stream it was allocated for.
+void used_on(const at::Tensor& t, c10::cuda::CUDAStream st) {
+    c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), st);
 }
 void check(int rc, const char* what) {
     if (rc != HRA_OK) refuse(std::string(what) + " failed: " + f_status(rc) + " (" + std::to_string(rc) + ")");
@@ -120,7 +126,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int32_t* pcu = ints(cu, batch + 1, 1, index, "cu");
         const int32_t* ps = ints(start, batch, 1, index, "start");
         if (batch > INT32_MAX || k.size(0) > INT32_MAX) refuse("too many rows");
-        void* st = stream_of(a[8], index);
+        void* st = stream_of(a[8], index).stream();
         const int layer = integer(a[2]), most = integer(a[7]);
         check(on(index, [&] {
                   return f_append(c, layer, k.data_ptr(), v.data_ptr(), stride, pcu, ps, static_cast<int32_t>(batch),
@@ -147,6 +153,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const double scale = PyFloat_AsDouble(a[8]);
         if (PyErr_Occurred()) throw std::nullopt;
         const bool own = a[11] == Py_True;
+        const c10::cuda::CUDAStream st = stream_of(a[12], index);
         void* ws = nullptr;
         size_t bytes = 0;
         if (a[10] != Py_None) {
@@ -155,6 +162,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (!w.is_contiguous()) refuse("workspace must be contiguous");
             ws = w.data_ptr();
             bytes = w.nbytes();
+            if (own) used_on(w, st);
         }
         size_t need = 0;
         if (own) {
@@ -168,18 +176,22 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         at::Tensor out;
         if (a[9] == Py_None) {
             const Unlocked unlocked;
-            out = at::empty(q.sizes(), q.options());
+            const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index));
+            const bool other = st.stream() != now.stream();
+            c10::cuda::OptionalCUDAStreamGuard guard;
+            if (other) guard.reset_stream(st);
+            out = at::empty(q.sizes(), q.options());   // memory of the stream that writes it ...
+            if (other) used_on(out, now);              // ... kept for the caller's, too
         } else {
             out = tensor(a[9], "out");
             on_device(out, index, "out");
             if (out.scalar_type() != at::kBFloat16 || !out.sizes().equals(q.sizes()) || !out.is_contiguous())
                 refuse("out must be contiguous bf16 [T, n_q_heads, head_dim] on the device of the cache");
         }
-        void* st = stream_of(a[12], index);
         check(on(index, [&] {
                   return f_attend(c, layer, q.data_ptr(), stride, static_cast<int32_t>(heads), static_cast<float>(scale), pcu, pl,
                                   static_cast<int32_t>(batch), static_cast<int32_t>(rows), max_new, max_len, out.data_ptr(),
-                                  ws, bytes, st);
+                                  ws, bytes, st.stream());
               }), "hra_kv8_attention");
         if (a[9] != Py_None) {
             Py_INCREF(a[9]);
@@ -189,9 +201,9 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// pages(cache, device, update, parents or None, room or None, table, lens, refs, workspace, stream)
+// pages(cache, device, update, parents or None, room or None, table, lens, refs, workspace, own, stream)
 PyObject* pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!counted(n, 10)) return nullptr;
+    if (!counted(n, 11)) return nullptr;
     return guarded([&]() -> PyObject* {
         const hra_kv8_cache* c = cache(a[0]);
         const int index = integer(a[1]);
@@ -206,10 +218,11 @@ PyObject* pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor& w = tensor(a[8], "workspace");
         on_device(w, index, "workspace");
         if (!w.is_contiguous()) refuse("workspace must be contiguous");
-        void* st = stream_of(a[9], index);
+        const c10::cuda::CUDAStream st = stream_of(a[10], index);
+        if (a[9] == Py_True) used_on(w, st);
         check(on(index, [&] {
-                  return update ? f_update(c, parents, room, table, lens, refs, w.data_ptr(), w.nbytes(), st)
-                                : f_compact(c, table, lens, refs, w.data_ptr(), w.nbytes(), st);
+                  return update ? f_update(c, parents, room, table, lens, refs, w.data_ptr(), w.nbytes(), st.stream())
+                                : f_compact(c, table, lens, refs, w.data_ptr(), w.nbytes(), st.stream());
               }), update ? "hra_kv8_update" : "hra_kv8_compact");
         Py_RETURN_NONE;
     });

@@ -151,3 +151,66 @@ def test_a_scale_of_zero_makes_values_of_zero(hra, G, D, new, which):  # noqa: F
         c["scales"][0, :, 1] = torch.where(torch.isnan(c["scales"][0, :, 1]), c["scales"][0, :, 1], torch.zeros(()))
     got = check(hra, c, new, lens, G)
     assert which != "all V" or bool((got == 0).all())
+
+
+# ------------------------------------------------------------------- memory of calls on another stream than the current one
+
+def freed_in_use(nbytes):
+    """Address of a block that the current stream still writes after it went back to the allocator."""
+    x = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    torch.cuda._sleep(20_000_000)
+    x.fill_(1)
+    return x.data_ptr()
+
+
+@pytest.mark.parametrize("new", [1, 70])
+def test_outputs_and_workspaces_are_memory_of_the_stream_they_are_written_on(hra, new):  # noqa: F811
+    H, G, D = 2, 4, 128
+    lens = [2500, 900]
+    c = build(lens, H=H, D=D, P=16, seed=12)
+    q = torch.randn(2 * new, H * G, D, generator=torch.Generator().manual_seed(3)).to(BF16).cuda()
+    cu, n = i32([0, new, 2 * new]).cuda(), i32(lens).cuda()
+    want = gpu(hra, c).attend(0, q, cu, n, new, 2500).clone()
+    kv, side = gpu(hra, c), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    size = kv.attention_workspace_size(2, 2 * new, H * G, new, 2500)
+    busy = [freed_in_use(size), freed_in_use(q.nbytes)]      # what the current stream's pool would hand out
+    out = kv.attend(0, q, cu, n, new, 2500, stream=side)
+    assert kv._attn_ws.buf.data_ptr() not in busy and out.data_ptr() not in busy
+    assert not torch.cuda.current_stream().query()           # the current stream was still at work
+    side.synchronize()
+    assert torch.equal(out, want)
+    # dropped while the side stream still writes it
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    out = kv.attend(0, q, cu, n, new, 2500, stream=side)
+    at = out.data_ptr()
+    del out
+    assert torch.empty_like(q).data_ptr() != at and not side.query()
+    # a workspace that another stream than its own uses goes back only when that one is done
+    at = kv._attn_ws.buf.data_ptr()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    kv.attend(0, q, cu, n, new, 2500)                        # on the current stream
+    kv._attn_ws.buf = None
+    with torch.cuda.stream(side):
+        assert torch.empty(size, dtype=torch.uint8, device="cuda").data_ptr() != at
+    assert not torch.cuda.current_stream().query()
+
+
+def test_page_workspaces_are_memory_of_the_stream_they_are_used_on(hra):  # noqa: F811
+    c = build([20, 17], L=1, H=1, D=64, P=16, rows=300, width=8, spare=30, seed=3, stale=0x22)
+    c["scales"] = torch.nan_to_num(c["scales"], nan=0.5)
+    kv, side = gpu(hra, c), torch.cuda.Stream()
+    room = i32([30] * 2 + [0] * 298).cuda()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    import ctypes
+    busy = freed_in_use(hra.lib().hra_kv8_pages_workspace_size(ctypes.byref(kv.struct)))
+    kv.update(None, room, stream=side)
+    assert kv._pages_ws.buf.data_ptr() != busy and not torch.cuda.current_stream().query()
+    side.synchronize()
+    want = R.update(c, None, room.tolist())
+    assert torch.equal(kv.page_table.cpu(), want[0]) and torch.equal(kv.refs.cpu(), want[2])
