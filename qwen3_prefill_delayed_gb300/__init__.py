@@ -264,13 +264,24 @@ def _memory_of(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _hidden_for(B: int, H: int, device, stream) -> torch.Tensor:
+    """An output bf16 [B, H] of a call on `stream`, kept for the caller's stream too."""
+    with _memory_of(stream, device):
+        out = torch.empty(B, H, dtype=torch.bfloat16, device=device)
+    if stream is not None:
+        out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 class _Workspace:
     def __init__(self):
         self.buf: Optional[torch.Tensor] = None
 
-    def get(self, nbytes: int, device) -> torch.Tensor:
-        if self.buf is None or self.buf.numel() < nbytes or self.buf.device != torch.device(device):
-            self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    def get(self, nbytes: int, device, stream=None) -> torch.Tensor:
+        with _memory_of(stream, device):
+            if self.buf is None or self.buf.numel() < nbytes or self.buf.device != torch.device(device):
+                self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+            self.buf.record_stream(torch.cuda.current_stream(self.buf.device))   # (nothing to do on its own stream)
         return self.buf
 
 
@@ -286,8 +297,7 @@ class _KeptWorkspace(_Workspace):
         if self.buf is not None and self.buf.numel() < nbytes:
             self.outgrown.append(self.buf)
             nbytes = max(nbytes, 2 * self.buf.numel())
-        with _memory_of(stream, device):
-            return super().get(nbytes, device)
+        return super().get(nbytes, device, stream)
 
 
 _LAYER_KEYS = ("attn_norm", "w_qkv", "q_norm", "k_norm", "w_o", "mlp_norm", "w_gate_up", "w_down")
@@ -337,13 +347,13 @@ class Backbone:
         B, P = tokens.shape
         lens = (ctypes.c_int32 * B)(*[int(x) for x in seq_lens])
         if out is None:
-            out = torch.empty(B, self.d.hidden, dtype=torch.bfloat16, device=tokens.device)
+            out = _hidden_for(B, self.d.hidden, tokens.device, stream)
         flags = PREFILL_FULL_LAST_LAYER if full_last_layer else 0
         if isinstance(cache, Kv8Cache):
             starts = None if start_pos is None else (ctypes.c_int32 * B)(*[int(x) for x in start_pos])
             max_end = max(int(n) + (0 if start_pos is None else int(start_pos[b])) for b, n in enumerate(seq_lens))
             need = lib().hra_prefill_kv8_workspace_size(ctypes.byref(self.dims), cache.ref, B, int(sum(seq_lens)), P, max_end)
-            ws = workspace if workspace is not None else self.ws.get(need, tokens.device)
+            ws = workspace if workspace is not None else self.ws.get(need, tokens.device, stream)
             rc = lib().hra_prefill_kv8(ctypes.byref(self.dims), ctypes.byref(self.table),
                                        _ptr(tokens, torch.int32, "tokens"), lens, starts, B, P, cache.ref,
                                        _ptr(out, torch.bfloat16, "last_hidden"), _ptr(ws, None, "workspace"), ws.numel(),
@@ -358,7 +368,7 @@ class Backbone:
             starts = (ctypes.c_int32 * B)(*[int(x) for x in start_pos])
             max_end = max(int(a) + int(n) for a, n in zip(start_pos, seq_lens))
             need = self.prefill_chunk_workspace_size(B, int(sum(seq_lens)), P, max(max_end, P))
-        ws = workspace if workspace is not None else self.ws.get(need, tokens.device)
+        ws = workspace if workspace is not None else self.ws.get(need, tokens.device, stream)
         if start_pos is None:
             rc = lib().hra_prefill(ctypes.byref(self.dims), ctypes.byref(self.table),
                                    _ptr(tokens, torch.int32, "tokens"), lens, B, P, ctypes.byref(kv),
@@ -381,9 +391,9 @@ class Backbone:
         `advance`); pos_bound is a host upper bound of every position.  With a Kv8Cache, hra_decode_dev_kv8."""
         B = in_emb.shape[0]
         if out is None:
-            out = torch.empty(B, self.d.hidden, dtype=torch.bfloat16, device=in_emb.device)
+            out = _hidden_for(B, self.d.hidden, in_emb.device, stream)
         need = self._decode_need(B, cache)
-        ws = workspace if workspace is not None else self.ws.get(need, in_emb.device)
+        ws = workspace if workspace is not None else self.ws.get(need, in_emb.device, stream)
         if isinstance(cache, Kv8Cache):
             rc = lib().hra_decode_dev_kv8(ctypes.byref(self.dims), ctypes.byref(self.table),
                                           _ptr(in_emb, torch.bfloat16, "in_emb"), _ptr(pos, torch.int32, "pos"),
@@ -418,9 +428,9 @@ class Backbone:
         B = in_emb.shape[0]
         p = (ctypes.c_int32 * B)(*[int(x) for x in pos])
         if out is None:
-            out = torch.empty(B, self.d.hidden, dtype=torch.bfloat16, device=in_emb.device)
+            out = _hidden_for(B, self.d.hidden, in_emb.device, stream)
         need = self._decode_need(B, cache)
-        ws = workspace if workspace is not None else self.ws.get(need, in_emb.device)
+        ws = workspace if workspace is not None else self.ws.get(need, in_emb.device, stream)
         if isinstance(cache, Kv8Cache):
             rc = lib().hra_decode_kv8(ctypes.byref(self.dims), ctypes.byref(self.table),
                                       _ptr(in_emb, torch.bfloat16, "in_emb"), p, B, cache.ref,

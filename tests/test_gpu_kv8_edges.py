@@ -214,3 +214,47 @@ def test_page_workspaces_are_memory_of_the_stream_they_are_used_on(hra):  # noqa
     side.synchronize()
     want = R.update(c, None, room.tolist())
     assert torch.equal(kv.page_table.cpu(), want[0]) and torch.equal(kv.refs.cpu(), want[2])
+
+
+@pytest.fixture(scope="module")
+def model(hra):  # noqa: F811
+    import workloads as W
+    d = W.tiny_dims()
+    w = W.make_backbone(d, 21)
+    return d, {"embed": w["embed"].cuda(), "final_norm": w["final_norm"].cuda(),
+               "layers": [{k: v.cuda() for k, v in l.items()} for l in w["layers"]]}
+
+
+@pytest.mark.parametrize("paged", [True, False])
+def test_the_backbones_outputs_and_workspace_are_memory_of_the_call_s_stream(hra, model, paged):  # noqa: F811
+    d, w = model
+    toks = torch.randint(0, d.vocab, (2, 40), generator=torch.Generator().manual_seed(1), dtype=torch.int32).cuda()
+    lens, results = [40, 23], []
+    for other in (False, True):
+        bb = hra.Backbone(d, w)
+        if paged:
+            cache = hra.Kv8Cache.new(d, 2, 64)
+            cache.update(room=i32([64, 64]).cuda())
+            need = hra.lib().hra_prefill_kv8_workspace_size(__import__("ctypes").byref(bb.dims), cache.ref, 2, 63, 40, 40)
+        else:
+            cache = hra.new_kv_cache(d, 2, 64, fill=0.0)
+            need = bb.prefill_workspace_size(2, 63, 40)
+        side = torch.cuda.Stream() if other else None
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        busy = [freed_in_use(need), freed_in_use(4 * d.hidden)] if other else []
+        a = bb.prefill(toks, lens, cache, stream=side)
+        assert bb.ws.buf.data_ptr() not in busy and a.data_ptr() not in busy
+        b = bb.decode(a, lens, cache, stream=side)
+        pos = i32([n + 1 for n in lens]).cuda() if side is None else torch.tensor([n + 1 for n in lens], dtype=torch.int32).pin_memory()
+        if other:
+            with torch.cuda.stream(side):
+                pos = pos.cuda(non_blocking=True)
+        c = bb.decode_dev(b, pos, 63, cache, stream=side)
+        assert a.data_ptr() != b.data_ptr() != c.data_ptr()
+        if other:
+            assert not torch.cuda.current_stream().query()   # all of it while the current stream was at work
+            side.synchronize()
+        results.append((a.clone(), b.clone(), c.clone()))
+        torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(*results))
