@@ -276,11 +276,16 @@ def _hidden_for(B: int, H: int, device, stream) -> torch.Tensor:
 class _Workspace:
     def __init__(self):
         self.buf: Optional[torch.Tensor] = None
+        self.captured, self.in_graphs = False, []   # a captured graph uses buf; the earlier ones that graphs use
 
     def get(self, nbytes: int, device, stream=None) -> torch.Tensor:
         with _memory_of(stream, device):
             if self.buf is None or self.buf.numel() < nbytes or self.buf.device != torch.device(device):
+                if self.captured:
+                    self.in_graphs.append(self.buf)
+                    self.captured = False
                 self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+            self.captured |= torch.cuda.is_current_stream_capturing()
             self.buf.record_stream(torch.cuda.current_stream(self.buf.device))   # (nothing to do on its own stream)
         return self.buf
 

@@ -258,3 +258,31 @@ def test_the_backbones_outputs_and_workspace_are_memory_of_the_call_s_stream(hra
         results.append((a.clone(), b.clone(), c.clone()))
         torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(*results))
+
+
+@pytest.mark.parametrize("paged", [True, False])
+def test_a_captured_decode_keeps_its_workspace(hra, model, paged):  # noqa: F811
+    """A later call needs a larger workspace; a graph captured before still has the one it was captured with.  (Its token sits
+    at position 0 and attends itself alone, so what the prefill leaves in the cache does not matter.)"""
+    d, w = model
+    bb = hra.Backbone(d, w)
+    if paged:
+        cache = hra.Kv8Cache.new(d, 4, 96)
+        cache.update(room=i32([96] * 4).cuda())
+    else:
+        cache = hra.new_kv_cache(d, 4, 96, fill=0.0)
+    emb = torch.randn(1, d.hidden, generator=torch.Generator().manual_seed(2)).mul(0.05).to(BF16).cuda()
+    pos, out = i32([0]).cuda(), torch.zeros(1, d.hidden, dtype=BF16, device="cuda")
+    first = bb.decode_dev(emb, pos, 95, cache, advance=False).clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bb.decode_dev(emb, pos, 95, cache, advance=False, out=out)
+    small = bb.ws.buf.data_ptr(), bb.ws.buf.numel()
+    toks = torch.randint(0, d.vocab, (4, 90), generator=torch.Generator().manual_seed(3), dtype=torch.int32).cuda()
+    bb.prefill(toks[1:], [90, 80, 70], cache)
+    assert bb.ws.buf.data_ptr() != small[0]
+    torch.cuda.synchronize()
+    fill = [torch.full((small[1],), 3, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first) and all(bool((f == 3).all()) for f in fill)
