@@ -63,6 +63,12 @@ KV8_HD uint32_t kv8_scale_bits(uint32_t a_bits) {
     const int e = (int)(a_bits >> 23) - 8 + ((a_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
     return (uint32_t)(e < 1 ? 1 : e) << 23;
 }
+// Turns blk, blk + step, ... below blk1, at most `most`: with a ring of `most` stages of which one is requested at the start of a
+// turn, the copies under way before turn blk has taken its own.
+KV8_HD int kv8_turns_left(int blk, int blk1, int step, int most) {
+    const int left = blk < blk1 ? (blk1 - blk - 1) / step + 1 : 0;
+    return left < most ? left : most;
+}
 // Most blocks of 16 that n >= 1 consecutive positions can touch.
 KV8_HD int kv8_max_blocks(int n) { return (n + kKv8Block - 2) / kKv8Block + 1; }
 

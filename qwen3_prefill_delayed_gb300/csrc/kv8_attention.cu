@@ -389,9 +389,15 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
             ahead += STEP;
             st_in = st_in + 1 == kStages ? 0 : st_in + 1;
             cp_async_wait<kStages - 1>();
-            if (!mbar_wait(ring_bar + 8 * st, (phases >> st) & 1u, &abort_flag)) {
+            if (!__all_sync(0xffffffffu, mbar_wait(ring_bar + 8 * st, (phases >> st) & 1u, &abort_flag))) {
+                // no further request; the copies under way land, or are waited for as long, before the CTA goes
                 abort_flag = 1;
                 raise_error(c.err, HRA_DEVERR_WAIT_TIMEOUT);
+                volatile int never = 0;
+                const int under_way = kv8_turns_left(blk, blk1, STEP, kStages);
+                for (int i = 0; i < under_way; ++i, st = st + 1 == kStages ? 0 : st + 1)
+                    (void)mbar_wait(ring_bar + 8 * st, (phases >> st) & 1u, &never);
+                break;
             }
             phases ^= 1u << st;
             const uint8_t* codes = ring + st * R::CODES;
@@ -538,6 +544,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
         }
         cp_async_wait<0>();
         __syncthreads();   // the rings are empty: the warps' results go over them
+        if (abort_flag) return;   // a wait ran out: nothing is stored
 
         // ---- join the four warps: [warp][row][HD] sums and [warp][row] (m, l, M)
         float* s_o = reinterpret_cast<float*>(sm);

@@ -15,3 +15,41 @@ def test_append_refuses_start_and_cu_inside_lens(hra, kw):  # noqa: F811
     """The call writes lens while other CTAs of the row still read start and cu."""
     c = _cache(hra, lens=LENS)                       # four rows: 16 bytes; start 8 bytes, cu 12
     assert _append(hra, c, **{**dict(cu=FAKE, start=FAKE), **kw}) == -1
+
+
+RING = r"""
+#include <cstdio>
+#include "kv8.cuh"
+int main() {   // a warp's turns: stages requested and not yet taken, at the wait of every turn
+    for (int stages = 2; stages < 5; ++stages) for (int step = 1; step < 12; step += 5) for (int blk0 = 0; blk0 < 9; ++blk0)
+        for (int blk1 = 0; blk1 < 60; ++blk1) {
+            int ahead = blk0, under_way = 0;
+            auto request = [&] { if (ahead < blk1) ++under_way; ahead += step; };
+            for (int s = 0; s < stages - 1; ++s) request();
+            for (int blk = blk0; blk < blk1; blk += step) {
+                request();
+                if (under_way != hra::kv8_turns_left(blk, blk1, step, stages)) { std::printf("%d %d\n", blk, blk1); return 1; }
+                --under_way;
+            }
+            if (under_way != 0 || hra::kv8_turns_left(blk1, blk1, step, stages) != 0) return 2;
+        }
+    return 0;
+}
+"""
+
+
+def test_a_ring_knows_its_copies_under_way(tmp_path):
+    """What the single-token kernel waits for before it gives up."""
+    import os
+    import shutil
+    import subprocess
+
+    from test_kv8 import ROOT
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no g++")
+    (tmp_path / "r.cpp").write_text(RING)
+    subprocess.run([cxx, "-std=c++17", "-O1", "-I", os.path.join(ROOT, "qwen3_prefill_delayed_gb300", "csrc"),
+                    str(tmp_path / "r.cpp"), "-o", str(tmp_path / "r")], check=True)
+    r = subprocess.run([str(tmp_path / "r")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
