@@ -505,7 +505,8 @@ int hra_kv8_attention(const hra_kv8_cache* cache, int32_t layer, const void* q_d
  *   parents_dev  int32 [rows]: new row b is a copy of old row parents[b]; -1 empties it; NULL: every row stays
  *   room_dev     int32 [rows]: pages are taken for lens[b] + room[b] positions; NULL: 0
  *   table_out, lens_out, refs_out: as the cache's page_table, lens, refs.  Each may be its own input; otherwise they, the
- *                workspace and the inputs must not overlap (HRA_ERR_INVALID_ARG)
+ *                workspace and the cache's three must not overlap, nor the workspace and parents_dev or room_dev
+ *                (HRA_ERR_INVALID_ARG)
  * Pages whose page_size tokens are all filled are shared by the rows that copy them.  The pages behind (the
  * part-filled one, and reserved ones) stay with the lowest row of each parent; the others get fresh pages, and the
  * part-filled one's codes and scales are copied in every layer.  Rows take fresh pages in order, each the

@@ -99,6 +99,9 @@ int pages_impl(const hra_kv8_cache* cache, const int32_t* parents, const int32_t
         for (int j = 0; j < 3; ++j)
             if ((i != j && overlap(out[i], out[j])) || (overlap(out[i], in[j]) && (i != j || out[i].at != in[j].at)))
                 return HRA_ERR_INVALID_ARG;
+    // parents and room are read before any output is written, but while the workspace is
+    for (const int32_t* p : {parents, room})
+        if (p != nullptr && overlap(out[3], {p, n_rows})) return HRA_ERR_INVALID_ARG;
     const Kv8View v = kv8_view(c, 0);
     Kv8PagesArgs a{};
     a.codes = v.codes;

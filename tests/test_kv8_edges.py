@@ -53,3 +53,12 @@ def test_a_ring_knows_its_copies_under_way(tmp_path):
                     str(tmp_path / "r.cpp"), "-o", str(tmp_path / "r")], check=True)
     r = subprocess.run([str(tmp_path / "r")], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+def test_page_calls_refuse_parents_and_room_inside_the_workspace(hra):  # noqa: F811
+    L = hra.lib()
+    c = _cache(hra, page_table=0x10000, lens=0x11000, refs=0x12000)
+    need = L.hra_kv8_pages_workspace_size(ctypes.byref(c))
+    ws = 0x50000
+    for parents, room in ((ws, FAKE), (FAKE, ws + 4), (ws - 4, None), (None, ws + need - 4)):
+        assert L.hra_kv8_update(ctypes.byref(c), parents, room, 0x20000, 0x30000, 0x40000, ws, need, None) == -1
