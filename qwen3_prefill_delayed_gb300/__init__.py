@@ -925,6 +925,14 @@ class Kv8Cache:
         self._call = _kv8_calls()
         self._attn_ws, self._pages_ws = _KeptWorkspace(), _KeptWorkspace()
 
+    _BOUND = frozenset(("codes", "scales", "page_table", "lens", "refs", "errors"))
+
+    def __setattr__(self, name, value):
+        # the calls read and write the tensors that the object was made of
+        if name in self._BOUND and self.__dict__.get(name, value) is not value:
+            raise HraError(f"{name} belongs to the cache: copy into it, or make a Kv8Cache of the new tensors")
+        super().__setattr__(name, value)
+
     @classmethod
     def new(cls, d, rows: int, n_slots: int, n_pages: Optional[int] = None, page_size: int = 64,
             device="cuda") -> "Kv8Cache":
@@ -982,7 +990,8 @@ class Kv8Cache:
     def update(self, parents: Optional[torch.Tensor] = None, room: Optional[torch.Tensor] = None, out=None,
                workspace: Optional[torch.Tensor] = None, stream=None):
         """hra_kv8_update: rows forked, reordered or freed by parents (int32 [rows], -1 = empty) and given pages for
-        room (int32 [rows]) more tokens.  In place, or into out (see empty_pages): (page table, lens, refs)."""
+        room (int32 [rows]) more tokens.  In place, or into out (see empty_pages): (page table, lens, refs); the cache
+        itself then keeps its own, until they are copied there or become those of a new Kv8Cache."""
         return self._pages(True, parents, room, out, workspace, stream)
 
     def compact(self, out=None, workspace: Optional[torch.Tensor] = None, stream=None):

@@ -286,3 +286,20 @@ def test_a_captured_decode_keeps_its_workspace(hra, model, paged):  # noqa: F811
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, first) and all(bool((f == 3).all()) for f in fill)
+
+
+# ------------------------------------------------------------------------------------- the object and its tensors
+
+def test_the_tensors_of_a_cache_cannot_be_replaced(hra):  # noqa: F811
+    """Its calls would go on reading the ones it was made of."""
+    kv = gpu(hra, build([20], H=1, D=64, P=16))
+    for name in ("codes", "scales", "page_table", "lens", "refs", "errors"):
+        was = getattr(kv, name)
+        with pytest.raises(hra.HraError):
+            setattr(kv, name, was.clone())
+        assert getattr(kv, name) is was
+    kv.lens += 1                                             # in place: the same tensor
+    assert kv.lens.tolist() == [21]
+    bare = hra.Kv8Cache(kv.codes, kv.scales, kv.page_table, kv.lens)
+    with pytest.raises(hra.HraError):
+        bare.refs = kv.refs
