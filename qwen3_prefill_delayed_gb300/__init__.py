@@ -328,6 +328,8 @@ class Backbone:
 
     def kv(self, cache: torch.Tensor) -> HraKvCache:
         d = self.d
+        if not isinstance(cache, torch.Tensor):
+            raise HraError("this path takes the bf16 KV cache tensor only")
         if cache.dtype != torch.bfloat16 or cache.dim() != 6 or cache.shape[0] != d.n_layers \
                 or cache.shape[2] != 2 or cache.shape[3] != d.n_kv_heads or cache.shape[5] != d.head_dim:
             raise HraError("KV cache must be bf16 [n_layers, batch, 2, n_kv_heads, n_slots, head_dim]")

@@ -62,3 +62,11 @@ def test_page_calls_refuse_parents_and_room_inside_the_workspace(hra):  # noqa: 
     ws = 0x50000
     for parents, room in ((ws, FAKE), (FAKE, ws + 4), (ws - 4, None), (None, ws + need - 4)):
         assert L.hra_kv8_update(ctypes.byref(c), parents, room, 0x20000, 0x30000, 0x40000, ws, need, None) == -1
+
+
+def test_a_path_without_the_8_bit_cache_says_so(hra):  # noqa: F811
+    """FP8 and NVFP4 prefill take the bf16 tensor alone, and check their cache here."""
+    from types import SimpleNamespace
+    paged = hra.Kv8Cache.__new__(hra.Kv8Cache)
+    with pytest.raises(hra.HraError):
+        hra.Backbone.kv(SimpleNamespace(d=None), paged)
