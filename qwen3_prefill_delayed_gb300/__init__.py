@@ -488,7 +488,7 @@ class ARLoop:
         self.bws = torch.empty(bb._decode_need(B, cache), dtype=torch.uint8, device=dev)
         self.cws = torch.empty(head.workspace_size(B), dtype=torch.uint8, device=dev)
         self.paged = isinstance(cache, Kv8Cache)
-        self.kv = cache.ref if self.paged else ctypes.byref(bb.kv(cache))
+        self.kv = cache.struct if self.paged else bb.kv(cache)
         self.graph = None
 
     def frame(self, codes: Optional[torch.Tensor] = None, done: Optional[torch.Tensor] = None,
@@ -507,7 +507,7 @@ class ARLoop:
                                 ctypes.byref(self.sampling) if self.sampling is not None else None,
                                 _ptr(self.seeds, torch.int64, "seeds"),
                                 _ptr(self.hidden, torch.bfloat16, "hidden"), _ptr(self.pos, torch.int32, "pos"),
-                                self.pos_bound, self.B, self.kv,
+                                self.pos_bound, self.B, ctypes.byref(self.kv),
                                 _ptr(codes, torch.int32, "codes"), _ptr(self.next_emb, torch.bfloat16, "next_emb"),
                                 _ptr(done, torch.int32, "done"), _ptr(self.bws, None, "backbone workspace"),
                                 self.bws.numel(), _ptr(self.cws, None, "codebook workspace"), self.cws.numel(),

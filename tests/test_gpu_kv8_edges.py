@@ -303,3 +303,17 @@ def test_the_tensors_of_a_cache_cannot_be_replaced(hra):  # noqa: F811
     bare = hra.Kv8Cache(kv.codes, kv.scales, kv.page_table, kv.lens)
     with pytest.raises(hra.HraError):
         bare.refs = kv.refs
+
+
+def test_a_loop_s_cache_struct_is_the_cache_s(hra, model):  # noqa: F811
+    """ARLoop.kv: the struct that describes the cache, of either kind."""
+    import workloads as W
+    d, w = model
+    audio = W.make_audio(d, torch.Generator().manual_seed(8))
+    head, bb = hra.AudioHead(d, audio["head_w"].cuda(), audio["code_emb"].cuda()), hra.Backbone(d, w)
+    hid = torch.zeros(2, d.hidden, dtype=BF16, device="cuda")
+    flat, paged = hra.new_kv_cache(d, 2, 32, fill=0.0), hra.Kv8Cache.new(d, 2, 32)
+    loop = hra.ARLoop(bb, head, flat, hid, [3, 4], 31)
+    assert loop.kv.base == flat.data_ptr() and (loop.kv.batch, loop.kv.n_slots) == (2, 32)
+    loop = hra.ARLoop(bb, head, paged, hid, [3, 4], 31)
+    assert loop.kv.codes == paged.codes.data_ptr() and loop.kv.rows == 2
