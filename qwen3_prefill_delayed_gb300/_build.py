@@ -57,6 +57,20 @@ def _binding_command(out: str):
             "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + os.path.join(t, "lib")]
 
 
+def _binding_needs() -> str:
+    """What the binding is made with, as text."""
+    import torch
+    return "\n".join(_binding_command("") + [torch.__version__, sys.implementation.cache_tag or ""])
+
+
+def _read(path: str) -> str:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -71,26 +85,35 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, *ARCH, *FLAGS, *extra_flags, "-c", s, "-o", o])
 
+    # the binding depends on torch and Python too: it is made anew when they, or the command, are others than last time
     binding_tmp = os.path.join(BUILD, f"{os.path.basename(BINDING)}.tmp{os.getpid()}")
-    binding = force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "hra.h")])
-    if binding:
-        jobs.append(_binding_command(binding_tmp))
+    made_with = os.path.join(BUILD, os.path.basename(BINDING) + ".made_with")
+    binding, binding_error, now = None, None, ""
+    try:
+        now = _binding_needs()
+        if force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "hra.h")]) or _read(made_with) != now:
+            binding = _binding_command(binding_tmp)
+            jobs.append(binding)
+    except ImportError as e:
+        binding_error = str(e)
 
     def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        return cmd, r
+        try:
+            return cmd, subprocess.run(cmd, capture_output=True, text=True)
+        except OSError as e:
+            return cmd, subprocess.CompletedProcess(cmd, 127, "", f"{e}\n")
 
     failed = []
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
         for cmd, r in ex.map(run, jobs):
             if verbose or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-            if r.returncode != 0:
+            if r.returncode != 0 and cmd is binding:
+                binding_error = f"{cmd[0]} failed for {BINDING_SRC}"
+            elif r.returncode != 0:
                 failed.append(next(a for a in cmd if a.startswith(CSRC)))
     if failed:
         raise RuntimeError("nvcc failed for: " + ", ".join(failed))
-    if binding:
-        os.replace(binding_tmp, BINDING)
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
@@ -98,6 +121,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
         os.replace(tmp, LIB)
+    if binding_error is not None:   # the library does not need it
+        raise RuntimeError("libhra.so is built; the Python calls of the 8-bit cache are not: " + binding_error)
+    if binding is not None:
+        os.replace(binding_tmp, BINDING)
+        with open(made_with, "w") as f:
+            f.write(now)
     return LIB
 
 

@@ -70,3 +70,48 @@ def test_a_path_without_the_8_bit_cache_says_so(hra):  # noqa: F811
     paged = hra.Kv8Cache.__new__(hra.Kv8Cache)
     with pytest.raises(hra.HraError):
         hra.Backbone.kv(SimpleNamespace(d=None), paged)
+
+
+@pytest.fixture
+def small_build(tmp_path, monkeypatch):
+    """The build of one small source and a binding, in a folder of its own."""
+    from qwen3_prefill_delayed_gb300 import _build
+    try:
+        _build._nvcc()
+    except RuntimeError:
+        pytest.skip("no nvcc")
+    src = tmp_path / "binding.cpp"
+    src.write_text("extern \"C\" int answer() { return 42; }\n")
+    for name, value in (("SOURCES", ["noalloc.cu"]), ("BUILD", str(tmp_path / "build")), ("LIB", str(tmp_path / "libhra.so")),
+                        ("BINDING", str(tmp_path / "binding.so")), ("BINDING_SRC", str(src))):
+        monkeypatch.setattr(_build, name, value)
+    return _build, src, tmp_path
+
+
+@pytest.mark.parametrize("why", ["source", "compiler", "torch"])
+def test_the_library_is_built_where_the_binding_cannot_be(small_build, monkeypatch, why):
+    build, src, tmp = small_build
+    if why == "source":
+        src.write_text("#error no headers\n")
+    elif why == "compiler":
+        which = build.shutil.which
+        monkeypatch.setattr(build.shutil, "which", lambda n: str(tmp / "no-such-compiler") if n == "g++" else which(n))
+    else:
+        def missing(out):
+            raise ImportError("No module named 'torch'")
+        monkeypatch.setattr(build, "_binding_command", missing)
+    with pytest.raises(RuntimeError, match="8-bit cache"):
+        build.build()
+    assert (tmp / "libhra.so").exists() and not (tmp / "binding.so").exists()
+
+
+def test_the_binding_follows_torch(small_build, monkeypatch):
+    import torch
+    build, _, tmp = small_build
+    build.build()
+    first = (tmp / "binding.so").stat().st_mtime_ns
+    build.build()
+    assert (tmp / "binding.so").stat().st_mtime_ns == first
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    build.build()
+    assert (tmp / "binding.so").stat().st_mtime_ns != first
