@@ -532,7 +532,9 @@ int hra_kv8_compact(const hra_kv8_cache* cache, int32_t* table_out, int32_t* len
  * positions reach up to max_pages * page_size.  The rows must own pages for the positions a call writes (hra_kv8_update
  * with room): a missing one drops the token's K and V (HRA_DEVERR_PAGE_RANGE in cache->errors).  Each layer's K and V
  * are quantised from their bf16 rounding, and its attention reads them from the cache, the new tokens' included.
- * cache->lens is set to the positions each row holds.  The error word of the pass itself stays the workspace's. */
+ * cache->lens is set to the positions each row holds, as by hra_kv8_append.  The error word of the pass itself stays the
+ * workspace's.  A row that has ended: one hra_kv8_update frees it (parent -1) and moves the live rows below it, and the
+ * next calls have a smaller batch; inside the batch a row without pages sets HRA_DEVERR_PAGE_RANGE at every call. */
 size_t hra_prefill_kv8_workspace_size(const hra_dims* dims, const hra_kv8_cache* cache, int32_t batch,
                                       int32_t total_tokens, int32_t max_len, int32_t max_end);
 int hra_prefill_kv8(const hra_dims* dims, const hra_weights* weights, const int32_t* tokens_dev,

@@ -317,3 +317,75 @@ def test_a_loop_s_cache_struct_is_the_cache_s(hra, model):  # noqa: F811
     assert loop.kv.base == flat.data_ptr() and (loop.kv.batch, loop.kv.n_slots) == (2, 32)
     loop = hra.ARLoop(bb, head, paged, hid, [3, 4], 31)
     assert loop.kv.codes == paged.codes.data_ptr() and loop.kv.rows == 2
+
+
+# --------------------------------------------------------------------------------------- the path at its main shape
+
+def test_one_layer_at_full_width(hra):  # noqa: F811
+    """head_dim 128, 32 q and 8 kv heads, hidden 2560, over 512 rows: the keys and values that prefill writes are the bf16 path's,
+    quantised; its last rows, those of a chunk after over 2048 positions, and a token's are a plain layer's over that cache."""
+    import dataclasses
+
+    import workloads as W
+    from test_gpu_kv8_model import close, cpu, plain
+    d = dataclasses.replace(W.full_dims(1), vocab=2048)
+    assert (d.hidden, d.n_q_heads, d.n_kv_heads, d.head_dim) == (2560, 32, 8, 128)
+    w = W.make_backbone(d, 31)
+    bb = hra.Backbone(d, {"embed": w["embed"].cuda(), "final_norm": w["final_norm"].cuda(),
+                          "layers": [{k: v.cuda() for k, v in l.items()} for l in w["layers"]]})
+    g = torch.Generator().manual_seed(32)
+    new, start = [2300, 613], [0, 0]
+    toks = torch.randint(0, d.vocab, (2, 2300), generator=g, dtype=torch.int32)
+    kv = hra.Kv8Cache.new(d, 2, 2560)
+    kv.update(room=i32([2500, 900]).cuda())
+    want, cu = cpu(kv), cu_of(new)
+    out = bb.prefill(toks.cuda(), new, kv)
+    flat = hra.new_kv_cache(d, 2, 2560, fill=0.0)
+    bb.prefill(toks.cuda(), new, flat)
+    k, v = (torch.cat([flat[0, b, i, :, :n].transpose(0, 1).cpu() for b, n in enumerate(new)]) for i in (0, 1))
+    R.append(want, 0, k, v, cu, start)
+    same(kv, want)
+    # the last rows again, each as one token at the end of its row
+    embed = lambda t: w["embed"][t.long()].double()  # noqa: E731
+    last = torch.stack([toks[b, n - 1] for b, n in enumerate(new)])
+    close(out, plain(d, w, embed(last), cpu(kv), [1, 1], [n - 1 for n in new]))
+    # a chunk, every row through the whole layer
+    start, new = new, [130, 64]
+    toks = torch.randint(0, d.vocab, (2, 130), generator=g, dtype=torch.int32)
+    c = cpu(kv)
+    out = bb.prefill(toks.cuda(), new, kv, start_pos=start, full_last_layer=True)
+    x = torch.cat([embed(toks[b, :n]) for b, n in enumerate(new)])
+    close(out, plain(d, w, x, c, new, start)[[129, 193]])
+    # a token
+    start = [s + n for s, n in zip(start, new)]
+    emb = torch.randn(2, d.hidden, generator=g).mul(0.05).to(BF16)
+    c = cpu(kv)
+    close(bb.decode(emb.cuda(), start, kv), plain(d, w, emb.double(), c, [1, 1], start))
+    assert kv.device_error() == 0 and kv.lens.tolist() == [s + 1 for s in start]
+
+
+def test_a_row_that_has_ended_leaves_the_batch(hra, model):  # noqa: F811
+    """Freed and moved behind the live rows by one update; a smaller batch goes on as before and sets no error bit."""
+    d, w = model
+    bb = hra.Backbone(d, w)
+    g = torch.Generator().manual_seed(41)
+    toks = torch.randint(0, d.vocab, (4, 40), generator=g, dtype=torch.int32).cuda()
+    lens, outs = [37, 12, 21, 30], []
+    for ended in (False, True):
+        kv = hra.Kv8Cache.new(d, 4, 64, page_size=16)
+        kv.update(room=i32([n + 8 for n in lens]).cuda())
+        bb.prefill(toks, lens, kv)
+        rows = [0, 1, 2, 3]
+        if ended:                                            # row 1: its pages are free, rows 2 and 3 move down
+            rows = [0, 2, 3]
+            kv.update(i32(rows + [-1]).cuda(), i32([8, 8, 8, 0]).cuda())
+            assert kv.lens.tolist() == [37, 21, 30, 0] and kv.page_table[3].tolist() == [-1] * 4
+        e = torch.Generator().manual_seed(42)
+        for step in range(3):
+            emb = torch.randn(4, d.hidden, generator=e).mul(0.05).to(BF16).cuda()
+            out = bb.decode(emb[rows].contiguous(), [lens[r] + step for r in rows], kv)
+            outs.append(out if ended else out[[0, 2, 3]])
+        assert kv.device_error() == 0
+        assert kv.lens.tolist() == ([40, 24, 33, 0] if ended else [n + 3 for n in lens])
+    for a, b in zip(outs[:3], outs[3:]):
+        assert torch.equal(a, b)
