@@ -490,8 +490,8 @@ int hra_kv8_append(const hra_kv8_cache* cache, int32_t layer, const void* k_dev,
  * A kv_len outside [0, max_pages * page_size] is clamped (HRA_DEVERR_POS_RANGE); a table entry that is no page of
  * the pool hides its positions (HRA_DEVERR_PAGE_RANGE).  Slots that hold no token are never used, whatever they
  * contain, and a NaN in a token's K or V reaches the tokens that see it alone.  Scores, softmax statistics and output sums are fp32; q and the probabilities enter the products in f16
- * under powers of two, the probabilities rounded to 11 bits, q exactly but for elements below 2^-10 of its row's
- * largest, which may be off by 2^-18 of that where max_new * (n_q_heads / n_kv_heads) > 16.  The call can be captured and replayed
+ * under powers of two, the probabilities rounded to 11 bits, q exactly but for elements below 2^-9.8 of its row's
+ * largest, which may be off by 2^-17.8 of that where max_new * (n_q_heads / n_kv_heads) > 16.  The call can be captured and replayed
  * while max_new and max_len hold.  Calls that may overlap need workspaces of their own; the size never falls when an
  * argument grows, so one sized for the largest call does for all. */
 size_t hra_kv8_attention_workspace_size(const hra_kv8_cache* cache, int32_t batch, int32_t total_rows,

@@ -5,8 +5,9 @@
 // over all their keys, in tiles of 64 keys:
 //   S = Q K^T    kind::f8f6f4 on the codes as they lie in the pages.  Q enters as the sum of two E4M3
 //                matrices under a power of two s per row: hi = e4m3(q / s), lo = e4m3(q / s - hi).  A bf16 value
-//                has 8 significant bits and each E4M3 value 4, so hi + lo is q / s exactly, except that elements
-//                below 2^-10 of the row's largest are off by at most 2^-18 of it (E4M3's subnormals).  Two MMAs
+//                has 8 significant bits and each E4M3 value 4, so hi + lo is q / s exactly where lo's last bit is
+//                2^-9 or more, from q / s = 2^-2 on.  The row's largest has q / s in (224, 448]: elements below 2^-2 / 224 =
+//                2^-9.8 of it are off by at most half a subnormal step, 2^-10 / 224 = 2^-17.8 of it.  Two MMAs
 //                at twice the f16 rate cost what one f16 MMA would, and no K is converted.
 //   O += P V     kind::f16: P, the probabilities times their blocks' V scales in f16 relative to a lazy
 //                running maximum M (it moves when it is exceeded by 2^4; 2^11 is the unit, so weights stay

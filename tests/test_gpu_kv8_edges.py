@@ -389,3 +389,28 @@ def test_a_row_that_has_ended_leaves_the_batch(hra, model):  # noqa: F811
         assert kv.lens.tolist() == ([40, 24, 33, 0] if ended else [n + 3 for n in lens])
     for a, b in zip(outs[:3], outs[3:]):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------------------------------ queries of a wide range
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 9]])
+def test_queries_whose_largest_element_lies_just_below_a_power_of_two(hra, new):  # noqa: F811
+    """Mantissas of the largest element above 1.75, where q / s is least, and others down to 2^-15 of it that alone meet large
+    keys.  Two E4M3 values may lose 2^-10 / 224 = 1.143 * 2^-18 of the largest (tests/test_kv8_edges.py), so a score may be off by
+    8 / 7 of what kv8_ref.attend's split counts.  Its relative term expm1(w) of the worst score error w grows with w to at most
+    expm1(8/7 w) <= 8/7 expm1(w) exp(w / 7): 1.3 times the split's share covers it while w <= 0.9."""
+    kv_len = [300, 170]
+    c = build(kv_len, H=1, D=64, P=16, seed=13)
+    c["codes"][..., 0] &= 0x87                     # dim 0 of K and V: zero or subnormal
+    T = sum(new)
+    g = torch.Generator().manual_seed(14)
+    q = torch.randn(T, 2, 64, generator=g) * 0.1
+    mantissa = 1.7578125 + torch.arange(T * 2) % 31 * 0.0078125
+    q[..., 0] = (0.125 * mantissa * torch.exp2(torch.arange(T * 2) % 15)).view(T, 2)
+    q = q.to(BF16)
+    kv = gpu(hra, c)
+    got = kv.attend(0, q.cuda(), i32(cu_of(new)).cuda(), i32(kv_len).cuda(), max(new), 300).double().cpu()
+    want, bound = R.attend(c, 0, q, cu_of(new), kv_len)
+    if 2 * max(new) > 16:
+        bound = bound + 1.3 * (R.attend(c, 0, q, cu_of(new), kv_len, split=True)[1] - bound)
+    assert bool(((got - want).abs() <= bound).all()) and kv.device_error() == 0

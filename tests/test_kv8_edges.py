@@ -115,3 +115,24 @@ def test_the_binding_follows_torch(small_build, monkeypatch):
     monkeypatch.setattr(torch, "__version__", "0.0.1")
     build.build()
     assert (tmp / "binding.so").stat().st_mtime_ns != first
+
+
+def test_what_two_e4m3_values_keep_of_a_query():
+    """q as e4m3(q / s) + e4m3(the rest) under the largest element's scale, for every bf16 magnitude and every mantissa of the
+    largest: exact from 2^-9.8 of it on, below off by 2^-17.8 of it at most."""
+    import torch
+
+    import kv8_ref as R
+    e4m3 = lambda x: x.float().to(torch.float8_e4m3fn).double()  # noqa: E731
+    every = (torch.arange(0x7F80, dtype=torch.int32) << 16).view(torch.float32).double()
+    worst = 0.0
+    for top in [m * 2.0 ** e for m in range(128, 256) for e in (-90, -7, 60)] + [2.0 ** -126, 255 * 2.0 ** -133]:
+        s = R.scale_of(top)
+        x = every[every <= top]
+        v = (x / s).half()                                   # as the kernel forms it
+        hi = e4m3(v)
+        lo = e4m3(v - hi.half())
+        off = ((hi + lo) * s - x).abs() / top
+        assert float(off[x >= top * 2.0 ** -9.8].max()) == 0.0
+        worst = max(worst, float(off.max()))
+    assert 2.0 ** -18 < worst <= 2.0 ** -17.8
