@@ -486,7 +486,8 @@ int hra_kv8_append(const hra_kv8_cache* cache, int32_t layer, const void* k_dev,
  *                (HRA_DEVERR_POS_RANGE)
  *   max_len      host upper bound of kv_len (<= max_pages * page_size).  It chooses how the work is split;
  *                larger lengths give the same values
- *   out_dev      bf16 [total_rows][n_q_heads][head_dim]; rows behind cu[batch] are left as they are
+ *   out_dev      bf16 [total_rows][n_q_heads][head_dim], apart from q (HRA_ERR_INVALID_ARG); rows behind cu[batch] are
+ *                left as they are
  * A kv_len outside [0, max_pages * page_size] is clamped (HRA_DEVERR_POS_RANGE); a table entry that is no page of
  * the pool hides its positions (HRA_DEVERR_PAGE_RANGE).  Slots that hold no token are never used, whatever they
  * contain, and a NaN in a token's K or V reaches the tokens that see it alone.  Scores, softmax statistics and output sums are fp32; q and the probabilities enter the products in f16

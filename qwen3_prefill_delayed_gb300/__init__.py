@@ -968,7 +968,7 @@ class Kv8Cache:
                stream=None) -> torch.Tensor:
         """hra_kv8_attention: q bf16 [T, n_q_heads, head_dim] (rows may be strided) of rows' last tokens, kv_len int32
         [B] positions held -> bf16 [T, n_q_heads, head_dim].  Without a workspace, one of the object's own, which grows
-        with the calls."""
+        with the calls.  Rows that no sequence has are not written: in an output that the call makes they hold anything."""
         own = workspace is None
         r = self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out,
                               self._attn_ws.buf if own else workspace, own, stream)

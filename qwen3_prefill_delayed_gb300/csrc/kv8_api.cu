@@ -190,6 +190,10 @@ int hra_kv8_attention(const hra_kv8_cache* cache, int32_t layer, const void* q_d
     a.view = kv8_view(c, layer);
     if (workspace_bytes < 256 + kv8_attention_scratch_bytes(a.view, batch, total_rows, n_q_heads, max_new, max_len))
         return HRA_ERR_WORKSPACE;
+    // q is read again behind the output of a row with a NaN (kv8_row_again)
+    const size_t q_row = 2 * (size_t)n_q_heads * c.head_dim;
+    if (overlap({q_dev, 2 * (size_t)q_row_stride * (total_rows - 1) + q_row}, {out_dev, q_row * total_rows}))
+        return HRA_ERR_INVALID_ARG;
     a.q = reinterpret_cast<const bf16*>(q_dev);
     a.row_stride = q_row_stride;
     a.out = reinterpret_cast<bf16*>(out_dev);

@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from test_kv8 import FAKE, _append, _cache, hra  # noqa: F401  (hra: the fixture)
+from test_kv8 import FAKE, _append, _attend, _cache, hra  # noqa: F401  (hra: the fixture)
 
 LENS = 0x40000
 
@@ -136,3 +136,9 @@ def test_what_two_e4m3_values_keep_of_a_query():
         assert float(off[x >= top * 2.0 ** -9.8].max()) == 0.0
         worst = max(worst, float(off.max()))
     assert 2.0 ** -18 < worst <= 2.0 ** -17.8
+
+
+@pytest.mark.parametrize("off", [0, 512 * 2 - 16, -(3 * 256 * 2 - 16)])
+def test_attention_refuses_an_output_over_its_queries(hra, off):  # noqa: F811
+    # three rows: of q 512 elements apart and 256 long, of the output 256
+    assert _attend(hra, _cache(hra), q=0x100000, stride=512, out=0x100000 + off) == -1
