@@ -152,6 +152,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int layer = integer(a[2]), max_new = integer(a[6]), max_len = integer(a[7]);
         const double scale = PyFloat_AsDouble(a[8]);
         if (PyErr_Occurred()) throw std::nullopt;
+        if (scale != 0.0 && static_cast<float>(scale) == 0.f) refuse("scale is below float32's smallest");   // 0: the default
         const bool own = a[11] == Py_True;
         const c10::cuda::CUDAStream st = stream_of(a[12], index);
         void* ws = nullptr;

@@ -414,3 +414,12 @@ def test_queries_whose_largest_element_lies_just_below_a_power_of_two(hra, new):
     if 2 * max(new) > 16:
         bound = bound + 1.3 * (R.attend(c, 0, q, cu_of(new), kv_len, split=True)[1] - bound)
     assert bool(((got - want).abs() <= bound).all()) and kv.device_error() == 0
+
+
+def test_a_scale_that_float32_rounds_to_zero_is_not_the_default(hra):  # noqa: F811
+    kv = gpu(hra, build([20], H=2, D=64, P=16))
+    q, cu, n = torch.ones(1, 2, 64, dtype=BF16, device="cuda"), i32([0, 1]).cuda(), i32([20]).cuda()
+    for scale in (1e-46, -1e-46, 1e39, float("nan")):
+        with pytest.raises(hra.HraError):
+            kv.attend(0, q, cu, n, 1, 20, scale=scale)
+    assert torch.equal(kv.attend(0, q, cu, n, 1, 20, scale=0.125), kv.attend(0, q, cu, n, 1, 20))
