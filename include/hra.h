@@ -427,7 +427,9 @@ int hra_prefill_fp8(const hra_dims* dims, const hra_weights* weights, const hra_
 /* ---- paged 8-bit K/V cache -------------------------------------------------------------------- */
 /* K and V in OCP E4M3 with one fp32 scale for each block of 16 tokens, kv head, and K or V, in pages
  * that rows share: half the bytes of the bf16 cache, and several continuations of one prompt hold its
- * pages once.  An element's value is code * scale.  All pointers are device memory of the caller.
+ * pages once.  It pays where bytes or sharing decide: over it a decode pass takes longer than over the bf16 cache while
+ * 8 rows hold fewer than about 3500 positions each, and less time beyond.  An element's value is code * scale.  All
+ * pointers are device memory of the caller.
  *   codes       uint8 [n_layers][n_pages][2][n_kv_heads][page_size][head_dim] (0 = K, 1 = V)
  *   scales      fp32 [n_layers][n_pages][2][n_kv_heads][page_size / 16]; each 0 (its block's values
  *               are 0) or a power of two from 2^-126 on

@@ -32,7 +32,7 @@
 // Each warp has its own ring of stages that TMA fills, one box of 16 rows for K and one for V a block, so a
 // block costs one lane two instructions to request.  64 sequences of up to 8192 keys, 8 kv heads of 128, 4 q heads
 // each (559 MB): 108 us, 5.2 TB/s; with the pieces copied by cp.async, an address a lane each, 140 us; one block at a
-// time 117-124 us (both against 112 then).  What is left is the warps' own work: 43% of issue slots, 12 warps an SM.
+// time 117-124 us (both against 112 then).  What is left is the warps' own work: 48% of issue slots, 12 warps an SM.
 #include <math.h>
 
 #include <algorithm>
@@ -48,9 +48,15 @@ constexpr int kPair = 2;        // blocks a warp works on at once: two chains of
 constexpr int kStages = 2;      // pairs of a warp in shared memory: 12 warps an SM; with 3, 8 warps fit (121 us against 112)
 constexpr int kUnit = kWarps * kPair * kKv8Block;   // keys of a unit: a pair of blocks a warp
 constexpr int kMaxBatch = 1024;             // sequences whose units fit the CTA's table
-constexpr int kWholeUnits = 4;  // items of at most so many units go whole, one a CTA, and need no second kernel
+// Items of at most so many units go whole, one a CTA, and need no second kernel.  One token, 8 kv heads of 128, in a graph,
+// whole / split: 8 rows after 512 positions 8.6 / 10.2 us, after 768 11.2 / 10.3; 1 row 8.0 / 7.7 and 10.6 / 8.1; 64 rows
+// after 512 19.6 / 24.0, after 1024 33.2 / 33.2.
+constexpr int kWholeUnits = 4;
 constexpr int kShortRows = 16;  // (position, head) rows of a kv head that fit this kernel's tile
-constexpr int kSerialKeys = 2048;   // keys that a short sequence may walk alone among prompts
+// Keys that a short sequence may walk alone among prompts.  One prompt of 256 tokens beside single tokens, among the prompts /
+// in this kernel: 8 of them after 1024 positions 25 / 32 us, after 2048 40 / 39, after 4096 83 / 54; 48 of them 49 / 60, 81 / 83
+// and 277 / 126.
+constexpr int kSerialKeys = 2048;
 constexpr float kPScale = 15.f; // log2 of the largest p
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
@@ -618,7 +624,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
 
 // One CTA per share: the item that begins in it and goes on behind it.  The rows' maxima and sums over all parts
 // come first (a warp a row, a lane a part), then every thread adds its columns, parts in order, with the loads free of
-// each other and the first ones under way before (8 rows after 1024-2112 positions: 14.6 us without that, 13.2 with).
+// each other and the first ones under way before (8 rows after 1024-2112 positions, both kernels in a graph over 36 layers: 15.6 us, and 17.0
+// with one under way instead of eight).
 template <int HD, int NG, bool ONE>
 __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ SplitArgs s) {
     pdl_launch();

@@ -26,7 +26,7 @@
 //   warps 6-9  V: codes from global memory in registers, two tiles ahead, to f16 in shared memory (keys that
 //              do not count as zeros, so stale slots never reach a product); and the items' Q.
 // What bounds it: the chain S -> softmax -> PV of a tile, about 2800 clocks with two CTAs at work, in which the tensor
-// pipe is 35% busy and 53% of the issue slots are taken.  No part carries it alone (chunks after many positions, 338 us,
+// pipe is 35% busy and 53% of the issue slots are taken.  No part carries it alone (chunks after many positions, then 338 us,
 // with work left out: the exponentials and packing 0, half of S's MMAs 8%, V's conversion 9%, all but one of PV's MMAs
 // 4%, the maxima 2%): the MMAs and the shared memory of two CTAs queue behind one another.  Two groups of softmax warps
 // that take the tiles in turn (448 threads at 72 registers) took 410 us against 353, a third V buffer 349 against 338.
@@ -50,7 +50,11 @@ constexpr int TROWS = 128;
 constexpr int TK = 64;             // keys a tile
 constexpr int NB = TK / kKv8Block; // blocks a tile
 constexpr float kUnit = 11.f;      // log2 of the weight of the reference maximum
-constexpr int kSharesFrom = 2048;  // keys from which items count as long
+// Keys from which items count as long (see prompt_shares).  8 kv heads of 128, 4 q heads each, in a graph, equal shares / whole
+// items: 1 row of 128 tokens after 2000 positions 36 / 42 us, after 16000 64 / 245; 2 rows of 500 and 1021 after 8000 210 / 224,
+// after 16000 362 / 424, but after 4000 137 / 125; 4 of 512 after 8000 295 / 312; from 8 of 1024 on equal after 4000 (617 / 618),
+// shares slower below (306 / 256 after 1000).  2 of 600 are as many items as CTAs, and whole ones better at any length.
+constexpr int kSharesFrom = 2048;
 constexpr float kSlack = 4.f;      // how far a maximum may pass the reference before it moves
 
 struct PromptRec {   // 32 bytes: one (query tile, sequence) pair
