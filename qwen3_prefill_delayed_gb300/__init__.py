@@ -260,7 +260,8 @@ def _memory_of(stream, device):
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+        at = stream.cuda_stream
+        stream = torch.cuda.default_stream(device) if at <= 2 else torch.cuda.ExternalStream(at, device=device)
     return torch.cuda.stream(stream)
 
 
@@ -297,12 +298,16 @@ class _KeptWorkspace(_Workspace):
     def __init__(self):
         super().__init__()
         self.outgrown = []
+        self.home = 0   # the stream whose memory buf is
 
     def get(self, nbytes: int, device, stream=None) -> torch.Tensor:
         if self.buf is not None and self.buf.numel() < nbytes:
             self.outgrown.append(self.buf)
             nbytes = max(nbytes, 2 * self.buf.numel())
-        return super().get(nbytes, device, stream)
+        before, buf = self.buf, super().get(nbytes, device, stream)
+        if buf is not before:
+            self.home = stream.cuda_stream if stream is not None else torch.cuda.current_stream(buf.device).cuda_stream
+        return buf
 
 
 _LAYER_KEYS = ("attn_norm", "w_qkv", "q_norm", "k_norm", "w_o", "mlp_norm", "w_gate_up", "w_down")
@@ -969,24 +974,27 @@ class Kv8Cache:
         """hra_kv8_attention: q bf16 [T, n_q_heads, head_dim] (rows may be strided) of rows' last tokens, kv_len int32
         [B] positions held -> bf16 [T, n_q_heads, head_dim].  Without a workspace, one of the object's own, which grows
         with the calls.  Rows that no sequence has are not written: in an output that the call makes they hold anything."""
-        own = workspace is None
-        r = self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out,
-                              self._attn_ws.buf if own else workspace, own, stream)
+        if workspace is not None:
+            return self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out, workspace, None,
+                                     stream)
+        own = self._attn_ws
+        r = self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out, own.buf, own.home, stream)
         if type(r) is int:
-            r = self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out,
-                                  self._attn_ws.get(r, self.device, stream), own, stream)
+            ws = own.get(r, self.device, stream)
+            r = self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out, ws, own.home, stream)
         return r
 
     def _pages(self, update, parents, room, out, workspace, stream):
         if self.refs is None:
             raise HraError("this needs the cache's refs")
         out = (self.page_table, self.lens, self.refs) if out is None else tuple(out)
-        own = workspace is None
-        if own:
+        home = None
+        if workspace is None:
             workspace = self._pages_ws.buf   # one size for the object's life
             if workspace is None:
                 workspace = self._pages_ws.get(lib().hra_kv8_pages_workspace_size(self.ref), self.device, stream)
-        self._call.pages(self._at, self._index, update, parents, room, *out, workspace, own, stream)
+            home = self._pages_ws.home
+        self._call.pages(self._at, self._index, update, parents, room, *out, workspace, home, stream)
         return out
 
     def update(self, parents: Optional[torch.Tensor] = None, room: Optional[torch.Tensor] = None, out=None,

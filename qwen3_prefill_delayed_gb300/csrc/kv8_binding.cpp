@@ -62,19 +62,35 @@ int integer(PyObject* o) {
     if (v != static_cast<int>(v)) refuse("an integer argument is out of range");
     return static_cast<int>(v);
 }
-// The stream of a call: the device's current one (None), or any object's cuda_stream.
-c10::cuda::CUDAStream stream_of(PyObject* o, int index) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index));
+// The stream of a call, the device's current one (None) or any object's cuda_stream: as launches take it, and as the allocator
+// does, which does not know CUDA's special handles (1: the default stream, 2: the thread's default stream).
+struct Stream {
+    void* raw;
+    c10::cuda::CUDAStream memory;
+};
+Stream stream_of(PyObject* o, int index) {
+    const auto device = static_cast<c10::DeviceIndex>(index);
+    if (o == Py_None) {
+        const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(device);
+        return {now.stream(), now};
+    }
     PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
     if (h == nullptr) throw std::nullopt;
     void* p = PyLong_AsVoidPtr(h);
     Py_DECREF(h);
     if (PyErr_Occurred()) throw std::nullopt;
-    return c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), static_cast<c10::DeviceIndex>(index));
+    if (reinterpret_cast<uintptr_t>(p) <= 2) return {p, c10::cuda::getDefaultCUDAStream(device)};
+    return {p, c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), device)};
 }
 // The allocator must not hand out t's memory before `st` is done with it, whichever stream it was allocated for.
 void used_on(const at::Tensor& t, c10::cuda::CUDAStream st) {
     c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), st);
+}
+// Whether a call on `st` uses memory of another stream.
+bool away(PyObject* home, const Stream& st) {
+    void* h = PyLong_AsVoidPtr(home);
+    if (PyErr_Occurred()) throw std::nullopt;
+    return h != st.raw;
 }
 void check(int rc, const char* what) {
     if (rc != HRA_OK) refuse(std::string(what) + " failed: " + f_status(rc) + " (" + std::to_string(rc) + ")");
@@ -126,7 +142,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int32_t* pcu = ints(cu, batch + 1, 1, index, "cu");
         const int32_t* ps = ints(start, batch, 1, index, "start");
         if (batch > INT32_MAX || k.size(0) > INT32_MAX) refuse("too many rows");
-        void* st = stream_of(a[8], index).stream();
+        void* st = stream_of(a[8], index).raw;
         const int layer = integer(a[2]), most = integer(a[7]);
         check(on(index, [&] {
                   return f_append(c, layer, k.data_ptr(), v.data_ptr(), stride, pcu, ps, static_cast<int32_t>(batch),
@@ -136,8 +152,9 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// attend(cache, device, layer, q, cu, kv_len, max_new, max_len, scale, out or None, workspace or None, own, stream) -> out;
-// where `own` is true and the workspace is too small, the size it has to have
+// attend(cache, device, layer, q, cu, kv_len, max_new, max_len, scale, out or None, workspace or None, home, stream) -> out.
+// home: None for a workspace of the caller's; of the cache's own one the stream whose memory it is, and where that workspace is
+// too small, the answer is the size it has to have
 PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!counted(n, 13)) return nullptr;
     return guarded([&]() -> PyObject* {
@@ -153,8 +170,8 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const double scale = PyFloat_AsDouble(a[8]);
         if (PyErr_Occurred()) throw std::nullopt;
         if (scale != 0.0 && static_cast<float>(scale) == 0.f) refuse("scale is below float32's smallest");   // 0: the default
-        const bool own = a[11] == Py_True;
-        const c10::cuda::CUDAStream st = stream_of(a[12], index);
+        const bool own = a[11] != Py_None;
+        const Stream st = stream_of(a[12], index);
         void* ws = nullptr;
         size_t bytes = 0;
         if (a[10] != Py_None) {
@@ -163,7 +180,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (!w.is_contiguous()) refuse("workspace must be contiguous");
             ws = w.data_ptr();
             bytes = w.nbytes();
-            if (own) used_on(w, st);
+            if (own && away(a[11], st)) used_on(w, st.memory);
         }
         size_t need = 0;
         if (own) {
@@ -178,9 +195,9 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (a[9] == Py_None) {
             const Unlocked unlocked;
             const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index));
-            const bool other = st.stream() != now.stream();
+            const bool other = st.memory.stream() != now.stream();
             c10::cuda::OptionalCUDAStreamGuard guard;
-            if (other) guard.reset_stream(st);
+            if (other) guard.reset_stream(st.memory);
             out = at::empty(q.sizes(), q.options());   // memory of the stream that writes it ...
             if (other) used_on(out, now);              // ... kept for the caller's, too
         } else {
@@ -192,7 +209,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         check(on(index, [&] {
                   return f_attend(c, layer, q.data_ptr(), stride, static_cast<int32_t>(heads), static_cast<float>(scale), pcu, pl,
                                   static_cast<int32_t>(batch), static_cast<int32_t>(rows), max_new, max_len, out.data_ptr(),
-                                  ws, bytes, st.stream());
+                                  ws, bytes, st.raw);
               }), "hra_kv8_attention");
         if (a[9] != Py_None) {
             Py_INCREF(a[9]);
@@ -202,7 +219,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// pages(cache, device, update, parents or None, room or None, table, lens, refs, workspace, own, stream)
+// pages(cache, device, update, parents or None, room or None, table, lens, refs, workspace, home (see attend), stream)
 PyObject* pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!counted(n, 11)) return nullptr;
     return guarded([&]() -> PyObject* {
@@ -219,11 +236,11 @@ PyObject* pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor& w = tensor(a[8], "workspace");
         on_device(w, index, "workspace");
         if (!w.is_contiguous()) refuse("workspace must be contiguous");
-        const c10::cuda::CUDAStream st = stream_of(a[10], index);
-        if (a[9] == Py_True) used_on(w, st);
+        const Stream st = stream_of(a[10], index);
+        if (a[9] != Py_None && away(a[9], st)) used_on(w, st.memory);
         check(on(index, [&] {
-                  return update ? f_update(c, parents, room, table, lens, refs, w.data_ptr(), w.nbytes(), st.stream())
-                                : f_compact(c, table, lens, refs, w.data_ptr(), w.nbytes(), st.stream());
+                  return update ? f_update(c, parents, room, table, lens, refs, w.data_ptr(), w.nbytes(), st.raw)
+                                : f_compact(c, table, lens, refs, w.data_ptr(), w.nbytes(), st.raw);
               }), update ? "hra_kv8_update" : "hra_kv8_compact");
         Py_RETURN_NONE;
     });

@@ -423,3 +423,24 @@ def test_a_scale_that_float32_rounds_to_zero_is_not_the_default(hra):  # noqa: F
         with pytest.raises(hra.HraError):
             kv.attend(0, q, cu, n, 1, 20, scale=scale)
     assert torch.equal(kv.attend(0, q, cu, n, 1, 20, scale=0.125), kv.attend(0, q, cu, n, 1, 20))
+
+
+def test_streams_by_any_object_with_a_handle(hra):  # noqa: F811
+    """A torch stream, another object with its handle, and CUDA's own handles of the default stream."""
+    from types import SimpleNamespace
+    c = build([600, 40], H=2, D=64, P=16, seed=51)
+    q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(1)).to(BF16).cuda()
+    cu, n = i32([0, 1, 2]).cuda(), i32([600, 40]).cuda()
+    want = gpu(hra, c).attend(0, q, cu, n, 1, 600).clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, SimpleNamespace(cuda_stream=side.cuda_stream), SimpleNamespace(cuda_stream=0), SimpleNamespace(cuda_stream=1),
+                   SimpleNamespace(cuda_stream=2)):
+        kv = gpu(hra, c)
+        torch.cuda.synchronize()
+        out = kv.attend(0, q, cu, n, 1, 600, stream=stream)
+        kv.update(stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(kv.page_table.cpu(), c["table"])
+    with pytest.raises(AttributeError):
+        kv.attend(0, q, cu, n, 1, 600, stream=7)
