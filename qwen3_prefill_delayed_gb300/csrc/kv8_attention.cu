@@ -624,8 +624,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
 
 // One CTA per share: the item that begins in it and goes on behind it.  The rows' maxima and sums over all parts
 // come first (a warp a row, a lane a part), then every thread adds its columns, parts in order, with the loads free of
-// each other and the first ones under way before (8 rows after 1024-2112 positions, both kernels in a graph over 36 layers: 15.6 us, and 17.0
-// with one under way instead of eight).
+// each other and the first ones under way before (8 rows after 1024-2112 positions, both kernels in a graph over 36
+// layers: 15.6 us, and 17.0 with one under way instead of eight).
 template <int HD, int NG, bool ONE>
 __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ SplitArgs s) {
     pdl_launch();

@@ -421,7 +421,7 @@ __device__ __noinline__ void outputs_again(const PromptArgs& p, const int* first
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_constant__ CUtensorMap tmK,
-                                                                      const __grid_constant__ PromptArgs p) {
+                                                                 const __grid_constant__ PromptArgs p) {
     using C = Cfg<HD>;
     pdl_launch();
     pdl_wait();
