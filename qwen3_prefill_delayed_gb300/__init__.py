@@ -15,6 +15,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
+import inspect
 import os
 from typing import List, Optional, Sequence
 
@@ -265,13 +267,24 @@ def _memory_of(stream, device):
     return torch.cuda.stream(stream)
 
 
-def _hidden_for(B: int, H: int, device, stream) -> torch.Tensor:
-    """An output bf16 [B, H] of a call on `stream`, kept for the caller's stream too."""
-    with _memory_of(stream, device):
-        out = torch.empty(B, H, dtype=torch.bfloat16, device=device)
-    if stream is not None:
-        out.record_stream(torch.cuda.current_stream(device))
-    return out
+def _allocates(fn):
+    """A call that takes `stream` and allocates its outputs or workspaces: on another stream than the current one they are that
+    stream's memory, and outputs are kept for the caller's stream too."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        device = next((a.device for a in (*args, *kw.values()) if isinstance(a, torch.Tensor)), None)
+        with _memory_of(stream, device):
+            result = fn(*args, **kw)
+        for t in result if isinstance(result, tuple) else (result,):
+            t.record_stream(torch.cuda.current_stream(t.device))
+        return result
+
+    return call
 
 
 class _Workspace:
@@ -279,15 +292,14 @@ class _Workspace:
         self.buf: Optional[torch.Tensor] = None
         self.captured, self.in_graphs = False, []   # a captured graph uses buf; the earlier ones that graphs use
 
-    def get(self, nbytes: int, device, stream=None) -> torch.Tensor:
-        with _memory_of(stream, device):
-            if self.buf is None or self.buf.numel() < nbytes or self.buf.device != torch.device(device):
-                if self.captured:
-                    self.in_graphs.append(self.buf)
-                    self.captured = False
-                self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-            self.captured |= torch.cuda.is_current_stream_capturing()
-            self.buf.record_stream(torch.cuda.current_stream(self.buf.device))   # (nothing to do on its own stream)
+    def get(self, nbytes: int, device) -> torch.Tensor:
+        if self.buf is None or self.buf.numel() < nbytes or self.buf.device != torch.device(device):
+            if self.captured:
+                self.in_graphs.append(self.buf)
+                self.captured = False
+            self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        self.captured |= torch.cuda.is_current_stream_capturing()
+        self.buf.record_stream(torch.cuda.current_stream(self.buf.device))   # (nothing to do on its own stream)
         return self.buf
 
 
@@ -304,7 +316,9 @@ class _KeptWorkspace(_Workspace):
         if self.buf is not None and self.buf.numel() < nbytes:
             self.outgrown.append(self.buf)
             nbytes = max(nbytes, 2 * self.buf.numel())
-        before, buf = self.buf, super().get(nbytes, device, stream)
+        before = self.buf
+        with _memory_of(stream, device):
+            buf = super().get(nbytes, device)
         if buf is not before:
             self.home = stream.cuda_stream if stream is not None else torch.cuda.current_stream(buf.device).cuda_stream
         return buf
@@ -346,6 +360,7 @@ class Backbone:
     def prefill_chunk_workspace_size(self, batch, total, max_len, max_end) -> int:
         return lib().hra_prefill_chunk_workspace_size(ctypes.byref(self.dims), batch, total, max_len, max_end)
 
+    @_allocates
     def prefill(self, tokens: torch.Tensor, seq_lens: Sequence[int], cache: torch.Tensor,
                 out: Optional[torch.Tensor] = None, full_last_layer: bool = False,
                 workspace: Optional[torch.Tensor] = None, stream=None,
@@ -359,13 +374,13 @@ class Backbone:
         B, P = tokens.shape
         lens = (ctypes.c_int32 * B)(*[int(x) for x in seq_lens])
         if out is None:
-            out = _hidden_for(B, self.d.hidden, tokens.device, stream)
+            out = torch.empty(B, self.d.hidden, dtype=torch.bfloat16, device=tokens.device)
         flags = PREFILL_FULL_LAST_LAYER if full_last_layer else 0
         if isinstance(cache, Kv8Cache):
             starts = None if start_pos is None else (ctypes.c_int32 * B)(*[int(x) for x in start_pos])
             max_end = max(int(n) + (0 if start_pos is None else int(start_pos[b])) for b, n in enumerate(seq_lens))
             need = lib().hra_prefill_kv8_workspace_size(ctypes.byref(self.dims), cache.ref, B, int(sum(seq_lens)), P, max_end)
-            ws = workspace if workspace is not None else self.ws.get(need, tokens.device, stream)
+            ws = workspace if workspace is not None else self.ws.get(need, tokens.device)
             rc = lib().hra_prefill_kv8(ctypes.byref(self.dims), ctypes.byref(self.table),
                                        _ptr(tokens, torch.int32, "tokens"), lens, starts, B, P, cache.ref,
                                        _ptr(out, torch.bfloat16, "last_hidden"), _ptr(ws, None, "workspace"), ws.numel(),
@@ -380,7 +395,7 @@ class Backbone:
             starts = (ctypes.c_int32 * B)(*[int(x) for x in start_pos])
             max_end = max(int(a) + int(n) for a, n in zip(start_pos, seq_lens))
             need = self.prefill_chunk_workspace_size(B, int(sum(seq_lens)), P, max(max_end, P))
-        ws = workspace if workspace is not None else self.ws.get(need, tokens.device, stream)
+        ws = workspace if workspace is not None else self.ws.get(need, tokens.device)
         if start_pos is None:
             rc = lib().hra_prefill(ctypes.byref(self.dims), ctypes.byref(self.table),
                                    _ptr(tokens, torch.int32, "tokens"), lens, B, P, ctypes.byref(kv),
@@ -396,6 +411,7 @@ class Backbone:
         self.last_ws = ws
         return out
 
+    @_allocates
     def decode_dev(self, in_emb: torch.Tensor, pos: torch.Tensor, pos_bound: int, cache: torch.Tensor,
                    advance: bool = True, out: Optional[torch.Tensor] = None,
                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -403,9 +419,9 @@ class Backbone:
         `advance`); pos_bound is a host upper bound of every position.  With a Kv8Cache, hra_decode_dev_kv8."""
         B = in_emb.shape[0]
         if out is None:
-            out = _hidden_for(B, self.d.hidden, in_emb.device, stream)
+            out = torch.empty(B, self.d.hidden, dtype=torch.bfloat16, device=in_emb.device)
         need = self._decode_need(B, cache)
-        ws = workspace if workspace is not None else self.ws.get(need, in_emb.device, stream)
+        ws = workspace if workspace is not None else self.ws.get(need, in_emb.device)
         if isinstance(cache, Kv8Cache):
             rc = lib().hra_decode_dev_kv8(ctypes.byref(self.dims), ctypes.byref(self.table),
                                           _ptr(in_emb, torch.bfloat16, "in_emb"), _ptr(pos, torch.int32, "pos"),
@@ -433,6 +449,7 @@ class Backbone:
     def decode_workspace_size(self, batch, n_slots) -> int:
         return lib().hra_decode_workspace_size(ctypes.byref(self.dims), batch, n_slots)
 
+    @_allocates
     def decode(self, in_emb: torch.Tensor, pos: Sequence[int], cache: torch.Tensor,
                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
@@ -440,9 +457,9 @@ class Backbone:
         B = in_emb.shape[0]
         p = (ctypes.c_int32 * B)(*[int(x) for x in pos])
         if out is None:
-            out = _hidden_for(B, self.d.hidden, in_emb.device, stream)
+            out = torch.empty(B, self.d.hidden, dtype=torch.bfloat16, device=in_emb.device)
         need = self._decode_need(B, cache)
-        ws = workspace if workspace is not None else self.ws.get(need, in_emb.device, stream)
+        ws = workspace if workspace is not None else self.ws.get(need, in_emb.device)
         if isinstance(cache, Kv8Cache):
             rc = lib().hra_decode_kv8(ctypes.byref(self.dims), ctypes.byref(self.table),
                                       _ptr(in_emb, torch.bfloat16, "in_emb"), p, B, cache.ref,
@@ -554,6 +571,7 @@ class AudioHead:
     def workspace_size(self, batch: int) -> int:
         return lib().hra_codebook_workspace_size(ctypes.byref(self.dims), batch)
 
+    @_allocates
     def step(self, hidden: torch.Tensor, state: torch.Tensor, eoc_bias: Optional[torch.Tensor] = None,
              codes: Optional[torch.Tensor] = None, next_emb: Optional[torch.Tensor] = None,
              done: Optional[torch.Tensor] = None, logits: Optional[torch.Tensor] = None,
@@ -606,6 +624,7 @@ class AudioHead:
         self.last_ws = ws
         return codes, next_emb, done
 
+    @_allocates
     def step_noalloc(self, hidden: torch.Tensor, state: torch.Tensor, eoc_bias: Optional[torch.Tensor] = None,
                      codes: Optional[torch.Tensor] = None, next_emb: Optional[torch.Tensor] = None,
                      done: Optional[torch.Tensor] = None, logits: Optional[torch.Tensor] = None, stream=None):
@@ -636,6 +655,7 @@ class AudioHead:
         return codes, next_emb, done
 
 
+@_allocates
 def hra_linear(a: torch.Tensor, w: torch.Tensor, epilogue: int = EPI_STORE,
                out: Optional[torch.Tensor] = None, split_k: int = 0, stream=None) -> torch.Tensor:
     """out = epilogue(a [M, K] @ w^T) through the tensor-core GEMM of the library."""
@@ -656,6 +676,7 @@ def hra_linear(a: torch.Tensor, w: torch.Tensor, epilogue: int = EPI_STORE,
     return out
 
 
+@_allocates
 def fp8_quantize_weight(w: torch.Tensor, stream=None):
     """hra_fp8_quantize_weight: bf16 CUDA tensor -> (E4M3 codes uint8 same shape, scale float32 [1])."""
     w8 = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
@@ -665,6 +686,7 @@ def fp8_quantize_weight(w: torch.Tensor, stream=None):
     return w8, sc
 
 
+@_allocates
 def fp8_quantize(x: torch.Tensor, scale: torch.Tensor, stream=None) -> torch.Tensor:
     """hra_fp8_quantize: e4m3(x / scale) as uint8 codes (scale: CUDA float32 scalar tensor)."""
     x8 = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
@@ -673,6 +695,7 @@ def fp8_quantize(x: torch.Tensor, scale: torch.Tensor, stream=None) -> torch.Ten
     return x8
 
 
+@_allocates
 def nvfp4_quantize(x: torch.Tensor, g: torch.Tensor, stream=None):
     """hra_nvfp4_quantize: bf16 CUDA [rows, K] and the global scale (CUDA float32 scalar) ->
     (E2M1 codes uint8 [rows, K], E4M3 block scales uint8 [rows, K / 16])."""
@@ -685,6 +708,7 @@ def nvfp4_quantize(x: torch.Tensor, g: torch.Tensor, stream=None):
     return codes, scales
 
 
+@_allocates
 def hra_linear_fp8(a8: torch.Tensor, w8: torch.Tensor, a_scale: torch.Tensor, w_scale: torch.Tensor,
                    epilogue: int = EPI_STORE, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """hra_linear_fp8: a8 [M, K] and w8 [N or 2N, K] E4M3 codes (uint8), per-tensor scales."""
@@ -732,6 +756,7 @@ class Fp8Backbone:
             t[l].a_scale = self.a_scale[l].data_ptr()
         self.table = t
 
+    @_allocates
     def calibrate(self, tokens: torch.Tensor, seq_lens: Sequence[int], cache: torch.Tensor, stream=None):
         """hra_fp8_calibrate on a calibration batch: fills amax and a_scale [n_layers, 4]."""
         B, P = tokens.shape
@@ -749,6 +774,7 @@ class Fp8Backbone:
     def prefill_workspace_size(self, batch, total, max_len) -> int:
         return lib().hra_prefill_fp8_workspace_size(ctypes.byref(self.bb.dims), batch, total, max_len)
 
+    @_allocates
     def prefill(self, tokens: torch.Tensor, seq_lens: Sequence[int], cache: torch.Tensor,
                 out: Optional[torch.Tensor] = None, full_last_layer: bool = False,
                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -769,6 +795,7 @@ class Fp8Backbone:
         return out
 
 
+@_allocates
 def nvfp4_quantize_weight(w: torch.Tensor, stream=None):
     """hra_nvfp4_quantize_weight: bf16 CUDA [rows, K] -> (E2M1 codes uint8 [rows, K], E4M3 block
     scales uint8 [rows, K / 16], global scale float32 [1] = max|w| / (6 * 448))."""
@@ -782,6 +809,7 @@ def nvfp4_quantize_weight(w: torch.Tensor, stream=None):
     return codes, scales, g
 
 
+@_allocates
 def hra_linear_nvfp4(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
                      g_a: torch.Tensor, g_w: torch.Tensor, epilogue: int = EPI_STORE,
                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -842,6 +870,7 @@ class Nvfp4Backbone:
             t[l].a_scale = self.a_scale[l].data_ptr()
         self.table = t
 
+    @_allocates
     def calibrate(self, tokens: torch.Tensor, seq_lens: Sequence[int], cache: torch.Tensor, stream=None):
         """hra_fp8_calibrate's amax, then a_scale [n_layers, 4] as described above."""
         amax, _ = self.fp8.calibrate(tokens, seq_lens, cache, stream=stream)
@@ -852,6 +881,7 @@ class Nvfp4Backbone:
     def prefill_workspace_size(self, batch, total, max_len) -> int:
         return lib().hra_prefill_nvfp4_workspace_size(ctypes.byref(self.bb.dims), batch, total, max_len)
 
+    @_allocates
     def prefill(self, tokens: torch.Tensor, seq_lens: Sequence[int], cache: torch.Tensor,
                 out: Optional[torch.Tensor] = None, full_last_layer: bool = False,
                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:

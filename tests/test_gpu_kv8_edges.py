@@ -156,9 +156,10 @@ def test_a_scale_of_zero_makes_values_of_zero(hra, G, D, new, which):  # noqa: F
 # ------------------------------------------------------------------- memory of calls on another stream than the current one
 
 def freed_in_use(nbytes):
-    """Address of a block that the current stream still writes after it went back to the allocator."""
+    """Address of a block that the current stream still writes after it went back to the allocator.  (The stream is busy for
+    some 50 ms; what runs meanwhile has run before, since the first launch of a kernel loads it and may take as long.)"""
     x = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-    torch.cuda._sleep(20_000_000)
+    torch.cuda._sleep(100_000_000)
     x.fill_(1)
     return x.data_ptr()
 
@@ -184,7 +185,7 @@ def test_outputs_and_workspaces_are_memory_of_the_stream_they_are_written_on(hra
     # dropped while the side stream still writes it
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(20_000_000)
+        torch.cuda._sleep(100_000_000)
     out = kv.attend(0, q, cu, n, new, 2500, stream=side)
     at = out.data_ptr()
     del out
@@ -192,7 +193,7 @@ def test_outputs_and_workspaces_are_memory_of_the_stream_they_are_written_on(hra
     # a workspace that another stream than its own uses goes back only when that one is done
     at = kv._attn_ws.buf.data_ptr()
     torch.cuda.synchronize()
-    torch.cuda._sleep(20_000_000)
+    torch.cuda._sleep(100_000_000)
     kv.attend(0, q, cu, n, new, 2500)                        # on the current stream
     kv._attn_ws.buf = None
     with torch.cuda.stream(side):
@@ -205,6 +206,7 @@ def test_page_workspaces_are_memory_of_the_stream_they_are_used_on(hra):  # noqa
     c["scales"] = torch.nan_to_num(c["scales"], nan=0.5)
     kv, side = gpu(hra, c), torch.cuda.Stream()
     room = i32([30] * 2 + [0] * 298).cuda()
+    gpu(hra, c).update(None, room)
     torch.cuda.synchronize()
     torch.cuda.empty_cache()
     import ctypes
@@ -444,3 +446,32 @@ def test_streams_by_any_object_with_a_handle(hra):  # noqa: F811
         assert torch.equal(out, want) and torch.equal(kv.page_table.cpu(), c["table"])
     with pytest.raises(AttributeError):
         kv.attend(0, q, cu, n, 1, 600, stream=7)
+
+
+def test_other_calls_outputs_are_memory_of_the_call_s_stream(hra, model):  # noqa: F811
+    """The codebook step, a linear layer and a quantisation, with stream= by name or by position."""
+    import workloads as W
+    d, _ = model
+    audio = W.make_audio(d, torch.Generator().manual_seed(8))
+    head = hra.AudioHead(d, audio["head_w"].cuda(), audio["code_emb"].cuda())
+    g = torch.Generator().manual_seed(9)
+    hid = torch.randn(3, d.hidden, generator=g).mul(0.1).to(BF16).cuda()
+    a, w = torch.randn(200, 256, generator=g).to(BF16).cuda(), torch.randn(384, 256, generator=g).to(BF16).cuda()
+    scale = torch.ones(1, device="cuda")
+    results = []
+    for other in (False, True):
+        side = torch.cuda.Stream() if other else None
+        state = torch.zeros(3, 4, dtype=torch.int32, device="cuda")
+        state[:, 1] = -1
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        busy = [freed_in_use(n) for n in (3 * d.n_codebooks * 4, 3 * d.hidden * 2, 200 * 384 * 2, 200 * 256)] if other else []
+        codes, emb, _ = head.step(hid, state, stream=side)
+        x8 = hra.fp8_quantize(a, scale, side)
+        if other:
+            assert not torch.cuda.current_stream().query()
+        y = hra.hra_linear(a, w, stream=side)                # (waits for its stream)
+        assert not {codes.data_ptr(), emb.data_ptr(), x8.data_ptr(), y.data_ptr()} & set(busy)
+        torch.cuda.synchronize()
+        results.append([t.clone() for t in (codes, emb, x8, y)])
+    assert all(torch.equal(p, q) for p, q in zip(*results))
