@@ -504,6 +504,40 @@ int hra_kv8_attention(const hra_kv8_cache* cache, int32_t layer, const void* q_d
                       int32_t batch, int32_t total_rows, int32_t max_new, int32_t max_len, void* out_dev,
                       void* workspace, size_t workspace_bytes, void* stream);
 
+/* What the attention of a call reads, where that is not every position up to the token's own. */
+typedef struct hra_kv8_reach {
+    const int32_t* group_cu_dev;   /* int32 [groups + 1], device */
+    const int32_t* prefix_dev;     /* int32 [groups], device */
+    int32_t groups, max_prefix, max_own;
+    int32_t window, sinks;
+} hra_kv8_reach;
+/* A window: the token at position p attends the positions of [0, p] from p - window + 1 on and those below sinks.
+ *   window       >= 1, or 0: no window (then sinks is 0)
+ *   sinks        >= 0; both at most 2^30 (else HRA_ERR_RANGE)
+ * Table entries of pages that no token of the call sees are not looked at: hra_kv8_update_reach drops such pages.
+ * A shared prefix: groups of rows whose tables list the same pages for their first positions (continuations of one prompt,
+ * as hra_kv8_update forks them).  Those pages are read once for all the tokens of a group instead of once a row.
+ *   group_cu     group g is rows group_cu[g] .. group_cu[g + 1) of the batch, ascending; rows of no group share nothing
+ *   prefix       positions that the rows of group g share: of them the whole pages, and no more than the positions that each
+ *                of its rows with new tokens holds before them, are read through the table of the group's first row
+ *   max_prefix   host upper bound of prefix
+ *   max_own      host upper bound of kv_len - prefix (0 or more).  Both choose how the work is split; larger ones give the
+ *                same values
+ *   groups       0: none (the pointers are then not looked at); at most 1024 (else HRA_ERR_UNSUPPORTED)
+ * The values are those of hra_kv8_attention, in another order of sums; where sharing would not pay, it is that call.  A window
+ * and groups in one call are HRA_ERR_UNSUPPORTED. */
+
+/* hra_kv8_attention with a reach; NULL: every position.  The arguments and what is said of them are the same; workspace sizes
+ * do not fall when an argument, a bound of the reach or its number of groups grows. */
+size_t hra_kv8_attention_reach_workspace_size(const hra_kv8_cache* cache, int32_t batch, int32_t total_rows,
+                                              int32_t n_q_heads, int32_t max_new, int32_t max_len,
+                                              const hra_kv8_reach* reach);
+int hra_kv8_attention_reach(const hra_kv8_cache* cache, int32_t layer, const void* q_dev, int64_t q_row_stride,
+                            int32_t n_q_heads, float scale, const int32_t* cu_dev, const int32_t* kv_len_dev,
+                            int32_t batch, int32_t total_rows, int32_t max_new, int32_t max_len,
+                            const hra_kv8_reach* reach, void* out_dev, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
 /* The rows of the next step: forked, reordered, freed, extended.
  *   parents_dev  int32 [rows]: new row b is a copy of old row parents[b]; -1 empties it; NULL: every row stays
  *   room_dev     int32 [rows]: pages are taken for lens[b] + room[b] positions; NULL: 0
@@ -522,6 +556,14 @@ size_t hra_kv8_pages_workspace_size(const hra_kv8_cache* cache);
 int hra_kv8_update(const hra_kv8_cache* cache, const int32_t* parents_dev, const int32_t* room_dev,
                    int32_t* table_out, int32_t* lens_out, int32_t* refs_out, void* workspace,
                    size_t workspace_bytes, void* stream);
+
+/* hra_kv8_update for rows of which a window is seen: page i of a new row of n positions is dropped (its entry is -1, now and
+ * in later calls with the same window) when no token behind them sees any of it: i * page_size >= sinks and
+ * (i + 1) * page_size <= n - window + 1.  It counts as no page the row lists, so it is free once no row keeps it.  reach: its
+ * window and sinks (groups must be 0: HRA_ERR_INVALID_ARG); NULL or window 0: hra_kv8_update. */
+int hra_kv8_update_reach(const hra_kv8_cache* cache, const int32_t* parents_dev, const int32_t* room_dev,
+                         const hra_kv8_reach* reach, int32_t* table_out, int32_t* lens_out, int32_t* refs_out,
+                         void* workspace, size_t workspace_bytes, void* stream);
 
 /* With U pages in use (refs > 0), the i-th used page numbered U or more (ascending) moves to the i-th unused page
  * below U, in every layer; table_out and refs_out follow, lens_out = lens.  Pages U .. n_pages - 1 are free
@@ -557,6 +599,32 @@ int hra_ar_frame_kv8(const hra_dims* dims, const hra_weights* weights, const voi
                      int32_t pos_bound, int32_t batch, const hra_kv8_cache* cache, int32_t* codes_dev,
                      void* next_emb_dev, int32_t* done_dev, void* backbone_ws, size_t backbone_ws_bytes,
                      void* codebook_ws, size_t codebook_ws_bytes, void* stream);
+
+/* The same with a reach of every layer's attention (NULL: every position).  Where it has groups, the batch's rows are the
+ * rows of group_cu, and the device arrays are read at each call, a captured one's replays among them. */
+size_t hra_prefill_kv8_reach_workspace_size(const hra_dims* dims, const hra_kv8_cache* cache, int32_t batch,
+                                            int32_t total_tokens, int32_t max_len, int32_t max_end,
+                                            const hra_kv8_reach* reach);
+int hra_prefill_kv8_reach(const hra_dims* dims, const hra_weights* weights, const int32_t* tokens_dev,
+                          const int32_t* seq_lens, const int32_t* start_pos, int32_t batch, int32_t max_len,
+                          const hra_kv8_cache* cache, const hra_kv8_reach* reach, void* last_hidden_dev,
+                          void* workspace, size_t workspace_bytes, uint32_t flags, void* stream);
+size_t hra_decode_kv8_reach_workspace_size(const hra_dims* dims, const hra_kv8_cache* cache, int32_t batch,
+                                           const hra_kv8_reach* reach);
+int hra_decode_kv8_reach(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev, const int32_t* pos,
+                         int32_t batch, const hra_kv8_cache* cache, const hra_kv8_reach* reach, void* hidden_dev,
+                         void* workspace, size_t workspace_bytes, void* stream);
+int hra_decode_dev_kv8_reach(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev,
+                             int32_t* pos_dev, int32_t pos_bound, int32_t advance, int32_t batch,
+                             const hra_kv8_cache* cache, const hra_kv8_reach* reach, void* hidden_dev,
+                             void* workspace, size_t workspace_bytes, void* stream);
+int hra_ar_frame_kv8_reach(const hra_dims* dims, const hra_weights* weights, const void* head_w_dev,
+                           const void* code_emb_dev, hra_delay_state* state_dev, const float* eoc_bias_dev,
+                           const hra_sampling* sampling, const uint64_t* seeds_dev, void* hidden_dev,
+                           int32_t* pos_dev, int32_t pos_bound, int32_t batch, const hra_kv8_cache* cache,
+                           const hra_kv8_reach* reach, int32_t* codes_dev, void* next_emb_dev, int32_t* done_dev,
+                           void* backbone_ws, size_t backbone_ws_bytes, void* codebook_ws,
+                           size_t codebook_ws_bytes, void* stream);
 
 /* ---- measurement ---------------------------------------------------------------------------- */
 /* Number of kernels the library has launched in this process (host-side count). */

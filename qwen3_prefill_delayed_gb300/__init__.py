@@ -47,6 +47,9 @@ EXPORTED = ["hra_prefill_workspace_size", "hra_prefill", "hra_prefill_chunk_work
             "hra_kv8_append", "hra_kv8_attention_workspace_size", "hra_kv8_attention", "hra_kv8_pages_workspace_size",
             "hra_kv8_update", "hra_kv8_compact", "hra_prefill_kv8_workspace_size", "hra_prefill_kv8",
             "hra_decode_kv8_workspace_size", "hra_decode_kv8", "hra_decode_dev_kv8", "hra_ar_frame_kv8",
+            "hra_kv8_attention_reach_workspace_size", "hra_kv8_attention_reach", "hra_kv8_update_reach",
+            "hra_prefill_kv8_reach_workspace_size", "hra_prefill_kv8_reach", "hra_decode_kv8_reach_workspace_size",
+            "hra_decode_kv8_reach", "hra_decode_dev_kv8_reach", "hra_ar_frame_kv8_reach",
             "hra_launch_counter", "hra_probe_select", "hra_probe_collect", "hra_set_decode_pass",
             "hra_set_gemm_pairs", "hra_device_error", "hra_status_string"]
 PROBE = {"none": 0, "qkv": 1, "o_proj": 2, "gate_up": 3, "down": 4, "attention": 5, "audio_head": 6,
@@ -94,6 +97,11 @@ class HraKv8Cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "scales", "page_table", "lens", "refs", "errors")] + \
                [(n, ctypes.c_int32) for n in ("n_layers", "n_pages", "n_kv_heads", "head_dim", "page_size", "rows",
                                               "max_pages")]
+
+
+class HraKv8Reach(ctypes.Structure):
+    _fields_ = [("group_cu", ctypes.c_void_p), ("prefix", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int32) for n in ("groups", "max_prefix", "max_own", "window", "sinks")]
 
 
 class HraSampling(ctypes.Structure):
@@ -193,6 +201,16 @@ def lib() -> ctypes.CDLL:
         L.hra_decode_dev_kv8.argtypes = [dp, ctypes.POINTER(HraWeights), vp, vp, i32, i32, i32, kp, vp, vp, sz, vp]
         L.hra_ar_frame_kv8.argtypes = [dp, ctypes.POINTER(HraWeights), vp, vp, vp, vp, ctypes.POINTER(HraSampling), vp,
                                        vp, vp, i32, i32, kp, vp, vp, vp, vp, sz, vp, sz, vp]
+        rp = ctypes.POINTER(HraKv8Reach)
+        # the calls with a reach: one more argument behind the bounds, the cache, or a pass's sizes
+        for name, at in (("hra_kv8_attention_workspace_size", 6), ("hra_kv8_attention", 12), ("hra_kv8_update", 3),
+                         ("hra_prefill_kv8_workspace_size", 6), ("hra_prefill_kv8", 8), ("hra_decode_kv8_workspace_size", 3),
+                         ("hra_decode_kv8", 6), ("hra_decode_dev_kv8", 8), ("hra_ar_frame_kv8", 13)):
+            args = list(getattr(L, name).argtypes)
+            size = name.endswith("_workspace_size")
+            f = getattr(L, name.replace("_workspace_size", "") + "_reach" + ("_workspace_size" if size else ""))
+            f.argtypes = args[:at] + [rp] + args[at:]
+            f.restype = sz if size else ctypes.c_int
         for f in ("hra_kv8_append", "hra_kv8_attention", "hra_kv8_update", "hra_kv8_compact", "hra_prefill_kv8",
                   "hra_decode_kv8", "hra_decode_dev_kv8", "hra_ar_frame_kv8"):
             getattr(L, f).restype = ctypes.c_int
@@ -364,13 +382,15 @@ class Backbone:
     def prefill(self, tokens: torch.Tensor, seq_lens: Sequence[int], cache: torch.Tensor,
                 out: Optional[torch.Tensor] = None, full_last_layer: bool = False,
                 workspace: Optional[torch.Tensor] = None, stream=None,
-                start_pos: Optional[Sequence[int]] = None) -> torch.Tensor:
+                start_pos: Optional[Sequence[int]] = None, reach: Optional["Kv8Reach"] = None) -> torch.Tensor:
         """hra_prefill: tokens int32 [B, P_max] (CUDA), seq_lens host ints -> last hidden [B, H].
 
         With start_pos (host ints), hra_prefill_chunk: row b's tokens sit at positions
         start_pos[b] .. start_pos[b] + seq_lens[b] - 1 after the ones already in the cache.
 
-        With a Kv8Cache, hra_prefill_kv8; the rows must own pages for these positions (Kv8Cache.update)."""
+        With a Kv8Cache, hra_prefill_kv8 (hra_prefill_kv8_reach with a reach); the rows must own pages for these positions
+        (Kv8Cache.update)."""
+        reach = _reach(reach, cache)
         B, P = tokens.shape
         lens = (ctypes.c_int32 * B)(*[int(x) for x in seq_lens])
         if out is None:
@@ -379,12 +399,13 @@ class Backbone:
         if isinstance(cache, Kv8Cache):
             starts = None if start_pos is None else (ctypes.c_int32 * B)(*[int(x) for x in start_pos])
             max_end = max(int(n) + (0 if start_pos is None else int(start_pos[b])) for b, n in enumerate(seq_lens))
-            need = lib().hra_prefill_kv8_workspace_size(ctypes.byref(self.dims), cache.ref, B, int(sum(seq_lens)), P, max_end)
+            need = lib().hra_prefill_kv8_reach_workspace_size(ctypes.byref(self.dims), cache.ref, B, int(sum(seq_lens)), P,
+                                                              max_end, reach)
             ws = workspace if workspace is not None else self.ws.get(need, tokens.device)
-            rc = lib().hra_prefill_kv8(ctypes.byref(self.dims), ctypes.byref(self.table),
-                                       _ptr(tokens, torch.int32, "tokens"), lens, starts, B, P, cache.ref,
-                                       _ptr(out, torch.bfloat16, "last_hidden"), _ptr(ws, None, "workspace"), ws.numel(),
-                                       flags, _stream(stream))
+            rc = lib().hra_prefill_kv8_reach(ctypes.byref(self.dims), ctypes.byref(self.table),
+                                             _ptr(tokens, torch.int32, "tokens"), lens, starts, B, P, cache.ref, reach,
+                                             _ptr(out, torch.bfloat16, "last_hidden"), _ptr(ws, None, "workspace"),
+                                             ws.numel(), flags, _stream(stream))
             _check(rc, "hra_prefill_kv8")
             self.last_ws = ws
             return out
@@ -414,20 +435,23 @@ class Backbone:
     @_allocates
     def decode_dev(self, in_emb: torch.Tensor, pos: torch.Tensor, pos_bound: int, cache: torch.Tensor,
                    advance: bool = True, out: Optional[torch.Tensor] = None,
-                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                   workspace: Optional[torch.Tensor] = None, stream=None,
+                   reach: Optional["Kv8Reach"] = None) -> torch.Tensor:
         """hra_decode_dev: positions in the CUDA int32 tensor `pos` (advanced in place when
-        `advance`); pos_bound is a host upper bound of every position.  With a Kv8Cache, hra_decode_dev_kv8."""
+        `advance`); pos_bound is a host upper bound of every position.  With a Kv8Cache, hra_decode_dev_kv8
+        (hra_decode_dev_kv8_reach with a reach)."""
+        reach = _reach(reach, cache)
         B = in_emb.shape[0]
         if out is None:
             out = torch.empty(B, self.d.hidden, dtype=torch.bfloat16, device=in_emb.device)
-        need = self._decode_need(B, cache)
+        need = self._decode_need(B, cache, reach)
         ws = workspace if workspace is not None else self.ws.get(need, in_emb.device)
         if isinstance(cache, Kv8Cache):
-            rc = lib().hra_decode_dev_kv8(ctypes.byref(self.dims), ctypes.byref(self.table),
-                                          _ptr(in_emb, torch.bfloat16, "in_emb"), _ptr(pos, torch.int32, "pos"),
-                                          int(pos_bound), 1 if advance else 0, B, cache.ref,
-                                          _ptr(out, torch.bfloat16, "hidden"), _ptr(ws, None, "workspace"), ws.numel(),
-                                          _stream(stream))
+            rc = lib().hra_decode_dev_kv8_reach(ctypes.byref(self.dims), ctypes.byref(self.table),
+                                                _ptr(in_emb, torch.bfloat16, "in_emb"), _ptr(pos, torch.int32, "pos"),
+                                                int(pos_bound), 1 if advance else 0, B, cache.ref, reach,
+                                                _ptr(out, torch.bfloat16, "hidden"), _ptr(ws, None, "workspace"),
+                                                ws.numel(), _stream(stream))
             _check(rc, "hra_decode_dev_kv8")
             self.last_ws = ws
             return out
@@ -441,9 +465,9 @@ class Backbone:
         self.last_ws = ws
         return out
 
-    def _decode_need(self, batch, cache) -> int:
+    def _decode_need(self, batch, cache, reach=None) -> int:
         if isinstance(cache, Kv8Cache):
-            return lib().hra_decode_kv8_workspace_size(ctypes.byref(self.dims), cache.ref, batch)
+            return lib().hra_decode_kv8_reach_workspace_size(ctypes.byref(self.dims), cache.ref, batch, reach)
         return self.decode_workspace_size(batch, cache.shape[4])
 
     def decode_workspace_size(self, batch, n_slots) -> int:
@@ -452,19 +476,21 @@ class Backbone:
     @_allocates
     def decode(self, in_emb: torch.Tensor, pos: Sequence[int], cache: torch.Tensor,
                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-               stream=None) -> torch.Tensor:
-        """hra_decode: in_emb bf16 [B, H] (CUDA), pos host ints -> hidden [B, H].  With a Kv8Cache, hra_decode_kv8."""
+               stream=None, reach: Optional["Kv8Reach"] = None) -> torch.Tensor:
+        """hra_decode: in_emb bf16 [B, H] (CUDA), pos host ints -> hidden [B, H].  With a Kv8Cache, hra_decode_kv8
+        (hra_decode_kv8_reach with a reach)."""
+        reach = _reach(reach, cache)
         B = in_emb.shape[0]
         p = (ctypes.c_int32 * B)(*[int(x) for x in pos])
         if out is None:
             out = torch.empty(B, self.d.hidden, dtype=torch.bfloat16, device=in_emb.device)
-        need = self._decode_need(B, cache)
+        need = self._decode_need(B, cache, reach)
         ws = workspace if workspace is not None else self.ws.get(need, in_emb.device)
         if isinstance(cache, Kv8Cache):
-            rc = lib().hra_decode_kv8(ctypes.byref(self.dims), ctypes.byref(self.table),
-                                      _ptr(in_emb, torch.bfloat16, "in_emb"), p, B, cache.ref,
-                                      _ptr(out, torch.bfloat16, "hidden"), _ptr(ws, None, "workspace"), ws.numel(),
-                                      _stream(stream))
+            rc = lib().hra_decode_kv8_reach(ctypes.byref(self.dims), ctypes.byref(self.table),
+                                            _ptr(in_emb, torch.bfloat16, "in_emb"), p, B, cache.ref, reach,
+                                            _ptr(out, torch.bfloat16, "hidden"), _ptr(ws, None, "workspace"), ws.numel(),
+                                            _stream(stream))
             _check(rc, "hra_decode_kv8")
             self.last_ws = ws
             return out
@@ -486,12 +512,14 @@ class ARLoop:
 
     pos0: host ints, the position of each row's first decoded frame (its prompt length); pos_bound
     (host) must cover every position the loop will reach.  cache: the bf16 tensor, or a Kv8Cache (hra_ar_frame_kv8) whose
-    rows own pages for those positions."""
+    rows own pages for those positions; reach: what its attention reads (hra_ar_frame_kv8_reach)."""
 
     def __init__(self, bb: "Backbone", head: "AudioHead", cache: torch.Tensor, hidden: torch.Tensor,
                  pos0: Sequence[int], pos_bound: int, eoc_bias: Optional[torch.Tensor] = None,
-                 sampling=None, seeds: Optional[torch.Tensor] = None):
+                 sampling=None, seeds: Optional[torch.Tensor] = None, reach: Optional["Kv8Reach"] = None):
         self.bb, self.head, self.cache = bb, head, cache
+        self.reach = reach   # (its tensors live as long as the loop)
+        at = _reach(reach, cache)
         self.sampling = None if sampling is None else HraSampling(*sampling)   # (temperature, top_k, top_p)
         self.seeds = seeds                                                      # CUDA int64 [B] (uint64 bits)
         d = bb.d
@@ -507,7 +535,7 @@ class ARLoop:
         self.codes = torch.empty(B, d.n_codebooks, dtype=torch.int32, device=dev)
         self.next_emb = torch.empty(B, d.hidden, dtype=torch.bfloat16, device=dev)
         self.done = torch.empty(B, dtype=torch.int32, device=dev)
-        self.bws = torch.empty(bb._decode_need(B, cache), dtype=torch.uint8, device=dev)
+        self.bws = torch.empty(bb._decode_need(B, cache, at), dtype=torch.uint8, device=dev)
         self.cws = torch.empty(head.workspace_size(B), dtype=torch.uint8, device=dev)
         self.paged = isinstance(cache, Kv8Cache)
         self.kv = cache.struct if self.paged else bb.kv(cache)
@@ -520,7 +548,8 @@ class ARLoop:
         codes = self.codes if codes is None else codes
         done = self.done if done is None else done
         bias = self.eoc_bias if eoc_bias is None else eoc_bias
-        name = "hra_ar_frame_kv8" if self.paged else "hra_ar_frame"
+        name = "hra_ar_frame_kv8_reach" if self.paged else "hra_ar_frame"
+        reach = (_reach(self.reach, self.cache),) if self.paged else ()
         rc = getattr(lib(), name)(ctypes.byref(self.bb.dims), ctypes.byref(self.bb.table),
                                 _ptr(self.head.head_w, torch.bfloat16, "head_w"),
                                 _ptr(self.head.code_emb, torch.bfloat16, "code_emb"),
@@ -529,7 +558,7 @@ class ARLoop:
                                 ctypes.byref(self.sampling) if self.sampling is not None else None,
                                 _ptr(self.seeds, torch.int64, "seeds"),
                                 _ptr(self.hidden, torch.bfloat16, "hidden"), _ptr(self.pos, torch.int32, "pos"),
-                                self.pos_bound, self.B, ctypes.byref(self.kv),
+                                self.pos_bound, self.B, ctypes.byref(self.kv), *reach,
                                 _ptr(codes, torch.int32, "codes"), _ptr(self.next_emb, torch.bfloat16, "next_emb"),
                                 _ptr(done, torch.int32, "done"), _ptr(self.bws, None, "backbone workspace"),
                                 self.bws.numel(), _ptr(self.cws, None, "codebook workspace"), self.cws.numel(),
@@ -915,10 +944,61 @@ def _kv8_calls():
             raise HraError(f"the binding of the 8-bit cache is missing: build it with __graft_entry__.build() ({e})") from e
         L = lib()
         m.connect(HraError, *[ctypes.cast(f, ctypes.c_void_p).value for f in
-                              (L.hra_kv8_append, L.hra_kv8_attention, L.hra_kv8_attention_workspace_size, L.hra_kv8_update,
-                               L.hra_kv8_compact, L.hra_status_string)])
+                              (L.hra_kv8_append, L.hra_kv8_attention_reach, L.hra_kv8_attention_reach_workspace_size,
+                               L.hra_kv8_update_reach, L.hra_kv8_compact, L.hra_status_string)])
         _binding = m
     return _binding
+
+
+class Kv8Reach:
+    """What the attention of a call over a Kv8Cache reads (``hra_kv8_reach``), where that is not every position up to the
+    token's own: one of
+
+    window, sinks      the last `window` positions up to the token's own and the first `sinks`;
+    groups, prefix     rows groups[g] .. groups[g + 1) of the batch list the same pages for their first prefix[g] positions,
+                       which are read once for all of them.  CUDA int32 tensors [n + 1] and [n], read at each call.
+                       max_prefix and max_own are host upper bounds of prefix and of the rows' positions behind it (by
+                       default all that the cache's rows can hold)."""
+
+    def __init__(self, window: int = 0, sinks: int = 0, groups: Optional[torch.Tensor] = None,
+                 prefix: Optional[torch.Tensor] = None, max_prefix: Optional[int] = None, max_own: Optional[int] = None):
+        for name, v in (("window", window), ("sinks", sinks), ("max_prefix", max_prefix), ("max_own", max_own)):
+            if v is not None and not 0 <= int(v) <= 1 << 30:
+                raise HraError(f"{name} must lie in [0, 2^30]")
+        if sinks and not window:
+            raise HraError("sinks need a window")
+        if (groups is None) != (prefix is None):
+            raise HraError("groups and prefix go together")
+        if groups is None and (max_prefix is not None or max_own is not None):
+            raise HraError("max_prefix and max_own are bounds of groups")
+        if groups is not None and window:
+            raise HraError("a window and groups cannot be read in one call")
+        self.window, self.sinks, self.groups, self.prefix = int(window), int(sinks), groups, prefix
+        n, most = 0, 1 << 30
+        if groups is not None:
+            if groups.dim() != 1 or prefix.dim() != 1 or groups.numel() != prefix.numel() + 1 or prefix.numel() < 1:
+                raise HraError("groups must be int32 [n + 1] and prefix int32 [n]")
+            if groups.device != prefix.device:
+                raise HraError("groups and prefix must be on one device")
+            n = prefix.numel()
+        p_groups, p_prefix = _ptr(groups, torch.int32, "groups"), _ptr(prefix, torch.int32, "prefix")
+        self.struct = HraKv8Reach(p_groups.value if n else None, p_prefix.value if n else None, n,
+                                  most if max_prefix is None else int(max_prefix), most if max_own is None else int(max_own),
+                                  self.window, self.sinks)
+        self.ref, self.at = ctypes.byref(self.struct), ctypes.addressof(self.struct)
+
+
+def _reach(reach: Optional[Kv8Reach], cache):
+    """The reach as a call on this cache takes it (None: every position)."""
+    if reach is None:
+        return None
+    if not isinstance(reach, Kv8Reach):
+        raise HraError("reach must be a Kv8Reach")
+    if not isinstance(cache, Kv8Cache):
+        raise HraError("a reach needs a Kv8Cache")
+    if reach.groups is not None and reach.groups.device != cache.device:
+        raise HraError("groups and prefix must be on the device of the cache")
+    return reach.ref
 
 
 class Kv8Cache:
@@ -994,27 +1074,40 @@ class Kv8Cache:
         the cache's own lens, which the call writes: pass a copy, the same one for every layer."""
         self._call.append(self._at, self._index, layer, k, v, cu, start, max_new, stream)
 
-    def attention_workspace_size(self, batch: int, total_rows: int, n_q_heads: int, max_new: int, max_len: int) -> int:
+    def attention_workspace_size(self, batch: int, total_rows: int, n_q_heads: int, max_new: int, max_len: int,
+                                 reach: Optional[Kv8Reach] = None) -> int:
         with torch.cuda.device(self._index):
-            return lib().hra_kv8_attention_workspace_size(self.ref, batch, total_rows, n_q_heads, max_new, max_len)
+            return lib().hra_kv8_attention_reach_workspace_size(self.ref, batch, total_rows, n_q_heads, max_new, max_len,
+                                                                _reach(reach, self))
 
     def attend(self, layer: int, q: torch.Tensor, cu: torch.Tensor, kv_len: torch.Tensor, max_new: int, max_len: int,
                scale: float = 0.0, out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-               stream=None) -> torch.Tensor:
+               stream=None, reach: Optional[Kv8Reach] = None) -> torch.Tensor:
         """hra_kv8_attention: q bf16 [T, n_q_heads, head_dim] (rows may be strided) of rows' last tokens, kv_len int32
         [B] positions held -> bf16 [T, n_q_heads, head_dim].  Without a workspace, one of the object's own, which grows
-        with the calls.  Rows that no sequence has are not written: in an output that the call makes they hold anything."""
+        with the calls.  Rows that no sequence has are not written: in an output that the call makes they hold anything.
+        With a reach, hra_kv8_attention_reach."""
+        at = None
+        if reach is not None:
+            _reach(reach, self)
+            at = reach.at
         if workspace is not None:
             return self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out, workspace, None,
-                                     stream)
+                                     stream, at)
         own = self._attn_ws
-        r = self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out, own.buf, own.home, stream)
+        r = self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out, own.buf, own.home, stream,
+                              at)
         if type(r) is int:
             ws = own.get(r, self.device, stream)
-            r = self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out, ws, own.home, stream)
+            r = self._call.attend(self._at, self._index, layer, q, cu, kv_len, max_new, max_len, scale, out, ws, own.home, stream,
+                                  at)
         return r
 
-    def _pages(self, update, parents, room, out, workspace, stream):
+    def _pages(self, update, parents, room, out, workspace, stream, reach=None):
+        at = None
+        if reach is not None:
+            _reach(reach, self)
+            at = reach.at
         if self.refs is None:
             raise HraError("this needs the cache's refs")
         out = (self.page_table, self.lens, self.refs) if out is None else tuple(out)
@@ -1024,15 +1117,16 @@ class Kv8Cache:
             if workspace is None:
                 workspace = self._pages_ws.get(lib().hra_kv8_pages_workspace_size(self.ref), self.device, stream)
             home = self._pages_ws.home
-        self._call.pages(self._at, self._index, update, parents, room, *out, workspace, home, stream)
+        self._call.pages(self._at, self._index, update, parents, room, *out, workspace, home, stream, at)
         return out
 
     def update(self, parents: Optional[torch.Tensor] = None, room: Optional[torch.Tensor] = None, out=None,
-               workspace: Optional[torch.Tensor] = None, stream=None):
+               workspace: Optional[torch.Tensor] = None, stream=None, reach: Optional[Kv8Reach] = None):
         """hra_kv8_update: rows forked, reordered or freed by parents (int32 [rows], -1 = empty) and given pages for
         room (int32 [rows]) more tokens.  In place, or into out (see empty_pages): (page table, lens, refs); the cache
-        itself then keeps its own, until they are copied there or become those of a new Kv8Cache."""
-        return self._pages(True, parents, room, out, workspace, stream)
+        itself then keeps its own, until they are copied there or become those of a new Kv8Cache.  With a reach that has a
+        window, hra_kv8_update_reach: the pages that no later token sees are dropped."""
+        return self._pages(True, parents, room, out, workspace, stream, reach)
 
     def compact(self, out=None, workspace: Optional[torch.Tensor] = None, stream=None):
         """hra_kv8_compact: the pages in use to the low end of the pool; outputs as update."""

@@ -87,6 +87,7 @@ struct Layout {
 struct Kv8Pass {
     const hra_kv8_cache* cache;
     int max_new, max_end;
+    const hra_kv8_reach* reach;   // or null: every position
 };
 
 bool dims_ok(const hra_dims* d) {
@@ -161,8 +162,13 @@ Layout backbone_layout(const hra_dims& d, int batch, int rows, int rope_rows, in
         L.kv_len = g.take((size_t)batch * 4);
         L.one_each = g.take((size_t)(batch + 1) * 4);
         L.q_last = g.take((size_t)batch * Dq * 2);
-        L.kscratch = g.take(std::max(kv8_attention_scratch_bytes(v, batch, (int)T, d.n_q_heads, k8->max_new, k8->max_end),
-                                     kv8_attention_scratch_bytes(v, batch, batch, d.n_q_heads, 1, k8->max_end)) + 16);
+        auto scratch = [&](int total, int max_new) {
+            const hra_kv8_reach* r = k8->reach;
+            return r != nullptr && r->groups > 0
+                       ? kv8_shared_scratch_bytes(v, batch, total, d.n_q_heads, max_new, k8->max_end, r->groups, r->max_prefix, r->max_own)
+                       : kv8_attention_scratch_bytes(v, batch, total, d.n_q_heads, max_new, k8->max_end);
+        };
+        L.kscratch = g.take(std::max(scratch((int)T, k8->max_new), scratch(batch, 1)) + 16);
     }
     L.total = g.off;
     return L;
@@ -404,6 +410,7 @@ int run_layers(const hra_dims& d, const hra_weights& w, const hra_kv_cache& kv, 
         a.max_new = max_new;
         a.max_len = k8->max_end;
         a.scratch = P.at<uint8_t>(L.kscratch);
+        kv8_set_reach(a, k8->reach);
         return launch_kv8_attention(a, st);
     };
     if (k8 != nullptr)
@@ -630,7 +637,8 @@ int prefill_impl(const hra_dims* dims, const hra_weights* weights, const int32_t
                  const int32_t* start_pos, int32_t batch, int32_t max_len, const hra_kv_cache* kv,
                  void* last_hidden_dev, void* workspace, size_t workspace_bytes, uint32_t flags, void* stream,
                  const hra_fp8_layer* fp8 = nullptr, float* amax = nullptr, bool validate_only = false,
-                 const hra_nvfp4_layer* nv4 = nullptr, const hra_kv8_cache* kv8 = nullptr) {
+                 const hra_nvfp4_layer* nv4 = nullptr, const hra_kv8_cache* kv8 = nullptr,
+                 const hra_kv8_reach* reach = nullptr) {
     if (dims == nullptr || weights == nullptr || tokens_dev == nullptr || seq_lens == nullptr ||
         (kv == nullptr && kv8 == nullptr))
         return HRA_ERR_INVALID_ARG;
@@ -641,6 +649,8 @@ int prefill_impl(const hra_dims* dims, const hra_weights* weights, const int32_t
     if (kv8 != nullptr) {
         const int rc = kv8_for_model(d, kv8, paged);
         if (rc != HRA_OK) return rc;
+        const int rr = kv8_reach_check(reach, batch);
+        if (rr != HRA_OK) return rr;
         kv = &paged;
     }
     if (!aligned16(weights->embed) || !weights_ok(d, weights) || (kv8 == nullptr && !kv_ok(kv)) ||
@@ -685,7 +695,7 @@ int prefill_impl(const hra_dims* dims, const hra_weights* weights, const int32_t
                 if (!aligned16(f.codes[p]) || f.scales[p] == nullptr) return HRA_ERR_INVALID_ARG;
         }
     }
-    const Kv8Pass pass{kv8, max_len, max_end};
+    const Kv8Pass pass{kv8, max_len, max_end, reach};
     const Kv8Pass* k8 = kv8 != nullptr ? &pass : nullptr;
     const Layout L = backbone_layout(d, batch, (int)T, max_end, max_end - 1, fp8 != nullptr, nv4 != nullptr, k8);
     if (workspace_bytes < L.total) return HRA_ERR_WORKSPACE;
@@ -709,23 +719,36 @@ int prefill_impl(const hra_dims* dims, const hra_weights* weights, const int32_t
 
 }  // namespace
 
-size_t hra_prefill_kv8_workspace_size(const hra_dims* dims, const hra_kv8_cache* cache, int32_t batch,
-                                      int32_t total_tokens, int32_t max_len, int32_t max_end) {
+size_t hra_prefill_kv8_reach_workspace_size(const hra_dims* dims, const hra_kv8_cache* cache, int32_t batch,
+                                            int32_t total_tokens, int32_t max_len, int32_t max_end,
+                                            const hra_kv8_reach* reach) {
     hra_kv_cache paged{};
     if (!dims_ok(dims) || kv8_for_model(*dims, cache, paged) != HRA_OK || batch < 1 || total_tokens < batch ||
-        max_len < 1 || max_end < 1 || max_end > paged.n_slots)
+        max_len < 1 || max_end < 1 || max_end > paged.n_slots || kv8_reach_check(reach, batch) != HRA_OK)
         return 0;
-    const Kv8Pass pass{cache, max_len, max_end};
+    const Kv8Pass pass{cache, max_len, max_end, reach};
     return backbone_layout(*dims, batch, total_tokens, max_end, max_end - 1, false, false, &pass).total;
+}
+size_t hra_prefill_kv8_workspace_size(const hra_dims* dims, const hra_kv8_cache* cache, int32_t batch,
+                                      int32_t total_tokens, int32_t max_len, int32_t max_end) {
+    return hra_prefill_kv8_reach_workspace_size(dims, cache, batch, total_tokens, max_len, max_end, nullptr);
 }
 
 int hra_prefill_kv8(const hra_dims* dims, const hra_weights* weights, const int32_t* tokens_dev,
                     const int32_t* seq_lens, const int32_t* start_pos, int32_t batch, int32_t max_len,
                     const hra_kv8_cache* cache, void* last_hidden_dev, void* workspace, size_t workspace_bytes,
                     uint32_t flags, void* stream) {
+    return hra_prefill_kv8_reach(dims, weights, tokens_dev, seq_lens, start_pos, batch, max_len, cache, nullptr,
+                                 last_hidden_dev, workspace, workspace_bytes, flags, stream);
+}
+
+int hra_prefill_kv8_reach(const hra_dims* dims, const hra_weights* weights, const int32_t* tokens_dev,
+                          const int32_t* seq_lens, const int32_t* start_pos, int32_t batch, int32_t max_len,
+                          const hra_kv8_cache* cache, const hra_kv8_reach* reach, void* last_hidden_dev,
+                          void* workspace, size_t workspace_bytes, uint32_t flags, void* stream) {
     if (cache == nullptr) return HRA_ERR_INVALID_ARG;
     return prefill_impl(dims, weights, tokens_dev, seq_lens, start_pos, batch, max_len, nullptr, last_hidden_dev,
-                        workspace, workspace_bytes, flags, stream, nullptr, nullptr, false, nullptr, cache);
+                        workspace, workspace_bytes, flags, stream, nullptr, nullptr, false, nullptr, cache, reach);
 }
 
 int hra_prefill(const hra_dims* dims, const hra_weights* weights, const int32_t* tokens_dev,
@@ -907,7 +930,7 @@ namespace {
 int decode_impl(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev, const int32_t* pos_host,
                 int32_t* pos_dev, int32_t pos_bound, int advance, int32_t batch, const hra_kv_cache* kv,
                 void* hidden_dev, void* workspace, size_t workspace_bytes, void* stream, bool validate_only = false,
-                const hra_kv8_cache* kv8 = nullptr) {
+                const hra_kv8_cache* kv8 = nullptr, const hra_kv8_reach* reach = nullptr) {
     if (dims == nullptr || weights == nullptr || in_emb_dev == nullptr || (kv == nullptr && kv8 == nullptr) ||
         (pos_host == nullptr && pos_dev == nullptr))
         return HRA_ERR_INVALID_ARG;
@@ -918,6 +941,8 @@ int decode_impl(const hra_dims* dims, const hra_weights* weights, const void* in
     if (kv8 != nullptr) {
         const int rc = kv8_for_model(d, kv8, paged);
         if (rc != HRA_OK) return rc;
+        const int rr = kv8_reach_check(reach, batch);
+        if (rr != HRA_OK) return rr;
         kv = &paged;
     }
     if (!weights_ok(d, weights) || (kv8 == nullptr && !kv_ok(kv)) || !aligned16(in_emb_dev) || !aligned16(hidden_dev) ||
@@ -942,7 +967,7 @@ int decode_impl(const hra_dims* dims, const hra_weights* weights, const void* in
         meta.advance = advance ? 1 : 0;
         max_pos = pos_bound;
     }
-    const Kv8Pass whole{kv8, 1, kv->n_slots}, pass{kv8, 1, max_pos + 1};
+    const Kv8Pass whole{kv8, 1, kv->n_slots, reach}, pass{kv8, 1, max_pos + 1, reach};
     const Layout L = backbone_layout(d, batch, batch, batch, kv->n_slots - 1, false, false, kv8 ? &whole : nullptr);
     if (workspace_bytes < L.total) return HRA_ERR_WORKSPACE;
     if (validate_only) return HRA_OK;
@@ -964,27 +989,48 @@ int decode_impl(const hra_dims* dims, const hra_weights* weights, const void* in
 
 }  // namespace
 
-size_t hra_decode_kv8_workspace_size(const hra_dims* dims, const hra_kv8_cache* cache, int32_t batch) {
+size_t hra_decode_kv8_reach_workspace_size(const hra_dims* dims, const hra_kv8_cache* cache, int32_t batch,
+                                           const hra_kv8_reach* reach) {
     hra_kv_cache paged{};
-    if (!dims_ok(dims) || kv8_for_model(*dims, cache, paged) != HRA_OK || batch < 1) return 0;
-    const Kv8Pass pass{cache, 1, paged.n_slots};
+    if (!dims_ok(dims) || kv8_for_model(*dims, cache, paged) != HRA_OK || batch < 1 ||
+        kv8_reach_check(reach, batch) != HRA_OK)
+        return 0;
+    const Kv8Pass pass{cache, 1, paged.n_slots, reach};
     return backbone_layout(*dims, batch, batch, batch, paged.n_slots - 1, false, false, &pass).total;
+}
+size_t hra_decode_kv8_workspace_size(const hra_dims* dims, const hra_kv8_cache* cache, int32_t batch) {
+    return hra_decode_kv8_reach_workspace_size(dims, cache, batch, nullptr);
 }
 
 int hra_decode_kv8(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev, const int32_t* pos,
                    int32_t batch, const hra_kv8_cache* cache, void* hidden_dev, void* workspace,
                    size_t workspace_bytes, void* stream) {
+    return hra_decode_kv8_reach(dims, weights, in_emb_dev, pos, batch, cache, nullptr, hidden_dev, workspace, workspace_bytes,
+                                stream);
+}
+
+int hra_decode_kv8_reach(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev, const int32_t* pos,
+                         int32_t batch, const hra_kv8_cache* cache, const hra_kv8_reach* reach, void* hidden_dev,
+                         void* workspace, size_t workspace_bytes, void* stream) {
     if (pos == nullptr || cache == nullptr) return HRA_ERR_INVALID_ARG;
     return decode_impl(dims, weights, in_emb_dev, pos, nullptr, 0, 0, batch, nullptr, hidden_dev, workspace,
-                       workspace_bytes, stream, false, cache);
+                       workspace_bytes, stream, false, cache, reach);
 }
 
 int hra_decode_dev_kv8(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev, int32_t* pos_dev,
                        int32_t pos_bound, int32_t advance, int32_t batch, const hra_kv8_cache* cache, void* hidden_dev,
                        void* workspace, size_t workspace_bytes, void* stream) {
+    return hra_decode_dev_kv8_reach(dims, weights, in_emb_dev, pos_dev, pos_bound, advance, batch, cache, nullptr, hidden_dev,
+                                    workspace, workspace_bytes, stream);
+}
+
+int hra_decode_dev_kv8_reach(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev,
+                             int32_t* pos_dev, int32_t pos_bound, int32_t advance, int32_t batch,
+                             const hra_kv8_cache* cache, const hra_kv8_reach* reach, void* hidden_dev,
+                             void* workspace, size_t workspace_bytes, void* stream) {
     if (pos_dev == nullptr || cache == nullptr) return HRA_ERR_INVALID_ARG;
     return decode_impl(dims, weights, in_emb_dev, nullptr, pos_dev, pos_bound, advance, batch, nullptr, hidden_dev,
-                       workspace, workspace_bytes, stream, false, cache);
+                       workspace, workspace_bytes, stream, false, cache, reach);
 }
 
 int hra_decode(const hra_dims* dims, const hra_weights* weights, const void* in_emb_dev, const int32_t* pos,
@@ -1155,11 +1201,11 @@ int ar_frame_impl(const hra_dims* dims, const hra_weights* weights, const void* 
                  const uint64_t* seeds_dev, void* hidden_dev, int32_t* pos_dev, int32_t pos_bound, int32_t batch,
                  const hra_kv_cache* kv, int32_t* codes_dev, void* next_emb_dev, int32_t* done_dev, void* backbone_ws,
                  size_t backbone_ws_bytes, void* codebook_ws, size_t codebook_ws_bytes, void* stream,
-                 const hra_kv8_cache* kv8 = nullptr) {
+                 const hra_kv8_cache* kv8 = nullptr, const hra_kv8_reach* reach = nullptr) {
     if (pos_dev == nullptr) return HRA_ERR_INVALID_ARG;
     // both steps' arguments are checked before anything is enqueued
     int rc = decode_impl(dims, weights, next_emb_dev, nullptr, pos_dev, pos_bound, 1, batch, kv, hidden_dev,
-                         backbone_ws, backbone_ws_bytes, stream, /*validate_only=*/true, kv8);
+                         backbone_ws, backbone_ws_bytes, stream, /*validate_only=*/true, kv8, reach);
     if (rc != HRA_OK) return rc;
     rc = codebook_impl(dims, hidden_dev, head_w_dev, code_emb_dev, state_dev, eoc_bias_dev, sampling, seeds_dev, batch,
                        codes_dev, next_emb_dev, done_dev, nullptr, codebook_ws, codebook_ws_bytes, stream, true);
@@ -1168,7 +1214,7 @@ int ar_frame_impl(const hra_dims* dims, const hra_weights* weights, const void* 
                        codes_dev, next_emb_dev, done_dev, nullptr, codebook_ws, codebook_ws_bytes, stream, false);
     if (rc != HRA_OK) return rc;
     return decode_impl(dims, weights, next_emb_dev, nullptr, pos_dev, pos_bound, 1, batch, kv, hidden_dev,
-                       backbone_ws, backbone_ws_bytes, stream, false, kv8);
+                       backbone_ws, backbone_ws_bytes, stream, false, kv8, reach);
 }
 
 }  // namespace
@@ -1189,10 +1235,22 @@ int hra_ar_frame_kv8(const hra_dims* dims, const hra_weights* weights, const voi
                      int32_t pos_bound, int32_t batch, const hra_kv8_cache* cache, int32_t* codes_dev,
                      void* next_emb_dev, int32_t* done_dev, void* backbone_ws, size_t backbone_ws_bytes,
                      void* codebook_ws, size_t codebook_ws_bytes, void* stream) {
+    return hra_ar_frame_kv8_reach(dims, weights, head_w_dev, code_emb_dev, state_dev, eoc_bias_dev, sampling, seeds_dev,
+                                  hidden_dev, pos_dev, pos_bound, batch, cache, nullptr, codes_dev, next_emb_dev, done_dev,
+                                  backbone_ws, backbone_ws_bytes, codebook_ws, codebook_ws_bytes, stream);
+}
+
+int hra_ar_frame_kv8_reach(const hra_dims* dims, const hra_weights* weights, const void* head_w_dev,
+                           const void* code_emb_dev, hra_delay_state* state_dev, const float* eoc_bias_dev,
+                           const hra_sampling* sampling, const uint64_t* seeds_dev, void* hidden_dev,
+                           int32_t* pos_dev, int32_t pos_bound, int32_t batch, const hra_kv8_cache* cache,
+                           const hra_kv8_reach* reach, int32_t* codes_dev, void* next_emb_dev, int32_t* done_dev,
+                           void* backbone_ws, size_t backbone_ws_bytes, void* codebook_ws,
+                           size_t codebook_ws_bytes, void* stream) {
     if (cache == nullptr) return HRA_ERR_INVALID_ARG;
     return ar_frame_impl(dims, weights, head_w_dev, code_emb_dev, state_dev, eoc_bias_dev, sampling, seeds_dev,
                          hidden_dev, pos_dev, pos_bound, batch, nullptr, codes_dev, next_emb_dev, done_dev, backbone_ws,
-                         backbone_ws_bytes, codebook_ws, codebook_ws_bytes, stream, cache);
+                         backbone_ws_bytes, codebook_ws, codebook_ws_bytes, stream, cache, reach);
 }
 
 size_t hra_linear_workspace_size(int32_t M, int32_t N, int32_t K, int32_t epilogue, int32_t split_k) {

@@ -365,8 +365,16 @@ struct Kv8AttnArgs {
     float scale_log2;       // softmax scale * log2(e)
     int batch, total_rows, nq, max_new, max_len;
     void* scratch;
+    int window, sinks;      // a token sees the last `window` positions up to its own and the first `sinks`; window 0: all
+    // groups of rows that share the pages of a prefix (groups 0: none), see hra_kv8_reach
+    const int32_t* group_cu;
+    const int32_t* prefix;
+    int groups, max_prefix, max_own;
 };
 size_t kv8_attention_scratch_bytes(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int max_len);
+// ... and with shared prefixes
+size_t kv8_shared_scratch_bytes(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int max_len, int groups,
+                                int max_prefix, int max_own);
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st);
 // the tcgen05 form (kv8_prompt.cu) for sequences with more than short_rows (position, head) rows a kv head
 size_t kv8_prompt_scratch_bytes(const Kv8View& c, int batch, int total_rows, int G, int max_len);
@@ -391,6 +399,7 @@ struct Kv8PagesArgs {
     long long code_page;    // bytes of a page's codes and of its scales
     int scale_page;
     int n_layers, n_pages, page_shift, rows, max_pages;
+    int window, sinks;      // update: pages that no later token sees are dropped; window 0: none
 };
 size_t kv8_pages_scratch_bytes(int rows, int max_pages, int n_pages);
 cudaError_t launch_kv8_update(const Kv8PagesArgs& a, cudaStream_t st);

@@ -20,6 +20,7 @@
 namespace hra {
 
 constexpr int kKv8Block = 16;       // tokens that share a scale
+constexpr int kKv8MaxGroups = 1024; // of rows that share a prefix
 constexpr float kKv8Top = 448.0f;   // largest E4M3 value
 
 // One layer of the cache.
@@ -68,6 +69,24 @@ KV8_HD uint32_t kv8_scale_bits(uint32_t a_bits) {
 KV8_HD int kv8_turns_left(int blk, int blk1, int step, int most) {
     const int left = blk < blk1 ? (blk1 - blk - 1) / step + 1 : 0;
     return left < most ? left : most;
+}
+// Positions that a window hides.  A token at position p sees those of [0, p] from p - window + 1 on and those below `sinks`; of
+// tokens from position `first` on, the units of `per` positions that hold anything they see are 0 .. from - 1 and then
+// from + by, from + by + 1, ...  window 0: everything is seen.
+struct Kv8Skip {
+    int from, by;
+};
+KV8_HD Kv8Skip kv8_skip(int first, int window, int sinks, int per) {
+    const int near = window > 0 && first >= window ? (first - window + 1) / per : 0;
+    const int keep = (sinks + per - 1) / per;
+    const int from = near < keep ? near : keep;
+    return {from, near - from};
+}
+KV8_HD int kv8_unit_at(const Kv8Skip& s, int i) { return i < s.from ? i : i + s.by; }
+// Most positions that tokens within a span of `tokens` see of max_len.
+KV8_HD int kv8_most_seen(int max_len, int window, int sinks, int tokens) {
+    const long long n = (long long)window + sinks + tokens;
+    return window > 0 && n < max_len ? (int)n : max_len;
 }
 // Most blocks of 16 that n >= 1 consecutive positions can touch.
 KV8_HD int kv8_max_blocks(int n) { return (n + kKv8Block - 2) / kKv8Block + 1; }

@@ -44,6 +44,28 @@ int kv8_check(const hra_kv8_cache* c) {
     return HRA_OK;
 }
 
+int kv8_reach_check(const hra_kv8_reach* r, int batch) {
+    if (r == nullptr) return HRA_OK;
+    if (r->window < 0 || r->sinks < 0 || (r->window == 0 && r->sinks != 0) || r->groups < 0) return HRA_ERR_INVALID_ARG;
+    if (r->window > (1 << 30) || r->sinks > (1 << 30)) return HRA_ERR_RANGE;
+    if (r->groups == 0) return HRA_OK;
+    if (r->window > 0 || r->groups > kKv8MaxGroups) return HRA_ERR_UNSUPPORTED;
+    if (!aligned(r->group_cu_dev, 4) || !aligned(r->prefix_dev, 4) || r->groups > batch || r->max_prefix < 0 || r->max_own < 0)
+        return HRA_ERR_INVALID_ARG;
+    return HRA_OK;
+}
+
+void kv8_set_reach(Kv8AttnArgs& a, const hra_kv8_reach* r) {
+    if (r == nullptr) return;
+    a.window = r->window;
+    a.sinks = r->sinks;
+    a.groups = r->groups;
+    a.group_cu = r->group_cu_dev;
+    a.prefix = r->prefix_dev;
+    a.max_prefix = r->max_prefix;
+    a.max_own = r->max_own;
+}
+
 Kv8View kv8_view(const hra_kv8_cache& c, int layer) {
     Kv8View v{};
     const long long codes = 2LL * c.n_kv_heads * c.page_size * c.head_dim;
@@ -77,11 +99,20 @@ int rows_check(const hra_kv8_cache& c, const int32_t* cu, const int32_t* per_row
     return HRA_OK;
 }
 
+size_t attention_scratch(const Kv8View& v, int batch, int total, int nq, int max_new, int max_len, const hra_kv8_reach* r) {
+    if (r == nullptr || r->groups == 0) return kv8_attention_scratch_bytes(v, batch, total, nq, max_new, max_len);
+    return kv8_shared_scratch_bytes(v, batch, total, nq, max_new, max_len, r->groups, r->max_prefix, r->max_own);
+}
+
 bool heads_dims_ok(int nq, int nkv) { return nq >= 1 && nq % nkv == 0 && nq / nkv <= 16; }
 
 int pages_impl(const hra_kv8_cache* cache, const int32_t* parents, const int32_t* room, int32_t* table_out,
-               int32_t* lens_out, int32_t* refs_out, void* workspace, size_t workspace_bytes, void* stream, bool update) {
-    const int rc = kv8_check(cache);
+               int32_t* lens_out, int32_t* refs_out, void* workspace, size_t workspace_bytes, void* stream, bool update,
+               const hra_kv8_reach* reach = nullptr) {
+    int rc = kv8_check(cache);
+    if (rc != HRA_OK) return rc;
+    if (reach != nullptr && reach->groups != 0) return HRA_ERR_INVALID_ARG;
+    rc = kv8_reach_check(reach, 0);
     if (rc != HRA_OK) return rc;
     const hra_kv8_cache& c = *cache;
     if (c.refs == nullptr || !aligned(table_out, 4) || !aligned(lens_out, 4) || !aligned(refs_out, 4) ||
@@ -123,6 +154,10 @@ int pages_impl(const hra_kv8_cache* cache, const int32_t* parents, const int32_t
     a.page_shift = v.page_shift;
     a.rows = c.rows;
     a.max_pages = c.max_pages;
+    if (reach != nullptr) {
+        a.window = reach->window;
+        a.sinks = reach->sinks;
+    }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return status(update ? launch_kv8_update(a, st) : launch_kv8_compact(a, st));
 }
@@ -162,18 +197,33 @@ int hra_kv8_append(const hra_kv8_cache* cache, int32_t layer, const void* k_dev,
     return status(launch_kv8_append(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-size_t hra_kv8_attention_workspace_size(const hra_kv8_cache* cache, int32_t batch, int32_t total_rows,
-                                        int32_t n_q_heads, int32_t max_new, int32_t max_len) {
+size_t hra_kv8_attention_reach_workspace_size(const hra_kv8_cache* cache, int32_t batch, int32_t total_rows,
+                                              int32_t n_q_heads, int32_t max_new, int32_t max_len,
+                                              const hra_kv8_reach* reach) {
     if (kv8_check(cache) != HRA_OK || batch < 1 || batch > cache->rows || total_rows < 0 || max_new < 0 ||
         max_new > total_rows || max_len < 0 || !heads_dims_ok(n_q_heads, cache->n_kv_heads))
         return 0;
-    return 256 + kv8_attention_scratch_bytes(kv8_view(*cache, 0), batch, total_rows, n_q_heads, max_new, max_len);
+    if (kv8_reach_check(reach, batch) != HRA_OK) return 0;
+    return 256 + attention_scratch(kv8_view(*cache, 0), batch, total_rows, n_q_heads, max_new, max_len, reach);
+}
+size_t hra_kv8_attention_workspace_size(const hra_kv8_cache* cache, int32_t batch, int32_t total_rows,
+                                        int32_t n_q_heads, int32_t max_new, int32_t max_len) {
+    return hra_kv8_attention_reach_workspace_size(cache, batch, total_rows, n_q_heads, max_new, max_len, nullptr);
 }
 
 int hra_kv8_attention(const hra_kv8_cache* cache, int32_t layer, const void* q_dev, int64_t q_row_stride,
                       int32_t n_q_heads, float scale, const int32_t* cu_dev, const int32_t* kv_len_dev, int32_t batch,
                       int32_t total_rows, int32_t max_new, int32_t max_len, void* out_dev, void* workspace,
                       size_t workspace_bytes, void* stream) {
+    return hra_kv8_attention_reach(cache, layer, q_dev, q_row_stride, n_q_heads, scale, cu_dev, kv_len_dev, batch, total_rows,
+                                   max_new, max_len, nullptr, out_dev, workspace, workspace_bytes, stream);
+}
+
+int hra_kv8_attention_reach(const hra_kv8_cache* cache, int32_t layer, const void* q_dev, int64_t q_row_stride,
+                            int32_t n_q_heads, float scale, const int32_t* cu_dev, const int32_t* kv_len_dev,
+                            int32_t batch, int32_t total_rows, int32_t max_new, int32_t max_len,
+                            const hra_kv8_reach* reach, void* out_dev, void* workspace, size_t workspace_bytes,
+                            void* stream) {
     int rc = kv8_check(cache);
     if (rc != HRA_OK) return rc;
     const hra_kv8_cache& c = *cache;
@@ -182,13 +232,15 @@ int hra_kv8_attention(const hra_kv8_cache* cache, int32_t layer, const void* q_d
     rc = rows_check(c, cu_dev, kv_len_dev, batch, total_rows, max_new);
     if (rc != HRA_OK) return rc;
     if (max_len < 0 || max_len > (long long)c.max_pages * c.page_size) return HRA_ERR_RANGE;
+    rc = kv8_reach_check(reach, batch);
+    if (rc != HRA_OK) return rc;
     if (total_rows == 0) return HRA_OK;
     if (!aligned(q_dev, 16) || !aligned(out_dev, 16) || q_row_stride < (int64_t)n_q_heads * c.head_dim ||
         q_row_stride % 8 != 0 || !aligned(workspace, 16))
         return HRA_ERR_INVALID_ARG;
     Kv8AttnArgs a{};
     a.view = kv8_view(c, layer);
-    if (workspace_bytes < 256 + kv8_attention_scratch_bytes(a.view, batch, total_rows, n_q_heads, max_new, max_len))
+    if (workspace_bytes < 256 + attention_scratch(a.view, batch, total_rows, n_q_heads, max_new, max_len, reach))
         return HRA_ERR_WORKSPACE;
     // q is read again behind the output of a row with a NaN (kv8_row_again)
     const size_t q_row = 2 * (size_t)n_q_heads * c.head_dim;
@@ -206,6 +258,7 @@ int hra_kv8_attention(const hra_kv8_cache* cache, int32_t layer, const void* q_d
     a.max_new = max_new;
     a.max_len = max_len;
     a.scratch = workspace;
+    kv8_set_reach(a, reach);
     return status(launch_kv8_attention(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -219,6 +272,13 @@ int hra_kv8_update(const hra_kv8_cache* cache, const int32_t* parents_dev, const
                    void* stream) {
     return pages_impl(cache, parents_dev, room_dev, table_out, lens_out, refs_out, workspace, workspace_bytes, stream,
                       true);
+}
+
+int hra_kv8_update_reach(const hra_kv8_cache* cache, const int32_t* parents_dev, const int32_t* room_dev,
+                         const hra_kv8_reach* reach, int32_t* table_out, int32_t* lens_out, int32_t* refs_out,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+    return pages_impl(cache, parents_dev, room_dev, table_out, lens_out, refs_out, workspace, workspace_bytes, stream,
+                      true, reach);
 }
 
 int hra_kv8_compact(const hra_kv8_cache* cache, int32_t* table_out, int32_t* lens_out, int32_t* refs_out,

@@ -43,6 +43,7 @@ namespace hra {
 
 namespace {
 
+enum { kAll, kWindow };   // the positions that tokens see
 constexpr int kWarps = 4;
 constexpr int kPair = 2;        // blocks a warp works on at once: two chains of MMAs and shuffles instead of one
 constexpr int kStages = 2;      // pairs of a warp in shared memory: 12 warps an SM; with 3, 8 warps fit (121 us against 112)
@@ -114,11 +115,14 @@ __device__ __noinline__ void look_again(const SplitArgs& s, int b, int head, int
     const int qi = r / s.G, hq = r - qi * s.G;
     const int before = min(c.max_pages << c.page_shift, max(0, s.a.kv_len[b])) - n;   // positions before the first token
     const bf16* q = s.a.q + (long long)(row0 + qi) * s.a.row_stride + (long long)(head * s.G + hq) * c.head_dim;
-    kv8_row_again(c, q, b, head, before + qi + 1, before + n, d, 2, s.a.scale_log2, dst);
+    const int lo = s.a.window > 0 ? before + qi + 1 - s.a.window : 0;
+    kv8_row_again(c, q, b, head, before + qi + 1, before + n, d, 2, s.a.scale_log2, dst, lo, s.a.sinks, max(0, lo - qi));
 }
 
-// NG x 8 rows of (position, head) pairs.  ONE: sequences of one new token, whose rows all see the same keys.
-template <int HD, int NG, bool ONE>
+// NG x 8 rows of (position, head) pairs.  ONE: sequences of one new token, whose rows all see the same keys.  MODE: all
+// positions, or those of a window and the sinks: then units, blocks and lengths below count what some token of the sequence
+// sees, kv8_unit_at says which block that is, and only blocks at the window's edge look at its border.
+template <int HD, int NG, bool ONE, int MODE>
 __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_constant__ CUtensorMap codes_map,
                                                                   const __grid_constant__ SplitArgs s) {
     pdl_launch();
@@ -146,6 +150,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
     }
     __syncthreads();
     auto length = [&](int b) { return min(room, max(0, a.kv_len[b])); };
+    auto skipped = [&](int len, int n) {   // blocks that no token sees of a sequence of `len` positions, n of them new
+        return MODE == kWindow ? kv8_skip(len - n, a.window, a.sinks, kKv8Block) : Kv8Skip{0, 0};
+    };
 
     // ---- this CTA's share
     long long u = 0, u_end = 1;
@@ -162,7 +169,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
                 int row0, n;
                 kv8_rows(a.cu, b, a.total_rows, row0, n);
                 // a sequence with new tokens but no keys has one unit: its rows get 0
-                if (n > 0 && n <= s.max_rows / G) units = max(1, (length(b) + kUnit - 1) / kUnit);
+                if (n > 0 && n <= s.max_rows / G) {
+                    const int len = length(b);
+                    units = max(1, (len - skipped(len, n).by * kKv8Block + kUnit - 1) / kUnit);
+                }
                 before[b] = units;
             }
             mine += units;
@@ -241,7 +251,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
             raise_error(c.err, HRA_DEVERR_POS_RANGE);
         const int q_n = min(min(ROWS / G, n), a.max_new);   // tokens beyond max_new get no output
         const int keys = max(0, kv_len - n + q_n);     // positions below the last of them
-        const int blk1 = min((keys + kKv8Block - 1) / kKv8Block, i1 >= (1 << 28) ? 1 << 28 : i1 * (kWarps * kPair));
+        const Kv8Skip skip = skipped(kv_len, n);
+        auto first_key = [&](int x) { return (MODE == kAll ? x : kv8_unit_at(skip, x)) * kKv8Block; };   // of block x
+        const int blk1 = min((keys + kKv8Block - 1) / kKv8Block - skip.by, i1 >= (1 << 28) ? 1 << 28 : i1 * (kWarps * kPair));
+        const int lo0 = kv_len - n + 1 - a.window;     // window: the first position of the first token's
         int blk = (i0 * kWarps + warp) * kPair;
         constexpr int STEP = kWarps * kPair;
 
@@ -255,8 +268,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
 #pragma unroll
             for (int y = 0; y < kPair; ++y) {
                 r.p[y] = -2;
-                if (x + y < blk1) {   // (x + y) * 16 < keys <= max_pages * page_size
-                    const int page = table[(x + y) * kKv8Block >> c.page_shift];
+                if (x + y < blk1) {   // first_key(x + y) < keys <= max_pages * page_size
+                    const int page = table[first_key(x + y) >> c.page_shift];
                     r.p[y] = page >= 0 && page < c.n_pages ? page : -1;
                 }
             }
@@ -271,7 +284,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
                 const int page = pages.p[y];
                 bad_page |= page == -1;
                 boxes += page >= 0 ? 2 : 0;
-                const int slot0 = ((x0 + y) * kKv8Block) & (c.page_size - 1);
+                const int slot0 = first_key(x0 + y) & (c.page_size - 1);
                 const float* sp = head_scales + (long long)max(page, 0) * page_scales + (slot0 / kKv8Block);
                 const uint32_t to = smem_u32(ring_scales + st * R::SCALES + y * 32 * 8);
                 if (page >= 0) {
@@ -290,7 +303,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
 #pragma unroll
                 for (int y = 0; y < kPair; ++y) {
                     if (pages.p[y] >= 0) {   // rows of the map are counted in 32 bits (checked before the launch)
-                        const int row = pages.p[y] * page_rows + head * c.page_size + (((x0 + y) * kKv8Block) & (c.page_size - 1));
+                        const int row = pages.p[y] * page_rows + head * c.page_size + (first_key(x0 + y) & (c.page_size - 1));
                         const uint32_t to = smem_u32(ring + st * R::CODES + 2 * y * R::BLOCK);
                         tma_load_2d(to, &codes_map, bar, 0, row);
                         tma_load_2d(to + R::BLOCK, &codes_map, bar, 0, row + v_rows);
@@ -412,6 +425,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
 
             float sv[kPair][2][4];
             float2 sc[kPair];
+            int key0[kPair];
+#pragma unroll
+            for (int y = 0; y < kPair; ++y) key0[y] = first_key(blk + y);
 #pragma unroll
             for (int y = 0; y < kPair; ++y) {
                 sc[y] = *reinterpret_cast<const float2*>(scales + y * 32 * 8);
@@ -454,10 +470,18 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
                 for (int y = 0; y < kPair; ++y) {
                     const float coef = q_unscale[x] * sc[y].x;
                     // a scale of -1: the block is absent
-                    const int lim = sc[y].x >= 0.f ? limit[x] - (blk + y) * kKv8Block : 0;
+                    const int lim = sc[y].x >= 0.f ? limit[x] - key0[y] : 0;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         z[y][e] = (e & 1 ? key_1 : key_0) + 8 * (e >> 1) < lim ? sv[y][e >> 1][2 * x + (e & 1)] * coef : -INFINITY;
+                    if (MODE == kWindow && key0[y] < lo0 + q_n - 1 && key0[y] + kKv8Block > a.sinks) {   // some row's border
+                        const int lo = limit[x] - a.window - key0[y], sinks = a.sinks - key0[y];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = (e & 1 ? key_1 : key_0) + 8 * (e >> 1);
+                            if (k < lo && k >= sinks) z[y][e] = -INFINITY;
+                        }
+                    }
                     mx[y] = fmaxf(fmaxf(z[y][0], z[y][1]), fmaxf(z[y][2], z[y][3]));
                 }
                 float top = mx[0], Top = mx[0] + ev[0];
@@ -525,13 +549,22 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
                     }
                 }
                 // keys that do not count: whatever their slots hold (a NaN times a weight of 0 is none)
-                const int left = sc[y].x >= 0.f ? keys - (blk + y) * kKv8Block : 0;
+                const int left = sc[y].x >= 0.f ? keys - key0[y] : 0;
                 if (left < kKv8Block) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if ((i & 1 ? key_1 : key_0) + 8 * (i >> 1) >= left)
 #pragma unroll
                             for (int j = 0; j < HD / 32; ++j) vw[i][j] = 0u;
+                }
+                if (MODE == kWindow && key0[y] < lo0 && key0[y] + kKv8Block > a.sinks) {   // behind every row's window
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = key0[y] + (i & 1 ? key_1 : key_0) + 8 * (i >> 1);
+                        if (k < lo0 && k >= a.sinks)
+#pragma unroll
+                            for (int j = 0; j < HD / 32; ++j) vw[i][j] = 0u;
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < HD / 32; ++j) {
@@ -714,7 +747,7 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ S
 
 int split_grid() { return 3 * device_sm_count(); }
 
-template <int HD, int NG, bool ONE>
+template <int HD, int NG, bool ONE, int MODE>
 cudaError_t launch_ng(const SplitArgs& s, cudaStream_t st) {
     constexpr int join = kWarps * 8 * NG * (HD + 3) * 4;
     constexpr int smem = (Ring<HD>::BYTES > join ? Ring<HD>::BYTES : join) + 1024;   // aligned up to 1024 bytes
@@ -726,24 +759,25 @@ cudaError_t launch_ng(const SplitArgs& s, cudaStream_t st) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(kv8_attn_kernel<HD, NG, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(kv8_attn_kernel<HD, NG, ONE, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
     if (s.whole) {
         const dim3 grid((unsigned)s.a.view.n_kv, (unsigned)s.a.batch);
-        HRA_LAUNCH((kv8_attn_kernel<HD, NG, ONE>), grid, dim3(kWarps * 32), smem, st, map, s);
+        HRA_LAUNCH((kv8_attn_kernel<HD, NG, ONE, MODE>), grid, dim3(kWarps * 32), smem, st, map, s);
         return cudaGetLastError();
     }
     const dim3 grid((unsigned)split_grid());
-    HRA_LAUNCH((kv8_attn_kernel<HD, NG, ONE>), grid, dim3(kWarps * 32), smem, st, map, s);
+    HRA_LAUNCH((kv8_attn_kernel<HD, NG, ONE, MODE>), grid, dim3(kWarps * 32), smem, st, map, s);
     HRA_LAUNCH((kv8_join_kernel<HD, NG, ONE>), grid, dim3(256), 0, st, s);
     return cudaGetLastError();
 }
 
 template <int HD, int NG>
 cudaError_t launch_tokens(const SplitArgs& s, cudaStream_t st) {
-    return s.a.max_new == 1 ? launch_ng<HD, NG, true>(s, st) : launch_ng<HD, NG, false>(s, st);
+    if (s.a.window > 0) return s.a.max_new == 1 ? launch_ng<HD, NG, true, kWindow>(s, st) : launch_ng<HD, NG, false, kWindow>(s, st);
+    return s.a.max_new == 1 ? launch_ng<HD, NG, true, kAll>(s, st) : launch_ng<HD, NG, false, kAll>(s, st);
 }
 
 // One n = 8 column group while the rows of a tile fit it, else two.
@@ -767,13 +801,20 @@ size_t kv8_attention_scratch_bytes(const Kv8View& c, int batch, int total_rows, 
     return n;
 }
 
+size_t kv8_shared_scratch_bytes(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int max_len, int groups,
+                                int max_prefix, int max_own) {
+    (void)groups, (void)max_prefix, (void)max_own;
+    return kv8_attention_scratch_bytes(c, batch, total_rows, nq, max_new, max_len);
+}
+
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st) {
     const int G = a.nq / a.view.n_kv;
     const bool prompts = (long long)G * a.max_new > kShortRows;
     uint8_t* scratch = reinterpret_cast<uint8_t*>(a.scratch);
     if (prompts) {
         // short sequences go with the prompts unless they may hold many keys (and unless the counts say that there are none)
-        const int short_rows = a.max_len > kSerialKeys && (long long)a.batch * a.max_new != a.total_rows ? kShortRows : 0;
+        const int most = kv8_most_seen(a.max_len, a.window, a.sinks, kShortRows + 2 * kKv8Block);
+        const int short_rows = most > kSerialKeys && (long long)a.batch * a.max_new != a.total_rows ? kShortRows : 0;
         cudaError_t e = launch_kv8_prompt(a, short_rows, st);
         if (e != cudaSuccess || short_rows == 0) return e;
         scratch += (kv8_prompt_scratch_bytes(a.view, a.batch, a.total_rows, G, a.max_len) + 255) & ~size_t(255);
@@ -782,7 +823,7 @@ cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st) {
     s.a = a;
     s.G = G;
     s.max_rows = prompts ? kShortRows : 1 << 30;
-    s.whole = goes_whole(a.batch, a.max_len) ? 1 : 0;
+    s.whole = goes_whole(a.batch, kv8_most_seen(a.max_len, a.window, a.sinks, kShortRows + 2 * kKv8Block)) ? 1 : 0;
     s.desc = reinterpret_cast<SplitDesc*>(scratch);
     s.parts = reinterpret_cast<float*>(scratch + split_grid() * sizeof(SplitDesc));
     const bool one = column_groups(G, a.max_new) == 1;

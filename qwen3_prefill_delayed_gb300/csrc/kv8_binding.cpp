@@ -20,9 +20,9 @@ namespace {
 
 PyObject* g_error = nullptr;                            // HraError
 decltype(&hra_kv8_append) f_append = nullptr;
-decltype(&hra_kv8_attention) f_attend = nullptr;
-decltype(&hra_kv8_attention_workspace_size) f_attend_size = nullptr;
-decltype(&hra_kv8_update) f_update = nullptr;
+decltype(&hra_kv8_attention_reach) f_attend = nullptr;
+decltype(&hra_kv8_attention_reach_workspace_size) f_attend_size = nullptr;
+decltype(&hra_kv8_update_reach) f_update = nullptr;
 decltype(&hra_kv8_compact) f_compact = nullptr;
 decltype(&hra_status_string) f_status = nullptr;
 
@@ -56,6 +56,13 @@ int64_t row_stride(const at::Tensor& t, int64_t heads, int64_t head_dim, int ind
     return t.size(0) > 1 ? t.stride(0) : t.size(1) * head_dim;
 }
 const hra_kv8_cache* cache(PyObject* o) { return static_cast<const hra_kv8_cache*>(PyLong_AsVoidPtr(o)); }
+// None, or the address of a Kv8Reach's struct
+const hra_kv8_reach* reach_of(PyObject* o) {
+    if (o == Py_None) return nullptr;
+    void* p = PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred()) throw std::nullopt;
+    return static_cast<const hra_kv8_reach*>(p);
+}
 int integer(PyObject* o) {
     const long v = PyLong_AsLong(o);
     if (PyErr_Occurred()) throw std::nullopt;
@@ -152,11 +159,12 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// attend(cache, device, layer, q, cu, kv_len, max_new, max_len, scale, out or None, workspace or None, home, stream) -> out.
+// attend(cache, device, layer, q, cu, kv_len, max_new, max_len, scale, out or None, workspace or None, home, stream, reach or
+// None) -> out.
 // home: None for a workspace of the caller's; of the cache's own one the stream whose memory it is, and where that workspace is
 // too small, the answer is the size it has to have
 PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!counted(n, 13)) return nullptr;
+    if (!counted(n, 14)) return nullptr;
     return guarded([&]() -> PyObject* {
         const hra_kv8_cache* c = cache(a[0]);
         const int index = integer(a[1]);
@@ -172,6 +180,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (scale != 0.0 && static_cast<float>(scale) == 0.f) refuse("scale is below float32's smallest");   // 0: the default
         const bool own = a[11] != Py_None;
         const Stream st = stream_of(a[12], index);
+        const hra_kv8_reach* reach = reach_of(a[13]);
         void* ws = nullptr;
         size_t bytes = 0;
         if (a[10] != Py_None) {
@@ -185,7 +194,8 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         size_t need = 0;
         if (own) {
             on(index, [&] {
-                need = f_attend_size(c, static_cast<int32_t>(batch), static_cast<int32_t>(rows), static_cast<int32_t>(heads), max_new, max_len);
+                need = f_attend_size(c, static_cast<int32_t>(batch), static_cast<int32_t>(rows), static_cast<int32_t>(heads), max_new, max_len,
+                                     reach);
                 return 0;
             });
             // (0: the call below refuses the arguments)
@@ -208,7 +218,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         check(on(index, [&] {
                   return f_attend(c, layer, q.data_ptr(), stride, static_cast<int32_t>(heads), static_cast<float>(scale), pcu, pl,
-                                  static_cast<int32_t>(batch), static_cast<int32_t>(rows), max_new, max_len, out.data_ptr(),
+                                  static_cast<int32_t>(batch), static_cast<int32_t>(rows), max_new, max_len, reach, out.data_ptr(),
                                   ws, bytes, st.raw);
               }), "hra_kv8_attention");
         if (a[9] != Py_None) {
@@ -219,9 +229,10 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// pages(cache, device, update, parents or None, room or None, table, lens, refs, workspace, home (see attend), stream)
+// pages(cache, device, update, parents or None, room or None, table, lens, refs, workspace, home (see attend), stream, reach
+// or None)
 PyObject* pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!counted(n, 11)) return nullptr;
+    if (!counted(n, 12)) return nullptr;
     return guarded([&]() -> PyObject* {
         const hra_kv8_cache* c = cache(a[0]);
         const int index = integer(a[1]);
@@ -237,16 +248,17 @@ PyObject* pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
         on_device(w, index, "workspace");
         if (!w.is_contiguous()) refuse("workspace must be contiguous");
         const Stream st = stream_of(a[10], index);
+        const hra_kv8_reach* reach = reach_of(a[11]);
         if (a[9] != Py_None && away(a[9], st)) used_on(w, st.memory);
         check(on(index, [&] {
-                  return update ? f_update(c, parents, room, table, lens, refs, w.data_ptr(), w.nbytes(), st.raw)
+                  return update ? f_update(c, parents, room, reach, table, lens, refs, w.data_ptr(), w.nbytes(), st.raw)
                                 : f_compact(c, table, lens, refs, w.data_ptr(), w.nbytes(), st.raw);
               }), update ? "hra_kv8_update" : "hra_kv8_compact");
         Py_RETURN_NONE;
     });
 }
 
-// connect(HraError, append, attention, attention_workspace_size, update, compact, status_string): the library's entry points
+// connect(HraError, append, attention_reach, attention_reach_workspace_size, update_reach, compact, status_string): the library's entry points
 PyObject* connect(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!counted(n, 7)) return nullptr;
     void* p[6];

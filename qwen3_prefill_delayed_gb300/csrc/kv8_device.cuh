@@ -42,12 +42,19 @@ __device__ __forceinline__ float mantissa_of(float s) {
 
 // A V with a NaN at a position that some rows of a tile see and others do not: the tile's product carries it, by a weight of 0,
 // to the rows that do not.  Nothing on the way looks for that; an output that is a NaN is looked at here, by the thread that
-// wrote it: dims dim .. dim + n - 1 (n <= 32) of a row that sees positions [0, end) while its tile's last row sees
-// [0, keys).  Those with a NaN behind `end` are done again, from the definition.
+// wrote it: dims dim .. dim + n - 1 (n <= 32) of a row that sees positions [lo, end) and, below lo, [0, sinks), while its tile
+// holds those of [tile_lo, keys) and of [0, sinks).  Those with a NaN that the row does not see are done again, from the definition.
 [[maybe_unused]] static __device__ __noinline__ void kv8_row_again(const Kv8View& c, const bf16* q, int row, int head, int end,
-                                                                   int keys, int dim, int n, float scale_log2, bf16* out) {
+                                                                   int keys, int dim, int n, float scale_log2, bf16* out,
+                                                                   int lo = 0, int sinks = 0, int tile_lo = 0) {
     uint32_t dims = 0u;
-    for (int pos = max(0, end); pos < keys; ++pos) {
+    lo = max(0, lo);
+    sinks = min(sinks, lo);
+    for (int pos = max(sinks, tile_lo); pos < keys; ++pos) {
+        if (pos >= lo && pos < end) {
+            pos = end - 1;
+            continue;
+        }
         const int page = kv8_page_of(c, row, pos);
         if (page < 0) continue;
         const uint8_t* v = c.codes + kv8_code_at(c, page, 1, head, pos & (c.page_size - 1)) + dim;
@@ -60,7 +67,8 @@ __device__ __forceinline__ float mantissa_of(float s) {
     };
     float m = -INFINITY, l = 0.f, acc[32];
     for (int i = 0; i < n; ++i) acc[i] = 0.f;
-    for (int pos = 0; pos < end; ++pos) {
+    for (int seen = 0; seen < sinks + max(0, end - lo); ++seen) {
+        const int pos = seen < sinks ? seen : lo + seen - sinks;
         const int page = kv8_page_of(c, row, pos), slot = pos & (c.page_size - 1);
         if (page < 0) continue;
         const uint8_t* k = c.codes + kv8_code_at(c, page, 0, head, slot);

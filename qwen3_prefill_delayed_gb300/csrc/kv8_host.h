@@ -10,4 +10,9 @@ int kv8_check(const hra_kv8_cache* c);
 // The kernels' view of one layer.
 Kv8View kv8_view(const hra_kv8_cache& c, int layer);
 
+// HRA_OK, or the status a call of `batch` rows with this reach (null: every position) returns.
+int kv8_reach_check(const hra_kv8_reach* reach, int batch);
+// The reach in the kernels' terms.
+void kv8_set_reach(Kv8AttnArgs& a, const hra_kv8_reach* reach);
+
 }  // namespace hra

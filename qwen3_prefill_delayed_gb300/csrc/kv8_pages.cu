@@ -8,6 +8,8 @@
 //   Pages that no new row lists are free; rows then get fresh pages for room[b] more tokens.  Fresh pages
 //   are the lowest-numbered free ones, in (row, index) order, so the result is one function of the
 //   inputs.  When too few are free, or a row's table is too short, nothing changes at all.
+//   Where a window bounds what is seen, the pages of a row that no later token sees are dropped before all this: the row
+//   neither keeps them nor needs fresh ones in their place.
 // compact: with U pages in use, the i-th used page with number >= U (ascending) moves to the i-th free
 //   page with number < U.  Sources and destinations are disjoint, so the copies need no order.
 //
@@ -160,6 +162,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8
             }
         }
     };
+    // pages [gone_lo, gone_hi) of a row of `len` positions: behind the window of every later token and no sinks
+    const int gone_lo = (int)(((long long)a.sinks + P - 1) >> a.page_shift);
+    auto gone_hi = [&](int len) { return a.window > 0 && len >= a.window ? (len - a.window + 1) >> a.page_shift : 0; };
     // the pages each new row keeps, and how many fresh ones it needs: one warp a row
     bool too_long = false, wrong = false;
     for (int b = warp; b < R; b += team.kWarps) {
@@ -167,6 +172,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8
         const int more = p >= 0 && a.room ? max(0, a.room[b]) : 0;
         const long long ends = ((long long)len + more + P - 1) >> a.page_shift;
         const bool heir = p >= 0 && s.first[p] == b;
+        const int gone = gone_hi(len);
         too_long |= p >= 0 && ends > W;
         int need = 0;
         for (int i0 = 0; i0 < W; i0 += 32 * kCells) {
@@ -175,9 +181,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8
 #pragma unroll
             for (int c = 0; c < kCells; ++c) {
                 const int i = i0 + 32 * c + lane;
-                const bool keep = old[c] >= 0 && (heir || i < (len >> a.page_shift));
+                const bool out = i >= gone_lo && i < gone;
+                const bool keep = !out && old[c] >= 0 && (heir || i < (len >> a.page_shift));
                 if (keep) atomicAdd(&s.refs[old[c]], 1);
-                need += __popc(__ballot_sync(0xffffffffu, p >= 0 && i < ends && i < W && !keep));
+                need += __popc(__ballot_sync(0xffffffffu, p >= 0 && i < ends && i < W && !keep && !out));
             }
         }
         if (lane == 0) s.base[b] = need;
@@ -237,6 +244,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8
             const int more = p >= 0 && a.room ? max(0, a.room[b]) : 0;
             const long long ends = ((long long)len + more + P - 1) >> a.page_shift;
             const bool heir = p >= 0 && s.first[p] == b;
+            const int gone = gone_hi(len);
             int at = s.base[b];
             for (int i0 = 0; i0 < W; i0 += 32 * kCells) {
                 int old[kCells];
@@ -244,8 +252,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8
 #pragma unroll
                 for (int c = 0; c < kCells; ++c) {
                     const int i = i0 + 32 * c + lane;
-                    const bool keep = old[c] >= 0 && (heir || i < (len >> a.page_shift));
-                    const bool fresh = p >= 0 && i < ends && i < W && !keep;
+                    const bool out = i >= gone_lo && i < gone;
+                    const bool keep = !out && old[c] >= 0 && (heir || i < (len >> a.page_shift));
+                    const bool fresh = p >= 0 && i < ends && i < W && !keep && !out;
                     const unsigned int mask = __ballot_sync(0xffffffffu, fresh);
                     int now = keep ? old[c] : -1;
                     if (fresh) {

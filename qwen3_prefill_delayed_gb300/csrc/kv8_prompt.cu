@@ -64,6 +64,14 @@ struct PromptRec {   // 32 bytes: one (query tile, sequence) pair
 __host__ __device__ __forceinline__ int key_tiles(int keys) {   // an item without keys has one empty tile: its rows get 0
     return keys > 0 ? (keys + TK - 1) / TK : 1;
 }
+enum { kAll, kWindow };   // the positions that tokens see
+// Tiles that no token of an item sees, and the tiles it has
+__device__ __forceinline__ Kv8Skip skipped(const PromptRec& r, int window, int sinks) {
+    return kv8_skip(r.kv_len - r.n + r.q_lo, window, sinks, TK);
+}
+__device__ __forceinline__ int item_tiles(const PromptRec& r, int window, int sinks) {
+    return key_tiles(r.keys) - skipped(r, window, sinks).by;
+}
 // Parts of split items, as for single tokens: CTA c has slots 2 c (the item that its share begins in) and 2 c + 1 (the
 // one it ends in); a slot is [TROWS][HD] sums, then m, l and M of the rows.
 struct PromptDesc {   // the item whose first part is slot 2 c + 1, and the last CTA that has a part of it
@@ -112,6 +120,7 @@ struct PromptArgs {
     float scale_log2;
     int nq, G, QT;
     int v8;                 // out 32-byte aligned
+    int window, sinks;      // as in Kv8AttnArgs
 };
 
 // two fp32 operations in one instruction
@@ -181,7 +190,8 @@ __device__ __forceinline__ void tmem_max32(uint32_t taddr, float& top0, float& t
 __device__ __noinline__ void look_again(const PromptArgs& p, const PromptRec& r, int head, int row, int dim, int n, bf16* out) {
     const int qi = row / p.G, hq = row - qi * p.G;
     const bf16* q = p.q + (long long)(r.row0 + r.q_lo + qi) * p.row_stride + (long long)(head * p.G + hq) * p.view.head_dim;
-    kv8_row_again(p.view, q, r.b, head, r.kv_len - r.n + r.q_lo + qi + 1, r.keys, dim, n, p.scale_log2, out);
+    const int end = r.kv_len - r.n + r.q_lo + qi + 1, lo = p.window > 0 ? end - p.window : 0;
+    kv8_row_again(p.view, q, r.b, head, end, r.keys, dim, n, p.scale_log2, out, lo, p.sinks, max(0, lo - qi));
 }
 __device__ __forceinline__ int snake(int k) {
     return k * (int)gridDim.x + ((k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
@@ -204,8 +214,9 @@ __device__ __forceinline__ void max_pass_whole(uint32_t lS, const float* ks, flo
         Mx = max3(Mx, z0 + e2.x, z1 + e2.y);
     }
 }
-__device__ __forceinline__ void max_pass_masked(uint32_t lS, const float* ks, float q_unscale, int limit, float& mx,
-                                                float& Mx) {
+template <int MODE>
+__device__ __forceinline__ void max_pass_masked(uint32_t lS, const float* ks, float q_unscale, int limit, int lo, int sinks,
+                                                float& mx, float& Mx) {
 #pragma unroll 1
     for (int ch = 0; ch < TK / 32; ++ch) {
         float a[32];
@@ -217,7 +228,7 @@ __device__ __forceinline__ void max_pass_masked(uint32_t lS, const float* ks, fl
             const int n = k >= 0.f ? limit - 32 * ch - 16 * h : 0;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                if (e >= n) a[16 * h + e] = -INFINITY;
+                if (e >= n || (MODE == kWindow && e < lo - 32 * ch - 16 * h && e >= sinks - 32 * ch - 16 * h)) a[16 * h + e] = -INFINITY;
             float top[2] = {fmaxf(a[16 * h], a[16 * h + 1]), fmaxf(a[16 * h + 2], a[16 * h + 3])};
 #pragma unroll
             for (int e = 4; e < 16; e += 2) top[(e >> 1) & 1] = max3(top[(e >> 1) & 1], a[16 * h + e], a[16 * h + e + 1]);
@@ -230,9 +241,9 @@ __device__ __forceinline__ void max_pass_masked(uint32_t lS, const float* ks, fl
 }
 // The weights: l's terms 2^(s - mr) are returned summed; times the block's V scale and 2^(mr - Mr + 11)
 // (`up` its exponent) they go as f16 to columns 16 ch, which this row has read.
-template <bool MASK>
-__device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float q_unscale, int limit, float mr,
-                                             float up) {
+template <bool MASK, int MODE>
+__device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float q_unscale, int limit, int lo, int sinks,
+                                             float mr, float up) {
     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float2 neg = make_float2(-mr, -mr);
 #pragma unroll 1
@@ -254,8 +265,9 @@ __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float
                 const float2 z = fma2(make_float2(a[16 * h + e], a[16 * h + e + 1]), coef2, neg);
                 float2 x = make_float2(ex2(z.x), ex2(z.y));
                 if (MASK) {
-                    if (e >= n) x.x = 0.f;
-                    if (e + 1 >= n) x.y = 0.f;
+                    const int l = lo - 32 * ch - 16 * h, s = sinks - 32 * ch - 16 * h;
+                    if (e >= n || (MODE == kWindow && e < l && e >= s)) x.x = 0.f;
+                    if (e + 1 >= n || (MODE == kWindow && e + 1 < l && e + 1 >= s)) x.y = 0.f;
                 }
                 ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], x);
                 const float2 y = mul2(x, f2);
@@ -324,7 +336,7 @@ __global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a,
         r.q_lo = (p - at_s[lo]) * QT;
         r.kv_len = len_s[lo];
         r.keys = max(0, r.kv_len - r.n + min(r.n, r.q_lo + QT));
-        return kBins - 1 - min(kBins - 1, (r.keys + TK - 1) / TK);
+        return kBins - 1 - min(kBins - 1, (r.keys + TK - 1) / TK - skipped(r, a.window, a.sinks).by);
     };
     auto put = [&](int i, const PromptRec& r, long long before) {
         int4* to = reinterpret_cast<int4*>(list + kRecWords * (1 + (long long)i));
@@ -341,7 +353,7 @@ __global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a,
                 const bool in = p0 + tid < here;
                 if (in) pair(p0 + tid, b0, r);
                 long long units;
-                const long long at = block_scan((long long)(in ? key_tiles(r.keys) : 0), units);
+                const long long at = block_scan((long long)(in ? item_tiles(r, a.window, a.sinks) : 0), units);
                 if (in) put(count + p0 + tid, r, before + a.view.n_kv * at);
                 before += a.view.n_kv * units;
             }
@@ -404,7 +416,7 @@ __device__ __noinline__ void outputs_again(const PromptArgs& p, const int* first
         const PromptRec r{rec[0], rec[1], rec[2], rec[3], rec[4], rec[5], 0};
         const int head = i % p.view.n_kv;
         if (shares) {   // not the parts: they are looked at where they are joined
-            const int from = k == 0 ? first[1] : 0, all = key_tiles(r.keys), n = min(left, all - from);
+            const int from = k == 0 ? first[1] : 0, all = item_tiles(r, p.window, p.sinks), n = min(left, all - from);
             left -= n;
             if (n < all) continue;
         }
@@ -419,7 +431,7 @@ __device__ __noinline__ void outputs_again(const PromptArgs& p, const int* first
     }
 }
 
-template <int HD>
+template <int HD, int MODE>
 __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_constant__ CUtensorMap tmK,
                                                                  const __grid_constant__ PromptArgs p) {
     using C = Cfg<HD>;
@@ -466,7 +478,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     if (before(mid) <= u) lo = mid;
                     else hi = mid;
                 }
-                const int n = key_tiles(p.list[kRecWords * (1 + (long long)lo) + 5]);
+                const int32_t* rec = p.list + kRecWords * (1 + (long long)lo);
+                const int n = item_tiles(PromptRec{rec[0], rec[1], rec[2], rec[3], rec[4], rec[5], 0}, p.window, p.sinks);
                 const long long at = u - before(lo);
                 first_s[0] = lo * c.n_kv + (int)(at / n);
                 first_s[1] = (int)(at % n);
@@ -498,6 +511,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         }
     };
     int t_first = 0, t_all = 0;                         // this item's tiles [t_first, t_first + count) of t_all
+    Kv8Skip skip{0, 0};
+    // the first key of the item's tile t of this CTA, and whether some row sees any of the 16 keys from pos on
+    auto tile_key = [&](int t) { return (MODE == kAll ? t_first + t : kv8_unit_at(skip, t_first + t)) * TK; };
+    auto in_sight = [&](const PromptRec& r, int pos) {
+        return MODE == kAll || pos < p.sinks || pos + kKv8Block > r.kv_len - r.n + r.q_lo + 1 - p.window;
+    };
     auto item = [&](int k, PromptRec& r, int& head) {   // its count, 0 when there is none
         const int i = index(k);
         if (i >= n_items || (shares && left == 0)) return 0;
@@ -509,7 +528,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         r.kv_len = next_y.x;
         r.keys = next_y.y;
         fetch(k + 1);
-        t_all = key_tiles(r.keys);
+        if (MODE == kWindow) skip = skipped(r, p.window, p.sinks);
+        t_all = key_tiles(r.keys) - skip.by;
         if (!shares) return t_all;
         t_first = k == 0 ? first_s[1] : 0;
         const int n = min(left, t_all - t_first);
@@ -529,11 +549,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             const int n_kt = item(k, r, head);
             if (n_kt == 0) break;
             auto page_of = [&](int t) {
-                const int pos = (t_first + t) * TK + blk * kKv8Block;
-                return lane < 2 * NB && pos < r.keys ? kv8_page_of(c, r.b, pos) : -1;
+                const int pos = tile_key(t) + blk * kKv8Block;
+                return lane < 2 * NB && pos < r.keys && in_sight(r, pos) ? kv8_page_of(c, r.b, pos) : -1;
             };
             auto scale_of = [&](int t, int page) {   // -1: the block's keys are absent
-                const int pos = (t_first + t) * TK + blk * kKv8Block;
+                const int pos = tile_key(t) + blk * kKv8Block;
                 return page < 0 ? -1.f : c.scales[kv8_scale_at(c, page, which, head, pos & (c.page_size - 1))];
             };
             int page = page_of(0), page1 = n_kt > 1 ? page_of(1) : -1;
@@ -546,8 +566,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 if (g >= NK) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_KE + st), (uint32_t)(g / NK - 1) & 1u, abort_flag));
                 if (!ok) break;
                 const bool want = lane < NB && page >= 0;
-                const int pos = (t_first + t) * TK + blk * kKv8Block;
-                if (lane < NB && pos < r.keys && page < 0) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
+                const int pos = tile_key(t) + blk * kKv8Block;
+                if (lane < NB && pos < r.keys && page < 0 && in_sight(r, pos)) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
                 if (lane < NB) {
                     sc[(g % NSC) * 3 * NB + blk] = s;
                 } else if (lane < 2 * NB) {
@@ -642,6 +662,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             const bool row_ok = qi < p.QT && r.q_lo + qi < r.n;
             const int limit = row_ok ? r.kv_len - r.n + r.q_lo + qi + 1 : 0;      // keys below it count
             const int clear = r.kv_len - r.n + r.q_lo + 1;                        // ... for every row of the tile
+            const int lo = limit - p.window;                                      // window: the row's first key
+            const int lo_last = r.kv_len - r.n + min(r.n, r.q_lo + p.QT) - p.window;   // ... and the last row's
             ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QS + it % NQS), (uint32_t)(it / NQS) & 1u, abort_flag));
             if (!ok) break;
             const float q_unscale = qs[(it % NQS) * TROWS + row] * p.scale_log2;
@@ -654,13 +676,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 tc_fence_after();
                 const uint32_t lS = lS0 + (g & 1) * TK;
                 const float* ks = sc + (g % NSC) * 3 * NB;   // then the V exponents and factors
-                const int j0 = (t_first + t) * TK;
-                const bool whole = j0 + TK <= clear && there[g % NSC] != 0;   // every key counts for every row
+                const int j0 = tile_key(t);
+                const bool whole = j0 + TK <= clear && there[g % NSC] != 0 &&   // every key counts for every row
+                                   (MODE == kAll || j0 >= lo_last || j0 + TK <= p.sinks);
                 float mx = -INFINITY, Mx = -INFINITY;
                 if (whole)
                     max_pass_whole(lS, ks, q_unscale, mx, Mx);
                 else
-                    max_pass_masked(lS, ks, q_unscale, limit - j0, mx, Mx);
+                    max_pass_masked<MODE>(lS, ks, q_unscale, limit - j0, lo - j0, p.sinks - j0, mx, Mx);
                 const float mn = fmaxf(m, mx);
                 const float mr = mn == -INFINITY ? 0.f : mn;
                 l *= ex2(m - mr);
@@ -683,8 +706,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     }
                 }
                 const float up = mr - Mr + kUnit;
-                l += whole ? weight_pass<false>(lS, ks, q_unscale, 0, mr, up)
-                           : weight_pass<true>(lS, ks, q_unscale, limit - j0, mr, up);
+                l += whole ? weight_pass<false, MODE>(lS, ks, q_unscale, 0, 0, 0, mr, up)
+                           : weight_pass<true, MODE>(lS, ks, q_unscale, limit - j0, lo - j0, p.sinks - j0, mr, up);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
@@ -769,15 +792,18 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             const uint8_t* head_v = c.codes + kv8_code_at(c, 0, 1, head, 0) + kq * HD + c16 * 16;
             const int32_t* table = c.table + (long long)r.b * c.max_pages;
             auto page_of = [&](int t) {
-                const int pos = (t_first + t) * TK + w * kKv8Block;
-                if (pos >= r.keys) return -1;   // below it: inside the row of the table
+                const int pos = tile_key(t) + w * kKv8Block;
+                if (pos >= r.keys || !in_sight(r, pos)) return -1;   // below it: inside the row of the table
                 const int page = table[pos >> c.page_shift];
                 return page < c.n_pages ? page : -1;
             };
             auto request = [&](uint4(&v)[2 * HALVES], int t, int page) {
-                const int pos = (t_first + t) * TK + w * kKv8Block;
+                const int pos = tile_key(t) + w * kKv8Block;
                 const uint8_t* src = head_v + (long long)max(page, 0) * page_bytes + (pos & (c.page_size - 1)) * HD;
-                if (page >= 0 && pos + kKv8Block <= r.keys) {
+                // window: keys of the block behind every row's
+                const int lo0 = MODE == kWindow ? r.kv_len - r.n + r.q_lo + 1 - p.window : 0;
+                const bool edge = MODE == kWindow && pos < lo0 && pos + kKv8Block > p.sinks;
+                if (page >= 0 && pos + kKv8Block <= r.keys && !edge) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -789,7 +815,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
 #pragma unroll
                         for (int h = 0; h < HALVES; ++h) {
                             uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                            if (page >= 0 && pos + 8 * y + kq < r.keys)
+                            const int key = pos + 8 * y + kq;
+                            if (page >= 0 && key < r.keys && (MODE != kWindow || key >= lo0 || key < p.sinks))
                                 u = *reinterpret_cast<const uint4*>(src + 8 * y * HD + h * 64);
                             v[y * HALVES + h] = u;
                         }
@@ -986,7 +1013,7 @@ size_t list_bytes(int batch, int total_rows, int G) {
     return (size_t)(list_pairs(batch, total_rows, G) + 1) * kRecWords * sizeof(int32_t);
 }
 
-template <int HD>
+template <int HD, int MODE>
 cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaStream_t st) {
     using C = Cfg<HD>;
     alignas(64) CUtensorMap map;
@@ -997,13 +1024,13 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(kv8_prompt_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
+        e = cudaFuncSetAttribute(kv8_prompt_kernel<HD, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
     int32_t* list = reinterpret_cast<int32_t*>(a.scratch);
     const long long pairs = most_pairs(a.batch, a.total_rows, QT, a.max_new);
-    const bool shares = prompt_shares(pairs, a.view.n_kv, a.max_len);
+    const bool shares = prompt_shares(pairs, a.view.n_kv, kv8_most_seen(a.max_len, a.window, a.sinks, QT + 2 * TK));
     HRA_LAUNCH(kv8_schedule_kernel, dim3(1), dim3(1024), 0, st, a, G, QT, short_rows, shares ? 1 : 0,
                (int)list_pairs(a.batch, a.total_rows, G), list);
     PromptArgs p{};
@@ -1016,6 +1043,8 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
     p.nq = a.nq;
     p.G = G;
     p.QT = QT;
+    p.window = a.window;
+    p.sinks = a.sinks;
     p.v8 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
     const int grid = shares ? prompt_slots() : (int)std::max<long long>(1, std::min<long long>(pairs * a.view.n_kv, prompt_slots()));
     if (shares) {
@@ -1023,7 +1052,7 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
         p.desc = reinterpret_cast<PromptDesc*>(at);
         p.parts = reinterpret_cast<float*>(at + grid * sizeof(PromptDesc));
     }
-    HRA_LAUNCH(kv8_prompt_kernel<HD>, dim3(grid), dim3(kThreads), C::ALLOC, st, map, p);
+    HRA_LAUNCH((kv8_prompt_kernel<HD, MODE>), dim3(grid), dim3(kThreads), C::ALLOC, st, map, p);
     if (shares) HRA_LAUNCH(kv8_prompt_join_kernel<HD>, dim3(grid, TROWS / 8), dim3(256), 0, st, p);
     return cudaGetLastError();
 }
@@ -1041,7 +1070,9 @@ size_t kv8_prompt_scratch_bytes(const Kv8View& c, int batch, int total_rows, int
 
 cudaError_t launch_kv8_prompt(const Kv8AttnArgs& a, int short_rows, cudaStream_t st) {
     const int G = a.nq / a.view.n_kv, QT = TROWS / G;
-    return a.view.head_dim == 128 ? launch_hd<128>(a, G, QT, short_rows, st) : launch_hd<64>(a, G, QT, short_rows, st);
+    if (a.window > 0)
+        return a.view.head_dim == 128 ? launch_hd<128, kWindow>(a, G, QT, short_rows, st) : launch_hd<64, kWindow>(a, G, QT, short_rows, st);
+    return a.view.head_dim == 128 ? launch_hd<128, kAll>(a, G, QT, short_rows, st) : launch_hd<64, kAll>(a, G, QT, short_rows, st);
 }
 
 }  // namespace hra
