@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libhra.so")
 BINDING_SRC = os.path.join(CSRC, "kv8_binding.cpp")
 BINDING = os.path.join(PKG, "_kv8_binding.so")
 SOURCES = ["api.cu", "gemm_tc.cu", "attention.cu", "attention_tc.cu", "elementwise.cu", "codebook.cu", "fp8.cu",
-           "noalloc.cu", "head.cu", "nvfp4.cu", "decode_pass.cu", "kv8_append.cu", "kv8_attention.cu", "kv8_prompt.cu", "kv8_pages.cu",
+           "noalloc.cu", "head.cu", "nvfp4.cu", "decode_pass.cu", "kv8_append.cu", "kv8_attention.cu", "kv8_prompt.cu", "kv8_shared.cu",
+           "kv8_pages.cu",
            "kv8_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fno-strict-aliasing",

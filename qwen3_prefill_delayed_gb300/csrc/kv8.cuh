@@ -88,6 +88,27 @@ KV8_HD int kv8_most_seen(int max_len, int window, int sinks, int tokens) {
     const long long n = (long long)window + sinks + tokens;
     return window > 0 && n < max_len ? (int)n : max_len;
 }
+// Tile `tile` of the n new tokens (of which max_new count) of a sequence of kv_len positions, over its positions from `prefix`
+// (whole blocks) on in units of 128 keys, in up to `splits` parts: its tokens t0 .. t0 + tokens - 1, the positions below the last
+// of them, the blocks, the units of a part, and how many parts there are.
+struct Kv8Own {
+    int t0, tokens, keys, blocks, per, parts;
+};
+KV8_HD Kv8Own kv8_own(int kv_len, int n, int tile, int tile_tokens, int max_new, int prefix, int splits) {
+    Kv8Own o;
+    const int count = n < max_new ? n : max_new;
+    o.t0 = tile * tile_tokens;
+    o.tokens = count - o.t0 < tile_tokens ? count - o.t0 : tile_tokens;
+    if (o.tokens < 0) o.tokens = 0;
+    o.keys = kv_len - n + o.t0 + o.tokens;
+    if (o.keys < 0) o.keys = 0;
+    o.blocks = (o.keys + kKv8Block - 1) / kKv8Block - prefix / kKv8Block;
+    if (o.blocks < 0) o.blocks = 0;
+    const int units = o.blocks > 0 ? (o.blocks + 7) / 8 : 1;
+    o.per = (units + splits - 1) / splits;
+    o.parts = (units + o.per - 1) / o.per;
+    return o;
+}
 // Most blocks of 16 that n >= 1 consecutive positions can touch.
 KV8_HD int kv8_max_blocks(int n) { return (n + kKv8Block - 2) / kKv8Block + 1; }
 

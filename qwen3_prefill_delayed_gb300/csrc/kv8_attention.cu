@@ -37,13 +37,14 @@
 
 #include <algorithm>
 
-#include "kv8_device.cuh"
+#include "kv8_parts.cuh"
 
 namespace hra {
 
 namespace {
 
-enum { kAll, kWindow };   // the positions that tokens see
+// The positions that tokens see: all, a window's and the sinks', or those behind a shared prefix (and then only parts are written)
+enum { kAll, kWindow, kOwn };
 constexpr int kWarps = 4;
 constexpr int kPair = 2;        // blocks a warp works on at once: two chains of MMAs and shuffles instead of one
 constexpr int kStages = 2;      // pairs of a warp in shared memory: 12 warps an SM; with 3, 8 warps fit (121 us against 112)
@@ -58,7 +59,8 @@ constexpr int kShortRows = 16;  // (position, head) rows of a kv head that fit t
 // in this kernel: 8 of them after 1024 positions 25 / 32 us, after 2048 40 / 39, after 4096 83 / 54; 48 of them 49 / 60, 81 / 83
 // and 277 / 126.
 constexpr int kSerialKeys = 2048;
-constexpr float kPScale = 15.f; // log2 of the largest p
+constexpr float kPScale = kRowsUnit;   // log2 of the largest p
+static_assert(kUnit == 128, "units of kv8_own");
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -87,24 +89,21 @@ struct Ring {
 };
 
 // Parts of split items: CTA c has slots 2 c (the item that its share begins in) and 2 c + 1 (the one it ends in).
-// A slot: [ROWS][HD] sums, then [ROWS][3] (m, l, M).  desc[c]: the item whose first part is CTA c's slot 2 c + 1 and
+// desc[c]: the item whose first part is CTA c's slot 2 c + 1 and
 // the last CTA that has a part of it.
 struct SplitDesc {
     int row0, n, head, last;   // n: tokens; row0 < 0: no item begins in this share and goes on behind it
     int b, pad[3];
 };
-template <int HD, int NG>
-struct Slot {
-    static constexpr int ROWS = 8 * NG;
-    static constexpr int FLOATS = ROWS * (HD + 3);
-};
-
 struct SplitArgs {
     Kv8AttnArgs a;
     SplitDesc* desc;
     float* parts;
     int G, max_rows;   // sequences with at most max_rows (position, head) rows a kv head
     int whole;         // one item a CTA: blockIdx = (head, sequence)
+    // behind a shared prefix: blockIdx = (head, tile of a sequence's tokens, split)
+    const SharedRow* shared;
+    int row_tiles;
 };
 
 // Dims d and d + 1 of row r, written to dst, are or hold a NaN: see kv8_row_again.
@@ -120,8 +119,9 @@ __device__ __noinline__ void look_again(const SplitArgs& s, int b, int head, int
 }
 
 // NG x 8 rows of (position, head) pairs.  ONE: sequences of one new token, whose rows all see the same keys.  MODE: all
-// positions, or those of a window and the sinks: then units, blocks and lengths below count what some token of the sequence
-// sees, kv8_unit_at says which block that is, and only blocks at the window's edge look at its border.
+// positions, or those of a window and the sinks, or those behind a shared prefix: then units, blocks and lengths below count what
+// some token of the sequence sees, kv8_unit_at says which block that is, and only blocks at the window's edge look at its
+// border.
 template <int HD, int NG, bool ONE, int MODE>
 __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_constant__ CUtensorMap codes_map,
                                                                   const __grid_constant__ SplitArgs s) {
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
     // ---- this CTA's share
     long long u = 0, u_end = 1;
     long long share = 0;
-    if (!s.whole) {
+    if (MODE != kOwn && !s.whole) {
         // units of the sequences, summed up front: consecutive sequences a thread, then across threads
         const int per = (a.batch + kWarps * 32 - 1) / (kWarps * 32);
         const int b0 = threadIdx.x * per;
@@ -219,7 +219,18 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
         // ---- the segment: units [i0, i1) of item (b, head)
         int b, head, i0 = 0, i1, row0, n;
         bool first_part = true, last_part = true;
-        if (s.whole) {
+        Kv8Own own{};
+        if (MODE == kOwn) {
+            b = blockIdx.y / s.row_tiles;
+            head = blockIdx.x;
+            kv8_rows(a.cu, b, a.total_rows, row0, n);
+            own = kv8_own(length(b), n, blockIdx.y - b * s.row_tiles, ROWS / G, a.max_new, s.shared[b].prefix, gridDim.z);
+            if (own.tokens == 0 || blockIdx.z >= own.parts) return;
+            i0 = blockIdx.z * own.per;
+            i1 = i0 + own.per;
+            row0 += own.t0;
+            u = u_end;
+        } else if (s.whole) {
             b = blockIdx.y;
             head = blockIdx.x;
             kv8_rows(a.cu, b, a.total_rows, row0, n);
@@ -246,15 +257,16 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
             kv8_rows(a.cu, b, a.total_rows, row0, n);
         }
         const int kv_len = length(b);
-        if (head == 0 && threadIdx.x == 0 && first_part &&
+        if (head == 0 && threadIdx.x == 0 && first_part && blockIdx.z == 0 && own.t0 == 0 &&
             (a.kv_len[b] != kv_len || n > a.max_new))
             raise_error(c.err, HRA_DEVERR_POS_RANGE);
-        const int q_n = min(min(ROWS / G, n), a.max_new);   // tokens beyond max_new get no output
-        const int keys = max(0, kv_len - n + q_n);     // positions below the last of them
-        const Kv8Skip skip = skipped(kv_len, n);
+        const int q_n = MODE == kOwn ? own.tokens : min(min(ROWS / G, n), a.max_new);   // tokens beyond max_new get no output
+        const int first = kv_len - n + own.t0;         // position of the first token
+        const int keys = max(0, first + q_n);          // positions below the last of them
+        const Kv8Skip skip = MODE == kOwn ? Kv8Skip{0, s.shared[b].prefix / kKv8Block} : skipped(kv_len, n);
         auto first_key = [&](int x) { return (MODE == kAll ? x : kv8_unit_at(skip, x)) * kKv8Block; };   // of block x
         const int blk1 = min((keys + kKv8Block - 1) / kKv8Block - skip.by, i1 >= (1 << 28) ? 1 << 28 : i1 * (kWarps * kPair));
-        const int lo0 = kv_len - n + 1 - a.window;     // window: the first position of the first token's
+        const int lo0 = first + 1 - a.window;          // window: the first position of the first token's
         int blk = (i0 * kWarps + warp) * kPair;
         constexpr int STEP = kWarps * kPair;
 
@@ -347,7 +359,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
         for (int x = 0; x < NG; ++x) {
             const int r = g + 8 * x, qi = r / G, hq = r - qi * G;
             const bool ok = qi < q_n;
-            limit[x] = ok ? min(keys, kv_len - n + qi + 1) : 0;
+            limit[x] = ok ? min(keys, first + qi + 1) : 0;
             const uint4(&raw)[HD / 64][2] = q_raw[x];
             uint32_t top = 0u;     // bf16 bits without their sign order like the values
 #pragma unroll
@@ -607,8 +619,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
             }
         }
         __syncthreads();
-        const bool whole = first_part && last_part;
-        float* part = s.parts + (2LL * blockIdx.x + (first_part ? 1 : 0)) * Slot<HD, NG>::FLOATS;
+        const bool whole = MODE != kOwn && first_part && last_part;
+        const long long slot = MODE == kOwn ? ((long long)blockIdx.y * c.n_kv + head) * gridDim.z + blockIdx.z
+                                            : 2LL * blockIdx.x + (first_part ? 1 : 0);
+        float* part = s.parts + slot * Slot<HD, NG>::FLOATS;
         for (int i = threadIdx.x; i < q_n * G * (HD / 2); i += kWarps * 32) {
             const int r = i / (HD / 2), d = (i - r * (HD / 2)) * 2;
             const int qi = r / G, hq = r - qi * G;
@@ -645,7 +659,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
                 }
             }
         }
-        if (first_part && !last_part && threadIdx.x == 0) {
+        if (MODE != kOwn && first_part && !last_part && threadIdx.x == 0) {
             const long long end = (long long)before[b] * c.n_kv + (long long)(head + 1) * (before[b + 1] - before[b]);
             s.desc[blockIdx.x] = SplitDesc{row0, q_n, head, (int)((end - 1) / share), b, {0, 0, 0}};
         }
@@ -748,7 +762,7 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ S
 int split_grid() { return 3 * device_sm_count(); }
 
 template <int HD, int NG, bool ONE, int MODE>
-cudaError_t launch_ng(const SplitArgs& s, cudaStream_t st) {
+cudaError_t launch_ng(const SplitArgs& s, cudaStream_t st, int splits = 1) {
     constexpr int join = kWarps * 8 * NG * (HD + 3) * 4;
     constexpr int smem = (Ring<HD>::BYTES > join ? Ring<HD>::BYTES : join) + 1024;   // aligned up to 1024 bytes
     alignas(64) CUtensorMap map;
@@ -762,6 +776,11 @@ cudaError_t launch_ng(const SplitArgs& s, cudaStream_t st) {
         e = cudaFuncSetAttribute(kv8_attn_kernel<HD, NG, ONE, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
+    }
+    if (MODE == kOwn) {
+        const dim3 grid((unsigned)s.a.view.n_kv, (unsigned)(s.a.batch * s.row_tiles), (unsigned)splits);
+        HRA_LAUNCH((kv8_attn_kernel<HD, NG, ONE, MODE>), grid, dim3(kWarps * 32), smem, st, map, s);
+        return cudaGetLastError();
     }
     if (s.whole) {
         const dim3 grid((unsigned)s.a.view.n_kv, (unsigned)s.a.batch);
@@ -779,9 +798,6 @@ cudaError_t launch_tokens(const SplitArgs& s, cudaStream_t st) {
     if (s.a.window > 0) return s.a.max_new == 1 ? launch_ng<HD, NG, true, kWindow>(s, st) : launch_ng<HD, NG, false, kWindow>(s, st);
     return s.a.max_new == 1 ? launch_ng<HD, NG, true, kAll>(s, st) : launch_ng<HD, NG, false, kAll>(s, st);
 }
-
-// One n = 8 column group while the rows of a tile fit it, else two.
-int column_groups(int G, int max_new) { return (long long)G * max_new <= 8 ? 1 : 2; }
 
 // Items go whole, one a CTA, while they are short, and where the sequences do not fit the table of a CTA.
 bool goes_whole(int batch, int max_len) { return max_len <= kWholeUnits * kUnit || batch > kMaxBatch; }
@@ -801,13 +817,21 @@ size_t kv8_attention_scratch_bytes(const Kv8View& c, int batch, int total_rows, 
     return n;
 }
 
-size_t kv8_shared_scratch_bytes(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int max_len, int groups,
-                                int max_prefix, int max_own) {
-    (void)groups, (void)max_prefix, (void)max_own;
-    return kv8_attention_scratch_bytes(c, batch, total_rows, nq, max_new, max_len);
+cudaError_t launch_kv8_own(const Kv8AttnArgs& a, const SharedCall& c, cudaStream_t st) {
+    SplitArgs s{};
+    s.a = a;
+    s.G = a.nq / a.view.n_kv;
+    s.parts = c.own_parts;
+    s.shared = c.rows;
+    s.row_tiles = c.row_tiles;
+    const bool one = column_groups(s.G, a.max_new) == 1;
+    if (a.view.head_dim == 128)
+        return one ? launch_ng<128, 1, false, kOwn>(s, st, c.splits) : launch_ng<128, 2, false, kOwn>(s, st, c.splits);
+    return one ? launch_ng<64, 1, false, kOwn>(s, st, c.splits) : launch_ng<64, 2, false, kOwn>(s, st, c.splits);
 }
 
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st) {
+    if (kv8_shares(a.view, a.batch, a.nq, a.max_new, a.groups, a.max_prefix)) return launch_kv8_shared(a, st);
     const int G = a.nq / a.view.n_kv;
     const bool prompts = (long long)G * a.max_new > kShortRows;
     uint8_t* scratch = reinterpret_cast<uint8_t*>(a.scratch);

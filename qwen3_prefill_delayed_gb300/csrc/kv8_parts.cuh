@@ -1,0 +1,60 @@
+// kv8_parts.cuh -- partial results of attention over the paged 8-bit cache, which the kernels that write them share with the
+// ones that join them.
+//
+// A part of an output row is the sum over some of its keys: m, the largest score s; l, the sum of 2^(s - m); M, the largest
+// s + log2 of its block's V scale; and per dim the sum of 2^(s - M) times V, in units of 2^-15 (kv8_attention.cu) or 2^-11
+// (kv8_prompt.cu).
+#pragma once
+
+#include "kv8_device.cuh"
+
+namespace hra {
+
+constexpr int kTileRows = 128;     // (position, head) rows of a prompt item
+constexpr int kTileKeys = 64;      // keys of its tiles
+constexpr float kTileUnit = 11.f;  // log2 of the weight of the reference maximum in a prompt's sums ...
+constexpr float kRowsUnit = 15.f;  // ... and in a short sequence's
+
+struct PromptRec {   // 32 bytes: one (query tile, sequence) pair
+    int b, row0, n, q_lo, kv_len, keys;
+    long long before;   // equal shares: tiles of the items of the pairs before
+};
+constexpr int kRecWords = 8;
+__host__ __device__ __forceinline__ int key_tiles(int keys) {   // an item without keys has one empty tile: its rows get 0
+    return keys > 0 ? (keys + kTileKeys - 1) / kTileKeys : 1;
+}
+
+// A prompt item's part: [kTileRows][HD] sums, then m, l and M of the rows.
+template <int HD>
+struct PromptSlot {
+    static constexpr int FLOATS = kTileRows * (HD + 3);
+};
+// A short sequence's part: [ROWS][HD] sums, then [ROWS][3] (m, l, M).
+template <int HD, int NG>
+struct Slot {
+    static constexpr int ROWS = 8 * NG;
+    static constexpr int FLOATS = ROWS * (HD + 3);
+};
+
+// Shared prefixes (kv8_shared.cu).  Of batch row b: the positions that it reads through its group's first row, the group's
+// first (query tile, group) pair, first packed row and key tiles.
+struct SharedRow {
+    int prefix, pair0, row0, tiles;
+};
+// What the kernels of one call share in scratch.
+struct SharedCall {
+    int32_t* list;       // [0] = pairs, [2..3] all items' tiles, records from word 8 on (as for prompts)
+    SharedRow* rows;     // [batch]
+    float* prefix_parts; // PromptSlots: two for each CTA, then one for each item that lies inside a CTA's share
+    float* own_parts;    // Slots: [batch][row_tiles][n_kv][splits]
+    int prefix_grid, row_tiles, splits, most_pairs;
+};
+cudaError_t launch_kv8_prefix(const Kv8AttnArgs& a, const SharedCall& c, cudaStream_t st);   // kv8_prompt.cu
+cudaError_t launch_kv8_own(const Kv8AttnArgs& a, const SharedCall& c, cudaStream_t st);      // kv8_attention.cu
+cudaError_t launch_kv8_shared(const Kv8AttnArgs& a, cudaStream_t st);                        // kv8_shared.cu
+// Whether a call's prefixes are read once; if not, launch_kv8_attention goes row by row.
+bool kv8_shares(const Kv8View& c, int batch, int nq, int max_new, int groups, int max_prefix);
+// Rows of a short sequence's tile: one n = 8 column group of the MMAs while its (position, head) rows fit, else two.
+inline int column_groups(int G, int max_new) { return (long long)G * max_new <= 8 ? 1 : 2; }
+
+}  // namespace hra

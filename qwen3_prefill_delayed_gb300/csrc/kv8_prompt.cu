@@ -39,17 +39,17 @@
 #include <algorithm>
 #include <math.h>
 
-#include "kv8_device.cuh"
+#include "kv8_parts.cuh"
 
 namespace hra {
 
 namespace {
 
 constexpr int kThreads = 320;
-constexpr int TROWS = 128;
-constexpr int TK = 64;             // keys a tile
+constexpr int TROWS = kTileRows;
+constexpr int TK = kTileKeys;      // keys a tile
 constexpr int NB = TK / kKv8Block; // blocks a tile
-constexpr float kUnit = 11.f;      // log2 of the weight of the reference maximum
+constexpr float kUnit = kTileUnit; // log2 of the weight of the reference maximum
 // Keys from which items count as long (see prompt_shares).  8 kv heads of 128, 4 q heads each, in a graph, equal shares / whole
 // items: 1 row of 128 tokens after 2000 positions 36 / 42 us, after 16000 64 / 245; 2 rows of 500 and 1021 after 8000 210 / 224,
 // after 16000 362 / 424, but after 4000 137 / 125; 4 of 512 after 8000 295 / 312; from 8 of 1024 on equal after 4000 (617 / 618),
@@ -57,14 +57,9 @@ constexpr float kUnit = 11.f;      // log2 of the weight of the reference maximu
 constexpr int kSharesFrom = 2048;
 constexpr float kSlack = 4.f;      // how far a maximum may pass the reference before it moves
 
-struct PromptRec {   // 32 bytes: one (query tile, sequence) pair
-    int b, row0, n, q_lo, kv_len, keys;
-    long long before;   // equal shares: tiles of the items of the pairs before
-};
-__host__ __device__ __forceinline__ int key_tiles(int keys) {   // an item without keys has one empty tile: its rows get 0
-    return keys > 0 ? (keys + TK - 1) / TK : 1;
-}
-enum { kAll, kWindow };   // the positions that tokens see
+// The positions that tokens see: all, a window's and the sinks', or (of an item whose rows are those of a group of sequences)
+// the shared prefix, all of it; then every item's sums go to scratch as parts.
+enum { kAll, kWindow, kPrefix };
 // Tiles that no token of an item sees, and the tiles it has
 __device__ __forceinline__ Kv8Skip skipped(const PromptRec& r, int window, int sinks) {
     return kv8_skip(r.kv_len - r.n + r.q_lo, window, sinks, TK);
@@ -73,16 +68,11 @@ __device__ __forceinline__ int item_tiles(const PromptRec& r, int window, int si
     return key_tiles(r.keys) - skipped(r, window, sinks).by;
 }
 // Parts of split items, as for single tokens: CTA c has slots 2 c (the item that its share begins in) and 2 c + 1 (the
-// one it ends in); a slot is [TROWS][HD] sums, then m, l and M of the rows.
+// one it ends in).
 struct PromptDesc {   // the item whose first part is slot 2 c + 1, and the last CTA that has a part of it
     int row0, n, q_lo, head, last;   // row0 < 0: none
     int b, kv_len, keys;             // as in the pair's record
 };
-template <int HD>
-struct PromptSlot {
-    static constexpr int FLOATS = TROWS * (HD + 3);
-};
-constexpr int kRecWords = 8;
 
 constexpr int NK = 4;              // K stages
 constexpr int NSC = 8;             // tiles whose scales are held
@@ -462,10 +452,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         *abort_flag = 0;
         *issued = 0;
         *nan_out = 0;
-        if (p.desc != nullptr) {
+        if (MODE == kPrefix || p.desc != nullptr) {
             const long long all = *reinterpret_cast<const long long*>(p.list + 2);
             const long long share = (all + gridDim.x - 1) / gridDim.x, u = blockIdx.x * share;
-            p.desc[blockIdx.x].row0 = -1;
+            if (MODE != kPrefix) p.desc[blockIdx.x].row0 = -1;
             first_s[0] = first_s[1] = 0;
             first_s[2] = (int)max(0LL, min(share, all - u));
             if (u < all) {
@@ -498,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     const uint32_t tS = slots[0], tO = tS + 2 * TK;   // two S buffers, then O
     // Items k = 0, 1, ... of this CTA; the next one's record is on its way while one is worked on.  Every role calls
     // item(0), item(1), ... until there is none.
-    const bool shares = p.desc != nullptr;
+    const bool shares = MODE == kPrefix || p.desc != nullptr;
     int left = shares ? first_s[2] : 0;   // tiles of the share
     int4 next_x = make_int4(0, 0, 0, 0), next_y = next_x;
     auto index = [&](int k) { return shares ? first_s[0] + k : snake(k); };
@@ -513,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     int t_first = 0, t_all = 0;                         // this item's tiles [t_first, t_first + count) of t_all
     Kv8Skip skip{0, 0};
     // the first key of the item's tile t of this CTA, and whether some row sees any of the 16 keys from pos on
-    auto tile_key = [&](int t) { return (MODE == kAll ? t_first + t : kv8_unit_at(skip, t_first + t)) * TK; };
+    auto tile_key = [&](int t) { return (MODE != kWindow ? t_first + t : kv8_unit_at(skip, t_first + t)) * TK; };
     auto in_sight = [&](const PromptRec& r, int pos) {
-        return MODE == kAll || pos < p.sinks || pos + kKv8Block > r.kv_len - r.n + r.q_lo + 1 - p.window;
+        return MODE != kWindow || pos < p.sinks || pos + kKv8Block > r.kv_len - r.n + r.q_lo + 1 - p.window;
     };
     auto item = [&](int k, PromptRec& r, int& head) {   // its count, 0 when there is none
         const int i = index(k);
@@ -660,8 +650,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             const int n_kt = item(k, r, head);
             if (n_kt == 0) break;
             const bool row_ok = qi < p.QT && r.q_lo + qi < r.n;
-            const int limit = row_ok ? r.kv_len - r.n + r.q_lo + qi + 1 : 0;      // keys below it count
-            const int clear = r.kv_len - r.n + r.q_lo + 1;                        // ... for every row of the tile
+            const int first = MODE == kPrefix ? r.keys - 1 : r.kv_len - r.n + r.q_lo;   // the last key of the first row
+            const int limit = row_ok ? first + (MODE == kPrefix ? 0 : qi) + 1 : 0;      // keys below it count
+            const int clear = first + 1;                                                // ... for every row of the tile
             const int lo = limit - p.window;                                      // window: the row's first key
             const int lo_last = r.kv_len - r.n + min(r.n, r.q_lo + p.QT) - p.window;   // ... and the last row's
             ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QS + it % NQS), (uint32_t)(it / NQS) & 1u, abort_flag));
@@ -678,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const float* ks = sc + (g % NSC) * 3 * NB;   // then the V exponents and factors
                 const int j0 = tile_key(t);
                 const bool whole = j0 + TK <= clear && there[g % NSC] != 0 &&   // every key counts for every row
-                                   (MODE == kAll || j0 >= lo_last || j0 + TK <= p.sinks);
+                                   (MODE != kWindow || j0 >= lo_last || j0 + TK <= p.sinks);
                 float mx = -INFINITY, Mx = -INFINITY;
                 if (whole)
                     max_pass_whole(lS, ks, q_unscale, mx, Mx);
@@ -718,8 +709,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV + ((g - 1) & 1)), (uint32_t)((g - 1) >> 1) & 1u, abort_flag));
             if (!ok) break;
             tc_fence_after();
-            if (shares && n_kt < t_all) {   // a part: the sums as they are
-                float* part = p.parts + (2LL * blockIdx.x + (t_first == 0 ? 1 : 0)) * PromptSlot<HD>::FLOATS;
+            if (MODE == kPrefix || (shares && n_kt < t_all)) {   // a part: the sums as they are
+                const long long slot = MODE == kPrefix && n_kt == t_all ? 2LL * gridDim.x + index(k) : 2LL * blockIdx.x + (t_first == 0 ? 1 : 0);
+                float* part = p.parts + slot * PromptSlot<HD>::FLOATS;
 #pragma unroll 1
                 for (int ch = 0; ch < HD; ch += 32) {
                     float o[32];
@@ -732,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 part[row] = m;
                 part[TROWS + row] = l;
                 part[2 * TROWS + row] = M;
-                if (t_first == 0 && row == 0) {   // its first part; the share is at its end
+                if (MODE != kPrefix && t_first == 0 && row == 0) {   // its first part; the share is at its end
                     const long long all = *reinterpret_cast<const long long*>(p.list + 2);
                     const long long share = (all + gridDim.x - 1) / gridDim.x;
                     const long long end = (blockIdx.x + 1LL) * share - n_kt + t_all;
@@ -950,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         tc_fence_after();
         tmem_dealloc(tS, 256);
     }
-    if (*nan_out && !*abort_flag) outputs_again<HD>(p, first_s);
+    if (MODE != kPrefix && *nan_out && !*abort_flag) outputs_again<HD>(p, first_s);
 }
 
 // The parts of the item that begins in share blockIdx.x and goes on behind it, in order; 8 rows a CTA.
@@ -1014,20 +1006,48 @@ size_t list_bytes(int batch, int total_rows, int G) {
 }
 
 template <int HD, int MODE>
-cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaStream_t st) {
-    using C = Cfg<HD>;
-    alignas(64) CUtensorMap map;
-    const long long rows = 2LL * a.view.n_pages * a.view.n_kv * a.view.page_size;
-    if (!make_map_codes(&map, a.view.codes, rows, HD, kKv8Block)) return cudaErrorInvalidValue;
+cudaError_t configure() {
     static bool configured[64] = {false};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(kv8_prompt_kernel<HD, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
+        e = cudaFuncSetAttribute(kv8_prompt_kernel<HD, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::ALLOC);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
+    return cudaSuccess;
+}
+
+template <int HD>
+cudaError_t launch_prefix(const Kv8AttnArgs& a, const SharedCall& s, cudaStream_t st) {
+    alignas(64) CUtensorMap map;
+    if (!make_map_codes(&map, a.view.codes, 2LL * a.view.n_pages * a.view.n_kv * a.view.page_size, HD, kKv8Block))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = configure<HD, kPrefix>();
+    if (e != cudaSuccess) return e;
+    PromptArgs p{};
+    p.view = a.view;
+    p.q = a.q;
+    p.row_stride = a.row_stride;
+    p.list = s.list;
+    p.parts = s.prefix_parts;
+    p.scale_log2 = a.scale_log2;
+    p.nq = a.nq;
+    p.G = a.nq / a.view.n_kv;
+    p.QT = TROWS / p.G;
+    HRA_LAUNCH((kv8_prompt_kernel<HD, kPrefix>), dim3(s.prefix_grid), dim3(kThreads), Cfg<HD>::ALLOC, st, map, p);
+    return cudaGetLastError();
+}
+
+template <int HD, int MODE>
+cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaStream_t st) {
+    using C = Cfg<HD>;
+    alignas(64) CUtensorMap map;
+    const long long rows = 2LL * a.view.n_pages * a.view.n_kv * a.view.page_size;
+    if (!make_map_codes(&map, a.view.codes, rows, HD, kKv8Block)) return cudaErrorInvalidValue;
+    const cudaError_t e = configure<HD, MODE>();
+    if (e != cudaSuccess) return e;
     int32_t* list = reinterpret_cast<int32_t*>(a.scratch);
     const long long pairs = most_pairs(a.batch, a.total_rows, QT, a.max_new);
     const bool shares = prompt_shares(pairs, a.view.n_kv, kv8_most_seen(a.max_len, a.window, a.sinks, QT + 2 * TK));
@@ -1066,6 +1086,10 @@ size_t kv8_prompt_scratch_bytes(const Kv8View& c, int batch, int total_rows, int
     if (max_len > kSharesFrom)
         n += (size_t)prompt_slots() * (sizeof(PromptDesc) + 2 * sizeof(float) * TROWS * (c.head_dim + 3));
     return n;
+}
+
+cudaError_t launch_kv8_prefix(const Kv8AttnArgs& a, const SharedCall& s, cudaStream_t st) {
+    return a.view.head_dim == 128 ? launch_prefix<128>(a, s, st) : launch_prefix<64>(a, s, st);
 }
 
 cudaError_t launch_kv8_prompt(const Kv8AttnArgs& a, int short_rows, cudaStream_t st) {
