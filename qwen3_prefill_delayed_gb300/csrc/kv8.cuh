@@ -89,12 +89,13 @@ KV8_HD int kv8_most_seen(int max_len, int window, int sinks, int tokens) {
     return window > 0 && n < max_len ? (int)n : max_len;
 }
 // Tile `tile` of the n new tokens (of which max_new count) of a sequence of kv_len positions, over its positions from `prefix`
-// (whole blocks) on in units of 128 keys, in up to `splits` parts: its tokens t0 .. t0 + tokens - 1, the positions below the last
+// (whole blocks) on in units of 128 keys, in parts of `least` units or, where more than `splits` of
+// them would do, in `splits`: its tokens t0 .. t0 + tokens - 1, the positions below the last
 // of them, the blocks, the units of a part, and how many parts there are.
 struct Kv8Own {
     int t0, tokens, keys, blocks, per, parts;
 };
-KV8_HD Kv8Own kv8_own(int kv_len, int n, int tile, int tile_tokens, int max_new, int prefix, int splits) {
+KV8_HD Kv8Own kv8_own(int kv_len, int n, int tile, int tile_tokens, int max_new, int prefix, int splits, int least) {
     Kv8Own o;
     const int count = n < max_new ? n : max_new;
     o.t0 = tile * tile_tokens;
@@ -106,6 +107,7 @@ KV8_HD Kv8Own kv8_own(int kv_len, int n, int tile, int tile_tokens, int max_new,
     if (o.blocks < 0) o.blocks = 0;
     const int units = o.blocks > 0 ? (o.blocks + 7) / 8 : 1;
     o.per = (units + splits - 1) / splits;
+    if (o.per < least) o.per = least;
     o.parts = (units + o.per - 1) / o.per;
     return o;
 }

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
             b = blockIdx.y / s.row_tiles;
             head = blockIdx.x;
             kv8_rows(a.cu, b, a.total_rows, row0, n);
-            own = kv8_own(length(b), n, blockIdx.y - b * s.row_tiles, ROWS / G, a.max_new, s.shared[b].prefix, gridDim.z);
+            own = kv8_own(length(b), n, blockIdx.y - b * s.row_tiles, ROWS / G, a.max_new, s.shared[b].prefix, gridDim.z, kOwnUnits);
             if (own.tokens == 0 || blockIdx.z >= own.parts) return;
             i0 = blockIdx.z * own.per;
             i1 = i0 + own.per;

@@ -36,22 +36,30 @@ struct Slot {
     static constexpr int FLOATS = ROWS * (HD + 3);
 };
 
-// Shared prefixes (kv8_shared.cu).  Of batch row b: the positions that it reads through its group's first row, the group's
-// first (query tile, group) pair, first packed row and key tiles.
+// Shared prefixes (kv8_shared.cu).  A unit: part of the key tiles of one (query tile, group, kv head).
+struct PrefixUnit {
+    int b, row0, n, q_lo;             // the group's first row, its tokens' packed rows, the tile's first token
+    int keys, head, t_first, count;   // the prefix, and the unit's tiles (0: no unit)
+};
+// Of batch row b: the positions that it reads through its group's first row, the group's first unit and packed row, and the
+// units of each (query tile, kv head).
 struct SharedRow {
-    int prefix, pair0, row0, tiles;
+    int prefix, unit0, row0, parts;
 };
 // What the kernels of one call share in scratch.
 struct SharedCall {
-    int32_t* list;       // [0] = pairs, [2..3] all items' tiles, records from word 8 on (as for prompts)
+    PrefixUnit* units;   // [most_units]; unit u is CTA u % prefix_grid's
+    int32_t* n_units;
     SharedRow* rows;     // [batch]
-    float* prefix_parts; // PromptSlots: two for each CTA, then one for each item that lies inside a CTA's share
+    float* prefix_parts; // PromptSlots: [most_units]
     float* own_parts;    // Slots: [batch][row_tiles][n_kv][splits]
-    int prefix_grid, row_tiles, splits, most_pairs;
+    int prefix_grid, most_units, row_tiles, splits;
 };
 cudaError_t launch_kv8_prefix(const Kv8AttnArgs& a, const SharedCall& c, cudaStream_t st);   // kv8_prompt.cu
 cudaError_t launch_kv8_own(const Kv8AttnArgs& a, const SharedCall& c, cudaStream_t st);      // kv8_attention.cu
 cudaError_t launch_kv8_shared(const Kv8AttnArgs& a, cudaStream_t st);                        // kv8_shared.cu
+// Units of 128 keys that a CTA takes of a row's own positions at least.  (64 rows of 15-1000 positions: TODO)
+constexpr int kOwnUnits = 2;
 // Whether a call's prefixes are read once; if not, launch_kv8_attention goes row by row.
 bool kv8_shares(const Kv8View& c, int batch, int nq, int max_new, int groups, int max_prefix);
 // Rows of a short sequence's tile: one n = 8 column group of the MMAs while its (position, head) rows fit, else two.

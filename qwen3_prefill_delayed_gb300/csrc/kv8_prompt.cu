@@ -105,6 +105,8 @@ struct PromptArgs {
     long long row_stride;
     bf16* out;
     const int32_t* list;    // [0] = pairs, [2..3] all items' tiles, records from word 8 on
+    const PrefixUnit* units;   // a shared prefix: the CTAs' work, in place of the list
+    const int32_t* n_units;
     PromptDesc* desc;       // equal shares (null: snake order)
     float* parts;
     float scale_log2;
@@ -182,6 +184,9 @@ __device__ __noinline__ void look_again(const PromptArgs& p, const PromptRec& r,
     const bf16* q = p.q + (long long)(r.row0 + r.q_lo + qi) * p.row_stride + (long long)(head * p.G + hq) * p.view.head_dim;
     const int end = r.kv_len - r.n + r.q_lo + qi + 1, lo = p.window > 0 ? end - p.window : 0;
     kv8_row_again(p.view, q, r.b, head, end, r.keys, dim, n, p.scale_log2, out, lo, p.sinks, max(0, lo - qi));
+}
+__device__ __forceinline__ uint4 as_uint4(float a, float b, float c, float d) {
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
 }
 __device__ __forceinline__ int snake(int k) {
     return k * (int)gridDim.x + ((k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
@@ -442,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     auto bar = [&](int i) { return smem_u32(bars + i); };
     const Kv8View& c = p.view;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_items = p.list[0] * c.n_kv;
+    const int n_items = MODE == kPrefix ? *p.n_units : p.list[0] * c.n_kv;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBARS; ++i) {
@@ -452,10 +457,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         *abort_flag = 0;
         *issued = 0;
         *nan_out = 0;
-        if (MODE == kPrefix || p.desc != nullptr) {
+        if (MODE != kPrefix && p.desc != nullptr) {
             const long long all = *reinterpret_cast<const long long*>(p.list + 2);
             const long long share = (all + gridDim.x - 1) / gridDim.x, u = blockIdx.x * share;
-            if (MODE != kPrefix) p.desc[blockIdx.x].row0 = -1;
+            p.desc[blockIdx.x].row0 = -1;
             first_s[0] = first_s[1] = 0;
             first_s[2] = (int)max(0LL, min(share, all - u));
             if (u < all) {
@@ -488,13 +493,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     const uint32_t tS = slots[0], tO = tS + 2 * TK;   // two S buffers, then O
     // Items k = 0, 1, ... of this CTA; the next one's record is on its way while one is worked on.  Every role calls
     // item(0), item(1), ... until there is none.
-    const bool shares = MODE == kPrefix || p.desc != nullptr;
+    const bool shares = MODE != kPrefix && p.desc != nullptr;
     int left = shares ? first_s[2] : 0;   // tiles of the share
     int4 next_x = make_int4(0, 0, 0, 0), next_y = next_x;
-    auto index = [&](int k) { return shares ? first_s[0] + k : snake(k); };
+    auto index = [&](int k) { return MODE == kPrefix ? (int)blockIdx.x + k * (int)gridDim.x : shares ? first_s[0] + k : snake(k); };
     auto fetch = [&](int k) {
         const int i = index(k);
-        if (i < n_items) {
+        if (MODE == kPrefix && (k == 0 || i < n_items)) {   // (there is a unit for every CTA, if an empty one)
+            const int4* at = reinterpret_cast<const int4*>(p.units + i);
+            next_x = at[0];
+            next_y = at[1];
+        } else if (MODE != kPrefix && i < n_items) {
             const int4* at = reinterpret_cast<const int4*>(p.list + kRecWords * (1 + (long long)(i / c.n_kv)));
             next_x = at[0];
             next_y = at[1];
@@ -509,14 +518,20 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     };
     auto item = [&](int k, PromptRec& r, int& head) {   // its count, 0 when there is none
         const int i = index(k);
-        if (i >= n_items || (shares && left == 0)) return 0;
-        head = i % c.n_kv;
+        if (MODE == kPrefix ? k > 0 && i >= n_items : i >= n_items || (shares && left == 0)) return 0;
+        head = MODE == kPrefix ? next_y.y : i % c.n_kv;
         r.b = next_x.x;
         r.row0 = next_x.y;
         r.n = next_x.z;
         r.q_lo = next_x.w;
         r.kv_len = next_y.x;
-        r.keys = next_y.y;
+        r.keys = MODE == kPrefix ? next_y.x : next_y.y;
+        if (MODE == kPrefix) {
+            t_first = next_y.z;
+            const int n = next_y.w;
+            fetch(k + 1);
+            return n;
+        }
         fetch(k + 1);
         if (MODE == kWindow) skip = skipped(r, p.window, p.sinks);
         t_all = key_tiles(r.keys) - skip.by;
@@ -710,15 +725,22 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             if (!ok) break;
             tc_fence_after();
             if (MODE == kPrefix || (shares && n_kt < t_all)) {   // a part: the sums as they are
-                const long long slot = MODE == kPrefix && n_kt == t_all ? 2LL * gridDim.x + index(k) : 2LL * blockIdx.x + (t_first == 0 ? 1 : 0);
+                const long long slot = MODE == kPrefix ? index(k) : 2LL * blockIdx.x + (t_first == 0 ? 1 : 0);
                 float* part = p.parts + slot * PromptSlot<HD>::FLOATS;
 #pragma unroll 1
                 for (int ch = 0; ch < HD; ch += 32) {
                     float o[32];
                     tmem_ld32(lO + ch, o);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4*>(part + row * HD + ch + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    for (int e = 0; e < 32; e += 8) {
+                        float* to = part + row * HD + ch + e;
+                        if (MODE != kPrefix) {
+                            *reinterpret_cast<float4*>(to) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            *reinterpret_cast<float4*>(to + 4) = make_float4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
+                        } else if (row_ok) {   // (32-byte aligned)
+                            st_global_32(to, as_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]), as_uint4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]));
+                        }
+                    }
                 }
                 part += TROWS * HD;
                 part[row] = m;
@@ -839,6 +861,15 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     if (p0 == 0 && it >= 1)
                         ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QE), (uint32_t)(it - 1) & 1u, abort_flag));
                     if (!ok) break;
+                    if (MODE == kPrefix && (w * 32 + p0 * RPP) / p.G >= r.n - r.q_lo) {   // no row of these has a token
+                        for (int y = 0; y < 4; ++y) {
+                            const int row = w * 32 + (p0 + y) * RPP + lane / LPR;
+                            *reinterpret_cast<uint4*>(smem + row * HD + (x << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4*>(smem + C::QB + row * HD + (x << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                            if (x == 0) qs[(it % NQS) * TROWS + row] = 1.f;
+                        }
+                        continue;
+                    }
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
                         const int row = w * 32 + (p0 + y) * RPP + lane / LPR;
@@ -1030,7 +1061,8 @@ cudaError_t launch_prefix(const Kv8AttnArgs& a, const SharedCall& s, cudaStream_
     p.view = a.view;
     p.q = a.q;
     p.row_stride = a.row_stride;
-    p.list = s.list;
+    p.units = s.units;
+    p.n_units = s.n_units;
     p.parts = s.prefix_parts;
     p.scale_log2 = a.scale_log2;
     p.nq = a.nq;

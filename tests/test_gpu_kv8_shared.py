@@ -12,9 +12,17 @@ pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
 
 
+LEAST = 96 << 20     # bytes that reading a prefix once has to save, by the call's bounds, before it is done
+
+
+def wide(H, D, P, rows, groups):
+    """Pages of a table row whose positions, as the bound of a prefix, make any call worth sharing."""
+    return LEAST // (2 * H * D * P * max(1, rows - groups)) + 1
+
+
 def shared(group_cu, prefix, lens, H, D, P, seed=0, **kw):
     """A cache whose rows of a group list their first row's pages for the prefix's whole pages."""
-    c = build(lens, H=H, D=D, P=P, seed=seed, **kw)
+    c = build(lens, H=H, D=D, P=P, seed=seed, width=wide(H, D, P, len(lens), len(prefix)), **kw)
     for g, p in enumerate(prefix):
         for b in range(group_cu[g] + 1, group_cu[g + 1]):
             c["table"][b, :p // P] = c["table"][group_cu[g], :p // P]
@@ -22,7 +30,7 @@ def shared(group_cu, prefix, lens, H, D, P, seed=0, **kw):
 
 
 def run(hra, c, kv, q, new, lens, group_cu, prefix, max_new=None, max_len=None, max_own=None, max_prefix=None, **kw):  # noqa: F811
-    reach = hra.Kv8Reach(groups=i32(group_cu).cuda(), prefix=i32(prefix).cuda(), max_prefix=max_prefix or max(prefix),
+    reach = hra.Kv8Reach(groups=i32(group_cu).cuda(), prefix=i32(prefix).cuda(), max_prefix=max_prefix or 1 << 30,
                          max_own=max_own)
     T = q.shape[0]
     out = torch.full((T + 2,) + q.shape[1:], 7.0, dtype=BF16, device="cuda")
@@ -36,14 +44,19 @@ def run(hra, c, kv, q, new, lens, group_cu, prefix, max_new=None, max_len=None, 
 def check(hra, c, new, lens, G, group_cu, prefix, errors=0, seed=3, **kw):  # noqa: F811
     H, D = c["codes"].shape[3], c["codes"].shape[5]
     T = sum(new)
-    wide = torch.randn(T, H * G + 1, D, generator=torch.Generator().manual_seed(seed)).to(BF16)
-    q = wide[:, 1:]
+    q = torch.randn(T, H * G + 1, D, generator=torch.Generator().manual_seed(seed)).to(BF16)[:, 1:]
     want, bound = R.attend(c, 0, q, cu_of(new), lens, split=True)
     kv = gpu(hra, c)
-    got = run(hra, c, kv, q, new, lens, group_cu, prefix, **kw)
-    over = float(((got.double() - want).abs() - bound).max())
-    assert over <= 0, f"{over:.3g} over the bound"      # (a NaN is not)
-    assert kv.device_error() == errors
+    for max_prefix in ((max(prefix), None) if "max_prefix" not in kw else (kw.pop("max_prefix"),)):   # row by row (mostly), and once
+        before = hra.hra_launch_counter()
+        got = run(hra, c, kv, q, new, lens, group_cu, prefix, max_prefix=max_prefix, **kw)
+        kernels = hra.hra_launch_counter() - before
+        over = float(((got.double() - want).abs() - bound).max())
+        assert over <= 0, f"{over:.3g} over the bound"      # (a NaN is not)
+        assert kv.device_error() == errors
+        kv.errors.zero_()
+    if max_prefix is None and len(prefix) < len(lens) and G * (kw.get("max_new") or max(new)) <= 64:
+        assert kernels == 4                                 # read once
     return got
 
 
@@ -90,8 +103,7 @@ def test_long_prefixes_and_many_rows(hra, H, G, D, P, rows, prefix):  # noqa: F8
     c = shared([0, rows], [prefix], lens, H, D, P, seed=rows)
     a = check(hra, c, [1] * rows, lens, G, [0, rows], [prefix], max_own=900)
     assert torch.equal(a, check(hra, c, [1] * rows, lens, G, [0, rows], [prefix], max_own=900))   # again: the same sums
-    # bounds that say nothing: other parts, the same values
-    check(hra, c, [1] * rows, lens, G, [0, rows], [prefix], max_prefix=1 << 30)
+    # another bound: other parts, the same values
     check(hra, c, [1] * rows, lens, G, [0, rows], [prefix], max_own=1)
 
 
@@ -113,27 +125,27 @@ def test_a_prefix_is_no_longer_than_what_its_rows_hold(hra):  # noqa: F811
     """Rows that hold less than the prefix, nothing, or fewer positions than new tokens: the group shares less or nothing."""
     for lens, new in (([300, 40, 300], [1, 1, 1]), ([300, 1, 300], [1, 1, 1]), ([300, 0, 300], [1, 1, 1]), ([64, 2, 64], [3, 3, 1]),
                       ([300, 0, 300], [1, 0, 1])):
-        c = build([300, 300, 300], H=2, D=64, P=16, seed=2)
+        c = build([300, 300, 300], H=2, D=64, P=16, seed=2, width=wide(2, 64, 16, 3, 1))
         c["table"][1:, :18] = c["table"][0, :18]
         check(hra, c, new, lens, 4, [0, 3], [288], max_len=300)
 
 
 def test_group_numbers_outside_the_batch_are_clamped(hra):  # noqa: F811
     lens = [100, 90, 80, 120]
-    c = build(lens, H=1, D=64, P=16, seed=2)
+    c = build(lens, H=1, D=64, P=16, seed=2, width=wide(1, 64, 16, 4, 3))
     c["table"][1:, :4] = c["table"][0, :4]
     for group_cu, prefix in (([-3, 2, 9], [64, 64]), ([0, 3, 1, 4], [64, 64, 64]), ([0, 4], [-5]), ([7, 9], [64]), ([2, 0], [64])):
-        check(hra, c, [1] * 4, lens, 2, group_cu, prefix, errors=hra.DEVERR_POS_RANGE, max_prefix=64)
+        check(hra, c, [1] * 4, lens, 2, group_cu, prefix, errors=hra.DEVERR_POS_RANGE, max_prefix=1 << 30)
 
 
 def test_packed_rows_out_of_order_stay_inside_the_workspace(hra):  # noqa: F811
     """cu that claims rows twice: no result is promised, and nothing outside the output is written."""
     lens = [100, 90, 80, 120]
-    c = build(lens, H=1, D=64, P=16, seed=2)
+    c = build(lens, H=1, D=64, P=16, seed=2, width=wide(1, 64, 16, 4, 3))
     c["table"][1:, :4] = c["table"][0, :4]
     kv = gpu(hra, c)
     q = torch.randn(4, 2, 64).to(BF16).cuda()
-    reach = hra.Kv8Reach(groups=i32([0, 2, 4]).cuda(), prefix=i32([64, 64]).cuda(), max_prefix=64)
+    reach = hra.Kv8Reach(groups=i32([0, 2, 4]).cuda(), prefix=i32([64, 64]).cuda())
     for cu in ([0, 4, 0, 4, 0], [4, 3, 2, 1, 0], [-7, 100, 2, 3, 4], [0, 1, 1, 1, 99]):
         need = kv.attention_workspace_size(4, 4, 2, 4, 120, reach)
         ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
@@ -150,9 +162,9 @@ def test_hidden_pages_and_clamped_lengths(hra, new):  # noqa: F811
     c["table"][:, 3] = -1
     c["table"][1, 9] = 1 << 20
     check(hra, c, new, lens, 2, [0, 3], [128], errors=hra.DEVERR_PAGE_RANGE)
-    c = build([96, 96, 96], H=1, D=64, P=16, width=6)
+    c = build([96, 96, 96], H=1, D=64, P=16, width=wide(1, 64, 16, 3, 1))
     c["table"][:, :2] = c["table"][0, :2]
-    check(hra, c, new, [100, 70, 96], 2, [0, 3], [32], errors=hra.DEVERR_POS_RANGE, max_len=96)
+    check(hra, c, new, [96, -70, 96], 2, [0, 3], [32], errors=hra.DEVERR_POS_RANGE, max_len=96)
 
 
 def test_tokens_beyond_max_new_get_no_output(hra):  # noqa: F811
@@ -162,7 +174,7 @@ def test_tokens_beyond_max_new_get_no_output(hra):  # noqa: F811
     kv = gpu(hra, c)
     want, bound = R.attend(c, 0, q, [0, 9, 11], lens, split=True)
     for max_new in (2, 5):
-        have = run(hra, c, kv, q, new, lens, [0, 2], [128], max_new=max_new)
+        have = run(hra, c, kv, q, new, lens, [0, 2], [128], max_new=max_new, max_len=200)
         assert kv.device_error() == hra.DEVERR_POS_RANGE
         rows = list(range(max_new)) + [9, 10]
         assert float(((have.double() - want).abs() - bound)[rows].max()) <= 0
@@ -218,13 +230,13 @@ def test_captured_and_replayed_with_other_groups(hra):  # noqa: F811
     """The device arrays are read at each replay: other groups, prefixes and lengths under the same bounds."""
     lens = [[300, 280, 290, 310], [200, 170, 290, 150]]
     groups = [([0, 4], [256]), ([0, 2], [160])]
-    c = build([320] * 4, H=2, D=64, P=16, seed=7)
+    c = build([320] * 4, H=2, D=64, P=16, seed=7, width=wide(2, 64, 16, 4, 1))
     c["table"][1:, :16] = c["table"][0, :16]
     kv = gpu(hra, c)
     q = torch.randn(4, 8, 64, generator=torch.Generator().manual_seed(1)).to(BF16)
     cu, kl, qg = i32(range(5)).cuda(), i32(lens[0]).cuda(), q.cuda()
     g, p = i32(groups[0][0]).cuda(), i32(groups[0][1]).cuda()
-    reach = hra.Kv8Reach(groups=g, prefix=p, max_prefix=256, max_own=200)
+    reach = hra.Kv8Reach(groups=g, prefix=p, max_own=200)
     out = torch.zeros_like(qg)
     ws = torch.empty(kv.attention_workspace_size(4, 4, 8, 1, 320, reach), dtype=torch.uint8, device="cuda")
     kv.attend(0, qg, cu, kl, 1, 320, out=out, workspace=ws, reach=reach)
@@ -245,7 +257,7 @@ def test_calls_at_once_with_workspaces_of_their_own(hra):  # noqa: F811
     lens = [3000 + i for i in range(8)]
     c = shared([0, 8], [2048], lens, 2, 128, 64, seed=3)
     kv = gpu(hra, c)
-    reach = hra.Kv8Reach(groups=i32([0, 8]).cuda(), prefix=i32([2048]).cuda(), max_prefix=2048, max_own=1000)
+    reach = hra.Kv8Reach(groups=i32([0, 8]).cuda(), prefix=i32([2048]).cuda(), max_own=1000)
     cu, kl = i32(range(9)).cuda(), i32(lens).cuda()
     qs = [torch.randn(8, 8, 128, generator=torch.Generator().manual_seed(i)).to(BF16).cuda() for i in range(4)]
     alone = [kv.attend(0, q, cu, kl, 1, 3008, reach=reach) for q in qs]
