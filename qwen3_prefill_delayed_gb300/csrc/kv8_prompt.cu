@@ -88,7 +88,7 @@ struct Cfg {
     static constexpr int OFF_BAR = OFF_V + 2 * VB;
     static constexpr int OFF_SC = OFF_BAR + 320;             // [NSC][3][NB]: K scale, V scale's exponent and factor
     static constexpr int OFF_QS = OFF_SC + NSC * 3 * NB * 4; // [NQS][TROWS] q scales
-    static constexpr int OFF_TH = OFF_QS + NQS * TROWS * 4;  // [NSC] whether a tile's blocks are all there
+    static constexpr int OFF_TH = OFF_QS + NQS * TROWS * 4;  // [NSC] a tile's blocks that are there, a bit each
     static constexpr int SMEM = OFF_TH + NSC * 4;
     static constexpr int ALLOC = SMEM + 1024;           // the base is aligned up to 1024 bytes
     // tile g: K stage g % NK, S / P / V buffer g & 1, scales g % NSC; item it: q scales it % NQS
@@ -160,6 +160,11 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st8_async(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 // the maxima of columns 0 .. 15 and 16 .. 31 of each lane's row (the columns themselves are dropped)
 __device__ __forceinline__ void tmem_max32(uint32_t taddr, float& top0, float& top1) {
     float v[16], w[16];
@@ -198,20 +203,25 @@ __device__ __forceinline__ int snake(int k) {
 // mx: the maximum of s; Mx: the maximum of s + log2 of the block's V scale.  The loads themselves take the maximum of a
 // block's 16 scores (chunks after many positions: 353 us by max instructions, 339 so; holding the scores for the weights
 // meanwhile spills, 494).
+template <int MODE>
+__device__ __forceinline__ float coef_of(float q_unscale, float k) {   // window: positive, so that -inf stays what it is
+    const float c = q_unscale * k;
+    return MODE == kWindow && c < 0x1p-126f ? 0x1p-126f : c;
+}
+template <int MODE>
 __device__ __forceinline__ void max_pass_whole(uint32_t lS, const float* ks, float q_unscale, float& mx, float& Mx) {
 #pragma unroll
     for (int ch = 0; ch < TK / 32; ++ch) {
         float top0, top1;
         const float2 k2 = *reinterpret_cast<const float2*>(ks + 2 * ch), e2 = *reinterpret_cast<const float2*>(ks + NB + 2 * ch);
         tmem_max32(lS + 32 * ch, top0, top1);
-        const float z0 = top0 * (q_unscale * k2.x), z1 = top1 * (q_unscale * k2.y);
+        const float z0 = top0 * coef_of<MODE>(q_unscale, k2.x), z1 = top1 * coef_of<MODE>(q_unscale, k2.y);
         mx = max3(mx, z0, z1);
         Mx = max3(Mx, z0 + e2.x, z1 + e2.y);
     }
 }
-template <int MODE>
-__device__ __forceinline__ void max_pass_masked(uint32_t lS, const float* ks, float q_unscale, int limit, int lo, int sinks,
-                                                float& mx, float& Mx) {
+__device__ __forceinline__ void max_pass_masked(uint32_t lS, const float* ks, float q_unscale, int limit, float& mx,
+                                                float& Mx) {
 #pragma unroll 1
     for (int ch = 0; ch < TK / 32; ++ch) {
         float a[32];
@@ -223,7 +233,7 @@ __device__ __forceinline__ void max_pass_masked(uint32_t lS, const float* ks, fl
             const int n = k >= 0.f ? limit - 32 * ch - 16 * h : 0;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                if (e >= n || (MODE == kWindow && e < lo - 32 * ch - 16 * h && e >= sinks - 32 * ch - 16 * h)) a[16 * h + e] = -INFINITY;
+                if (e >= n) a[16 * h + e] = -INFINITY;
             float top[2] = {fmaxf(a[16 * h], a[16 * h + 1]), fmaxf(a[16 * h + 2], a[16 * h + 3])};
 #pragma unroll
             for (int e = 4; e < 16; e += 2) top[(e >> 1) & 1] = max3(top[(e >> 1) & 1], a[16 * h + e], a[16 * h + e + 1]);
@@ -237,8 +247,8 @@ __device__ __forceinline__ void max_pass_masked(uint32_t lS, const float* ks, fl
 // The weights: l's terms 2^(s - mr) are returned summed; times the block's V scale and 2^(mr - Mr + 11)
 // (`up` its exponent) they go as f16 to columns 16 ch, which this row has read.
 template <bool MASK, int MODE>
-__device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float q_unscale, int limit, int lo, int sinks,
-                                             float mr, float up) {
+__device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float q_unscale, int limit, float mr,
+                                             float up) {
     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float2 neg = make_float2(-mr, -mr);
 #pragma unroll 1
@@ -251,7 +261,7 @@ __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const float k = h ? k2.y : k2.x, ev = h ? e2.y : e2.x;
-            const float coef = q_unscale * k;
+            const float coef = coef_of<MODE>(q_unscale, k);
             const float f = ex2(fminf(up + ev, 126.f)) * (h ? m2.y : m2.x);
             const int n = MASK ? (k >= 0.f ? limit - 32 * ch - 16 * h : 0) : 16;
             const float2 coef2 = make_float2(coef, coef), f2 = make_float2(f, f);
@@ -260,9 +270,8 @@ __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float
                 const float2 z = fma2(make_float2(a[16 * h + e], a[16 * h + e + 1]), coef2, neg);
                 float2 x = make_float2(ex2(z.x), ex2(z.y));
                 if (MASK) {
-                    const int l = lo - 32 * ch - 16 * h, s = sinks - 32 * ch - 16 * h;
-                    if (e >= n || (MODE == kWindow && e < l && e >= s)) x.x = 0.f;
-                    if (e + 1 >= n || (MODE == kWindow && e + 1 < l && e + 1 >= s)) x.y = 0.f;
+                    if (e >= n) x.x = 0.f;
+                    if (e + 1 >= n) x.y = 0.f;
                 }
                 ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], x);
                 const float2 y = mul2(x, f2);
@@ -272,6 +281,24 @@ __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float
         tmem_st16_async(lS + 16 * ch, w);
     }
     return (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+}
+
+// A tile at a window's edge: the scores that a row does not see become -inf where they are, and the passes above go over it like
+// over any other (passes with masks of their own, run once an item, wait for their instructions: 2.4 us a tile, and 0.9 for the
+// others).  seen: keys [lo, limit) and those below sinks, relative to the tile's first; there: blocks that are.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+__device__ __forceinline__ void hide_unseen(uint32_t lS, int limit, int lo, int sinks, uint32_t there) {
+#pragma unroll 1
+    for (int ch = 0; ch < TK / 32; ++ch, limit -= 32, lo -= 32, sinks -= 32, there >>= 2) {
+        const uint32_t blocks = (there & 1u ? 0xFFFFu : 0u) | (there & 2u ? 0xFFFF0000u : 0u);
+        const uint32_t seen = bits_below(limit) & (~bits_below(lo) | bits_below(sinks)) & blocks;
+        float a[32];
+        tmem_ld32(lS + 32 * ch, a);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (!(seen & (1u << e))) a[e] = -INFINITY;
+        tmem_st32(lS + 32 * ch, a);
+    }
 }
 
 // One CTA.  The non-empty (query tile, sequence) pairs: by a counting sort, most key tiles first, or, for equal shares,
@@ -511,8 +538,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     };
     int t_first = 0, t_all = 0;                         // this item's tiles [t_first, t_first + count) of t_all
     Kv8Skip skip{0, 0};
+    int rotate = 0;
     // the first key of the item's tile t of this CTA, and whether some row sees any of the 16 keys from pos on
-    auto tile_key = [&](int t) { return (MODE != kWindow ? t_first + t : kv8_unit_at(skip, t_first + t)) * TK; };
+    auto tile_key = [&](int t) {
+        int i = t_first + t;
+        if (MODE == kWindow) {   // from the first tile behind the window's edge on, the edge and the sinks last: the maxima then
+            i += rotate;         // start from a whole tile and seldom move
+            if (i >= t_all) i -= t_all;
+            i = kv8_unit_at(skip, i);
+        }
+        return i * TK;
+    };
     auto in_sight = [&](const PromptRec& r, int pos) {
         return MODE != kWindow || pos < p.sinks || pos + kKv8Block > r.kv_len - r.n + r.q_lo + 1 - p.window;
     };
@@ -533,7 +569,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             return n;
         }
         fetch(k + 1);
-        if (MODE == kWindow) skip = skipped(r, p.window, p.sinks);
+        if (MODE == kWindow) {
+            skip = skipped(r, p.window, p.sinks);
+            rotate = r.kv_len - r.n + r.q_lo >= p.window ? skip.from + 1 : 0;
+        }
         t_all = key_tiles(r.keys) - skip.by;
         if (!shares) return t_all;
         t_first = k == 0 ? first_s[1] : 0;
@@ -573,14 +612,16 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const bool want = lane < NB && page >= 0;
                 const int pos = tile_key(t) + blk * kKv8Block;
                 if (lane < NB && pos < r.keys && page < 0 && in_sight(r, pos)) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
+                if (MODE == kWindow && s < 0.f) s = 1.f;   // absent: `there` says so
                 if (lane < NB) {
                     sc[(g % NSC) * 3 * NB + blk] = s;
                 } else if (lane < 2 * NB) {
                     sc[((g % NSC) * 3 + 1) * NB + blk] = exponent_of(s);
                     sc[((g % NSC) * 3 + 2) * NB + blk] = mantissa_of(s);
                 }
-                const int boxes = __popc(__ballot_sync(0xffffffffu, want));
-                if (lane == 0) there[g % NSC] = boxes == NB;
+                const uint32_t wanted = __ballot_sync(0xffffffffu, want);
+                const int boxes = __popc(wanted);
+                if (lane == 0) there[g % NSC] = (int)wanted;
                 __syncwarp();   // the scales are written
                 if (lane == 0) {
                     *issued = g + 1;
@@ -668,8 +709,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             const int first = MODE == kPrefix ? r.keys - 1 : r.kv_len - r.n + r.q_lo;   // the last key of the first row
             const int limit = row_ok ? first + (MODE == kPrefix ? 0 : qi) + 1 : 0;      // keys below it count
             const int clear = first + 1;                                                // ... for every row of the tile
-            const int lo = limit - p.window;                                      // window: the row's first key
-            const int lo_last = r.kv_len - r.n + min(r.n, r.q_lo + p.QT) - p.window;   // ... and the last row's
+            int lim_min = 0, lo_max = 0;   // window: of the warp's rows that count
+            if (MODE == kWindow) {
+                lim_min = __reduce_min_sync(0xffffffffu, row_ok ? limit : INT32_MAX);
+                lo_max = __reduce_max_sync(0xffffffffu, row_ok ? limit - p.window : -(1 << 30));
+            }
             ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QS + it % NQS), (uint32_t)(it / NQS) & 1u, abort_flag));
             if (!ok) break;
             const float q_unscale = qs[(it % NQS) * TROWS + row] * p.scale_log2;
@@ -683,13 +727,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const uint32_t lS = lS0 + (g & 1) * TK;
                 const float* ks = sc + (g % NSC) * 3 * NB;   // then the V exponents and factors
                 const int j0 = tile_key(t);
-                const bool whole = j0 + TK <= clear && there[g % NSC] != 0 &&   // every key counts for every row
-                                   (MODE != kWindow || j0 >= lo_last || j0 + TK <= p.sinks);
+                const int blocks = there[g % NSC];
+                // every key counts for every row (window: of the warp)
+                const bool whole = blocks == (1 << NB) - 1 &&
+                                   (MODE != kWindow ? j0 + TK <= clear
+                                                    : j0 + TK <= lim_min && (j0 >= lo_max || j0 + TK <= p.sinks));
+                if (MODE == kWindow && !whole) hide_unseen(lS, limit - j0, limit - p.window - j0, p.sinks - j0, (uint32_t)blocks);
                 float mx = -INFINITY, Mx = -INFINITY;
-                if (whole)
-                    max_pass_whole(lS, ks, q_unscale, mx, Mx);
+                if (MODE == kWindow || whole)
+                    max_pass_whole<MODE>(lS, ks, q_unscale, mx, Mx);
                 else
-                    max_pass_masked<MODE>(lS, ks, q_unscale, limit - j0, lo - j0, p.sinks - j0, mx, Mx);
+                    max_pass_masked(lS, ks, q_unscale, limit - j0, mx, Mx);
                 const float mn = fmaxf(m, mx);
                 const float mr = mn == -INFINITY ? 0.f : mn;
                 l *= ex2(m - mr);
@@ -712,8 +760,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     }
                 }
                 const float up = mr - Mr + kUnit;
-                l += whole ? weight_pass<false, MODE>(lS, ks, q_unscale, 0, 0, 0, mr, up)
-                           : weight_pass<true, MODE>(lS, ks, q_unscale, limit - j0, lo - j0, p.sinks - j0, mr, up);
+                l += MODE == kWindow || whole ? weight_pass<false, MODE>(lS, ks, q_unscale, 0, mr, up)
+                                              : weight_pass<true, MODE>(lS, ks, q_unscale, limit - j0, mr, up);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
@@ -836,20 +884,20 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                         }
                 }
             };
-            int page = page_of(0), page1 = page_of(1);
+            int page = -1, page1 = -1;
             {   // Q: hi and lo codes of rows 32 w .. 32 w + 31, LPR lanes a row, 16 elements a lane
                 int qi = qi_first, hq = hq_first;   // of this lane's row of a pass
-#pragma unroll 1
-                for (int p0 = 0; p0 < LPR; p0 += 4) {
-                    uint4 u[4][2];   // four passes in flight; the first ones while the item before still runs
+                constexpr int PIF = 2;              // passes in flight while as many are worked on: short code, run over and over
+                uint4 u[PIF][2], v[PIF][2];
+                auto fetch_q = [&](uint4(&to)[PIF][2]) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        u[y][0] = u[y][1] = make_uint4(0u, 0u, 0u, 0u);
+                    for (int y = 0; y < PIF; ++y) {
+                        to[y][0] = to[y][1] = make_uint4(0u, 0u, 0u, 0u);
                         if (qi < p.QT && r.q_lo + qi < r.n) {
                             const uint4* src = reinterpret_cast<const uint4*>(
                                 p.q + (long long)(r.row0 + r.q_lo + qi) * p.row_stride + (long long)(head * p.G + hq) * HD + 16 * x);
-                            u[y][0] = src[0];
-                            u[y][1] = src[1];
+                            to[y][0] = src[0];
+                            to[y][1] = src[1];
                         }
                         qi += rpp_qi;   // RPP rows on
                         hq += rpp_hq;
@@ -858,20 +906,22 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                             ++qi;
                         }
                     }
-                    if (p0 == 0 && it >= 1)
-                        ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QE), (uint32_t)(it - 1) & 1u, abort_flag));
-                    if (!ok) break;
-                    if (MODE == kPrefix && (w * 32 + p0 * RPP) / p.G >= r.n - r.q_lo) {   // no row of these has a token
-                        for (int y = 0; y < 4; ++y) {
-                            const int row = w * 32 + (p0 + y) * RPP + lane / LPR;
-                            *reinterpret_cast<uint4*>(smem + row * HD + (x << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                            *reinterpret_cast<uint4*>(smem + C::QB + row * HD + (x << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                            if (x == 0) qs[(it % NQS) * TROWS + row] = 1.f;
-                        }
-                        continue;
-                    }
+                };
+                fetch_q(v);   // the first ones while the item before still runs
+                page = page_of(0);   // (behind them: a page number is waited for where it is checked)
+                page1 = page_of(1);
+                if (it >= 1) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QE), (uint32_t)(it - 1) & 1u, abort_flag));
+                if (!ok) break;
+#pragma unroll 1
+                for (int p0 = 0; p0 < LPR; p0 += PIF) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
+                    for (int y = 0; y < PIF; ++y) {
+                        u[y][0] = v[y][0];
+                        u[y][1] = v[y][1];
+                    }
+                    if (p0 + PIF < LPR) fetch_q(v);
+#pragma unroll
+                    for (int y = 0; y < PIF; ++y) {
                         const int row = w * 32 + (p0 + y) * RPP + lane / LPR;
                         const uint32_t in[8] = {u[y][0].x, u[y][0].y, u[y][0].z, u[y][0].w,
                                                 u[y][1].x, u[y][1].y, u[y][1].z, u[y][1].w};
@@ -890,11 +940,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                             uint32_t hc[2], lc[2];
 #pragma unroll
                             for (int z = 0; z < 2; ++z) {   // q / s fits f16 exactly, but for what is under 2^-25
-                                const uint32_t v = pack_h2(__uint_as_float(in[e + z] << 16) * inv,
+                                const uint32_t f = pack_h2(__uint_as_float(in[e + z] << 16) * inv,
                                                            __uint_as_float(in[e + z] & 0xFFFF0000u) * inv);
-                                hc[z] = f16x2_e4m3x2(v);
+                                hc[z] = f16x2_e4m3x2(f);
                                 const uint32_t back = e4m3x2_f16x2(hc[z]);
-                                const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&back));
+                                const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&f), *reinterpret_cast<const __half2*>(&back));
                                 lc[z] = f16x2_e4m3x2(*reinterpret_cast<const uint32_t*>(&d));
                             }
                             hi[e >> 1] = __byte_perm(hc[0], hc[1], 0x5410);
@@ -918,6 +968,16 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             request(raw[0], 0, page);
             request(raw[1], 1, page1);
             page = page_of(2);
+            // the next item's queries to the L2 meanwhile
+            if (index(k + 1) < n_items && (!shares || left > 0)) {
+                const int row = w * 32 + lane, qi = row / p.G, hq = row - qi * p.G;
+                const int at = next_x.w + qi, h = MODE == kPrefix ? next_y.y : index(k + 1) % c.n_kv;
+                if (qi < p.QT && at < next_x.z) {
+                    const bf16* q = p.q + (long long)(next_x.y + at) * p.row_stride + (long long)(h * p.G + hq) * HD;
+                    prefetch_l2(q);
+                    if (HD == 128) prefetch_l2(q + 64);
+                }
+            }
             // tile t from v, tile t + 2 into it
             auto turn = [&](uint4(&v)[2 * HALVES], int t) {
                 if (g >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV + (g & 1)), (uint32_t)((g >> 1) - 1) & 1u, abort_flag));
