@@ -246,6 +246,11 @@ int hra_kv8_attention_reach(const hra_kv8_cache* cache, int32_t layer, const voi
     const size_t q_row = 2 * (size_t)n_q_heads * c.head_dim;
     if (overlap({q_dev, 2 * (size_t)q_row_stride * (total_rows - 1) + q_row}, {out_dev, q_row * total_rows}))
         return HRA_ERR_INVALID_ARG;
+    if (reach != nullptr && reach->groups > 0) {   // nor what the groups are read from
+        const Range in[2] = {{reach->group_cu_dev, 4 * ((size_t)reach->groups + 1)}, {reach->prefix_dev, 4 * (size_t)reach->groups}};
+        for (const Range& r : in)
+            if (overlap(r, {workspace, workspace_bytes}) || overlap(r, {out_dev, q_row * total_rows})) return HRA_ERR_INVALID_ARG;
+    }
     a.q = reinterpret_cast<const bf16*>(q_dev);
     a.row_stride = q_row_stride;
     a.out = reinterpret_cast<bf16*>(out_dev);
