@@ -27,23 +27,40 @@ constexpr int kMostParts = 32;  // of a prefix: what the lanes of a joining warp
 // 64 after 1024 (132 MB) 38 / 39; 8 groups of 6 after 1024 (84 MB) 34 / 34, after 2048 39 / 47; 64 rows after 16384 59 / 330.
 // Tokens of more than 8 rows take twice as long row by row: 16 rows of 8 tokens after 2048 (63 MB) 40 / 49.
 constexpr long long kLeastSaved = 96LL << 20;
+constexpr int kHeldRows = 1024; // rows whose lengths the plan holds in shared memory
 constexpr int kOwnSplits = 8;   // most CTAs that a row's own positions are split over
 
 __global__ void __launch_bounds__(1024) kv8_shared_plan_kernel(const Kv8AttnArgs a, int QT, const SharedCall s) {
     pdl_launch();
     pdl_wait();
     __shared__ int first_s[kKv8MaxGroups + 1];   // the groups' first rows, made ascending
-    __shared__ int prefix_s[kKv8MaxGroups], row0_s[kKv8MaxGroups], n_s[kKv8MaxGroups];
+    __shared__ int prefix_s[kKv8MaxGroups], row0_s[kKv8MaxGroups], n_s[kKv8MaxGroups], pairs_s[kKv8MaxGroups];
     const Kv8View& c = a.view;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int room = c.max_pages << c.page_shift;
-    for (int b = threadIdx.x; b < a.batch; b += 1024) s.rows[b] = SharedRow{0, 0, 0, 0};
+    const int threads = blockDim.x, warps = threads >> 5;
+    // every array at once, where they fit: one way to memory and back
+    const bool held = a.batch <= kHeldRows;
+    __shared__ int cu_s[kHeldRows + 1], len_s[kHeldRows];
+    if (held)
+        for (int b = threadIdx.x; b <= a.batch; b += threads) {
+            cu_s[b] = a.cu[b];
+            if (b < a.batch) len_s[b] = a.kv_len[b];
+        }
+    for (int g = threadIdx.x; g <= a.groups; g += threads) {
+        first_s[g] = a.group_cu[g];
+        if (g < a.groups) prefix_s[g] = a.prefix[g];
+    }
+    for (int b = threadIdx.x; b < a.batch; b += threads) s.rows[b] = SharedRow{0, 0, 0, 0};
+    const int32_t* const cu = held ? cu_s : a.cu;
+    const int32_t* const kv_len = held ? len_s : a.kv_len;
+    __syncthreads();
     if (warp == 0) {
         int run = 0;
         bool bad = false;
         for (int i0 = 0; i0 <= a.groups; i0 += 32) {
             const int i = i0 + lane;
-            const int at = i <= a.groups ? a.group_cu[i] : 0;
+            const int at = i <= a.groups ? first_s[i] : 0;
             int v = min(a.batch, max(0, at));
             bad |= i <= a.groups && v != at;
             const int mine = v;
@@ -61,16 +78,16 @@ __global__ void __launch_bounds__(1024) kv8_shared_plan_kernel(const Kv8AttnArgs
     }
     __syncthreads();
     // a warp a group: no row reads more of the prefix than it holds before its new tokens
-    for (int g = warp; g < a.groups; g += 32) {
+    for (int g = warp; g < a.groups; g += warps) {
         const int b0 = first_s[g], b1 = first_s[g + 1];
-        int least = a.prefix[g], rows = 0;
-        int lo = a.cu[b0], hi = a.cu[b1];
+        int least = prefix_s[g], rows = 0;
+        int lo = cu[b0], hi = cu[b1];
         if (lane == 0 && least < 0) raise_error(c.err, HRA_DEVERR_POS_RANGE);
         for (int b = b0 + lane; b < b1; b += 32) {
             int row0, n;
-            kv8_rows(a.cu, b, a.total_rows, row0, n);
+            kv8_rows(cu, b, a.total_rows, row0, n);
             if (n > 0) {
-                least = min(least, min(room, max(0, a.kv_len[b])) - n);
+                least = min(least, min(room, max(0, kv_len[b])) - n);
                 ++rows;
             }
         }
@@ -82,6 +99,7 @@ __global__ void __launch_bounds__(1024) kv8_shared_plan_kernel(const Kv8AttnArgs
             prefix_s[g] = max(0, least) >> c.page_shift << c.page_shift;
             row0_s[g] = lo;
             n_s[g] = prefix_s[g] > 0 ? hi - lo : 0;
+            pairs_s[g] = (n_s[g] + QT - 1) / QT;
         }
     }
     __syncthreads();
@@ -91,7 +109,7 @@ __global__ void __launch_bounds__(1024) kv8_shared_plan_kernel(const Kv8AttnArgs
     __shared__ int unit_s[kKv8MaxGroups], parts_s[kKv8MaxGroups];
     __shared__ int total_s;
     if (warp == 0) {
-        auto items_of = [&](int g) { return g < a.groups ? (long long)((n_s[g] + QT - 1) / QT) * c.n_kv : 0; };
+        auto items_of = [&](int g) { return g < a.groups ? (long long)pairs_s[g] * c.n_kv : 0; };
         long long items = 0, tiles = 0;
         for (int g = lane; g < a.groups; g += 32) {
             items += items_of(g);
@@ -148,7 +166,7 @@ __global__ void __launch_bounds__(1024) kv8_shared_plan_kernel(const Kv8AttnArgs
     }
     __syncthreads();
     const int total = total_s;
-    for (int u = threadIdx.x; u < max(total, s.prefix_grid); u += 1024) {
+    for (int u = threadIdx.x; u < max(total, s.prefix_grid); u += threads) {
         PrefixUnit unit{0, 0, 0, 0, 0, 0, 0, 0};
         if (u < total) {
             int lo = 0, hi = a.groups;   // the last group with a first unit <= u: it has units
@@ -167,33 +185,40 @@ __global__ void __launch_bounds__(1024) kv8_shared_plan_kernel(const Kv8AttnArgs
         to[0] = make_int4(unit.b, unit.row0, unit.n, unit.q_lo);
         to[1] = make_int4(unit.keys, unit.head, unit.t_first, unit.count);
     }
-    for (int x = warp; x < a.groups; x += 32) {
+    for (int x = warp; x < a.groups; x += warps) {
         if (prefix_s[x] == 0) continue;
         for (int b = first_s[x] + lane; b < first_s[x + 1]; b += 32) {
             int row0, n;
-            kv8_rows(a.cu, b, a.total_rows, row0, n);
+            kv8_rows(cu, b, a.total_rows, row0, n);
             if (n > 0 && row0 >= row0_s[x] && row0 + n <= row0_s[x] + n_s[x])
                 s.rows[b] = SharedRow{prefix_s[x], unit_s[x], row0_s[x], parts_s[x]};
         }
     }
 }
 
-// A CTA a (kv head, tile of a sequence's tokens), a warp a row of it: every load but the first few is free of the others, and
-// the first parts are on their way while the row's maxima are found.
+// A CTA a (kv head, tile of a sequence's tokens), a warp a row of it, or several that take its parts in turn: every load but the
+// first few is free of the others, and the first parts are on their way while the row's maxima are found.
 template <int HD, int NG>
 __global__ void __launch_bounds__(256 * NG) kv8_shared_join_kernel(const Kv8AttnArgs a, int G, int QT, const SharedCall s) {
     pdl_launch();
     pdl_wait();
     constexpr int ROWS = 8 * NG, E = HD / 32, AHEAD = 8;
     const Kv8View& c = a.view;
-    const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
     const int head = blockIdx.x, b = blockIdx.y / s.row_tiles;
     int row0, n;
     kv8_rows(a.cu, b, a.total_rows, row0, n);
     const int kv_len = min(c.max_pages << c.page_shift, max(0, a.kv_len[b]));
     const SharedRow sh = s.rows[b];
     const Kv8Own o = kv8_own(kv_len, n, blockIdx.y - b * s.row_tiles, ROWS / G, a.max_new, sh.prefix, s.splits, kOwnUnits);
-    if (r >= o.tokens * G) return;
+    const int rows = o.tokens * G;
+    if (rows == 0) return;
+    // warps a row: one where it has all parts on their way at once (with more, 4.6 -> 5.4 us at 8 groups of 4-8 rows); several
+    // where there are more parts (64 rows, 38 of a prefix of 16,001: 14 -> 10.9 us)
+    const int each = (sh.prefix > 0 ? sh.parts : 0) + o.parts <= AHEAD || rows > ROWS / 2 ? 1 : rows > ROWS / 4 ? 2 : 4;
+    const int r = (threadIdx.x >> 5) / each, sub = (threadIdx.x >> 5) % each;
+    __shared__ float acc_s[ROWS][HD + 1];   // a warp's sums and their l
+    if (r >= rows) return;   // (whole warps of rows that are not waited for)
     row0 += o.t0;
     const float* own = s.own_parts + ((long long)blockIdx.y * c.n_kv + head) * s.splits * Slot<HD, NG>::FLOATS;
     const int qi = r / G, hq = r - qi * G;
@@ -228,7 +253,7 @@ __global__ void __launch_bounds__(256 * NG) kv8_shared_join_kernel(const Kv8Attn
     float ahead[AHEAD][E];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k)
-        if (k < count) part(k, ahead[k]);
+        if (sub + k * each < count) part(sub + k * each, ahead[k]);
     float pm0 = -INFINITY, pl0 = 0.f, pM0 = -INFINITY;   // part `lane`'s
     if (lane < count) stats(lane, pm0, pl0, pM0);
     float m = pm0, M = pM0;
@@ -266,13 +291,28 @@ __global__ void __launch_bounds__(256 * NG) kv8_shared_join_kernel(const Kv8Attn
         if (i0 == 0) {
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k)
-                if (k < count) add(k, ahead[k]);
+                if (sub + k * each < here) add(sub + k * each, ahead[k]);
         }
 #pragma unroll 4
-        for (int i = i0 == 0 ? AHEAD : 0; i < here; ++i) {
+        for (int i = sub + (i0 == 0 ? AHEAD * each : 0); i < here; i += each) {
             float v[E];
             part(i0 + i, v);
             add(i, v);
+        }
+    }
+    if (each > 1) {   // the first warp of a row adds the others' sums, in order
+        float* mine = acc_s[r * each + sub];
+#pragma unroll
+        for (int e = 0; e < E; ++e) mine[lane * E + e] = acc[e];
+        if (lane == 0) mine[HD] = L;
+        // (the row's warps alone)
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + r), "r"(32 * each) : "memory");
+        if (sub != 0) return;
+        for (int k = 1; k < each; ++k) {
+            const float* other = acc_s[r * each + k];
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += other[lane * E + e];
+            L += other[HD];
         }
     }
     const float f = L == 0.f ? 0.f : exp2f(Mr - mr) / L;
@@ -349,7 +389,7 @@ cudaError_t launch_kv8_shared(const Kv8AttnArgs& a, cudaStream_t st) {
     s.rows = reinterpret_cast<SharedRow*>(take(a.batch * sizeof(SharedRow)));
     s.prefix_parts = reinterpret_cast<float*>(take(4ull * s.most_units * kTileRows * (c.head_dim + 3)));
     s.own_parts = reinterpret_cast<float*>(at);
-    if (!a.planned) HRA_LAUNCH(kv8_shared_plan_kernel, dim3(1), dim3(1024), 0, st, a, QT, s);
+    if (!a.planned) HRA_LAUNCH(kv8_shared_plan_kernel, dim3(1), dim3(a.batch <= 256 && a.groups <= 64 ? 256 : 1024), 0, st, a, QT, s);
     cudaError_t e = launch_kv8_prefix(a, s, st);
     if (e != cudaSuccess) return e;
     e = launch_kv8_own(a, s, st);
