@@ -103,7 +103,7 @@ struct SplitArgs {
     int whole;         // one item a CTA: blockIdx = (head, sequence)
     // behind a shared prefix: blockIdx = (head, tile of a sequence's tokens, split)
     const SharedRow* shared;
-    int row_tiles;
+    int row_tiles, own_units;
 };
 
 // Dims d and d + 1 of row r, written to dst, are or hold a NaN: see kv8_row_again.
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv8_attn_kernel(const __grid_c
             b = blockIdx.y / s.row_tiles;
             head = blockIdx.x;
             kv8_rows(a.cu, b, a.total_rows, row0, n);
-            own = kv8_own(length(b), n, blockIdx.y - b * s.row_tiles, ROWS / G, a.max_new, s.shared[b].prefix, gridDim.z, kOwnUnits);
+            own = kv8_own(length(b), n, blockIdx.y - b * s.row_tiles, ROWS / G, a.max_new, s.shared[b].prefix, gridDim.z, s.own_units);
             if (own.tokens == 0 || blockIdx.z >= own.parts) return;
             i0 = blockIdx.z * own.per;
             i1 = i0 + own.per;
@@ -824,6 +824,7 @@ cudaError_t launch_kv8_own(const Kv8AttnArgs& a, const SharedCall& c, cudaStream
     s.parts = c.own_parts;
     s.shared = c.rows;
     s.row_tiles = c.row_tiles;
+    s.own_units = c.own_units;
     const bool one = column_groups(s.G, a.max_new) == 1;
     if (a.view.head_dim == 128)
         return one ? launch_ng<128, 1, false, kOwn>(s, st, c.splits) : launch_ng<128, 2, false, kOwn>(s, st, c.splits);

@@ -54,12 +54,11 @@ struct SharedCall {
     float* prefix_parts; // PromptSlots: [most_units]
     float* own_parts;    // Slots: [batch][row_tiles][n_kv][splits]
     int prefix_grid, most_units, row_tiles, splits;
+    int own_units;       // of 128 keys, that a CTA takes of a row's own positions at least
 };
 cudaError_t launch_kv8_prefix(const Kv8AttnArgs& a, const SharedCall& c, cudaStream_t st);   // kv8_prompt.cu
 cudaError_t launch_kv8_own(const Kv8AttnArgs& a, const SharedCall& c, cudaStream_t st);      // kv8_attention.cu
 cudaError_t launch_kv8_shared(const Kv8AttnArgs& a, cudaStream_t st);                        // kv8_shared.cu
-// Units of 128 keys that a CTA takes of a row's own positions at least.  (64 rows of 15-1000 positions: TODO)
-constexpr int kOwnUnits = 2;
 // Whether a call's prefixes are read once; if not, launch_kv8_attention goes row by row.
 bool kv8_shares(const Kv8View& c, int batch, int nq, int max_new, int groups, int max_prefix);
 // Rows of a short sequence's tile: one n = 8 column group of the MMAs while its (position, head) rows fit, else two.

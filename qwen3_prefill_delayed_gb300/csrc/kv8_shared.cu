@@ -29,6 +29,11 @@ constexpr int kMostParts = 32;  // of a prefix: what the lanes of a joining warp
 constexpr long long kLeastSaved = 96LL << 20;
 constexpr int kHeldRows = 1024; // rows whose lengths the plan holds in shared memory
 constexpr int kOwnSplits = 8;   // most CTAs that a row's own positions are split over
+// Units of 128 keys that a CTA takes of a row's own positions at least: more where the CTAs are more than the SMs hold at
+// once.  The whole call with 2 / 4 units (8 kv heads of 128): 16 rows of 1000 own positions on one prefix (512 CTAs of 2) 38.8 / 40.9 us,
+// 32 rows of 500 (512) 41.6 / 42.5, 8 groups of 6 with 300 (768) 38.2 / 36.9 and with 700 (1152) 49.9 / 47.3, 64 rows of 2000 (4096)
+// 106 / 96.
+constexpr int kFewUnits = 2, kMoreUnits = 4, kManyCtas = 4;
 
 __global__ void __launch_bounds__(1024) kv8_shared_plan_kernel(const Kv8AttnArgs a, int QT, const SharedCall s) {
     pdl_launch();
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(256 * NG) kv8_shared_join_kernel(const Kv8Attn
     kv8_rows(a.cu, b, a.total_rows, row0, n);
     const int kv_len = min(c.max_pages << c.page_shift, max(0, a.kv_len[b]));
     const SharedRow sh = s.rows[b];
-    const Kv8Own o = kv8_own(kv_len, n, blockIdx.y - b * s.row_tiles, ROWS / G, a.max_new, sh.prefix, s.splits, kOwnUnits);
+    const Kv8Own o = kv8_own(kv_len, n, blockIdx.y - b * s.row_tiles, ROWS / G, a.max_new, sh.prefix, s.splits, s.own_units);
     const int rows = o.tokens * G;
     if (rows == 0) return;
     // warps a row: one where it has all parts on their way at once (with more, 4.6 -> 5.4 us at 8 groups of 4-8 rows); several
@@ -334,10 +339,10 @@ int row_tiles(int G, int max_new) {
     const int tokens = 8 * column_groups(G, max_new) / G;
     return (max_new + tokens - 1) / tokens;
 }
-// Parts of a row's own positions, of kOwnUnits units of 128 keys while so many CTAs do.
-int own_splits(int max_own) {
+// Parts of a row's own positions, of `least` units of 128 keys while so many CTAs do.
+int own_splits(int max_own, int least) {
     const long long units = std::max<long long>(1, ((long long)max_own + 127) / 128);
-    return (int)std::min<long long>((units + kOwnUnits - 1) / kOwnUnits, kOwnSplits);
+    return (int)std::min<long long>((units + least - 1) / least, kOwnSplits);
 }
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
 int prefix_grid() { return 2 * device_sm_count(); }
@@ -364,7 +369,7 @@ size_t kv8_shared_scratch_bytes(const Kv8View& c, int batch, int total_rows, int
     // also for calls that then share nothing, so that the size never falls
     const int G = nq / c.n_kv, most = std::min(max_new, std::max(1, kMostRows / G));
     const size_t units = (size_t)most_units(c, total_rows, G, groups);
-    const size_t slots = (size_t)batch * row_tiles(G, most) * c.n_kv * own_splits(max_own);
+    const size_t slots = (size_t)batch * row_tiles(G, most) * c.n_kv * own_splits(max_own, kFewUnits);
     n = up(n) + 512 + up(units * sizeof(PrefixUnit)) + up(batch * sizeof(SharedRow));
     n += up(4 * units * kTileRows * (c.head_dim + 3));
     return n + 4 * slots * 16 * (c.head_dim + 3);
@@ -377,7 +382,10 @@ cudaError_t launch_kv8_shared(const Kv8AttnArgs& a, cudaStream_t st) {
     s.prefix_grid = prefix_grid();
     s.most_units = (int)most_units(c, a.total_rows, G, a.groups);
     s.row_tiles = row_tiles(G, a.max_new);
-    s.splits = own_splits(std::min(a.max_own, a.max_len));
+    const int own = std::min(a.max_own, a.max_len);
+    const long long ctas = (long long)a.batch * s.row_tiles * c.n_kv * own_splits(own, kFewUnits);
+    s.own_units = ctas > kManyCtas * device_sm_count() ? kMoreUnits : kFewUnits;
+    s.splits = own_splits(own, s.own_units);
     uint8_t* at = reinterpret_cast<uint8_t*>(up(reinterpret_cast<uintptr_t>(a.scratch)));
     auto take = [&](size_t n) {
         uint8_t* p = at;
