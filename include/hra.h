@@ -519,7 +519,7 @@ typedef struct hra_kv8_reach {
  * as hra_kv8_update forks them).  Those pages are read once for all the tokens of a group instead of once a row.
  *   group_cu     group g is rows group_cu[g] .. group_cu[g + 1) of the batch, ascending; rows of no group share nothing
  *   prefix       positions that the rows of group g share: of them the whole pages, and no more than the positions that each
- *                of its rows with new tokens holds before them, are read through the table of the group's first row
+ *                of its rows with new tokens holds before them, are read through the table of the first of those rows
  *   max_prefix   host upper bound of prefix
  *   max_own      host upper bound of kv_len - prefix (0 or more).  Both choose how the work is split; larger ones give the
  *                same values

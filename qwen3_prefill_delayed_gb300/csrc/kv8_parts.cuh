@@ -38,10 +38,10 @@ struct Slot {
 
 // Shared prefixes (kv8_shared.cu).  A unit: part of the key tiles of one (query tile, group, kv head).
 struct PrefixUnit {
-    int b, row0, n, q_lo;             // the group's first row, its tokens' packed rows, the tile's first token
+    int b, row0, n, q_lo;             // the group's first row with new tokens, its packed rows, the tile's first token
     int keys, head, t_first, count;   // the prefix, and the unit's tiles (0: no unit)
 };
-// Of batch row b: the positions that it reads through its group's first row, the group's first unit and packed row, and the
+// Of batch row b: the positions that it reads through another row of its group, the group's first unit and packed row, and the
 // units of each (query tile, kv head).
 struct SharedRow {
     int prefix, unit0, row0, parts;

@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(1024) kv8_shared_plan_kernel(const Kv8AttnArgs
     pdl_wait();
     __shared__ int first_s[kKv8MaxGroups + 1];   // the groups' first rows, made ascending
     __shared__ int prefix_s[kKv8MaxGroups], row0_s[kKv8MaxGroups], n_s[kKv8MaxGroups], pairs_s[kKv8MaxGroups];
+    __shared__ int lead_s[kKv8MaxGroups];
     const Kv8View& c = a.view;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int room = c.max_pages << c.page_shift;
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(1024) kv8_shared_plan_kernel(const Kv8AttnArgs
     // a warp a group: no row reads more of the prefix than it holds before its new tokens
     for (int g = warp; g < a.groups; g += warps) {
         const int b0 = first_s[g], b1 = first_s[g + 1];
-        int least = prefix_s[g], rows = 0;
+        int least = prefix_s[g], rows = 0, lead = a.batch;   // lead: the group's first row with new tokens
         int lo = cu[b0], hi = cu[b1];
         if (lane == 0 && least < 0) raise_error(c.err, HRA_DEVERR_POS_RANGE);
         for (int b = b0 + lane; b < b1; b += 32) {
@@ -97,14 +98,17 @@ __global__ void __launch_bounds__(1024) kv8_shared_plan_kernel(const Kv8AttnArgs
             if (n > 0) {
                 least = min(least, min(room, max(0, kv_len[b])) - n);
                 ++rows;
+                lead = min(lead, b);
             }
         }
         least = __reduce_min_sync(0xffffffffu, least);
         rows = __reduce_add_sync(0xffffffffu, rows);
+        lead = __reduce_min_sync(0xffffffffu, lead);
         if (lane == 0) {
             lo = min(a.total_rows, max(0, lo));
             hi = rows > 0 ? min(a.total_rows, max(lo, hi)) : lo;
-            prefix_s[g] = max(0, least) >> c.page_shift << c.page_shift;
+            prefix_s[g] = rows > 0 ? max(0, least) >> c.page_shift << c.page_shift : 0;
+            lead_s[g] = lead;
             row0_s[g] = lo;
             n_s[g] = prefix_s[g] > 0 ? hi - lo : 0;
             pairs_s[g] = (n_s[g] + QT - 1) / QT;
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(1024) kv8_shared_plan_kernel(const Kv8AttnArgs
             const int p = parts_s[lo], keys = prefix_s[lo], all_tiles = key_tiles(keys), len = (all_tiles + p - 1) / p;
             const int item = (u - unit_s[lo]) / p, part = (u - unit_s[lo]) % p, pair = item / c.n_kv;
             if (keys > 0)
-                unit = PrefixUnit{first_s[lo], row0_s[lo], n_s[lo], pair * QT, keys, item % c.n_kv, part * len,
+                unit = PrefixUnit{lead_s[lo], row0_s[lo], n_s[lo], pair * QT, keys, item % c.n_kv, part * len,
                                   max(0, min(len, all_tiles - part * len))};
         }
         int4* to = reinterpret_cast<int4*>(s.units + u);

@@ -130,6 +130,33 @@ def test_a_prefix_is_no_longer_than_what_its_rows_hold(hra):  # noqa: F811
         check(hra, c, new, lens, 4, [0, 3], [288], max_len=300)
 
 
+@pytest.mark.parametrize("new", [[0, 1, 1, 0], [0, 0, 3, 2], [0, 2, 0, 0]])
+def test_a_group_goes_on_without_its_first_rows(hra, new):  # noqa: F811
+    """Rows that ended list no pages: the prefix is read through a row that has new tokens."""
+    lens = [140 + n for n in new]
+    c = shared([0, 4], [128], lens, 2, 64, 16, seed=9)
+    c["table"][[b for b in range(4) if new[b] == 0]] = -1
+    check(hra, c, new, [n if m else 0 for n, m in zip(lens, new)], 4, [0, 4], [128])
+
+
+def test_prefixes_of_groups_without_new_tokens_do_not_count(hra):  # noqa: F811
+    lens = [200, 180, 0, 0, 190]
+    c = shared([0, 2, 4, 4], [128, 0, 0], lens, 1, 64, 16, seed=12)
+    check(hra, c, [1, 1, 0, 0, 1], lens, 4, [0, 2, 4, 4], [128, 2 ** 31 - 1, 2 ** 31 - 1], max_prefix=1 << 30)
+
+
+def test_more_rows_than_the_plan_holds_and_the_most_groups(hra):  # noqa: F811
+    rows, rng = 1100, random.Random(2)
+    group_cu = [min(g, 1000) + max(0, g - 1000) * 4 for g in range(1025)]     # 1000 groups of one row, 24 of four
+    prefix = [rng.randrange(0, 70) for _ in range(1024)]
+    lens = [1] * rows
+    for g, p in enumerate(prefix):
+        for b in range(group_cu[g], group_cu[g + 1]):
+            lens[b] = p + rng.randrange(1, 40)
+    c = shared(group_cu, prefix, lens, 1, 64, 16, seed=2)
+    check(hra, c, [1] * rows, lens, 2, group_cu, prefix)
+
+
 def test_group_numbers_outside_the_batch_are_clamped(hra):  # noqa: F811
     lens = [100, 90, 80, 120]
     c = build(lens, H=1, D=64, P=16, seed=2, width=wide(1, 64, 16, 4, 3))
