@@ -353,6 +353,8 @@ int own_splits(int max_own, int least) {
 }
 size_t up(size_t n) { return (n + 255) & ~size_t(255); }
 int prefix_grid() { return 2 * device_sm_count(); }
+// Packed rows of sequences of at most max_new tokens.
+int most_rows(int batch, int total_rows, int max_new) { return (int)std::min<long long>(total_rows, (long long)batch * max_new); }
 // Items of groups that share no packed rows: sum ceil(n / QT) <= total / QT + groups tiles a kv head.
 long long most_units(const Kv8View& c, int total_rows, int G, int groups) {
     return std::max<long long>(prefix_grid(), ((long long)total_rows / (kTileRows / G) + groups) * c.n_kv);
@@ -375,7 +377,7 @@ size_t kv8_shared_scratch_bytes(const Kv8View& c, int batch, int total_rows, int
     if (groups < 1 || max_prefix < c.page_size) return n;
     // also for calls that then share nothing, so that the size never falls
     const int G = nq / c.n_kv, most = std::min(max_new, std::max(1, kMostRows / G));
-    const size_t units = (size_t)most_units(c, total_rows, G, groups);
+    const size_t units = (size_t)most_units(c, most_rows(batch, total_rows, most), G, groups);
     const size_t slots = (size_t)batch * row_tiles(G, most) * c.n_kv * own_splits(max_own, kFewUnits);
     n = up(n) + 512 + up(units * sizeof(PrefixUnit)) + up(batch * sizeof(SharedRow));
     n += up(4 * units * kTileRows * (c.head_dim + 3));
@@ -387,7 +389,7 @@ cudaError_t launch_kv8_shared(const Kv8AttnArgs& a, cudaStream_t st) {
     const int G = a.nq / c.n_kv, QT = kTileRows / G;
     SharedCall s{};
     s.prefix_grid = prefix_grid();
-    s.most_units = (int)most_units(c, a.total_rows, G, a.groups);
+    s.most_units = (int)most_units(c, most_rows(a.batch, a.total_rows, a.max_new), G, a.groups);
     s.row_tiles = row_tiles(G, a.max_new);
     const int own = std::min(a.max_own, a.max_len);
     const long long ctas = (long long)a.batch * s.row_tiles * c.n_kv * own_splits(own, kFewUnits);

@@ -114,6 +114,17 @@ def test_workspaces_never_fall_when_a_call_grows(hra):  # noqa: F811
     assert seen > 1000
 
 
+def test_prompts_need_no_room_for_what_they_do_not_share(hra):  # noqa: F811
+    """Prompts too long to share a prefix: the scratch is that of as many rows with as many tokens as share one at most."""
+    c = _cache(hra, rows=64, max_pages=4096)
+    L = hra.lib()
+    for total in (2000, 16384, 1 << 20):
+        r = reach(hra, **dict(GROUPS, max_prefix=4096, max_own=4096))
+        with_groups = L.hra_kv8_attention_reach_workspace_size(ctypes.byref(c), 8, total, 4, 2000, 8192, ctypes.byref(r))
+        without = L.hra_kv8_attention_workspace_size(ctypes.byref(c), 8, total, 4, 2000, 8192)
+        assert 0 < with_groups - without < 64 << 20, total
+
+
 HARNESS = r"""
 #include <cstdio>
 #include <algorithm>
