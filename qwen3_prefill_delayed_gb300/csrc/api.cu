@@ -702,6 +702,9 @@ int prefill_impl(const hra_dims* dims, const hra_weights* weights, const int32_t
     const Kv8Pass* k8 = kv8 != nullptr ? &pass : nullptr;
     const Layout L = backbone_layout(d, batch, (int)T, max_end, max_end - 1, fp8 != nullptr, nv4 != nullptr, k8);
     if (workspace_bytes < L.total) return HRA_ERR_WORKSPACE;
+    if (kv8_reach_touches(reach, workspace, workspace_bytes) ||
+        kv8_reach_touches(reach, last_hidden_dev, (size_t)batch * d.hidden * 2))
+        return HRA_ERR_INVALID_ARG;
     if (validate_only) return HRA_OK;
 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -973,6 +976,10 @@ int decode_impl(const hra_dims* dims, const hra_weights* weights, const void* in
     const Kv8Pass whole{kv8, 1, kv->n_slots, reach}, pass{kv8, 1, max_pos + 1, reach};
     const Layout L = backbone_layout(d, batch, batch, batch, kv->n_slots - 1, false, false, kv8 ? &whole : nullptr);
     if (workspace_bytes < L.total) return HRA_ERR_WORKSPACE;
+    if (kv8_reach_touches(reach, workspace, workspace_bytes) ||
+        kv8_reach_touches(reach, hidden_dev, (size_t)batch * d.hidden * 2) ||
+        (pos_dev != nullptr && kv8_reach_touches(reach, pos_dev, (size_t)batch * 4)))
+        return HRA_ERR_INVALID_ARG;
     if (validate_only) return HRA_OK;
 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

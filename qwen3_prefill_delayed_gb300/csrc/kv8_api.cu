@@ -55,6 +55,11 @@ int kv8_reach_check(const hra_kv8_reach* r, int batch) {
     return HRA_OK;
 }
 
+bool kv8_reach_touches(const hra_kv8_reach* r, const void* at, size_t n) {
+    if (r == nullptr || r->groups == 0) return false;
+    return overlap({r->group_cu_dev, 4 * ((size_t)r->groups + 1)}, {at, n}) || overlap({r->prefix_dev, 4 * (size_t)r->groups}, {at, n});
+}
+
 void kv8_set_reach(Kv8AttnArgs& a, const hra_kv8_reach* r) {
     if (r == nullptr) return;
     a.window = r->window;
@@ -246,11 +251,8 @@ int hra_kv8_attention_reach(const hra_kv8_cache* cache, int32_t layer, const voi
     const size_t q_row = 2 * (size_t)n_q_heads * c.head_dim;
     if (overlap({q_dev, 2 * (size_t)q_row_stride * (total_rows - 1) + q_row}, {out_dev, q_row * total_rows}))
         return HRA_ERR_INVALID_ARG;
-    if (reach != nullptr && reach->groups > 0) {   // nor what the groups are read from
-        const Range in[2] = {{reach->group_cu_dev, 4 * ((size_t)reach->groups + 1)}, {reach->prefix_dev, 4 * (size_t)reach->groups}};
-        for (const Range& r : in)
-            if (overlap(r, {workspace, workspace_bytes}) || overlap(r, {out_dev, q_row * total_rows})) return HRA_ERR_INVALID_ARG;
-    }
+    if (kv8_reach_touches(reach, workspace, workspace_bytes) || kv8_reach_touches(reach, out_dev, q_row * total_rows))
+        return HRA_ERR_INVALID_ARG;
     a.q = reinterpret_cast<const bf16*>(q_dev);
     a.row_stride = q_row_stride;
     a.out = reinterpret_cast<bf16*>(out_dev);

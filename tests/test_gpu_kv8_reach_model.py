@@ -161,3 +161,25 @@ def test_refusals(hra, model):  # noqa: F811
     ws = torch.empty(256, dtype=torch.uint8, device="cuda")
     with pytest.raises(hra.HraError):
         bb.decode(emb, [0, 0], kv, workspace=ws, reach=w)
+
+
+def test_group_arrays_inside_what_a_pass_writes_are_refused(hra, model):  # noqa: F811
+    d, _, bb = model
+    kv = paged(hra, d, 2, 32, 4, [8, 8])
+    emb = torch.zeros(2, d.hidden, dtype=BF16, device="cuda")
+    toks = torch.zeros(2, 8, dtype=torch.int32, device="cuda")
+    bb.prefill(toks, [8, 8], kv)
+    ws = torch.zeros(2 * bb.last_ws.numel() + (1 << 20), dtype=torch.uint8, device="cuda")
+    out = torch.zeros(2, d.hidden, dtype=BF16, device="cuda")
+    pos = i32([0, 0]).cuda()
+    prefix = i32([0]).cuda()
+    for groups in (ws[256:264].view(torch.int32), out.view(torch.int32).view(-1)[:2], pos):
+        r = hra.Kv8Reach(groups=groups, prefix=prefix)
+        with pytest.raises(hra.HraError):
+            bb.decode_dev(emb, pos, 4, kv, out=out, workspace=ws, reach=r)
+        if groups is not pos:
+            with pytest.raises(hra.HraError):
+                bb.decode(emb, [0, 0], kv, out=out, workspace=ws, reach=r)
+            with pytest.raises(hra.HraError):
+                bb.prefill(toks, [8, 8], kv, out=out, workspace=ws, reach=r)
+    bb.decode_dev(emb, pos, 4, kv, out=out, workspace=ws, reach=hra.Kv8Reach(groups=i32([0, 2]).cuda(), prefix=prefix))
