@@ -493,6 +493,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_l2_3d(const CUtensorMap* map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 // Shared-memory descriptor of an MN-major tile with the 128-byte swizzle: rows of 128 bytes hold 64
 // consecutive elements of the M (or N) dimension for one K index; 8 such rows (K) form a 1024-byte
 // swizzle atom.  lbo = bytes between atoms along M/N (64-element steps), sbo = bytes between atoms

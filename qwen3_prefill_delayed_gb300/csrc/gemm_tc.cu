@@ -1221,6 +1221,17 @@ bool make_map_codes(CUtensorMap* m, const void* base, long long rows, int hd, in
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_queries(CUtensorMap* m, const void* base, int rows, int heads, int hd, long long row_stride, int box_heads, int box_rows) {
+    if (!get_encoder()) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {2 * (cuuint64_t)hd, 2 * (cuuint64_t)(rows > 1 ? row_stride : (long long)heads * hd)};
+    cuuint32_t box[3] = {(cuuint32_t)hd / 2, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    cuuint32_t es[3] = {1, 1, 1};
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_map_2d(CUtensorMap* m, const void* base, int rows, int cols, int box_rows) {
     return get_encoder() && make_map(m, base, rows, cols, box_rows, 2);
 }

@@ -382,6 +382,8 @@ size_t kv8_prompt_scratch_bytes(const Kv8View& c, int batch, int total_rows, int
 cudaError_t launch_kv8_prompt(const Kv8AttnArgs& a, int short_rows, cudaStream_t st);
 // 2-D map of E4M3 rows [rows, hd]: boxes of box_rows whole rows, swizzled over the row's bytes (128 or 64)
 bool make_map_codes(CUtensorMap* m, const void* base, long long rows, int hd, int box_rows);
+// bf16 rows of [heads][hd], row_stride elements apart: boxes of half a head, box_heads heads and box_rows rows
+bool make_map_queries(CUtensorMap* m, const void* base, int rows, int heads, int hd, long long row_stride, int box_heads, int box_rows);
 
 // Page tables, row lengths and reference counts of the next step, and the page copies they need.
 struct Kv8PagesArgs {

@@ -98,7 +98,7 @@ struct Cfg {
     // tile g: K stage g % NK, S / P / V buffer g & 1, scales g % NSC; item it: q scales it % NQS
     static constexpr int B_QF = 0, B_QE = 1, B_KF = 2, B_KE = B_KF + NK, B_SF = B_KE + NK, B_PF = B_SF + 2, B_VF = B_PF + 2,
                          B_PV = B_VF + 2, B_OF = B_PV + 2, B_IDLE = B_OF + 1, B_SC = B_IDLE + 1, B_QS = B_SC + NSC,
-                         NBARS = B_QS + NQS;
+                         B_QR = B_QS + NQS, NBARS = B_QR + 1;
     static_assert(NBARS * 8 + 16 <= 320, "barrier area");
     static_assert(ALLOC <= 115712, "two CTAs an SM");
 };
@@ -459,6 +459,7 @@ __device__ __noinline__ void outputs_again(const PromptArgs& p, const int* first
 
 template <int HD, int MODE>
 __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                                 const __grid_constant__ CUtensorMap tmQ,
                                                                  const __grid_constant__ PromptArgs p) {
     using C = Cfg<HD>;
     pdl_launch();
@@ -466,9 +467,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-    uint32_t* slots = reinterpret_cast<uint32_t*>(bars + C::NBARS);   // tmem, abort, K tiles requested
+    uint32_t* slots = reinterpret_cast<uint32_t*>(bars + C::NBARS);   // tmem, abort, K tiles requested, items' Q requested
     volatile int* abort_flag = reinterpret_cast<volatile int*>(slots + 1);
     volatile int* issued = reinterpret_cast<volatile int*>(slots + 2);
+    volatile int* q_issued = reinterpret_cast<volatile int*>(slots + 3);
     float* sc = reinterpret_cast<float*>(smem + C::OFF_SC);
     float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
     __shared__ int nan_out_s;    // a row of an item that this CTA did alone has a NaN
@@ -482,11 +484,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBARS; ++i) {
-            const bool four = i == C::B_QF || (i >= C::B_PF && i < C::B_PV) || i == C::B_OF || i >= C::B_QS;
+            const bool four = i == C::B_QF || (i >= C::B_PF && i < C::B_PV) || i == C::B_OF || (i >= C::B_QS && i < C::B_QR);
             mbar_init(bar(i), four ? 4 : 1);
         }
         *abort_flag = 0;
         *issued = 0;
+        *q_issued = 0;
         *nan_out = 0;
         if (MODE != kPrefix && p.desc != nullptr) {
             const long long all = *reinterpret_cast<const long long*>(p.list + 2);
@@ -513,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         }
         mbar_fence_init();
         tma_prefetch_map(&tmK);
+        tma_prefetch_map(&tmQ);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(slots), 256);
@@ -654,9 +658,30 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             const uint64_t k_desc = HD == 128 ? sdesc_sw128(sK) : sdesc_sw64(sK);
             const uint64_t v_desc = sdesc_sw128_mn(smem_u32(smem + C::OFF_V), TK * 128, 1024);
             int g = 0, it = 0;
+            // Q as it is, half a head where the hi codes go and half where the lo ones do
+            auto request_q = [&](int from_row, int from_head) {
+                *q_issued = *q_issued + 1;
+                mbar_expect_tx(bar(C::B_QR), (uint32_t)(p.QT * p.G * HD * 2));
+                tma_load_3d(sQ, &tmQ, bar(C::B_QR), 0, from_head, from_row);
+                tma_load_3d(sQ + C::QB, &tmQ, bar(C::B_QR), HD / 2, from_head, from_row);
+            };
             for (int k = 0; ok; ++k) {
                 const int n_kt = item(k, r, head);
                 if (n_kt == 0) break;
+                if (k == 0) request_q(r.row0 + r.q_lo, head * p.G);
+                // the next item's: to the L2 now, and from there once no S of this one is to come
+                const bool next = index(k + 1) < n_items && (!shares || left > 0) && (MODE != kPrefix || next_y.w > 0);
+                const int next_row = next_x.y + next_x.w, next_head = (MODE == kPrefix ? next_y.y : index(k + 1) % c.n_kv) * p.G;
+                if (next) {
+                    tma_prefetch_l2_3d(&tmQ, 0, next_head, next_row);
+                    tma_prefetch_l2_3d(&tmQ, HD / 2, next_head, next_row);
+                }
+                auto next_q = [&] {
+                    if (!next) return true;
+                    if (!mbar_wait(bar(C::B_QE), (uint32_t)it & 1u, abort_flag)) return false;
+                    request_q(next_row, next_head);
+                    return true;
+                };
                 // S(x) into buffer x & 1, over P(x - 2): its PV is done
                 auto issue_s = [&](int x) {
                     const int st = x % NK;
@@ -676,7 +701,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     return true;
                 };
                 ok = mbar_wait(bar(C::B_QF), (uint32_t)it & 1u, abort_flag) && issue_s(g);
-                if (n_kt == 1) tc_commit(bar(C::B_QE));
+                if (n_kt == 1 && ok) {
+                    tc_commit(bar(C::B_QE));
+                    ok = next_q();
+                }
                 for (int t = 0; t < n_kt && ok; ++t, ++g) {
                     if (t + 1 < n_kt) {
                         ok = issue_s(g + 1);
@@ -694,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                         tc_mma_f16_ts(tO, tP + 8 * ks, v_desc + (uint64_t)((g & 1) * (C::VB >> 4) + ks * (16 * 128 >> 4)), idesc_o,
                                       (t > 0 || ks > 0) ? 1u : 0u);
                     tc_commit(bar(C::B_PV + (g & 1)));
+                    if (t + 2 == n_kt) ok = next_q();
                 }
                 ++it;
             }
@@ -823,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     float2 t2 = make_float2(o[0], o[1]);
 #pragma unroll
                     for (int e = 2; e < 32; e += 2) t2 = add2(t2, make_float2(o[e], o[e + 1]));
-                    if (t2.x != t2.x || t2.y != t2.y) *nan_out = 1;
+                    if (row_ok && (t2.x != t2.x || t2.y != t2.y)) *nan_out = 1;
                 }
                 if (row_ok) {
                     if (p.v8) {
@@ -848,8 +877,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         const int kq = ((lane >> 2) & 1) + 2 * (lane >> 3), c16 = lane & 3;
         const long long page_bytes = 2LL * c.n_kv * c.page_size * HD;
         constexpr int LPR = HD / 16, RPP = 32 / LPR;
-        const int x = lane % LPR, qi_first = (w * 32 + lane / LPR) / p.G, hq_first = w * 32 + lane / LPR - qi_first * p.G;
-        const int rpp_qi = RPP / p.G, rpp_hq = RPP - rpp_qi * p.G;
+        const int x = lane % LPR, row_first = w * 32 + lane / LPR;
+        // rows behind the last whole position are never loaded: zeros from here on
+        for (int row = p.QT * p.G + lane / LPR; row < TROWS; row += RPP)
+            if (w == 3) *reinterpret_cast<uint4*>(smem + row * HD + x * 16) = *reinterpret_cast<uint4*>(smem + C::QB + row * HD + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
         int g = 0, it = 0;
         for (int k = 0; ok; ++k) {
             const int n_kt = item(k, r, head);
@@ -889,77 +921,47 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 }
             };
             int page = -1, page1 = -1;
-            {   // Q: hi and lo codes of rows 32 w .. 32 w + 31, LPR lanes a row, 16 elements a lane
-                int qi = qi_first, hq = hq_first;   // of this lane's row of a pass
-                constexpr int PIF = 2;              // passes in flight while as many are worked on: short code, run over and over
-                uint4 u[PIF][2], v[PIF][2];
-                auto fetch_q = [&](uint4(&to)[PIF][2]) {
-#pragma unroll
-                    for (int y = 0; y < PIF; ++y) {
-                        to[y][0] = to[y][1] = make_uint4(0u, 0u, 0u, 0u);
-                        if (qi < p.QT && r.q_lo + qi < r.n) {
-                            const uint4* src = reinterpret_cast<const uint4*>(
-                                p.q + (long long)(r.row0 + r.q_lo + qi) * p.row_stride + (long long)(head * p.G + hq) * HD + 16 * x);
-                            to[y][0] = src[0];
-                            to[y][1] = src[1];
-                        }
-                        qi += rpp_qi;   // RPP rows on
-                        hq += rpp_hq;
-                        if (hq >= p.G) {
-                            hq -= p.G;
-                            ++qi;
-                        }
-                    }
-                };
-                fetch_q(v);   // the first ones while the item before still runs
-                page = page_of(0);   // (behind them: a page number is waited for where it is checked)
+            {   // Q: hi and lo codes of rows 32 w .. 32 w + 31, LPR lanes a row, 16 elements a lane, in the place of what they
+                // are made of
+                page = page_of(0);
                 page1 = page_of(1);
-                if (it >= 1) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QE), (uint32_t)(it - 1) & 1u, abort_flag));
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QR), (uint32_t)it & 1u, abort_flag));
                 if (!ok) break;
 #pragma unroll 1
-                for (int p0 = 0; p0 < LPR; p0 += PIF) {
+                for (int row = row_first; row < w * 32 + 32; row += RPP) {   // short code: the fetch of instructions counts here
+                    const int sw = HD == 128 ? row & 7 : (row >> 1) & 3;
+                    const uint8_t* from = smem + (x >= LPR / 2 ? C::QB : 0) + row * HD;
+                    const uint4 u0 = *reinterpret_cast<const uint4*>(from + (((2 * x) & (LPR - 1)) ^ sw) * 16);
+                    const uint4 u1 = *reinterpret_cast<const uint4*>(from + (((2 * x + 1) & (LPR - 1)) ^ sw) * 16);
+                    const uint32_t in[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+                    // the row's largest magnitude: bf16 bits without their sign order like the values
+                    uint32_t top = 0u;
 #pragma unroll
-                    for (int y = 0; y < PIF; ++y) {
-                        u[y][0] = v[y][0];
-                        u[y][1] = v[y][1];
+                    for (int e = 0; e < 8; ++e) top = __vmaxu2(top, in[e] & 0x7FFF7FFFu);
+                    top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+                    for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const uint32_t s = kv8_scale_bits(min(top, 0x7F7Fu) << 16);
+                    const float inv = __uint_as_float((254u << 23) - s);   // 1 / s: a power of two
+                    uint32_t hc[8], lc[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {   // q / s fits f16 exactly, but for what is under 2^-25
+                        const uint32_t f = pack_h2(__uint_as_float(in[e] << 16) * inv, __uint_as_float(in[e] & 0xFFFF0000u) * inv);
+                        hc[e] = f16x2_e4m3x2(f);
+                        const uint32_t back = e4m3x2_f16x2(hc[e]);
+                        const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&f), *reinterpret_cast<const __half2*>(&back));
+                        lc[e] = f16x2_e4m3x2(*reinterpret_cast<const uint32_t*>(&d));
                     }
-                    if (p0 + PIF < LPR) fetch_q(v);
-#pragma unroll
-                    for (int y = 0; y < PIF; ++y) {
-                        const int row = w * 32 + (p0 + y) * RPP + lane / LPR;
-                        const uint32_t in[8] = {u[y][0].x, u[y][0].y, u[y][0].z, u[y][0].w,
-                                                u[y][1].x, u[y][1].y, u[y][1].z, u[y][1].w};
-                        // the row's largest magnitude: bf16 bits without their sign order like the values
-                        uint32_t top = 0u;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) top = __vmaxu2(top, in[e] & 0x7FFF7FFFu);
-                        top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-                        for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const uint32_t s = kv8_scale_bits(min(top, 0x7F7Fu) << 16);
-                        const float inv = __uint_as_float((254u << 23) - s);   // 1 / s: a power of two
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            uint32_t hc[2], lc[2];
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {   // q / s fits f16 exactly, but for what is under 2^-25
-                                const uint32_t f = pack_h2(__uint_as_float(in[e + z] << 16) * inv,
-                                                           __uint_as_float(in[e + z] & 0xFFFF0000u) * inv);
-                                hc[z] = f16x2_e4m3x2(f);
-                                const uint32_t back = e4m3x2_f16x2(hc[z]);
-                                const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&f), *reinterpret_cast<const __half2*>(&back));
-                                lc[z] = f16x2_e4m3x2(*reinterpret_cast<const uint32_t*>(&d));
-                            }
-                            hi[e >> 1] = __byte_perm(hc[0], hc[1], 0x5410);
-                            lo[e >> 1] = __byte_perm(lc[0], lc[1], 0x5410);
-                        }
-                        const int at = row * HD + ((HD == 128 ? x ^ (row & 7) : x ^ ((row >> 1) & 3)) << 4);
-                        *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(smem + C::QB + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        // a row with an infinity or a NaN gives NaN
-                        if (x == 0) qs[(it % NQS) * TROWS + row] = __uint_as_float(top < 0x7F80u ? s : 0x7FC00000u);
-                    }
+                    auto four = [](const uint32_t(&v)[8]) {
+                        return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                                          __byte_perm(v[4], v[5], 0x5410), __byte_perm(v[6], v[7], 0x5410));
+                    };
+                    __syncwarp();   // every lane of a row has read before one writes
+                    const int at = row * HD + ((x ^ sw) << 4);
+                    *reinterpret_cast<uint4*>(smem + at) = four(hc);
+                    *reinterpret_cast<uint4*>(smem + C::QB + at) = four(lc);
+                    // a row with an infinity or a NaN gives NaN
+                    if (x == 0) qs[(it % NQS) * TROWS + row] = __uint_as_float(top < 0x7F80u ? s : 0x7FC00000u);
                 }
                 if (!ok) break;
                 fence_proxy_async_smem();
@@ -972,16 +974,6 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             request(raw[0], 0, page);
             request(raw[1], 1, page1);
             page = page_of(2);
-            // the next item's queries to the L2 meanwhile
-            if (index(k + 1) < n_items && (!shares || left > 0)) {
-                const int row = w * 32 + lane, qi = row / p.G, hq = row - qi * p.G;
-                const int at = next_x.w + qi, h = MODE == kPrefix ? next_y.y : index(k + 1) % c.n_kv;
-                if (qi < p.QT && at < next_x.z) {
-                    const bf16* q = p.q + (long long)(next_x.y + at) * p.row_stride + (long long)(h * p.G + hq) * HD;
-                    prefetch_l2(q);
-                    if (HD == 128) prefetch_l2(q + 64);
-                }
-            }
             // tile t from v, tile t + 2 into it
             auto turn = [&](uint4(&v)[2 * HALVES], int t) {
                 if (g >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV + (g & 1)), (uint32_t)((g >> 1) - 1) & 1u, abort_flag));
@@ -1029,6 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         volatile int never = 0;
         if (*abort_flag)
             for (int g = max(0, *issued - NK); g < *issued; ++g) (void)mbar_wait(bar(C::B_KF + g % NK), (uint32_t)(g / NK) & 1u, &never);
+        if (*abort_flag && *q_issued > 0) (void)mbar_wait(bar(C::B_QR), (uint32_t)(*q_issued - 1) & 1u, &never);
         (void)mbar_wait(bar(C::B_IDLE), 0u, &never);
     }
     __syncthreads();
@@ -1116,8 +1109,10 @@ cudaError_t configure() {
 
 template <int HD>
 cudaError_t launch_prefix(const Kv8AttnArgs& a, const SharedCall& s, cudaStream_t st) {
-    alignas(64) CUtensorMap map;
-    if (!make_map_codes(&map, a.view.codes, 2LL * a.view.n_pages * a.view.n_kv * a.view.page_size, HD, kKv8Block))
+    alignas(64) CUtensorMap map, queries;
+    const int G = a.nq / a.view.n_kv, QT = TROWS / G;
+    if (!make_map_codes(&map, a.view.codes, 2LL * a.view.n_pages * a.view.n_kv * a.view.page_size, HD, kKv8Block) ||
+        !make_map_queries(&queries, a.q, a.total_rows, a.nq, HD, a.row_stride, G, QT))
         return cudaErrorInvalidValue;
     const cudaError_t e = configure<HD, kPrefix>();
     if (e != cudaSuccess) return e;
@@ -1130,18 +1125,20 @@ cudaError_t launch_prefix(const Kv8AttnArgs& a, const SharedCall& s, cudaStream_
     p.parts = s.prefix_parts;
     p.scale_log2 = a.scale_log2;
     p.nq = a.nq;
-    p.G = a.nq / a.view.n_kv;
-    p.QT = TROWS / p.G;
-    HRA_LAUNCH((kv8_prompt_kernel<HD, kPrefix>), dim3(s.prefix_grid), dim3(kThreads), Cfg<HD>::ALLOC, st, map, p);
+    p.G = G;
+    p.QT = QT;
+    HRA_LAUNCH((kv8_prompt_kernel<HD, kPrefix>), dim3(s.prefix_grid), dim3(kThreads), Cfg<HD>::ALLOC, st, map, queries, p);
     return cudaGetLastError();
 }
 
 template <int HD, int MODE>
 cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaStream_t st) {
     using C = Cfg<HD>;
-    alignas(64) CUtensorMap map;
+    alignas(64) CUtensorMap map, queries;
     const long long rows = 2LL * a.view.n_pages * a.view.n_kv * a.view.page_size;
-    if (!make_map_codes(&map, a.view.codes, rows, HD, kKv8Block)) return cudaErrorInvalidValue;
+    if (!make_map_codes(&map, a.view.codes, rows, HD, kKv8Block) ||
+        !make_map_queries(&queries, a.q, a.total_rows, a.nq, HD, a.row_stride, G, QT))
+        return cudaErrorInvalidValue;
     const cudaError_t e = configure<HD, MODE>();
     if (e != cudaSuccess) return e;
     int32_t* list = reinterpret_cast<int32_t*>(a.scratch);
@@ -1168,7 +1165,7 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
         p.desc = reinterpret_cast<PromptDesc*>(at);
         p.parts = reinterpret_cast<float*>(at + grid * sizeof(PromptDesc));
     }
-    HRA_LAUNCH((kv8_prompt_kernel<HD, MODE>), dim3(grid), dim3(kThreads), C::ALLOC, st, map, p);
+    HRA_LAUNCH((kv8_prompt_kernel<HD, MODE>), dim3(grid), dim3(kThreads), C::ALLOC, st, map, queries, p);
     if (shares) HRA_LAUNCH(kv8_prompt_join_kernel<HD>, dim3(grid, TROWS / 8), dim3(256), 0, st, p);
     return cudaGetLastError();
 }
