@@ -395,7 +395,7 @@ int run_layers(const hra_dims& d, const hra_weights& w, const hra_kv_cache& kv, 
 
     // the 8-bit cache: each layer's new K/V in bf16 to the staging rows, from there into the pages, then
     // attention of `n` rows of q over the pages
-    const int32_t* planned = nullptr;   // the cu whose groups the attention's scratch holds: the same in every layer
+    const int32_t* planned = nullptr;   // the cu whose list or plan the attention's scratch holds: the same in every layer
     auto attend8 = [&](int l, const bf16* q_rows, const int32_t* cu, int n, int max_new, bf16* out) {
         Kv8AttnArgs a{};
         a.view = kv8_view(*k8->cache, l);

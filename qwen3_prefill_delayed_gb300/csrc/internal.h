@@ -370,7 +370,7 @@ struct Kv8AttnArgs {
     const int32_t* group_cu;
     const int32_t* prefix;
     int groups, max_prefix, max_own;
-    int planned;            // an earlier call with this scratch has worked out the same groups, lengths and bounds
+    int planned;            // an earlier call with this scratch, of the same lengths, groups and bounds, has left its list or plan there
 };
 size_t kv8_attention_scratch_bytes(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int max_len);
 // ... and with shared prefixes

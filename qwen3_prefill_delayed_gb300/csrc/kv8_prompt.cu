@@ -1144,8 +1144,9 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
     int32_t* list = reinterpret_cast<int32_t*>(a.scratch);
     const long long pairs = most_pairs(a.batch, a.total_rows, QT, a.max_new);
     const bool shares = prompt_shares(pairs, a.view.n_kv, kv8_most_seen(a.max_len, a.window, a.sinks, QT + 2 * TK));
-    HRA_LAUNCH(kv8_schedule_kernel, dim3(1), dim3(1024), 0, st, a, G, QT, short_rows, shares ? 1 : 0,
-               (int)list_pairs(a.batch, a.total_rows, G), list);
+    if (!a.planned)
+        HRA_LAUNCH(kv8_schedule_kernel, dim3(1), dim3(1024), 0, st, a, G, QT, short_rows, shares ? 1 : 0,
+                   (int)list_pairs(a.batch, a.total_rows, G), list);
     PromptArgs p{};
     p.view = a.view;
     p.q = a.q;
