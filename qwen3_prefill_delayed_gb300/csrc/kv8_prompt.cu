@@ -749,7 +749,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             }
             ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QS + it % NQS), (uint32_t)(it / NQS) & 1u, abort_flag));
             if (!ok) break;
-            const float q_unscale = qs[(it % NQS) * TROWS + row] * p.scale_log2;
+            // (a row that sees no key is 0 whatever its q is)
+            const float q_unscale = limit > 0 ? qs[(it % NQS) * TROWS + row] * p.scale_log2 : 1.f;
             float m = -INFINITY, M = -INFINITY, l = 0.f;
             for (int t = 0; t < n_kt && ok; ++t, ++g) {
                 ok = __all_sync(0xffffffffu,

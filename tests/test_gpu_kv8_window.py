@@ -129,6 +129,25 @@ def test_a_nan_reaches_only_the_tokens_that_see_it(hra, new, G):  # noqa: F811
     assert float(over.max()) <= 0
 
 
+@pytest.mark.parametrize("new,lens", [([1, 1, 1], [0, 5, 0]), ([4, 3], [2, 30]), ([40, 33], [5, 100]), ([70, 1], [66, 0])])
+@pytest.mark.parametrize("window", [0, 20])
+def test_rows_that_see_no_position_are_zero_whatever_their_q_is(hra, new, lens, window):  # noqa: F811
+    c = build([max(1, n) for n in lens], H=1, D=64, P=16, seed=3)
+    G, T, cu = 4, sum(new), cu_of(new)
+    q = torch.randn(T, G, 64, generator=torch.Generator().manual_seed(6)).to(BF16)
+    empty = torch.zeros(T, dtype=torch.bool)
+    for b, n in enumerate(new):
+        for i in range(n):
+            empty[cu[b] + i] = lens[b] - n + i < 0
+    clean = q.clone()
+    q[empty] = torch.tensor([float("nan"), float("inf")]).repeat(32).to(BF16)
+    reach = hra.Kv8Reach(window=window) if window else None
+    kv = gpu(hra, c)
+    args = (i32(cu).cuda(), i32(lens).cuda(), max(new), max(lens))
+    got, want = (kv.attend(0, x.cuda(), *args, reach=reach).cpu() for x in (q, clean))
+    assert bool(empty.any()) and bool((got[empty] == 0).all()) and torch.equal(got, want)
+
+
 @pytest.mark.parametrize("new", [[1, 1], [40, 3]])
 def test_missing_pages_in_sight_are_reported(hra, new):  # noqa: F811
     lens = [200, 150]
