@@ -24,7 +24,11 @@
 //   warps 2-5  softmax, one row a thread, S read twice from tensor memory (maximum, then weights), O rescaled
 //              when M moves, and the output;
 //   warps 6-9  V: codes from global memory in registers, two tiles ahead, to f16 in shared memory (keys that
-//              do not count as zeros, so stale slots never reach a product); and the items' Q.
+//              do not count as zeros, so stale slots never reach a product); and the items' Q: TMA, asked for by warp 1's
+//              thread when no S of the item before is to come, puts a row's halves where its hi and lo codes go, and the row's lanes
+//              turn them into these.
+// Code that runs once an item is kept short: with 4 / 2 / 1 rows of Q worked on at once by a lane (and as much more code) 8
+// long prompts take 235 / 227 / 215 us, the fetch of instructions against their latency.
 // What bounds it: the chain S -> softmax -> PV of a tile, about 2800 clocks with two CTAs at work, in which the tensor
 // pipe is 35% busy and 53% of the issue slots are taken.  No part carries it alone (chunks after many positions, then 338 us,
 // with work left out: the exponentials and packing 0, half of S's MMAs 8%, V's conversion 9%, all but one of PV's MMAs
@@ -35,8 +39,8 @@
 // form a line of which every CTA takes an equal share; parts of an item go to scratch as fp32 sums with their
 // (m, l, M) and a second kernel joins them in order.  2 rows of 500-1021 tokens after 9-16 thousand: 376 items on 304
 // CTAs took two turns of the longest, 405 us; equal shares 371.
-// Through a window an item has the tiles that some row of it sees.  8 prompts of 1024-2048 tokens, window 512, 16 sinks: 204 us,
-// 436 TFLOP/s of seen pairs; 2 chunks after 9-16 thousand, window 4001: 175 us, 661 TFLOP/s.  Hidden scores at the edges are
+// Through a window an item has the tiles that some row of it sees.  8 prompts of 1024-2048 tokens, window 512, 16 sinks: 184 us,
+// 483 TFLOP/s of seen pairs; 2 chunks after 9-16 thousand, window 4001: 175 us, 661 TFLOP/s.  Hidden scores at the edges are
 // overwritten where they are (hide_unseen): with masks in the softmax passes by blocks of 16 keys 232 / 185 us, by bits of 32 keys
 // 232 / 201, which spilled.
 
@@ -202,57 +206,28 @@ __device__ __forceinline__ int snake(int k) {
 }
 
 // One row's tile of S, 32 columns at a time: unrolled as straight code, the weights and masks make the softmax warps wait
-// for instructions (a tile of it took 4600 clocks instead of 2400).  Where not every key of the tile counts, the keys below
-// `limit` of blocks that are there (scale >= 0) do.
+// for instructions (a tile of it took 4600 clocks instead of 2400).
 // mx: the maximum of s; Mx: the maximum of s + log2 of the block's V scale.  The loads themselves take the maximum of a
 // block's 16 scores (chunks after many positions: 353 us by max instructions, 339 so; holding the scores for the weights
 // meanwhile spills, 494).
-template <int MODE>
-__device__ __forceinline__ float coef_of(float q_unscale, float k) {   // window: positive, so that -inf stays what it is
+__device__ __forceinline__ float coef_of(float q_unscale, float k) {   // positive, so that -inf stays what it is
     const float c = q_unscale * k;
-    return MODE == kWindow && c < 0x1p-126f ? 0x1p-126f : c;
+    return c < 0x1p-126f ? 0x1p-126f : c;
 }
-template <int MODE>
-__device__ __forceinline__ void max_pass_whole(uint32_t lS, const float* ks, float q_unscale, float& mx, float& Mx) {
+__device__ __forceinline__ void max_pass(uint32_t lS, const float* ks, float q_unscale, float& mx, float& Mx) {
 #pragma unroll
     for (int ch = 0; ch < TK / 32; ++ch) {
         float top0, top1;
         const float2 k2 = *reinterpret_cast<const float2*>(ks + 2 * ch), e2 = *reinterpret_cast<const float2*>(ks + NB + 2 * ch);
         tmem_max32(lS + 32 * ch, top0, top1);
-        const float z0 = top0 * coef_of<MODE>(q_unscale, k2.x), z1 = top1 * coef_of<MODE>(q_unscale, k2.y);
+        const float z0 = top0 * coef_of(q_unscale, k2.x), z1 = top1 * coef_of(q_unscale, k2.y);
         mx = max3(mx, z0, z1);
         Mx = max3(Mx, z0 + e2.x, z1 + e2.y);
     }
 }
-__device__ __forceinline__ void max_pass_masked(uint32_t lS, const float* ks, float q_unscale, int limit, float& mx,
-                                                float& Mx) {
-#pragma unroll 1
-    for (int ch = 0; ch < TK / 32; ++ch) {
-        float a[32];
-        tmem_ld32(lS + 32 * ch, a);
-        const float2 k2 = *reinterpret_cast<const float2*>(ks + 2 * ch), e2 = *reinterpret_cast<const float2*>(ks + NB + 2 * ch);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float k = h ? k2.y : k2.x, ev = h ? e2.y : e2.x;
-            const int n = k >= 0.f ? limit - 32 * ch - 16 * h : 0;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (e >= n) a[16 * h + e] = -INFINITY;
-            float top[2] = {fmaxf(a[16 * h], a[16 * h + 1]), fmaxf(a[16 * h + 2], a[16 * h + 3])};
-#pragma unroll
-            for (int e = 4; e < 16; e += 2) top[(e >> 1) & 1] = max3(top[(e >> 1) & 1], a[16 * h + e], a[16 * h + e + 1]);
-            const float bm = fmaxf(top[0], top[1]);
-            const float z = bm == -INFINITY ? bm : bm * (q_unscale * k);
-            mx = fmaxf(mx, z);
-            Mx = fmaxf(Mx, z + ev);
-        }
-    }
-}
 // The weights: l's terms 2^(s - mr) are returned summed; times the block's V scale and 2^(mr - Mr + 11)
 // (`up` its exponent) they go as f16 to columns 16 ch, which this row has read.
-template <bool MASK, int MODE>
-__device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float q_unscale, int limit, float mr,
-                                             float up) {
+__device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float q_unscale, float mr, float up) {
     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float2 neg = make_float2(-mr, -mr);
 #pragma unroll 1
@@ -265,18 +240,13 @@ __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const float k = h ? k2.y : k2.x, ev = h ? e2.y : e2.x;
-            const float coef = coef_of<MODE>(q_unscale, k);
+            const float coef = coef_of(q_unscale, k);
             const float f = ex2(fminf(up + ev, 126.f)) * (h ? m2.y : m2.x);
-            const int n = MASK ? (k >= 0.f ? limit - 32 * ch - 16 * h : 0) : 16;
             const float2 coef2 = make_float2(coef, coef), f2 = make_float2(f, f);
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
                 const float2 z = fma2(make_float2(a[16 * h + e], a[16 * h + e + 1]), coef2, neg);
-                float2 x = make_float2(ex2(z.x), ex2(z.y));
-                if (MASK) {
-                    if (e >= n) x.x = 0.f;
-                    if (e + 1 >= n) x.y = 0.f;
-                }
+                const float2 x = make_float2(ex2(z.x), ex2(z.y));
                 ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], x);
                 const float2 y = mul2(x, f2);
                 w[8 * h + e / 2] = pack_h2(y.x, y.y);
@@ -287,9 +257,9 @@ __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float
     return (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
 }
 
-// A tile at a window's edge: the scores that a row does not see become -inf where they are, and the passes above go over it like
-// over any other (passes with masks of their own, run once an item, wait for their instructions: 2.4 us a tile, and 0.9 for the
-// others).  seen: keys [lo, limit) and those below sinks, relative to the tile's first; there: blocks that are.
+// A tile whose keys not every row sees: the scores that a row does not see become -inf where they are, and the passes above go over
+// it like over any other (passes with masks of their own, run once or twice an item, wait for their instructions: 2.4 us a tile,
+// and 0.9 for the others; 8 long prompts 215 us with them, 204 without).  seen: keys [lo, limit) and those below sinks, relative to the tile's first; there: blocks that are.
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 __device__ __forceinline__ void hide_unseen(uint32_t lS, int limit, int lo, int sinks, uint32_t there) {
 #pragma unroll 1
@@ -620,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const bool want = lane < NB && page >= 0;
                 const int pos = tile_key(t) + blk * kKv8Block;
                 if (lane < NB && pos < r.keys && page < 0 && in_sight(r, pos)) raise_error(c.err, HRA_DEVERR_PAGE_RANGE);
-                if (MODE == kWindow && s < 0.f) s = 1.f;   // absent: `there` says so
+                if (s < 0.f) s = 1.f;   // absent: `there` says so
                 if (lane < NB) {
                     sc[(g % NSC) * 3 * NB + blk] = s;
                 } else if (lane < 2 * NB) {
@@ -766,12 +736,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const bool whole = blocks == (1 << NB) - 1 &&
                                    (MODE != kWindow ? j0 + TK <= clear
                                                     : j0 + TK <= lim_min && (j0 >= lo_max || j0 + TK <= p.sinks));
-                if (MODE == kWindow && !whole) hide_unseen(lS, limit - j0, limit - p.window - j0, p.sinks - j0, (uint32_t)blocks);
+                if (!whole)
+                    hide_unseen(lS, limit - j0, MODE == kWindow ? limit - p.window - j0 : -(1 << 30), p.sinks - j0, (uint32_t)blocks);
                 float mx = -INFINITY, Mx = -INFINITY;
-                if (MODE == kWindow || whole)
-                    max_pass_whole<MODE>(lS, ks, q_unscale, mx, Mx);
-                else
-                    max_pass_masked(lS, ks, q_unscale, limit - j0, mx, Mx);
+                max_pass(lS, ks, q_unscale, mx, Mx);
                 const float mn = fmaxf(m, mx);
                 const float mr = mn == -INFINITY ? 0.f : mn;
                 l *= ex2(m - mr);
@@ -794,8 +762,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     }
                 }
                 const float up = mr - Mr + kUnit;
-                l += MODE == kWindow || whole ? weight_pass<false, MODE>(lS, ks, q_unscale, 0, mr, up)
-                                              : weight_pass<true, MODE>(lS, ks, q_unscale, limit - j0, mr, up);
+                l += weight_pass(lS, ks, q_unscale, mr, up);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
@@ -921,11 +888,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                         }
                 }
             };
-            int page = -1, page1 = -1;
+            int page = page_of(0);
+            const int page1 = page_of(1);
+            request(raw[0], 0, page);   // (on their way while Q is waited for and converted)
+            request(raw[1], 1, page1);
+            page = page_of(2);
             {   // Q: hi and lo codes of rows 32 w .. 32 w + 31, LPR lanes a row, 16 elements a lane, in the place of what they
                 // are made of
-                page = page_of(0);
-                page1 = page_of(1);
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QR), (uint32_t)it & 1u, abort_flag));
                 if (!ok) break;
 #pragma unroll 1
@@ -972,9 +941,6 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     mbar_arrive(bar(C::B_QS + it % NQS));
                 }
             }
-            request(raw[0], 0, page);
-            request(raw[1], 1, page1);
-            page = page_of(2);
             // tile t from v, tile t + 2 into it
             auto turn = [&](uint4(&v)[2 * HALVES], int t) {
                 if (g >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV + (g & 1)), (uint32_t)((g >> 1) - 1) & 1u, abort_flag));
