@@ -23,10 +23,13 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((unsigned short)w));
     return d;
 }
-__device__ __forceinline__ uint32_t f16x2_e4m3x2(uint32_t v) {
-    unsigned short d;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(v));
-    return d;
+__device__ __forceinline__ uint32_t f16x4_e4m3x4(uint32_t lo, uint32_t hi) {
+    uint32_t w;
+    asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f16x2 l, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(w)
+        : "r"(lo), "r"(hi));
+    return w;
 }
 __device__ __forceinline__ void e4m3x4_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"

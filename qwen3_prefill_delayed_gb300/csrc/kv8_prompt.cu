@@ -913,23 +913,22 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                     const uint32_t s = kv8_scale_bits(min(top, 0x7F7Fu) << 16);
                     const float inv = __uint_as_float((254u << 23) - s);   // 1 / s: a power of two
-                    uint32_t hc[8], lc[8];
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {   // q / s fits f16 exactly, but for what is under 2^-25
-                        const uint32_t f = pack_h2(__uint_as_float(in[e] << 16) * inv, __uint_as_float(in[e] & 0xFFFF0000u) * inv);
-                        hc[e] = f16x2_e4m3x2(f);
-                        const uint32_t back = e4m3x2_f16x2(hc[e]);
-                        const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&f), *reinterpret_cast<const __half2*>(&back));
-                        lc[e] = f16x2_e4m3x2(*reinterpret_cast<const uint32_t*>(&d));
+                    for (int e = 0; e < 4; ++e) {   // q / s fits f16 exactly, but for what is under 2^-25
+                        const uint32_t f0 = pack_h2(__uint_as_float(in[2 * e] << 16) * inv, __uint_as_float(in[2 * e] & 0xFFFF0000u) * inv);
+                        const uint32_t f1 = pack_h2(__uint_as_float(in[2 * e + 1] << 16) * inv, __uint_as_float(in[2 * e + 1] & 0xFFFF0000u) * inv);
+                        hi[e] = f16x4_e4m3x4(f0, f1);
+                        uint32_t back0, back1;
+                        e4m3x4_f16x4(hi[e], back0, back1);
+                        const __half2 d0 = __hsub2(*reinterpret_cast<const __half2*>(&f0), *reinterpret_cast<const __half2*>(&back0));
+                        const __half2 d1 = __hsub2(*reinterpret_cast<const __half2*>(&f1), *reinterpret_cast<const __half2*>(&back1));
+                        lo[e] = f16x4_e4m3x4(*reinterpret_cast<const uint32_t*>(&d0), *reinterpret_cast<const uint32_t*>(&d1));
                     }
-                    auto four = [](const uint32_t(&v)[8]) {
-                        return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
-                                          __byte_perm(v[4], v[5], 0x5410), __byte_perm(v[6], v[7], 0x5410));
-                    };
                     __syncwarp();   // every lane of a row has read before one writes
                     const int at = row * HD + ((x ^ sw) << 4);
-                    *reinterpret_cast<uint4*>(smem + at) = four(hc);
-                    *reinterpret_cast<uint4*>(smem + C::QB + at) = four(lc);
+                    *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(smem + C::QB + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     // a row with an infinity or a NaN gives NaN
                     if (x == 0) qs[(it % NQS) * TROWS + row] = __uint_as_float(top < 0x7F80u ? s : 0x7FC00000u);
                 }
