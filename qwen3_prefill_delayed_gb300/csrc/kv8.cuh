@@ -70,6 +70,18 @@ KV8_HD int kv8_turns_left(int blk, int blk1, int step, int most) {
     const int left = blk < blk1 ? (blk1 - blk - 1) / step + 1 : 0;
     return left < most ? left : most;
 }
+// i / d for 0 <= i < 2^31 and 1 <= d <= 2^30: with 2^(b - 1) < d <= 2^b and m = ceil(2^(31 + b) / d), i m / 2^(31 + b) exceeds i / d
+// by less than 1 / d.
+struct Kv8Div {
+    uint32_t mul;
+    int shift;
+};
+KV8_HD Kv8Div kv8_div(int d) {
+    int b = 0;
+    while ((1 << b) < d) ++b;
+    return {(uint32_t)(((1ull << (31 + b)) + d - 1) / d), 31 + b};
+}
+KV8_HD int kv8_over(const Kv8Div& d, int i) { return (int)((unsigned long long)(uint32_t)i * d.mul >> d.shift); }
 // Positions that a window hides.  A token at position p sees those of [0, p] from p - window + 1 on and those below `sinks`; of
 // tokens from position `first` on, the units of `per` positions that hold anything they see are 0 .. from - 1 and then
 // from + by, from + by + 1, ...  window 0: everything is seen.

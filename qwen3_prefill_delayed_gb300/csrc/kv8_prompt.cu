@@ -121,6 +121,7 @@ struct PromptArgs {
     int nq, G, QT;
     int v8;                 // out 32-byte aligned
     int window, sinks;      // as in Kv8AttnArgs
+    Kv8Div by_heads;        // by n_kv: an instruction or two where a division would be forty, in every role's code
 };
 
 // two fp32 operations in one instruction
@@ -501,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     const bool shares = MODE != kPrefix && p.desc != nullptr;
     int left = shares ? first_s[2] : 0;   // tiles of the share
     int4 next_x = make_int4(0, 0, 0, 0), next_y = next_x;
+    auto pair_of = [&](int i) { return kv8_over(p.by_heads, i); };
     auto index = [&](int k) { return MODE == kPrefix ? (int)blockIdx.x + k * (int)gridDim.x : shares ? first_s[0] + k : snake(k); };
     auto fetch = [&](int k) {
         const int i = index(k);
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             next_x = at[0];
             next_y = at[1];
         } else if (MODE != kPrefix && i < n_items) {
-            const int4* at = reinterpret_cast<const int4*>(p.list + kRecWords * (1 + (long long)(i / c.n_kv)));
+            const int4* at = reinterpret_cast<const int4*>(p.list + kRecWords * (1 + (long long)pair_of(i)));
             next_x = at[0];
             next_y = at[1];
         }
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     auto item = [&](int k, PromptRec& r, int& head) {   // its count, 0 when there is none
         const int i = index(k);
         if (MODE == kPrefix ? k > 0 && i >= n_items : i >= n_items || (shares && left == 0)) return 0;
-        head = MODE == kPrefix ? next_y.y : i % c.n_kv;
+        head = MODE == kPrefix ? next_y.y : i - pair_of(i) * c.n_kv;
         r.b = next_x.x;
         r.row0 = next_x.y;
         r.n = next_x.z;
@@ -641,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 if (k == 0) request_q(r.row0 + r.q_lo, head * p.G);
                 // the next item's: to the L2 now, and from there once no S of this one is to come
                 const bool next = index(k + 1) < n_items && (!shares || left > 0) && (MODE != kPrefix || next_y.w > 0);
-                const int next_row = next_x.y + next_x.w, next_head = (MODE == kPrefix ? next_y.y : index(k + 1) % c.n_kv) * p.G;
+                const int next_row = next_x.y + next_x.w, next_head = (MODE == kPrefix ? next_y.y : index(k + 1) - pair_of(index(k + 1)) * c.n_kv) * p.G;
                 if (next) {
                     tma_prefetch_l2_3d(&tmQ, 0, next_head, next_row);
                     tma_prefetch_l2_3d(&tmQ, HD / 2, next_head, next_row);
@@ -1125,6 +1127,7 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
     p.QT = QT;
     p.window = a.window;
     p.sinks = a.sinks;
+    p.by_heads = kv8_div(a.view.n_kv);
     p.v8 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
     const int grid = shares ? prompt_slots() : (int)std::max<long long>(1, std::min<long long>(pairs * a.view.n_kv, prompt_slots()));
     if (shares) {

@@ -184,18 +184,50 @@ int main() {
 """
 
 
-def test_index_arithmetic(tmp_path):
+def run_harness(tmp_path, text):
     cxx = shutil.which("g++")
     if cxx is None:
         pytest.skip("no g++")
     src = tmp_path / "h.cpp"
-    src.write_text(HARNESS)
+    src.write_text(text)
     exe = tmp_path / "h"
     inc = os.path.join(ROOT, "qwen3_prefill_delayed_gb300", "csrc")
     subprocess.run([cxx, "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover=undefined", "-I", inc,
                     str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout + r.stderr
+
+
+def test_index_arithmetic(tmp_path):
+    run_harness(tmp_path, HARNESS)
+
+
+DIVISIONS = r"""
+#include <cstdio>
+#include "kv8.cuh"
+using namespace hra;
+int main() {
+    const int ends[] = {1, 2, 3, 7, 8, 100, 1023, 1024, 1025, 65535, (1 << 30) - 1, 1 << 30};
+    for (int d : ends) {
+        const Kv8Div by = kv8_div(d);
+        auto right = [&](long long i) { return i < 0 || i > 0x7FFFFFFF || kv8_over(by, (int)i) == (int)i / d; };
+        for (long long i = 0; i < 5000; ++i)
+            if (!right(i) || !right(0x7FFFFFFFLL - i)) return printf("%lld / %d\n", i, d), 1;
+        for (long long q = 0x7FFFFFFFLL / d; q > 0; q = q * 3 / 4)
+            for (int e = -1; e <= 1; ++e)
+                if (!right(q * d + e)) return printf("%lld / %d\n", q * d + e, d), 1;
+    }
+    for (int d = 1; d <= 1024; ++d)
+        for (long long i = 0; i < 0x80000000LL; i += 104729)
+            if (kv8_over(kv8_div(d), (int)i) != (int)i / d) return printf("%lld / %d\n", i, d), 1;
+    puts("ok");
+    return 0;
+}
+"""
+
+
+def test_divisions_without_one(tmp_path):
+    run_harness(tmp_path, DIVISIONS)
 
 
 # ---- the plain forms themselves
