@@ -784,13 +784,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                     tmem_ld32(lO + ch, o);
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
-                        float* to = part + row * HD + ch + e;
-                        if (MODE != kPrefix) {
-                            *reinterpret_cast<float4*>(to) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                            *reinterpret_cast<float4*>(to + 4) = make_float4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
-                        } else if (row_ok) {   // (32-byte aligned)
-                            st_global_32(to, as_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]), as_uint4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]));
-                        }
+                        if (row_ok)   // (32-byte aligned)
+                            st_global_32(part + row * HD + ch + e, as_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]),
+                                         as_uint4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]));
                     }
                 }
                 part += TROWS * HD;
@@ -1131,7 +1127,8 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
     p.v8 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
     const int grid = shares ? prompt_slots() : (int)std::max<long long>(1, std::min<long long>(pairs * a.view.n_kv, prompt_slots()));
     if (shares) {
-        uint8_t* at = reinterpret_cast<uint8_t*>(a.scratch) + list_bytes(a.batch, a.total_rows, G);
+        const uintptr_t behind = reinterpret_cast<uintptr_t>(a.scratch) + list_bytes(a.batch, a.total_rows, G);
+        uint8_t* at = reinterpret_cast<uint8_t*>((behind + 31) & ~uintptr_t(31));
         p.desc = reinterpret_cast<PromptDesc*>(at);
         p.parts = reinterpret_cast<float*>(at + grid * sizeof(PromptDesc));
     }
@@ -1147,7 +1144,7 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
 size_t kv8_prompt_scratch_bytes(const Kv8View& c, int batch, int total_rows, int G, int max_len) {
     size_t n = list_bytes(batch, total_rows, G);
     if (max_len > kSharesFrom)
-        n += (size_t)prompt_slots() * (sizeof(PromptDesc) + 2 * sizeof(float) * TROWS * (c.head_dim + 3));
+        n += 32 + (size_t)prompt_slots() * (sizeof(PromptDesc) + 2 * sizeof(float) * TROWS * (c.head_dim + 3));
     return n;
 }
 
