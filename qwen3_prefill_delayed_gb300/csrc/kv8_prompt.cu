@@ -39,8 +39,8 @@
 // form a line of which every CTA takes an equal share; parts of an item go to scratch as fp32 sums with their
 // (m, l, M) and a second kernel joins them in order.  2 rows of 500-1021 tokens after 9-16 thousand: 376 items on 304
 // CTAs took two turns of the longest, 405 us; equal shares 371.
-// Through a window an item has the tiles that some row of it sees.  8 prompts of 1024-2048 tokens, window 512, 16 sinks: 184 us,
-// 483 TFLOP/s of seen pairs; 2 chunks after 9-16 thousand, window 4001: 175 us, 661 TFLOP/s.  Hidden scores at the edges are
+// Through a window an item has the tiles that some row of it sees.  8 prompts of 1024-2048 tokens, window 512, 16 sinks: 186 us,
+// 479 TFLOP/s of seen pairs; 2 chunks after 9-16 thousand, window 4001: 172 us, 675 TFLOP/s.  Hidden scores at the edges are
 // overwritten where they are (hide_unseen): with masks in the softmax passes by blocks of 16 keys 232 / 185 us, by bits of 32 keys
 // 232 / 201, which spilled.
 

@@ -10,8 +10,8 @@
 //   own     (sequence, head, split): the row's own positions, as parts
 //   join    a warp a (token, head) row: its parts in order, prefix first (the last CTA of a sequence and head to do it, in the
 //           place of a kernel of its own: 46 us against 43 for 46 rows in 8 groups, 78 against 73 for 64 in one)
-// 64 rows on 16,001 positions, 15-1000 of their own: 70 us (plan 6.5, prefix 29, own 23, join 10.5), row by row 330; 8 groups of 4-8
-// rows on 1024-2112: 41 us (6.5, 16, 14, 5).  A pass plans once.  The prefix is bound by its chain of tiles, 45% of the issue slots
+// 64 rows on 16,001 positions, 15-1000 of their own: 69 us (plan 6.5, prefix 29, own 23, join 10.5), row by row 330; 8 groups of 4-8
+// rows on 1024-2112: 40 us (6.5, 16, 14, 5).  A pass plans once.  The prefix is bound by its chain of tiles, 45% of the issue slots
 // and 27% of the tensor pipe; own positions and joins by latency.
 #include <algorithm>
 #include <math.h>
