@@ -47,6 +47,8 @@
 #include <algorithm>
 #include <math.h>
 
+#include <cmath>
+
 #include "kv8_parts.cuh"
 
 namespace hra {
@@ -58,11 +60,14 @@ constexpr int TROWS = kTileRows;
 constexpr int TK = kTileKeys;      // keys a tile
 constexpr int NB = TK / kKv8Block; // blocks a tile
 constexpr float kUnit = kTileUnit; // log2 of the weight of the reference maximum
-// Keys from which items count as long (see prompt_shares).  8 kv heads of 128, 4 q heads each, in a graph, equal shares / whole
-// items: 1 row of 128 tokens after 2000 positions 36 / 42 us, after 16000 64 / 245; 2 rows of 500 and 1021 after 8000 210 / 224,
-// after 16000 362 / 424, but after 4000 137 / 125; 4 of 512 after 8000 295 / 312; from 8 of 1024 on equal after 4000 (617 / 618),
-// shares slower below (306 / 256 after 1000).  2 of 600 are as many items as CTAs, and whole ones better at any length.
-constexpr int kSharesFrom = 2048;
+// Keys of work that CTAs may be without in the last turn, and per turn, before equal shares pay for their parts, the join and
+// items in the order of the sequences.  8 kv heads of 128, 4 q heads each, in a graph, turns and idle keys, then equal shares / whole items:
+// 1 row of 64 tokens after 1700 positions (0.05; 1670) 25 / 36 us, of 128 after 16000 (0.1; 14,500) 59 / 252; 2 rows of 700 after
+// 2000 (1.2; 1470) 88 / 88, of 500 and 1021 after 4000 (1.3; 2640) 145 / 158, after 16000 423 / 558; 4 of 512 after 2500 (1.7; 780)
+// 127 / 116, after 8000 (1.7; 2510) 295 / 314; 4 of 700 after 3000 (2.3; 2130) 190 / 187, of 1000 after 6000 (3.4; 3730) 467 / 474;
+// 8 of 650 after 3000 (4.4; 1790) 339 / 316, of 800 after 8000 (5.3; 5850) 856 / 912; 1 of 2500 from the start (2.1; 90) 163 / 65,
+// of 6000 (4.9; 600) 535 / 301: shares count tiles only, and many of the items are short.
+constexpr int kLeastIdle = 1200, kIdleATurn = 450;
 constexpr float kSlack = 4.f;      // how far a maximum may pass the reference before it moves
 
 // The positions that tokens see: all, a window's and the sinks', or (of an item whose rows are those of a group of sequences)
@@ -1043,9 +1048,16 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_const
 
 int prompt_slots() { return 2 * device_sm_count(); }
 
-// Equal shares where the items are long and so few that the CTAs' turns would not come out even.
-bool prompt_shares(long long pairs, int n_kv, int max_len) {
-    return max_len > kSharesFrom && pairs * n_kv < 8LL * prompt_slots();
+// Whether equal shares pay.  Of N items on S CTAs (rho = N / S, w turns, the last of them not full) whose keys fall evenly from
+// `longest` to `shortest`, snake order gives the CTA with most work the turns' sum, pair by pair of turns w longest - (longest -
+// shortest) w^2 / (2 rho) for an even w; an odd turn more begins with its longest item.  What that is above the average is idle time.
+bool prompt_shares(long long pairs, int n_kv, int shortest, int longest) {
+    const double items = (double)pairs * n_kv, slots = prompt_slots();
+    const double rho = items / slots, turns = std::ceil(rho), even = turns - std::fmod(turns, 2.0), fall = longest - shortest;
+    double most = even * longest - fall * even * even / (2.0 * rho);
+    if (even < turns) most += longest - fall * even / rho;
+    const double idle = std::max(most, (double)longest) - rho * 0.5 * (shortest + longest);
+    return rho > 0.0 && idle > kLeastIdle + kIdleATurn * rho;
 }
 long long most_pairs(int batch, int total_rows, int QT, int max_new) {
     return std::min((long long)((max_new + QT - 1) / QT) * batch, (long long)total_rows / QT + batch);
@@ -1107,7 +1119,8 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
     if (e != cudaSuccess) return e;
     int32_t* list = reinterpret_cast<int32_t*>(a.scratch);
     const long long pairs = most_pairs(a.batch, a.total_rows, QT, a.max_new);
-    const bool shares = prompt_shares(pairs, a.view.n_kv, kv8_most_seen(a.max_len, a.window, a.sinks, QT + 2 * TK));
+    auto seen = [&](int len) { return kv8_most_seen(len, a.window, a.sinks, QT + 2 * TK); };
+    const bool shares = prompt_shares(pairs, a.view.n_kv, seen(std::max(0, a.max_len - a.max_new)), seen(a.max_len));
     if (!a.planned)
         HRA_LAUNCH(kv8_schedule_kernel, dim3(1), dim3(1024), 0, st, a, G, QT, short_rows, shares ? 1 : 0,
                    (int)list_pairs(a.batch, a.total_rows, G), list);
@@ -1143,7 +1156,7 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
 // many pairs that they are not used.
 size_t kv8_prompt_scratch_bytes(const Kv8View& c, int batch, int total_rows, int G, int max_len) {
     size_t n = list_bytes(batch, total_rows, G);
-    if (max_len > kSharesFrom)
+    if (max_len > kLeastIdle)
         n += 32 + (size_t)prompt_slots() * (sizeof(PromptDesc) + 2 * sizeof(float) * TROWS * (c.head_dim + 3));
     return n;
 }
