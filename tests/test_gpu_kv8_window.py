@@ -148,6 +148,52 @@ def test_rows_that_see_no_position_are_zero_whatever_their_q_is(hra, new, lens, 
     assert bool(empty.any()) and bool((got[empty] == 0).all()) and torch.equal(got, want)
 
 
+@pytest.mark.parametrize("new", [1, 3, 6])
+def test_more_rows_than_a_table_of_sequences_holds(hra, new):  # noqa: F811
+    """1100 rows: single tokens, short chunks and prompts; beyond 1024 the single tokens' items go whole."""
+    rng = random.Random(new)
+    news = [rng.choice([0, new, rng.randrange(0, new + 1)]) for _ in range(1100)]
+    lens = [n + rng.choice([0, rng.randrange(60), 700 if b % 300 == 0 else 5]) for b, n in enumerate(news)]
+    c = build(lens, H=1, D=64, P=16, seed=new)
+    hide(c, news, lens, 30, 5, 16, drop=True)
+    check(hra, c, news, lens, 4, 30, 5)
+
+
+def test_strided_queries_on_another_stream(hra):  # noqa: F811
+    new, lens = [40, 1, 33], [340, 77, 33]
+    c = build(lens, H=2, D=64, P=16, seed=9)
+    hide(c, new, lens, 50, 7, 16, drop=False)
+    q = torch.randn(sum(new), 11, 64, generator=torch.Generator().manual_seed(5)).to(BF16)
+    want, bound = W.attend(c, 0, q[:, 2:10], cu_of(new), lens, 50, 7, split=True)
+    kv, side = gpu(hra, c), torch.cuda.Stream()
+    args = q.cuda()[:, 2:10], i32(cu_of(new)).cuda(), i32(lens).cuda(), 40, 340
+    side.wait_stream(torch.cuda.current_stream())
+    got = kv.attend(0, *args, reach=hra.Kv8Reach(window=50, sinks=7), stream=side)
+    side.synchronize()
+    assert float(((got.cpu().double() - want).abs() - bound).max()) <= 0 and kv.device_error() == 0
+
+
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("G", [3, 4, 16])
+def test_a_nan_in_queries_stays_in_its_sequence(hra, window, G):  # noqa: F811
+    """A tile's rows behind its sequence's last hold the next one's queries: nothing of them reaches an output."""
+    new, lens = [40, 33, 5, 50], [340, 33, 90, 201]
+    c = build(lens, H=2, D=64, P=16, seed=4)
+    cu = cu_of(new)
+    q = torch.randn(sum(new), 2 * G, 64, generator=torch.Generator().manual_seed(5)).to(BF16)
+    kv = gpu(hra, c)
+    reach = hra.Kv8Reach(window=window) if window else None
+    args = i32(cu).cuda(), i32(lens).cuda(), 50, 340
+    clean = kv.attend(0, q.cuda(), *args, reach=reach).cpu()
+    for b in range(4):
+        bad = q.clone()
+        bad[cu[b]:cu[b + 1]] = float("nan")
+        got = kv.attend(0, bad.cuda(), *args, reach=reach).cpu()
+        mine = torch.zeros(sum(new), dtype=torch.bool)
+        mine[cu[b]:cu[b + 1]] = True
+        assert bool(torch.isnan(got[mine]).all()) and torch.equal(got[~mine], clean[~mine])
+
+
 @pytest.mark.parametrize("new", [[1, 1], [40, 3]])
 def test_missing_pages_in_sight_are_reported(hra, new):  # noqa: F811
     lens = [200, 150]
