@@ -34,7 +34,7 @@
 // with work left out: the exponentials and packing 0, half of S's MMAs 8%, V's conversion 9%, all but one of PV's MMAs
 // 4%, the maxima 2%): the MMAs and the shared memory of two CTAs queue behind one another.  Two groups of softmax warps
 // that take the tiles in turn (448 threads at 72 registers) took 410 us against 353, a third V buffer 349 against 338.
-// The items come from a list built on the device (kv8_schedule_kernel).  Many items: most key tiles first, and CTA c
+// A few items are looked for by their CTAs; more come from a list built on the device (kv8_schedule_kernel).  Many items: most key tiles first, and CTA c
 // takes entries in snake order.  Few long ones (prompt chunks after many cached positions): the tiles of all items
 // form a line of which every CTA takes an equal share; parts of an item go to scratch as fp32 sums with their
 // (m, l, M) and a second kernel joins them in order.  2 rows of 500-1021 tokens after 9-16 thousand: 376 items on 304
@@ -68,6 +68,10 @@ constexpr float kUnit = kTileUnit; // log2 of the weight of the reference maximu
 // 8 of 650 after 3000 (4.4; 1790) 339 / 316, of 800 after 8000 (5.3; 5850) 856 / 912; 1 of 2500 from the start (2.1; 90) 163 / 65,
 // of 6000 (4.9; 600) 535 / 301: shares count tiles only, and many of the items are short.
 constexpr int kLeastIdle = 1200, kIdleATurn = 450;
+// Sequences among which a CTA looks for its own item, where none has more than one; otherwise, and among more, a kernel before lists
+// them.  8 kv heads of 128, 4 q heads each, in a graph, looked for / listed: 1 prompt of 64 tokens 8.0 / 11.1 us, of 500 14.9 / 18.1, 8 of
+// 100 11.5 / 13.7; 2 kv heads of 64: 60 rows of 6 tokens 7.9 / 10.5, 30 of 40 8.4 / 11.5.
+constexpr int kMostLooked = 64;
 constexpr float kSlack = 4.f;      // how far a maximum may pass the reference before it moves
 
 // The positions that tokens see: all, a window's and the sinks', or (of an item whose rows are those of a group of sequences)
@@ -126,6 +130,11 @@ struct PromptArgs {
     int nq, G, QT;
     int v8;                 // out 32-byte aligned
     int window, sinks;      // as in Kv8AttnArgs
+    // few items: no list, every CTA looks for its own one
+    int direct;
+    const int32_t* cu;
+    const int32_t* kv_len;
+    int batch, total_rows, max_new, short_tokens, most_pairs;
     Kv8Div by_heads;        // by n_kv: an instruction or two where a division would be forty, in every role's code
 };
 
@@ -404,17 +413,59 @@ __global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a,
     if (tid == 0) list[0] = total;
 }
 
+// One warp: pair `want` of the calls' (query tile, sequence) pairs in the order of the sequences, as the list's kernel makes them.
+__device__ __forceinline__ bool find_pair(const PromptArgs& p, int want, bool report, int* rec) {
+    const int lane = threadIdx.x & 31;
+    const long long room = (long long)p.view.max_pages << p.view.page_shift;
+    int run = 0;
+    bool found = false;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        int row0 = 0, n = 0, len = 0;
+        if (b < p.batch) {
+            kv8_rows(p.cu, b, p.total_rows, row0, n);
+            const int held = p.kv_len[b];
+            if (n > 0) {
+                len = held < 0 ? 0 : (int)min(room, (long long)held);
+                const int over = max(0, n - p.max_new);
+                if (report && n > p.short_tokens && (len != held || over)) raise_error(p.view.err, HRA_DEVERR_POS_RANGE);
+                if (n <= p.short_tokens) n = 0;
+                else n -= over;
+                len -= over;
+            }
+        }
+        const int tiles = (n + p.QT - 1) / p.QT;
+        int incl = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const int at = run + incl - tiles;
+        const bool mine = want >= at && want < at + tiles;
+        if (mine) {
+            const int q_lo = (want - at) * p.QT, keys = max(0, len - n + min(n, q_lo + p.QT));
+            reinterpret_cast<int4*>(rec)[0] = make_int4(b, row0, n, q_lo);
+            reinterpret_cast<int4*>(rec)[1] = make_int4(len, keys, 0, 0);
+        }
+        found |= __any_sync(0xffffffffu, mine);
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (report && lane == 0 && run > p.most_pairs) raise_error(p.view.err, HRA_DEVERR_POS_RANGE);
+    return found;
+}
+
 // The outputs of the items that this CTA did alone once more, a thread 32 dims of a row.  first: equal shares' first item, its
-// first tile, the tiles of the share.
+// first tile, the tiles of the share.  own: the record of the one item, where there is no list.
 template <int HD>
-__device__ __noinline__ void outputs_again(const PromptArgs& p, const int* first) {
+__device__ __noinline__ void outputs_again(const PromptArgs& p, const int* first, int n_items, const int* own) {
     const bool shares = p.desc != nullptr;
-    const int n_items = p.list[0] * p.view.n_kv;
     int left = shares ? first[2] : 0;
     for (int k = 0;; ++k) {
         const int i = shares ? first[0] + k : snake(k);
         if (i >= n_items || (shares && left == 0)) return;
-        const int32_t* rec = p.list + kRecWords * (1 + (long long)(i / p.view.n_kv));
+        const int32_t* rec = p.direct ? own : p.list + kRecWords * (1 + (long long)(i / p.view.n_kv));
         const PromptRec r{rec[0], rec[1], rec[2], rec[3], rec[4], rec[5], 0};
         const int head = i % p.view.n_kv;
         if (shares) {   // not the parts: they are looked at where they are joined
@@ -456,7 +507,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     auto bar = [&](int i) { return smem_u32(bars + i); };
     const Kv8View& c = p.view;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_items = MODE == kPrefix ? *p.n_units : p.list[0] * c.n_kv;
+    int n_items = MODE == kPrefix ? *p.n_units : p.direct ? 0 : p.list[0] * c.n_kv;
+    auto pair_of = [&](int i) { return kv8_over(p.by_heads, i); };
+    __shared__ __align__(16) int rec_s[kRecWords];
+    __shared__ bool found_s;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBARS; ++i) {
@@ -494,6 +548,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         tma_prefetch_map(&tmK);
         tma_prefetch_map(&tmQ);
     }
+    if (MODE != kPrefix && warp == 2 && p.direct) {
+        const bool found = find_pair(p, pair_of(blockIdx.x), blockIdx.x == 0, rec_s);
+        if (lane == 0) found_s = found;
+    }
     if (warp == 1) {
         tmem_alloc(smem_u32(slots), 256);
         tmem_relinquish();
@@ -501,13 +559,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (MODE != kPrefix && p.direct) n_items = found_s ? blockIdx.x + 1 : 0;
     const uint32_t tS = slots[0], tO = tS + 2 * TK;   // two S buffers, then O
     // Items k = 0, 1, ... of this CTA; the next one's record is on its way while one is worked on.  Every role calls
     // item(0), item(1), ... until there is none.
     const bool shares = MODE != kPrefix && p.desc != nullptr;
     int left = shares ? first_s[2] : 0;   // tiles of the share
     int4 next_x = make_int4(0, 0, 0, 0), next_y = next_x;
-    auto pair_of = [&](int i) { return kv8_over(p.by_heads, i); };
     auto index = [&](int k) { return MODE == kPrefix ? (int)blockIdx.x + k * (int)gridDim.x : shares ? first_s[0] + k : snake(k); };
     auto fetch = [&](int k) {
         const int i = index(k);
@@ -516,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             next_x = at[0];
             next_y = at[1];
         } else if (MODE != kPrefix && i < n_items) {
-            const int4* at = reinterpret_cast<const int4*>(p.list + kRecWords * (1 + (long long)pair_of(i)));
+            const int4* at = reinterpret_cast<const int4*>(p.direct ? rec_s : p.list + kRecWords * (1 + (long long)pair_of(i)));
             next_x = at[0];
             next_y = at[1];
         }
@@ -999,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         tc_fence_after();
         tmem_dealloc(tS, 256);
     }
-    if (MODE != kPrefix && *nan_out && !*abort_flag) outputs_again<HD>(p, first_s);
+    if (MODE != kPrefix && *nan_out && !*abort_flag) outputs_again<HD>(p, first_s, n_items, rec_s);
 }
 
 // The parts of the item that begins in share blockIdx.x and goes on behind it, in order; 8 rows a CTA.
@@ -1121,9 +1179,11 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
     const long long pairs = most_pairs(a.batch, a.total_rows, QT, a.max_new);
     auto seen = [&](int len) { return kv8_most_seen(len, a.window, a.sinks, QT + 2 * TK); };
     const bool shares = prompt_shares(pairs, a.view.n_kv, seen(std::max(0, a.max_len - a.max_new)), seen(a.max_len));
-    if (!a.planned)
+    const long long room = list_pairs(a.batch, a.total_rows, G);
+    const bool direct = !shares && room * a.view.n_kv <= prompt_slots() && a.batch <= kMostLooked;
+    if (!direct && !a.planned)
         HRA_LAUNCH(kv8_schedule_kernel, dim3(1), dim3(1024), 0, st, a, G, QT, short_rows, shares ? 1 : 0,
-                   (int)list_pairs(a.batch, a.total_rows, G), list);
+                   (int)room, list);
     PromptArgs p{};
     p.view = a.view;
     p.q = a.q;
@@ -1137,8 +1197,16 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
     p.window = a.window;
     p.sinks = a.sinks;
     p.by_heads = kv8_div(a.view.n_kv);
+    p.direct = direct ? 1 : 0;
+    p.cu = a.cu;
+    p.kv_len = a.kv_len;
+    p.batch = a.batch;
+    p.total_rows = a.total_rows;
+    p.max_new = a.max_new;
+    p.short_tokens = short_rows / G;
+    p.most_pairs = (int)room;
     p.v8 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
-    const int grid = shares ? prompt_slots() : (int)std::max<long long>(1, std::min<long long>(pairs * a.view.n_kv, prompt_slots()));
+    const int grid = direct ? (int)(room * a.view.n_kv) : shares ? prompt_slots() : (int)std::max<long long>(1, std::min<long long>(pairs * a.view.n_kv, prompt_slots()));
     if (shares) {
         const uintptr_t behind = reinterpret_cast<uintptr_t>(a.scratch) + list_bytes(a.batch, a.total_rows, G);
         uint8_t* at = reinterpret_cast<uint8_t*>((behind + 31) & ~uintptr_t(31));

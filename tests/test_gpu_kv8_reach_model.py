@@ -185,15 +185,17 @@ def test_group_arrays_inside_what_a_pass_writes_are_refused(hra, model):  # noqa
     bb.decode_dev(emb, pos, 4, kv, out=out, workspace=ws, reach=hra.Kv8Reach(groups=i32([0, 2]).cuda(), prefix=prefix))
 
 
-def test_prompts_are_listed_once_a_pass(hra, model):  # noqa: F811
-    """Prompts of more (token, head) rows than a short sequence's tile has take the list's kernel, once, and no other more."""
+@pytest.mark.parametrize("rows,kernels", [(80, 1), (2, 0)])
+def test_prompts_are_listed_once_a_pass(hra, model, rows, kernels):  # noqa: F811
+    """Prompts of more (token, head) rows than a short sequence's tile has take the list's kernel, once, and no other more; a few
+    of them do without it."""
     d, _, bb = model
     G = d.n_q_heads // d.n_kv_heads
     counts = []
     for n in (16 // G, 16 // G + 1):
-        kv = paged(hra, d, 2, 32, 4, [16, 16])
-        toks = torch.zeros(2, n, dtype=torch.int32, device="cuda")
+        kv = paged(hra, d, rows, 32, 2 * rows, [16] * rows)
+        toks = torch.zeros(rows, n, dtype=torch.int32, device="cuda")
         before = hra.hra_launch_counter()
-        bb.prefill(toks, [n, n], kv, full_last_layer=True)
+        bb.prefill(toks, [n] * rows, kv, full_last_layer=True)
         counts.append(hra.hra_launch_counter() - before)
-    assert d.n_layers > 1 and counts[1] - counts[0] == 1
+    assert d.n_layers > 1 and counts[1] - counts[0] == kernels
