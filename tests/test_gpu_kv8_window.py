@@ -75,6 +75,24 @@ def test_prompts(hra, H, G, D, P, window, sinks, new, kept):  # noqa: F811
     check(hra, c, new, lens, G, window, sinks)
 
 
+@pytest.mark.parametrize("H,G,D,P", [(2, 4, 128, 64), (8, 3, 64, 16), (5, 16, 64, 32)])
+@pytest.mark.parametrize("window,sinks", [(40, 17), (130, 0), (5000, 1)])
+@pytest.mark.parametrize("rows", [64, 65, 90])
+def test_many_prompts(hra, H, G, D, P, window, sinks, rows):  # noqa: F811
+    """Both sides of the number of sequences and of items up to which a CTA looks for its own."""
+    rng = random.Random(rows + G)
+    new = [rng.choice([0, 1, rng.randrange(2, 30), rng.randrange(2, 60)]) for _ in range(rows)]
+    new[0] = 40
+    lens = [n + rng.choice([0, rng.randrange(200)]) for n in new]
+    c = build(lens, H=H, D=D, P=P, seed=rows)
+    hide(c, new, lens, window, sinks, P, drop=True)
+    got = check(hra, c, new, lens, G, window, sinks)
+    q = torch.randn(sum(new), H * G, D, generator=torch.Generator().manual_seed(3)).to(BF16)
+    if window == 5000:
+        plain = gpu(hra, c).attend(0, q.cuda(), i32(cu_of(new)).cuda(), i32(lens).cuda(), max(new), max(lens)).cpu()
+        assert torch.equal(plain, got)
+
+
 @pytest.mark.parametrize("H,G,D,P", [(2, 4, 128, 64), (1, 2, 64, 16), (1, 5, 128, 128)])
 @pytest.mark.parametrize("window,sinks", [(2500, 0), (3001, 7), (1000, 2000), (200, 4)])
 @pytest.mark.parametrize("new,kept", [([130], [5500]), ([33, 1, 90, 0, 2], [4100, 5000, 5, 40, 4047]), ([1, 200], [6000, 0])])
