@@ -274,7 +274,8 @@ __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float
 
 // A tile whose keys not every row sees: the scores that a row does not see become -inf where they are, and the passes above go over
 // it like over any other (passes with masks of their own, run once or twice an item, wait for their instructions: 2.4 us a tile,
-// and 0.9 for the others; 8 long prompts 215 us with them, 204 without).  seen: keys [lo, limit) and those below sinks, relative to the tile's first; there: blocks that are.
+// and 0.9 for the others; 8 long prompts 215 us with them, 204 without).  seen: keys [lo, limit) and those
+// below sinks, relative to the tile's first; there: blocks that are.
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 __device__ __forceinline__ void hide_unseen(uint32_t lS, int limit, int lo, int sinks, uint32_t there) {
 #pragma unroll 1
@@ -706,7 +707,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 if (k == 0) request_q(r.row0 + r.q_lo, head * p.G);
                 // the next item's: to the L2 now, and from there once no S of this one is to come
                 const bool next = index(k + 1) < n_items && (!shares || left > 0) && (MODE != kPrefix || next_y.w > 0);
-                const int next_row = next_x.y + next_x.w, next_head = (MODE == kPrefix ? next_y.y : index(k + 1) - pair_of(index(k + 1)) * c.n_kv) * p.G;
+                const int next_row = next_x.y + next_x.w;
+                const int next_head = (MODE == kPrefix ? next_y.y : index(k + 1) - pair_of(index(k + 1)) * c.n_kv) * p.G;
                 if (next) {
                     tma_prefetch_l2_3d(&tmQ, 0, next_head, next_row);
                     tma_prefetch_l2_3d(&tmQ, HD / 2, next_head, next_row);
@@ -909,7 +911,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         const int x = lane % LPR, row_first = w * 32 + lane / LPR;
         // rows behind the last whole position are never loaded: zeros from here on
         for (int row = p.QT * p.G + lane / LPR; row < TROWS; row += RPP)
-            if (w == 3) *reinterpret_cast<uint4*>(smem + row * HD + x * 16) = *reinterpret_cast<uint4*>(smem + C::QB + row * HD + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+            if (w == 3)
+                *reinterpret_cast<uint4*>(smem + row * HD + x * 16) = *reinterpret_cast<uint4*>(smem + C::QB + row * HD + x * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
         __syncwarp();
         int g = 0, it = 0;
         for (int k = 0; ok; ++k) {

@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(1024) kv8_shared_plan_kernel(const Kv8AttnArgs
         for (int g = lane; g < a.groups; g += 32) longest = max(longest, key_tiles(prefix_s[g]));
         longest = __reduce_max_sync(0xffffffffu, longest);
         const int whole = 1 << 24;   // more than any prefix has
-        const int least = max((int)min((tiles + s.prefix_grid - 1) / s.prefix_grid, (long long)whole), max(1, (longest + kMostParts - 1) / kMostParts));
+        const int least = max((int)min((tiles + s.prefix_grid - 1) / s.prefix_grid, (long long)whole),
+                              max(1, (longest + kMostParts - 1) / kMostParts));
         const unsigned int fits = __ballot_sync(0xffffffffu, count(least + lane) <= most);
         int per = whole;
         if (fits) per = least + __ffs(fits) - 1;
