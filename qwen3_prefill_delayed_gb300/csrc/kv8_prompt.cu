@@ -879,11 +879,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 tmem_ld32(lO + ch, o);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = o[e] * 0x1p-11f * f;
-                if (ch == 32 * (quad % (HD / 32))) {   // (a NaN of V is in every row's sum of its dim)
+                // a NaN of V is in every row's sum of its dim, rows without a token among them: the four warps look at all dims between
+                // them however few tokens a tile has (a NaN of such a row's own, which its q may give, costs a second look)
+                if (ch == 32 * (quad % (HD / 32))) {
                     float2 t2 = make_float2(o[0], o[1]);
 #pragma unroll
                     for (int e = 2; e < 32; e += 2) t2 = add2(t2, make_float2(o[e], o[e + 1]));
-                    if (row_ok && (t2.x != t2.x || t2.y != t2.y)) *nan_out = 1;
+                    if (t2.x != t2.x || t2.y != t2.y) *nan_out = 1;
                 }
                 if (row_ok) {
                     if (p.v8) {
