@@ -275,13 +275,15 @@ __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float
 // A tile whose keys not every row sees: the scores that a row does not see become -inf where they are, and the passes above go over
 // it like over any other (passes with masks of their own, run once or twice an item, wait for their instructions: 2.4 us a tile,
 // and 0.9 for the others; 8 long prompts 215 us with them, 204 without).  seen: keys [lo, limit) and those
-// below sinks, relative to the tile's first; there: blocks that are.
+// below sinks, relative to the tile's first; there: blocks that are.  False: the row sees none of the tile's keys.
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-__device__ __forceinline__ void hide_unseen(uint32_t lS, int limit, int lo, int sinks, uint32_t there) {
+__device__ __forceinline__ bool hide_unseen(uint32_t lS, int limit, int lo, int sinks, uint32_t there) {
+    uint32_t any = 0u;
 #pragma unroll 1
     for (int ch = 0; ch < TK / 32; ++ch, limit -= 32, lo -= 32, sinks -= 32, there >>= 2) {
         const uint32_t blocks = (there & 1u ? 0xFFFFu : 0u) | (there & 2u ? 0xFFFF0000u : 0u);
         const uint32_t seen = bits_below(limit) & (~bits_below(lo) | bits_below(sinks)) & blocks;
+        any |= seen;
         float a[32];
         tmem_ld32(lS + 32 * ch, a);
 #pragma unroll
@@ -289,6 +291,7 @@ __device__ __forceinline__ void hide_unseen(uint32_t lS, int limit, int lo, int 
             if (!(seen & (1u << e))) a[e] = -INFINITY;
         tmem_st32(lS + 32 * ch, a);
     }
+    return any != 0u;
 }
 
 // One CTA.  The non-empty (query tile, sequence) pairs: by a counting sort, most key tiles first, or, for equal shares,
@@ -786,8 +789,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             }
             ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QS + it % NQS), (uint32_t)(it / NQS) & 1u, abort_flag));
             if (!ok) break;
-            // (a row that sees no key is 0 whatever its q is)
-            const float q_unscale = limit > 0 ? qs[(it % NQS) * TROWS + row] * p.scale_log2 : 1.f;
+            const float q_scale = limit > 0 ? qs[(it % NQS) * TROWS + row] * p.scale_log2 : 1.f;
             float m = -INFINITY, M = -INFINITY, l = 0.f;
             for (int t = 0; t < n_kt && ok; ++t, ++g) {
                 ok = __all_sync(0xffffffffu,
@@ -803,8 +805,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const bool whole = blocks == (1 << NB) - 1 &&
                                    (MODE != kWindow ? j0 + TK <= clear
                                                     : j0 + TK <= lim_min && (j0 >= lo_max || j0 + TK <= p.sinks));
-                if (!whole)
-                    hide_unseen(lS, limit - j0, MODE == kWindow ? limit - p.window - j0 : -(1 << 30), p.sinks - j0, (uint32_t)blocks);
+                // (keys that a row does not see are nothing to it whatever its q is: a scale of NaN would make them NaN)
+                float q_unscale = q_scale;
+                if (!whole && !hide_unseen(lS, limit - j0, MODE == kWindow ? limit - p.window - j0 : -(1 << 30), p.sinks - j0, (uint32_t)blocks))
+                    q_unscale = 1.f;
                 float mx = -INFINITY, Mx = -INFINITY;
                 max_pass(lS, ks, q_unscale, mx, Mx);
                 const float mn = fmaxf(m, mx);

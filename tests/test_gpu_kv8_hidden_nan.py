@@ -1,11 +1,12 @@
 """Not-a-numbers that a token does not see, in prompts over the paged 8-bit cache: one V element at a time in tiles of every
-fill, against the plain 64-bit forms of kv8_ref and kv8_reach_ref."""
+fill, and queries that see absent pages alone; against the plain 64-bit forms of kv8_ref and kv8_reach_ref."""
 import pytest
 import torch
 
 import kv8_reach_ref as W
 import kv8_ref as R
 from test_gpu_kv8 import build, cu_of, gpu, hra, i32  # noqa: F401
+from test_gpu_kv8_shared import wide
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -65,3 +66,58 @@ def test_v_at_other_heads(hra, G, D, n, window):  # noqa: F811
 def test_v_of_one_sequence_among_others(hra, G, D, new, b, window):  # noqa: F811
     """Short sequences beside prompts, with and without a list of the items."""
     one_mark_at_a_time(hra, new, [n + 40 for n in new], b, G, D, window, H=1)
+
+
+# ------------------------------------------------------------------------- queries that see absent pages alone
+
+def blind(c, new, lens, rows, window):
+    """The packed tokens of which every position that they see is absent, once the pages of `rows` ({row: pages}) are."""
+    for b, pages in rows.items():
+        c["table"][b, pages] = -1
+    P, out = c["codes"].shape[4], torch.zeros(sum(new), dtype=torch.bool)
+    for b, n in enumerate(new):
+        for i in range(n):
+            p = lens[b] - n + i
+            lo = max(0, p - window + 1) if window else 0
+            out[cu_of(new)[b] + i] = all(int(c["table"][b, j // P]) < 0 for j in range(lo, p + 1))
+    return out
+
+
+@pytest.mark.parametrize("window", [0, 25])
+@pytest.mark.parametrize("G,D", [(4, 64), (2, 128)])
+@pytest.mark.parametrize("new,kept,rows", [
+    ([40], [30], {0: slice(None)}), ([40, 33], [0, 100], {0: slice(0, 1)}), ([40, 33], [90, 7], {0: slice(None), 1: slice(1, 2)}),
+    ([130], [5000], {0: slice(None)}), ([20] * 70, [9] * 70, {3: slice(None), 69: slice(0, 1)}), ([3, 2], [20, 60], {1: slice(None)})])
+def test_queries_that_see_absent_pages_alone(hra, G, D, new, kept, rows, window):  # noqa: F811
+    """They see no position, so they are 0 whatever they hold, and a page that is absent is reported."""
+    lens, T = [a + b for a, b in zip(new, kept)], sum(new)
+    c = build(lens, H=1, D=D, P=16, seed=5)
+    none = blind(c, new, lens, rows, window)
+    q = torch.randn(T, G, D, generator=torch.Generator().manual_seed(6)).to(BF16)
+    clean = q.clone()
+    q[none] = torch.tensor([float("nan"), float("inf"), -float("inf"), 1.0]).repeat(D // 4).to(BF16)
+    reach = hra.Kv8Reach(window=window) if window else None
+    kv = gpu(hra, c)
+    args = (i32(cu_of(new)).cuda(), i32(lens).cuda(), max(new), max(lens))
+    got, want = (kv.attend(0, x.cuda(), *args, reach=reach).cpu() for x in (q, clean))
+    assert bool(none.any()) and bool((got[none] == 0).all()) and torch.equal(got, want)
+    assert kv.device_error() == hra.DEVERR_PAGE_RANGE
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [3, 2, 4]])
+def test_queries_of_a_group_that_see_absent_pages_alone(hra, new):  # noqa: F811
+    """The same over a shared prefix: of a row that shares pages none of which is there, and has none of its own."""
+    lens = [128 + 40 + n for n in new]
+    c = build(lens, H=1, D=64, P=16, seed=5, width=wide(1, 64, 16, 3, 1))
+    c["table"][:, :8] = -1
+    c["table"][1] = -1
+    T, G, cu = sum(new), 4, cu_of(new)
+    q = torch.randn(T, G, 64, generator=torch.Generator().manual_seed(6)).to(BF16)
+    clean = q.clone()
+    q[cu[1]:cu[2]] = float("nan")
+    kv = gpu(hra, c)
+    reach = hra.Kv8Reach(groups=i32([0, 3]).cuda(), prefix=i32([128]).cuda(), max_own=64)
+    got, want = (kv.attend(0, x.cuda(), i32(cu).cuda(), i32(lens).cuda(), max(new), max(lens), reach=reach).cpu()
+                 for x in (q, clean))
+    assert bool((got[cu[1]:cu[2]] == 0).all()) and torch.equal(got, want)
+    assert kv.device_error() == hra.DEVERR_PAGE_RANGE
