@@ -958,7 +958,9 @@ class Kv8Reach:
     groups, prefix     rows groups[g] .. groups[g + 1) of the batch list the same pages for their first prefix[g] positions,
                        which are read once for all of them.  CUDA int32 tensors [n + 1] and [n], read at each call.
                        max_prefix and max_own are host upper bounds of prefix and of the rows' positions behind it (by
-                       default all that the cache's rows can hold)."""
+                       default all that the cache's rows can hold).
+
+    An object stays what it was made of; the two tensors' contents may change between calls."""
 
     def __init__(self, window: int = 0, sinks: int = 0, groups: Optional[torch.Tensor] = None,
                  prefix: Optional[torch.Tensor] = None, max_prefix: Optional[int] = None, max_own: Optional[int] = None):
@@ -986,6 +988,15 @@ class Kv8Reach:
                                   most if max_prefix is None else int(max_prefix), most if max_own is None else int(max_own),
                                   self.window, self.sinks)
         self.ref, self.at = ctypes.byref(self.struct), ctypes.addressof(self.struct)
+
+    # the calls read the struct: what it was made of stays, and so does what keeps its addresses alive
+    def __setattr__(self, name, value):
+        if self.__dict__.get(name, value) is not value:
+            raise HraError(f"{name} belongs to the reach: make a Kv8Reach of the new values")
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        raise HraError(f"{name} belongs to the reach")
 
 
 def _reach(reach: Optional[Kv8Reach], cache):
