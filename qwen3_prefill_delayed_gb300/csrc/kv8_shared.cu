@@ -376,10 +376,15 @@ size_t kv8_shared_scratch_bytes(const Kv8View& c, int batch, int total_rows, int
                                 int max_prefix, int max_own) {
     size_t n = kv8_attention_scratch_bytes(c, batch, total_rows, nq, max_new, max_len);
     if (groups < 1 || max_prefix < c.page_size) return n;
-    // also for calls that then share nothing, so that the size never falls
-    const int G = nq / c.n_kv, most = std::min(max_new, std::max(1, kMostRows / G));
-    const size_t units = (size_t)most_units(c, most_rows(batch, total_rows, most), G, groups);
-    const size_t slots = (size_t)batch * row_tiles(G, most) * c.n_kv * own_splits(max_own, kFewUnits);
+    // also for calls that then share nothing, and the most of as many or fewer heads (their tiles divide unevenly), so that the
+    // size never falls
+    size_t units = 0, tiles = 0;
+    for (int G = 1; G <= nq / c.n_kv; ++G) {
+        const int most = std::min(max_new, std::max(1, kMostRows / G));
+        units = std::max(units, (size_t)most_units(c, most_rows(batch, total_rows, most), G, groups));
+        tiles = std::max(tiles, (size_t)row_tiles(G, most));
+    }
+    const size_t slots = (size_t)batch * tiles * c.n_kv * own_splits(max_own, kFewUnits);
     n = up(n) + 512 + up(units * sizeof(PrefixUnit)) + up(batch * sizeof(SharedRow));
     n += up(4 * units * kTileRows * (c.head_dim + 3));
     return n + 4 * slots * 16 * (c.head_dim + 3);

@@ -1,8 +1,11 @@
-"""A Kv8Reach keeps what its calls read: its attributes cannot be replaced under the struct that holds their values and addresses."""
+"""A Kv8Reach keeps what its calls read: its attributes cannot be replaced under the struct that holds their values and addresses; and
+workspaces sized for the largest call of a reach do for every smaller one."""
+import ctypes
+
 import pytest
 import torch
 
-from test_kv8 import hra  # noqa: F401
+from test_kv8 import FAKE, _cache, hra  # noqa: F401
 
 
 def refuses_changes(hra, r):  # noqa: F811
@@ -33,3 +36,25 @@ def test_groups_cannot_be_changed_under_their_struct(hra):  # noqa: F811
     assert r.groups is g and r.prefix is p and (r.struct.group_cu, r.struct.prefix) == (g.data_ptr(), p.data_ptr())
     other = hra.Kv8Reach(groups=g, prefix=p.clone(), max_prefix=64)
     assert other.struct.prefix != r.struct.prefix
+
+
+def test_workspaces_never_fall_with_more_heads_or_tokens(hra):  # noqa: F811
+    """Every number of q heads a kv head, beside the other arguments that the tiles of a sequence depend on."""
+    c, L = _cache(hra, rows=4096, max_pages=4096), hra.lib()
+
+    def size(batch, total, heads, max_new, max_own, groups=1):
+        r = hra.HraKv8Reach(FAKE, FAKE, groups, 9000, max_own, 0, 0)
+        return L.hra_kv8_attention_reach_workspace_size(ctypes.byref(c), batch, total, 2 * heads, max_new, 60000, ctypes.byref(r))
+
+    for batch, total in ((1, 70), (5, 70), (64, 2000), (4096, 9000)):
+        for max_own in (0, 300, 9000):
+            for most in [*range(1, 70), 100, 1000]:
+                if most > total:
+                    continue
+                sizes = [size(batch, total, g, most, max_own) for g in range(1, 17)]
+                assert all(sizes) and sizes == sorted(sizes), (batch, total, max_own, most)
+            for g in range(1, 17):
+                sizes = [size(batch, total, g, most, max_own) for most in range(1, 71)]
+                assert sizes == sorted(sizes), (batch, total, max_own, g)
+                sizes = [size(batch, total + i, g, 20, max_own) for i in range(0, 200, 7)]
+                assert sizes == sorted(sizes), (batch, total, max_own, g)
