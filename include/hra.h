@@ -527,8 +527,8 @@ typedef struct hra_kv8_reach {
  * The values are those of hra_kv8_attention, in another order of sums, and q enters the scores of a prefix as it does where
  * max_new * (n_q_heads / n_kv_heads) > 16; where sharing would not pay, it is that call.  Entries of group_cu outside
  * [0, batch] or descending are clamped, a prefix below 0 counts as 0 (HRA_DEVERR_POS_RANGE).  A window and groups in one call are
- * HRA_ERR_UNSUPPORTED; group_cu and prefix inside the workspace or out (in the model's passes: hidden, pos) are
- * HRA_ERR_INVALID_ARG. */
+ * HRA_ERR_UNSUPPORTED; group_cu and prefix inside the workspace or out (in the model's passes: hidden, pos, and what the
+ * codebook step of a frame writes) are HRA_ERR_INVALID_ARG. */
 
 /* hra_kv8_attention with a reach; NULL: every position.  The arguments and what is said of them are the same; workspace sizes
  * do not fall when an argument, a bound of the reach or its number of groups grows. */

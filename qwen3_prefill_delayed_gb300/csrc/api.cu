@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <utility>
 #include <vector>
 
 #include "internal.h"
@@ -1220,6 +1221,13 @@ int ar_frame_impl(const hra_dims* dims, const hra_weights* weights, const void* 
     rc = codebook_impl(dims, hidden_dev, head_w_dev, code_emb_dev, state_dev, eoc_bias_dev, sampling, seeds_dev, batch,
                        codes_dev, next_emb_dev, done_dev, nullptr, codebook_ws, codebook_ws_bytes, stream, true);
     if (rc != HRA_OK) return rc;
+    // what the codebook step writes before the attention reads the groups
+    const size_t B = (size_t)batch;
+    const std::pair<const void*, size_t> written[] = {{codebook_ws, codebook_ws_bytes}, {codes_dev, B * dims->n_codebooks * 4},
+                                                      {next_emb_dev, B * dims->hidden * 2}, {done_dev, B * 4},
+                                                      {state_dev, B * sizeof(hra_delay_state)}};
+    for (const auto& w : written)
+        if (kv8_reach_touches(reach, w.first, w.second)) return HRA_ERR_INVALID_ARG;
     rc = codebook_impl(dims, hidden_dev, head_w_dev, code_emb_dev, state_dev, eoc_bias_dev, sampling, seeds_dev, batch,
                        codes_dev, next_emb_dev, done_dev, nullptr, codebook_ws, codebook_ws_bytes, stream, false);
     if (rc != HRA_OK) return rc;

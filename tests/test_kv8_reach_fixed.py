@@ -5,6 +5,7 @@ import ctypes
 import pytest
 import torch
 
+from test_abi import _dims
 from test_kv8 import FAKE, _cache, hra  # noqa: F401
 
 
@@ -58,3 +59,30 @@ def test_workspaces_never_fall_with_more_heads_or_tokens(hra):  # noqa: F811
                 assert sizes == sorted(sizes), (batch, total, max_own, g)
                 sizes = [size(batch, total + i, g, 20, max_own) for i in range(0, 200, 7)]
                 assert sizes == sorted(sizes), (batch, total, max_own, g)
+
+
+def test_group_arrays_inside_what_a_frame_writes_are_refused(hra):  # noqa: F811
+    """The codebook step's outputs, state and workspace too: they are written before the attention reads the groups."""
+    L, d = hra.lib(), _dims(hra)
+    layers = (hra.HraLayerWeights * d.n_layers)()
+    for layer in layers:
+        for f, _ in hra.HraLayerWeights._fields_:
+            setattr(layer, f, FAKE)
+    w = hra.HraWeights(FAKE, layers, FAKE)
+    c = _cache(hra, n_layers=d.n_layers, n_kv_heads=d.n_kv_heads, head_dim=d.head_dim)
+    at = {n: (i + 16) << 28 for i, n in enumerate(("state", "hidden", "pos", "codes", "next_emb", "done", "bws", "cws"))}
+    size = {"state": 32, "hidden": 4 * d.hidden, "pos": 8, "codes": 8 * d.n_codebooks, "next_emb": 4 * d.hidden, "done": 8,
+            "bws": 1 << 24, "cws": 1 << 24}
+
+    def frame(group_cu, prefix):
+        r = hra.HraKv8Reach(group_cu, prefix, 1, 32, 8, 0, 0)
+        return L.hra_ar_frame_kv8_reach(ctypes.byref(d), ctypes.byref(w), FAKE, FAKE, at["state"], None, None, None, at["hidden"],
+                                        at["pos"], 7, 2, ctypes.byref(c), ctypes.byref(r), at["codes"], at["next_emb"], at["done"],
+                                        at["bws"], size["bws"], at["cws"], size["cws"], None)
+
+    for name in at:
+        for where in (at[name], at[name] + size[name] - 4, at[name] - 4):
+            assert frame(where, 0x9000000) == -1, name
+            if where >= at[name]:
+                assert frame(0x9000000, where) == -1, name
+    assert L.hra_launch_counter() == 0
