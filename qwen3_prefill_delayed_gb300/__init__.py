@@ -581,7 +581,7 @@ class ARLoop:
                 bias = None if eoc_bias_seq is None else eoc_bias_seq[f]
                 self.frame(self.codes_seq[f], self.done_seq[f], eoc_bias=bias, stream=side)
         torch.cuda.current_stream(dev).wait_stream(side)
-        self.graph = g
+        self.graph, self._graph_reach = g, self.reach   # (replays read the groups' tensors)
 
     def replay(self) -> None:
         self.graph.replay()

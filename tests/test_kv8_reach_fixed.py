@@ -1,6 +1,8 @@
 """A Kv8Reach keeps what its calls read: its attributes cannot be replaced under the struct that holds their values and addresses; and
 workspaces sized for the largest call of a reach do for every smaller one."""
 import ctypes
+import gc
+import weakref
 
 import pytest
 import torch
@@ -86,3 +88,29 @@ def test_group_arrays_inside_what_a_frame_writes_are_refused(hra):  # noqa: F811
             if where >= at[name]:
                 assert frame(0x9000000, where) == -1, name
     assert L.hra_launch_counter() == 0
+
+
+def test_a_captured_loop_keeps_the_reach_that_it_reads(hra, monkeypatch):  # noqa: F811
+    """Replays read the groups at the addresses that were captured, whatever the loop's reach is by then."""
+    class Graph:
+        def __enter__(self):
+            return self
+
+        def __exit__(self, *a):
+            pass
+
+    loop = hra.ARLoop.__new__(hra.ARLoop)
+    loop.hidden, loop.B, loop.bb = torch.zeros(1), 1, type("B", (), {"d": _dims(hra)})
+    loop.reach = hra.Kv8Reach(window=5)
+    for name in ("Stream", "current_stream", "CUDAGraph", "graph"):
+        monkeypatch.setattr(torch.cuda, name, lambda *a, **k: type("S", (Graph,), {"wait_stream": lambda *a: None})())
+    monkeypatch.setattr(hra.ARLoop, "frame", lambda *a, **k: None)
+    loop.capture(2)
+    alive = weakref.ref(loop.reach)
+    loop.reach = None
+    gc.collect()
+    assert alive() is not None
+    loop.reach = hra.Kv8Reach(window=7)
+    loop.capture(2)                                       # the next graph reads the next one
+    gc.collect()
+    assert alive() is None
