@@ -789,7 +789,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             }
             ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QS + it % NQS), (uint32_t)(it / NQS) & 1u, abort_flag));
             if (!ok) break;
-            const float q_scale = limit > 0 ? qs[(it % NQS) * TROWS + row] * p.scale_log2 : 1.f;
+            // rows without a token, or a key: scores of almost 0 (coef_of), whose maximum never moves their warp to rescale O
+            const float q_scale = limit > 0 ? qs[(it % NQS) * TROWS + row] * p.scale_log2 : 0.f;
             float m = -INFINITY, M = -INFINITY, l = 0.f;
             for (int t = 0; t < n_kt && ok; ++t, ++g) {
                 ok = __all_sync(0xffffffffu,
@@ -808,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 // (keys that a row does not see are nothing to it whatever its q is: a scale of NaN would make them NaN)
                 float q_unscale = q_scale;
                 if (!whole && !hide_unseen(lS, limit - j0, MODE == kWindow ? limit - p.window - j0 : -(1 << 30), p.sinks - j0, (uint32_t)blocks))
-                    q_unscale = 1.f;
+                    q_unscale = 0.f;
                 float mx = -INFINITY, Mx = -INFINITY;
                 max_pass(lS, ks, q_unscale, mx, Mx);
                 const float mn = fmaxf(m, mx);
