@@ -553,7 +553,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         tma_prefetch_map(&tmQ);
     }
     if (MODE != kPrefix && warp == 2 && p.direct) {
-        const bool found = find_pair(p, pair_of(blockIdx.x), blockIdx.x == 0, rec_s);
+        // a sequence's last tokens first: its longest items, which then have their SMs to themselves for longest
+        const bool found = find_pair(p, p.most_pairs - 1 - pair_of(blockIdx.x), blockIdx.x == 0, rec_s);
         if (lane == 0) found_s = found;
     }
     if (warp == 1) {
