@@ -37,7 +37,7 @@
 // A few items are looked for by their CTAs; more come from a list built on the device (kv8_schedule_kernel).  Many items: most key tiles first, and CTA c
 // takes entries in snake order.  Few long ones (prompt chunks after many cached positions): the tiles of all items
 // form a line of which every CTA takes an equal share; parts of an item go to scratch as fp32 sums with their
-// (m, l, M) and a second kernel joins them in order.  2 rows of 500-1021 tokens after 9-16 thousand: 376 items on 304
+// (m, l, M) and a second kernel joins them in order.  Where the bounds leave it open, the list's kernel chooses by the lengths.  2 rows of 500-1021 tokens after 9-16 thousand: 376 items on 304
 // CTAs took two turns of the longest, 405 us; equal shares 371.
 // Through a window an item has the tiles that some row of it sees.  8 prompts of 1024-2048 tokens, window 512, 16 sinks: 186 us,
 // 479 TFLOP/s of seen pairs; 2 chunks after 9-16 thousand, window 4001: 172 us, 675 TFLOP/s.  Hidden scores at the edges are
@@ -68,6 +68,18 @@ constexpr float kUnit = kTileUnit; // log2 of the weight of the reference maximu
 // 8 of 650 after 3000 (4.4; 1790) 339 / 316, of 800 after 8000 (5.3; 5850) 856 / 912; 1 of 2500 from the start (2.1; 90) 163 / 65,
 // of 6000 (4.9; 600) 535 / 301: shares count tiles only, and many of the items are short.
 constexpr int kLeastIdle = 1200, kIdleATurn = 450;
+// The bounds leave open whether all sequences are as long as the longest: of 9 rows of 128 tokens up to 16,000 positions on, all may be
+// (302 us whole, 316 in shares), or one (254 and 120).  Where whole items could so lose kLeastLoss key tiles, the list's kernel weighs
+// the lengths that there are (with the join that may have nothing to do, 4 us).  In key tiles, with an item's start worth kItemTiles of
+// them, whole items take what the CTA with most has in snake order; shares the equal share, as many starts as a share has at most
+// (few of a long sequence, many where prompts are short), and kSharesTiles for their parts and the join; they have to win by an eighth.
+// Of 34 such calls (2 to 64 rows of up to 4096 tokens, all, half or one of them after up to 16,000 positions or each after another number;
+// 1 to 8 kv heads of 64 and 128, 1 to 16 q heads each) every one goes the faster way so.  8 kv heads of 128, 4 q heads each, in a graph,
+// shares / whole: 18 rows of 64, one after 16,000, 86 / 254 us, one after 4000 44 / 73; 9 of 256, one after 6000, 115 / 110; 2 of 608, one
+// after 16,000, 339 / 262; 4096 tokens beside 15 rows of 64 497 / 166.
+constexpr int kItemTiles = 3, kSharesTiles = 12, kLeastLoss = 25;
+constexpr int kMostWeighed = 2560;   // pairs that the list's kernel holds for that
+enum { kWhole, kShares, kWeigh };
 // Sequences among which a CTA looks for its own item, where none has more than one; otherwise, and among more, a kernel before lists
 // them.  8 kv heads of 128, 4 q heads each, in a graph, looked for / listed: 1 prompt of 64 tokens 8.0 / 11.1 us, of 500 14.9 / 18.1, 8 of
 // 100 11.5 / 13.7; 2 kv heads of 64: 60 rows of 6 tokens 7.9 / 10.5, 30 of 40 8.4 / 11.5.
@@ -121,10 +133,10 @@ struct PromptArgs {
     const bf16* q;
     long long row_stride;
     bf16* out;
-    const int32_t* list;    // [0] = pairs, [2..3] all items' tiles, records from word 8 on
+    const int32_t* list;    // see kv8_schedule_kernel; records from word 8 on
     const PrefixUnit* units;   // a shared prefix: the CTAs' work, in place of the list
     const int32_t* n_units;
-    PromptDesc* desc;       // equal shares (null: snake order)
+    PromptDesc* desc;       // equal shares, if the list says so (null: snake order)
     float* parts;
     float scale_log2;
     int nq, G, QT;
@@ -298,14 +310,17 @@ __device__ __forceinline__ bool hide_unseen(uint32_t lS, int limit, int lo, int 
 // in the order of the sequences with the tiles before each (the shares' borders decide where sums are split, so the
 // order must not depend on which thread comes first).  A thread a sequence counts its tiles, then a thread a pair
 // finds its sequence in their running sum: the time follows the tiles there are, not batch times the longest.
+// list[0]: the pairs; [1]: whether they go in equal shares; [2..3]: then all items' tiles.
 constexpr int kBins = 1024;
-__global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a, int G, int QT, int short_rows, int shares,
+template <bool WEIGH>
+__global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a, int G, int QT, int short_rows, int shares, int slots,
                                                             int most, int32_t* __restrict__ list) {
     pdl_launch();
     pdl_wait();
     __shared__ int hist[kBins];
     __shared__ int at_s[1025], row0_s[1024], n_s[1024], len_s[1024];
-    __shared__ int total;
+    __shared__ int total, load_s, starts_s;
+    __shared__ uint32_t before_s[WEIGH ? kMostWeighed + 1 : 1];   // tiles of the pairs before, for one kv head
     const int tid = threadIdx.x;
     for (int i = tid; i < kBins; i += blockDim.x) hist[i] = 0;
     const long long room = (long long)a.view.max_pages << a.view.page_shift;
@@ -360,10 +375,12 @@ __global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a,
     };
     PromptRec r;
     int count = 0;
-    if (shares) {
+    const bool held = a.batch <= 1024;   // (one chunk, which stays)
+    auto in_shares = [&](bool first) {
         long long before = 0;
+        count = 0;
         for (int b0 = 0; b0 < a.batch; b0 += 1024) {
-            const int here = chunk(b0, count, true);
+            const int here = first || !held ? chunk(b0, count, first) : at_s[1024];
             for (int p0 = 0; p0 < here; p0 += 1024) {
                 const bool in = p0 + tid < here;
                 if (in) pair(p0 + tid, b0, r);
@@ -376,13 +393,31 @@ __global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a,
         }
         if (tid == 0) {
             list[0] = count;
+            list[1] = 1;
             *reinterpret_cast<long long*>(list + 2) = before;
         }
+    };
+    if (!WEIGH && shares) {
+        in_shares(true);
         return;
     }
+    uint32_t tiles = 0;   // (counted up to 1023 a pair where they are weighed, in units of one kv head)
+    if (tid == 0) load_s = starts_s = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 1024) {
         const int here = chunk(b0, count, true);
-        for (int p = tid; p < here; p += 1024) atomicAdd(&hist[pair(p, b0, r)], 1);
+        for (int p0 = 0; p0 < here; p0 += 1024) {
+            const int p = p0 + tid;
+            int bin = kBins - 1;
+            if (p < here) {
+                bin = pair(p, b0, r);
+                atomicAdd(&hist[bin], 1);
+            }
+            if (!WEIGH) continue;
+            uint32_t units;
+            const uint32_t at = block_scan((uint32_t)(p < here ? max(1, kBins - 1 - bin) : 0), units);
+            if (p < here) before_s[count + p] = tiles + at;
+            tiles += units;
+        }
         count += here;
         __syncthreads();
     }
@@ -403,10 +438,55 @@ __global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a,
         }
         if (tid == 31) total = incl;
     }
+    if (WEIGH && tid == 0) before_s[count] = tiles;
     __syncthreads();
+    if (WEIGH) {
+        // everything in 32 bits: 2560 pairs of 1023 tiles for 1024 kv heads are less than 2^32
+        const uint32_t n_kv = a.view.n_kv, items = (uint32_t)total * n_kv, all = tiles * n_kv;
+        const uint32_t share = all / (uint32_t)slots + (all % (uint32_t)slots ? 1 : 0);
+        int load = 0, starts = 0;
+        for (uint32_t c = tid; c < (uint32_t)slots; c += 1024) {
+            int mine = 0;
+            for (uint32_t k = 0;; ++k) {
+                const uint32_t i = k * slots + (k & 1u ? slots - 1 - c : c);   // snake order
+                if (i >= items) break;
+                const int j = (int)(i / n_kv);
+                int lo = 0;   // the last bin that begins at j or before
+#pragma unroll
+                for (int step = kBins / 2; step > 0; step >>= 1)
+                    if (hist[lo + step] <= j) lo += step;
+                mine += max(1, kBins - 1 - lo) + kItemTiles;
+            }
+            load = max(load, mine);
+            const uint32_t u = c * share;
+            if (share > 0 && c <= (all - 1) / share) {   // (u < all)
+                auto item_at = [&](uint32_t x) {
+                    int lo = 0, hi = total;   // the last pair with no more tiles before it
+                    while (hi - lo > 1) {
+                        const int mid = (lo + hi) >> 1;
+                        if (before_s[mid] * n_kv <= x) lo = mid;
+                        else hi = mid;
+                    }
+                    return (int)(lo * n_kv + (x - before_s[lo] * n_kv) / (before_s[lo + 1] - before_s[lo]));
+                };
+                starts = max(starts, item_at(u + min(share, all - u) - 1) - item_at(u) + 1);
+            }
+        }
+        load = __reduce_max_sync(0xffffffffu, load);
+        starts = __reduce_max_sync(0xffffffffu, starts);
+        if ((tid & 31) == 0 && (load > 0 || starts > 0)) {
+            atomicMax(&load_s, load);
+            atomicMax(&starts_s, starts);
+        }
+        __syncthreads();
+        if (kSharesTiles + (long long)share + (long long)kItemTiles * starts_s < load_s - load_s / 8) {
+            in_shares(false);
+            return;
+        }
+    }
     count = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 1024) {
-        const int here = a.batch <= 1024 ? at_s[1024] : chunk(b0, count, false);
+        const int here = held ? at_s[1024] : chunk(b0, count, false);
         for (int p = tid; p < here; p += 1024) {
             const int bin = pair(p, b0, r);
             put(atomicAdd(&hist[bin], 1), r, 0);
@@ -414,7 +494,10 @@ __global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a,
         count += here;
         __syncthreads();
     }
-    if (tid == 0) list[0] = total;
+    if (tid == 0) {
+        list[0] = total;
+        list[1] = 0;
+    }
 }
 
 // One warp: pair `want` of the calls' (query tile, sequence) pairs in the order of the sequences, as the list's kernel makes them.
@@ -464,7 +547,7 @@ __device__ __forceinline__ bool find_pair(const PromptArgs& p, int want, bool re
 // first tile, the tiles of the share.  own: the record of the one item, where there is no list.
 template <int HD>
 __device__ __noinline__ void outputs_again(const PromptArgs& p, const int* first, int n_items, const int* own) {
-    const bool shares = p.desc != nullptr;
+    const bool shares = p.desc != nullptr && p.list[1] != 0;
     int left = shares ? first[2] : 0;
     for (int k = 0;; ++k) {
         const int i = shares ? first[0] + k : snake(k);
@@ -512,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     const Kv8View& c = p.view;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int n_items = MODE == kPrefix ? *p.n_units : p.direct ? 0 : p.list[0] * c.n_kv;
+    const bool shares = MODE != kPrefix && p.desc != nullptr && p.list[1] != 0;
     auto pair_of = [&](int i) { return kv8_over(p.by_heads, i); };
     __shared__ __align__(16) int rec_s[kRecWords];
     __shared__ bool found_s;
@@ -525,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         *issued = 0;
         *q_issued = 0;
         *nan_out = 0;
-        if (MODE != kPrefix && p.desc != nullptr) {
+        if (shares) {
             const long long all = *reinterpret_cast<const long long*>(p.list + 2);
             const long long share = (all + gridDim.x - 1) / gridDim.x, u = blockIdx.x * share;
             p.desc[blockIdx.x].row0 = -1;
@@ -568,7 +652,6 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     const uint32_t tS = slots[0], tO = tS + 2 * TK;   // two S buffers, then O
     // Items k = 0, 1, ... of this CTA; the next one's record is on its way while one is worked on.  Every role calls
     // item(0), item(1), ... until there is none.
-    const bool shares = MODE != kPrefix && p.desc != nullptr;
     int left = shares ? first_s[2] : 0;   // tiles of the share
     int4 next_x = make_int4(0, 0, 0, 0), next_y = next_x;
     auto index = [&](int k) { return MODE == kPrefix ? (int)blockIdx.x + k * (int)gridDim.x : shares ? first_s[0] + k : snake(k); };
@@ -1072,15 +1155,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
     if (MODE != kPrefix && *nan_out && !*abort_flag) outputs_again<HD>(p, first_s, n_items, rec_s);
 }
 
-// The parts of the item that begins in share blockIdx.x and goes on behind it, in order; 8 rows a CTA.
-template <int HD>
-__global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_constant__ PromptArgs p) {
+// The parts of the item that begins in share blockIdx.x and goes on behind it, in order; ROWS rows a CTA, a warp each: 32 where there may
+// be nothing to join (the 4864 CTAs of 8 rows take 7 us to find that out).
+template <int HD, int ROWS>
+__global__ void __launch_bounds__(32 * ROWS) kv8_prompt_join_kernel(const __grid_constant__ PromptArgs p) {
     pdl_launch();
     pdl_wait();
+    if (p.list[1] == 0) return;   // whole items
     const int c0 = blockIdx.x;
     const PromptDesc d = p.desc[c0];
     if (d.row0 < 0) return;
-    const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int row = blockIdx.y * ROWS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int qi = row / p.G, hq = row - qi * p.G;
     if (qi >= p.QT || d.q_lo + qi >= d.n) return;
     constexpr int E = HD / 32;
@@ -1128,6 +1213,13 @@ bool prompt_shares(long long pairs, int n_kv, int shortest, int longest) {
     if (even < turns) most += longest - fall * even / rho;
     const double idle = std::max(most, (double)longest) - rho * 0.5 * (shortest + longest);
     return rho > 0.0 && idle > kLeastIdle + kIdleATurn * rho;
+}
+// Whether the lengths are weighed: what whole items lose at most by the bounds, when one sequence is as long as they allow and the others
+// hold their new tokens alone.
+bool prompt_weighs(long long pairs, long long room, int n_kv, int batch, int total_rows, int longest) {
+    const double rho = (double)pairs * n_kv / prompt_slots(), tokens = (double)total_rows / batch;
+    const double other = std::min(rho, 1.0) * (std::max(1.0, tokens / (2 * TK)) + kItemTiles);
+    return batch > 1 && room <= kMostWeighed && rho < 8.0 && longest / TK - kSharesTiles - other > kLeastLoss;
 }
 long long most_pairs(int batch, int total_rows, int QT, int max_new) {
     return std::min((long long)((max_new + QT - 1) / QT) * batch, (long long)total_rows / QT + batch);
@@ -1190,12 +1282,16 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
     int32_t* list = reinterpret_cast<int32_t*>(a.scratch);
     const long long pairs = most_pairs(a.batch, a.total_rows, QT, a.max_new);
     auto seen = [&](int len) { return kv8_most_seen(len, a.window, a.sinks, QT + 2 * TK); };
-    const bool shares = prompt_shares(pairs, a.view.n_kv, seen(std::max(0, a.max_len - a.max_new)), seen(a.max_len));
     const long long room = list_pairs(a.batch, a.total_rows, G);
-    const bool direct = !shares && room * a.view.n_kv <= prompt_slots() && a.batch <= kMostLooked;
-    if (!direct && !a.planned)
-        HRA_LAUNCH(kv8_schedule_kernel, dim3(1), dim3(1024), 0, st, a, G, QT, short_rows, shares ? 1 : 0,
-                   (int)room, list);
+    const int slots = prompt_slots(), longest = seen(a.max_len);
+    const int way = prompt_shares(pairs, a.view.n_kv, seen(std::max(0, a.max_len - a.max_new)), longest) ? kShares
+                    : prompt_weighs(pairs, room, a.view.n_kv, a.batch, a.total_rows, longest)            ? kWeigh
+                                                                                                         : kWhole;
+    const bool direct = way == kWhole && room * a.view.n_kv <= slots && a.batch <= kMostLooked;
+    if (!direct && !a.planned) {
+        if (way == kWeigh) HRA_LAUNCH(kv8_schedule_kernel<true>, dim3(1), dim3(1024), 0, st, a, G, QT, short_rows, 0, slots, (int)room, list);
+        else HRA_LAUNCH(kv8_schedule_kernel<false>, dim3(1), dim3(1024), 0, st, a, G, QT, short_rows, way == kShares ? 1 : 0, slots, (int)room, list);
+    }
     PromptArgs p{};
     p.view = a.view;
     p.q = a.q;
@@ -1218,15 +1314,16 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
     p.short_tokens = short_rows / G;
     p.most_pairs = (int)room;
     p.v8 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
-    const int grid = direct ? (int)(room * a.view.n_kv) : shares ? prompt_slots() : (int)std::max<long long>(1, std::min<long long>(pairs * a.view.n_kv, prompt_slots()));
-    if (shares) {
+    const int grid = direct ? (int)(room * a.view.n_kv) : way != kWhole ? slots : (int)std::max<long long>(1, std::min<long long>(pairs * a.view.n_kv, slots));
+    if (way != kWhole) {
         const uintptr_t behind = reinterpret_cast<uintptr_t>(a.scratch) + list_bytes(a.batch, a.total_rows, G);
         uint8_t* at = reinterpret_cast<uint8_t*>((behind + 31) & ~uintptr_t(31));
         p.desc = reinterpret_cast<PromptDesc*>(at);
         p.parts = reinterpret_cast<float*>(at + grid * sizeof(PromptDesc));
     }
     HRA_LAUNCH((kv8_prompt_kernel<HD, MODE>), dim3(grid), dim3(kThreads), C::ALLOC, st, map, queries, p);
-    if (shares) HRA_LAUNCH(kv8_prompt_join_kernel<HD>, dim3(grid, TROWS / 8), dim3(256), 0, st, p);
+    if (way == kShares) HRA_LAUNCH((kv8_prompt_join_kernel<HD, 8>), dim3(grid, TROWS / 8), dim3(256), 0, st, p);
+    if (way == kWeigh) HRA_LAUNCH((kv8_prompt_join_kernel<HD, 32>), dim3(grid, TROWS / 32), dim3(1024), 0, st, p);
     return cudaGetLastError();
 }
 
