@@ -91,7 +91,8 @@ struct Team {
     }
 };
 
-template <int CS>
+// WINDOW: pages that no later token sees are dropped (looked for in every update, that takes 0.6 us of 16)
+template <int CS, bool WINDOW>
 __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8PagesArgs a) {
     pdl_launch();
     pdl_wait();
@@ -163,8 +164,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8
         }
     };
     // pages [gone_lo, gone_hi) of a row of `len` positions: behind the window of every later token and no sinks
-    const int gone_lo = (int)(((long long)a.sinks + P - 1) >> a.page_shift);
-    auto gone_hi = [&](int len) { return a.window > 0 && len >= a.window ? (len - a.window + 1) >> a.page_shift : 0; };
+    const int gone_lo = WINDOW ? (int)(((long long)a.sinks + P - 1) >> a.page_shift) : 0;
+    auto gone_hi = [&](int len) { return WINDOW && len >= a.window ? (len - a.window + 1) >> a.page_shift : 0; };
     // the pages each new row keeps, and how many fresh ones it needs: one warp a row
     bool too_long = false, wrong = false;
     for (int b = warp; b < R; b += team.kWarps) {
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8
 #pragma unroll
             for (int c = 0; c < kCells; ++c) {
                 const int i = i0 + 32 * c + lane;
-                const bool out = i >= gone_lo && i < gone;
+                const bool out = WINDOW && i >= gone_lo && i < gone;
                 const bool keep = !out && old[c] >= 0 && (heir || i < (len >> a.page_shift));
                 if (keep) atomicAdd(&s.refs[old[c]], 1);
                 need += __popc(__ballot_sync(0xffffffffu, p >= 0 && i < ends && i < W && !keep && !out));
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_update_plan_kernel(const Kv8
 #pragma unroll
                 for (int c = 0; c < kCells; ++c) {
                     const int i = i0 + 32 * c + lane;
-                    const bool out = i >= gone_lo && i < gone;
+                    const bool out = WINDOW && i >= gone_lo && i < gone;
                     const bool keep = !out && old[c] >= 0 && (heir || i < (len >> a.page_shift));
                     const bool fresh = p >= 0 && i < ends && i < W && !keep && !out;
                     const unsigned int mask = __ballot_sync(0xffffffffu, fresh);
@@ -447,6 +448,24 @@ cudaError_t launch_team(K kernel, const Kv8PagesArgs& a, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+template <bool WINDOW>
+cudaError_t launch_update_plan(const Kv8PagesArgs& a, cudaStream_t st) {
+    const size_t bytes = one_cta_bytes(a.rows, a.n_pages);
+    if ((long long)a.rows * a.max_pages + a.n_pages >= kTeamFrom || bytes > kOneCtaMost)
+        return launch_team(kv8_update_plan_kernel<kTeam, WINDOW>, a, st);
+    static bool configured[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(kv8_update_plan_kernel<1, WINDOW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kOneCtaMost);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev] = true;
+    }
+    HRA_LAUNCH((kv8_update_plan_kernel<1, WINDOW>), dim3(1), dim3(kPlanThreads), bytes, st, a);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 size_t kv8_pages_scratch_bytes(int rows, int max_pages, int n_pages) {
@@ -455,23 +474,8 @@ size_t kv8_pages_scratch_bytes(int rows, int max_pages, int n_pages) {
 }
 
 cudaError_t launch_kv8_update(const Kv8PagesArgs& a, cudaStream_t st) {
-    const size_t bytes = one_cta_bytes(a.rows, a.n_pages);
-    if ((long long)a.rows * a.max_pages + a.n_pages >= kTeamFrom || bytes > kOneCtaMost) {
-        const cudaError_t e = launch_team(kv8_update_plan_kernel<kTeam>, a, st);
-        if (e != cudaSuccess) return e;
-    } else {
-        static bool configured[64] = {false};
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        if (dev < 0 || dev >= 64 || !configured[dev]) {
-            e = cudaFuncSetAttribute(kv8_update_plan_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kOneCtaMost);
-            if (e != cudaSuccess) return e;
-            if (dev >= 0 && dev < 64) configured[dev] = true;
-        }
-        HRA_LAUNCH(kv8_update_plan_kernel<1>, dim3(1), dim3(kPlanThreads), bytes, st, a);
-    }
-    return launch_copy<false>(a, a.rows, st);
+    const cudaError_t e = a.window > 0 ? launch_update_plan<true>(a, st) : launch_update_plan<false>(a, st);
+    return e != cudaSuccess ? e : launch_copy<false>(a, a.rows, st);
 }
 
 cudaError_t launch_kv8_compact(const Kv8PagesArgs& a, cudaStream_t st) {
