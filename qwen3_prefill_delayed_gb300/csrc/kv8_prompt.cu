@@ -83,7 +83,11 @@ enum { kWhole, kShares, kWeigh };
 // Sequences among which a CTA looks for its own item, where none has more than one; otherwise, and among more, a kernel before lists
 // them.  8 kv heads of 128, 4 q heads each, in a graph, looked for / listed: 1 prompt of 64 tokens 8.0 / 11.1 us, of 500 14.9 / 18.1, 8 of
 // 100 11.5 / 13.7; 2 kv heads of 64: 60 rows of 6 tokens 7.9 / 10.5, 30 of 40 8.4 / 11.5.
-constexpr int kMostLooked = 64;
+constexpr int kMostLooked = 64;   // two a lane
+// By length where SMs get two CTAs and items are longer than this: the warp's turn over the sequences takes 0.03 us each.  24 rows of 18
+// tokens and 100 to 1700 positions, one q head a kv head, in ascending, descending and mixed order 34.2, 36.1, 37.0 us by length, else
+// 40.1, 37.3, 42.5; 628 tokens after 688 positions, 4 q heads, last tokens first 28.8, in order 32.6.
+constexpr int kLongLooked = 512;
 constexpr float kSlack = 4.f;      // how far a maximum may pass the reference before it moves
 
 // The positions that tokens see: all, a window's and the sinks', or (of an item whose rows are those of a group of sequences)
@@ -143,7 +147,7 @@ struct PromptArgs {
     int v8;                 // out 32-byte aligned
     int window, sinks;      // as in Kv8AttnArgs
     // few items: no list, every CTA looks for its own one
-    int direct;
+    int direct, by_length;
     const int32_t* cu;
     const int32_t* kv_len;
     int batch, total_rows, max_new, short_tokens, most_pairs;
@@ -500,47 +504,68 @@ __global__ void __launch_bounds__(1024) kv8_schedule_kernel(const Kv8AttnArgs a,
     }
 }
 
-// One warp: pair `want` of the calls' (query tile, sequence) pairs in the order of the sequences, as the list's kernel makes them.
+// One warp: pair `want` of a call's (query tile, sequence) pairs, two sequences a lane; a sequence's last tokens first and, by_length,
+// the longest sequences first (of as long ones, the first): the longest items then have their SMs to themselves for longest.
 __device__ __forceinline__ bool find_pair(const PromptArgs& p, int want, bool report, int* rec) {
     const int lane = threadIdx.x & 31;
     const long long room = (long long)p.view.max_pages << p.view.page_shift;
-    int run = 0;
-    bool found = false;
-#pragma unroll 1
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        const int b = b0 + lane;
-        int row0 = 0, n = 0, len = 0;
+    int row0[2], n[2], len[2], tiles[2], at[2] = {0, 0};
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int b = 32 * s + lane;
+        row0[s] = n[s] = len[s] = 0;
         if (b < p.batch) {
-            kv8_rows(p.cu, b, p.total_rows, row0, n);
+            kv8_rows(p.cu, b, p.total_rows, row0[s], n[s]);
             const int held = p.kv_len[b];
-            if (n > 0) {
-                len = held < 0 ? 0 : (int)min(room, (long long)held);
-                const int over = max(0, n - p.max_new);
-                if (report && n > p.short_tokens && (len != held || over)) raise_error(p.view.err, HRA_DEVERR_POS_RANGE);
-                if (n <= p.short_tokens) n = 0;
-                else n -= over;
-                len -= over;
+            if (n[s] > 0) {
+                len[s] = held < 0 ? 0 : (int)min(room, (long long)held);
+                const int over = max(0, n[s] - p.max_new);
+                if (report && n[s] > p.short_tokens && (len[s] != held || over)) raise_error(p.view.err, HRA_DEVERR_POS_RANGE);
+                if (n[s] <= p.short_tokens) n[s] = 0;
+                else n[s] -= over;
+                len[s] -= over;
             }
         }
-        const int tiles = (n + p.QT - 1) / p.QT;
-        int incl = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        const int at = run + incl - tiles;
-        const bool mine = want >= at && want < at + tiles;
-        if (mine) {
-            const int q_lo = (want - at) * p.QT, keys = max(0, len - n + min(n, q_lo + p.QT));
-            reinterpret_cast<int4*>(rec)[0] = make_int4(b, row0, n, q_lo);
-            reinterpret_cast<int4*>(rec)[1] = make_int4(len, keys, 0, 0);
-        }
-        found |= __any_sync(0xffffffffu, mine);
-        run += __shfl_sync(0xffffffffu, incl, 31);
+        tiles[s] = (n[s] + p.QT - 1) / p.QT;
     }
-    if (report && lane == 0 && run > p.most_pairs) raise_error(p.view.err, HRA_DEVERR_POS_RANGE);
-    return found;
+    int total = 0;
+    if (p.by_length) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll 1
+            for (int j = 0; j < min(32, p.batch - 32 * s); ++j) {
+                const int t = __shfl_sync(0xffffffffu, tiles[s], j), l = __shfl_sync(0xffffffffu, len[s], j);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (l > len[x] || (l == len[x] && 32 * s + j < 32 * x + lane)) at[x] += t;
+                total += t;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            int incl = tiles[s];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            at[s] = total + incl - tiles[s];
+            total += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    bool found = false;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        if (want >= at[s] && want < at[s] + tiles[s]) {
+            const int q_lo = (tiles[s] - 1 - (want - at[s])) * p.QT, keys = max(0, len[s] - n[s] + min(n[s], q_lo + p.QT));
+            reinterpret_cast<int4*>(rec)[0] = make_int4(32 * s + lane, row0[s], n[s], q_lo);
+            reinterpret_cast<int4*>(rec)[1] = make_int4(len[s], keys, 0, 0);
+            found = true;
+        }
+    }
+    if (report && lane == 0 && total > p.most_pairs) raise_error(p.view.err, HRA_DEVERR_POS_RANGE);
+    return __any_sync(0xffffffffu, found);
 }
 
 // The outputs of the items that this CTA did alone once more, a thread 32 dims of a row.  first: equal shares' first item, its
@@ -637,8 +662,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
         tma_prefetch_map(&tmQ);
     }
     if (MODE != kPrefix && warp == 2 && p.direct) {
-        // a sequence's last tokens first: its longest items, which then have their SMs to themselves for longest
-        const bool found = find_pair(p, p.most_pairs - 1 - pair_of(blockIdx.x), blockIdx.x == 0, rec_s);
+        const bool found = find_pair(p, pair_of(blockIdx.x), blockIdx.x == 0, rec_s);
         if (lane == 0) found_s = found;
     }
     if (warp == 1) {
@@ -1306,6 +1330,7 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
     p.sinks = a.sinks;
     p.by_heads = kv8_div(a.view.n_kv);
     p.direct = direct ? 1 : 0;
+    p.by_length = a.batch > 1 && room * a.view.n_kv > slots / 2 && longest > kLongLooked ? 1 : 0;
     p.cu = a.cu;
     p.kv_len = a.kv_len;
     p.batch = a.batch;
