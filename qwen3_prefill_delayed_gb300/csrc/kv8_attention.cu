@@ -833,7 +833,7 @@ cudaError_t launch_kv8_own(const Kv8AttnArgs& a, const SharedCall& c, cudaStream
 }
 
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, cudaStream_t st) {
-    if (kv8_shares(a.view, a.batch, a.nq, a.max_new, a.groups, a.max_prefix)) return launch_kv8_shared(a, st);
+    if (kv8_shares(a.view, a.batch, a.total_rows, a.nq, a.max_new, a.groups, a.max_prefix)) return launch_kv8_shared(a, st);
     const int G = a.nq / a.view.n_kv;
     const bool prompts = (long long)G * a.max_new > kShortRows;
     uint8_t* scratch = reinterpret_cast<uint8_t*>(a.scratch);

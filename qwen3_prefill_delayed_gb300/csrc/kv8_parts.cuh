@@ -60,7 +60,7 @@ cudaError_t launch_kv8_prefix(const Kv8AttnArgs& a, const SharedCall& c, cudaStr
 cudaError_t launch_kv8_own(const Kv8AttnArgs& a, const SharedCall& c, cudaStream_t st);      // kv8_attention.cu
 cudaError_t launch_kv8_shared(const Kv8AttnArgs& a, cudaStream_t st);                        // kv8_shared.cu
 // Whether a call's prefixes are read once; if not, launch_kv8_attention goes row by row.
-bool kv8_shares(const Kv8View& c, int batch, int nq, int max_new, int groups, int max_prefix);
+bool kv8_shares(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int groups, int max_prefix);
 // Rows of a short sequence's tile: one n = 8 column group of the MMAs while its (position, head) rows fit, else two.
 inline int column_groups(int G, int max_new) { return (long long)G * max_new <= 8 ? 1 : 2; }
 

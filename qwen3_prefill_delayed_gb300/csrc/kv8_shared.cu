@@ -30,6 +30,10 @@ constexpr int kMostParts = 32;  // of a prefix: what the lanes of a joining warp
 // 64 after 1024 (132 MB) 38 / 39; 8 groups of 6 after 1024 (84 MB) 34 / 34, after 2048 39 / 47; 64 rows after 16384 59 / 330.
 // Tokens of more than 8 rows take twice as long row by row: 16 rows of 8 tokens after 2048 (63 MB) 40 / 49.
 constexpr long long kLeastSaved = 96LL << 20;
+// ... and for each (token, head) row of such tokens, in units of head_dim^2 / 8, what its own positions and its join cost: 64 rows of
+// 4 / 8 / 16 tokens after 1024 (252 MB, counted twice) 45 / 64 / 106 us, row by row 63 / 57 / 57, of 16 after 4096 (1008 MB) 164 / 170; with
+// heads of 64 31 / 44 / 72 (126 MB), row by row 42 / 49 / 49, and 119 / 146 (504 MB).
+constexpr long long kSavedARow = 5;
 constexpr int kHeldRows = 1024; // rows whose lengths the plan holds in shared memory
 constexpr int kOwnSplits = 8;   // most CTAs that a row's own positions are split over
 // Units of 128 keys that a CTA takes of a row's own positions at least: more where the CTAs are more than the SMs hold at
@@ -363,13 +367,14 @@ long long most_units(const Kv8View& c, int total_rows, int G, int groups) {
 
 }  // namespace
 
-bool kv8_shares(const Kv8View& c, int batch, int nq, int max_new, int groups, int max_prefix) {
+bool kv8_shares(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int groups, int max_prefix) {
     const int G = nq / c.n_kv;
     if (groups < 1 || groups >= batch || (long long)G * max_new > kMostRows) return false;
     if (max_prefix < c.page_size || (long long)batch * row_tiles(G, max_new) > 65535) return false;
     const long long held = std::min<long long>(max_prefix, (long long)c.max_pages * c.page_size);
     const long long saved = 2LL * c.n_kv * c.head_dim * held * (batch - groups);   // bytes, if the groups are alike
-    return saved * (column_groups(G, max_new) == 1 ? 1 : 2) >= kLeastSaved;
+    if (column_groups(G, max_new) == 1) return saved >= kLeastSaved;
+    return 2 * saved >= kLeastSaved + (long long)most_rows(batch, total_rows, max_new) * nq * (c.head_dim * c.head_dim / 8 * kSavedARow);
 }
 
 size_t kv8_shared_scratch_bytes(const Kv8View& c, int batch, int total_rows, int nq, int max_new, int max_len, int groups,

@@ -1,5 +1,6 @@
 """Prompts of mixed lengths over the paged 8-bit cache: whole items or equal shares by the lengths that the call finds on the device,
-against the plain 64-bit forms of kv8_ref and kv8_reach_ref; and captured calls replayed with lengths that ask for the other."""
+against the plain 64-bit forms of kv8_ref and kv8_reach_ref; captured calls replayed with lengths that ask for the other; and steps of
+many tokens behind prefixes that are and are not worth sharing."""
 import pytest
 import torch
 
@@ -118,3 +119,31 @@ def test_lengths_far_below_the_bound(hra, H, new, lens):  # noqa: F811
     want, bound = R.attend(c, 0, call.q, cu_of(new), lens, split=True)
     assert float(((call.out.cpu().double() - want).abs() - bound).max()) <= 0
     assert call.shares() == (len(new) == 2)
+
+
+@pytest.mark.parametrize("n,prefix,kernels", [(16, 1024, 0), (8, 1024, 0), (4, 1024, 4), (8, 4096, 4)])
+def test_steps_of_many_tokens_share_long_prefixes_alone(hra, n, prefix, kernels):  # noqa: F811
+    """Many tokens behind a prefix that is not long for them: the call with groups is the one without, launches among it."""
+    H, G, D, P, rows = 8, 4, 128, 64, 64
+    c = build([prefix], H=H, D=D, P=P, seed=n, spare=rows + 1)
+    used = [int(x) for x in c["table"][0]]
+    free = [x for x in range(c["refs"].numel()) if x not in used]
+    c["codes"][0, free] = c["codes"][0, used[0]].clone()
+    c["scales"][0, free] = c["scales"][0, used[0]].clone()
+    c["table"] = torch.tensor([used + [free[b]] for b in range(rows)], dtype=torch.int32)
+    c["lens"] = i32([prefix + n] * rows)
+    kv = gpu(hra, c)
+    q = torch.randn(rows * n, H * G, D, generator=torch.Generator().manual_seed(3)).to(BF16).cuda()
+    args = (0, q, i32(range(0, rows * n + 1, n)).cuda(), i32([prefix + n] * rows).cuda(), n, prefix + n)
+    reach = hra.Kv8Reach(groups=i32([0, rows]).cuda(), prefix=i32([prefix]).cuda(), max_prefix=prefix, max_own=n)
+    before = hra.hra_launch_counter()
+    plain = kv.attend(*args)
+    middle = hra.hra_launch_counter()
+    got = kv.attend(*args, reach=reach)
+    after = hra.hra_launch_counter()
+    if kernels:
+        assert after - middle == kernels
+        want, bound = R.attend({**c, "table": c["table"][-1:]}, 0, q.cpu()[-n:], [0, n], [prefix + n], split=True)   # the last row
+        assert float(((got.cpu()[-n:].double() - want).abs() - bound).max()) <= 0
+    else:
+        assert after - middle == middle - before and torch.equal(got, plain)
