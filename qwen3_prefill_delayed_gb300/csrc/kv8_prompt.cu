@@ -291,15 +291,13 @@ __device__ __forceinline__ float weight_pass(uint32_t lS, const float* ks, float
 // A tile whose keys not every row sees: the scores that a row does not see become -inf where they are, and the passes above go over
 // it like over any other (passes with masks of their own, run once or twice an item, wait for their instructions: 2.4 us a tile,
 // and 0.9 for the others; 8 long prompts 215 us with them, 204 without).  seen: keys [lo, limit) and those
-// below sinks, relative to the tile's first; there: blocks that are.  False: the row sees none of the tile's keys.
+// below sinks, relative to the tile's first; there: blocks that are.
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-__device__ __forceinline__ bool hide_unseen(uint32_t lS, int limit, int lo, int sinks, uint32_t there) {
-    uint32_t any = 0u;
+__device__ __forceinline__ void hide_unseen(uint32_t lS, int limit, int lo, int sinks, uint32_t there) {
 #pragma unroll 1
     for (int ch = 0; ch < TK / 32; ++ch, limit -= 32, lo -= 32, sinks -= 32, there >>= 2) {
         const uint32_t blocks = (there & 1u ? 0xFFFFu : 0u) | (there & 2u ? 0xFFFF0000u : 0u);
         const uint32_t seen = bits_below(limit) & (~bits_below(lo) | bits_below(sinks)) & blocks;
-        any |= seen;
         float a[32];
         tmem_ld32(lS + 32 * ch, a);
 #pragma unroll
@@ -307,7 +305,6 @@ __device__ __forceinline__ bool hide_unseen(uint32_t lS, int limit, int lo, int 
             if (!(seen & (1u << e))) a[e] = -INFINITY;
         tmem_st32(lS + 32 * ch, a);
     }
-    return any != 0u;
 }
 
 // One CTA.  The non-empty (query tile, sequence) pairs: by a counting sort, most key tiles first, or, for equal shares,
@@ -898,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
             ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_QS + it % NQS), (uint32_t)(it / NQS) & 1u, abort_flag));
             if (!ok) break;
             // rows without a token, or a key: scores of almost 0 (coef_of), whose maximum never moves their warp to rescale O
-            const float q_scale = limit > 0 ? qs[(it % NQS) * TROWS + row] * p.scale_log2 : 0.f;
+            const float q_unscale = limit > 0 ? qs[(it % NQS) * TROWS + row] * p.scale_log2 : 0.f;
             float m = -INFINITY, M = -INFINITY, l = 0.f;
             for (int t = 0; t < n_kt && ok; ++t, ++g) {
                 ok = __all_sync(0xffffffffu,
@@ -914,10 +911,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                 const bool whole = blocks == (1 << NB) - 1 &&
                                    (MODE != kWindow ? j0 + TK <= clear
                                                     : j0 + TK <= lim_min && (j0 >= lo_max || j0 + TK <= p.sinks));
-                // (keys that a row does not see are nothing to it whatever its q is: a scale of NaN would make them NaN)
-                float q_unscale = q_scale;
-                if (!whole && !hide_unseen(lS, limit - j0, MODE == kWindow ? limit - p.window - j0 : -(1 << 30), p.sinks - j0, (uint32_t)blocks))
-                    q_unscale = 0.f;
+                if (!whole)
+                    hide_unseen(lS, limit - j0, MODE == kWindow ? limit - p.window - j0 : -(1 << 30), p.sinks - j0, (uint32_t)blocks);
                 float mx = -INFINITY, Mx = -INFINITY;
                 max_pass(lS, ks, q_unscale, mx, Mx);
                 const float mn = fmaxf(m, mx);
@@ -1105,12 +1100,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_prompt_kernel(const __grid_co
                         const __half2 d1 = __hsub2(*reinterpret_cast<const __half2*>(&f1), *reinterpret_cast<const __half2*>(&back1));
                         lo[e] = f16x4_e4m3x4(*reinterpret_cast<const uint32_t*>(&d0), *reinterpret_cast<const uint32_t*>(&d1));
                     }
+                    // a row with an infinity or a NaN: its scores are NaN, and nothing where they are hidden, which a scale of NaN would
+                    // not leave them
+                    if (top >= 0x7F80u) hi[0] = 0x7F7F7F7Fu;
                     __syncwarp();   // every lane of a row has read before one writes
                     const int at = row * HD + ((x ^ sw) << 4);
                     *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(smem + C::QB + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    // a row with an infinity or a NaN gives NaN
-                    if (x == 0) qs[(it % NQS) * TROWS + row] = __uint_as_float(top < 0x7F80u ? s : 0x7FC00000u);
+                    if (x == 0) qs[(it % NQS) * TROWS + row] = __uint_as_float(s);
                 }
                 if (!ok) break;
                 fence_proxy_async_smem();
