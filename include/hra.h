@@ -523,10 +523,12 @@ typedef struct hra_kv8_reach {
  *   max_prefix   host upper bound of prefix
  *   max_own      host upper bound of kv_len - prefix (0 or more).  Both choose how the work is split; larger ones give the
  *                same values
- *   groups       0: none (the pointers are then not looked at); at most 1024 (else HRA_ERR_UNSUPPORTED)
+ *   groups       0: none (the pointers are then not looked at); at most batch and 1024 (else HRA_ERR_INVALID_ARG,
+ *                HRA_ERR_UNSUPPORTED)
  * The values are those of hra_kv8_attention, in another order of sums, and q enters the scores of a prefix as it does where
- * max_new * (n_q_heads / n_kv_heads) > 16; where sharing would not pay, it is that call.  Entries of group_cu outside
- * [0, batch] or descending are clamped, a prefix below 0 counts as 0 (HRA_DEVERR_POS_RANGE).  A window and groups in one call are
+ * max_new * (n_q_heads / n_kv_heads) > 16.  Where by max_prefix, max_new, total_rows and the heads sharing would not pay, it is that
+ * call, and the arrays are not read; a max_prefix far above the prefixes makes short ones shared, which is slower.  Entries of
+ * group_cu that are read and lie outside [0, batch] or descend are clamped, a prefix below 0 counts as 0 (HRA_DEVERR_POS_RANGE).  A window and groups in one call are
  * HRA_ERR_UNSUPPORTED; group_cu and prefix inside the workspace or out (in the model's passes: hidden, pos, and what the
  * codebook step of a frame writes) are HRA_ERR_INVALID_ARG. */
 

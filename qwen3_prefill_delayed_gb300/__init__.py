@@ -958,7 +958,8 @@ class Kv8Reach:
     groups, prefix     rows groups[g] .. groups[g + 1) of the batch list the same pages for their first prefix[g] positions,
                        which are read once for all of them.  CUDA int32 tensors [n + 1] and [n], read at each call.
                        max_prefix and max_own are host upper bounds of prefix and of the rows' positions behind it (by
-                       default all that the cache's rows can hold).
+                       default all that the cache's rows can hold).  Whether sharing pays is judged by max_prefix: where the table
+                       is wide and prefixes are short, give it.
 
     An object stays what it was made of; the two tensors' contents may change between calls."""
 

@@ -33,7 +33,8 @@
 // block costs one lane two instructions to request.  64 sequences of up to 8192 keys, 8 kv heads of 128, 4 q heads
 // each (559 MB): 108 us, 5.2 TB/s; with the pieces copied by cp.async, an address a lane each, 140 us; one block at a
 // time 117-124 us (both against 112 then).  What is left is the warps' own work: 48% of issue slots, 12 warps an SM.
-// Through a window of 2048 and 4 sinks the same 64 rows, of up to 32,768 positions (254 MB seen), take 58 us, 4.4 TB/s.
+// Through a window of 2048 and 4 sinks the same 64 rows, of up to 32,768 positions (254 MB seen), take 58 us, 4.4 TB/s.  Heads of 128 in two
+// column groups are at the limit of their registers: 100 bytes spilled a thread, 142-158 through a window.
 #include <math.h>
 
 #include <algorithm>

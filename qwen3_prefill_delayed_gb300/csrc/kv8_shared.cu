@@ -9,7 +9,8 @@
 //   prefix  the units, each one's sums to scratch as a part
 //   own     (sequence, head, split): the row's own positions, as parts
 //   join    a warp a (token, head) row: its parts in order, prefix first (the last CTA of a sequence and head to do it, in the
-//           place of a kernel of its own: 46 us against 43 for 46 rows in 8 groups, 78 against 73 for 64 in one)
+//           place of a kernel of its own: 46 us against 43 for 46 rows in 8 groups, 78 against 76 for 64 in one, but 50 against 53 for
+//           32 rows of 0-12 tokens, whose own positions are one part)
 // 64 rows on 16,001 positions, 15-1000 of their own: 69 us (plan 6.5, prefix 29, own 23, join 10.5), row by row 330; 8 groups of 4-8
 // rows on 1024-2112: 40 us (6.5, 16, 14, 5).  A pass plans once.  The prefix is bound by its chain of tiles, 45% of the issue slots
 // and 27% of the tensor pipe; own positions and joins by latency.
@@ -22,13 +23,18 @@ namespace hra {
 
 namespace {
 
-// (token, head) rows of a sequence from which its own prompt tiles are at least half full: it then shares nothing
+// (token, head) rows of a sequence from which its own prompt tiles are at least half full: it then shares nothing.  32 rows of 8 / 12 / 16 /
+// 20 / 24 / 31 tokens, 4 q heads a kv head, after 4096 shared positions 62 / 76 / 98 / 139 / 152 / 172 us, row by row 92 in all; 8 rows of
+// 16 / 20 / 31 after 8192 52 / 57 / 81, row by row 54 / 56 / 61; 16 q heads, 32 rows of 4 / 5 / 8 after 8192 49 / 55 / 77, row by row 55 / 57 / 62;
+// one q head, 16 rows of 32 / 64 / 80 after 4096 43 / 61 / 73, row by row 55 / 57 / 58.
 constexpr int kMostRows = 64;
 constexpr int kMostParts = 32;  // of a prefix: what the lanes of a joining warp look at in one turn
 // Bytes of K and V that a call has to save: below them its three further kernels cost more.  8 kv heads of 128, 4 q heads each, 200
 // own positions, in a graph, once a group / row by row: 16 rows after 4096 shared positions (126 MB) 35 / 33 us, after 8192 38 / 53;
 // 64 after 1024 (132 MB) 38 / 39; 8 groups of 6 after 1024 (84 MB) 34 / 34, after 2048 39 / 47; 64 rows after 16384 59 / 330.
-// Tokens of more than 8 rows take twice as long row by row: 16 rows of 8 tokens after 2048 (63 MB) 40 / 49.
+// Tokens of more than 8 rows take twice as long row by row: 16 rows of 8 tokens after 2048 (63 MB) 40 / 49.  Other heads, single tokens, once a
+// group / row by row: 2 kv heads of 128, 64 rows after 4096 (126 MB) 29 / 34 us; 8 of 64 with 4 q heads, 64 rows after 1024 (63 MB) 23 / 32,
+// 16 after 4096 (60 MB) 25 / 28, 4 after 16384 (48 MB) 30 / 29: with heads of 64 half as much would do.
 constexpr long long kLeastSaved = 96LL << 20;
 // ... and for each (token, head) row of such tokens, in units of head_dim^2 / 8, what its own positions and its join cost: 64 rows of
 // 4 / 8 / 16 tokens after 1024 (252 MB, counted twice) 45 / 64 / 106 us, row by row 63 / 57 / 57, of 16 after 4096 (1008 MB) 164 / 170; with
