@@ -37,8 +37,8 @@
 // A few items are looked for by their CTAs; more come from a list built on the device (kv8_schedule_kernel).  Many items: most key tiles first, and CTA c
 // takes entries in snake order.  Few long ones (prompt chunks after many cached positions): the tiles of all items
 // form a line of which every CTA takes an equal share; parts of an item go to scratch as fp32 sums with their
-// (m, l, M) and a second kernel joins them in order.  Where the bounds leave it open, the list's kernel chooses by the lengths.  2 rows of 500-1021 tokens after 9-16 thousand: 376 items on 304
-// CTAs took two turns of the longest, 405 us; equal shares 371.
+// (m, l, M) and a second kernel joins them in order.  Where the bounds leave it open, the list's kernel chooses by the lengths.  2 rows of
+// 500-1021 tokens after 9-16 thousand: 376 items on 304 CTAs took two turns of the longest, 405 us; equal shares 371.
 // Through a window an item has the tiles that some row of it sees.  8 prompts of 1024-2048 tokens, window 512, 16 sinks: 186 us,
 // 479 TFLOP/s of seen pairs; 2 chunks after 9-16 thousand, window 4001: 172 us, 675 TFLOP/s.  Hidden scores at the edges are
 // overwritten where they are (hide_unseen): with masks in the softmax passes by blocks of 16 keys 232 / 185 us, by bits of 32 keys
@@ -1310,8 +1310,9 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
                                                                                                          : kWhole;
     const bool direct = way == kWhole && room * a.view.n_kv <= slots && a.batch <= kMostLooked;
     if (!direct && !a.planned) {
-        if (way == kWeigh) HRA_LAUNCH(kv8_schedule_kernel<true>, dim3(1), dim3(1024), 0, st, a, G, QT, short_rows, 0, slots, (int)room, list);
-        else HRA_LAUNCH(kv8_schedule_kernel<false>, dim3(1), dim3(1024), 0, st, a, G, QT, short_rows, way == kShares ? 1 : 0, slots, (int)room, list);
+        const int shares = way == kShares ? 1 : 0, most = (int)room;
+        if (way == kWeigh) HRA_LAUNCH(kv8_schedule_kernel<true>, dim3(1), dim3(1024), 0, st, a, G, QT, short_rows, shares, slots, most, list);
+        else HRA_LAUNCH(kv8_schedule_kernel<false>, dim3(1), dim3(1024), 0, st, a, G, QT, short_rows, shares, slots, most, list);
     }
     PromptArgs p{};
     p.view = a.view;
@@ -1336,7 +1337,9 @@ cudaError_t launch_hd(const Kv8AttnArgs& a, int G, int QT, int short_rows, cudaS
     p.short_tokens = short_rows / G;
     p.most_pairs = (int)room;
     p.v8 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
-    const int grid = direct ? (int)(room * a.view.n_kv) : way != kWhole ? slots : (int)std::max<long long>(1, std::min<long long>(pairs * a.view.n_kv, slots));
+    const int grid = direct           ? (int)(room * a.view.n_kv)
+                     : way != kWhole ? slots
+                                     : (int)std::max<long long>(1, std::min<long long>(pairs * a.view.n_kv, slots));
     if (way != kWhole) {
         const uintptr_t behind = reinterpret_cast<uintptr_t>(a.scratch) + list_bytes(a.batch, a.total_rows, G);
         uint8_t* at = reinterpret_cast<uint8_t*>((behind + 31) & ~uintptr_t(31));
